@@ -9,7 +9,8 @@ The 4-bit cache of one sequence is two planes, quants then scales: row t's
 kv_width/32 blocks of 16 bytes at byte t * kv_width/2, its f16 scales at byte
 cap * kv_width/2 + t * kv_width/16.  Byte i of a block holds element i in its
 low half and element i + 16 in its high half, the value being
-scale * (nibble - 8)."""
+scale * (nibble - 8).  Every sequence's cache starts at a multiple of 256
+elements."""
 import math
 
 import torch
@@ -117,6 +118,12 @@ def _starts(case):
     return [int(room * (((i + 3) * GOLDEN) % 1.0)) for i in range(case["batch"])]
 
 
+def _stride(case):
+    """Elements from one sequence's cache to the next's: whole lines of memory for every cache type."""
+    width = case["width"] if case["op"] == "kv" else case["kv_heads"] * case["dim"]
+    return -(-case["cap"] * width // 256) * 256
+
+
 def _row_bytes(cache, width):
     return {"f32": 4 * width, "f16": 2 * width, "q8_0": width // 32 * 34, "q4": width // 32 * 18}[cache]
 
@@ -148,7 +155,7 @@ def prepare(case, seed):
         s["pos"], s["count"] = _ints(_starts(case)), _ints(_counts(case))
         s["err"] = _ints([0])
         for x in ("k", "v"):
-            s[x + "cache"] = _filled(gen, case["cache"], batch, cap, width)
+            s[x + "cache"] = _filled(gen, case["cache"], batch, cap, width, _stride(case))
             s[x + "_out"] = torch.zeros(batch, rows, width, dtype=TORCH[case["dst"]], device="cuda")
         if case["src"]:
             ld = case["ld"] or width
@@ -162,8 +169,8 @@ def prepare(case, seed):
     elif case["op"] == "attn":
         batch, heads, kv_heads, dim, cap = (case[x] for x in ("batch", "heads", "kv_heads", "dim", "cap"))
         s["q"] = _normal(gen, (batch, heads * dim))
-        s["kcache"] = _filled(gen, "q4", batch, cap, kv_heads * dim)
-        s["vcache"] = _filled(gen, "q4", batch, cap, kv_heads * dim)
+        s["kcache"] = _filled(gen, "q4", batch, cap, kv_heads * dim, _stride(case))
+        s["vcache"] = _filled(gen, "q4", batch, cap, kv_heads * dim, _stride(case))
         s["lens"], s["err"] = _ints(_lens(case)), _ints([0])
         s["out"] = torch.empty(batch, heads * dim, device="cuda")
     else:
@@ -197,22 +204,22 @@ def _normal(gen, shape):
     return torch.randn(shape, generator=gen, device="cuda")
 
 
-def _filled(gen, cache, batch, cap, width):
-    """A cache of normally distributed rows."""
-    n = cap * _row_bytes(cache, width)
+def _filled(gen, cache, batch, cap, width, stride):
+    """Caches [batch][stride elements] of normally distributed rows."""
     if cache in TORCH:
-        return _normal(gen, (batch, cap, width)).to(TORCH[cache])
+        return _normal(gen, (batch, stride)).to(TORCH[cache])
     blocks = width // 32
+    c = torch.zeros(batch, _row_bytes(cache, stride), dtype=torch.uint8, device="cuda")
     # the scales that blocks of 32 normal values get, and quants of about their spread
+    planes = _planes(c, cache, cap, width)
     if cache == "q8_0":
-        c = torch.randint(-100, 101, (batch, cap, blocks, 34), generator=gen, device="cuda", dtype=torch.int8).view(torch.uint8)
-        c[..., :2] = (_top(gen, batch, cap, blocks) / 127).half().unsqueeze(-1).view(torch.uint8)
-        return c.view(batch, n)
-    c = torch.empty(batch, n, dtype=torch.uint8, device="cuda")
-    q = c[:, :cap * width // 2]
-    q.copy_(torch.randint(0, 256, q.shape, generator=gen, device="cuda", dtype=torch.uint8))
+        rows = torch.randint(-100, 101, (batch, cap, blocks, 34), generator=gen, device="cuda", dtype=torch.int8).view(torch.uint8)
+        rows[..., :2] = (_top(gen, batch, cap, blocks) / 127).half().unsqueeze(-1).view(torch.uint8)
+        planes[0].copy_(rows.flatten(2))
+        return c
+    planes[0].copy_(torch.randint(0, 256, planes[0].shape, generator=gen, device="cuda", dtype=torch.uint8))
     sign = torch.randint(0, 2, (batch, cap, blocks), generator=gen, device="cuda") * 2 - 1
-    c[:, cap * width // 2:] = (_top(gen, batch, cap, blocks) * sign / 8).half().view(torch.uint8).view(batch, -1)
+    planes[1].copy_((_top(gen, batch, cap, blocks) * sign / 8).half().view(torch.uint8))
     return c
 
 
@@ -247,16 +254,16 @@ def _run_kv(s):
         q8d = s["q8d"]
         if c["src"]:
             q8d.q8d_kv_append_rows(s["k"], s["v"], KV[c["src"]], s["ld"], s["kcache"], s["vcache"], KV[c["cache"]], batch, rows,
-                                   width, cap, cap * width, s["pos"], s["count"], s["err"])
+                                   width, cap, _stride(c), s["pos"], s["count"], s["err"])
         q8d.q8d_kv_read_rows(s["kcache"], s["vcache"], KV[c["cache"]], s["k_out"], s["v_out"], KV[c["dst"]], width, batch, rows,
-                             width, cap, cap * width, s["pos"], s["count"], s["err"])
+                             width, cap, _stride(c), s["pos"], s["count"], s["err"])
         return {"k": s["k_out"], "v": s["v_out"]}
     step = torch.arange(rows, device="cuda")
     at = s["pos"].long()[:, None] + step  # [batch][rows] cache rows
     live = (step < s["count"][:, None])[..., None]
     seq = torch.arange(batch, device="cuda")[:, None]
     for x in ("k", "v"):
-        planes = _planes(s[x + "cache"], c["cache"], batch, cap, width)
+        planes = _planes(s[x + "cache"], c["cache"], cap, width)
         if c["src"]:
             new = _encode(s[x].float().view(batch, rows, width), c["cache"])
             for plane, rows_new in zip(planes, new):
@@ -267,14 +274,13 @@ def _run_kv(s):
     return {"k": s["k_out"], "v": s["v_out"]}
 
 
-def _planes(cache, kind, batch, cap, width):
-    """Views [batch][cap][...] of what a cache keeps for each row."""
-    if kind in TORCH:
-        return [cache]
-    if kind == "q8_0":
-        return [cache.view(batch, cap, width // 32 * 34)]
-    n = cap * width // 2
-    return [cache[:, :n].view(batch, cap, width // 2), cache[:, n:].view(batch, cap, width // 16)]
+def _planes(cache, kind, cap, width):
+    """Views [batch][cap][...] of what the caches [batch][...] keep for each row."""
+    if kind == "q4":
+        n = cap * width // 2
+        return [cache[:, :n].unflatten(1, (cap, width // 2)), cache[:, n:n + n // 8].unflatten(1, (cap, width // 16))]
+    row = width if kind in TORCH else _row_bytes(kind, width)
+    return [cache[:, :cap * row].unflatten(1, (cap, row))]
 
 
 def _encode(x, kind):
@@ -283,7 +289,8 @@ def _encode(x, kind):
         return [x.to(TORCH[kind])]
     b = x.unflatten(-1, (-1, 32))
     if kind == "q8_0":
-        d = b.abs().amax(-1, keepdim=True) / 127
+        d = b.abs().amax(-1, keepdim=True)
+        d = d / torch.full_like(d, 127)  # (a tensor's division by a number is a product with its inverse)
         r = b * torch.where(d > 0, 1 / d, torch.zeros_like(d))
         q = torch.trunc(r)
         q = (q + torch.sign(r) * ((r - q).abs() >= 0.5)).to(torch.int8)  # to nearest, halves away from zero
@@ -313,10 +320,10 @@ def _run_attn(s):
     batch, heads, kv_heads, dim, cap = (c[x] for x in ("batch", "heads", "kv_heads", "dim", "cap"))
     if own:
         s["q8d"].q8d_gqa_decode_attn(s["q"], None, None, s["kcache"], s["vcache"], Q4, s["out"], batch, heads, kv_heads, dim, cap,
-                                     cap * kv_heads * dim, s["lens"], 1 / math.sqrt(dim), s["ws"], s["ws_bytes"], s["err"])
+                                     _stride(c), s["lens"], 1 / math.sqrt(dim), s["ws"], s["ws_bytes"], s["err"])
         return s["out"]
     width = kv_heads * dim
-    k, v = (_decode(_planes(s[x], "q4", batch, cap, width), "q4").view(batch, cap, kv_heads, dim).transpose(1, 2)
+    k, v = (_decode(_planes(s[x], "q4", cap, width), "q4").view(batch, cap, kv_heads, dim).transpose(1, 2)
             for x in ("kcache", "vcache"))
     q = s["q"].view(batch, kv_heads, heads // kv_heads, dim)
     p = torch.matmul(q, k.transpose(2, 3)) * (1 / math.sqrt(dim))
@@ -377,7 +384,7 @@ def exact(case, seed):
 def _exact_q4(cache, width, cap, rows):
     """Rows of one sequence's 4-bit cache as f64 [rows][width]."""
     quants = cache[:cap * width // 2].view(cap, width // 32, 16)[rows].int()
-    scales = cache[cap * width // 2:].view(torch.float16).view(cap, width // 32, 1)[rows].double()
+    scales = cache[cap * width // 2:cap * width // 16 * 9].view(torch.float16).view(cap, width // 32, 1)[rows].double()
     return (torch.cat([quants % 16, quants // 16], 2).double() - 8).mul_(scales).view(-1, width)
 
 
@@ -401,9 +408,9 @@ def _exact_kv(case, s, x):
             if kind == "q4":
                 out[b, :n] = _exact_q4(cache, width, cap, at)
             elif kind == "q8_0":
-                out[b, :n] = _exact_q8(cache.view(cap, width // 32, 34)[at]).view(n, width)
+                out[b, :n] = _exact_q8(cache[:cap * width // 32 * 34].view(cap, width // 32, 34)[at]).view(n, width)
             else:
-                out[b, :n] = cache[at].double()
+                out[b, :n] = cache[:cap * width].view(cap, width)[at].double()
             continue
         v = s[x][b * rows:b * rows + n].double().reshape(n, width // 32, 32)
         # the quantizers' steps are 32-bit ones by definition: each is done in 64 bits and rounded
@@ -412,8 +419,9 @@ def _exact_kv(case, s, x):
             r = torch.where(d > 0, _round32(v * _round32(1 / d)), 0.0)
             v = torch.sign(r) * torch.floor(r.abs() + 0.5) * d.half().double()
         elif kind == "q4":
-            hi, lo = v.max(2, keepdim=True).values, v.min(2, keepdim=True).values
-            d = torch.where(hi > -lo, hi, lo) / -8
+            largest = v.abs() == v.abs().max(2, keepdim=True).values
+            first = torch.where(largest, torch.arange(32, device="cuda"), 32).min(2, keepdim=True).values
+            d = v.gather(2, first) / -8
             r = torch.where(_round32(1 / d).isfinite(), _round32(v * _round32(1 / d)), 0.0)
             v = (torch.floor(_round32(r + 8.5)).clamp(0, 15) - 8) * d.half().double()
         elif kind == "f16":
