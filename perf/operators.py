@@ -17,7 +17,7 @@ import torch
 
 own = False
 
-F32, F16, Q8_0, Q4 = 0, 1, 2, 3
+F32, F16, Q8_0, Q4 = 0, 1, 2, 4
 KV = {"f32": F32, "f16": F16, "q8_0": Q8_0, "q4": Q4}
 TORCH = {"f32": torch.float32, "f16": torch.float16}
 GOLDEN = 0.6180339887498949
