@@ -45,6 +45,19 @@
  *               d = max|x| / 127, q_j = x_j * (1/d) rounded to nearest with
  *               halves away from zero, scale = d rounded to binary16, all in
  *               f32 (an all-zero block stores zeros); inputs must be finite.
+ *   4-bit KV    Q8D_KV_Q4: blocks of 32 elements as 16 bytes of quants and
+ *               one binary16 scale, kept as two planes: row t's quants are
+ *               the kv_width/2 bytes from byte t * kv_width/2 of the
+ *               sequence's cache, its scales the kv_width/16 bytes from byte
+ *               cap * kv_width/2 + t * kv_width/16 (9/16 bytes an element in
+ *               all).  Byte i of a block holds element i in its low half and
+ *               element i + 16 in its high half; value = scale * (n - 8) of
+ *               the half-byte n.  The quantizer: m = the block's element of
+ *               largest magnitude (the first of them), d = m / -8, id = 1/d
+ *               (0 where that is not finite), n_j = floor(x_j * id + 8.5)
+ *               limited to [0, 15], scale = d rounded to binary16, all in
+ *               f32; inputs must be finite, and below 2^19 in magnitude for
+ *               a finite scale.
  */
 #ifndef Q8D_H
 #define Q8D_H
@@ -68,6 +81,7 @@ extern "C" {
 #define Q8D_KV_F32 0
 #define Q8D_KV_F16 1
 #define Q8D_KV_Q8_0 2 /* packed: every cache row is kv_width/32 Q8_0 blocks */
+#define Q8D_KV_Q4 4   /* 4-bit: a plane of quants, then a plane of scales (3 is no type) */
 
 /* Bits of the device-side error word. */
 #define Q8D_DERR_POS_RANGE 0x1   /* append position outside [0, cap)          */
@@ -148,16 +162,60 @@ int q8d_matmul_small_m_ws(const float* X, int ldx, const void* w_q8, float* Y, i
  * ("IV.4: One command buffer per token", "Eight kernels": append_kv).
  *   kcache[pos][i] = cvt(k[i]), vcache[pos][i] = cvt(v[i]), i < kv_width
  * cvt is the identity for an f32 cache, round-to-nearest-even to binary16
- * for an f16 cache and the Q8_0 quantizer of each 32-element block for a
- * packed cache (kv_width % 32 == 0, else Q8D_EUNSUPPORTED; the stored bytes
- * equal a scalar CPU quantizer's).  pos is read from device memory (*d_pos)
+ * for an f16 cache and the quantizer of each 32-element block for a packed
+ * Q8_0 or a 4-bit cache (kv_width % 32 == 0, else Q8D_EUNSUPPORTED; the
+ * stored bytes equal a scalar CPU quantizer's).  pos is read from device memory (*d_pos)
  * so a captured graph replays unchanged; pos outside [0, cap) sets
  * Q8D_DERR_POS_RANGE in *d_err and writes nothing.  k, v: device
- * f32[kv_width]; caches: device, cap rows (a packed cache 16-byte aligned,
- * else Q8D_EALIGN); d_err: device int (OR-ed into, never cleared).
+ * f32[kv_width]; caches: device, cap rows (a packed or 4-bit cache 16-byte
+ * aligned, else Q8D_EALIGN); d_err: device int (OR-ed into, never cleared).
  * ---------------------------------------------------------------------- */
 int q8d_kv_append(const float* k, const float* v, void* kcache, void* vcache, int kv_dtype,
                   int kv_width, int cap, const int* d_pos, int* d_err, void* stream);
+
+/* Bytes of one sequence's K (or V) cache of cap rows of kv_width elements;
+ * 0 for a type, width or capacity that no cache has (kv_width % 32 != 0 for
+ * a packed or 4-bit cache). */
+size_t q8d_kv_cache_bytes(int kv_dtype, int kv_width, int cap);
+
+/* ------------------------------------------------------------------------
+ * q8d_kv_append_rows — store up to `rows` rows of every sequence of a batch
+ * (a prompt, or one token of each sequence) into the caches.
+ *   kcache[s][d_pos[s] + i] = cvt(k[s][i]), vcache likewise,
+ *   s < batch, i < d_counts[s] (`rows` for every sequence if d_counts is
+ *   NULL), with q8d_kv_append's cvt (f16 rows are exact in f32 first).
+ * k, v: device rows of kv_width elements of row_dtype (Q8D_KV_F32 or
+ *   Q8D_KV_F16); row i of sequence s starts at element (s * rows + i) * ld
+ *   (ld >= kv_width: k and v may be columns of one projection's output);
+ *   element-aligned, read 16 bytes at a time where the pointers and ld allow.
+ * kcache, vcache: device, every kv_dtype; sequence s's cache of cap rows
+ *   starts at element s * cache_batch_stride (at least cap * kv_width when
+ *   batch > 1; starts must be 16-byte aligned: a multiple of 256 elements
+ *   suits every type), and must not overlap k, v or each other.
+ * d_pos, d_counts: device int[batch].  A count outside [0, rows] sets
+ *   Q8D_DERR_LEN_RANGE, a row outside [0, cap) Q8D_DERR_POS_RANGE in *d_err
+ *   (may be NULL), and nothing of that sequence is written; a count of 0
+ *   writes nothing whatever the position.
+ * kv_width % 32 == 0 for a packed or 4-bit cache.  rows == 0: no-op.
+ * ---------------------------------------------------------------------- */
+int q8d_kv_append_rows(const void* k, const void* v, int row_dtype, int ld, void* kcache,
+                       void* vcache, int kv_dtype, int batch, int rows, int kv_width, int cap,
+                       long long cache_batch_stride, const int* d_pos, const int* d_counts,
+                       int* d_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * q8d_kv_read_rows — the values of cache rows (q8d_kv_append_rows reversed):
+ *   k_out[s][i] = value of kcache[s][d_pos[s] + i], v_out likewise,
+ *   s < batch, i < d_counts[s],
+ * as f32 or f16 rows (row_dtype; f16 rounds to nearest even once).  Rows
+ * i >= d_counts[s] of the outputs are left as they were; the rows of a
+ * sequence whose count or position is refused (as above) are set to NaN,
+ * all `rows` of them.  Other arguments as for q8d_kv_append_rows.
+ * ---------------------------------------------------------------------- */
+int q8d_kv_read_rows(const void* kcache, const void* vcache, int kv_dtype, void* k_out,
+                     void* v_out, int row_dtype, int ld, int batch, int rows, int kv_width,
+                     int cap, long long cache_batch_stride, const int* d_pos,
+                     const int* d_counts, int* d_err, void* stream);
 
 /* Bytes of scratch q8d_gqa_decode_attn needs for these sizes: the split-K
  * partials {m, l, O} of up to a fixed number of chunk slots per sequence
@@ -188,7 +246,9 @@ size_t q8d_gqa_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_
  *   workspace: device scratch of at least
  *            q8d_gqa_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, cap)
  *            bytes (contents need no initialisation)
- * head_dim in {64, 128}; n_heads % n_kv_heads == 0; n_heads/n_kv_heads <= 16.
+ * head_dim in {64, 128}; n_heads % n_kv_heads == 0; n_heads/n_kv_heads <= 16;
+ * every kv_dtype (a packed or 4-bit cache's stride is still in elements:
+ * a multiple of 256, so that sequences start on 16-byte boundaries).
  * ---------------------------------------------------------------------- */
 int q8d_gqa_decode_attn(const float* q, const float* k_new, const float* v_new, void* kcache,
                         void* vcache, int kv_dtype, float* out, int batch, int n_heads,
@@ -217,7 +277,7 @@ int q8d_gqa_decode_attn(const float* q, const float* k_new, const float* v_new, 
  * attended to; that row must not be read by another sequence of the same
  * call (the calls' writes and reads would race).
  * Other arguments, the workspace and the results are those of
- * q8d_gqa_decode_attn (f32, f16 and packed Q8_0 caches).
+ * q8d_gqa_decode_attn (f32, f16, packed Q8_0 and 4-bit caches).
  * ---------------------------------------------------------------------- */
 #define Q8D_MAX_RUNS 4
 int q8d_gqa_decode_attn_window(const float* q, const float* k_new, const float* v_new,

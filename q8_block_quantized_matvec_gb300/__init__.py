@@ -27,6 +27,7 @@ Q8D_ENOMEM = -7
 Q8D_KV_F32 = 0
 Q8D_KV_F16 = 1
 Q8D_KV_Q8_0 = 2
+Q8D_KV_Q4 = 4
 
 Q8D_MAX_RUNS = 4
 
@@ -85,6 +86,14 @@ def lib():
         L.q8d_matmul_small_m_ws.restype = i32
         L.q8d_kv_append.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
         L.q8d_kv_append.restype = i32
+        L.q8d_kv_cache_bytes.argtypes = [i32, i32, i32]
+        L.q8d_kv_cache_bytes.restype = sz
+        L.q8d_kv_append_rows.argtypes = [vp, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, i64, vp,
+                                         vp, vp, vp]
+        L.q8d_kv_append_rows.restype = i32
+        L.q8d_kv_read_rows.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i64, vp,
+                                       vp, vp, vp]
+        L.q8d_kv_read_rows.restype = i32
         L.q8d_gqa_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         L.q8d_gqa_workspace_bytes.restype = sz
         L.q8d_gqa_decode_attn.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32,
@@ -178,6 +187,28 @@ def q8d_kv_append(k, v, kcache, vcache, kv_dtype: int, kv_width: int, cap: int, 
     return _check(lib().q8d_kv_append(_ptr(k), _ptr(v), _ptr(kcache), _ptr(vcache), int(kv_dtype),
                                       int(kv_width), int(cap), _ptr(d_pos), _ptr(d_err),
                                       _stream(stream)), "q8d_kv_append")
+
+
+def q8d_kv_cache_bytes(kv_dtype: int, kv_width: int, cap: int) -> int:
+    return int(lib().q8d_kv_cache_bytes(int(kv_dtype), int(kv_width), int(cap)))
+
+
+def q8d_kv_append_rows(k, v, row_dtype: int, ld: int, kcache, vcache, kv_dtype: int, batch: int,
+                       rows: int, kv_width: int, cap: int, cache_batch_stride: int, d_pos,
+                       d_counts, d_err, stream=None) -> int:
+    return _check(lib().q8d_kv_append_rows(
+        _ptr(k), _ptr(v), int(row_dtype), int(ld), _ptr(kcache), _ptr(vcache), int(kv_dtype),
+        int(batch), int(rows), int(kv_width), int(cap), int(cache_batch_stride), _ptr(d_pos),
+        _ptr(d_counts), _ptr(d_err), _stream(stream)), "q8d_kv_append_rows")
+
+
+def q8d_kv_read_rows(kcache, vcache, kv_dtype: int, k_out, v_out, row_dtype: int, ld: int,
+                     batch: int, rows: int, kv_width: int, cap: int, cache_batch_stride: int,
+                     d_pos, d_counts, d_err, stream=None) -> int:
+    return _check(lib().q8d_kv_read_rows(
+        _ptr(kcache), _ptr(vcache), int(kv_dtype), _ptr(k_out), _ptr(v_out), int(row_dtype),
+        int(ld), int(batch), int(rows), int(kv_width), int(cap), int(cache_batch_stride),
+        _ptr(d_pos), _ptr(d_counts), _ptr(d_err), _stream(stream)), "q8d_kv_read_rows")
 
 
 def q8d_gqa_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,

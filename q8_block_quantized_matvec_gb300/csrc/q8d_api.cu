@@ -13,6 +13,7 @@
 
 #include "q8d_attn.cuh"
 #include "q8d_internal.cuh"
+#include "q8d_kv_rows.cuh"
 #include "q8d_rows.cuh"
 
 namespace q8d {
@@ -88,6 +89,22 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 static size_t q8_bytes(long long rows, int n) { return (size_t)rows * (size_t)(n / 32) * 34; }
+
+// Bytes of n cache elements of a type (a whole number of blocks for the
+// packed types).
+static long long kv_bytes(int kv_dtype, long long n) {
+  switch (kv_dtype) {
+    case Q8D_KV_F32: return n * 4;
+    case Q8D_KV_F16: return n * 2;
+    case Q8D_KV_Q8_0: return n / 32 * 34;
+    default: return n / 32 * 18;
+  }
+}
+static bool kv_known(int kv_dtype) {
+  return kv_dtype == Q8D_KV_F32 || kv_dtype == Q8D_KV_F16 || kv_dtype == Q8D_KV_Q8_0 ||
+         kv_dtype == Q8D_KV_Q4;
+}
+static bool kv_packed(int kv_dtype) { return kv_dtype == Q8D_KV_Q8_0 || kv_dtype == Q8D_KV_Q4; }
 
 int step_validate(const q8d_step_desc* d) {
   if (!d || !d->layers || !d->embed || !d->out_norm || !d->lm_head || !d->d_token || !d->d_pos ||
@@ -255,17 +272,117 @@ int q8d_matmul_small_m(const float* X, int ldx, const void* w_q8, float* Y, int 
 int q8d_kv_append(const float* k, const float* v, void* kcache, void* vcache, int kv_dtype,
                   int kv_width, int cap, const int* d_pos, int* d_err, void* stream) {
   if (!k || !v || !kcache || !vcache || !d_pos || kv_width <= 0 || cap <= 0) return Q8D_EINVAL;
-  if (kv_dtype != Q8D_KV_F32 && kv_dtype != Q8D_KV_F16 && kv_dtype != Q8D_KV_Q8_0)
-    return Q8D_EUNSUPPORTED;
-  if (kv_dtype == Q8D_KV_Q8_0 && kv_width % 32) return Q8D_EUNSUPPORTED;
+  if (!kv_known(kv_dtype)) return Q8D_EUNSUPPORTED;
+  if (kv_packed(kv_dtype) && kv_width % 32) return Q8D_EUNSUPPORTED;
   // (a packed cache's blocks are written with 16-bit scale stores)
   const size_t es = kv_dtype == Q8D_KV_F32 ? 4 : (kv_dtype == Q8D_KV_F16 ? 2 : 16);
   if (!aligned(kcache, es) || !aligned(vcache, es) || !aligned(k, 4) || !aligned(v, 4))
     return Q8D_EALIGN;
-  const size_t cb = kv_dtype == Q8D_KV_Q8_0 ? q8_bytes(cap, kv_width) : es * (size_t)kv_width * cap;
+  const size_t cb = (size_t)kv_bytes(kv_dtype, (long long)kv_width * cap);
   if (overlap(kcache, cb, vcache, cb)) return Q8D_EINVAL;
+  if (kv_dtype == Q8D_KV_Q4) {
+    KvRowsParams P{};
+    P.k = const_cast<float*>(k);
+    P.v = const_cast<float*>(v);
+    P.row_dtype = Q8D_KV_F32;
+    P.ld = kv_width;
+    P.kc = static_cast<uint8_t*>(kcache);
+    P.vc = static_cast<uint8_t*>(vcache);
+    P.kv_dtype = kv_dtype;
+    P.batch = P.rows = 1;
+    P.width = kv_width;
+    P.cap = cap;
+    P.d_pos = d_pos;
+    P.d_err = d_err;
+    return kv_append_rows_launch(P, static_cast<cudaStream_t>(stream));
+  }
   return kv_append_launch(k, v, kcache, vcache, kv_dtype, kv_width, cap, d_pos, d_err,
                           static_cast<cudaStream_t>(stream));
+}
+
+size_t q8d_kv_cache_bytes(int kv_dtype, int kv_width, int cap) {
+  if (!kv_known(kv_dtype) || kv_width <= 0 || cap <= 0) return 0;
+  if (kv_packed(kv_dtype) && kv_width % 32) return 0;
+  return (size_t)kv_bytes(kv_dtype, (long long)kv_width * cap);
+}
+
+}  // extern "C"
+
+namespace q8d {
+// Checks shared by storing and reading rows; fills *P (not for rows == 0).
+static int kv_rows_params(const void* k, const void* v, int row_dtype, int ld, const void* kcache,
+                          const void* vcache, int kv_dtype, int batch, int rows, int kv_width,
+                          int cap, long long stride, const int* d_pos, const int* d_counts,
+                          int* d_err, KvRowsParams* P) {
+  if (!k || !v || !kcache || !vcache || !d_pos) return Q8D_EINVAL;
+  if (batch <= 0 || rows < 0 || kv_width <= 0 || cap <= 0 || ld < kv_width || stride < 0)
+    return Q8D_EINVAL;
+  if (!kv_known(kv_dtype)) return Q8D_EUNSUPPORTED;
+  if (row_dtype != Q8D_KV_F32 && row_dtype != Q8D_KV_F16) return Q8D_EUNSUPPORTED;
+  if (kv_packed(kv_dtype) && kv_width % 32) return Q8D_EUNSUPPORTED;
+  const long long need = (long long)cap * kv_width;
+  if (batch > 1 && stride < need) return Q8D_EINVAL;
+  if (kv_packed(kv_dtype) && stride % 32) return Q8D_EALIGN;
+  const int es = row_dtype == Q8D_KV_F32 ? 4 : 2;
+  if (!aligned(kcache, 16) || !aligned(vcache, 16) || kv_bytes(kv_dtype, stride) % 16)
+    return Q8D_EALIGN;
+  if (!aligned(k, es) || !aligned(v, es) || !aligned(d_pos, 4) || !aligned(d_counts, 4))
+    return Q8D_EALIGN;
+  if (rows == 0) return Q8D_OK;
+  const size_t cb = (size_t)(kv_bytes(kv_dtype, stride) * (batch - 1) + kv_bytes(kv_dtype, need));
+  const size_t rb = es * (((size_t)batch * rows - 1) * ld + kv_width);
+  if (overlap(kcache, cb, vcache, cb)) return Q8D_EINVAL;
+  const void* const caches[] = {kcache, vcache};
+  for (const void* c : caches)
+    if (overlap(c, cb, k, rb) || overlap(c, cb, v, rb)) return Q8D_EINVAL;
+  P->k = const_cast<void*>(k);
+  P->v = const_cast<void*>(v);
+  P->row_dtype = row_dtype;
+  P->ld = ld;
+  P->kc = static_cast<uint8_t*>(const_cast<void*>(kcache));
+  P->vc = static_cast<uint8_t*>(const_cast<void*>(vcache));
+  P->kv_dtype = kv_dtype;
+  P->seq_bytes = kv_bytes(kv_dtype, stride);
+  P->batch = batch;
+  P->rows = rows;
+  P->width = kv_width;
+  P->cap = cap;
+  P->d_pos = d_pos;
+  P->d_counts = d_counts;
+  P->d_err = d_err;
+  return Q8D_OK;
+}
+}  // namespace q8d
+
+extern "C" {
+
+int q8d_kv_append_rows(const void* k, const void* v, int row_dtype, int ld, void* kcache,
+                       void* vcache, int kv_dtype, int batch, int rows, int kv_width, int cap,
+                       long long cache_batch_stride, const int* d_pos, const int* d_counts,
+                       int* d_err, void* stream) {
+  KvRowsParams P{};
+  const int rc = kv_rows_params(k, v, row_dtype, ld, kcache, vcache, kv_dtype, batch, rows, kv_width,
+                                cap, cache_batch_stride, d_pos, d_counts, d_err, &P);
+  if (rc || rows == 0) return rc;
+  return kv_append_rows_launch(P, static_cast<cudaStream_t>(stream));
+}
+
+int q8d_kv_read_rows(const void* kcache, const void* vcache, int kv_dtype, void* k_out,
+                     void* v_out, int row_dtype, int ld, int batch, int rows, int kv_width,
+                     int cap, long long cache_batch_stride, const int* d_pos,
+                     const int* d_counts, int* d_err, void* stream) {
+  KvRowsParams P{};
+  const int rc = kv_rows_params(k_out, v_out, row_dtype, ld, kcache, vcache, kv_dtype, batch, rows,
+                                kv_width, cap, cache_batch_stride, d_pos, d_counts, d_err, &P);
+  if (rc || rows == 0) return rc;
+  // the two outputs may interleave (columns of one buffer) but not share a value
+  const size_t es = row_dtype == Q8D_KV_F32 ? 4 : 2;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(k_out), b = reinterpret_cast<uintptr_t>(v_out);
+  const size_t apart = a < b ? b - a : a - b, pitch = es * ld, span = es * (size_t)kv_width;
+  if (apart < pitch * ((size_t)batch * rows - 1) + span &&
+      (apart % pitch < span || pitch - apart % pitch < span))
+    return Q8D_EINVAL;
+  return kv_read_rows_launch(P, static_cast<cudaStream_t>(stream));
 }
 
 size_t q8d_gqa_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim, int max_len) {
@@ -288,8 +405,7 @@ static int attn_entry(const float* q, const float* k_new, const float* v_new, vo
   if (batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || cap <= 0) return Q8D_EINVAL;
   if (head_dim != 64 && head_dim != 128) return Q8D_EUNSUPPORTED;
   if (n_heads % n_kv_heads || n_heads / n_kv_heads > 16) return Q8D_EUNSUPPORTED;
-  if (kv_dtype != Q8D_KV_F32 && kv_dtype != Q8D_KV_F16 && kv_dtype != Q8D_KV_Q8_0)
-    return Q8D_EUNSUPPORTED;
+  if (!kv_known(kv_dtype)) return Q8D_EUNSUPPORTED;
   if (!std::isfinite(scale)) return Q8D_EINVAL;
   const long long kvw = (long long)n_kv_heads * head_dim;
   if (cache_batch_stride < 0) return Q8D_EINVAL;
@@ -297,11 +413,10 @@ static int attn_entry(const float* q, const float* k_new, const float* v_new, vo
   if (batch > 1 && cache_batch_stride < kvw * cap && !(d_runs && cache_batch_stride == 0))
     return Q8D_EINVAL;
   // sequence starts 16-byte aligned: for a packed cache the stride (in
-  // elements) is a whole number of blocks, 34 bytes per 32 elements
-  const long long stride_bytes =
-      kv_dtype == Q8D_KV_Q8_0
-          ? (cache_batch_stride % 32 ? 1 : cache_batch_stride / 32 * 34)
-          : cache_batch_stride * (kv_dtype == Q8D_KV_F16 ? 2 : 4);
+  // elements) is a whole number of blocks, 34 (4-bit: 18) bytes per 32 elements
+  const long long stride_bytes = kv_packed(kv_dtype) && cache_batch_stride % 32
+                                     ? 1
+                                     : kv_bytes(kv_dtype, cache_batch_stride);
   if (!aligned(kcache, 16) || !aligned(vcache, 16) || (stride_bytes % 16)) return Q8D_EALIGN;
   if (!aligned(q, 4) || !aligned(out, 4) || !aligned(workspace, 16)) return Q8D_EALIGN;
   if (d_runs && !aligned(d_runs, 4)) return Q8D_EALIGN;

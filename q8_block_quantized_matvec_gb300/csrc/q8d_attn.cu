@@ -505,6 +505,7 @@ int attn_launch(AttnParams P, cudaStream_t stream) {
   P.ws_l = P.ws_m + (size_t)P.batch * P.n_heads * nc;
   if (P.kv_dtype == Q8D_KV_F16) return attn_mma_launch(P, stream);
   if (P.kv_dtype == Q8D_KV_Q8_0) return attn_q8kv_launch(P, stream);
+  if (P.kv_dtype == Q8D_KV_Q4) return attn_q4kv_launch(P, stream);
   if (P.head_dim == 128) return launch_attn_g<128, float>(P, stream);
   return launch_attn_g<64, float>(P, stream);
 }
