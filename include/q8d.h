@@ -315,6 +315,47 @@ int q8d_gqa_decode_attn_noalloc(const float* q, const float* k_new, const float*
                                 int* d_err, void* stream);
 
 /* ------------------------------------------------------------------------
+ * q8d_moe_ffn — a mixture-of-experts feed-forward layer over Q8_0 experts
+ * for a few tokens (the expert form of the dense gate / up / down products
+ * of the decode step).  For token t with x = X[t]:
+ *   l_e = sum_i router[e][i] * x[i],   p = softmax(l) over all experts
+ *   the top_k experts of largest l (ties: the lower index; NaN last),
+ *   largest first; w_k = p of the k-th, divided by their sum if norm_topk
+ *   Y[t] = residual[t] + sum_k w_k * Wd_k (silu(Wg_k x) * (Wu_k x))
+ * The logits, the softmax and the choice are computed beyond f32 accuracy,
+ * so that neighbours in rank are told apart as 64-bit arithmetic would.
+ * The products are f32-accurate (within 1e-5 of their sums of |terms|), and
+ * every expert's weights are read once per call however many tokens chose
+ * it.  Nothing depends on the order in which threads finish.
+ *   X: device f32, token t at X + t*ldx (ldx >= hidden, ldx % 4 == 0),
+ *      16-byte aligned
+ *   router: device f32 [n_experts][hidden], 16-byte aligned
+ *   wg, wu: device Q8_0 [n_experts][ffn][hidden], wd: [n_experts][hidden]
+ *      [ffn], the experts' matrices one behind the other, 16-byte aligned
+ *   residual: device f32, token t at residual + t*ldr (ldr >= hidden), or
+ *      NULL; may be Y itself (same pointer, ldr == ldy)
+ *   Y: device f32, token t at Y + t*ldy (ldy >= hidden); only the first
+ *      hidden entries of a row are written
+ *   experts, weights: device int / f32 [m][top_k], the choice made and its
+ *      weights, or NULL
+ *   workspace: device scratch of q8d_moe_workspace_bytes(m, hidden, ffn,
+ *      n_experts, top_k) bytes, 16-byte aligned; its contents need no
+ *      initialisation and belong to the call until its work on `stream` is
+ *      done (calls that may overlap, or graphs replayed at the same time,
+ *      need one each)
+ *   d_err: device int error word (OR-ed into) or NULL
+ * 0 <= m <= 64 (m == 0: no-op), hidden % 32 == 0, ffn % 32 == 0,
+ * 1 <= n_experts <= 512, 1 <= top_k <= min(n_experts, 32), hidden and ffn
+ * at most 32768; else Q8D_EUNSUPPORTED.  Outputs must not overlap inputs
+ * (but Y may be residual), the workspace or each other.
+ * ---------------------------------------------------------------------- */
+size_t q8d_moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);
+int q8d_moe_ffn(const float* X, int ldx, const float* router, const void* wg, const void* wu,
+                const void* wd, const float* residual, int ldr, float* Y, int ldy, int m,
+                int hidden, int ffn, int n_experts, int top_k, int norm_topk, int* experts,
+                float* weights, void* workspace, size_t ws_bytes, int* d_err, void* stream);
+
+/* ------------------------------------------------------------------------
  * Decode step graph ("IV.4: One command buffer per token", "One command
  * buffer": the whole step encoded once and submitted as one unit).
  * The step, per layer: RMSNorm -> q/k/v Q8_0 matvecs -> (q/k/v bias) ->

@@ -107,6 +107,11 @@ def lib():
         L.q8d_gqa_decode_attn_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
                                                   i32, i64, vp, f32, vp, vp]
         L.q8d_gqa_decode_attn_noalloc.restype = i32
+        L.q8d_moe_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.q8d_moe_workspace_bytes.restype = sz
+        L.q8d_moe_ffn.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32,
+                                  i32, vp, vp, vp, sz, vp, vp]
+        L.q8d_moe_ffn.restype = i32
         L.q8d_step_create.argtypes = [C.POINTER(StepDesc), vp, C.POINTER(vp)]
         L.q8d_step_create.restype = i32
         L.q8d_step_launch.argtypes = [vp, vp]
@@ -253,6 +258,21 @@ def q8d_gqa_decode_attn_noalloc(q, k_new, v_new, kcache, vcache, kv_dtype: int, 
         int(batch), int(n_heads), int(n_kv_heads), int(head_dim), int(cap),
         int(cache_batch_stride), _ptr(d_lens), float(scale), _ptr(d_err), _stream(stream)),
         "q8d_gqa_decode_attn_noalloc")
+
+
+def q8d_moe_workspace_bytes(m: int, hidden: int, ffn: int, n_experts: int, top_k: int) -> int:
+    return int(lib().q8d_moe_workspace_bytes(int(m), int(hidden), int(ffn), int(n_experts),
+                                             int(top_k)))
+
+
+def q8d_moe_ffn(X, ldx: int, router, wg, wu, wd, residual, ldr: int, Y, ldy: int, m: int,
+                hidden: int, ffn: int, n_experts: int, top_k: int, norm_topk: int, experts, weights,
+                workspace, ws_bytes: int, d_err, stream=None) -> int:
+    return _check(lib().q8d_moe_ffn(
+        _ptr(X), int(ldx), _ptr(router), _ptr(wg), _ptr(wu), _ptr(wd), _ptr(residual), int(ldr),
+        _ptr(Y), int(ldy), int(m), int(hidden), int(ffn), int(n_experts), int(top_k),
+        int(norm_topk), _ptr(experts), _ptr(weights), _ptr(workspace), int(ws_bytes), _ptr(d_err),
+        _stream(stream)), "q8d_moe_ffn")
 
 
 class Step:

@@ -14,6 +14,7 @@
 #include "q8d_attn.cuh"
 #include "q8d_internal.cuh"
 #include "q8d_kv_rows.cuh"
+#include "q8d_moe.cuh"
 #include "q8d_rows.cuh"
 
 namespace q8d {
@@ -469,6 +470,88 @@ int q8d_gqa_decode_attn_window(const float* q, const float* k_new, const float* 
   return attn_entry(q, k_new, v_new, kcache, vcache, kv_dtype, out, batch, n_heads, n_kv_heads,
                     head_dim, cap, cache_batch_stride, nullptr, d_runs, scale, workspace,
                     ws_bytes, d_err, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+namespace q8d {
+static bool moe_shape(int m, int hidden, int ffn, int n_experts, int top_k) {
+  return m >= 0 && m <= kMoeMaxTokens && hidden > 0 && hidden % 32 == 0 && hidden <= 32768 &&
+         ffn > 0 && ffn % 32 == 0 && ffn <= 32768 && n_experts >= 1 &&
+         n_experts <= kMoeMaxExperts && top_k >= 1 && top_k <= n_experts && top_k <= kMoeMaxTop;
+}
+}  // namespace q8d
+
+extern "C" {
+
+size_t q8d_moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k) {
+  if (!moe_shape(m, hidden, ffn, n_experts, top_k) || m == 0) return 0;
+  return moe_workspace_bytes(m, hidden, ffn, n_experts, top_k);
+}
+
+int q8d_moe_ffn(const float* X, int ldx, const float* router, const void* wg, const void* wu,
+                const void* wd, const float* residual, int ldr, float* Y, int ldy, int m,
+                int hidden, int ffn, int n_experts, int top_k, int norm_topk, int* experts,
+                float* weights, void* workspace, size_t ws_bytes, int* d_err, void* stream) {
+  if (m < 0 || hidden <= 0 || ffn <= 0 || n_experts <= 0 || top_k <= 0 || top_k > n_experts)
+    return Q8D_EINVAL;
+  if (!moe_shape(m, hidden, ffn, n_experts, top_k)) return Q8D_EUNSUPPORTED;
+  if (m == 0) return Q8D_OK;
+  if (!X || !router || !wg || !wu || !wd || !Y || !workspace) return Q8D_EINVAL;
+  if (ldx < hidden || ldy < hidden || (residual && ldr < hidden)) return Q8D_EINVAL;
+  if (!aligned(X, 16) || ldx % 4 || !aligned(router, 16) || !aligned(wg, 16) || !aligned(wu, 16) ||
+      !aligned(wd, 16) || !aligned(workspace, 16))
+    return Q8D_EALIGN;
+  if (!aligned(Y, 4) || !aligned(residual, 4) || !aligned(experts, 4) || !aligned(weights, 4) ||
+      !aligned(d_err, 4))
+    return Q8D_EALIGN;
+  const size_t need = moe_workspace_bytes(m, hidden, ffn, n_experts, top_k);
+  if (ws_bytes < need) return Q8D_EINVAL;
+  struct Span {
+    const void* p;
+    size_t n;
+  };
+  const auto rows = [&](const float* p, int ld) {
+    return Span{p, p ? 4 * ((size_t)(m - 1) * ld + hidden) : 0};
+  };
+  const size_t gb = q8_bytes((long long)n_experts * ffn, hidden);
+  const Span in[] = {rows(X, ldx),
+                     {router, 4 * (size_t)n_experts * hidden},
+                     {wg, gb},
+                     {wu, gb},
+                     {wd, q8_bytes((long long)n_experts * hidden, ffn)},
+                     rows(residual, ldr)};
+  const size_t pairs = experts ? 4 * (size_t)m * top_k : 0, wpairs = weights ? 4 * (size_t)m * top_k : 0;
+  const Span out[] = {rows(Y, ldy), {experts, pairs}, {weights, wpairs}, {workspace, need}};
+  for (const Span& o : out)
+    for (const Span& i : in)
+      if (overlap(o.p, o.n, i.p, i.n) &&
+          !(o.p == Y && i.p == residual && o.p == i.p && ldr == ldy && &i == &in[5]))
+        return Q8D_EINVAL;
+  for (int a = 0; a < 4; ++a)
+    for (int b = a + 1; b < 4; ++b)
+      if (overlap(out[a].p, out[a].n, out[b].p, out[b].n)) return Q8D_EINVAL;
+  MoeParams P{};
+  P.X = X;
+  P.ldx = ldx;
+  P.router = router;
+  P.wg = static_cast<const uint8_t*>(wg);
+  P.wu = static_cast<const uint8_t*>(wu);
+  P.wd = static_cast<const uint8_t*>(wd);
+  P.residual = residual;
+  P.ldr = ldr;
+  P.Y = Y;
+  P.ldy = ldy;
+  P.m = m;
+  P.hidden = hidden;
+  P.ffn = ffn;
+  P.n_experts = n_experts;
+  P.top_k = top_k;
+  P.norm = norm_topk != 0;
+  P.experts = experts;
+  P.weights = weights;
+  P.d_err = d_err;
+  return moe_launch(P, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,34 @@
+// Parameters of the mixture-of-experts feed-forward kernels.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace q8d {
+
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxTop = 32;
+
+struct MoeParams {
+  const float* X;  // token t at X + t * ldx
+  int ldx;
+  const float* router;  // [E][hidden]
+  const uint8_t *wg, *wu, *wd;  // Q8_0 [E][ffn][hidden] x2, [E][hidden][ffn]
+  const float* residual;  // or nullptr; token t at residual + t * ldr
+  int ldr;
+  float* Y;
+  int ldy;
+  int m, hidden, ffn, n_experts, top_k, norm;
+  int* experts;    // [m][top_k] (the caller's, or in the workspace)
+  float* weights;  // [m][top_k]
+  int* d_err;
+  // carved from the workspace
+  double* logits;  // [m][E]
+  float* h;        // [m * top_k][ffn]
+};
+
+size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);
+int moe_launch(MoeParams P, void* workspace, cudaStream_t stream);
+
+}  // namespace q8d
