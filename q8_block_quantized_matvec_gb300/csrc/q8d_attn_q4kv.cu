@@ -1,9 +1,35 @@
-// Split-K decode attention over a 4-bit KV cache (Q8D_KV_Q4): the contract
-// and the split of the other decode-attention kernels.
+// Split-K decode attention over a 4-bit KV cache (Q8D_KV_Q4) on the tensor
+// cores: the contract and the split of the other decode-attention kernels.
 //
-// One CTA per (sequence, KV head, chunk); its warps take tokens in turn with
-// their own online softmax, lane j holding element j of every block, and
-// merge once.
+// At 9/16 byte an element the arithmetic, not HBM, is what such a kernel runs
+// out of first: at the copy rate an SM gets one token of one KV head (144
+// bytes at head_dim 128) every 6 cycles, about 390 warp instructions for 16
+// tokens.  So the layout below spends nothing on moving values between lanes
+// and about five integer instructions on eight quants:
+//  * A half-byte n put under the exponent of 1024 is the f16 1024 + n (1024 +
+//    16 n for the upper one): one LOP3 a pair, and one sub.f16x2 leaves the
+//    exact n - 8 (16 (n - 8)).  (Masked out alone it would be the subnormal
+//    n * 2^-24, without a subtraction; but the tensor core aligns products by
+//    the operands' exponent fields, and a subnormal's loses it 7 bits.)
+//  * Q.K^T: rows of A are the heads' q, hi and lo f16 parts in rows g and
+//    g + 8 (so one MMA does both and they meet in one lane), columns of B
+//    eight tokens.  A block's two k-steps are scaled by the token's block
+//    scale.  Lane (g, c) ends with head g and tokens 2c,
+//    2c+1: exactly the B fragment that P.V wants.
+//  * P.V: rows of A are dims, columns of B heads, the contraction runs over
+//    tokens; ldmatrix.trans hands a lane the same two bytes of tokens 2c and
+//    2c+1.  V's scale depends on the token and the block, so it multiplies P
+//    once per block before the hi + lo split.  With at most four heads a KV
+//    head the eight columns hold hi and lo of four heads: half the MMAs.
+//  * P * scale * 2^fe stays inside f16: fe follows the largest V scale seen
+//    (a power of two, so changing it is exact).  Both fe and the running
+//    maximum move only when they must (the maximum when a score exceeds it
+//    by 2^8), so an ordinary tile does no reduction across lanes.
+//  * Eight warps, each with its own softmax over 32-token tiles and its own
+//    two-stage cp.async ring (16-byte chunks, XOR-swizzled for ldmatrix),
+//    merge once; partials are combined as in the other kernels.
+#include <cuda_fp16.h>
+
 #include "q8d_attn.cuh"
 #include "q8d_attn_common.cuh"
 #include "q8d_internal.cuh"
@@ -12,24 +38,128 @@
 namespace q8d {
 namespace {
 
-constexpr int kWarps4 = 4;
+constexpr int kWarps4 = 8;
+constexpr int kThreads4 = kWarps4 * 32;
 constexpr float kLog2e4 = 1.4426950408889634f;
+constexpr int kTile4 = 32;        // tokens a warp step
+constexpr int kStages4 = 2;
+constexpr float kSlack4 = 8.f;    // the running maximum may lag by this (log2)
+constexpr int kFe0 = 7;           // P <= 2^8, |scale| < 2^ev, 2^fe = 2^(7 - ev): products < 2^15
 
-template <int D, int GMAX>
-__global__ void __launch_bounds__(kWarps4 * 32) gqa_q4kv_kernel(const AttnParams P) {
-  constexpr int NB = D / 32;
+template <int D, int NH>
+struct Cfg4 {
+  static constexpr int kNB = D / 32;                      // blocks of a head row
+  static constexpr int kRow = D / 2;                      // quant bytes of a head row
+  static constexpr int kSRow = D / 16;                    // scale bytes of a head row
+  static constexpr int kQuants = kTile4 * kRow;
+  static constexpr int kScales = kTile4 * kSRow;
+  static constexpr int kStage = 2 * (kQuants + kScales);  // K, V quants, K, V scales
+  static constexpr int kOffQf = kWarps4 * kStages4 * kStage;      // A fragments of q
+  static constexpr int kQf = NH * (D / 16) * 32 * 16;
+  static constexpr int kOffQs = kOffQf + kQf;             // f32 q [8 NH][D], power-of-two scaled
+  static constexpr int kOffF = kOffQs + 8 * NH * D * 4;   // score factors [8 NH]
+  static constexpr int kSmem = kOffF + 8 * NH * 4;
+  static_assert(kWarps4 * 8 * NH * (D + 2) * 4 <= kOffQf + kQf, "merge buffer fits");
+};
+
+template <int N>
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
+  const int n = live ? N : 0;  // (0: the destination is filled with zeros)
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                     uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// n - 8 of the low half-bytes n of bytes 0 and 2 of w as an exact f16 pair
+// (kHi: 16 (n - 8) of the high half-bytes).
+template <bool kHi>
+__device__ __forceinline__ uint32_t nib8(uint32_t w) {
+  const uint32_t x = (w & (kHi ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(kHi ? 0x64806480u : 0x64086408u));
+  return r;
+}
+__device__ __forceinline__ float2 h2f(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t f2h(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// This CTA's sequence and chunk, worked out by every warp with a sequence a
+// lane (attn_chunk_of walks the batch in one thread).
+__device__ __forceinline__ bool chunk_of_warp(const AttnParams& P, int k, int lane, int& b, int& c,
+                                              int& n, int& L) {
+  long long total = attn_total_rows_warp(P, lane);
+  int first = 0;
+  for (int s0 = 0; s0 < P.batch; s0 += 32) {
+    const int s = s0 + lane;
+    const int len = s < P.batch ? attn_window_len(P, s) : 0;
+    const int ns = s < P.batch ? attn_nchunks(P, len, total) : 0;
+    int end = ns;  // inclusive prefix sum
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, k < first + end && s < P.batch);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      b = s0 + at;
+      n = __shfl_sync(0xffffffffu, ns, at);
+      c = k - first - (__shfl_sync(0xffffffffu, end, at) - n);
+      L = __shfl_sync(0xffffffffu, len, at);
+      return true;
+    }
+    first += __shfl_sync(0xffffffffu, end, 31);
+  }
+  return false;
+}
+
+// NH: tiles of eight heads (1 or 2).  kPack: at most four heads, hi and lo
+// parts of P side by side in one tile.
+template <int D, int NH, bool kPack>
+__global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(const AttnParams P) {
+  using C = Cfg4<D, NH>;
+  constexpr int NB = C::kNB;
+  constexpr int KS = D / 16;
+  constexpr int NT = kTile4 / 8;  // 8-token columns of a tile
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
+  float* fh = reinterpret_cast<float*>(smem + C::kOffF);
   __shared__ AttnWindow s_win;
-  __shared__ float sm[kWarps4][GMAX], sl[kWarps4][GMAX];
-  __shared__ float so[kWarps4][GMAX][D];
+
   const int g = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gq = lane >> 2, cq = lane & 3;
   const int G = P.n_heads / P.n_kv_heads;
-  griddep_launch_dependents();
-  griddep_wait();
-  int b, c, n;
-  if (!attn_chunk_of(P, blockIdx.x, b, c, n)) return;
-  const int L = attn_window_len(P, b);
-  if (L < 1) {
+  griddep_launch_dependents();  // the combine may be scheduled now
+  griddep_wait();               // (a programmatic dependent: the previous work is complete)
+  int b, c, n, L;
+  if (!chunk_of_warp(P, blockIdx.x, lane, b, c, n, L)) return;
+  if (L < 1) {  // (the combine writes NaN outputs)
     if (g == 0 && tid == 0 && P.d_err) atomicOr(P.d_err, Q8D_DERR_LEN_RANGE);
     return;
   }
@@ -37,80 +167,364 @@ __global__ void __launch_bounds__(kWarps4 * 32) gqa_q4kv_kernel(const AttnParams
   const int t_begin = c * tpc;
   if (t_begin >= L) return;
   const int t_end = min(L, t_begin + tpc);
-  if (tid == 0) attn_window_store(P, b, &s_win);
   const int width = P.n_kv_heads * D;
   const long long seq_off = (long long)b * (P.batch_stride / kQBlock) * 18;
   const long long splane = q4_scale_plane(P.cap, width);
-  uint8_t* kq = static_cast<uint8_t*>(P.kcache) + seq_off + g * (D / 2);
-  uint8_t* vq = static_cast<uint8_t*>(P.vcache) + seq_off + g * (D / 2);
-  uint8_t* ks = static_cast<uint8_t*>(P.kcache) + seq_off + splane + g * (D / 16);
-  uint8_t* vs = static_cast<uint8_t*>(P.vcache) + seq_off + splane + g * (D / 16);
+  const uint32_t rowq = (uint32_t)width / 2, rows = (uint32_t)width / 16;  // bytes a row
+  uint8_t* kq = static_cast<uint8_t*>(P.kcache) + seq_off + g * C::kRow;
+  uint8_t* vq = static_cast<uint8_t*>(P.vcache) + seq_off + g * C::kRow;
+  uint8_t* ks = static_cast<uint8_t*>(P.kcache) + seq_off + splane + g * C::kSRow;
+  uint8_t* vs = static_cast<uint8_t*>(P.vcache) + seq_off + splane + g * C::kSRow;
+  if (tid == 0) attn_window_store(P, b, &s_win);
+
+  // In-kernel append of row L-1 by the CTA that owns it; read back below.
   if (P.k_new != nullptr && t_end == L && warp < 2) {
     const float* src = (warp ? P.v_new : P.k_new) + (long long)b * width + (long long)g * D;
     const long long row = attn_cell(P, b, L - 1);
-    for (int t = 0; t < NB; ++t)
-      quantize_q4_warp(src[lane + 32 * t], (warp ? vq : kq) + row * (width / 2) + 16 * t,
-                       (warp ? vs : ks) + row * (width / 16) + 2 * t, lane);
-  }
-  __syncthreads();
-  float q[GMAX][NB], o[GMAX][NB], m[GMAX], l[GMAX];
 #pragma unroll
-  for (int h = 0; h < GMAX; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
+    for (int t = 0; t < NB; ++t)
+      quantize_q4_warp(src[lane + 32 * t], (warp ? vq : kq) + row * rowq + 16 * t,
+                       (warp ? vs : ks) + row * rows + 2 * t, lane);
+  }
+  __syncthreads();  // the window and the appended row
+
+  // ---- this warp's ring over its tiles (tile i: tokens t_begin + 32 (warp + 8 i)) ----
+  const int run0_len = s_win.len[0], run0_cell = s_win.cell[0];
+  const int ntiles = (t_end - t_begin + kTile4 - 1) / kTile4;
+  const int my_tiles = ntiles > warp ? (ntiles - warp + kWarps4 - 1) / kWarps4 : 0;
+  const uint32_t ring = smem_u32(smem) + warp * kStages4 * C::kStage;
+  constexpr int kCh = C::kRow / 16;          // 16-byte chunks of a head row
+  constexpr int kRowsPass = 32 / kCh;        // rows the lanes copy at once
+  const int ld_r = lane / kCh, ld_c = lane % kCh;
+  // (the swizzle repeats every 8 rows: it does not depend on the pass)
+  constexpr int kSwz = D == 128 ? 1 : 2;
+  const uint32_t ld_dst = ld_r * C::kRow + ((ld_c ^ ((ld_r >> kSwz) & (kCh - 1))) << 4);
+  auto load_tile = [&](int i) {
+    if (i < my_tiles) {
+      const int t0 = t_begin + (warp + kWarps4 * i) * kTile4;
+      const int nr = min(kTile4, t_end - t0);
+      const uint32_t st = ring + (i % kStages4) * C::kStage;
+      if (nr == kTile4 && t0 + kTile4 <= run0_len) {
+        const long long row = run0_cell + t0 + ld_r;
+        const uint8_t* kp = kq + row * rowq + ld_c * 16;
+        const uint8_t* vp = vq + row * rowq + ld_c * 16;
+#pragma unroll
+        for (int k = 0; k < kTile4 / kRowsPass; ++k) {
+          cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kp + k * kRowsPass * rowq, true);
+          cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vp + k * kRowsPass * rowq, true);
+        }
+        const long long sr = run0_cell + t0 + lane;
+        cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + sr * rows, true);
+        cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + sr * rows, true);
+      } else {
+        // rows past the chunk become zeros: scale 0, so they add nothing
+        for (int k = 0; k < kTile4 / kRowsPass; ++k) {
+          const int r = k * kRowsPass + ld_r;
+          const bool live = r < nr;
+          const long long off = (long long)s_win.cell_of(t0 + (live ? r : 0)) * rowq + ld_c * 16;
+          cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kq + off, live);
+          cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vq + off, live);
+        }
+        const bool live = lane < nr;
+        const long long off = (long long)s_win.cell_of(t0 + (live ? lane : 0)) * rows;
+        cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + off, live);
+        cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + off, live);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");  // (possibly empty: a uniform count)
+  };
+#pragma unroll
+  for (int i = 0; i < kStages4 - 1; ++i) load_tile(i);
+
+  // ---- q: rows scaled by 2^sh into [2^14, 2^15), score factors ----
+#pragma unroll
+  for (int u = 0; u < NH; ++u) {
+    const int hh = warp + 8 * u;                       // fragment row
+    const int head = kPack ? hh & 3 : hh;              // (packed: heads 0-3 twice)
+    float v[NB];
+    float mx = 0.f;
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
-      q[h][t] = h < G ? P.q[((long long)b * P.n_heads + g * G + h) * D + lane + 32 * t] *
-                            (P.scale * kLog2e4)
-                      : 0.f;
-      o[h][t] = 0.f;
-    }
-  }
-  for (int t = t_begin + warp; t < t_end; t += kWarps4) {
-    const long long row = s_win.cell_of(t);
-    float k[NB], v[NB];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int sh = lane & 16 ? 4 : 0;
-      const uint32_t nk = kq[row * (width / 2) + 16 * i + (lane & 15)] >> sh & 15u;
-      const uint32_t nv = vq[row * (width / 2) + 16 * i + (lane & 15)] >> sh & 15u;
-      k[i] = ((float)nk - 8.f) *
-             f16_bits_to_f32(*reinterpret_cast<unsigned short*>(ks + row * (width / 16) + 2 * i));
-      v[i] = ((float)nv - 8.f) *
-             f16_bits_to_f32(*reinterpret_cast<unsigned short*>(vs + row * (width / 16) + 2 * i));
+      v[t] = head < G ? P.q[((long long)b * P.n_heads + g * G + head) * D + lane + 32 * t] : 0.f;
+      mx = fmaxf(mx, fabsf(v[t]));
     }
 #pragma unroll
-    for (int h = 0; h < GMAX; ++h) {
-      if (h >= G) break;
-      float s = 0.f;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    int e = 0;
+    if (mx > 0.f) frexpf(mx, &e);
+    const int sh = mx > 0.f ? 15 - e : 0;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) s = fmaf(q[h][i], k[i], s);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      const float mn = fmaxf(m[h], s);
-      const float r = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn), p = exp2f(s - mn);
-      l[h] = l[h] * r + p;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) o[h][i] = fmaf(o[h][i], r, p * v[i]);
-      m[h] = mn;
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < GMAX; ++h) {
-    if (lane == 0) sm[warp][h] = m[h], sl[warp][h] = l[h];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) so[warp][h][lane + 32 * i] = o[h][i];
+    for (int t = 0; t < NB; ++t) qs[hh * D + lane + 32 * t] = ldexpf(v[t], sh);
+    if (lane == 0) fh[hh] = head < G ? ldexpf(P.scale * kLog2e4, -sh) : 0.f;
   }
   __syncthreads();
-  for (int e = tid; e < G * D; e += kWarps4 * 32) {
+  // A fragments: lane (g, c) of k-step kk = 2 blk + half holds dims 32 blk + 16
+  // half + 4c + {0, 2} (k slots 2c, 2c+1) and + {1, 3} (slots 2c+8, 2c+9), hi
+  // in row g, lo in row g + 8; the upper half-bytes count 16-fold, so theirs
+  // are divided by 16.
+  uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQf);
+  for (int i = tid; i < NH * KS * 32; i += kThreads4) {
+    const int ln = i & 31, kk = (i >> 5) % KS, ht = i / (32 * KS);
+    const float* q = qs + (ht * 8 + (ln >> 2)) * D + 16 * kk + 4 * (ln & 3);
+    const float f = kk & 1 ? 0.0625f : 1.f;
+    uint4 a;
+    attn_split2(q[0] * f, q[2] * f, a.x, a.y);
+    attn_split2(q[1] * f, q[3] * f, a.z, a.w);
+    qf[i] = a;
+  }
+  __syncthreads();
+  float fac[NH];
+#pragma unroll
+  for (int u = 0; u < NH; ++u) fac[u] = fh[u * 8 + gq];
+
+  // o[u][2 blk + half]: dims 32 blk + 16 half + 2 gq + {0 (rows g), 1 (rows g + 8)}, columns 2cq, 2cq+1
+  float o[NH][2 * NB][4];
+  float m[NH], l[NH];
+#pragma unroll
+  for (int u = 0; u < NH; ++u) {
+    m[u] = -INFINITY;
+    l[u] = 0.f;
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t) o[u][t][0] = o[u][t][1] = o[u][t][2] = o[u][t][3] = 0.f;
+  }
+  int lim = -1;       // exponent field of the largest V scale allowed for (-1: none yet)
+  float F = 0.f;      // 2^fe
+  const float lo_part = kPack && gq >= 4 ? -1.f : 0.f;
+
+  const uint4* qfl = qf + lane;
+  // ldmatrix row addresses.  K (x4): 8 tokens, blocks 0-3 (head_dim 64: 8
+  // tokens each of two columns, blocks 0-1); V (x4, transposed): tokens 0-7
+  // and 8-15 of block 2 i, then of block 2 i + 1.
+  const int mi = lane >> 3, mr = lane & 7;
+  const uint32_t k_row = D == 128 ? mr : (mi >> 1) * 8 + mr, k_blk = D == 128 ? mi : mi & 1;
+  const uint32_t k_off = k_row * C::kRow + ((k_blk ^ ((k_row >> kSwz) & (kCh - 1))) << 4);
+  const uint32_t v_row = (mi & 1) * 8 + mr;
+  uint32_t v_off[NB / 2];
+#pragma unroll
+  for (int i = 0; i < NB / 2; ++i)
+    v_off[i] = C::kQuants + v_row * C::kRow + (((2 * i + (mi >> 1)) ^ ((v_row >> kSwz) & (kCh - 1))) << 4);
+
+  for (int i = 0; i < my_tiles; ++i) {
+    load_tile(i + kStages4 - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages4 - 1) : "memory");
+    __syncwarp();
+    const int nr = min(kTile4, t_end - (t_begin + (warp + kWarps4 * i) * kTile4));
+    const uint32_t st = ring + (i % kStages4) * C::kStage;
+    const uint8_t* stp = smem + (st - smem_u32(smem));
+
+    // ---- S = Q.K^T ----
+    uint32_t kw[NT][NB];
+    if constexpr (D == 128) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) ldsm4(st + k_off + j * 8 * C::kRow, kw[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; j += 2) {
+        uint32_t r[4];
+        ldsm4(st + k_off + j * 8 * C::kRow, r);
+        kw[j][0] = r[0];
+        kw[j][1] = r[1];
+        kw[j + 1][0] = r[2];
+        kw[j + 1][1] = r[3];
+      }
+    }
+    // the scales of this lane's tokens 8j + 2cq, + 1: NB halves each
+    uint64_t s2[NH][NT];
+#pragma unroll
+    for (int u = 0; u < NH; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) s2[u][j] = pack2(0.f, 0.f);
+    const uint8_t* ksc = stp + 2 * C::kQuants + 2 * cq * C::kSRow;
+#pragma unroll
+    for (int bb = 0; bb < NB; ++bb) {
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        const uint4 a0 = qfl[(u * KS + 2 * bb) * 32], a1 = qfl[(u * KS + 2 * bb + 1) * 32];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint32_t w = kw[j][bb], w8 = w >> 8;
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma4(acc, a0.x, a0.y, a0.z, a0.w, nib8<false>(w), nib8<false>(w8));
+          mma4(acc, a1.x, a1.y, a1.z, a1.w, nib8<true>(w), nib8<true>(w8));
+          const unsigned short* sp = reinterpret_cast<const unsigned short*>(ksc + j * 8 * C::kSRow) + bb;
+          const uint64_t d2 = pack2(f16_bits_to_f32(sp[0]), f16_bits_to_f32(sp[C::kSRow / 2]));
+          s2[u][j] = fma2(d2, add2(pack2(acc[0], acc[1]), pack2(acc[2], acc[3])), s2[u][j]);
+        }
+      }
+    }
+
+    // ---- log2-domain scores and the running maximum ----
+    float s[NH][NT][2];
+    bool above = false;
+#pragma unroll
+    for (int u = 0; u < NH; ++u) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        unpack2(s2[u][j], s[u][j][0], s[u][j][1]);
+        s[u][j][0] *= fac[u];
+        s[u][j][1] *= fac[u];
+        if (nr < kTile4) {
+          if (8 * j + 2 * cq >= nr) s[u][j][0] = -INFINITY;
+          if (8 * j + 2 * cq + 1 >= nr) s[u][j][1] = -INFINITY;
+        }
+        mx = fmaxf(mx, fmaxf(s[u][j][0], s[u][j][1]));
+      }
+      above = above || mx > m[u] + kSlack4;
+    }
+    // the V scales of this lane's tokens and their largest exponent
+    uint32_t vsc[NT][NB];  // per 8 tokens: two tokens' NB halves
+    __half2 vm = __float2half2_rn(0.f);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint8_t* p = stp + 2 * C::kQuants + C::kScales + (8 * j + 2 * cq) * C::kSRow;
+      if constexpr (D == 128) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        vsc[j][0] = w.x;
+        vsc[j][1] = w.y;
+        vsc[j][2] = w.z;
+        vsc[j][3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        vsc[j][0] = w.x;
+        vsc[j][1] = w.y;
+      }
+#pragma unroll
+      for (int t = 0; t < NB; ++t) vm = __hmax2(vm, __habs2(*reinterpret_cast<const __half2*>(&vsc[j][t])));
+    }
+    const uint32_t vmb = *reinterpret_cast<const uint32_t*>(&vm);
+    int ve = (int)(max(vmb & 0xffffu, vmb >> 16) >> 10);
+    if (__any_sync(0xffffffffu, above || ve > lim)) {  // (rare after the first tiles)
+#pragma unroll
+      for (int of = 1; of < 32; of <<= 1) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, of));
+      float r = 1.f;
+      if (ve > lim) {
+        const float Fn = __int_as_float((127 + kFe0 + 14 - max(ve, 1)) << 23);  // |scale| < 2^(field - 14)
+        r = lim < 0 ? 0.f : Fn / F;
+        F = Fn;
+        lim = ve;
+      }
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[u][j][0], s[u][j][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[u], mx);
+        const float cf = m[u] == -INFINITY ? 0.f : exp2f(m[u] - mn);
+        m[u] = mn;
+        l[u] *= cf;
+        const float cr = cf * r;
+        const float c0 = __shfl_sync(0xffffffffu, cr, 8 * cq), c1 = __shfl_sync(0xffffffffu, cr, 8 * cq + 4);
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t) {
+          o[u][t][0] *= c0;
+          o[u][t][1] *= c1;
+          o[u][t][2] *= c0;
+          o[u][t][3] *= c1;
+        }
+      }
+    }
+
+    // ---- P, then O += (P * scale) . V per block ----
+#pragma unroll
+    for (int h = 0; h < NT / 2; ++h) {  // 16 tokens
+      uint64_t p2[NH][2];
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float pa = exp2f(s[u][2 * h + j][0] - m[u]), pb = exp2f(s[u][2 * h + j][1] - m[u]);
+          l[u] += pa + pb;
+          p2[u][j] = mul2(pack2(pa, pb), pack2(F, F));
+        }
+#pragma unroll
+      for (int bp = 0; bp < NB / 2; ++bp) {
+        uint32_t vw[4];
+        ldsm4t(st + v_off[bp] + h * 16 * C::kRow, vw);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int bb = 2 * bp + x;
+          const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1], w0s = w0 >> 8, w1s = w1 >> 8;
+          const uint32_t l0 = nib8<false>(w0), l1 = nib8<false>(w0s), l2 = nib8<false>(w1), l3 = nib8<false>(w1s);
+          const uint32_t u0 = nib8<true>(w0), u1 = nib8<true>(w0s), u2 = nib8<true>(w1), u3 = nib8<true>(w1s);
+#pragma unroll
+          for (int u = 0; u < NH; ++u) {
+            uint32_t ph[2], pl[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // halves bb of the two tokens' scales
+              const uint32_t wa = vsc[2 * h + j][bb / 2], wb = vsc[2 * h + j][NB / 2 + bb / 2];
+              const float2 fa = h2f(wa), fb = h2f(wb);
+              const uint64_t pd = mul2(p2[u][j], bb & 1 ? pack2(fa.y, fb.y) : pack2(fa.x, fb.x));
+              float a, d;
+              unpack2(pd, a, d);
+              ph[j] = f2h(a, d);
+              const float2 hf = h2f(ph[j]);
+              if constexpr (kPack) {
+                ph[j] = f2h(fmaf(hf.x, lo_part, a), fmaf(hf.y, lo_part, d));
+              } else {
+                pl[j] = f2h(a - hf.x, d - hf.y);
+              }
+            }
+            mma4(o[u][2 * bb], l0, l1, l2, l3, ph[0], ph[1]);
+            mma4(o[u][2 * bb + 1], u0, u1, u2, u3, ph[0], ph[1]);
+            if constexpr (!kPack) {
+              mma4(o[u][2 * bb], l0, l1, l2, l3, pl[0], pl[1]);
+              mma4(o[u][2 * bb + 1], u0, u1, u2, u3, pl[0], pl[1]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage is rewritten next
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+  // ---- merge the warps' {m, l, O}; write the chunk's partial ----
+  __syncthreads();
+  float* mm = reinterpret_cast<float*>(smem);
+  float* ll = mm + kWarps4 * 8 * NH;
+  float* oo = ll + kWarps4 * 8 * NH;
+  const float inv_f = lim < 0 ? 0.f : 1.f / F;
+#pragma unroll
+  for (int u = 0; u < NH; ++u) {
+    float sum = l[u];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (cq == 0) {
+      mm[warp * 8 * NH + 8 * u + gq] = m[u];
+      ll[warp * 8 * NH + 8 * u + gq] = sum;
+    }
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float sc = (h ? 0.0625f : 1.f) * inv_f;  // (upper half-bytes count 16-fold)
+        const int d0 = 32 * t + 16 * h + 2 * gq;
+        float* r0 = oo + (size_t)(warp * 8 * NH + 8 * u + 2 * cq) * D + d0;
+        *reinterpret_cast<float2*>(r0) = make_float2(o[u][2 * t + h][0] * sc, o[u][2 * t + h][2] * sc);
+        *reinterpret_cast<float2*>(r0 + D) = make_float2(o[u][2 * t + h][1] * sc, o[u][2 * t + h][3] * sc);
+      }
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < G * D; e += kThreads4) {
     const int h = e / D, j = e % D;
-    float M = -INFINITY, acc = 0.f, lsum = 0.f;
-    for (int w = 0; w < kWarps4; ++w) M = fmaxf(M, sm[w][h]);
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps4; ++w) M = fmaxf(M, mm[w * 8 * NH + h]);
+    float acc = 0.f, lsum = 0.f;
+#pragma unroll
     for (int w = 0; w < kWarps4; ++w) {
-      if (sm[w][h] == -INFINITY) continue;
-      const float wgt = exp2f(sm[w][h] - M);
-      acc = fmaf(so[w][h][j], wgt, acc);
-      lsum = fmaf(sl[w][h], wgt, lsum);
+      const float mw = mm[w * 8 * NH + h];
+      if (mw == -INFINITY) continue;
+      const float wgt = exp2f(mw - M);
+      float x = oo[(size_t)(w * 8 * NH + h) * D + j];
+      if constexpr (kPack) x += oo[(size_t)(w * 8 * NH + h + 4) * D + j];
+      acc = fmaf(x, wgt, acc);
+      lsum = fmaf(ll[w * 8 * NH + h], wgt, lsum);
     }
     const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
     P.ws_o[(hq * P.nc + c) * D + j] = acc;
@@ -121,20 +535,28 @@ __global__ void __launch_bounds__(kWarps4 * 32) gqa_q4kv_kernel(const AttnParams
   }
 }
 
-template <int D, int GMAX>
+template <int D, int NH, bool kPack>
 int launch_q4kv(const AttnParams& P, cudaStream_t stream) {
-  const int rc = launch_ex(gqa_q4kv_kernel<D, GMAX>, dim3(P.nct, P.n_kv_heads), dim3(kWarps4 * 32),
-                           0, stream, true, P);
+  using C = Cfg4<D, NH>;
+  const auto fn = gqa_q4kv_kernel<D, NH, kPack>;
+  int rc = configure_kernel(reinterpret_cast<const void*>(fn), C::kSmem, true);
+  if (rc) return rc;
+  rc = launch_ex(fn, dim3(P.nct, P.n_kv_heads), dim3(kThreads4), (size_t)C::kSmem, stream, true, P);
   return rc ? rc : attn_combine_launch(P, stream);
+}
+
+template <int D>
+int launch_q4kv_g(const AttnParams& P, cudaStream_t stream) {
+  const int G = P.n_heads / P.n_kv_heads;
+  if (G <= 4) return launch_q4kv<D, 1, true>(P, stream);
+  if (G <= 8) return launch_q4kv<D, 1, false>(P, stream);
+  return launch_q4kv<D, 2, false>(P, stream);
 }
 
 }  // namespace
 
 int attn_q4kv_launch(const AttnParams& P, cudaStream_t stream) {
-  const bool small = P.n_heads / P.n_kv_heads <= 8;
-  if (P.head_dim == 128)
-    return small ? launch_q4kv<128, 8>(P, stream) : launch_q4kv<128, 16>(P, stream);
-  return small ? launch_q4kv<64, 8>(P, stream) : launch_q4kv<64, 16>(P, stream);
+  return P.head_dim == 128 ? launch_q4kv_g<128>(P, stream) : launch_q4kv_g<64>(P, stream);
 }
 
 }  // namespace q8d
