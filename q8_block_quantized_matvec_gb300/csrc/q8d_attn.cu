@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kCombGroups * D) gqa_combine_kernel(const Attn
     return;
   }
   // the kernels' split of this sequence (chunks past the rows are unused)
-  const int n = attn_nchunks(P, L, attn_total_rows_warp(P, threadIdx.x & 31));
+  const int n = attn_nchunks(P, L, attn_total_rows(P));
   const int tpc = (L + n - 1) / n;
   const int nact = (L + tpc - 1) / tpc;
   const float* M = P.ws_m + (long long)hq * P.nc;

@@ -128,18 +128,6 @@ __device__ __forceinline__ long long attn_total_rows(const AttnParams& P) {
   return t;
 }
 
-// The same sum by a whole warp (every lane calls and gets it): a sequence a
-// lane, so that a large batch's windows are read side by side.
-__device__ __forceinline__ long long attn_total_rows_warp(const AttnParams& P, int lane) {
-  long long t = 0;
-  for (int s = lane; s < P.batch; s += 32) {
-    const int L = attn_window_len(P, s);
-    if (L >= 1) t += L;
-  }
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
-}
-
 // Chunks of a sequence attending L rows (1 for an invalid window, L < 1).
 __device__ __forceinline__ int attn_nchunks(const AttnParams& P, int L, long long total) {
   if (L < 1 || total <= 0) return 1;

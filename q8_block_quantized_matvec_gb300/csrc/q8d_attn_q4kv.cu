@@ -30,6 +30,8 @@
 //    merge once; partials are combined as in the other kernels.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "q8d_attn.cuh"
 #include "q8d_attn_common.cuh"
 #include "q8d_internal.cuh"
@@ -44,6 +46,7 @@ constexpr float kLog2e4 = 1.4426950408889634f;
 constexpr int kTile4 = 32;        // tokens a warp step
 constexpr int kStages4 = 2;
 constexpr float kSlack4 = 8.f;    // the running maximum may lag by this (log2)
+constexpr int kSeqCtas4 = 4;
 constexpr int kFe0 = 7;           // P <= 2^8, |scale| < 2^ev, 2^fe = 2^(7 - ev): products < 2^15
 
 template <int D, int NH>
@@ -57,7 +60,7 @@ struct Cfg4 {
   static constexpr int kOffQf = kWarps4 * kStages4 * kStage;      // A fragments of q
   static constexpr int kQf = NH * (D / 16) * 32 * 16;
   static constexpr int kOffQs = kOffQf + kQf;             // f32 q [8 NH][D], power-of-two scaled
-  static constexpr int kOffF = kOffQs + 8 * NH * D * 4;   // score factors [8 NH]
+  static constexpr int kOffF = kOffQs + 8 * NH * D * 4;   // score factors 2^-sh [8 NH]
   static constexpr int kSmem = kOffF + 8 * NH * 4;
   static_assert(kWarps4 * 8 * NH * (D + 2) * 4 <= kOffQf + kQf, "merge buffer fits");
 };
@@ -91,11 +94,49 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same from zero.
+__device__ __forceinline__ void mma4z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                      uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 2^x to two units in the last place; results below 2^-126 are 0 (a weight
+// that small next to 1 is beyond every sum's accuracy).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The larger magnitudes of two f16 pairs (signs mixed).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The NB halves of each of two neighbouring tokens' scales.
+template <int NB>
+__device__ __forceinline__ void scales2(const uint8_t* p, uint32_t (&w)[NB]) {
+  if constexpr (NB == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
 // n - 8 of the low half-bytes n of bytes 0 and 2 of w as an exact f16 pair
 // (kHi: 16 (n - 8) of the high half-bytes).
 template <bool kHi>
-__device__ __forceinline__ uint32_t nib8(uint32_t w) {
-  const uint32_t x = (w & (kHi ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+__device__ __forceinline__ uint32_t nib8(uint32_t w, uint32_t k1024) {
+  uint32_t x;  // (w & mask) | k1024: one LOP3 while k1024 is a register
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "n"(kHi ? 0x00f000f0 : 0x000f000f), "r"(k1024));
   uint32_t r;
   asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(kHi ? 0x64806480u : 0x64086408u));
   return r;
@@ -103,21 +144,60 @@ __device__ __forceinline__ uint32_t nib8(uint32_t w) {
 __device__ __forceinline__ float2 h2f(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
+// Half bb of both tokens of scales2, as an f32 pair.
+template <int NB>
+__device__ __forceinline__ uint64_t scale_pair(const uint32_t (&w)[NB], int bb) {
+  const float2 a = h2f(w[bb / 2]), b = h2f(w[NB / 2 + bb / 2]);
+  return bb & 1 ? pack2(a.y, b.y) : pack2(a.x, b.x);
+}
 __device__ __forceinline__ uint32_t f2h(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// This CTA's sequence and chunk, worked out by every warp with a sequence a
-// lane (attn_chunk_of walks the batch in one thread).
+// ---- the split: q8d_attn.cuh's rule in f32 steps, a sequence a lane ----
+// (There one thread walks the batch with 64-bit divisions: 32 sequences cost
+// it more than a tile of attention.)
+__device__ __forceinline__ int window_len4(const AttnParams& P, int b) {
+  if (!P.d_runs) {
+    const int L = __ldcg(P.d_lens + b);
+    return (L >= 1 && L <= P.cap) ? L : -1;
+  }
+  return attn_window_len(P, b);
+}
+// (nct - batch) / (the batch's rows), a shade less than exact so that the
+// chunks never outnumber the CTAs: the f32 sum and products are off by under
+// 2^-20.  Every lane of a warp calls.
+__device__ __forceinline__ float chunk_rate4(const AttnParams& P, int lane) {
+  if (P.batch == 1) return 0.f;
+  float t = 0.f;
+  for (int s = lane; s < P.batch; s += 32) t += (float)max(window_len4(P, s), 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t > 0.f ? 0.99999f * (float)(P.nct - P.batch) / t : 0.f;
+}
+__device__ __forceinline__ int nchunks4(const AttnParams& P, int L, float rate) {
+  int n = P.batch == 1 ? P.nct : 1 + (int)(rate * (float)L);
+  n = min(n, min((L + kMinChunk - 1) / kMinChunk, P.nc));
+  return max(n, 1);
+}
+
+// This CTA's sequence, chunk (of n) and the sequence's rows.
 __device__ __forceinline__ bool chunk_of_warp(const AttnParams& P, int k, int lane, int& b, int& c,
                                               int& n, int& L) {
-  long long total = attn_total_rows_warp(P, lane);
+  if (P.batch == 1) {
+    b = 0;
+    c = k;
+    L = window_len4(P, 0);
+    n = nchunks4(P, L, 0.f);
+    return k < n;
+  }
+  const float rate = chunk_rate4(P, lane);
   int first = 0;
   for (int s0 = 0; s0 < P.batch; s0 += 32) {
     const int s = s0 + lane;
-    const int len = s < P.batch ? attn_window_len(P, s) : 0;
-    const int ns = s < P.batch ? attn_nchunks(P, len, total) : 0;
+    const int len = s < P.batch ? window_len4(P, s) : 0;
+    const int ns = s < P.batch ? nchunks4(P, len, rate) : 0;
     int end = ns;  // inclusive prefix sum
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -155,8 +235,10 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, cq = lane & 3;
   const int G = P.n_heads / P.n_kv_heads;
-  griddep_launch_dependents();  // the combine may be scheduled now
-  griddep_wait();               // (a programmatic dependent: the previous work is complete)
+  griddep_wait();  // (a programmatic dependent: the previous work is complete)
+  // after the wait: the combine, scheduled from here on, may read the lengths
+  // before this grid is done
+  griddep_launch_dependents();
   int b, c, n, L;
   if (!chunk_of_warp(P, blockIdx.x, lane, b, c, n, L)) return;
   if (L < 1) {  // (the combine writes NaN outputs)
@@ -175,7 +257,6 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   uint8_t* vq = static_cast<uint8_t*>(P.vcache) + seq_off + g * C::kRow;
   uint8_t* ks = static_cast<uint8_t*>(P.kcache) + seq_off + splane + g * C::kSRow;
   uint8_t* vs = static_cast<uint8_t*>(P.vcache) + seq_off + splane + g * C::kSRow;
-  if (tid == 0) attn_window_store(P, b, &s_win);
 
   // In-kernel append of row L-1 by the CTA that owns it; read back below.
   if (P.k_new != nullptr && t_end == L && warp < 2) {
@@ -186,10 +267,20 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
       quantize_q4_warp(src[lane + 32 * t], (warp ? vq : kq) + row * rowq + 16 * t,
                        (warp ? vs : ks) + row * rows + 2 * t, lane);
   }
-  __syncthreads();  // the window and the appended row
+  // a causal window is the one run (0, L): only run maps and the appended row
+  // need the CTA's threads to meet here
+  int run0_len = L, run0_cell = 0;
+  if (P.d_runs) {
+    if (tid == 0) attn_window_store(P, b, &s_win);
+    __syncthreads();
+    run0_len = s_win.len[0];
+    run0_cell = s_win.cell[0];
+  } else if (P.k_new != nullptr && t_end == L) {
+    __syncthreads();
+  }
+  const auto cell_of = [&](int t) { return t < run0_len ? run0_cell + t : s_win.cell_of(t); };
 
   // ---- this warp's ring over its tiles (tile i: tokens t_begin + 32 (warp + 8 i)) ----
-  const int run0_len = s_win.len[0], run0_cell = s_win.cell[0];
   const int ntiles = (t_end - t_begin + kTile4 - 1) / kTile4;
   const int my_tiles = ntiles > warp ? (ntiles - warp + kWarps4 - 1) / kWarps4 : 0;
   const uint32_t ring = smem_u32(smem) + warp * kStages4 * C::kStage;
@@ -221,12 +312,12 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         for (int k = 0; k < kTile4 / kRowsPass; ++k) {
           const int r = k * kRowsPass + ld_r;
           const bool live = r < nr;
-          const long long off = (long long)s_win.cell_of(t0 + (live ? r : 0)) * rowq + ld_c * 16;
+          const long long off = (long long)cell_of(t0 + (live ? r : 0)) * rowq + ld_c * 16;
           cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kq + off, live);
           cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vq + off, live);
         }
         const bool live = lane < nr;
-        const long long off = (long long)s_win.cell_of(t0 + (live ? lane : 0)) * rows;
+        const long long off = (long long)cell_of(t0 + (live ? lane : 0)) * rows;
         cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + off, live);
         cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + off, live);
       }
@@ -236,7 +327,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 #pragma unroll
   for (int i = 0; i < kStages4 - 1; ++i) load_tile(i);
 
-  // ---- q: rows scaled by 2^sh into [2^14, 2^15), score factors ----
+  // ---- q * scale * log2(e), rows times 2^sh into [2^14, 2^15), 2^-sh ----
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
     const int hh = warp + 8 * u;                       // fragment row
@@ -245,17 +336,18 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
     float mx = 0.f;
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
-      v[t] = head < G ? P.q[((long long)b * P.n_heads + g * G + head) * D + lane + 32 * t] : 0.f;
+      v[t] = head < G ? P.q[((long long)b * P.n_heads + g * G + head) * D + lane + 32 * t] * (P.scale * kLog2e4) : 0.f;
       mx = fmaxf(mx, fabsf(v[t]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    int e = 0;
-    if (mx > 0.f) frexpf(mx, &e);
-    const int sh = mx > 0.f ? 15 - e : 0;
+    // mx < 2^(field - 126); sh in [-126, 126] keeps 2^sh and 2^-sh normal
+    const int field = (int)(__float_as_uint(mx) >> 23);
+    const int sh = max(-126, min(126, 15 + 126 - field));
+    const float up = __int_as_float((127 + sh) << 23);
 #pragma unroll
-    for (int t = 0; t < NB; ++t) qs[hh * D + lane + 32 * t] = ldexpf(v[t], sh);
-    if (lane == 0) fh[hh] = head < G ? ldexpf(P.scale * kLog2e4, -sh) : 0.f;
+    for (int t = 0; t < NB; ++t) qs[hh * D + lane + 32 * t] = v[t] * up;
+    if (lane == 0) fh[hh] = __int_as_float((127 - sh) << 23);
   }
   __syncthreads();
   // A fragments: lane (g, c) of k-step kk = 2 blk + half holds dims 32 blk + 16
@@ -279,18 +371,26 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 
   // o[u][2 blk + half]: dims 32 blk + 16 half + 2 gq + {0 (rows g), 1 (rows g + 8)}, columns 2cq, 2cq+1
   float o[NH][2 * NB][4];
-  float m[NH], l[NH];
+  // head gq of each tile: the running maximum m (log2), the raw score that
+  // moves it, m - fe, and this lane's sum of 2^fe P
+  float m[NH], top[NH], mf[NH];
+  uint64_t l2[NH];
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
-    m[u] = -INFINITY;
-    l[u] = 0.f;
+    m[u] = top[u] = -INFINITY;
+    mf[u] = 0.f;
+    l2[u] = pack2(0.f, 0.f);
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t) o[u][t][0] = o[u][t][1] = o[u][t][2] = o[u][t][3] = 0.f;
   }
   int lim = -1;       // exponent field of the largest V scale allowed for (-1: none yet)
-  float F = 0.f;      // 2^fe
-  const float lo_part = kPack && gq >= 4 ? -1.f : 0.f;
+  // what the second rounding of P * scale leaves off the first: the part
+  // already held by hi (packed: by the hi columns, for the lo columns)
+  const float hi_off = kPack && gq < 4 ? 0.f : -1.f;
+  const uint64_t hi_off2 = pack2(hi_off, hi_off);
 
+  uint32_t k1024;  // (1024, 1024), kept out of the compiler's sight as a constant
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
   const uint4* qfl = qf + lane;
   // ldmatrix row addresses.  K (x4): 8 tokens, blocks 0-3 (head_dim 64: 8
   // tokens each of two columns, blocks 0-1); V (x4, transposed): tokens 0-7
@@ -328,13 +428,16 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         kw[j + 1][1] = r[3];
       }
     }
-    // the scales of this lane's tokens 8j + 2cq, + 1: NB halves each
+    // raw scores of tokens 8j + 2cq, + 1 in units of fac
     uint64_t s2[NH][NT];
 #pragma unroll
     for (int u = 0; u < NH; ++u)
 #pragma unroll
       for (int j = 0; j < NT; ++j) s2[u][j] = pack2(0.f, 0.f);
-    const uint8_t* ksc = stp + 2 * C::kQuants + 2 * cq * C::kSRow;
+    const uint8_t* sc = stp + 2 * C::kQuants + 2 * cq * C::kSRow;
+    uint32_t ksc[NT][NB];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) scales2<NB>(sc + j * 8 * C::kSRow, ksc[j]);
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb) {
 #pragma unroll
@@ -343,79 +446,63 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const uint32_t w = kw[j][bb], w8 = w >> 8;
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma4(acc, a0.x, a0.y, a0.z, a0.w, nib8<false>(w), nib8<false>(w8));
-          mma4(acc, a1.x, a1.y, a1.z, a1.w, nib8<true>(w), nib8<true>(w8));
-          const unsigned short* sp = reinterpret_cast<const unsigned short*>(ksc + j * 8 * C::kSRow) + bb;
-          const uint64_t d2 = pack2(f16_bits_to_f32(sp[0]), f16_bits_to_f32(sp[C::kSRow / 2]));
-          s2[u][j] = fma2(d2, add2(pack2(acc[0], acc[1]), pack2(acc[2], acc[3])), s2[u][j]);
+          float acc[4];
+          mma4z(acc, a0.x, a0.y, a0.z, a0.w, nib8<false>(w, k1024), nib8<false>(w8, k1024));
+          mma4(acc, a1.x, a1.y, a1.z, a1.w, nib8<true>(w, k1024), nib8<true>(w8, k1024));
+          s2[u][j] = fma2(scale_pair<NB>(ksc[j], bb), add2(pack2(acc[0], acc[1]), pack2(acc[2], acc[3])),
+                          s2[u][j]);
         }
       }
     }
 
-    // ---- log2-domain scores and the running maximum ----
-    float s[NH][NT][2];
+    // ---- the running maximum ----
+    float s[NH][NT][2], mx[NH];
     bool above = false;
 #pragma unroll
     for (int u = 0; u < NH; ++u) {
-      float mx = -INFINITY;
+      mx[u] = -INFINITY;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         unpack2(s2[u][j], s[u][j][0], s[u][j][1]);
-        s[u][j][0] *= fac[u];
-        s[u][j][1] *= fac[u];
         if (nr < kTile4) {
           if (8 * j + 2 * cq >= nr) s[u][j][0] = -INFINITY;
           if (8 * j + 2 * cq + 1 >= nr) s[u][j][1] = -INFINITY;
         }
-        mx = fmaxf(mx, fmaxf(s[u][j][0], s[u][j][1]));
+        mx[u] = fmaxf(mx[u], fmaxf(s[u][j][0], s[u][j][1]));
       }
-      above = above || mx > m[u] + kSlack4;
+      above = above || mx[u] > top[u];
     }
     // the V scales of this lane's tokens and their largest exponent
-    uint32_t vsc[NT][NB];  // per 8 tokens: two tokens' NB halves
-    __half2 vm = __float2half2_rn(0.f);
+    uint32_t vsc[NT][NB];
+    uint32_t vm = 0u;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const uint8_t* p = stp + 2 * C::kQuants + C::kScales + (8 * j + 2 * cq) * C::kSRow;
-      if constexpr (D == 128) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        vsc[j][0] = w.x;
-        vsc[j][1] = w.y;
-        vsc[j][2] = w.z;
-        vsc[j][3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        vsc[j][0] = w.x;
-        vsc[j][1] = w.y;
-      }
+      scales2<NB>(sc + C::kScales + j * 8 * C::kSRow, vsc[j]);
 #pragma unroll
-      for (int t = 0; t < NB; ++t) vm = __hmax2(vm, __habs2(*reinterpret_cast<const __half2*>(&vsc[j][t])));
+      for (int t = 0; t < NB; ++t) vm = max_abs2(vm, vsc[j][t]);
     }
-    const uint32_t vmb = *reinterpret_cast<const uint32_t*>(&vm);
-    int ve = (int)(max(vmb & 0xffffu, vmb >> 16) >> 10);
+    vm &= 0x7fff7fffu;
+    int ve = (int)(max(vm & 0xffffu, vm >> 16) >> 10);
     if (__any_sync(0xffffffffu, above || ve > lim)) {  // (rare after the first tiles)
 #pragma unroll
       for (int of = 1; of < 32; of <<= 1) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, of));
       float r = 1.f;
-      if (ve > lim) {
-        const float Fn = __int_as_float((127 + kFe0 + 14 - max(ve, 1)) << 23);  // |scale| < 2^(field - 14)
-        r = lim < 0 ? 0.f : Fn / F;
-        F = Fn;
+      if (ve > lim) {  // 2^fe for |scale| < 2^(field - 14)
+        r = lim < 0 ? 0.f : __int_as_float((127 + max(lim, 1) - max(ve, 1)) << 23);
         lim = ve;
       }
+      const float fe = (float)(kFe0 + 14 - max(lim, 1));
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[u][j][0], s[u][j][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[u], mx);
-        const float cf = m[u] == -INFINITY ? 0.f : exp2f(m[u] - mn);
+        float x = mx[u];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float mn = fmaxf(m[u], x * fac[u]);
+        const float cr = m[u] == -INFINITY ? 0.f : exp2f(m[u] - mn) * r;
         m[u] = mn;
-        l[u] *= cf;
-        const float cr = cf * r;
+        mf[u] = mn - fe;
+        top[u] = (mn + kSlack4) / fac[u];
+        l2[u] = mul2(l2[u], pack2(cr, cr));
         const float c0 = __shfl_sync(0xffffffffu, cr, 8 * cq), c1 = __shfl_sync(0xffffffffu, cr, 8 * cq + 4);
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
@@ -427,17 +514,18 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
       }
     }
 
-    // ---- P, then O += (P * scale) . V per block ----
+    // ---- 2^fe P, then O += (2^fe P * scale) . V per block ----
 #pragma unroll
     for (int h = 0; h < NT / 2; ++h) {  // 16 tokens
+      if (h * 16 >= nr) break;
       uint64_t p2[NH][2];
 #pragma unroll
       for (int u = 0; u < NH; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float pa = exp2f(s[u][2 * h + j][0] - m[u]), pb = exp2f(s[u][2 * h + j][1] - m[u]);
-          l[u] += pa + pb;
-          p2[u][j] = mul2(pack2(pa, pb), pack2(F, F));
+          p2[u][j] = pack2(ex2(fmaf(s[u][2 * h + j][0], fac[u], -mf[u])),
+                           ex2(fmaf(s[u][2 * h + j][1], fac[u], -mf[u])));
+          l2[u] = add2(l2[u], p2[u][j]);
         }
 #pragma unroll
       for (int bp = 0; bp < NB / 2; ++bp) {
@@ -447,33 +535,27 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         for (int x = 0; x < 2; ++x) {
           const int bb = 2 * bp + x;
           const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1], w0s = w0 >> 8, w1s = w1 >> 8;
-          const uint32_t l0 = nib8<false>(w0), l1 = nib8<false>(w0s), l2 = nib8<false>(w1), l3 = nib8<false>(w1s);
-          const uint32_t u0 = nib8<true>(w0), u1 = nib8<true>(w0s), u2 = nib8<true>(w1), u3 = nib8<true>(w1s);
+          const uint32_t l0 = nib8<false>(w0, k1024), l1 = nib8<false>(w0s, k1024), l2w = nib8<false>(w1, k1024), l3 = nib8<false>(w1s, k1024);
+          const uint32_t u0 = nib8<true>(w0, k1024), u1 = nib8<true>(w0s, k1024), u2 = nib8<true>(w1, k1024), u3 = nib8<true>(w1s, k1024);
 #pragma unroll
           for (int u = 0; u < NH; ++u) {
             uint32_t ph[2], pl[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              // halves bb of the two tokens' scales
-              const uint32_t wa = vsc[2 * h + j][bb / 2], wb = vsc[2 * h + j][NB / 2 + bb / 2];
-              const float2 fa = h2f(wa), fb = h2f(wb);
-              const uint64_t pd = mul2(p2[u][j], bb & 1 ? pack2(fa.y, fb.y) : pack2(fa.x, fb.x));
+              const uint64_t pd = mul2(p2[u][j], scale_pair<NB>(vsc[2 * h + j], bb));
               float a, d;
               unpack2(pd, a, d);
               ph[j] = f2h(a, d);
               const float2 hf = h2f(ph[j]);
-              if constexpr (kPack) {
-                ph[j] = f2h(fmaf(hf.x, lo_part, a), fmaf(hf.y, lo_part, d));
-              } else {
-                pl[j] = f2h(a - hf.x, d - hf.y);
-              }
+              unpack2(fma2(pack2(hf.x, hf.y), hi_off2, pd), a, d);
+              pl[j] = f2h(a, d);
             }
-            mma4(o[u][2 * bb], l0, l1, l2, l3, ph[0], ph[1]);
-            mma4(o[u][2 * bb + 1], u0, u1, u2, u3, ph[0], ph[1]);
             if constexpr (!kPack) {
-              mma4(o[u][2 * bb], l0, l1, l2, l3, pl[0], pl[1]);
-              mma4(o[u][2 * bb + 1], u0, u1, u2, u3, pl[0], pl[1]);
+              mma4(o[u][2 * bb], l0, l1, l2w, l3, ph[0], ph[1]);
+              mma4(o[u][2 * bb + 1], u0, u1, u2, u3, ph[0], ph[1]);
             }
+            mma4(o[u][2 * bb], l0, l1, l2w, l3, pl[0], pl[1]);
+            mma4(o[u][2 * bb + 1], u0, u1, u2, u3, pl[0], pl[1]);
           }
         }
       }
@@ -487,10 +569,12 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   float* mm = reinterpret_cast<float*>(smem);
   float* ll = mm + kWarps4 * 8 * NH;
   float* oo = ll + kWarps4 * 8 * NH;
-  const float inv_f = lim < 0 ? 0.f : 1.f / F;
+  const float inv_f = lim < 0 ? 0.f : __int_as_float((127 - kFe0 - 14 + max(lim, 1)) << 23);  // 2^-fe
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
-    float sum = l[u];
+    float sum, odd;
+    unpack2(l2[u], sum, odd);
+    sum = (sum + odd) * inv_f;
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     if (cq == 0) {
@@ -519,8 +603,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 #pragma unroll
     for (int w = 0; w < kWarps4; ++w) {
       const float mw = mm[w * 8 * NH + h];
-      if (mw == -INFINITY) continue;
-      const float wgt = exp2f(mw - M);
+      const float wgt = mw == -INFINITY ? 0.f : ex2(mw - M);  // (a warp without a tile)
       float x = oo[(size_t)(w * 8 * NH + h) * D + j];
       if constexpr (kPack) x += oo[(size_t)(w * 8 * NH + h + 4) * D + j];
       acc = fmaf(x, wgt, acc);
@@ -535,14 +618,113 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   }
 }
 
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the chunks of one
+// (sequence, query head).  The kernel is all latency (one dependent launch),
+// so it asks for everything at once: the lengths before it waits for the
+// partials, then D/4 lanes a chunk keep up to kMine4 16-byte pieces of O in
+// flight while the first threads fetch m and l and work out the weights.
+constexpr int kCombThreads4 = 512;
+constexpr int kMine4 = 5;  // chunks a thread, per pass
+constexpr int kPass4 = 512;  // chunks a pass at most (weights in shared memory)
+
+template <int D>
+__global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const AttnParams P) {
+  constexpr int kLanes = D / 4, kGroups = kCombThreads4 / kLanes;
+  __shared__ float wt[kPass4], red[2][kCombThreads4 / 32];
+  __shared__ float4 so[kGroups][kLanes];
+  const int hq = blockIdx.x, b = hq / P.n_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int j = tid % kLanes, grp = tid / kLanes;
+  // the attention grid released this one after its own wait: the lengths are
+  // readable
+  const float rate = chunk_rate4(P, lane);
+  const int L = window_len4(P, b);
+  const int n = nchunks4(P, L, rate);
+  const int tpc = L >= 1 ? (L + n - 1) / n : 1;
+  const int nact = L >= 1 ? (L + tpc - 1) / tpc : 0;
+  griddep_wait();               // the partials are complete and visible
+  griddep_launch_dependents();  // (not earlier: the next kernel would take SMs from this one)
+  float* o = P.out + (long long)hq * D;
+  if (L < 1) {
+    if (grp == 0) {
+      const float q = __int_as_float(0x7fc00000);
+      for (int i = 0; i < 4; ++i) o[4 * j + i] = q;
+    }
+    return;
+  }
+  const float* O = P.ws_o + (long long)hq * P.nc * D;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, lsum = 0.f;
+  for (int c0 = 0; c0 < nact; c0 += kPass4) {  // (one pass up to 512 chunks)
+    const int nc = min(kPass4, nact - c0);
+    float4 v[kMine4];
+#pragma unroll
+    for (int u = 0; u < kMine4; ++u) {
+      const int c = grp + u * kGroups;
+      v[u] = c < nc ? __ldcg(reinterpret_cast<const float4*>(O + (long long)(c0 + c) * D) + j)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float mc = tid < nc ? __ldcg(P.ws_m + (long long)hq * P.nc + c0 + tid) : -INFINITY;
+    const float lc = tid < nc ? __ldcg(P.ws_l + (long long)hq * P.nc + c0 + tid) : 0.f;
+    float mx = mc;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    if (lane == 0) red[0][warp] = mx;
+    __syncthreads();
+    mx = M;
+#pragma unroll
+    for (int w = 0; w < kCombThreads4 / 32; ++w) mx = fmaxf(mx, red[0][w]);
+    const float old = M == -INFINITY ? 0.f : ex2(M - mx);
+    M = mx;
+    const float w = mc == -INFINITY ? 0.f : ex2(mc - M);
+    wt[tid] = w;
+    float ls = lc * w;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+    if (lane == 0) red[1][warp] = ls;
+    __syncthreads();
+    lsum *= old;
+#pragma unroll
+    for (int x = 0; x < kCombThreads4 / 32; ++x) lsum += red[1][x];
+    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+    for (int u0 = 0; grp + u0 * kGroups < nc; u0 += kMine4) {
+#pragma unroll
+      for (int u = 0; u < kMine4; ++u) {
+        const int c = grp + (u0 + u) * kGroups;
+        if (c >= nc) break;
+        const float4 x = u0 == 0 ? v[u]
+                                 : __ldcg(reinterpret_cast<const float4*>(O + (long long)(c0 + c) * D) + j);
+        const float g = wt[c];
+        acc.x = fmaf(x.x, g, acc.x);
+        acc.y = fmaf(x.y, g, acc.y);
+        acc.z = fmaf(x.z, g, acc.z);
+        acc.w = fmaf(x.w, g, acc.w);
+      }
+    }
+    __syncthreads();  // (wt and red are rewritten by another pass)
+  }
+  so[grp][j] = acc;
+  __syncthreads();
+  if (tid < D) {
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) s += reinterpret_cast<const float*>(so[x])[tid];
+    o[tid] = s / lsum;
+  }
+}
+
 template <int D, int NH, bool kPack>
 int launch_q4kv(const AttnParams& P, cudaStream_t stream) {
   using C = Cfg4<D, NH>;
   const auto fn = gqa_q4kv_kernel<D, NH, kPack>;
-  int rc = configure_kernel(reinterpret_cast<const void*>(fn), C::kSmem, true);
+  // (no carveout preference: a change of carveout between this kernel and
+  // the next drains the SMs, 2 us a call)
+  int rc = configure_kernel(reinterpret_cast<const void*>(fn), C::kSmem, false);
   if (rc) return rc;
   rc = launch_ex(fn, dim3(P.nct, P.n_kv_heads), dim3(kThreads4), (size_t)C::kSmem, stream, true, P);
-  return rc ? rc : attn_combine_launch(P, stream);
+  if (rc) return rc;
+  return launch_ex(gqa_q4kv_combine_kernel<D>, dim3((unsigned)(P.batch * P.n_heads)),
+                   dim3(kCombThreads4), 0, stream, true, P);
 }
 
 template <int D>
@@ -555,7 +737,13 @@ int launch_q4kv_g(const AttnParams& P, cudaStream_t stream) {
 
 }  // namespace
 
-int attn_q4kv_launch(const AttnParams& P, cudaStream_t stream) {
+int attn_q4kv_launch(const AttnParams& A, cudaStream_t stream) {
+  AttnParams P = A;
+  // About two CTAs an SM in all suit a few sequences; a larger batch gets at
+  // least kSeqCtas4 chunks a sequence on average, so that the longest of a
+  // ragged batch does not set the time (more than one wave of CTAs then).
+  const long long by_len = (long long)P.batch * ((P.cap + kMinChunk - 1) / kMinChunk);
+  if (P.batch > 1) P.nct = (int)std::min<long long>(by_len, std::max(P.nct, kSeqCtas4 * P.batch));
   return P.head_dim == 128 ? launch_q4kv_g<128>(P, stream) : launch_q4kv_g<64>(P, stream);
 }
 
