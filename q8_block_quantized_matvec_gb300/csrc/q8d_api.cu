@@ -476,8 +476,8 @@ int q8d_gqa_decode_attn_window(const float* q, const float* k_new, const float* 
 
 namespace q8d {
 static bool moe_shape(int m, int hidden, int ffn, int n_experts, int top_k) {
-  return m >= 0 && m <= kMoeMaxTokens && hidden > 0 && hidden % 32 == 0 && hidden <= 32768 &&
-         ffn > 0 && ffn % 32 == 0 && ffn <= 32768 && n_experts >= 1 &&
+  return m >= 0 && m <= kMoeMaxTokens && hidden > 0 && hidden % 32 == 0 && hidden <= 16384 &&
+         ffn > 0 && ffn % 32 == 0 && ffn <= 16384 && n_experts >= 1 &&
          n_experts <= kMoeMaxExperts && top_k >= 1 && top_k <= n_experts && top_k <= kMoeMaxTop;
 }
 }  // namespace q8d

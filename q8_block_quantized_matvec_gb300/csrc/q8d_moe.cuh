@@ -23,9 +23,10 @@ struct MoeParams {
   int* experts;    // [m][top_k] (the caller's, or in the workspace)
   float* weights;  // [m][top_k]
   int* d_err;
-  // carved from the workspace
-  double* logits;  // [m][E]
-  float* h;        // [m * top_k][ffn]
+  // activation images in the workspace (q8d_moe.cu): rows of 128 bytes a
+  // block of 32, and the blocks' inverse scales (rows padded to 4 floats)
+  uint8_t *ximg, *himg;  // [m], [m * top_k]
+  float *xinv, *hinv;
 };
 
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);

@@ -32,7 +32,7 @@ def test_moe_refusals(q8d):
     for bad in (dict(m=-1), dict(hidden=0), dict(ffn=-32), dict(E=0), dict(k=0), dict(k=9)):
         assert call(q8d, wsb=1 << 20, **bad) == EINVAL, bad
     for bad in (dict(m=65), dict(hidden=80, ldx=80, ldy=80, ldr=80), dict(ffn=100), dict(E=513, k=2),
-                dict(E=64, k=33), dict(hidden=32800, ldx=32800, ldy=32800, ldr=32800), dict(ffn=32800)):
+                dict(E=64, k=33), dict(hidden=16416, ldx=16416, ldy=16416, ldr=16416), dict(ffn=16416)):
         assert call(q8d, wsb=1 << 30, **bad) == EUNS, bad
     assert call(q8d, ldx=60) == EINVAL and call(q8d, ldy=63) == EINVAL and call(q8d, ldr=63) == EINVAL
     for bad in (dict(X=M + 8), dict(ldx=66), dict(router=2 * M + 4), dict(wg=3 * M + 2), dict(wu=4 * M + 8),
