@@ -7,10 +7,11 @@
 // What bounds it is reading the chosen experts' matrices once from HBM: with
 // m tokens choosing k of E, 2 and 3 stream about E (1 - (1 - k/E)^m) experts
 // of 34 bytes a block of 32, and a token adds only a column to each product.
-// So both are streaming kernels: one producer warp keeps a ring of shared
-// memory stages filled by bulk copies (every row of a stage in a slot of its
-// own, slots 4 (mod 8) words apart so that eight rows' words lie in distinct
-// banks), a second one the tokens' values, and up to sixteen consumer warps
+// So both are streaming kernels: four producer warps keep a ring of shared
+// memory stages filled with 16-byte cp.async copies (every row of a stage in a
+// slot of its own, slots 4 (mod 8) words apart so that eight rows' words lie in
+// distinct banks; bulk copies of such short pieces issue a lane at a time and
+// held the stream to 6 bytes a cycle and SM), and up to sixteen consumer warps
 // multiply with mma.sync m16n8k16:
 //  * A: sixteen weight rows, a lane's word of four quants made two exact f16
 //    pairs (one PRMT and one subtraction a pair); B: up to eight tokens of
@@ -21,8 +22,9 @@
 //    results are f32-accurate.
 //  * Whoever makes the values writes them in the operand's order: the router
 //    kernel for x, the gate / up epilogue for h (it owns whole blocks of 32
-//    rows), 16 bytes {hi01, hi23, lo01, lo23} a word, 128 a block, so the
-//    products fetch them with bulk copies and never convert.
+//    rows), 16 bytes {hi01, hi23, lo01, lo23} a word, 144 a block with its
+//    inverse scale, so the products copy them beside the weights and never
+//    convert.
 //  * An expert's tokens are taken eight at a time (fewer where long rows
 //    leave no room); experts nobody chose are not touched.
 //  * gate / up: a work unit is 32 rows of an expert (32 gate and 32 up rows:
@@ -45,21 +47,18 @@ namespace {
 
 using namespace mv;
 
-constexpr int kImgBlock = 128;  // image bytes a block
+constexpr int kImgBlock = 144;  // image bytes a block: 8 words of 16, the inverse scale, 12 unused
 constexpr int kMaxSmem = 222 * 1024;
 
-__host__ __device__ constexpr int inv_pitch(int bpr) { return (bpr + 3) & ~3; }
-
 // ---- 1. router --------------------------------------------------------------
-constexpr int kRtThreads = 256;
+constexpr int kRtThreads = 512;
 constexpr int kRtCluster = 8;
-constexpr int kRtTokens = 4;  // tokens a cluster, at most
 
 __device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
 
 // (s, c) += a * b as an unevaluated sum: the product's rounding error (one
-// FMA) and the sum's (TwoSum) go to c, so s + c carries about 48 bits.  f64
-// arithmetic would be exact enough as well, but this GPU has next to none.
+// FMA) and the sum's (TwoSum) go to c, so s + c carries about 48 bits.  (f64
+// arithmetic would do as well, but an SM of this GPU does two a cycle.)
 __device__ __forceinline__ void dot2(uint64_t& s, uint64_t& c, uint64_t a, uint64_t b) {
   const uint64_t m1 = pack2(-1.f, -1.f);
   const uint64_t p = mul2(a, b);
@@ -71,6 +70,13 @@ __device__ __forceinline__ void dot2(uint64_t& s, uint64_t& c, uint64_t a, uint6
   c = add2(c, add2(add2(x, y), e));
   s = t;
 }
+// (h, l) += (a, b), pairs as above.
+__device__ __forceinline__ void add_pair(float& h, float& l, float a, float b) {
+  const float t = __fadd_rn(h, a), z = __fsub_rn(t, h);
+  const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(a, z));
+  h = t;
+  l = __fadd_rn(l, __fadd_rn(b, e));
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -81,28 +87,31 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Stores v at p's place in the shared memory of the cluster's CTA 0.
-__device__ __forceinline__ void store_leader(double* p, double v) {
+__device__ __forceinline__ void store_leader(float2* p, float2 v) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Orders doubles as integers; NaN below every number, 0 free for "taken".
-__device__ __forceinline__ uint64_t rank_key(double v) {
-  if (isnan(v)) return 1ull;
-  const long long b = __double_as_longlong(v + 0.0);  // (-0 and 0 tie)
-  return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
+// Orders logits (h, l), l at most half a unit of h's last place, as integers;
+// NaN below every number, 0 free for "taken".
+__device__ __forceinline__ uint32_t order32(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);  // (-0 and 0 tie)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t rank_key(float2 v) {
+  return isnan(v.x) ? 1ull : (uint64_t)order32(v.x) << 32 | order32(v.y);
 }
 
 // Choice and weights of one token by a warp; kPer: experts a lane.
 template <int kPer>
-__device__ void choose(const MoeParams& P, int t, const double* logits, int lane) {
+__device__ void choose(const MoeParams& P, int t, const float2* logits, int lane) {
   const int E = P.n_experts;
   uint64_t key[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < E ? rank_key(logits[lane + 32 * i]) : 0ull;
   int mine = 0;
-  double top = 0.0;  // the largest logit
+  float2 top = make_float2(0.f, 0.f);  // the largest logit
   for (int k = 0; k < P.top_k; ++k) {
     uint64_t best = 0;
     int at = 0;
@@ -119,36 +128,39 @@ __device__ void choose(const MoeParams& P, int t, const double* logits, int lane
     if (k == 0) top = logits[e];
     if (lane == k) mine = e;
   }
-  // exp of the difference in two f32 parts (its rounding to one would cost up
-  // to 2^-24 of the difference)
+  // exp(l - top), the difference in two parts (rounded to one it would be off
+  // by up to 2^-24 of itself)
   const auto ex = [&](int e) {
-    const double d = logits[e] - top;
-    const float dh = (float)d;
-    const float x = expf(dh), dl = (float)(d - (double)dh);
-    return isinf(dh) ? x : fmaf(x, dl, x);
+    const float2 v = logits[e];
+    float d = v.x, r = v.y;
+    add_pair(d, r, -top.x, -top.y);
+    const float x = expf(d);
+    return isinf(d) ? x : fmaf(x, r, x);
   };
-  double all = 0.0;
+  float all = 0.f, all2 = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < E) all += (double)ex(lane + 32 * i);
+    if (lane + 32 * i < E) add_pair(all, all2, ex(lane + 32 * i), 0.f);
   const float w = lane < P.top_k ? ex(mine) : 0.f;
-  double chosen = (double)w;
+  float chosen = w, chosen2 = 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    chosen += __shfl_xor_sync(0xffffffffu, chosen, o);
+    const float a = __shfl_xor_sync(0xffffffffu, all, o), a2 = __shfl_xor_sync(0xffffffffu, all2, o);
+    const float c = __shfl_xor_sync(0xffffffffu, chosen, o), c2 = __shfl_xor_sync(0xffffffffu, chosen2, o);
+    add_pair(all, all2, a, a2);
+    add_pair(chosen, chosen2, c, c2);
   }
   if (lane < P.top_k) {
     P.experts[t * P.top_k + lane] = mine;
-    const float r = (float)((double)w / (P.norm ? chosen : all));
-    P.weights[t * P.top_k + lane] = isnan(all) ? __int_as_float(0x7fc00000) : r;
+    P.weights[t * P.top_k + lane] =
+        isnan(all) ? __int_as_float(0x7fc00000) : __fdiv_rn(w, P.norm ? chosen + chosen2 : all + all2);
   }
 }
 
 // One image word: the four values (already in operand order) of word w of a
 // block, the block's eight words in eight neighbouring lanes.  Every lane of
 // the warp calls; live: the word exists.
-__device__ __forceinline__ void image_word(const float (&v)[4], bool live, uint8_t* blk, float* inv, int w) {
+__device__ __forceinline__ void image_word(const float (&v)[4], bool live, uint8_t* blk, int w) {
   float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -159,12 +171,76 @@ __device__ __forceinline__ void image_word(const float (&v)[4], bool live, uint8
   const float sc = __int_as_float((127 + e) << 23);
   const float t[4] = {v[0] * sc, v[1] * sc, v[2] * sc, v[3] * sc};
   tc::store_x_word(blk + 16 * w, t);
-  if (w == 0) *inv = __int_as_float((127 - e) << 23);
+  if (w == 0) *reinterpret_cast<float*>(blk + 128) = __int_as_float((127 - e) << 23);
+}
+
+// Logits of kE experts e, e + stride, .. for kT tokens by a warp, to the
+// leader's table.
+template <int kT, int kE>
+__device__ __forceinline__ void logits_of(const MoeParams& P, int t0, int nt, int e, int stride, int e1,
+                                          float2 (*table)[kMoeMaxExperts], int lane) {
+  uint64_t s[kE][kT][2], c[kE][kT][2];
+#pragma unroll
+  for (int x = 0; x < kE; ++x)
+#pragma unroll
+    for (int t = 0; t < kT; ++t) s[x][t][0] = s[x][t][1] = c[x][t][0] = c[x][t][1] = pack2(0.f, 0.f);
+  constexpr int kAhead = kT * kE == 1 ? 8 : kT * kE <= 4 ? 4 : 2;  // loads in flight
+  const int n = P.hidden / 4;
+  for (int i0 = lane; i0 < n; i0 += 32 * kAhead) {
+    float4 a[kAhead][kE], b[kAhead][kT];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + 32 * u;
+      const bool ok = i < n;
+#pragma unroll
+      for (int x = 0; x < kE; ++x)
+        a[u][x] = ok ? __ldg(reinterpret_cast<const float4*>(
+                                 P.router + (size_t)min(e + x * stride, e1 - 1) * P.hidden) + i)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+        b[u][t] = ok ? *(reinterpret_cast<const float4*>(P.X + (size_t)(t0 + min(t, nt - 1)) * P.ldx) + i)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int x = 0; x < kE; ++x)
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          dot2(s[x][t][0], c[x][t][0], pack2(a[u][x].x, a[u][x].y), pack2(b[u][t].x, b[u][t].y));
+          dot2(s[x][t][1], c[x][t][1], pack2(a[u][x].z, a[u][x].w), pack2(b[u][t].z, b[u][t].w));
+        }
+  }
+#pragma unroll
+  for (int x = 0; x < kE; ++x)
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      float v[4], r[4];
+      unpack2(s[x][t][0], v[0], v[1]);
+      unpack2(s[x][t][1], v[2], v[3]);
+      unpack2(c[x][t][0], r[0], r[1]);
+      unpack2(c[x][t][1], r[2], r[3]);
+      float plain = (v[0] + v[1]) + (v[2] + v[3]);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) add_pair(v[0], r[0], v[k], r[k]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float a = __shfl_xor_sync(0xffffffffu, v[0], o), b = __shfl_xor_sync(0xffffffffu, r[0], o);
+        plain += __shfl_xor_sync(0xffffffffu, plain, o);
+        add_pair(v[0], r[0], a, b);
+      }
+      // normalise; the error terms of an overflowed or NaN sum mean nothing
+      const float h = v[0] + r[0];
+      const float2 l = isfinite(h) ? make_float2(h, __fsub_rn(r[0], __fsub_rn(h, v[0]))) : make_float2(plain, 0.f);
+      if (lane == 0 && t < nt && e + x * stride < e1) store_leader(&table[t][e + x * stride], l);
+    }
 }
 
 template <int kT>
 __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams P, int per_cluster, bool perm) {
-  __shared__ double logits[kRtTokens][kMoeMaxExperts];
+  __shared__ float2 logits[kT][kMoeMaxExperts];
+  constexpr int kWarps = kRtThreads / 32;
   const int rank = (int)cluster_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = (blockIdx.x / kRtCluster) * per_cluster;
   const int nt = min(per_cluster, P.m - t0);
@@ -172,7 +248,7 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
   const int e0 = rank * ep, e1 = min(P.n_experts, e0 + ep);
   griddep_launch_dependents();
   // the router's rows depend on nothing in flight: into L2 meanwhile
-  for (int e = e0 + warp; e < e1; e += kRtThreads / 32) {
+  for (int e = e0 + warp; e < e1; e += kWarps) {
     const char* r = reinterpret_cast<const char*>(P.router + (size_t)e * P.hidden);
     for (int o = lane * 4096; o < P.hidden * 4; o += 32 * 4096)
       bulk_prefetch_l2(r + o, (uint32_t)min(4096, P.hidden * 4 - o));
@@ -180,38 +256,9 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
   griddep_wait();
   // every CTA of the cluster is running before one stores to another's memory
   cluster_sync();
-  for (int e = e0 + warp; e < e1; e += kRtThreads / 32) {
-    const float4* r = reinterpret_cast<const float4*>(P.router + (size_t)e * P.hidden);
-    uint64_t s[kT][2], c[kT][2];
-#pragma unroll
-    for (int t = 0; t < kT; ++t) s[t][0] = s[t][1] = c[t][0] = c[t][1] = pack2(0.f, 0.f);
-#pragma unroll 4
-    for (int i = lane; i < P.hidden / 4; i += 32) {
-      const float4 a = __ldg(r + i);
-#pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        const float4 b = *(reinterpret_cast<const float4*>(P.X + (size_t)(t0 + min(t, nt - 1)) * P.ldx) + i);
-        dot2(s[t][0], c[t][0], pack2(a.x, a.y), pack2(b.x, b.y));
-        dot2(s[t][1], c[t][1], pack2(a.z, a.w), pack2(b.z, b.w));
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      float x[8];
-      unpack2(s[t][0], x[0], x[1]);
-      unpack2(s[t][1], x[2], x[3]);
-      unpack2(c[t][0], x[4], x[5]);
-      unpack2(c[t][1], x[6], x[7]);
-      // (the error terms of an overflowed or NaN sum mean nothing)
-      const float plain = (x[0] + x[1]) + (x[2] + x[3]);
-      double v = isfinite(plain) ? (((double)x[0] + x[1]) + ((double)x[2] + x[3])) +
-                                       (((double)x[4] + x[5]) + ((double)x[6] + x[7]))
-                                 : (double)plain;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0 && t < nt) store_leader(&logits[t][e], v);
-    }
-  }
+  int e = e0 + warp;
+  for (; e + kWarps < e1; e += 2 * kWarps) logits_of<kT, 2>(P, t0, nt, e, kWarps, e1, logits, lane);
+  if (e < e1) logits_of<kT, 1>(P, t0, nt, e, kWarps, e1, logits, lane);
   // the tokens' operand images, a word a thread, blocks dealt over the cluster
   const int bpr = P.hidden / kQBlock, words = nt * bpr * 8;
   for (int i0 = (rank * kRtThreads + warp * 32); i0 < words; i0 += kRtCluster * kRtThreads) {
@@ -221,12 +268,11 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
     const float* x = P.X + (size_t)(t0 + t) * P.ldx + (size_t)b * kQBlock;
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = x[tc::word_quant(perm && !(b & 1), w, k)];
-    image_word(v, i < words, P.ximg + ((size_t)(t0 + t) * bpr + b) * kImgBlock,
-               P.xinv + (size_t)(t0 + t) * inv_pitch(bpr) + b, w);
+    image_word(v, i < words, P.ximg + ((size_t)(t0 + t) * bpr + b) * kImgBlock, w);
   }
   cluster_sync();  // the logits are complete
   if (rank == 0 && warp < nt) {
-    const double* l = logits[warp];
+    const float2* l = logits[warp];
     if (P.n_experts <= 64)
       choose<2>(P, t0 + warp, l, lane);
     else if (P.n_experts <= 128)
@@ -238,20 +284,21 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
 
 // ---- 2, 3. the products -----------------------------------------------------
 
+constexpr int kProducers = 4;  // producer warps (the first brings the images too)
+
 // How a product kernel lays out its shared memory (host plan).
 struct MoePlan {
   int bpr;          // blocks a row
   int S, nsl;       // blocks a slice, slices a row
   int SR;           // slot bytes
   int slots;        // row slots of a stage
-  int stage_bytes, nst;
   int tg;           // tokens a group (1, 2, 4 or 8)
-  int XS, XI;       // image bytes and inverse scales a token in a buffer
-  int xbuf_bytes, nbuf;
-  int W, KW;        // consumer warps, warps over the blocks of a row
+  int XR;           // image bytes a token of a stage
+  int stage_bytes, nst;
+  int W;            // consumer warps
   int rows, mt;     // down: output rows a CTA takes at once, A tiles of 16
   int items;        // (expert, token group) pairs at most
-  int o_x, o_part, o_hq, o_mask, o_ebase, o_item, o_tok, o_bar;  // offsets
+  int o_part, o_hq, o_mask, o_ebase, o_item, o_tok, o_bar;  // offsets
   int smem;
 };
 
@@ -263,7 +310,7 @@ struct MoeShared {
   int2* item;                // (expert | tokens << 16, first pair row)
   float* pw;                 // [pairs] weight of a pair row
   uint8_t* ptok;             // [pairs] token of a pair row
-  uint64_t *full, *empty, *xfull, *xempty;
+  uint64_t *full, *empty;
   int n_items;
 };
 
@@ -278,8 +325,6 @@ __device__ __forceinline__ MoeShared carve(const MoePlan& L, uint8_t* smem, int 
   S.ptok = smem + L.o_tok + 4 * pairs;
   S.full = reinterpret_cast<uint64_t*>(smem + L.o_bar);
   S.empty = S.full + L.nst;
-  S.xfull = S.empty + L.nst;
-  S.xempty = S.xfull + L.nbuf;
   S.n_items = 0;
   return S;
 }
@@ -293,12 +338,8 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
   for (int e = threadIdx.x; e < E; e += nthr) S.mask[e] = 0ull;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L.nst; ++i) {
-      mbar_init(&S.full[i], 1);
+      mbar_init(&S.full[i], kProducers * 32 + 1);
       mbar_init(&S.empty[i], L.W);
-    }
-    for (int i = 0; i < L.nbuf; ++i) {
-      mbar_init(&S.xfull[i], 1);
-      mbar_init(&S.xempty[i], L.W);
     }
     fence_barrier_init();
   }
@@ -342,77 +383,74 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
   S.n_items = s_items;
 }
 
-// One warp fills stage `st` with blocks [c0, c0 + nb) of `n` rows: row(i)
-// gives slot i's matrix and row in it.  Rows start on any even byte unless
-// kAl: the copy covers the 16-byte lines the row touches, and the last bytes
-// of a matrix, when its end is no line's end, come by plain stores.
-template <bool kAl, typename RowFn>
-__device__ __forceinline__ void fill_stage(const MoePlan& L, uint8_t* st, uint64_t* full, int n, int c0, int nb,
-                                           long long mat_bytes, RowFn row, uint64_t pol, int lane) {
-  uint32_t bytes[2] = {0u, 0u};
-  const uint8_t* src[2] = {nullptr, nullptr};
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = lane + 32 * u;
-    if (i >= n) continue;
-    const uint8_t* base;
-    long long r;
-    row(i, base, r);
-    const long long a = r * (long long)(L.bpr * kQBlockBytes) + (long long)c0 * kQBlockBytes;
-    if constexpr (kAl) {
-      src[u] = base + a;
-      bytes[u] = (uint32_t)nb * kQBlockBytes;
-    } else {
-      const long long lo = a & ~15LL, end = a + (long long)nb * kQBlockBytes;
-      const long long hi = min((end + 15) & ~15LL, mat_bytes & ~15LL);
-      src[u] = base + lo;
-      bytes[u] = (uint32_t)(hi - lo);
-      for (long long x = hi; x < end; x += 2)  // (the matrix ends inside its last line)
-        *reinterpret_cast<unsigned short*>(st + (size_t)i * L.SR + (x - lo)) =
-            *reinterpret_cast<const unsigned short*>(base + x);
+// 16 bytes, of which n exist (the others become zeros).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// Arrives on bar once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A producer thread's share of a stage's rows: 16-byte line c of rows rg,
+// rg + step, ..  (Fixed for the kernel: the copy loops only add.)
+struct FillLane {
+  int c, rg, step;
+};
+template <bool kAl>
+__device__ __forceinline__ FillLane fill_lane(const MoePlan& L, int tid) {
+  const int len = L.S * kQBlockBytes;
+  const int cpr = kAl ? len / 16 : (len + 29) / 16;  // lines a row, at most
+  FillLane F;
+  F.step = kProducers * 32 / cpr;
+  F.rg = tid / cpr;
+  F.c = tid - F.rg * cpr;
+  if (F.rg >= F.step) F.rg = 1 << 20;  // (no rows)
+  return F;
+}
+
+// Copies blocks [c0, c0 + nb) of n consecutive rows, the first at byte `off`
+// of its matrix, into slots from `dst` on.  Rows start on any even byte
+// unless kAl, so the copy covers the 16-byte lines a row touches (no byte
+// past the matrix).
+template <bool kAl>
+__device__ __forceinline__ void fill_rows(const MoePlan& L, const FillLane& F, uint32_t dst, const uint8_t* base,
+                                          long long off, int n, int c0, int nb, long long mat_bytes) {
+  const int rb = L.bpr * kQBlockBytes, len = nb * kQBlockBytes;
+  if (F.c * 16 >= (kAl ? len : len + 14)) return;
+  const long long step = (long long)F.step * rb;
+  const uint32_t dstep = (uint32_t)(F.step * L.SR);
+  long long a = off + (long long)F.rg * rb + (long long)c0 * kQBlockBytes;
+  dst += (uint32_t)(F.rg * L.SR + F.c * 16);
+  if constexpr (kAl) {
+    const uint8_t* src = base + a + F.c * 16;
+#pragma unroll 4
+    for (int r = F.rg; r < n; r += F.step) {
+      cp16(dst, src, 16);
+      src += step;
+      dst += dstep;
+    }
+  } else {
+    const long long last = mat_bytes - F.c * 16;
+#pragma unroll 2
+    for (int r = F.rg; r < n; r += F.step) {
+      const long long lo = a & ~15LL, left = last - lo;
+      if (left > 0) cp16(dst, base + lo + F.c * 16, left < 16 ? (int)left : 16);
+      a += step;
+      dst += dstep;
     }
   }
-  if constexpr (!kAl) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (plain stores before later copies)
-    __syncwarp();
-  }
-  const uint32_t total = __reduce_add_sync(0xffffffffu, bytes[0] + bytes[1]);
-  if (lane == 0) mbar_arrive_expect_tx(full, total);
-  __syncwarp();
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-    if (bytes[u]) bulk_g2s(st + (size_t)(lane + 32 * u) * L.SR, src[u], bytes[u], full, pol);
 }
 
-// Buffers `n` tokens' images and inverse scales (token i's at rows(i)).
-template <typename RowFn>
-__device__ __forceinline__ void fill_x(const MoePlan& L, uint8_t* xb, uint64_t* full, const uint8_t* img,
-                                       const float* inv, int n, RowFn rows, uint64_t pol, int lane) {
-  const uint32_t ib = (uint32_t)L.bpr * kImgBlock, vb = (uint32_t)L.XI * 4;
-  if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)n * (ib + vb));
+// One warp: blocks [c0, c0 + nb) of n <= 8 tokens' images (token i's at
+// img(i)), a bulk copy each.
+template <typename ImgFn>
+__device__ __forceinline__ void fill_images(const MoePlan& L, uint8_t* dst, uint64_t* full, int n, int c0, int nb,
+                                            ImgFn img, uint64_t pol, int lane) {
+  const uint32_t bytes = (uint32_t)nb * kImgBlock;
+  if (lane == 0) mbar_arrive_expect_tx(full, bytes * n);
   __syncwarp();
-  if (lane < n) {
-    const size_t r = (size_t)rows(lane);
-    bulk_g2s(xb + (size_t)lane * L.XS, img + r * ib, ib, full, pol);
-    bulk_g2s(xb + (size_t)L.tg * L.XS + (size_t)lane * vb, inv + r * L.XI, vb, full, pol);
-  }
-}
-
-// The word of four quants w = 4 step + c of a block at smem address ba.
-// kAl: words are aligned in odd blocks; an even block's word 7 is its first
-// two and last two quants (tc::word_quant).  Otherwise any even address,
-// quants in order.
-template <bool kAl>
-__device__ __forceinline__ uint32_t quant_word(uint32_t ba, bool even, int step, int c) {
-  if constexpr (kAl) {
-    if (!even) return tc::lds32a(ba + 2u + 16u * step + 4u * c);
-    if (step == 0) return tc::lds32a(ba + 4u + 4u * c);
-    const uint32_t l0 = tc::lds32a(ba), l1 = tc::lds32a(ba + (c == 3 ? 32u : 20u + 4u * c));
-    return __byte_perm(l0, l1, c == 3 ? 0x5432u : 0x7654u);
-  } else {
-    const uint32_t q = ba + 2u + 16u * step + 4u * c, a = q & ~3u;
-    return __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), (q & 2u) ? 0x5432u : 0x3210u);
-  }
+  if (lane < n) bulk_g2s(dst + lane * L.XR, img(lane) + (size_t)c0 * kImgBlock, bytes, full, pol);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -421,30 +459,103 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// y[t] += the products of one block: kTiles A tiles whose rows g and g + 8 of
-// tile t start (this block) at ra[t][0] and ra[t][1]; xa: this lane's image
-// words, xi: the inverse scales of its two tokens.
+// What a lane reads of one block: its words of kTiles A tiles, their scales,
+// its columns' operand and inverse scales.  All loads of a block are issued
+// before its arithmetic (asm volatile keeps their order), and two blocks'
+// before either's.
+template <int kTiles>
+struct BlockIn {
+  uint32_t w[kTiles][2][3];  // row g or g + 8: word of step 0, words of step 1
+  uint32_t d[kTiles][2];
+  uint4 b0, b1;
+  float xi0, xi1;
+};
+
+// kAl: words are aligned in odd blocks; an even block's word 7 is its first
+// two and last two quants (tc::word_quant).  Otherwise a block starts at any
+// even address, quants in order.
 template <bool kAl, int kTiles>
-__device__ __forceinline__ void block_mma(const uint32_t (&ra)[kTiles][2], bool even, int c, uint32_t xa, float xi0,
-                                          float xi1, float (&y)[kTiles][4]) {
-  const uint4 b0 = lds128(xa), b1 = lds128(xa + 64u);
+__device__ __forceinline__ void load_block(const uint32_t (&ra)[kTiles][2], bool even, int c, uint32_t xa, uint32_t x0,
+                                           uint32_t x1, BlockIn<kTiles>& B) {
+  B.b0 = lds128(xa);
+  B.b1 = lds128(xa + 64u);
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t ba = ra[t][h];
+      B.d[t][h] = tc::lds16a(ba);
+      if constexpr (kAl) {
+        if (even) {
+          B.w[t][h][0] = tc::lds32a(ba + 4u + 4u * c);
+          B.w[t][h][1] = tc::lds32a(ba);
+          B.w[t][h][2] = tc::lds32a(ba + (c == 3 ? 32u : 20u + 4u * c));
+        } else {
+          B.w[t][h][0] = tc::lds32a(ba + 2u + 4u * c);
+          B.w[t][h][1] = tc::lds32a(ba + 18u + 4u * c);
+        }
+      } else {
+        const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
+        B.w[t][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
+        B.w[t][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
+      }
+    }
+  B.xi0 = tc::lds32f(x0 + 128u);
+  B.xi1 = tc::lds32f(x1 + 128u);
+}
+
+// y[t] += the products of a loaded block: columns 2c and 2c + 1 of rows g
+// ([0], [1]) and g + 8 ([2], [3]) of tile t.
+template <bool kAl, int kTiles>
+__device__ __forceinline__ void block_mma(const BlockIn<kTiles>& B, bool even, int c, float (&y)[kTiles][4]) {
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t a0, a1, a2, a3;
-    tc::quant_pairs(quant_word<kAl>(ra[t][0], even, 0, c), a0, a2);
-    tc::quant_pairs(quant_word<kAl>(ra[t][1], even, 0, c), a1, a3);
-    tc::mma_f16(acc, a0, a1, a2, a3, b0.x, b0.y);
-    tc::mma_f16(acc, a0, a1, a2, a3, b0.z, b0.w);
-    tc::quant_pairs(quant_word<kAl>(ra[t][0], even, 1, c), a0, a2);
-    tc::quant_pairs(quant_word<kAl>(ra[t][1], even, 1, c), a1, a3);
-    tc::mma_f16(acc, a0, a1, a2, a3, b1.x, b1.y);
-    tc::mma_f16(acc, a0, a1, a2, a3, b1.z, b1.w);
-    const float d0 = f16_bits_to_f32(tc::lds16a(ra[t][0])), d1 = f16_bits_to_f32(tc::lds16a(ra[t][1]));
-    y[t][0] = fmaf(d0 * xi0, acc[0], y[t][0]);
-    y[t][1] = fmaf(d0 * xi1, acc[1], y[t][1]);
-    y[t][2] = fmaf(d1 * xi0, acc[2], y[t][2]);
-    y[t][3] = fmaf(d1 * xi1, acc[3], y[t][3]);
+    tc::quant_pairs(B.w[t][0][0], a0, a2);
+    tc::quant_pairs(B.w[t][1][0], a1, a3);
+    tc::mma_f16(acc, a0, a1, a2, a3, B.b0.x, B.b0.y);
+    tc::mma_f16(acc, a0, a1, a2, a3, B.b0.z, B.b0.w);
+    uint32_t w0 = B.w[t][0][1], w1 = B.w[t][1][1];
+    if (kAl && even) {
+      const uint32_t sel = c == 3 ? 0x5432u : 0x7654u;
+      w0 = __byte_perm(w0, B.w[t][0][2], sel);
+      w1 = __byte_perm(w1, B.w[t][1][2], sel);
+    }
+    tc::quant_pairs(w0, a0, a2);
+    tc::quant_pairs(w1, a1, a3);
+    tc::mma_f16(acc, a0, a1, a2, a3, B.b1.x, B.b1.y);
+    tc::mma_f16(acc, a0, a1, a2, a3, B.b1.z, B.b1.w);
+    const float d0 = f16_bits_to_f32(B.d[t][0]), d1 = f16_bits_to_f32(B.d[t][1]);
+    y[t][0] = fmaf(d0 * B.xi0, acc[0], y[t][0]);
+    y[t][1] = fmaf(d0 * B.xi1, acc[1], y[t][1]);
+    y[t][2] = fmaf(d1 * B.xi0, acc[2], y[t][2]);
+    y[t][3] = fmaf(d1 * B.xi1, acc[3], y[t][3]);
+  }
+}
+
+// A warp's blocks first, first + step, .. < nb of a stage, two at a time.
+// ro: where this lane's rows' blocks start (block 0), xl, x0, x1: its image
+// words and its columns' images (block 0).
+template <bool kAl, int kTiles>
+__device__ __forceinline__ void stage_blocks(const uint32_t (&ro)[kTiles][2], uint32_t xl, uint32_t x0, uint32_t x1,
+                                             int first, int step, int nb, int c, float (&y)[kTiles][4]) {
+  const auto load = [&](int j, BlockIn<kTiles>& B) {
+    uint32_t ra[kTiles][2];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ra[t][h] = ro[t][h] + (uint32_t)j * kQBlockBytes;
+    const uint32_t xo = (uint32_t)j * kImgBlock;
+    load_block<kAl, kTiles>(ra, !(j & 1), c, xl + xo, x0 + xo, x1 + xo, B);
+  };
+  for (int j = first; j < nb; j += 2 * step) {
+    BlockIn<kTiles> A, B;
+    const int j1 = j + step;
+    load(j, A);
+    if (j1 < nb) load(j1, B);
+    block_mma<kAl, kTiles>(A, !(j & 1), c, y);
+    if (j1 < nb) block_mma<kAl, kTiles>(B, !(j1 & 1), c, y);
   }
 }
 
@@ -454,12 +565,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// Ends a product kernel: reports a wait that gave up, and has a producer
-// warp (of `issued` fills of the n buffers behind `full`) wait for its copies
-// in flight before the CTA leaves.
-__device__ __forceinline__ void finish(const MoeParams& P, uint64_t* full, int n, volatile int* abort, int issued) {
+// After a wait gave up: the bulk copies of the last fills (of i) have landed.
+__device__ __forceinline__ void drain(const MoePlan& L, const MoeShared& S, int i, volatile int* abort) {
   if (*abort)
-    for (int j = max(0, issued - n); j < issued; ++j) mbar_wait(&full[j % n], (uint32_t)(j / n) & 1u);
+    for (int j = max(0, i - L.nst); j < i; ++j) mbar_wait(&S.full[j % L.nst], (uint32_t)(j / L.nst) & 1u);
+}
+
+// Ends a product kernel: no copy is in flight when the CTA leaves, and a wait
+// that gave up is reported.
+__device__ __forceinline__ void finish(const MoeParams& P, volatile int* abort) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0 && *abort && P.d_err) atomicOr(P.d_err, Q8D_DERR_WAIT);
 }
@@ -469,7 +584,7 @@ constexpr int kGuRows = 32;             // h rows a unit
 constexpr int kGuTiles = 2;             // A tiles (8 gate + 8 up rows) a warp
 
 template <bool kAl>
-__global__ void __launch_bounds__((kGuWarps + 2) * 32, 1)
+__global__ void __launch_bounds__((kGuWarps + kProducers) * 32, 1)
     moe_gate_up_kernel(const MoeParams P, const MoePlan L, bool hperm) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_abort;
@@ -482,101 +597,76 @@ __global__ void __launch_bounds__((kGuWarps + 2) * 32, 1)
   const int nq = P.ffn / kGuRows;                // units an item
   const long long units = (long long)S.n_items * nq;
   const int q0 = (int)(units * blockIdx.x / gridDim.x), q1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
-  int issued = 0;
-  if (warp == kGuWarps) {
-    const uint64_t pol = policy_evict_first();
-    const long long mat = (long long)P.n_experts * P.ffn * L.bpr * kQBlockBytes;
+  if (warp >= kGuWarps) {
+    const int tid = threadIdx.x - kGuWarps * 32;
+    const int rb = L.bpr * kQBlockBytes;
+    const long long mat = (long long)P.n_experts * P.ffn * rb;
+    const uint32_t smem32 = smem_u32(smem);
+    const FillLane F = fill_lane<kAl>(L, tid);
+    const bool first = warp == kGuWarps;
+    const uint64_t keep = policy_evict_last();
+    fence_proxy_async_global();  // (the images were written by ordinary stores)
+    int issued = 0;
     bool ok = true;
     for (int q = q0; q < q1 && ok; ++q) {
       const int it = q / nq;
-      const long long r0 = (long long)(S.item[it].x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows;
+      const int2 I = S.item[it];
+      const long long r0 = ((long long)(I.x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows) * rb;
       for (int sl = 0; sl < L.nsl; ++sl, ++issued) {
         const int s = issued % L.nst;
         if (issued >= L.nst) ok = warp_wait(&S.empty[s], (uint32_t)(issued / L.nst - 1) & 1u, &s_abort, lane);
         if (!ok) break;
-        fill_stage<kAl>(L, smem + (size_t)s * L.stage_bytes, &S.full[s], 2 * kGuRows, sl * L.S,
-                        min(L.S, L.bpr - sl * L.S), mat,
-                        [&](int i, const uint8_t*& base, long long& r) {
-                          base = i < kGuRows ? P.wg : P.wu;
-                          r = r0 + (i & (kGuRows - 1));
-                        },
-                        pol, lane);
+        const uint32_t st = smem32 + (uint32_t)s * (uint32_t)L.stage_bytes;
+        const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
+        if (first)
+          fill_images(L, smem + (size_t)s * L.stage_bytes + L.slots * L.SR, &S.full[s], I.x >> 16, c0, nb,
+                      [&](int n) { return P.ximg + (size_t)S.ptok[I.y + n] * L.bpr * kImgBlock; }, keep, lane);
+        fill_rows<kAl>(L, F, st, P.wg, r0, kGuRows, c0, nb, mat);
+        fill_rows<kAl>(L, F, st + (uint32_t)(kGuRows * L.SR), P.wu, r0, kGuRows, c0, nb, mat);
+        cp_arrive(&S.full[s]);
       }
     }
-  } else if (warp == kGuWarps + 1) {
-    const uint64_t keep = policy_evict_last();
-    fence_proxy_async_global();  // (the images were written by ordinary stores)
-    for (int it = q0 / nq; it * nq < q1; ++it, ++issued) {
-      const int s = issued % L.nbuf;
-      if (issued >= L.nbuf && !warp_wait(&S.xempty[s], (uint32_t)(issued / L.nbuf - 1) & 1u, &s_abort, lane)) break;
-      const int2 I = S.item[it];
-      fill_x(L, smem + L.o_x + s * L.xbuf_bytes, &S.xfull[s], P.ximg, P.xinv, I.x >> 16,
-             [&](int i) { return (int)S.ptok[I.y + i]; }, keep, lane);
-    }
+    if (first) drain(L, S, issued, &s_abort);
   } else {
     const int gq = lane >> 2, cq = lane & 3;
     const int kb = warp % kGuK, th = warp / kGuK;  // blocks kb, kb + 8, ..; tiles 2 th, 2 th + 1
     const uint32_t smem32 = smem_u32(smem);
-    const uint32_t xl = (uint32_t)(min(gq, L.tg - 1) * L.XS + cq * 16);
+    const uint32_t xoff = (uint32_t)(L.slots * L.SR);
+    const uint32_t xl = xoff + (uint32_t)(min(gq, L.tg - 1) * L.XR + cq * 16);
+    const uint32_t x0 = xoff + (uint32_t)(min(2 * cq, L.tg - 1) * L.XR);
+    const uint32_t x1 = xoff + (uint32_t)(min(2 * cq + 1, L.tg - 1) * L.XR);
     float* hq = reinterpret_cast<float*>(smem + L.o_hq);  // [32 rows][8 tokens + 1]
-    int item = -1, xuse = -1, stage = 0;
-    bool ok = true;
-    uint32_t xb = 0;
-    const float* xiv = nullptr;
+    int stage = 0;
     for (int q = q0; q < q1; ++q) {
       const int it = q / nq;
-      if (it != item) {
-        if (xuse >= 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.xempty[xuse % L.nbuf]);
-        }
-        item = it;
-        ++xuse;
-        ok = wait_or_abort(&S.xfull[xuse % L.nbuf], (uint32_t)(xuse / L.nbuf) & 1u, &s_abort) && ok;
-        const uint32_t off = (uint32_t)(L.o_x + (xuse % L.nbuf) * L.xbuf_bytes);
-        xb = after_wait(smem32 + off) + xl;
-        xiv = reinterpret_cast<const float*>(smem + off + (size_t)L.tg * L.XS);
-      }
       const int2 I = S.item[it];
       const int ntok = I.x >> 16;
       const long long r0 = (long long)(I.x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows;
-      const float* xi0 = xiv + min(2 * cq, L.tg - 1) * L.XI;
-      const float* xi1 = xiv + min(2 * cq + 1, L.tg - 1) * L.XI;
       float y[kGuTiles][4];
 #pragma unroll
       for (int t = 0; t < kGuTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
-      // where this lane's rows start in their slots
-      uint32_t ro[kGuTiles][2];
+      // this lane's slots, and how far into its first line each row starts
+      uint32_t ro[kGuTiles][2], mis[kGuTiles];
 #pragma unroll
       for (int t = 0; t < kGuTiles; ++t) {
         const int r = (2 * th + t) * 8 + gq;
-        const uint32_t mis = kAl ? 0u : (uint32_t)(((r0 + r) * (L.bpr * kQBlockBytes)) & 15);
-        ro[t][0] = (uint32_t)(r * L.SR) + mis;
-        ro[t][1] = (uint32_t)((kGuRows + r) * L.SR) + mis;
+        mis[t] = kAl ? 0u : (uint32_t)(((r0 + r) * (L.bpr * kQBlockBytes)) & 15);
+        ro[t][0] = (uint32_t)(r * L.SR);
+        ro[t][1] = (uint32_t)((kGuRows + r) * L.SR);
       }
       for (int sl = 0; sl < L.nsl; ++sl, ++stage) {
         const int s = stage % L.nst;
-        ok = wait_or_abort(&S.full[s], (uint32_t)(stage / L.nst) & 1u, &s_abort) && ok;
+        wait_or_abort(&S.full[s], (uint32_t)(stage / L.nst) & 1u, &s_abort);
         const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
         const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
-        // (a slice's own misalignment: c0 * 34 beyond the row's)
-        for (int j = kb; j < nb; j += kGuK) {
-          uint32_t ra[kGuTiles][2];
+        uint32_t ra[kGuTiles][2];
 #pragma unroll
-          for (int t = 0; t < kGuTiles; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if constexpr (kAl) {
-                ra[t][h] = st + ro[t][h] + (uint32_t)j * kQBlockBytes;
-              } else {
-                const uint32_t slot = (uint32_t)((h * kGuRows + (2 * th + t) * 8 + gq) * L.SR);
-                ra[t][h] = st + slot + ((ro[t][h] - slot + (uint32_t)c0 * kQBlockBytes) & 15u) +
-                           (uint32_t)j * kQBlockBytes;
-              }
-            }
-          const int blk = c0 + j;
-          block_mma<kAl, kGuTiles>(ra, !(blk & 1), cq, xb + (uint32_t)blk * kImgBlock, xi0[blk], xi1[blk], y);
+        for (int t = 0; t < kGuTiles; ++t) {
+          const uint32_t o = st + (kAl ? 0u : (mis[t] + (uint32_t)c0 * kQBlockBytes) & 15u);
+          ra[t][0] = ro[t][0] + o;
+          ra[t][1] = ro[t][1] + o;
         }
+        stage_blocks<kAl, kGuTiles>(ra, st + xl, st + x0, st + x1, kb, kGuK, nb, cq, y);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.empty[s]);
       }
@@ -604,18 +694,17 @@ __global__ void __launch_bounds__((kGuWarps + 2) * 32, 1)
         float v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = hq[tc::word_quant(hperm && !(b & 1), w, k) * 9 + n];
-        image_word(v, n < ntok, P.himg + ((size_t)(I.y + n) * nq + b) * kImgBlock,
-                   P.hinv + (size_t)(I.y + n) * inv_pitch(nq) + b, w);
+        image_word(v, n < ntok, P.himg + ((size_t)(I.y + n) * nq + b) * kImgBlock, w);
       }
     }
   }
-  finish(P, warp == kGuWarps ? S.full : S.xfull, warp == kGuWarps ? L.nst : L.nbuf, &s_abort, issued);
+  finish(P, &s_abort);
 }
 
 constexpr int kDnMaxWarps = 16;
 
 template <bool kAl, int kTiles>
-__global__ void __launch_bounds__((kDnMaxWarps + 2) * 32, 1) moe_down_kernel(const MoeParams P, const MoePlan L) {
+__global__ void __launch_bounds__((kDnMaxWarps + kProducers) * 32, 1) moe_down_kernel(const MoeParams P, const MoePlan L) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_abort;
   MoeShared S = carve(L, smem, P.m * P.top_k);
@@ -623,74 +712,72 @@ __global__ void __launch_bounds__((kDnMaxWarps + 2) * 32, 1) moe_down_kernel(con
   if (threadIdx.x == 0) s_abort = 0;
   group_pairs(P, L, S);  // (the choice is complete: the gate / up kernel started behind it)
   const int chunks = (P.hidden + L.rows - 1) / L.rows;
-  int issued = 0;
-  if (warp == W) {
-    // Weights depend on nothing in flight: they fill the ring while the gate /
-    // up kernel ends.
-    const uint64_t pol = policy_evict_first();
-    const long long mat = (long long)P.n_experts * P.hidden * L.bpr * kQBlockBytes;
-    bool ok = true;
-    for (int ch = blockIdx.x; ch < chunks && ok; ch += gridDim.x) {
-      const int r0 = ch * L.rows, nr = min(L.rows, P.hidden - r0);
-      for (int it = 0; it < S.n_items && ok; ++it) {
-        const long long e0 = (long long)(S.item[it].x & 0xffff) * P.hidden + r0;
-        for (int sl = 0; sl < L.nsl; ++sl, ++issued) {
-          const int s = issued % L.nst;
-          if (issued >= L.nst) ok = warp_wait(&S.empty[s], (uint32_t)(issued / L.nst - 1) & 1u, &s_abort, lane);
-          if (!ok) break;
-          fill_stage<kAl>(L, smem + (size_t)s * L.stage_bytes, &S.full[s], nr, sl * L.S,
-                          min(L.S, L.bpr - sl * L.S), mat,
-                          [&](int i, const uint8_t*& base, long long& r) {
-                            base = P.wd;
-                            r = e0 + i;
-                          },
-                          pol, lane);
-        }
-      }
-    }
-  } else if (warp == W + 1) {
+  const int per = S.n_items * L.nsl;  // stages a chunk of rows
+  const int mine = blockIdx.x < chunks ? (chunks - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  const int total = mine * per;
+  if (warp >= W) {
+    const int tid = threadIdx.x - W * 32;
+    const int rb = L.bpr * kQBlockBytes;
+    const long long mat = (long long)P.n_experts * P.hidden * rb;
+    const uint32_t smem32 = smem_u32(smem);
+    const FillLane F = fill_lane<kAl>(L, tid);
+    const bool first = warp == W;
     const uint64_t keep = policy_evict_last();
-    griddep_wait();
+    // stage i of this CTA: its weights, its images
+    const auto weights = [&](int i) {
+      const int x = i % per, c0 = x % L.nsl * L.S, r0 = (blockIdx.x + i / per * gridDim.x) * L.rows;
+      fill_rows<kAl>(L, F, smem32 + (uint32_t)(i % L.nst) * (uint32_t)L.stage_bytes, P.wd,
+                     ((long long)(S.item[x / L.nsl].x & 0xffff) * P.hidden + r0) * rb, min(L.rows, P.hidden - r0), c0,
+                     min(L.S, L.bpr - c0), mat);
+      cp_arrive(&S.full[i % L.nst]);
+    };
+    const auto images = [&](int i) {
+      const int x = i % per, c0 = x % L.nsl * L.S, s = i % L.nst;
+      const int2 I = S.item[x / L.nsl];
+      fill_images(L, smem + (size_t)s * L.stage_bytes + L.slots * L.SR, &S.full[s], I.x >> 16, c0,
+                  min(L.S, L.bpr - c0),
+                  [&](int n) { return P.himg + (size_t)(I.y + n) * L.bpr * kImgBlock; }, keep, lane);
+    };
+    // Weights depend on nothing in flight: the first ring of them comes while
+    // the gate / up kernel ends.
+    const int ring = min(total, L.nst);
+    int i = 0;
+    for (; i < ring; ++i) weights(i);
+    griddep_wait();  // (h)
     fence_proxy_async_global();
-    bool ok = true;
-    for (int ch = blockIdx.x; ch < chunks && ok; ch += gridDim.x)
-      for (int it = 0; it < S.n_items; ++it, ++issued) {
-        const int s = issued % L.nbuf;
-        if (issued >= L.nbuf) ok = warp_wait(&S.xempty[s], (uint32_t)(issued / L.nbuf - 1) & 1u, &s_abort, lane);
-        if (!ok) break;
-        const int2 I = S.item[it];
-        fill_x(L, smem + L.o_x + s * L.xbuf_bytes, &S.xfull[s], P.himg, P.hinv, I.x >> 16,
-               [&](int i) { return I.y + i; }, keep, lane);
-      }
+    if (first)
+      for (int k = 0; k < ring; ++k) images(k);
+    for (; i < total; ++i) {
+      if (!warp_wait(&S.empty[i % L.nst], (uint32_t)(i / L.nst - 1) & 1u, &s_abort, lane)) break;
+      if (first) images(i);
+      weights(i);
+    }
+    if (first) drain(L, S, i, &s_abort);
   } else {
     griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
     const uint32_t smem32 = smem_u32(smem);
-    const uint32_t xl = (uint32_t)(min(gq, L.tg - 1) * L.XS + cq * 16);
+    const uint32_t xoff = (uint32_t)(L.slots * L.SR);
+    const uint32_t xl = xoff + (uint32_t)(min(gq, L.tg - 1) * L.XR + cq * 16);
+    const uint32_t x0 = xoff + (uint32_t)(min(2 * cq, L.tg - 1) * L.XR);
+    const uint32_t x1 = xoff + (uint32_t)(min(2 * cq + 1, L.tg - 1) * L.XR);
     const int yp = P.m | 1;                                 // table pitch (odd: rows in distinct banks)
     float* tab = S.part + (size_t)warp * L.mt * 16 * yp;    // this warp's [rows][tokens]
-    int xuse = 0, stage = 0;
-    bool ok = true;
+    int stage = 0;
     for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
       const int r0 = ch * L.rows, nr = min(L.rows, P.hidden - r0);
       for (int i = lane; i < L.mt * 16 * yp; i += 32) tab[i] = 0.f;
       __syncwarp();
-      for (int it = 0; it < S.n_items; ++it, ++xuse) {
+      for (int it = 0; it < S.n_items; ++it) {
         const int2 I = S.item[it];
         const int ntok = I.x >> 16;
         const long long e0 = (long long)(I.x & 0xffff) * P.hidden + r0;
-        ok = wait_or_abort(&S.xfull[xuse % L.nbuf], (uint32_t)(xuse / L.nbuf) & 1u, &s_abort) && ok;
-        const uint32_t off = (uint32_t)(L.o_x + (xuse % L.nbuf) * L.xbuf_bytes);
-        const uint32_t xb = after_wait(smem32 + off) + xl;
-        const float* xiv = reinterpret_cast<const float*>(smem + off + (size_t)L.tg * L.XS);
-        const float* xi0 = xiv + min(2 * cq, L.tg - 1) * L.XI;
-        const float* xi1 = xiv + min(2 * cq + 1, L.tg - 1) * L.XI;
         float y[kTiles][4];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
         for (int sl = 0; sl < L.nsl; ++sl, ++stage) {
           const int s = stage % L.nst;
-          ok = wait_or_abort(&S.full[s], (uint32_t)(stage / L.nst) & 1u, &s_abort) && ok;
+          wait_or_abort(&S.full[s], (uint32_t)(stage / L.nst) & 1u, &s_abort);
           const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
           const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
           uint32_t ro[kTiles][2];
@@ -703,19 +790,10 @@ __global__ void __launch_bounds__((kDnMaxWarps + 2) * 32, 1) moe_down_kernel(con
                   kAl ? 0u : (uint32_t)(((e0 + r) * (L.bpr * kQBlockBytes) + c0 * kQBlockBytes) & 15);
               ro[t][h] = st + (uint32_t)(r * L.SR) + mis;
             }
-          for (int j = warp; j < nb; j += W) {
-            uint32_t ra[kTiles][2];
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) ra[t][h] = ro[t][h] + (uint32_t)j * kQBlockBytes;
-            const int blk = c0 + j;
-            block_mma<kAl, kTiles>(ra, !(blk & 1), cq, xb + (uint32_t)blk * kImgBlock, xi0[blk], xi1[blk], y);
-          }
+          stage_blocks<kAl, kTiles>(ro, st + xl, st + x0, st + x1, warp, W, nb, cq, y);
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.empty[s]);
         }
-        if (lane == 0) mbar_arrive(&S.xempty[xuse % L.nbuf]);
         // weighted into the warp's table: lane (g, c) alone owns these entries
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -744,7 +822,7 @@ __global__ void __launch_bounds__((kDnMaxWarps + 2) * 32, 1) moe_down_kernel(con
       consumer_sync(W * 32);  // (the tables are cleared next)
     }
   }
-  finish(P, warp == W ? S.full : S.xfull, warp == W ? L.nst : L.nbuf, &s_abort, issued);
+  finish(P, &s_abort);
   griddep_launch_dependents();
 }
 
@@ -759,29 +837,37 @@ int slot_bytes(int n, bool aligned) {
   return b;
 }
 
-// Token groups and their buffers: as many tokens as can share an expert (up
-// to 8, a power of two), several buffers where they leave the ring its room.
-void plan_x(const MoeParams& P, int bpr, int most, int most_buf, MoePlan* L) {
-  L->bpr = bpr;
-  L->XI = inv_pitch(bpr);
-  // token rows half a bank cycle apart: the two tokens of a quarter warp's
-  // 16-byte loads lie in distinct banks
-  L->XS = bpr * kImgBlock + 64;
-  const int a_token = L->XS + L->XI * 4;
-  L->tg = 8;
-  while (L->tg > 1 && (L->tg / 2 >= P.m || L->tg * a_token > most)) L->tg /= 2;
-  L->xbuf_bytes = up16i(L->tg * a_token);
-  L->nbuf = std::max(1, std::min(most_buf, most / L->xbuf_bytes));
-  const int pairs = P.m * P.top_k;
-  L->items = std::min(pairs, P.n_experts + pairs / L->tg);
+// Tokens a group: about twice an expert's share of the (token, slot) pairs,
+// a power of two up to 8 (an expert with more is read once a group; with
+// fewer, its stage space idles).
+int group_tokens(const MoeParams& P) {
+  const int want = std::min(P.m, 2 * P.m * P.top_k / P.n_experts + 2);
+  int tg = 1;
+  while (tg < 8 && tg < want) tg *= 2;
+  return tg;
 }
 
-// Offsets behind the ring; returns the bytes used without the ring.
-int plan_rest(const MoeParams& P, int part_floats, int hq_floats, MoePlan* L) {
+// Slices of S blocks, tokens and stage of a plan whose slots are set.
+void plan_stage(const MoeParams& P, int S, bool al, int tg, MoePlan* L) {
+  L->S = S;
+  L->nsl = (L->bpr + S - 1) / S;
+  L->S = (L->bpr + L->nsl - 1) / L->nsl;  // (equal slices; whole groups of 8 blocks where rows are aligned)
+  if (al) L->S = (L->S + 7) / 8 * 8;
+  L->SR = slot_bytes(L->S, al);
+  // token rows half a bank cycle apart: the two tokens of a quarter warp's
+  // 16-byte loads lie in distinct banks
+  L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
+  L->tg = tg;
+  L->stage_bytes = L->slots * L->SR + tg * L->XR;
   const int pairs = P.m * P.top_k;
-  int o = L->nst * L->stage_bytes;
-  L->o_x = o;
-  o += L->nbuf * L->xbuf_bytes;
+  L->items = std::min(pairs, P.n_experts + pairs / tg);
+}
+
+// Offsets behind a ring of nst stages; sets smem.
+void plan_rest(const MoeParams& P, int nst, int part_floats, int hq_floats, MoePlan* L) {
+  const int pairs = P.m * P.top_k;
+  L->nst = nst;
+  int o = nst * L->stage_bytes;
   L->o_part = o;
   o += up16i(4 * part_floats);
   L->o_hq = o;
@@ -789,89 +875,74 @@ int plan_rest(const MoeParams& P, int part_floats, int hq_floats, MoePlan* L) {
   L->o_mask = o;
   o += 8 * P.n_experts;
   L->o_ebase = o;
-  o += up16i(4 * P.n_experts);
-  o = up16i(o);
+  o = up16i(o + 4 * P.n_experts);
   L->o_item = o;
   o += 8 * L->items;
   L->o_tok = o = up16i(o);
   o += up16i(5 * pairs);
-  L->o_bar = o = up16i(o);
-  o += 16 * L->nst + 16 * L->nbuf;
-  L->smem = o;
-  return o - L->nst * L->stage_bytes;
+  L->o_bar = o;
+  L->smem = o + 16 * nst;
+}
+
+// As many stages as fit, at least `least`.
+bool plan_ring(const MoeParams& P, int least, int most, int part_floats, int hq_floats, MoePlan* L) {
+  plan_rest(P, 0, part_floats, hq_floats, L);
+  const int n = L->smem < kMaxSmem ? std::min(most, (kMaxSmem - L->smem) / (L->stage_bytes + 16)) : 0;
+  if (n < least) return false;
+  plan_rest(P, n, part_floats, hq_floats, L);
+  return true;
 }
 
 int plan_gate_up(const MoeParams& P, MoePlan* L) {
-  const int bpr = P.hidden / kQBlock;
-  const bool al = bpr % 8 == 0;
-  plan_x(P, bpr, 120 * 1024, 2, L);
+  const bool al = P.hidden / kQBlock % 8 == 0;
+  L->bpr = P.hidden / kQBlock;
   L->W = kGuWarps;
-  L->KW = kGuK;
   L->slots = 2 * kGuRows;
   L->rows = kGuRows;
   L->mt = 4;
-  for (int nbuf = L->nbuf; nbuf >= 1; --nbuf) {
-    L->nbuf = nbuf;
-    // two blocks a warp in a stage, or one where that leaves too few stages
-    for (int s = std::min(16, bpr); s >= 1; s = s > 8 ? 8 : s / 2) {
-      L->S = s;
-      L->nsl = (bpr + s - 1) / s;
-      L->SR = slot_bytes(s, al);
-      L->stage_bytes = L->slots * L->SR;
-      L->nst = 0;
-      const int rest = plan_rest(P, kGuK * 4 * 128, kGuRows * 9, L) + 16 * 8;
-      L->nst = std::min(8, (kMaxSmem - rest) / L->stage_bytes);
-      if (L->nst >= 3) {
-        plan_rest(P, kGuK * 4 * 128, kGuRows * 9, L);
-        return Q8D_OK;
-      }
-      if (al && s <= 8) break;  // (aligned slices are whole groups of 8 blocks)
+  // two blocks a warp in a stage, or one where that leaves fewer than three
+  // stages
+  for (int tg = group_tokens(P); tg >= 1; tg /= 2)
+    for (int s = std::min(16, L->bpr); s >= std::min(8, L->bpr); s = s > 8 ? 8 : s - 1) {
+      plan_stage(P, s, al, tg, L);
+      if (plan_ring(P, 3, 8, kGuK * 4 * 128, kGuRows * 9, L)) return Q8D_OK;
     }
-  }
   return Q8D_EUNSUPPORTED;
 }
 
 int plan_down(const MoeParams& P, int sms, MoePlan* L) {
-  const int bpr = P.ffn / kQBlock;
-  const bool al = bpr % 8 == 0;
-  plan_x(P, bpr, 80 * 1024, 4, L);
-  // the warp count in 8 .. 16 that splits a row's blocks most evenly
+  const bool al = P.ffn / kQBlock % 8 == 0;
+  L->bpr = P.ffn / kQBlock;
+  // Few blocks a row: eight warps, since every warp pays for an item's
+  // bookkeeping; long rows: as many as split them evenly.
+  const int bpr = L->bpr;
+  int W = 8;
   double best = 0.0;
-  for (int w = kDnMaxWarps; w >= 8; --w) {
-    const double eff = (double)bpr / (w * ((bpr + w - 1) / w));
-    if (eff > best + 1e-9) {
-      best = eff;
-      L->W = w;
-    }
-  }
-  for (int w = L->W;; w = 8) {
-    L->W = L->KW = w;
-    // rows a CTA: an equal share of the output, in as few passes as 32 rows
-    // at a time allow
-    for (int most = 32; most >= 16; most -= 16) {
-      const int passes = (P.hidden + sms * most - 1) / (sms * most);
-      L->rows = std::min(most, (P.hidden + sms * passes - 1) / (sms * passes));
-      L->mt = L->rows > 16 ? 2 : 1;
-      L->slots = L->mt * 16;
-      const int table = w * L->mt * 16 * (P.m | 1);
-      for (int s = std::min(bpr, 64); s >= 1; s = al ? s - 8 : s - std::max(1, s / 8)) {
-        L->S = al ? s / 8 * 8 : s;
-        L->nsl = (bpr + L->S - 1) / L->S;
-        L->S = (bpr + L->nsl - 1) / L->nsl;  // (equal slices)
-        if (al) L->S = (L->S + 7) / 8 * 8;
-        L->SR = slot_bytes(L->S, al);
-        L->stage_bytes = L->slots * L->SR;
-        L->nst = 0;
-        const int rest = plan_rest(P, table, 0, L) + 16 * 12;
-        if (rest < kMaxSmem) L->nst = std::min(12, (kMaxSmem - rest) / L->stage_bytes);
-        if (L->nst >= 4) {
-          plan_rest(P, table, 0, L);
-          return Q8D_OK;
-        }
+  if (bpr >= 48)
+    for (int w = kDnMaxWarps; w >= 12; --w) {
+      const double eff = (double)bpr / (w * ((bpr + w - 1) / w));
+      if (eff > best + 1e-9) {
+        best = eff;
+        W = w;
       }
     }
-    if (w == 8) return Q8D_EUNSUPPORTED;
-  }
+  for (int tg = group_tokens(P); tg >= 1; tg /= 2)
+    for (int w = W; w >= 8; w -= w > 8 ? w - 8 : 1)
+      for (int most = 32; most >= 16; most -= 16) {
+        // rows a CTA: an equal share of the output, in as few passes as
+        // `most` rows at a time allow
+        const int passes = (P.hidden + sms * most - 1) / (sms * most);
+        L->W = w;
+        L->rows = std::min(most, (P.hidden + sms * passes - 1) / (sms * passes));
+        L->mt = L->rows > 16 ? 2 : 1;
+        L->slots = L->mt * 16;
+        const int table = w * L->slots * (P.m | 1);
+        for (int s = std::min(bpr, 56); s >= std::min(bpr, 8); s -= 8) {  // (a row's lines: a producer thread each)
+          plan_stage(P, s, al, tg, L);
+          if (plan_ring(P, 4, 12, table, 0, L)) return Q8D_OK;
+        }
+      }
+  return Q8D_EUNSUPPORTED;
 }
 
 }  // namespace
@@ -879,9 +950,7 @@ int plan_down(const MoeParams& P, int sms, MoePlan* L) {
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k) {
   (void)n_experts;
   const size_t pairs = (size_t)m * top_k;
-  return up16(4 * pairs) * 2 + (size_t)m * (hidden / kQBlock) * kImgBlock +
-         4 * (size_t)m * inv_pitch(hidden / kQBlock) + pairs * (ffn / kQBlock) * kImgBlock +
-         4 * pairs * inv_pitch(ffn / kQBlock);
+  return up16(4 * pairs) * 2 + (size_t)m * (hidden / kQBlock) * kImgBlock + pairs * (ffn / kQBlock) * kImgBlock;
 }
 
 int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
@@ -892,10 +961,6 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   ws += (size_t)P.m * bx * kImgBlock;
   P.himg = ws;
   ws += pairs * bh * kImgBlock;
-  P.xinv = reinterpret_cast<float*>(ws);
-  ws += 4 * (size_t)P.m * inv_pitch(bx);
-  P.hinv = reinterpret_cast<float*>(ws);
-  ws += 4 * pairs * inv_pitch(bh);
   if (!P.experts) P.experts = reinterpret_cast<int*>(ws);
   ws += up16(4 * pairs);
   if (!P.weights) P.weights = reinterpret_cast<float*>(ws);
@@ -933,10 +998,10 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, rt_fns[per - 1], P, per, gal);
   if (e != cudaSuccess) return record_cuda(e);
-  rc = launch_ex(gu_fn, dim3(sms), dim3((gu.W + 2) * 32), (size_t)gu.smem, stream, true, P, gu, dal);
+  rc = launch_ex(gu_fn, dim3(sms), dim3((gu.W + kProducers) * 32), (size_t)gu.smem, stream, true, P, gu, dal);
   if (rc) return rc;
   const int chunks = (P.hidden + dn.rows - 1) / dn.rows;
-  return launch_ex(dn_fn, dim3(std::min(sms, chunks)), dim3((dn.W + 2) * 32), (size_t)dn.smem, stream, true, P, dn);
+  return launch_ex(dn_fn, dim3(std::min(sms, chunks)), dim3((dn.W + kProducers) * 32), (size_t)dn.smem, stream, true, P, dn);
 }
 
 }  // namespace q8d

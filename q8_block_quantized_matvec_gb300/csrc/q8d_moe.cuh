@@ -23,10 +23,9 @@ struct MoeParams {
   int* experts;    // [m][top_k] (the caller's, or in the workspace)
   float* weights;  // [m][top_k]
   int* d_err;
-  // activation images in the workspace (q8d_moe.cu): rows of 128 bytes a
-  // block of 32, and the blocks' inverse scales (rows padded to 4 floats)
+  // activation images in the workspace (q8d_moe.cu): rows of 144 bytes a
+  // block of 32
   uint8_t *ximg, *himg;  // [m], [m * top_k]
-  float *xinv, *hinv;
 };
 
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);
