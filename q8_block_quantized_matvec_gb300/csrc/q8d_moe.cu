@@ -559,9 +559,33 @@ __device__ __forceinline__ void stage_blocks(const uint32_t (&ro)[kTiles][2], ui
   }
 }
 
+// Bounded wait that gives up when another thread of the CTA has.  (try_wait
+// without a time hint: with one it polls through nanosleep, and twenty
+// waiting warps then take the issue slots of those that work.)
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
+// A place in the ring: stage s, filled for the ph-th time (parity).
+struct Cursor {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int nst) {
+    if (++s == nst) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
 // One warp's wait on a barrier that lane 0 polls.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
-  const int ok = lane ? 1 : (wait_or_abort(bar, parity, abort) ? 1 : 0);
+  const int ok = lane ? 1 : (ring_wait(bar, parity, abort) ? 1 : 0);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -606,15 +630,16 @@ __global__ void __launch_bounds__((kGuWarps + kProducers) * 32, 1)
     const bool first = warp == kGuWarps;
     const uint64_t keep = policy_evict_last();
     fence_proxy_async_global();  // (the images were written by ordinary stores)
+    Cursor R;
     int issued = 0;
     bool ok = true;
-    for (int q = q0; q < q1 && ok; ++q) {
-      const int it = q / nq;
+    for (int q = q0, it = q0 / nq; q < q1 && ok; ++q) {
+      if (q >= (it + 1) * nq) ++it;
       const int2 I = S.item[it];
       const long long r0 = ((long long)(I.x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows) * rb;
-      for (int sl = 0; sl < L.nsl; ++sl, ++issued) {
-        const int s = issued % L.nst;
-        if (issued >= L.nst) ok = warp_wait(&S.empty[s], (uint32_t)(issued / L.nst - 1) & 1u, &s_abort, lane);
+      for (int sl = 0; sl < L.nsl; ++sl, ++issued, R.next(L.nst)) {
+        const int s = R.s;
+        if (issued >= L.nst) ok = warp_wait(&S.empty[s], R.ph ^ 1u, &s_abort, lane);
         if (!ok) break;
         const uint32_t st = smem32 + (uint32_t)s * (uint32_t)L.stage_bytes;
         const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
@@ -636,9 +661,9 @@ __global__ void __launch_bounds__((kGuWarps + kProducers) * 32, 1)
     const uint32_t x0 = xoff + (uint32_t)(min(2 * cq, L.tg - 1) * L.XR);
     const uint32_t x1 = xoff + (uint32_t)(min(2 * cq + 1, L.tg - 1) * L.XR);
     float* hq = reinterpret_cast<float*>(smem + L.o_hq);  // [32 rows][8 tokens + 1]
-    int stage = 0;
-    for (int q = q0; q < q1; ++q) {
-      const int it = q / nq;
+    Cursor R;
+    for (int q = q0, it = q0 / nq; q < q1; ++q) {
+      if (q >= (it + 1) * nq) ++it;
       const int2 I = S.item[it];
       const int ntok = I.x >> 16;
       const long long r0 = (long long)(I.x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows;
@@ -654,9 +679,9 @@ __global__ void __launch_bounds__((kGuWarps + kProducers) * 32, 1)
         ro[t][0] = (uint32_t)(r * L.SR);
         ro[t][1] = (uint32_t)((kGuRows + r) * L.SR);
       }
-      for (int sl = 0; sl < L.nsl; ++sl, ++stage) {
-        const int s = stage % L.nst;
-        wait_or_abort(&S.full[s], (uint32_t)(stage / L.nst) & 1u, &s_abort);
+      for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
+        const int s = R.s;
+        ring_wait(&S.full[s], R.ph, &s_abort);
         const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
         const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
         uint32_t ra[kGuTiles][2];
@@ -723,34 +748,50 @@ __global__ void __launch_bounds__((kDnMaxWarps + kProducers) * 32, 1) moe_down_k
     const FillLane F = fill_lane<kAl>(L, tid);
     const bool first = warp == W;
     const uint64_t keep = policy_evict_last();
-    // stage i of this CTA: its weights, its images
-    const auto weights = [&](int i) {
-      const int x = i % per, c0 = x % L.nsl * L.S, r0 = (blockIdx.x + i / per * gridDim.x) * L.rows;
-      fill_rows<kAl>(L, F, smem32 + (uint32_t)(i % L.nst) * (uint32_t)L.stage_bytes, P.wd,
-                     ((long long)(S.item[x / L.nsl].x & 0xffff) * P.hidden + r0) * rb, min(L.rows, P.hidden - r0), c0,
-                     min(L.S, L.bpr - c0), mat);
-      cp_arrive(&S.full[i % L.nst]);
+    // a place in this CTA's sequence of stages: chunk of rows, item, slice
+    struct Place {
+      Cursor R;
+      int ch, it = 0, sl = 0;
+      __device__ void next(const MoePlan& L, int items) {
+        R.next(L.nst);
+        if (++sl == L.nsl) {
+          sl = 0;
+          if (++it == items) {
+            it = 0;
+            ch += gridDim.x;
+          }
+        }
+      }
     };
-    const auto images = [&](int i) {
-      const int x = i % per, c0 = x % L.nsl * L.S, s = i % L.nst;
-      const int2 I = S.item[x / L.nsl];
-      fill_images(L, smem + (size_t)s * L.stage_bytes + L.slots * L.SR, &S.full[s], I.x >> 16, c0,
+    const auto weights = [&](const Place& p) {
+      const int c0 = p.sl * L.S, r0 = p.ch * L.rows;
+      fill_rows<kAl>(L, F, smem32 + (uint32_t)p.R.s * (uint32_t)L.stage_bytes, P.wd,
+                     ((long long)(S.item[p.it].x & 0xffff) * P.hidden + r0) * rb, min(L.rows, P.hidden - r0), c0,
+                     min(L.S, L.bpr - c0), mat);
+      cp_arrive(&S.full[p.R.s]);
+    };
+    const auto images = [&](const Place& p) {
+      const int c0 = p.sl * L.S;
+      const int2 I = S.item[p.it];
+      fill_images(L, smem + (size_t)p.R.s * L.stage_bytes + L.slots * L.SR, &S.full[p.R.s], I.x >> 16, c0,
                   min(L.S, L.bpr - c0),
                   [&](int n) { return P.himg + (size_t)(I.y + n) * L.bpr * kImgBlock; }, keep, lane);
     };
     // Weights depend on nothing in flight: the first ring of them comes while
     // the gate / up kernel ends.
     const int ring = min(total, L.nst);
+    Place w, x;
+    w.ch = x.ch = blockIdx.x;
     int i = 0;
-    for (; i < ring; ++i) weights(i);
+    for (; i < ring; ++i, w.next(L, S.n_items)) weights(w);
     griddep_wait();  // (h)
     fence_proxy_async_global();
     if (first)
-      for (int k = 0; k < ring; ++k) images(k);
-    for (; i < total; ++i) {
-      if (!warp_wait(&S.empty[i % L.nst], (uint32_t)(i / L.nst - 1) & 1u, &s_abort, lane)) break;
-      if (first) images(i);
-      weights(i);
+      for (int k = 0; k < ring; ++k, x.next(L, S.n_items)) images(x);
+    for (; i < total; ++i, w.next(L, S.n_items)) {
+      if (!warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+      if (first) images(w);
+      weights(w);
     }
     if (first) drain(L, S, i, &s_abort);
   } else {
@@ -763,7 +804,7 @@ __global__ void __launch_bounds__((kDnMaxWarps + kProducers) * 32, 1) moe_down_k
     const uint32_t x1 = xoff + (uint32_t)(min(2 * cq + 1, L.tg - 1) * L.XR);
     const int yp = P.m | 1;                                 // table pitch (odd: rows in distinct banks)
     float* tab = S.part + (size_t)warp * L.mt * 16 * yp;    // this warp's [rows][tokens]
-    int stage = 0;
+    Cursor R;
     for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
       const int r0 = ch * L.rows, nr = min(L.rows, P.hidden - r0);
       for (int i = lane; i < L.mt * 16 * yp; i += 32) tab[i] = 0.f;
@@ -775,9 +816,9 @@ __global__ void __launch_bounds__((kDnMaxWarps + kProducers) * 32, 1) moe_down_k
         float y[kTiles][4];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
-        for (int sl = 0; sl < L.nsl; ++sl, ++stage) {
-          const int s = stage % L.nst;
-          wait_or_abort(&S.full[s], (uint32_t)(stage / L.nst) & 1u, &s_abort);
+        for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
+          const int s = R.s;
+          ring_wait(&S.full[s], R.ph, &s_abort);
           const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
           const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
           uint32_t ro[kTiles][2];
