@@ -1,18 +1,22 @@
 // A mixture-of-experts feed-forward layer over Q8_0 experts for a few tokens,
-// in three launches that overlap (programmatic dependents):
+// in four launches that overlap (programmatic dependents):
 //  1. router: logits, choice and weights, and the tokens' operand image;
 //  2. gate / up: h = silu(Wg x) * (Wu x) of every (token, chosen expert);
-//  3. down: y = residual + sum over a token's experts of w * Wd h.
+//  3. down: w * Wd h of every (token, chosen expert);
+//  4. y = residual + the sum of a token's experts' rows.
 //
 // What bounds it is reading the chosen experts' matrices once from HBM: with
 // m tokens choosing k of E, 2 and 3 stream about E (1 - (1 - k/E)^m) experts
 // of 34 bytes a block of 32, and a token adds only a column to each product.
-// So both are streaming kernels: four producer warps keep a ring of shared
-// memory stages filled with 16-byte cp.async copies (every row of a stage in a
-// slot of its own, slots 4 (mod 8) words apart so that eight rows' words lie in
-// distinct banks; bulk copies of such short pieces issue a lane at a time and
-// held the stream to 6 bytes a cycle and SM), and up to sixteen consumer warps
-// multiply with mma.sync m16n8k16:
+// So both are streaming kernels: producer warps keep a ring of shared memory
+// stages filled, and sixteen consumer warps multiply with mma.sync m16n8k16.
+// Where rows are whole 16-byte lines (a multiple of 8 blocks) one TMA tensor
+// copy brings 8 blocks of 32 or 64 rows, 272 bytes a row: rows then lie 4 (mod
+// 32) banks apart and eight rows' words in distinct banks without padding.
+// (What feeds the ring is a matter of instructions: a lone warp takes some 5
+// cycles for each, and bulk or cp.async copies a row piece cost it 2000 and
+// more for a stage that HBM fills in 1500.)  Other rows come as 16-byte
+// cp.async copies into padded slots.
 //  * A: sixteen weight rows, a lane's word of four quants made two exact f16
 //    pairs (one PRMT and one subtraction a pair); B: up to eight tokens of
 //    the expert; the warps split the blocks of a row.
@@ -27,15 +31,19 @@
 //    convert.
 //  * An expert's tokens are taken eight at a time (fewer where long rows
 //    leave no room); experts nobody chose are not touched.
-//  * gate / up: a work unit is 32 rows of an expert (32 gate and 32 up rows:
-//    64 slots, four A tiles that share every B load), units dealt to the CTAs
-//    in contiguous ranges.  down: a CTA owns a few output rows of every
-//    expert, so the weighted sum over experts needs no other CTA; each warp
-//    adds its share of every expert into a table of its own, and the tables
-//    are added once, in order.  No atomics on results anywhere: the same
-//    bits every time.
+//  * A work unit is 64 slots of rows of one expert (32 gate and 32 up rows,
+//    or 64 down rows): four A tiles that share every B load.  Units are dealt
+//    to the CTAs in contiguous ranges.  (Giving each CTA a few output rows of
+//    every expert instead saves launch 4 but has every CTA fetch every h, 2.3
+//    bytes for one of weights at 64 tokens, and one tile per B load: 118
+//    against 62 us for the down products of moe_64.)
+//  * Sums are taken in a fixed order throughout and nothing is added to
+//    memory atomically: the same bits every time.
+#include <cuda.h>
+
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "q8d_gemv.cuh"
 #include "q8d_internal.cuh"
@@ -284,19 +292,18 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
 
 // ---- 2, 3. the products -----------------------------------------------------
 
-constexpr int kProducers = 4;  // producer warps (the first brings the images too)
+constexpr int kProducers = 4;  // producer warps (with tensor copies one brings the weights, one the images)
+constexpr int kSubBytes = 64 * 8 * kQBlockBytes;  // 64 row slots of 8 blocks
 
 // How a product kernel lays out its shared memory (host plan).
 struct MoePlan {
   int bpr;          // blocks a row
   int S, nsl;       // blocks a slice, slices a row
-  int SR;           // slot bytes
-  int slots;        // row slots of a stage
+  int SR;           // slot bytes (tensor copies: of 8 blocks)
+  int x_off;        // the images' offset in a stage
   int tg;           // tokens a group (1, 2, 4 or 8)
   int XR;           // image bytes a token of a stage
   int stage_bytes, nst;
-  int W;            // consumer warps
-  int rows, mt;     // down: output rows a CTA takes at once, A tiles of 16
   int items;        // (expert, token group) pairs at most
   int o_part, o_hq, o_mask, o_ebase, o_item, o_tok, o_bar;  // offsets
   int smem;
@@ -306,10 +313,11 @@ struct MoeShared {
   uint8_t* smem;
   float* part;
   unsigned long long* mask;  // [E] tokens of an expert
-  int* ebase;                // [E] first item (low half) and first pair row (high half)
-  int2* item;                // (expert | tokens << 16, first pair row)
-  float* pw;                 // [pairs] weight of a pair row
-  uint8_t* ptok;             // [pairs] token of a pair row
+  int* ebase;                // [E] first item (low half) and first row (high half)
+  int2* item;                // (expert | tokens << 16, first row)
+  float* pw;                 // [pairs] weight of a row
+  unsigned short* ppair;     // [pairs] pair (token * top_k + slot) of a row
+  unsigned short* ptok;      // [pairs] its token
   uint64_t *full, *empty;
   int n_items;
 };
@@ -322,30 +330,51 @@ __device__ __forceinline__ MoeShared carve(const MoePlan& L, uint8_t* smem, int 
   S.ebase = reinterpret_cast<int*>(smem + L.o_ebase);
   S.item = reinterpret_cast<int2*>(smem + L.o_item);
   S.pw = reinterpret_cast<float*>(smem + L.o_tok);
-  S.ptok = smem + L.o_tok + 4 * pairs;
+  S.ppair = reinterpret_cast<unsigned short*>(S.pw + pairs);
+  S.ptok = S.ppair + pairs;
   S.full = reinterpret_cast<uint64_t*>(smem + L.o_bar);
   S.empty = S.full + L.nst;
   S.n_items = 0;
   return S;
 }
 
+constexpr int kConsumers = 16;                              // consumer warps
+// The consumer warps are kGroups groups that take stages in turn: warps of
+// one stage load, decode and multiply at the same time, so groups on other
+// stages keep the pipes they do not use busy (one group of sixteen: 97 us of
+// arithmetic in the gate / up products of moe_64).
+constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups;
+constexpr int kThreads = (kConsumers + kProducers) * 32;
+constexpr int kPairsThread = (kMoeMaxTokens * kMoeMaxTop + kThreads - 1) / kThreads;
+
 // Groups the (token, slot) pairs by expert, in every CTA alike: experts in
 // order, an expert's tokens in order; a pair's row is its place in that
 // order.  The whole CTA calls.
 __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) {
   __shared__ int s_items;
-  const int pairs = P.m * P.top_k, E = P.n_experts, nthr = blockDim.x;
-  for (int e = threadIdx.x; e < E; e += nthr) S.mask[e] = 0ull;
+  const int pairs = P.m * P.top_k, E = P.n_experts;
+  int ex[kPairsThread];
+  float we[kPairsThread];
+#pragma unroll
+  for (int i = 0; i < kPairsThread; ++i) {
+    const int p = threadIdx.x + i * kThreads;
+    ex[i] = p < pairs ? __ldcg(P.experts + p) : 0;
+    we[i] = p < pairs ? __ldcg(P.weights + p) : 0.f;
+  }
+  for (int e = threadIdx.x; e < E; e += kThreads) S.mask[e] = 0ull;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L.nst; ++i) {
-      mbar_init(&S.full[i], kProducers * 32 + 1);
-      mbar_init(&S.empty[i], L.W);
+      mbar_init(&S.full[i], L.bpr % 8 ? kProducers * 32 : 2);
+      mbar_init(&S.empty[i], kGroupWarps);
     }
     fence_barrier_init();
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += nthr)
-    atomicOr(&S.mask[__ldcg(P.experts + p)], 1ull << (p / P.top_k));
+#pragma unroll
+  for (int i = 0; i < kPairsThread; ++i) {
+    const int p = threadIdx.x + i * kThreads;
+    if (p < pairs) atomicOr(&S.mask[ex[i]], 1ull << (p / P.top_k));
+  }
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (E + 31) / 32;
@@ -373,11 +402,16 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
     if (lane == 31) s_items = incl & 0xffff;
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += nthr) {
-    const int e = __ldcg(P.experts + p), t = p / P.top_k;
-    const int row = (S.ebase[e] >> 16) + __popcll(S.mask[e] & ((1ull << t) - 1ull));
-    S.ptok[row] = (uint8_t)t;
-    S.pw[row] = __ldcg(P.weights + p);
+#pragma unroll
+  for (int i = 0; i < kPairsThread; ++i) {
+    const int p = threadIdx.x + i * kThreads;
+    if (p < pairs) {
+      const int tok = p / P.top_k;
+      const int row = (S.ebase[ex[i]] >> 16) + __popcll(S.mask[ex[i]] & ((1ull << tok) - 1ull));
+      S.ptok[row] = (unsigned short)tok;
+      S.ppair[row] = (unsigned short)p;
+      S.pw[row] = we[i];
+    }
   }
   __syncthreads();
   S.n_items = s_items;
@@ -392,65 +426,100 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// A producer thread's share of a stage's rows: 16-byte line c of rows rg,
-// rg + step, ..  (Fixed for the kernel: the copy loops only add.)
-struct FillLane {
-  int c, rg, step;
-};
-template <bool kAl>
-__device__ __forceinline__ FillLane fill_lane(const MoePlan& L, int tid) {
-  const int len = L.S * kQBlockBytes;
-  const int cpr = kAl ? len / 16 : (len + 29) / 16;  // lines a row, at most
-  FillLane F;
-  F.step = kProducers * 32 / cpr;
-  F.rg = tid / cpr;
-  F.c = tid - F.rg * cpr;
-  if (F.rg >= F.step) F.rg = 1 << 20;  // (no rows)
-  return F;
-}
+__device__ __forceinline__ uint32_t token_off(int XR, int t) { return (uint32_t)(t * XR + (t >> 1) * 16); }
 
-// Copies blocks [c0, c0 + nb) of n consecutive rows, the first at byte `off`
-// of its matrix, into slots from `dst` on.  Rows start on any even byte
-// unless kAl, so the copy covers the 16-byte lines a row touches (no byte
-// past the matrix).
-template <bool kAl>
-__device__ __forceinline__ void fill_rows(const MoePlan& L, const FillLane& F, uint32_t dst, const uint8_t* base,
-                                          long long off, int n, int c0, int nb, long long mat_bytes) {
-  const int rb = L.bpr * kQBlockBytes, len = nb * kQBlockBytes;
-  if (F.c * 16 >= (kAl ? len : len + 14)) return;
-  const long long step = (long long)F.step * rb;
-  const uint32_t dstep = (uint32_t)(F.step * L.SR);
-  long long a = off + (long long)F.rg * rb + (long long)c0 * kQBlockBytes;
-  dst += (uint32_t)(F.rg * L.SR + F.c * 16);
-  if constexpr (kAl) {
-    const uint8_t* src = base + a + F.c * 16;
-#pragma unroll 4
-    for (int r = F.rg; r < n; r += F.step) {
-      cp16(dst, src, 16);
-      src += step;
-      dst += dstep;
-    }
-  } else {
-    const long long last = mat_bytes - F.c * 16;
-#pragma unroll 2
-    for (int r = F.rg; r < n; r += F.step) {
-      const long long lo = a & ~15LL, left = last - lo;
-      if (left > 0) cp16(dst, base + lo + F.c * 16, left < 16 ? (int)left : 16);
-      a += step;
-      dst += dstep;
-    }
-  }
+// Rows [y, y + box) of blocks x / 68 .. of a matrix (box: the tensor map's).
+__device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                           uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
 }
 
 // One warp: blocks [c0, c0 + nb) of n <= 8 tokens' images (token i's at
 // img(i)), a bulk copy each.
 template <typename ImgFn>
-__device__ __forceinline__ void fill_images(const MoePlan& L, uint8_t* dst, uint64_t* full, int n, int c0, int nb,
+__device__ __forceinline__ void bulk_images(const MoePlan& L, uint8_t* dst, uint64_t* full, int n, int c0, int nb,
                                             ImgFn img, uint64_t pol, int lane) {
   const uint32_t bytes = (uint32_t)nb * kImgBlock;
   if (lane == 0) mbar_arrive_expect_tx(full, bytes * n);
   __syncwarp();
-  if (lane < n) bulk_g2s(dst + lane * L.XR, img(lane) + (size_t)c0 * kImgBlock, bytes, full, pol);
+  if (lane < n) bulk_g2s(dst + token_off(L.XR, lane), img(lane) + (size_t)c0 * kImgBlock, bytes, full, pol);
+}
+
+// A producer thread's share of a stage's rows: 16-byte line c of rows rg,
+// rg + step, ..  (Fixed for the kernel: the copy loops only add.)
+struct FillLane {
+  int c, rg, step;
+};
+__device__ __forceinline__ FillLane fill_lane(const MoePlan& L, int tid) {
+  const int lines = (L.S * kQBlockBytes + 29) / 16;  // a row, at most
+  FillLane F;
+  F.step = kProducers * 32 / lines;
+  F.rg = tid / lines;
+  F.c = tid - F.rg * lines;
+  if (F.rg >= F.step) F.rg = 1 << 20;  // (no rows)
+  return F;
+}
+
+// Copies blocks [c0, c0 + nb) of n consecutive rows, the first at byte `off`
+// of its matrix, into slots from `dst` on.  Rows start on any even byte, so
+// the copy covers the 16-byte lines a row touches (no byte past the matrix).
+// kBatch addresses are worked out before their copies are issued.
+constexpr int kBatch = 6;
+__device__ __forceinline__ void fill_rows(const MoePlan& L, const FillLane& F, uint32_t dst, const uint8_t* base,
+                                          long long off, int n, int c0, int nb, long long mat_bytes) {
+  const int rb = L.bpr * kQBlockBytes;
+  if (F.c * 16 >= nb * kQBlockBytes + 14) return;
+  const long long a0 = off + (long long)c0 * kQBlockBytes;
+  const uint8_t* const b0 = base + F.c * 16;
+  const uint32_t d0 = dst + (uint32_t)(F.c * 16);
+  for (int r = F.rg; r < n; r += kBatch * F.step) {
+    const uint8_t* src[kBatch];
+    uint32_t d[kBatch];
+    int have[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int ru = min(r + u * F.step, n - 1);
+      const long long lo = (a0 + (long long)ru * rb) & ~15LL;
+      src[u] = b0 + lo;
+      d[u] = d0 + (uint32_t)(ru * L.SR);
+      have[u] = (int)max(0LL, min(16LL, mat_bytes - F.c * 16 - lo));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (r + u * F.step < n && have[u] > 0) cp16(d[u], src[u], have[u]);
+  }
+}
+
+// Copies blocks [c0, c0 + nb) of n tokens' images (token i's at img(i)), the
+// lines of all tokens dealt over the producer threads.  (Pairs of tokens lie
+// 16 bytes further apart: their inverse scales are in distinct banks.)
+template <typename ImgFn>
+__device__ __forceinline__ void fill_images(const MoePlan& L, uint32_t dst, int n, int c0, int nb, ImgFn img, int tid) {
+  constexpr int kU = 3;
+  const int lines = nb * (kImgBlock / 16);
+  int t = 0, c = tid;
+  while (c >= lines) c -= lines, ++t;
+  while (t < n) {
+    const uint8_t* src[kU];
+    uint32_t d[kU];
+    bool live[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      live[u] = t < n;
+      const int tt = min(t, n - 1);
+      src[u] = img(tt) + (size_t)c0 * kImgBlock + c * 16;
+      d[u] = dst + token_off(L.XR, tt) + c * 16;
+      c += kProducers * 32;
+      while (c >= lines) c -= lines, ++t;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (live[u]) cp16(d[u], src[u], 16);
+  }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -461,43 +530,43 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 
 // What a lane reads of one block: its words of kTiles A tiles, their scales,
 // its columns' operand and inverse scales.  All loads of a block are issued
-// before its arithmetic (asm volatile keeps their order), and two blocks'
-// before either's.
+// before its arithmetic (asm volatile keeps their order).
 template <int kTiles>
 struct BlockIn {
-  uint32_t w[kTiles][2][3];  // row g or g + 8: word of step 0, words of step 1
-  uint32_t d[kTiles][2];
+  uint32_t w[kTiles][2][3];  // row g or g + 8: words of steps 0 and 1, the scale (even blocks: and quants 0, 1)
   uint4 b0, b1;
   float xi0, xi1;
 };
 
-// kAl: words are aligned in odd blocks; an even block's word 7 is its first
-// two and last two quants (tc::word_quant).  Otherwise a block starts at any
-// even address, quants in order.
+// ra: where the lane's rows' blocks start.  kAl: words are aligned in odd
+// blocks; an even block's word 7 is its first two and last two quants
+// (tc::word_quant).  Otherwise a block starts at any even address, quants in
+// order.
 template <bool kAl, int kTiles>
-__device__ __forceinline__ void load_block(const uint32_t (&ra)[kTiles][2], bool even, int c, uint32_t xa, uint32_t x0,
-                                           uint32_t x1, BlockIn<kTiles>& B) {
+__device__ __forceinline__ void load_block(const uint32_t (&ra)[kTiles][2], uint32_t o, bool even, int c, uint32_t xa,
+                                           uint32_t x0, uint32_t x1, BlockIn<kTiles>& B) {
   B.b0 = lds128(xa);
   B.b1 = lds128(xa + 64u);
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t ba = ra[t][h];
-      B.d[t][h] = tc::lds16a(ba);
+      const uint32_t ba = ra[t][h] + o;
       if constexpr (kAl) {
         if (even) {
           B.w[t][h][0] = tc::lds32a(ba + 4u + 4u * c);
-          B.w[t][h][1] = tc::lds32a(ba);
-          B.w[t][h][2] = tc::lds32a(ba + (c == 3 ? 32u : 20u + 4u * c));
+          B.w[t][h][1] = tc::lds32a(ba + (c == 3 ? 32u : 20u + 4u * c));
+          B.w[t][h][2] = tc::lds32a(ba);
         } else {
           B.w[t][h][0] = tc::lds32a(ba + 2u + 4u * c);
           B.w[t][h][1] = tc::lds32a(ba + 18u + 4u * c);
+          B.w[t][h][2] = tc::lds16a(ba);
         }
       } else {
         const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
         B.w[t][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
         B.w[t][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
+        B.w[t][h][2] = tc::lds16a(ba);
       }
     }
   B.xi0 = tc::lds32f(x0 + 128u);
@@ -519,43 +588,18 @@ __device__ __forceinline__ void block_mma(const BlockIn<kTiles>& B, bool even, i
     uint32_t w0 = B.w[t][0][1], w1 = B.w[t][1][1];
     if (kAl && even) {
       const uint32_t sel = c == 3 ? 0x5432u : 0x7654u;
-      w0 = __byte_perm(w0, B.w[t][0][2], sel);
-      w1 = __byte_perm(w1, B.w[t][1][2], sel);
+      w0 = __byte_perm(B.w[t][0][2], w0, sel);
+      w1 = __byte_perm(B.w[t][1][2], w1, sel);
     }
     tc::quant_pairs(w0, a0, a2);
     tc::quant_pairs(w1, a1, a3);
     tc::mma_f16(acc, a0, a1, a2, a3, B.b1.x, B.b1.y);
     tc::mma_f16(acc, a0, a1, a2, a3, B.b1.z, B.b1.w);
-    const float d0 = f16_bits_to_f32(B.d[t][0]), d1 = f16_bits_to_f32(B.d[t][1]);
+    const float d0 = f16_bits_to_f32(B.w[t][0][2] & 0xffffu), d1 = f16_bits_to_f32(B.w[t][1][2] & 0xffffu);
     y[t][0] = fmaf(d0 * B.xi0, acc[0], y[t][0]);
     y[t][1] = fmaf(d0 * B.xi1, acc[1], y[t][1]);
     y[t][2] = fmaf(d1 * B.xi0, acc[2], y[t][2]);
     y[t][3] = fmaf(d1 * B.xi1, acc[3], y[t][3]);
-  }
-}
-
-// A warp's blocks first, first + step, .. < nb of a stage, two at a time.
-// ro: where this lane's rows' blocks start (block 0), xl, x0, x1: its image
-// words and its columns' images (block 0).
-template <bool kAl, int kTiles>
-__device__ __forceinline__ void stage_blocks(const uint32_t (&ro)[kTiles][2], uint32_t xl, uint32_t x0, uint32_t x1,
-                                             int first, int step, int nb, int c, float (&y)[kTiles][4]) {
-  const auto load = [&](int j, BlockIn<kTiles>& B) {
-    uint32_t ra[kTiles][2];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) ra[t][h] = ro[t][h] + (uint32_t)j * kQBlockBytes;
-    const uint32_t xo = (uint32_t)j * kImgBlock;
-    load_block<kAl, kTiles>(ra, !(j & 1), c, xl + xo, x0 + xo, x1 + xo, B);
-  };
-  for (int j = first; j < nb; j += 2 * step) {
-    BlockIn<kTiles> A, B;
-    const int j1 = j + step;
-    load(j, A);
-    if (j1 < nb) load(j1, B);
-    block_mma<kAl, kTiles>(A, !(j & 1), c, y);
-    if (j1 < nb) block_mma<kAl, kTiles>(B, !(j1 & 1), c, y);
   }
 }
 
@@ -566,6 +610,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volati
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
+    __nanosleep(20);
   }
   *abort = 1;
   return false;
@@ -603,279 +648,270 @@ __device__ __forceinline__ void finish(const MoeParams& P, volatile int* abort) 
   if (threadIdx.x == 0 && *abort && P.d_err) atomicOr(P.d_err, Q8D_DERR_WAIT);
 }
 
-constexpr int kGuWarps = 16, kGuK = 8;  // consumer warps; over the blocks of a row
-constexpr int kGuRows = 32;             // h rows a unit
-constexpr int kGuTiles = 2;             // A tiles (8 gate + 8 up rows) a warp
+constexpr int kSlots = 64;  // row slots of a stage
+constexpr int kTiles = 4;   // A tiles of a unit: a warp multiplies all four with its blocks
+constexpr int kGuRows = 32; // h rows of a gate / up unit: one block of the down products' rows
 
-template <bool kAl>
-__global__ void __launch_bounds__((kGuWarps + kProducers) * 32, 1)
-    moe_gate_up_kernel(const MoeParams P, const MoePlan L, bool hperm) {
+// Launches 2 (kGate) and 3.  P.ypart row p = token * top_k + slot receives
+// that pair's weighted down product.
+template <bool kAl, bool kGate>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_product_kernel(const MoeParams P, const MoePlan L, bool hperm,
+                                                                  const __grid_constant__ CUtensorMap map0,
+                                                                  const __grid_constant__ CUtensorMap map1) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_abort;
   MoeShared S = carve(L, smem, P.m * P.top_k);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s_abort = 0;
-  griddep_wait();
-  griddep_launch_dependents();  // (after the wait: the next kernel may read the choice at once)
+  // The gate / up kernel lets the down kernel start once it has itself waited
+  // for the router, so the down kernel may read the choice, and fill its ring
+  // with weights, before it waits for h.
+  if (kGate) griddep_wait();
+  griddep_launch_dependents();
   group_pairs(P, L, S);
-  const int nq = P.ffn / kGuRows;                // units an item
+  constexpr int kRows = kGate ? kGuRows : kSlots;  // rows of a unit
+  const int rows = kGate ? P.ffn : P.hidden;       // rows of a matrix
+  const int nq = (rows + kRows - 1) / kRows;       // units an item
   const long long units = (long long)S.n_items * nq;
   const int q0 = (int)(units * blockIdx.x / gridDim.x), q1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
-  if (warp >= kGuWarps) {
-    const int tid = threadIdx.x - kGuWarps * 32;
+  if (warp >= kConsumers) {
     const int rb = L.bpr * kQBlockBytes;
-    const long long mat = (long long)P.n_experts * P.ffn * rb;
+    const long long mat = (long long)P.n_experts * rows * rb;
     const uint32_t smem32 = smem_u32(smem);
-    const FillLane F = fill_lane<kAl>(L, tid);
-    const bool first = warp == kGuWarps;
-    const uint64_t keep = policy_evict_last();
-    fence_proxy_async_global();  // (the images were written by ordinary stores)
-    Cursor R;
-    int issued = 0;
-    bool ok = true;
-    for (int q = q0, it = q0 / nq; q < q1 && ok; ++q) {
-      if (q >= (it + 1) * nq) ++it;
-      const int2 I = S.item[it];
-      const long long r0 = ((long long)(I.x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows) * rb;
-      for (int sl = 0; sl < L.nsl; ++sl, ++issued, R.next(L.nst)) {
-        const int s = R.s;
-        if (issued >= L.nst) ok = warp_wait(&S.empty[s], R.ph ^ 1u, &s_abort, lane);
-        if (!ok) break;
-        const uint32_t st = smem32 + (uint32_t)s * (uint32_t)L.stage_bytes;
-        const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
-        if (first)
-          fill_images(L, smem + (size_t)s * L.stage_bytes + L.slots * L.SR, &S.full[s], I.x >> 16, c0, nb,
-                      [&](int n) { return P.ximg + (size_t)S.ptok[I.y + n] * L.bpr * kImgBlock; }, keep, lane);
-        fill_rows<kAl>(L, F, st, P.wg, r0, kGuRows, c0, nb, mat);
-        fill_rows<kAl>(L, F, st + (uint32_t)(kGuRows * L.SR), P.wu, r0, kGuRows, c0, nb, mat);
-        cp_arrive(&S.full[s]);
+    const int tid = threadIdx.x - kConsumers * 32;
+    const FillLane F = fill_lane(L, tid);
+    struct Place {  // a place in the CTA's sequence of stages: unit, its item, slice
+      Cursor R;
+      int q, it, sl = 0;
+      __device__ void next(const MoePlan& L, int nq) {
+        R.next(L.nst);
+        if (++sl == L.nsl) {
+          sl = 0;
+          if (++q >= (it + 1) * nq) ++it;
+        }
+      }
+    };
+    const auto img = [&](int row) {
+      return kGate ? P.ximg + (size_t)S.ptok[row] * L.bpr * kImgBlock : P.himg + (size_t)row * L.bpr * kImgBlock;
+    };
+    const int total = (q1 - q0) * L.nsl, ring = min(total, L.nst);
+    Place w, x;
+    w.q = x.q = q0;
+    w.it = x.it = q0 / nq;
+    int i = 0;
+    if constexpr (kAl) {
+      const int pw = warp - kConsumers;
+      if (pw == 0) {  // weights: they depend on nothing in flight, so the ring fills before h is there
+        const uint64_t pol = policy_evict_first();
+        for (; i < total; ++i, w.next(L, nq)) {
+          if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+          if (lane == 0) {
+            const int subs = min(L.S, L.bpr - w.sl * L.S) / 8, x0 = w.sl * L.S / 8 * (8 * kQBlockBytes / 4);
+            const int y0 = (S.item[w.it].x & 0xffff) * rows + (w.q - w.it * nq) * kRows;
+            const uint32_t st = smem32 + (uint32_t)w.R.s * (uint32_t)L.stage_bytes;
+            uint64_t* full = &S.full[w.R.s];
+            mbar_arrive_expect_tx(full, (uint32_t)(subs * kSubBytes));
+            for (int s = 0; s < subs; ++s) {
+              const uint32_t d = st + (uint32_t)(s * kSubBytes);
+              const int xs = x0 + s * (8 * kQBlockBytes / 4);
+              tensor_g2s(d, &map0, xs, y0, full, pol);
+              if (kGate) tensor_g2s(d + kSubBytes / 2, &map1, xs, y0, full, pol);
+            }
+          }
+          __syncwarp();
+        }
+        drain(L, S, i, &s_abort);
+      } else if (pw == 1) {
+        const uint64_t keep = policy_evict_last();
+        if (!kGate) griddep_wait();  // (h)
+        fence_proxy_async_global();  // (the images were written by ordinary stores)
+        for (; i < total; ++i, w.next(L, nq)) {
+          if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+          const int2 I = S.item[w.it];
+          bulk_images(L, smem + (size_t)w.R.s * L.stage_bytes + L.x_off, &S.full[w.R.s], I.x >> 16, w.sl * L.S,
+                      min(L.S, L.bpr - w.sl * L.S), [&](int n) { return img(I.y + n); }, keep, lane);
+        }
+        drain(L, S, i, &s_abort);
+      }
+    } else {
+      const auto weights = [&](const Place& p) {
+        const int c0 = p.sl * L.S, nb = min(L.S, L.bpr - c0), r0 = (p.q - p.it * nq) * kRows;
+        const uint32_t st = smem32 + (uint32_t)p.R.s * (uint32_t)L.stage_bytes;
+        const long long off = ((long long)(S.item[p.it].x & 0xffff) * rows + r0) * rb;
+        if constexpr (kGate) {
+          fill_rows(L, F, st, P.wg, off, kGuRows, c0, nb, mat);
+          fill_rows(L, F, st + (uint32_t)(kGuRows * L.SR), P.wu, off, kGuRows, c0, nb, mat);
+        } else {
+          fill_rows(L, F, st, P.wd, off, min(kRows, rows - r0), c0, nb, mat);
+        }
+      };
+      const auto images = [&](const Place& p) {
+        const int c0 = p.sl * L.S;
+        const int2 I = S.item[p.it];
+        fill_images(L, smem32 + (uint32_t)(p.R.s * L.stage_bytes + L.x_off), I.x >> 16, c0, min(L.S, L.bpr - c0),
+                    [&](int n) { return img(I.y + n); }, tid);
+        cp_arrive(&S.full[p.R.s]);
+      };
+      for (; i < ring; ++i, w.next(L, nq)) weights(w);
+      if (!kGate) griddep_wait();  // (h)
+      for (int k = 0; k < ring; ++k, x.next(L, nq)) images(x);
+      for (; i < total; ++i, w.next(L, nq)) {
+        if (!warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+        weights(w);
+        images(w);
       }
     }
-    if (first) drain(L, S, issued, &s_abort);
   } else {
+    if (!kGate) griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
-    const int kb = warp % kGuK, th = warp / kGuK;  // blocks kb, kb + 8, ..; tiles 2 th, 2 th + 1
     const uint32_t smem32 = smem_u32(smem);
-    const uint32_t xoff = (uint32_t)(L.slots * L.SR);
-    const uint32_t xl = xoff + (uint32_t)(min(gq, L.tg - 1) * L.XR + cq * 16);
-    const uint32_t x0 = xoff + (uint32_t)(min(2 * cq, L.tg - 1) * L.XR);
-    const uint32_t x1 = xoff + (uint32_t)(min(2 * cq + 1, L.tg - 1) * L.XR);
-    float* hq = reinterpret_cast<float*>(smem + L.o_hq);  // [32 rows][8 tokens + 1]
+    const uint32_t xoff = (uint32_t)L.x_off;
+    const uint32_t xl = xoff + token_off(L.XR, min(gq, L.tg - 1)) + (uint32_t)(cq * 16);
+    const uint32_t x0 = xoff + token_off(L.XR, min(2 * cq, L.tg - 1));
+    const uint32_t x1 = xoff + token_off(L.XR, min(2 * cq + 1, L.tg - 1));
+    float* hq = reinterpret_cast<float*>(smem + L.o_hq);  // gate: [32 rows][8 tokens + 1]
+    const int group = warp / kGroupWarps, member = warp % kGroupWarps;
+    int turn = 0;  // the group whose stage this is
     Cursor R;
     for (int q = q0, it = q0 / nq; q < q1; ++q) {
       if (q >= (it + 1) * nq) ++it;
       const int2 I = S.item[it];
-      const int ntok = I.x >> 16;
-      const long long r0 = (long long)(I.x & 0xffff) * P.ffn + (long long)(q - it * nq) * kGuRows;
-      float y[kGuTiles][4];
+      const int ntok = I.x >> 16, u = q - it * nq, r0 = u * kRows;
+      float y[kTiles][4];
 #pragma unroll
-      for (int t = 0; t < kGuTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
+      for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
       // this lane's slots, and how far into its first line each row starts
-      uint32_t ro[kGuTiles][2], mis[kGuTiles];
+      uint32_t slot[kTiles][2], mis[kTiles][2];
 #pragma unroll
-      for (int t = 0; t < kGuTiles; ++t) {
-        const int r = (2 * th + t) * 8 + gq;
-        mis[t] = kAl ? 0u : (uint32_t)(((r0 + r) * (L.bpr * kQBlockBytes)) & 15);
-        ro[t][0] = (uint32_t)(r * L.SR);
-        ro[t][1] = (uint32_t)((kGuRows + r) * L.SR);
-      }
-      for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
-        const int s = R.s;
-        ring_wait(&S.full[s], R.ph, &s_abort);
-        const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
-        const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
-        uint32_t ra[kGuTiles][2];
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int t = 0; t < kGuTiles; ++t) {
-          const uint32_t o = st + (kAl ? 0u : (mis[t] + (uint32_t)c0 * kQBlockBytes) & 15u);
-          ra[t][0] = ro[t][0] + o;
-          ra[t][1] = ro[t][1] + o;
+        for (int h = 0; h < 2; ++h) {
+          const int s = kGate ? 32 * h + 8 * t + gq : 16 * t + 8 * h + gq;
+          const int r = kGate ? 8 * t + gq : s;
+          slot[t][h] = (uint32_t)(s * L.SR);
+          mis[t][h] =
+              kAl ? 0u : (uint32_t)((((long long)(I.x & 0xffff) * rows + r0 + r) * (L.bpr * kQBlockBytes)) & 15);
         }
-        stage_blocks<kAl, kGuTiles>(ra, st + xl, st + x0, st + x1, kb, kGuK, nb, cq, y);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.empty[s]);
-      }
-      // the warps' shares of the unit: [kb][tile][row of 16][token]
+      for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
+        const bool mine = turn == group;
+        turn = turn + 1 == kGroups ? 0 : turn + 1;
+        if (!mine) continue;
+        ring_wait(&S.full[R.s], R.ph, &s_abort);
+        const uint32_t st = after_wait(smem32 + (uint32_t)R.s * (uint32_t)L.stage_bytes);
+        const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
+        for (int j = member; j < nb; j += kGroupWarps) {
+          uint32_t ra[kTiles][2];
 #pragma unroll
-      for (int t = 0; t < kGuTiles; ++t) {
-        float* p = S.part + ((kb * 4 + 2 * th + t) * 16 + gq) * 8 + 2 * cq;
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              ra[t][h] = slot[t][h] + (kAl ? 0u : (mis[t][h] + (uint32_t)c0 * kQBlockBytes) & 15u);
+          const uint32_t xo = st + (uint32_t)(j * kImgBlock);
+          BlockIn<kTiles> B;
+          // (tensor copies: sub-stages of 8 blocks)
+          const uint32_t jo = kAl ? (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes)
+                                  : (uint32_t)(j * kQBlockBytes);
+          load_block<kAl, kTiles>(ra, st + jo, !(j & 1), cq, xo + xl, xo + x0, xo + x1, B);
+          block_mma<kAl, kTiles>(B, !(j & 1), cq, y);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.empty[R.s]);
+      }
+      // the warps' shares of the unit: [warp][tile][row of 16][token]
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        float* p = S.part + ((warp * kTiles + t) * 16 + gq) * 8 + 2 * cq;
         *reinterpret_cast<float2*>(p) = make_float2(y[t][0], y[t][1]);
         *reinterpret_cast<float2*>(p + 64) = make_float2(y[t][2], y[t][3]);
       }
-      consumer_sync(kGuWarps * 32);
-      if (threadIdx.x < 256) {
-        const int tile = threadIdx.x >> 6, r = (threadIdx.x >> 3) & 7, n = threadIdx.x & 7;
-        float g = 0.f, u = 0.f;
+      consumer_sync(kConsumers * 32);
+      const int n = threadIdx.x & 7;
+      if constexpr (kGate) {
+        if (threadIdx.x < 256) {
+          const int t = threadIdx.x >> 6, r = (threadIdx.x >> 3) & 7;
+          float g = 0.f, v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kGuK; ++k) {
-          g += S.part[((k * 4 + tile) * 16 + r) * 8 + n];
-          u += S.part[((k * 4 + tile) * 16 + r + 8) * 8 + n];
+          for (int k = 0; k < kConsumers; ++k) {
+            g += S.part[((k * kTiles + t) * 16 + r) * 8 + n];
+            v += S.part[((k * kTiles + t) * 16 + r + 8) * 8 + n];
+          }
+          hq[(t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
         }
-        hq[(tile * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * u;
-      }
-      consumer_sync(kGuWarps * 32);
-      if (threadIdx.x < 64) {  // the unit is block q - it * nq of its tokens' h: token n, word w
-        const int n = threadIdx.x >> 3, w = threadIdx.x & 7, b = q - it * nq;
-        float v[4];
+        consumer_sync(kConsumers * 32);
+        if (threadIdx.x < 64) {  // the unit is block u of its tokens' h: token i, word w
+          const int i = threadIdx.x >> 3, w = threadIdx.x & 7;
+          float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = hq[tc::word_quant(hperm && !(b & 1), w, k) * 9 + n];
-        image_word(v, n < ntok, P.himg + ((size_t)(I.y + n) * nq + b) * kImgBlock, w);
+          for (int k = 0; k < 4; ++k) v[k] = hq[tc::word_quant(hperm && !(u & 1), w, k) * 9 + i];
+          image_word(v, i < ntok, P.himg + ((size_t)(I.y + i) * nq + u) * kImgBlock, w);
+        }
+      } else {
+        const int r = threadIdx.x >> 3;  // 64 rows x 8 tokens
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kConsumers; ++k) v += S.part[(k * kSlots + r) * 8 + n];
+        if (n < ntok && r0 + r < rows)
+          P.ypart[(size_t)S.ppair[I.y + n] * P.hidden + r0 + r] = S.pw[I.y + n] * v;
+        consumer_sync(kConsumers * 32);  // (the shares are rewritten next)
       }
     }
   }
   finish(P, &s_abort);
 }
 
-constexpr int kDnMaxWarps = 16;
-
-template <bool kAl, int kTiles>
-__global__ void __launch_bounds__((kDnMaxWarps + kProducers) * 32, 1) moe_down_kernel(const MoeParams P, const MoePlan L) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_abort;
-  MoeShared S = carve(L, smem, P.m * P.top_k);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = L.W;
-  if (threadIdx.x == 0) s_abort = 0;
-  group_pairs(P, L, S);  // (the choice is complete: the gate / up kernel started behind it)
-  const int chunks = (P.hidden + L.rows - 1) / L.rows;
-  const int per = S.n_items * L.nsl;  // stages a chunk of rows
-  const int mine = blockIdx.x < chunks ? (chunks - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-  const int total = mine * per;
-  if (warp >= W) {
-    const int tid = threadIdx.x - W * 32;
-    const int rb = L.bpr * kQBlockBytes;
-    const long long mat = (long long)P.n_experts * P.hidden * rb;
-    const uint32_t smem32 = smem_u32(smem);
-    const FillLane F = fill_lane<kAl>(L, tid);
-    const bool first = warp == W;
-    const uint64_t keep = policy_evict_last();
-    // a place in this CTA's sequence of stages: chunk of rows, item, slice
-    struct Place {
-      Cursor R;
-      int ch, it = 0, sl = 0;
-      __device__ void next(const MoePlan& L, int items) {
-        R.next(L.nst);
-        if (++sl == L.nsl) {
-          sl = 0;
-          if (++it == items) {
-            it = 0;
-            ch += gridDim.x;
-          }
-        }
-      }
-    };
-    const auto weights = [&](const Place& p) {
-      const int c0 = p.sl * L.S, r0 = p.ch * L.rows;
-      fill_rows<kAl>(L, F, smem32 + (uint32_t)p.R.s * (uint32_t)L.stage_bytes, P.wd,
-                     ((long long)(S.item[p.it].x & 0xffff) * P.hidden + r0) * rb, min(L.rows, P.hidden - r0), c0,
-                     min(L.S, L.bpr - c0), mat);
-      cp_arrive(&S.full[p.R.s]);
-    };
-    const auto images = [&](const Place& p) {
-      const int c0 = p.sl * L.S;
-      const int2 I = S.item[p.it];
-      fill_images(L, smem + (size_t)p.R.s * L.stage_bytes + L.slots * L.SR, &S.full[p.R.s], I.x >> 16, c0,
-                  min(L.S, L.bpr - c0),
-                  [&](int n) { return P.himg + (size_t)(I.y + n) * L.bpr * kImgBlock; }, keep, lane);
-    };
-    // Weights depend on nothing in flight: the first ring of them comes while
-    // the gate / up kernel ends.
-    const int ring = min(total, L.nst);
-    Place w, x;
-    w.ch = x.ch = blockIdx.x;
-    int i = 0;
-    for (; i < ring; ++i, w.next(L, S.n_items)) weights(w);
-    griddep_wait();  // (h)
-    fence_proxy_async_global();
-    if (first)
-      for (int k = 0; k < ring; ++k, x.next(L, S.n_items)) images(x);
-    for (; i < total; ++i, w.next(L, S.n_items)) {
-      if (!warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
-      if (first) images(w);
-      weights(w);
-    }
-    if (first) drain(L, S, i, &s_abort);
-  } else {
-    griddep_wait();
-    const int gq = lane >> 2, cq = lane & 3;
-    const uint32_t smem32 = smem_u32(smem);
-    const uint32_t xoff = (uint32_t)(L.slots * L.SR);
-    const uint32_t xl = xoff + (uint32_t)(min(gq, L.tg - 1) * L.XR + cq * 16);
-    const uint32_t x0 = xoff + (uint32_t)(min(2 * cq, L.tg - 1) * L.XR);
-    const uint32_t x1 = xoff + (uint32_t)(min(2 * cq + 1, L.tg - 1) * L.XR);
-    const int yp = P.m | 1;                                 // table pitch (odd: rows in distinct banks)
-    float* tab = S.part + (size_t)warp * L.mt * 16 * yp;    // this warp's [rows][tokens]
-    Cursor R;
-    for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
-      const int r0 = ch * L.rows, nr = min(L.rows, P.hidden - r0);
-      for (int i = lane; i < L.mt * 16 * yp; i += 32) tab[i] = 0.f;
-      __syncwarp();
-      for (int it = 0; it < S.n_items; ++it) {
-        const int2 I = S.item[it];
-        const int ntok = I.x >> 16;
-        const long long e0 = (long long)(I.x & 0xffff) * P.hidden + r0;
-        float y[kTiles][4];
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
-        for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
-          const int s = R.s;
-          ring_wait(&S.full[s], R.ph, &s_abort);
-          const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
-          const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
-          uint32_t ro[kTiles][2];
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int r = 16 * t + 8 * h + gq;
-              const uint32_t mis =
-                  kAl ? 0u : (uint32_t)(((e0 + r) * (L.bpr * kQBlockBytes) + c0 * kQBlockBytes) & 15);
-              ro[t][h] = st + (uint32_t)(r * L.SR) + mis;
-            }
-          stage_blocks<kAl, kTiles>(ro, st + xl, st + x0, st + x1, warp, W, nb, cq, y);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.empty[s]);
-        }
-        // weighted into the warp's table: lane (g, c) alone owns these entries
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int n = 2 * cq + k;
-          if (n < ntok) {
-            const float w = S.pw[I.y + n];
-            float* col = tab + S.ptok[I.y + n];
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              float* a = col + (16 * t + gq) * yp;
-              float* b = a + 8 * yp;
-              *a = fmaf(w, y[t][k], *a);
-              *b = fmaf(w, y[t][2 + k], *b);
-            }
-          }
-        }
-        __syncwarp();
-      }
-      consumer_sync(W * 32);
-      for (int i = threadIdx.x; i < nr * P.m; i += W * 32) {
-        const int r = i % nr, t = i / nr;
-        float sum = P.residual ? P.residual[(long long)t * P.ldr + r0 + r] : 0.f;
-        for (int w = 0; w < W; ++w) sum += S.part[((size_t)w * L.mt * 16 + r) * yp + t];
-        P.Y[(long long)t * P.ldy + r0 + r] = sum;
-      }
-      consumer_sync(W * 32);  // (the tables are cleared next)
-    }
-  }
-  finish(P, &s_abort);
+// 4. A thread an output: the experts' rows in the order of the choice.
+__global__ void __launch_bounds__(256) moe_sum_kernel(const MoeParams P) {
   griddep_launch_dependents();
+  const int r = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  griddep_wait();
+  if (r >= P.hidden) return;
+  float y = P.residual ? P.residual[(long long)t * P.ldr + r] : 0.f;
+  const float* p = P.ypart + (size_t)t * P.top_k * P.hidden + r;
+#pragma unroll 8
+  for (int k = 0; k < P.top_k; ++k) y += p[(size_t)k * P.hidden];
+  P.Y[(long long)t * P.ldy + r] = y;
 }
 
 int up16i(int n) { return (n + 15) / 16 * 16; }
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// A slot of n blocks: a multiple of 16 bytes, 4 (mod 8) words long; rows off
-// the 16-byte boundaries may start 14 bytes in and are read 4 bytes past.
-int slot_bytes(int n, bool aligned) {
-  int b = up16i(n * kQBlockBytes + (aligned ? 0 : 18));
+// A slot of n blocks of rows off the 16-byte boundaries: they start up to 14
+// bytes in and are read 4 bytes past; 4 (mod 8) words long, so that eight
+// slots' words lie in distinct banks.
+int slot_bytes(int n) {
+  int b = up16i(n * kQBlockBytes + 18);
   while ((b / 4) % 8 != 4) b += 16;
   return b;
+}
+
+// The map of n_rows rows of bpr blocks (a multiple of 8) as 32-bit words,
+// in boxes of box_rows rows by 8 blocks.
+int weight_map(const uint8_t* w, int bpr, long long n_rows, int box_rows, CUtensorMap* map) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::mutex mu;
+  static Encode encode = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult found;
+      const cudaError_t e =
+          cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+      if (e != cudaSuccess) return record_cuda(e);
+      if (found != cudaDriverEntryPointSuccess || !fn) return record_cuda(cudaErrorNotSupported);
+      encode = reinterpret_cast<Encode>(fn);
+    }
+  }
+  const cuuint64_t dim[2] = {(cuuint64_t)bpr * kQBlockBytes / 4, (cuuint64_t)n_rows};
+  const cuuint64_t stride[1] = {(cuuint64_t)bpr * kQBlockBytes};
+  const cuuint32_t box[2] = {8 * kQBlockBytes / 4, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(w), dim, stride, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? Q8D_OK : record_cuda(cudaErrorInvalidValue);
 }
 
 // Tokens a group: about twice an expert's share of the (token, slot) pairs,
@@ -888,101 +924,48 @@ int group_tokens(const MoeParams& P) {
   return tg;
 }
 
-// Slices of S blocks, tokens and stage of a plan whose slots are set.
-void plan_stage(const MoeParams& P, int S, bool al, int tg, MoePlan* L) {
-  L->S = S;
-  L->nsl = (L->bpr + S - 1) / S;
-  L->S = (L->bpr + L->nsl - 1) / L->nsl;  // (equal slices; whole groups of 8 blocks where rows are aligned)
-  if (al) L->S = (L->S + 7) / 8 * 8;
-  L->SR = slot_bytes(L->S, al);
-  // token rows half a bank cycle apart: the two tokens of a quarter warp's
-  // 16-byte loads lie in distinct banks
-  L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
-  L->tg = tg;
-  L->stage_bytes = L->slots * L->SR + tg * L->XR;
+// Lays out a product kernel over rows of bpr blocks.  A slice is up to two
+// blocks a warp of a group, one where that leaves too few stages.
+int plan_product(const MoeParams& P, int bpr, MoePlan* L) {
+  const bool al = bpr % 8 == 0;
   const int pairs = P.m * P.top_k;
-  L->items = std::min(pairs, P.n_experts + pairs / tg);
-}
-
-// Offsets behind a ring of nst stages; sets smem.
-void plan_rest(const MoeParams& P, int nst, int part_floats, int hq_floats, MoePlan* L) {
-  const int pairs = P.m * P.top_k;
-  L->nst = nst;
-  int o = nst * L->stage_bytes;
-  L->o_part = o;
-  o += up16i(4 * part_floats);
-  L->o_hq = o;
-  o += up16i(4 * hq_floats);
-  L->o_mask = o;
-  o += 8 * P.n_experts;
-  L->o_ebase = o;
-  o = up16i(o + 4 * P.n_experts);
-  L->o_item = o;
-  o += 8 * L->items;
-  L->o_tok = o = up16i(o);
-  o += up16i(5 * pairs);
-  L->o_bar = o;
-  L->smem = o + 16 * nst;
-}
-
-// As many stages as fit, at least `least`.
-bool plan_ring(const MoeParams& P, int least, int most, int part_floats, int hq_floats, MoePlan* L) {
-  plan_rest(P, 0, part_floats, hq_floats, L);
-  const int n = L->smem < kMaxSmem ? std::min(most, (kMaxSmem - L->smem) / (L->stage_bytes + 16)) : 0;
-  if (n < least) return false;
-  plan_rest(P, n, part_floats, hq_floats, L);
-  return true;
-}
-
-int plan_gate_up(const MoeParams& P, MoePlan* L) {
-  const bool al = P.hidden / kQBlock % 8 == 0;
-  L->bpr = P.hidden / kQBlock;
-  L->W = kGuWarps;
-  L->slots = 2 * kGuRows;
-  L->rows = kGuRows;
-  L->mt = 4;
-  // two blocks a warp in a stage, or one where that leaves fewer than three
-  // stages
+  L->bpr = bpr;
   for (int tg = group_tokens(P); tg >= 1; tg /= 2)
-    for (int s = std::min(16, L->bpr); s >= std::min(8, L->bpr); s = s > 8 ? 8 : s - 1) {
-      plan_stage(P, s, al, tg, L);
-      if (plan_ring(P, 3, 8, kGuK * 4 * 128, kGuRows * 9, L)) return Q8D_OK;
+    for (int s = 16; s >= 8; s -= 8) {
+      L->nsl = (bpr + s - 1) / s;
+      L->S = (bpr + L->nsl - 1) / L->nsl;  // (equal slices; whole groups of 8 blocks where rows are aligned)
+      if (al) L->S = (L->S + 7) / 8 * 8;
+      L->SR = al ? 8 * kQBlockBytes : slot_bytes(L->S);
+      L->x_off = al ? L->S / 8 * kSubBytes : kSlots * L->SR;
+      // token rows half a bank cycle apart: the two tokens of a quarter warp's
+      // 16-byte loads lie in distinct banks
+      L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
+      L->tg = tg;
+      L->stage_bytes = (L->x_off + tg * L->XR + 64 + 127) / 128 * 128;  // (tensor copies land on 128 bytes)
+      L->items = std::min(pairs, P.n_experts + pairs / tg);
+      int o = 0;  // behind the ring
+      L->o_part = o;
+      o += kConsumers * kSlots * 8 * 4;
+      L->o_hq = o;
+      o += up16i(kGuRows * 9 * 4);
+      L->o_mask = o;
+      o += 8 * P.n_experts;
+      L->o_ebase = o;
+      o = up16i(o + 4 * P.n_experts);
+      L->o_item = o;
+      o = up16i(o + 8 * L->items);
+      L->o_tok = o;
+      o = up16i(o + 8 * pairs);
+      L->o_bar = o;
+      // A barrier's parity tells two neighbouring phases apart, no more, so a
+      // stage always belongs to the same consumer group.
+      L->nst = std::min(12, (kMaxSmem - o) / (L->stage_bytes + 16)) / kGroups * kGroups;
+      if (L->nst < std::max(3, kGroups)) continue;
+      const int ring = L->nst * L->stage_bytes;
+      for (int* f : {&L->o_part, &L->o_hq, &L->o_mask, &L->o_ebase, &L->o_item, &L->o_tok, &L->o_bar}) *f += ring;
+      L->smem = ring + o + 16 * L->nst;
+      return Q8D_OK;
     }
-  return Q8D_EUNSUPPORTED;
-}
-
-int plan_down(const MoeParams& P, int sms, MoePlan* L) {
-  const bool al = P.ffn / kQBlock % 8 == 0;
-  L->bpr = P.ffn / kQBlock;
-  // Few blocks a row: eight warps, since every warp pays for an item's
-  // bookkeeping; long rows: as many as split them evenly.
-  const int bpr = L->bpr;
-  int W = 8;
-  double best = 0.0;
-  if (bpr >= 48)
-    for (int w = kDnMaxWarps; w >= 12; --w) {
-      const double eff = (double)bpr / (w * ((bpr + w - 1) / w));
-      if (eff > best + 1e-9) {
-        best = eff;
-        W = w;
-      }
-    }
-  for (int tg = group_tokens(P); tg >= 1; tg /= 2)
-    for (int w = W; w >= 8; w -= w > 8 ? w - 8 : 1)
-      for (int most = 32; most >= 16; most -= 16) {
-        // rows a CTA: an equal share of the output, in as few passes as
-        // `most` rows at a time allow
-        const int passes = (P.hidden + sms * most - 1) / (sms * most);
-        L->W = w;
-        L->rows = std::min(most, (P.hidden + sms * passes - 1) / (sms * passes));
-        L->mt = L->rows > 16 ? 2 : 1;
-        L->slots = L->mt * 16;
-        const int table = w * L->slots * (P.m | 1);
-        for (int s = std::min(bpr, 56); s >= std::min(bpr, 8); s -= 8) {  // (a row's lines: a producer thread each)
-          plan_stage(P, s, al, tg, L);
-          if (plan_ring(P, 4, 12, table, 0, L)) return Q8D_OK;
-        }
-      }
   return Q8D_EUNSUPPORTED;
 }
 
@@ -991,7 +974,8 @@ int plan_down(const MoeParams& P, int sms, MoePlan* L) {
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k) {
   (void)n_experts;
   const size_t pairs = (size_t)m * top_k;
-  return up16(4 * pairs) * 2 + (size_t)m * (hidden / kQBlock) * kImgBlock + pairs * (ffn / kQBlock) * kImgBlock;
+  return up16(4 * pairs) * 2 + (size_t)m * (hidden / kQBlock) * kImgBlock + pairs * (ffn / kQBlock) * kImgBlock +
+         4 * pairs * hidden;
 }
 
 int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
@@ -1002,21 +986,26 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   ws += (size_t)P.m * bx * kImgBlock;
   P.himg = ws;
   ws += pairs * bh * kImgBlock;
+  P.ypart = reinterpret_cast<float*>(ws);
+  ws += 4 * pairs * P.hidden;
   if (!P.experts) P.experts = reinterpret_cast<int*>(ws);
   ws += up16(4 * pairs);
   if (!P.weights) P.weights = reinterpret_cast<float*>(ws);
 
-  const int sms = sm_count();
   MoePlan gu{}, dn{};
-  int rc = plan_gate_up(P, &gu);
-  if (!rc) rc = plan_down(P, sms, &dn);
+  int rc = plan_product(P, bx, &gu);
+  if (!rc) rc = plan_product(P, bh, &dn);
   if (rc) return rc;
   const bool gal = bx % 8 == 0, dal = bh % 8 == 0;
-  void (*const gu_fn)(MoeParams, MoePlan, bool) = gal ? moe_gate_up_kernel<true> : moe_gate_up_kernel<false>;
-  void (*const dn_fns[2][2])(MoeParams, MoePlan) = {{moe_down_kernel<false, 1>, moe_down_kernel<false, 2>},
-                                                    {moe_down_kernel<true, 1>, moe_down_kernel<true, 2>}};
-  const auto dn_fn = dn_fns[dal][dn.mt - 1];
-  rc = configure_kernel(reinterpret_cast<const void*>(gu_fn), kMaxSmem, true);
+  const auto gu_fn = gal ? moe_product_kernel<true, true> : moe_product_kernel<false, true>;
+  const auto dn_fn = dal ? moe_product_kernel<true, false> : moe_product_kernel<false, false>;
+  CUtensorMap mg{}, mu{}, md{};
+  if (gal) {
+    rc = weight_map(P.wg, bx, (long long)P.n_experts * P.ffn, kGuRows, &mg);
+    if (!rc) rc = weight_map(P.wu, bx, (long long)P.n_experts * P.ffn, kGuRows, &mu);
+  }
+  if (!rc && dal) rc = weight_map(P.wd, bh, (long long)P.n_experts * P.hidden, kSlots, &md);
+  if (!rc) rc = configure_kernel(reinterpret_cast<const void*>(gu_fn), kMaxSmem, true);
   if (!rc) rc = configure_kernel(reinterpret_cast<const void*>(dn_fn), kMaxSmem, true);
   if (rc) return rc;
 
@@ -1039,10 +1028,11 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, rt_fns[per - 1], P, per, gal);
   if (e != cudaSuccess) return record_cuda(e);
-  rc = launch_ex(gu_fn, dim3(sms), dim3((gu.W + kProducers) * 32), (size_t)gu.smem, stream, true, P, gu, dal);
+  const int sms = sm_count();
+  rc = launch_ex(gu_fn, dim3(sms), dim3(kThreads), (size_t)gu.smem, stream, true, P, gu, dal, mg, mu);
+  if (!rc) rc = launch_ex(dn_fn, dim3(sms), dim3(kThreads), (size_t)dn.smem, stream, true, P, dn, dal, md, md);
   if (rc) return rc;
-  const int chunks = (P.hidden + dn.rows - 1) / dn.rows;
-  return launch_ex(dn_fn, dim3(std::min(sms, chunks)), dim3((dn.W + kProducers) * 32), (size_t)dn.smem, stream, true, P, dn);
+  return launch_ex(moe_sum_kernel, dim3((P.hidden + 255) / 256, P.m), dim3(256), 0, stream, true, P);
 }
 
 }  // namespace q8d

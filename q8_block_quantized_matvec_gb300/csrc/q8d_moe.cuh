@@ -26,6 +26,7 @@ struct MoeParams {
   // activation images in the workspace (q8d_moe.cu): rows of 144 bytes a
   // block of 32
   uint8_t *ximg, *himg;  // [m], [m * top_k]
+  float* ypart;          // [m * top_k][hidden]
 };
 
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);
