@@ -13,10 +13,8 @@
 // Where rows are whole 16-byte lines (a multiple of 8 blocks) one TMA tensor
 // copy brings 8 blocks of 32 or 64 rows, 272 bytes a row: rows then lie 4 (mod
 // 32) banks apart and eight rows' words in distinct banks without padding.
-// (What feeds the ring is a matter of instructions: a lone warp takes some 5
-// cycles for each, and bulk or cp.async copies a row piece cost it 2000 and
-// more for a stage that HBM fills in 1500.)  Other rows come as 16-byte
-// cp.async copies into padded slots.
+// Other rows come as a bulk copy each into padded slots, by four warps (a warp
+// issues such copies a lane at a time, some 90 cycles each).
 //  * A: sixteen weight rows, a lane's word of four quants made two exact f16
 //    pairs (one PRMT and one subtraction a pair); B: up to eight tokens of
 //    the expert; the warps split the blocks of a row.
@@ -292,8 +290,13 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
 
 // ---- 2, 3. the products -----------------------------------------------------
 
-constexpr int kProducers = 4;  // producer warps (with tensor copies one brings the weights, one the images)
-constexpr int kSubBytes = 64 * 8 * kQBlockBytes;  // 64 row slots of 8 blocks
+// Producer warps.  With tensor copies the first brings the weights, the others
+// the images; else each brings a quarter of the rows and of the images.
+constexpr int kProducers = 4;
+constexpr int kSlots = 64;   // row slots of a stage
+constexpr int kTiles = 4;    // A tiles of a unit: a warp multiplies all four with its blocks
+constexpr int kGuRows = 32;  // h rows of a gate / up unit: one block of the down products' rows
+constexpr int kSubBytes = kSlots * 8 * kQBlockBytes;  // 64 row slots of 8 blocks
 
 // How a product kernel lays out its shared memory (host plan).
 struct MoePlan {
@@ -364,7 +367,7 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
   for (int e = threadIdx.x; e < E; e += kThreads) S.mask[e] = 0ull;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L.nst; ++i) {
-      mbar_init(&S.full[i], L.bpr % 8 ? kProducers * 32 : 2);
+      mbar_init(&S.full[i], kProducers);
       mbar_init(&S.empty[i], kGroupWarps);
     }
     fence_barrier_init();
@@ -417,15 +420,6 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
   S.n_items = s_items;
 }
 
-// 16 bytes, of which n exist (the others become zeros).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-// Arrives on bar once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 __device__ __forceinline__ uint32_t token_off(int XR, int t) { return (uint32_t)(t * XR + (t >> 1) * 16); }
 
 // Rows [y, y + box) of blocks x / 68 .. of a matrix (box: the tensor map's).
@@ -438,88 +432,36 @@ __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
-// One warp: blocks [c0, c0 + nb) of n <= 8 tokens' images (token i's at
-// img(i)), a bulk copy each.
+// One warp: blocks [c0, c0 + nb) of the images of tokens first, first + step,
+// .. < n (token i's at img(i)), a bulk copy each, announced by the caller.
 template <typename ImgFn>
-__device__ __forceinline__ void bulk_images(const MoePlan& L, uint8_t* dst, uint64_t* full, int n, int c0, int nb,
-                                            ImgFn img, uint64_t pol, int lane) {
-  const uint32_t bytes = (uint32_t)nb * kImgBlock;
-  if (lane == 0) mbar_arrive_expect_tx(full, bytes * n);
-  __syncwarp();
-  if (lane < n) bulk_g2s(dst + token_off(L.XR, lane), img(lane) + (size_t)c0 * kImgBlock, bytes, full, pol);
+__device__ __forceinline__ void bulk_images(const MoePlan& L, uint8_t* dst, uint64_t* full, int first, int step, int n,
+                                            int c0, int nb, ImgFn img, uint64_t pol, int lane) {
+  const int i = first + lane * step;
+  if (i < n)
+    bulk_g2s(dst + token_off(L.XR, i), img(i) + (size_t)c0 * kImgBlock, (uint32_t)nb * kImgBlock, full, pol);
 }
 
-// A producer thread's share of a stage's rows: 16-byte line c of rows rg,
-// rg + step, ..  (Fixed for the kernel: the copy loops only add.)
-struct FillLane {
-  int c, rg, step;
+// The lines that blocks [c0, c0 + nb) of a row touch: rows start on any even
+// byte (off: the row's start in its matrix).
+struct RowLines {
+  long long lo;    // the first line's start
+  uint32_t bytes;  // whole lines inside the matrix
+  long long end;   // the blocks' end
 };
-__device__ __forceinline__ FillLane fill_lane(const MoePlan& L, int tid) {
-  const int lines = (L.S * kQBlockBytes + 29) / 16;  // a row, at most
-  FillLane F;
-  F.step = kProducers * 32 / lines;
-  F.rg = tid / lines;
-  F.c = tid - F.rg * lines;
-  if (F.rg >= F.step) F.rg = 1 << 20;  // (no rows)
-  return F;
+__device__ __forceinline__ RowLines row_lines(long long off, int c0, int nb, long long mat_bytes) {
+  RowLines R;
+  const long long a = off + (long long)c0 * kQBlockBytes;
+  R.lo = a & ~15LL;
+  R.end = a + (long long)nb * kQBlockBytes;
+  const long long hi = min((R.end + 15) & ~15LL, mat_bytes & ~15LL);
+  R.bytes = (uint32_t)(hi - R.lo);
+  return R;
 }
-
-// Copies blocks [c0, c0 + nb) of n consecutive rows, the first at byte `off`
-// of its matrix, into slots from `dst` on.  Rows start on any even byte, so
-// the copy covers the 16-byte lines a row touches (no byte past the matrix).
-// kBatch addresses are worked out before their copies are issued.
-constexpr int kBatch = 6;
-__device__ __forceinline__ void fill_rows(const MoePlan& L, const FillLane& F, uint32_t dst, const uint8_t* base,
-                                          long long off, int n, int c0, int nb, long long mat_bytes) {
-  const int rb = L.bpr * kQBlockBytes;
-  if (F.c * 16 >= nb * kQBlockBytes + 14) return;
-  const long long a0 = off + (long long)c0 * kQBlockBytes;
-  const uint8_t* const b0 = base + F.c * 16;
-  const uint32_t d0 = dst + (uint32_t)(F.c * 16);
-  for (int r = F.rg; r < n; r += kBatch * F.step) {
-    const uint8_t* src[kBatch];
-    uint32_t d[kBatch];
-    int have[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int ru = min(r + u * F.step, n - 1);
-      const long long lo = (a0 + (long long)ru * rb) & ~15LL;
-      src[u] = b0 + lo;
-      d[u] = d0 + (uint32_t)(ru * L.SR);
-      have[u] = (int)max(0LL, min(16LL, mat_bytes - F.c * 16 - lo));
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (r + u * F.step < n && have[u] > 0) cp16(d[u], src[u], have[u]);
-  }
-}
-
-// Copies blocks [c0, c0 + nb) of n tokens' images (token i's at img(i)), the
-// lines of all tokens dealt over the producer threads.  (Pairs of tokens lie
-// 16 bytes further apart: their inverse scales are in distinct banks.)
-template <typename ImgFn>
-__device__ __forceinline__ void fill_images(const MoePlan& L, uint32_t dst, int n, int c0, int nb, ImgFn img, int tid) {
-  constexpr int kU = 3;
-  const int lines = nb * (kImgBlock / 16);
-  int t = 0, c = tid;
-  while (c >= lines) c -= lines, ++t;
-  while (t < n) {
-    const uint8_t* src[kU];
-    uint32_t d[kU];
-    bool live[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      live[u] = t < n;
-      const int tt = min(t, n - 1);
-      src[u] = img(tt) + (size_t)c0 * kImgBlock + c * 16;
-      d[u] = dst + token_off(L.XR, tt) + c * 16;
-      c += kProducers * 32;
-      while (c >= lines) c -= lines, ++t;
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (live[u]) cp16(d[u], src[u], 16);
-  }
+// A matrix that ends inside a line: its last bytes, by plain stores.
+__device__ __forceinline__ void row_tail(uint8_t* slot, const uint8_t* base, const RowLines& R) {
+  for (long long x = R.lo + R.bytes; x < R.end; x += 2)
+    *reinterpret_cast<unsigned short*>(slot + (x - R.lo)) = *reinterpret_cast<const unsigned short*>(base + x);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -531,75 +473,119 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // What a lane reads of one block: its words of kTiles A tiles, their scales,
 // its columns' operand and inverse scales.  All loads of a block are issued
 // before its arithmetic (asm volatile keeps their order).
-template <int kTiles>
+// kPack: at most four tokens; columns 0-3 are their hi parts, 4-7 their lo
+// parts, so one MMA a step does what two do otherwise.
+template <bool kPack>
 struct BlockIn {
   uint32_t w[kTiles][2][3];  // row g or g + 8: words of steps 0 and 1, the scale (even blocks: and quants 0, 1)
-  uint4 b0, b1;
+  uint32_t b[2][kPack ? 2 : 4];
   float xi0, xi1;
 };
 
-// ra: where the lane's rows' blocks start.  kAl: words are aligned in odd
-// blocks; an even block's word 7 is its first two and last two quants
-// (tc::word_quant).  Otherwise a block starts at any even address, quants in
-// order.
-template <bool kAl, int kTiles>
-__device__ __forceinline__ void load_block(const uint32_t (&ra)[kTiles][2], uint32_t o, bool even, int c, uint32_t xa,
-                                           uint32_t x0, uint32_t x1, BlockIn<kTiles>& B) {
-  B.b0 = lds128(xa);
-  B.b1 = lds128(xa + 64u);
+template <bool kPack>
+__device__ __forceinline__ void load_x(uint32_t xa, uint32_t x0, uint32_t x1, BlockIn<kPack>& B) {
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t ba = ra[t][h] + o;
-      if constexpr (kAl) {
-        if (even) {
-          B.w[t][h][0] = tc::lds32a(ba + 4u + 4u * c);
-          B.w[t][h][1] = tc::lds32a(ba + (c == 3 ? 32u : 20u + 4u * c));
-          B.w[t][h][2] = tc::lds32a(ba);
-        } else {
-          B.w[t][h][0] = tc::lds32a(ba + 2u + 4u * c);
-          B.w[t][h][1] = tc::lds32a(ba + 18u + 4u * c);
-          B.w[t][h][2] = tc::lds16a(ba);
-        }
-      } else {
-        const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
-        B.w[t][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
-        B.w[t][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
-        B.w[t][h][2] = tc::lds16a(ba);
-      }
+  for (int s = 0; s < 2; ++s) {
+    if constexpr (kPack) {
+      const uint2 v = tc::lds64a(xa + 64u * s);
+      B.b[s][0] = v.x;
+      B.b[s][1] = v.y;
+    } else {
+      const uint4 v = lds128(xa + 64u * s);
+      B.b[s][0] = v.x;
+      B.b[s][1] = v.y;
+      B.b[s][2] = v.z;
+      B.b[s][3] = v.w;
     }
+  }
   B.xi0 = tc::lds32f(x0 + 128u);
   B.xi1 = tc::lds32f(x1 + 128u);
 }
 
+template <int OFF>
+__device__ __forceinline__ uint32_t lds32i(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds16i(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.shared.b16 %0, [%1+%2];" : "=h"(v) : "r"(a), "n"(OFF));
+  return v;
+}
+
+// Slot of row g + 8 h of tile t, less g.
+template <bool kGate>
+__host__ __device__ constexpr int slot_of(int t, int h) {
+  return kGate ? kGuRows * h + 8 * t : 16 * t + 8 * h;
+}
+
+// Rows from tensor copies: 272 bytes a slot, so that a slot is an immediate
+// offset.  bg: block start in slot g.  Words are aligned in odd blocks; an
+// even block's word 7 is its first two and last two quants (tc::word_quant).
+template <bool kGate, bool kPack, int I = 0>
+__device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, BlockIn<kPack>& B) {
+  if constexpr (I < 2 * kTiles) {
+    constexpr int t = I / 2, h = I % 2, so = slot_of<kGate>(t, h) * 8 * kQBlockBytes;
+    if (even) {
+      B.w[t][h][0] = lds32i<so + 4>(bg + 4u * c);
+      B.w[t][h][1] = lds32i<so>(bg + (c == 3 ? 32u : 20u + 4u * c));
+      B.w[t][h][2] = lds32i<so>(bg);
+    } else {
+      B.w[t][h][0] = lds32i<so + 2>(bg + 4u * c);
+      B.w[t][h][1] = lds32i<so + 18>(bg + 4u * c);
+      B.w[t][h][2] = lds16i<so>(bg);
+    }
+    load_aligned<kGate, kPack, I + 1>(bg, even, c, B);
+  }
+}
+// Other rows: a block starts at any even address, quants in order.
+template <bool kPack>
+__device__ __forceinline__ void load_unaligned(uint32_t ba, int t, int h, int c, BlockIn<kPack>& B) {
+  const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
+  B.w[t][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
+  B.w[t][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
+  B.w[t][h][2] = tc::lds16a(ba);
+}
+
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // y[t] += the products of a loaded block: columns 2c and 2c + 1 of rows g
-// ([0], [1]) and g + 8 ([2], [3]) of tile t.
-template <bool kAl, int kTiles>
-__device__ __forceinline__ void block_mma(const BlockIn<kTiles>& B, bool even, int c, float (&y)[kTiles][4]) {
+// ([0]) and g + 8 ([1]) of tile t.
+template <bool kAl, bool kPack>
+__device__ __forceinline__ void block_mma(const BlockIn<kPack>& B, bool even, int c, uint64_t (&y)[kTiles][2]) {
+  const uint64_t xi = pack2(B.xi0, B.xi1);
+  const uint32_t sel = c == 3 ? 0x5432u : 0x7654u;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[4];
     uint32_t a0, a1, a2, a3;
     tc::quant_pairs(B.w[t][0][0], a0, a2);
     tc::quant_pairs(B.w[t][1][0], a1, a3);
-    tc::mma_f16(acc, a0, a1, a2, a3, B.b0.x, B.b0.y);
-    tc::mma_f16(acc, a0, a1, a2, a3, B.b0.z, B.b0.w);
+    mma_zero(acc, a0, a1, a2, a3, B.b[0][0], B.b[0][1]);
+    if constexpr (!kPack) tc::mma_f16(acc, a0, a1, a2, a3, B.b[0][2], B.b[0][3]);
     uint32_t w0 = B.w[t][0][1], w1 = B.w[t][1][1];
     if (kAl && even) {
-      const uint32_t sel = c == 3 ? 0x5432u : 0x7654u;
       w0 = __byte_perm(B.w[t][0][2], w0, sel);
       w1 = __byte_perm(B.w[t][1][2], w1, sel);
     }
     tc::quant_pairs(w0, a0, a2);
     tc::quant_pairs(w1, a1, a3);
-    tc::mma_f16(acc, a0, a1, a2, a3, B.b1.x, B.b1.y);
-    tc::mma_f16(acc, a0, a1, a2, a3, B.b1.z, B.b1.w);
-    const float d0 = f16_bits_to_f32(B.w[t][0][2] & 0xffffu), d1 = f16_bits_to_f32(B.w[t][1][2] & 0xffffu);
-    y[t][0] = fmaf(d0 * B.xi0, acc[0], y[t][0]);
-    y[t][1] = fmaf(d0 * B.xi1, acc[1], y[t][1]);
-    y[t][2] = fmaf(d1 * B.xi0, acc[2], y[t][2]);
-    y[t][3] = fmaf(d1 * B.xi1, acc[3], y[t][3]);
+    tc::mma_f16(acc, a0, a1, a2, a3, B.b[1][0], B.b[1][1]);
+    if constexpr (!kPack) tc::mma_f16(acc, a0, a1, a2, a3, B.b[1][2], B.b[1][3]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float d = __low2float(*reinterpret_cast<const __half2*>(&B.w[t][h][2]));
+      y[t][h] = fma2(mul2(pack2(d, d), xi), pack2(acc[2 * h], acc[2 * h + 1]), y[t][h]);
+    }
   }
 }
 
@@ -640,21 +626,15 @@ __device__ __forceinline__ void drain(const MoePlan& L, const MoeShared& S, int 
     for (int j = max(0, i - L.nst); j < i; ++j) mbar_wait(&S.full[j % L.nst], (uint32_t)(j / L.nst) & 1u);
 }
 
-// Ends a product kernel: no copy is in flight when the CTA leaves, and a wait
-// that gave up is reported.
+// Ends a product kernel: a wait that gave up is reported.
 __device__ __forceinline__ void finish(const MoeParams& P, volatile int* abort) {
-  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0 && *abort && P.d_err) atomicOr(P.d_err, Q8D_DERR_WAIT);
 }
 
-constexpr int kSlots = 64;  // row slots of a stage
-constexpr int kTiles = 4;   // A tiles of a unit: a warp multiplies all four with its blocks
-constexpr int kGuRows = 32; // h rows of a gate / up unit: one block of the down products' rows
-
 // Launches 2 (kGate) and 3.  P.ypart row p = token * top_k + slot receives
 // that pair's weighted down product.
-template <bool kAl, bool kGate>
+template <bool kAl, bool kGate, bool kPack>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_product_kernel(const MoeParams P, const MoePlan L, bool hperm,
                                                                   const __grid_constant__ CUtensorMap map0,
@@ -679,8 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rb = L.bpr * kQBlockBytes;
     const long long mat = (long long)P.n_experts * rows * rb;
     const uint32_t smem32 = smem_u32(smem);
-    const int tid = threadIdx.x - kConsumers * 32;
-    const FillLane F = fill_lane(L, tid);
     struct Place {  // a place in the CTA's sequence of stages: unit, its item, slice
       Cursor R;
       int q, it, sl = 0;
@@ -695,81 +673,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto img = [&](int row) {
       return kGate ? P.ximg + (size_t)S.ptok[row] * L.bpr * kImgBlock : P.himg + (size_t)row * L.bpr * kImgBlock;
     };
-    const int total = (q1 - q0) * L.nsl, ring = min(total, L.nst);
-    Place w, x;
-    w.q = x.q = q0;
-    w.it = x.it = q0 / nq;
+    const int total = (q1 - q0) * L.nsl, pw = warp - kConsumers;
+    const uint64_t pol = policy_evict_first(), keep = policy_evict_last();
+    Place w;
+    w.q = q0;
+    w.it = q0 / nq;
     int i = 0;
-    if constexpr (kAl) {
-      const int pw = warp - kConsumers;
-      if (pw == 0) {  // weights: they depend on nothing in flight, so the ring fills before h is there
-        const uint64_t pol = policy_evict_first();
-        for (; i < total; ++i, w.next(L, nq)) {
-          if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
-          if (lane == 0) {
-            const int subs = min(L.S, L.bpr - w.sl * L.S) / 8, x0 = w.sl * L.S / 8 * (8 * kQBlockBytes / 4);
-            const int y0 = (S.item[w.it].x & 0xffff) * rows + (w.q - w.it * nq) * kRows;
-            const uint32_t st = smem32 + (uint32_t)w.R.s * (uint32_t)L.stage_bytes;
-            uint64_t* full = &S.full[w.R.s];
-            mbar_arrive_expect_tx(full, (uint32_t)(subs * kSubBytes));
-            for (int s = 0; s < subs; ++s) {
-              const uint32_t d = st + (uint32_t)(s * kSubBytes);
-              const int xs = x0 + s * (8 * kQBlockBytes / 4);
-              tensor_g2s(d, &map0, xs, y0, full, pol);
-              if (kGate) tensor_g2s(d + kSubBytes / 2, &map1, xs, y0, full, pol);
-            }
+    // Weights depend on nothing in flight, so the down kernel fills its ring
+    // with them before it waits for h.
+    if (kAl && pw == 0) {
+      for (; i < total; ++i, w.next(L, nq)) {
+        if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+        if (lane == 0) {
+          const int subs = min(L.S, L.bpr - w.sl * L.S) / 8, x0 = w.sl * L.S / 8 * (8 * kQBlockBytes / 4);
+          const int y0 = (S.item[w.it].x & 0xffff) * rows + (w.q - w.it * nq) * kRows;
+          const uint32_t st = smem32 + (uint32_t)w.R.s * (uint32_t)L.stage_bytes;
+          uint64_t* full = &S.full[w.R.s];
+          mbar_arrive_expect_tx(full, (uint32_t)(subs * kSubBytes));
+          for (int s = 0; s < subs; ++s) {
+            const uint32_t d = st + (uint32_t)(s * kSubBytes);
+            const int xs = x0 + s * (8 * kQBlockBytes / 4);
+            tensor_g2s(d, &map0, xs, y0, full, pol);
+            if (kGate) tensor_g2s(d + kSubBytes / 2, &map1, xs, y0, full, pol);
           }
-          __syncwarp();
         }
-        drain(L, S, i, &s_abort);
-      } else if (pw == 1) {
-        const uint64_t keep = policy_evict_last();
-        if (!kGate) griddep_wait();  // (h)
-        fence_proxy_async_global();  // (the images were written by ordinary stores)
-        for (; i < total; ++i, w.next(L, nq)) {
-          if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
-          const int2 I = S.item[w.it];
-          bulk_images(L, smem + (size_t)w.R.s * L.stage_bytes + L.x_off, &S.full[w.R.s], I.x >> 16, w.sl * L.S,
-                      min(L.S, L.bpr - w.sl * L.S), [&](int n) { return img(I.y + n); }, keep, lane);
-        }
-        drain(L, S, i, &s_abort);
+        __syncwarp();
+      }
+    } else if (kAl) {
+      if (!kGate) griddep_wait();  // (h)
+      fence_proxy_async_global();  // (the images were written by ordinary stores)
+      for (; i < total; ++i, w.next(L, nq)) {
+        if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+        const int2 I = S.item[w.it];
+        const int n = I.x >> 16, c0 = w.sl * L.S, nb = min(L.S, L.bpr - c0), f = pw - 1;
+        const int mine = f < n ? (n - f + kProducers - 2) / (kProducers - 1) : 0;  // tokens f, f + 3, ..
+        if (lane == 0) mbar_arrive_expect_tx(&S.full[w.R.s], (uint32_t)(mine * nb * kImgBlock));
+        __syncwarp();
+        bulk_images(L, smem + (size_t)w.R.s * L.stage_bytes + L.x_off, &S.full[w.R.s], f, kProducers - 1, n, c0, nb,
+                    [&](int k) { return img(I.y + k); }, keep, lane);
       }
     } else {
-      const auto weights = [&](const Place& p) {
-        const int c0 = p.sl * L.S, nb = min(L.S, L.bpr - c0), r0 = (p.q - p.it * nq) * kRows;
-        const uint32_t st = smem32 + (uint32_t)p.R.s * (uint32_t)L.stage_bytes;
-        const long long off = ((long long)(S.item[p.it].x & 0xffff) * rows + r0) * rb;
-        if constexpr (kGate) {
-          fill_rows(L, F, st, P.wg, off, kGuRows, c0, nb, mat);
-          fill_rows(L, F, st + (uint32_t)(kGuRows * L.SR), P.wu, off, kGuRows, c0, nb, mat);
-        } else {
-          fill_rows(L, F, st, P.wd, off, min(kRows, rows - r0), c0, nb, mat);
-        }
-      };
-      const auto images = [&](const Place& p) {
-        const int c0 = p.sl * L.S;
-        const int2 I = S.item[p.it];
-        fill_images(L, smem32 + (uint32_t)(p.R.s * L.stage_bytes + L.x_off), I.x >> 16, c0, min(L.S, L.bpr - c0),
-                    [&](int n) { return img(I.y + n); }, tid);
-        cp_arrive(&S.full[p.R.s]);
-      };
-      for (; i < ring; ++i, w.next(L, nq)) weights(w);
-      if (!kGate) griddep_wait();  // (h)
-      for (int k = 0; k < ring; ++k, x.next(L, nq)) images(x);
+      if (!kGate) griddep_wait();
+      fence_proxy_async_global();
       for (; i < total; ++i, w.next(L, nq)) {
-        if (!warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
-        weights(w);
-        images(w);
+        if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+        const int2 I = S.item[w.it];
+        const int n = I.x >> 16, c0 = w.sl * L.S, nb = min(L.S, L.bpr - c0), r0 = (w.q - w.it * nq) * kRows;
+        uint8_t* st = smem + (size_t)w.R.s * L.stage_bytes;
+        uint64_t* full = &S.full[w.R.s];
+        // lanes 0-15: a slot each; a warp's slots are one matrix's
+        const int slot = pw * (kSlots / kProducers) + lane;
+        const uint8_t* base = kGate ? (slot < kGuRows ? P.wg : P.wu) : P.wd;
+        const int r = kGate ? slot & (kGuRows - 1) : slot;
+        const bool live = lane < kSlots / kProducers && r0 + r < rows;
+        RowLines R{};
+        if (live) {
+          R = row_lines(((long long)(I.x & 0xffff) * rows + r0 + r) * rb, c0, nb, mat);
+          row_tail(st + (size_t)slot * L.SR, base, R);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (plain stores before later copies)
+        __syncwarp();
+        const int mine = pw < n ? (n - pw + kProducers - 1) / kProducers : 0;  // tokens pw, pw + 4, ..
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, live ? R.bytes : 0u);
+        if (lane == 0) mbar_arrive_expect_tx(full, sum + (uint32_t)(mine * nb * kImgBlock));
+        __syncwarp();
+        if (live && R.bytes) bulk_g2s(st + (size_t)slot * L.SR, base + R.lo, R.bytes, full, pol);
+        bulk_images(L, st + L.x_off, full, pw, kProducers, n, c0, nb, [&](int k) { return img(I.y + k); }, keep, lane);
       }
     }
+    drain(L, S, i, &s_abort);
   } else {
     if (!kGate) griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
     const uint32_t smem32 = smem_u32(smem);
     const uint32_t xoff = (uint32_t)L.x_off;
-    const uint32_t xl = xoff + token_off(L.XR, min(gq, L.tg - 1)) + (uint32_t)(cq * 16);
-    const uint32_t x0 = xoff + token_off(L.XR, min(2 * cq, L.tg - 1));
-    const uint32_t x1 = xoff + token_off(L.XR, min(2 * cq + 1, L.tg - 1));
+    // column g is token g (packed: token g % 4, hi or lo)
+    const auto col = [&](int n) { return xoff + token_off(L.XR, min(kPack ? n & 3 : n, L.tg - 1)); };
+    const uint32_t xl = col(gq) + (uint32_t)(cq * 16 + (kPack ? 8 * (gq >> 2) : 0));
+    const uint32_t x0 = col(2 * cq), x1 = col(2 * cq + 1);
     float* hq = reinterpret_cast<float*>(smem + L.o_hq);  // gate: [32 rows][8 tokens + 1]
     const int group = warp / kGroupWarps, member = warp % kGroupWarps;
     int turn = 0;  // the group whose stage this is
@@ -778,21 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (q >= (it + 1) * nq) ++it;
       const int2 I = S.item[it];
       const int ntok = I.x >> 16, u = q - it * nq, r0 = u * kRows;
-      float y[kTiles][4];
+      uint64_t y[kTiles][2];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.f;
-      // this lane's slots, and how far into its first line each row starts
-      uint32_t slot[kTiles][2], mis[kTiles][2];
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int s = kGate ? 32 * h + 8 * t + gq : 16 * t + 8 * h + gq;
-          const int r = kGate ? 8 * t + gq : s;
-          slot[t][h] = (uint32_t)(s * L.SR);
-          mis[t][h] =
-              kAl ? 0u : (uint32_t)((((long long)(I.x & 0xffff) * rows + r0 + r) * (L.bpr * kQBlockBytes)) & 15);
-        }
+      for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = pack2(0.f, 0.f);
       for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
         const bool mine = turn == group;
         turn = turn + 1 == kGroups ? 0 : turn + 1;
@@ -800,20 +769,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_wait(&S.full[R.s], R.ph, &s_abort);
         const uint32_t st = after_wait(smem32 + (uint32_t)R.s * (uint32_t)L.stage_bytes);
         const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
+        // where row g's slice starts in its slot (the tiles' other rows are
+        // multiples of 8 * 272 bytes on: the same number of bytes into a line)
+        const uint32_t mis = kAl ? 0u
+                                 : (uint32_t)(gq * L.SR) +
+                                       ((((uint32_t)(I.x & 0xffff) * (uint32_t)rows + (uint32_t)(r0 + gq)) *
+                                             (uint32_t)L.bpr + (uint32_t)c0) * (uint32_t)kQBlockBytes & 15u);
         for (int j = member; j < nb; j += kGroupWarps) {
-          uint32_t ra[kTiles][2];
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              ra[t][h] = slot[t][h] + (kAl ? 0u : (mis[t][h] + (uint32_t)c0 * kQBlockBytes) & 15u);
           const uint32_t xo = st + (uint32_t)(j * kImgBlock);
-          BlockIn<kTiles> B;
-          // (tensor copies: sub-stages of 8 blocks)
-          const uint32_t jo = kAl ? (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes)
-                                  : (uint32_t)(j * kQBlockBytes);
-          load_block<kAl, kTiles>(ra, st + jo, !(j & 1), cq, xo + xl, xo + x0, xo + x1, B);
-          block_mma<kAl, kTiles>(B, !(j & 1), cq, y);
+          BlockIn<kPack> B;
+          load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
+          if constexpr (kAl) {
+            // (sub-stages of 8 blocks)
+            load_aligned<kGate, kPack>(
+                st + (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes + gq * 8 * kQBlockBytes), !(j & 1), cq, B);
+          } else {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                load_unaligned<kPack>(st + mis + (uint32_t)(slot_of<kGate>(t, h) * L.SR + j * kQBlockBytes), t, h, cq,
+                                      B);
+          }
+          block_mma<kAl, kPack>(B, !(j & 1), cq, y);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.empty[R.s]);
@@ -822,8 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         float* p = S.part + ((warp * kTiles + t) * 16 + gq) * 8 + 2 * cq;
-        *reinterpret_cast<float2*>(p) = make_float2(y[t][0], y[t][1]);
-        *reinterpret_cast<float2*>(p + 64) = make_float2(y[t][2], y[t][3]);
+        *reinterpret_cast<uint64_t*>(p) = y[t][0];
+        *reinterpret_cast<uint64_t*>(p + 64) = y[t][1];
       }
       consumer_sync(kConsumers * 32);
       const int n = threadIdx.x & 7;
@@ -833,8 +811,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float g = 0.f, v = 0.f;
 #pragma unroll
           for (int k = 0; k < kConsumers; ++k) {
-            g += S.part[((k * kTiles + t) * 16 + r) * 8 + n];
-            v += S.part[((k * kTiles + t) * 16 + r + 8) * 8 + n];
+            const float* p = S.part + ((k * kTiles + t) * 16 + r) * 8;
+            g += kPack ? p[n & 3] + p[n & 3 | 4] : p[n];
+            v += kPack ? p[64 + (n & 3)] + p[64 + (n & 3 | 4)] : p[64 + n];
           }
           hq[(t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
         }
@@ -850,7 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = threadIdx.x >> 3;  // 64 rows x 8 tokens
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kConsumers; ++k) v += S.part[(k * kSlots + r) * 8 + n];
+        for (int k = 0; k < kConsumers; ++k) {
+          const float* p = S.part + (k * kSlots + r) * 8;
+          v += kPack ? p[n & 3] + p[n & 3 | 4] : p[n];
+        }
         if (n < ntok && r0 + r < rows)
           P.ypart[(size_t)S.ppair[I.y + n] * P.hidden + r0 + r] = S.pw[I.y + n] * v;
         consumer_sync(kConsumers * 32);  // (the shares are rewritten next)
@@ -997,8 +979,13 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   if (!rc) rc = plan_product(P, bh, &dn);
   if (rc) return rc;
   const bool gal = bx % 8 == 0, dal = bh % 8 == 0;
-  const auto gu_fn = gal ? moe_product_kernel<true, true> : moe_product_kernel<false, true>;
-  const auto dn_fn = dal ? moe_product_kernel<true, false> : moe_product_kernel<false, false>;
+  typedef void (*Product)(MoeParams, MoePlan, bool, CUtensorMap, CUtensorMap);
+  static const Product fns[2][2][2] = {
+      {{moe_product_kernel<false, false, false>, moe_product_kernel<false, false, true>},
+       {moe_product_kernel<false, true, false>, moe_product_kernel<false, true, true>}},
+      {{moe_product_kernel<true, false, false>, moe_product_kernel<true, false, true>},
+       {moe_product_kernel<true, true, false>, moe_product_kernel<true, true, true>}}};
+  const Product gu_fn = fns[gal][1][gu.tg <= 4], dn_fn = fns[dal][0][dn.tg <= 4];
   CUtensorMap mg{}, mu{}, md{};
   if (gal) {
     rc = weight_map(P.wg, bx, (long long)P.n_experts * P.ffn, kGuRows, &mg);
