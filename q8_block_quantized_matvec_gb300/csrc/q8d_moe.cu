@@ -342,11 +342,13 @@ __device__ __forceinline__ MoeShared carve(const MoePlan& L, uint8_t* smem, int 
 }
 
 constexpr int kConsumers = 16;                              // consumer warps
-// The consumer warps are kGroups groups that take stages in turn: warps of
-// one stage load, decode and multiply at the same time, so groups on other
-// stages keep the pipes they do not use busy (one group of sixteen: 97 us of
-// arithmetic in the gate / up products of moe_64).
-constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups;
+// Two groups of eight warps work on two units at a time, each with its own
+// sums and barriers: warps of one unit load, decode and multiply at about the
+// same time, so the other group's keep the pipes they do not use busy, and
+// one group's epilogue overlaps the other's products.  The stages of the two
+// units alternate, so a stage of the ring always belongs to the same group (a
+// barrier's parity tells two neighbouring phases apart, no more).
+constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups, kGroupThreads = kGroupWarps * 32;
 constexpr int kThreads = (kConsumers + kProducers) * 32;
 constexpr int kPairsThread = (kMoeMaxTokens * kMoeMaxTop + kThreads - 1) / kThreads;
 
@@ -596,34 +598,51 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volati
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    __nanosleep(20);
   }
   *abort = 1;
   return false;
 }
 
-// A place in the ring: stage s, filled for the ph-th time (parity).
-struct Cursor {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next(int nst) {
-    if (++s == nst) {
-      s = 0;
-      ph ^= 1u;
+// The producers' place in the CTA's sequence of stages: the units q0 .. q1
+// in pairs, a pair's slices in turn (group 0's, group 1's); a last unit
+// without a partner leaves the other group's stages out.
+struct Place {
+  int s = 0, ph = 0;  // stage of the ring; parity of its next fill
+  bool again = false; // filled before
+  int q, sl = 0, half = 0;  // the pair's first unit, slice, unit of the pair
+  __device__ __forceinline__ int unit() const { return q + half; }
+  __device__ __forceinline__ void next(const MoePlan& L, int q1) {
+    int step = 1;
+    if (half == 0 && q + 1 < q1) {
+      half = 1;
+    } else {
+      step = 1 + (half == 0 ? 1 : 0);
+      half = 0;
+      if (++sl == L.nsl) {
+        sl = 0;
+        q += 2;
+      }
+    }
+    s += step;
+    if (s >= L.nst) {
+      s -= L.nst;
+      ph ^= 1;
+      again = true;
     }
   }
 };
 
-// One warp's wait on a barrier that lane 0 polls.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
-  const int ok = lane ? 1 : (ring_wait(bar, parity, abort) ? 1 : 0);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// After a wait gave up: the bulk copies of the last fills (of i) have landed.
-__device__ __forceinline__ void drain(const MoePlan& L, const MoeShared& S, int i, volatile int* abort) {
+// After a wait gave up: every announced copy has landed (stages in `filled`,
+// the parity of their last fill in `parity`).
+__device__ __forceinline__ void drain(const MoePlan& L, const MoeShared& S, uint32_t filled, uint32_t parity,
+                                      volatile int* abort) {
   if (*abort)
-    for (int j = max(0, i - L.nst); j < i; ++j) mbar_wait(&S.full[j % L.nst], (uint32_t)(j / L.nst) & 1u);
+    for (int s = 0; s < L.nst; ++s)
+      if (filled >> s & 1u) mbar_wait(&S.full[s], parity >> s & 1u);
+}
+// Barrier among one group's threads.
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(kGroupThreads) : "memory");
 }
 
 // Ends a product kernel: a wait that gave up is reported.
@@ -659,36 +678,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rb = L.bpr * kQBlockBytes;
     const long long mat = (long long)P.n_experts * rows * rb;
     const uint32_t smem32 = smem_u32(smem);
-    struct Place {  // a place in the CTA's sequence of stages: unit, its item, slice
-      Cursor R;
-      int q, it, sl = 0;
-      __device__ void next(const MoePlan& L, int nq) {
-        R.next(L.nst);
-        if (++sl == L.nsl) {
-          sl = 0;
-          if (++q >= (it + 1) * nq) ++it;
-        }
-      }
-    };
     const auto img = [&](int row) {
       return kGate ? P.ximg + (size_t)S.ptok[row] * L.bpr * kImgBlock : P.himg + (size_t)row * L.bpr * kImgBlock;
     };
-    const int total = (q1 - q0) * L.nsl, pw = warp - kConsumers;
+    const int pw = warp - kConsumers;
     const uint64_t pol = policy_evict_first(), keep = policy_evict_last();
+    uint32_t filled = 0, parity = 0;
     Place w;
     w.q = q0;
-    w.it = q0 / nq;
-    int i = 0;
+    const auto ready = [&]() {  // the stage may be filled
+      const bool ok = !w.again || ring_wait(&S.empty[w.s], (uint32_t)w.ph ^ 1u, &s_abort);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      filled |= 1u << w.s;
+      parity = (parity & ~(1u << w.s)) | (uint32_t)w.ph << w.s;
+      return true;
+    };
     // Weights depend on nothing in flight, so the down kernel fills its ring
     // with them before it waits for h.
     if (kAl && pw == 0) {
-      for (; i < total; ++i, w.next(L, nq)) {
-        if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
+      for (; w.q < q1; w.next(L, q1)) {
+        if (!ready()) break;
         if (lane == 0) {
           const int subs = min(L.S, L.bpr - w.sl * L.S) / 8, x0 = w.sl * L.S / 8 * (8 * kQBlockBytes / 4);
-          const int y0 = (S.item[w.it].x & 0xffff) * rows + (w.q - w.it * nq) * kRows;
-          const uint32_t st = smem32 + (uint32_t)w.R.s * (uint32_t)L.stage_bytes;
-          uint64_t* full = &S.full[w.R.s];
+          const int it = w.unit() / nq, y0 = (S.item[it].x & 0xffff) * rows + (w.unit() - it * nq) * kRows;
+          const uint32_t st = smem32 + (uint32_t)w.s * (uint32_t)L.stage_bytes;
+          uint64_t* full = &S.full[w.s];
           mbar_arrive_expect_tx(full, (uint32_t)(subs * kSubBytes));
           for (int s = 0; s < subs; ++s) {
             const uint32_t d = st + (uint32_t)(s * kSubBytes);
@@ -702,25 +716,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (kAl) {
       if (!kGate) griddep_wait();  // (h)
       fence_proxy_async_global();  // (the images were written by ordinary stores)
-      for (; i < total; ++i, w.next(L, nq)) {
-        if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
-        const int2 I = S.item[w.it];
+      for (; w.q < q1; w.next(L, q1)) {
+        if (!ready()) break;
+        const int2 I = S.item[w.unit() / nq];
         const int n = I.x >> 16, c0 = w.sl * L.S, nb = min(L.S, L.bpr - c0), f = pw - 1;
         const int mine = f < n ? (n - f + kProducers - 2) / (kProducers - 1) : 0;  // tokens f, f + 3, ..
-        if (lane == 0) mbar_arrive_expect_tx(&S.full[w.R.s], (uint32_t)(mine * nb * kImgBlock));
+        if (lane == 0) mbar_arrive_expect_tx(&S.full[w.s], (uint32_t)(mine * nb * kImgBlock));
         __syncwarp();
-        bulk_images(L, smem + (size_t)w.R.s * L.stage_bytes + L.x_off, &S.full[w.R.s], f, kProducers - 1, n, c0, nb,
+        bulk_images(L, smem + (size_t)w.s * L.stage_bytes + L.x_off, &S.full[w.s], f, kProducers - 1, n, c0, nb,
                     [&](int k) { return img(I.y + k); }, keep, lane);
       }
     } else {
       if (!kGate) griddep_wait();
       fence_proxy_async_global();
-      for (; i < total; ++i, w.next(L, nq)) {
-        if (i >= L.nst && !warp_wait(&S.empty[w.R.s], w.R.ph ^ 1u, &s_abort, lane)) break;
-        const int2 I = S.item[w.it];
-        const int n = I.x >> 16, c0 = w.sl * L.S, nb = min(L.S, L.bpr - c0), r0 = (w.q - w.it * nq) * kRows;
-        uint8_t* st = smem + (size_t)w.R.s * L.stage_bytes;
-        uint64_t* full = &S.full[w.R.s];
+      for (; w.q < q1; w.next(L, q1)) {
+        if (!ready()) break;
+        const int it = w.unit() / nq;
+        const int2 I = S.item[it];
+        const int n = I.x >> 16, c0 = w.sl * L.S, nb = min(L.S, L.bpr - c0), r0 = (w.unit() - it * nq) * kRows;
+        uint8_t* st = smem + (size_t)w.s * L.stage_bytes;
+        uint64_t* full = &S.full[w.s];
         // lanes 0-15: a slot each; a warp's slots are one matrix's
         const int slot = pw * (kSlots / kProducers) + lane;
         const uint8_t* base = kGate ? (slot < kGuRows ? P.wg : P.wu) : P.wd;
@@ -741,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_images(L, st + L.x_off, full, pw, kProducers, n, c0, nb, [&](int k) { return img(I.y + k); }, keep, lane);
       }
     }
-    drain(L, S, i, &s_abort);
+    drain(L, S, filled, parity, &s_abort);
   } else {
     if (!kGate) griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
@@ -751,23 +766,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto col = [&](int n) { return xoff + token_off(L.XR, min(kPack ? n & 3 : n, L.tg - 1)); };
     const uint32_t xl = col(gq) + (uint32_t)(cq * 16 + (kPack ? 8 * (gq >> 2) : 0));
     const uint32_t x0 = col(2 * cq), x1 = col(2 * cq + 1);
-    float* hq = reinterpret_cast<float*>(smem + L.o_hq);  // gate: [32 rows][8 tokens + 1]
-    const int group = warp / kGroupWarps, member = warp % kGroupWarps;
-    int turn = 0;  // the group whose stage this is
-    Cursor R;
-    for (int q = q0, it = q0 / nq; q < q1; ++q) {
-      if (q >= (it + 1) * nq) ++it;
+    const int group = warp / kGroupWarps, member = warp % kGroupWarps, tid = threadIdx.x - group * kGroupThreads;
+    float* part = S.part + group * kGroupWarps * kSlots * 8;                                 // [warp][slot][token]
+    float* hq = reinterpret_cast<float*>(smem + L.o_hq) + group * kGuRows * 9;  // gate: [32 rows][8 tokens + 1]
+    int s = group;
+    uint32_t ph = 0;
+    for (int q = q0 + group; q < q1; q += kGroups) {
+      const int it = q / nq;
       const int2 I = S.item[it];
       const int ntok = I.x >> 16, u = q - it * nq, r0 = u * kRows;
       uint64_t y[kTiles][2];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = pack2(0.f, 0.f);
-      for (int sl = 0; sl < L.nsl; ++sl, R.next(L.nst)) {
-        const bool mine = turn == group;
-        turn = turn + 1 == kGroups ? 0 : turn + 1;
-        if (!mine) continue;
-        ring_wait(&S.full[R.s], R.ph, &s_abort);
-        const uint32_t st = after_wait(smem32 + (uint32_t)R.s * (uint32_t)L.stage_bytes);
+      for (int sl = 0; sl < L.nsl; ++sl) {
+        ring_wait(&S.full[s], ph, &s_abort);
+        const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
         const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
         // where row g's slice starts in its slot (the tiles' other rows are
         // multiples of 8 * 272 bytes on: the same number of bytes into a line)
@@ -794,48 +807,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           block_mma<kAl, kPack>(B, !(j & 1), cq, y);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.empty[R.s]);
+        if (lane == 0) mbar_arrive(&S.empty[s]);
+        s += kGroups;
+        if (s >= L.nst) {
+          s -= L.nst;
+          ph ^= 1u;
+        }
       }
-      // the warps' shares of the unit: [warp][tile][row of 16][token]
+      // the warps' shares of the unit
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        float* p = S.part + ((warp * kTiles + t) * 16 + gq) * 8 + 2 * cq;
+        float* p = part + ((member * kTiles + t) * 16 + gq) * 8 + 2 * cq;
         *reinterpret_cast<uint64_t*>(p) = y[t][0];
         *reinterpret_cast<uint64_t*>(p + 64) = y[t][1];
       }
-      consumer_sync(kConsumers * 32);
-      const int n = threadIdx.x & 7;
-      if constexpr (kGate) {
-        if (threadIdx.x < 256) {
-          const int t = threadIdx.x >> 6, r = (threadIdx.x >> 3) & 7;
-          float g = 0.f, v = 0.f;
-#pragma unroll
-          for (int k = 0; k < kConsumers; ++k) {
-            const float* p = S.part + ((k * kTiles + t) * 16 + r) * 8;
-            g += kPack ? p[n & 3] + p[n & 3 | 4] : p[n];
-            v += kPack ? p[64 + (n & 3)] + p[64 + (n & 3 | 4)] : p[64 + n];
-          }
-          hq[(t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
-        }
-        consumer_sync(kConsumers * 32);
-        if (threadIdx.x < 64) {  // the unit is block u of its tokens' h: token i, word w
-          const int i = threadIdx.x >> 3, w = threadIdx.x & 7;
-          float v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = hq[tc::word_quant(hperm && !(u & 1), w, k) * 9 + i];
-          image_word(v, i < ntok, P.himg + ((size_t)(I.y + i) * nq + u) * kImgBlock, w);
-        }
-      } else {
-        const int r = threadIdx.x >> 3;  // 64 rows x 8 tokens
+      group_sync(group);
+      const int n = tid & 7;
+      const auto total = [&](int row) {  // of slot `row` of the unit's A tiles, column n
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kConsumers; ++k) {
-          const float* p = S.part + (k * kSlots + r) * 8;
-          v += kPack ? p[n & 3] + p[n & 3 | 4] : p[n];
+        for (int k = 0; k < kGroupWarps; ++k) {
+          const float* p = part + (k * kSlots + row) * 8;
+          v += kPack ? p[n & 3] + p[(n & 3) | 4] : p[n];
         }
-        if (n < ntok && r0 + r < rows)
-          P.ypart[(size_t)S.ppair[I.y + n] * P.hidden + r0 + r] = S.pw[I.y + n] * v;
-        consumer_sync(kConsumers * 32);  // (the shares are rewritten next)
+        return v;
+      };
+      if constexpr (kGate) {
+        const int t = tid >> 6, r = (tid >> 3) & 7;
+        const float g = total(16 * t + r), v = total(16 * t + r + 8);
+        hq[(t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
+        group_sync(group);
+        if (tid < 64) {  // the unit is block u of its tokens' h: token i, word w
+          const int i = tid >> 3, w = tid & 7;
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = hq[tc::word_quant(hperm && !(u & 1), w, k) * 9 + i];
+          image_word(x, i < ntok, P.himg + ((size_t)(I.y + i) * nq + u) * kImgBlock, w);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // 64 rows x 8 tokens
+          const int r = (tid >> 3) + 32 * k;
+          const float v = total(r);
+          if (n < ntok && r0 + r < rows)
+            P.ypart[(size_t)S.ppair[I.y + n] * P.hidden + r0 + r] = S.pw[I.y + n] * v;
+        }
+        group_sync(group);  // (the shares are rewritten next)
       }
     }
   }
@@ -929,7 +946,7 @@ int plan_product(const MoeParams& P, int bpr, MoePlan* L) {
       L->o_part = o;
       o += kConsumers * kSlots * 8 * 4;
       L->o_hq = o;
-      o += up16i(kGuRows * 9 * 4);
+      o += up16i(kGroups * kGuRows * 9 * 4);
       L->o_mask = o;
       o += 8 * P.n_experts;
       L->o_ebase = o;
@@ -939,10 +956,8 @@ int plan_product(const MoeParams& P, int bpr, MoePlan* L) {
       L->o_tok = o;
       o = up16i(o + 8 * pairs);
       L->o_bar = o;
-      // A barrier's parity tells two neighbouring phases apart, no more, so a
-      // stage always belongs to the same consumer group.
       L->nst = std::min(12, (kMaxSmem - o) / (L->stage_bytes + 16)) / kGroups * kGroups;
-      if (L->nst < std::max(3, kGroups)) continue;
+      if (L->nst < 2 * kGroups) continue;
       const int ring = L->nst * L->stage_bytes;
       for (int* f : {&L->o_part, &L->o_hq, &L->o_mask, &L->o_ebase, &L->o_item, &L->o_tok, &L->o_bar}) *f += ring;
       L->smem = ring + o + 16 * L->nst;
