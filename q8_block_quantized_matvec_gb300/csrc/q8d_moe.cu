@@ -14,7 +14,8 @@
 // copy brings 8 blocks of 32 or 64 rows, 272 bytes a row: rows then lie 4 (mod
 // 32) banks apart and eight rows' words in distinct banks without padding.
 // Other rows come as a bulk copy each into padded slots, by four warps (a warp
-// issues such copies a lane at a time, some 90 cycles each).
+// issues such copies a lane at a time, some 90 cycles each), so their stages
+// are one tile of 16 rows by up to 64 blocks: fewer and longer pieces.
 //  * A: sixteen weight rows, a lane's word of four quants made two exact f16
 //    pairs (one PRMT and one subtraction a pair); B: up to eight tokens of
 //    the expert; the warps split the blocks of a row.
@@ -190,7 +191,7 @@ __device__ __forceinline__ void logits_of(const MoeParams& P, int t0, int nt, in
   for (int x = 0; x < kE; ++x)
 #pragma unroll
     for (int t = 0; t < kT; ++t) s[x][t][0] = s[x][t][1] = c[x][t][0] = c[x][t][1] = pack2(0.f, 0.f);
-  constexpr int kAhead = kT * kE == 1 ? 8 : kT * kE <= 4 ? 4 : 2;  // loads in flight
+  constexpr int kAhead = kT * kE == 1 ? 4 : kT * kE == 2 ? 2 : 1;  // loads in flight (64 registers)
   const int n = P.hidden / 4;
   for (int i0 = lane; i0 < n; i0 += 32 * kAhead) {
     float4 a[kAhead][kE], b[kAhead][kT];
@@ -244,7 +245,7 @@ __device__ __forceinline__ void logits_of(const MoeParams& P, int t0, int nt, in
 }
 
 template <int kT>
-__global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams P, int per_cluster, bool perm) {
+__global__ void __launch_bounds__(kRtThreads, 2) moe_router_kernel(const MoeParams P, int per_cluster, bool perm) {
   __shared__ float2 logits[kT][kMoeMaxExperts];
   constexpr int kWarps = kRtThreads / 32;
   const int rank = (int)cluster_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -263,8 +264,9 @@ __global__ void __launch_bounds__(kRtThreads) moe_router_kernel(const MoeParams 
   // every CTA of the cluster is running before one stores to another's memory
   cluster_sync();
   int e = e0 + warp;
-  for (; e + kWarps < e1; e += 2 * kWarps) logits_of<kT, 2>(P, t0, nt, e, kWarps, e1, logits, lane);
-  if (e < e1) logits_of<kT, 1>(P, t0, nt, e, kWarps, e1, logits, lane);
+  if constexpr (kT == 1)  // (two experts at once share a token's loads; with two tokens they spill)
+    for (; e + kWarps < e1; e += 2 * kWarps) logits_of<kT, 2>(P, t0, nt, e, kWarps, e1, logits, lane);
+  for (; e < e1; e += kWarps) logits_of<kT, 1>(P, t0, nt, e, kWarps, e1, logits, lane);
   // the tokens' operand images, a word a thread, blocks dealt over the cluster
   const int bpr = P.hidden / kQBlock, words = nt * bpr * 8;
   for (int i0 = (rank * kRtThreads + warp * 32); i0 < words; i0 += kRtCluster * kRtThreads) {
@@ -302,6 +304,7 @@ constexpr int kSubBytes = kSlots * 8 * kQBlockBytes;  // 64 row slots of 8 block
 struct MoePlan {
   int bpr;          // blocks a row
   int S, nsl;       // blocks a slice, slices a row
+  int stages;       // of a unit: a slice each (tensor copies), or a tile and slice each
   int SR;           // slot bytes (tensor copies: of 8 blocks)
   int x_off;        // the images' offset in a stage
   int tg;           // tokens a group (1, 2, 4 or 8)
@@ -472,20 +475,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// What a lane reads of one block: its words of kTiles A tiles, their scales,
+// What a lane reads of one block: its words of kN A tiles, their scales,
 // its columns' operand and inverse scales.  All loads of a block are issued
 // before its arithmetic (asm volatile keeps their order).
 // kPack: at most four tokens; columns 0-3 are their hi parts, 4-7 their lo
 // parts, so one MMA a step does what two do otherwise.
-template <bool kPack>
+template <bool kPack, int kN>
 struct BlockIn {
-  uint32_t w[kTiles][2][3];  // row g or g + 8: words of steps 0 and 1, the scale (even blocks: and quants 0, 1)
+  uint32_t w[kN][2][3];  // row g or g + 8: words of steps 0 and 1, the scale (even blocks: and quants 0, 1)
   uint32_t b[2][kPack ? 2 : 4];
   float xi0, xi1;
 };
 
-template <bool kPack>
-__device__ __forceinline__ void load_x(uint32_t xa, uint32_t x0, uint32_t x1, BlockIn<kPack>& B) {
+template <bool kPack, int kN>
+__device__ __forceinline__ void load_x(uint32_t xa, uint32_t x0, uint32_t x1, BlockIn<kPack, kN>& B) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if constexpr (kPack) {
@@ -527,7 +530,7 @@ __host__ __device__ constexpr int slot_of(int t, int h) {
 // offset.  bg: block start in slot g.  Words are aligned in odd blocks; an
 // even block's word 7 is its first two and last two quants (tc::word_quant).
 template <bool kGate, bool kPack, int I = 0>
-__device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, BlockIn<kPack>& B) {
+__device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, BlockIn<kPack, kTiles>& B) {
   if constexpr (I < 2 * kTiles) {
     constexpr int t = I / 2, h = I % 2, so = slot_of<kGate>(t, h) * 8 * kQBlockBytes;
     if (even) {
@@ -544,11 +547,11 @@ __device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, Bloc
 }
 // Other rows: a block starts at any even address, quants in order.
 template <bool kPack>
-__device__ __forceinline__ void load_unaligned(uint32_t ba, int t, int h, int c, BlockIn<kPack>& B) {
+__device__ __forceinline__ void load_unaligned(uint32_t ba, int h, int c, BlockIn<kPack, 1>& B) {
   const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
-  B.w[t][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
-  B.w[t][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
-  B.w[t][h][2] = tc::lds16a(ba);
+  B.w[0][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
+  B.w[0][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
+  B.w[0][h][2] = tc::lds16a(ba);
 }
 
 __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -562,12 +565,12 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
 
 // y[t] += the products of a loaded block: columns 2c and 2c + 1 of rows g
 // ([0]) and g + 8 ([1]) of tile t.
-template <bool kAl, bool kPack>
-__device__ __forceinline__ void block_mma(const BlockIn<kPack>& B, bool even, int c, uint64_t (&y)[kTiles][2]) {
+template <bool kAl, bool kPack, int kN>
+__device__ __forceinline__ void block_mma(const BlockIn<kPack, kN>& B, bool even, int c, uint64_t (&y)[kN][2]) {
   const uint64_t xi = pack2(B.xi0, B.xi1);
   const uint32_t sel = c == 3 ? 0x5432u : 0x7654u;
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
+  for (int t = 0; t < kN; ++t) {
     float acc[4];
     uint32_t a0, a1, a2, a3;
     tc::quant_pairs(B.w[t][0][0], a0, a2);
@@ -618,7 +621,7 @@ struct Place {
     } else {
       step = 1 + (half == 0 ? 1 : 0);
       half = 0;
-      if (++sl == L.nsl) {
+      if (++sl == L.stages) {
         sl = 0;
         q += 2;
       }
@@ -733,14 +736,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ready()) break;
         const int it = w.unit() / nq;
         const int2 I = S.item[it];
-        const int n = I.x >> 16, c0 = w.sl * L.S, nb = min(L.S, L.bpr - c0), r0 = (w.unit() - it * nq) * kRows;
+        const int tile = w.sl / L.nsl, c0 = (w.sl - tile * L.nsl) * L.S, nb = min(L.S, L.bpr - c0);
+        const int n = I.x >> 16, r0 = (w.unit() - it * nq) * kRows;
         uint8_t* st = smem + (size_t)w.s * L.stage_bytes;
         uint64_t* full = &S.full[w.s];
-        // lanes 0-15: a slot each; a warp's slots are one matrix's
-        const int slot = pw * (kSlots / kProducers) + lane;
-        const uint8_t* base = kGate ? (slot < kGuRows ? P.wg : P.wu) : P.wd;
-        const int r = kGate ? slot & (kGuRows - 1) : slot;
-        const bool live = lane < kSlots / kProducers && r0 + r < rows;
+        // lanes 0-3: a row of the tile's sixteen each; a warp's rows are one matrix's
+        constexpr int kMine = 16 / kProducers;
+        const int slot = pw * kMine + (lane & (kMine - 1));
+        const uint8_t* base = kGate ? (slot < 8 ? P.wg : P.wu) : P.wd;
+        const int r = kGate ? 8 * tile + (slot & 7) : 16 * tile + slot;
+        const bool live = lane < kMine && r0 + r < rows;
         RowLines R{};
         if (live) {
           R = row_lines(((long long)(I.x & 0xffff) * rows + r0 + r) * rb, c0, nb, mat);
@@ -778,40 +783,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t y[kTiles][2];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = pack2(0.f, 0.f);
-      for (int sl = 0; sl < L.nsl; ++sl) {
+      const auto stage = [&]() {  // the group's next stage
         ring_wait(&S.full[s], ph, &s_abort);
-        const uint32_t st = after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
-        const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
-        // where row g's slice starts in its slot (the tiles' other rows are
-        // multiples of 8 * 272 bytes on: the same number of bytes into a line)
-        const uint32_t mis = kAl ? 0u
-                                 : (uint32_t)(gq * L.SR) +
-                                       ((((uint32_t)(I.x & 0xffff) * (uint32_t)rows + (uint32_t)(r0 + gq)) *
-                                             (uint32_t)L.bpr + (uint32_t)c0) * (uint32_t)kQBlockBytes & 15u);
-        for (int j = member; j < nb; j += kGroupWarps) {
-          const uint32_t xo = st + (uint32_t)(j * kImgBlock);
-          BlockIn<kPack> B;
-          load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
-          if constexpr (kAl) {
-            // (sub-stages of 8 blocks)
-            load_aligned<kGate, kPack>(
-                st + (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes + gq * 8 * kQBlockBytes), !(j & 1), cq, B);
-          } else {
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                load_unaligned<kPack>(st + mis + (uint32_t)(slot_of<kGate>(t, h) * L.SR + j * kQBlockBytes), t, h, cq,
-                                      B);
-          }
-          block_mma<kAl, kPack>(B, !(j & 1), cq, y);
-        }
+        return after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
+      };
+      const auto release = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.empty[s]);
         s += kGroups;
         if (s >= L.nst) {
           s -= L.nst;
           ph ^= 1u;
+        }
+      };
+      if constexpr (kAl) {
+        for (int sl = 0; sl < L.nsl; ++sl) {
+          const uint32_t st = stage();
+          const int nb = min(L.S, L.bpr - sl * L.S);
+          for (int j = member; j < nb; j += kGroupWarps) {
+            const uint32_t xo = st + (uint32_t)(j * kImgBlock);
+            BlockIn<kPack, kTiles> B;
+            load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
+            // (sub-stages of 8 blocks)
+            load_aligned<kGate, kPack>(
+                st + (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes + gq * 8 * kQBlockBytes), !(j & 1), cq, B);
+            block_mma<kAl, kPack>(B, !(j & 1), cq, y);
+          }
+          release();
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          uint64_t yt[1][2] = {{y[t][0], y[t][1]}};
+          for (int sl = 0; sl < L.nsl; ++sl) {
+            const uint32_t st = stage();
+            const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
+            // where row g's slice starts in its slot (row g + 8's, 8 * 272
+            // bytes of the matrix on or in the other one: as far into a line)
+            const uint32_t r = (uint32_t)(r0 + (kGate ? 8 : 16) * t + gq);
+            const uint32_t mis = (((uint32_t)(I.x & 0xffff) * (uint32_t)rows + r) * (uint32_t)L.bpr + (uint32_t)c0) *
+                                 (uint32_t)kQBlockBytes & 15u;
+            for (int j = member; j < nb; j += kGroupWarps) {
+              const uint32_t xo = st + (uint32_t)(j * kImgBlock);
+              const uint32_t ba = st + (uint32_t)(gq * L.SR) + mis + (uint32_t)(j * kQBlockBytes);
+              BlockIn<kPack, 1> B;
+              load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
+              load_unaligned<kPack>(ba, 0, cq, B);
+              load_unaligned<kPack>(ba + (uint32_t)(8 * L.SR), 1, cq, B);
+              block_mma<kAl, kPack>(B, !(j & 1), cq, yt);
+            }
+            release();
+          }
+          y[t][0] = yt[0][0];
+          y[t][1] = yt[0][1];
         }
       }
       // the warps' shares of the unit
@@ -923,19 +947,21 @@ int group_tokens(const MoeParams& P) {
   return tg;
 }
 
-// Lays out a product kernel over rows of bpr blocks.  A slice is up to two
-// blocks a warp of a group, one where that leaves too few stages.
+// Lays out a product kernel over rows of bpr blocks: slices of 16 or 8 blocks
+// where tensor copies bring the rows, else the longest of up to 64 that leaves
+// two stages a group.
 int plan_product(const MoeParams& P, int bpr, MoePlan* L) {
   const bool al = bpr % 8 == 0;
   const int pairs = P.m * P.top_k;
   L->bpr = bpr;
   for (int tg = group_tokens(P); tg >= 1; tg /= 2)
-    for (int s = 16; s >= 8; s -= 8) {
+    for (int s = al ? 16 : 64; s >= 8; s -= 8) {
       L->nsl = (bpr + s - 1) / s;
       L->S = (bpr + L->nsl - 1) / L->nsl;  // (equal slices; whole groups of 8 blocks where rows are aligned)
       if (al) L->S = (L->S + 7) / 8 * 8;
+      L->stages = al ? L->nsl : kTiles * L->nsl;
       L->SR = al ? 8 * kQBlockBytes : slot_bytes(L->S);
-      L->x_off = al ? L->S / 8 * kSubBytes : kSlots * L->SR;
+      L->x_off = al ? L->S / 8 * kSubBytes : 16 * L->SR;
       // token rows half a bank cycle apart: the two tokens of a quarter warp's
       // 16-byte loads lie in distinct banks
       L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
@@ -1011,11 +1037,12 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   if (!rc) rc = configure_kernel(reinterpret_cast<const void*>(dn_fn), kMaxSmem, true);
   if (rc) return rc;
 
-  // the router: clusters of 8 CTAs, up to 4 tokens each, at most 16 clusters
-  const int per = (P.m + 15) / 16;
+  // The router: clusters of 8 CTAs, two CTAs an SM at once, a token each as
+  // long as that is one wave, else two (four a cluster at one CTA an SM left
+  // too few warps to cover the loads: 22 us at 64 tokens).
+  const int per = P.m * kRtCluster <= 2 * sm_count() ? 1 : 2;
   const int clusters = (P.m + per - 1) / per;
-  void (*const rt_fns[4])(MoeParams, int, bool) = {moe_router_kernel<1>, moe_router_kernel<2>, moe_router_kernel<3>,
-                                                   moe_router_kernel<4>};
+  void (*const rt_fns[2])(MoeParams, int, bool) = {moe_router_kernel<1>, moe_router_kernel<2>};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * kRtCluster);
   cfg.blockDim = dim3(kRtThreads);
