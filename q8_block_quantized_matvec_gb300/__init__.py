@@ -148,10 +148,29 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream on the current device.  torch.cuda.current_stream
+    builds a Stream object (3 us on the Arm host, more than a launch); its raw
+    handle comes from the same place without one."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # (initialises CUDA)
+        try:
+            get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            get(device())
+            _raw_stream = lambda: get(device())  # noqa: E731
+        except AttributeError:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

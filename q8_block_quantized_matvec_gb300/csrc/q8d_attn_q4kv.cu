@@ -62,7 +62,8 @@ struct Cfg4 {
   static constexpr int kOffQs = kOffQf + kQf;             // f32 q [8 NH][D], power-of-two scaled
   static constexpr int kOffF = kOffQs + 8 * NH * D * 4;   // score factors 2^-sh [8 NH]
   static constexpr int kSmem = kOffF + 8 * NH * 4;
-  static_assert(kWarps4 * 8 * NH * (D + 2) * 4 <= kOffQf + kQf, "merge buffer fits");
+  static constexpr int kOStride = D + 4;  // merge rows: a half warp's pairs in distinct banks
+  static_assert(kWarps4 * 8 * NH * (kOStride + 2) * 4 <= kOffQf + kQf, "merge buffer fits");
 };
 
 template <int N>
@@ -587,34 +588,50 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
       for (int h = 0; h < 2; ++h) {
         const float sc = (h ? 0.0625f : 1.f) * inv_f;  // (upper half-bytes count 16-fold)
         const int d0 = 32 * t + 16 * h + 2 * gq;
-        float* r0 = oo + (size_t)(warp * 8 * NH + 8 * u + 2 * cq) * D + d0;
+        float* r0 = oo + (warp * 8 * NH + 8 * u + 2 * cq) * C::kOStride + d0;
         *reinterpret_cast<float2*>(r0) = make_float2(o[u][2 * t + h][0] * sc, o[u][2 * t + h][2] * sc);
-        *reinterpret_cast<float2*>(r0 + D) = make_float2(o[u][2 * t + h][1] * sc, o[u][2 * t + h][3] * sc);
+        *reinterpret_cast<float2*>(r0 + C::kOStride) = make_float2(o[u][2 * t + h][1] * sc, o[u][2 * t + h][3] * sc);
       }
     }
   }
   __syncthreads();
-  for (int e = tid; e < G * D; e += kThreads4) {
-    const int h = e / D, j = e % D;
-    float M = -INFINITY;
+  // head h's weights of the warps (each replaces its maximum), its sum
+  if (tid < G) {
+    const int h = tid;
+    float M = -INFINITY, lsum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps4; ++w) M = fmaxf(M, mm[w * 8 * NH + h]);
-    float acc = 0.f, lsum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps4; ++w) {
       const float mw = mm[w * 8 * NH + h];
       const float wgt = mw == -INFINITY ? 0.f : ex2(mw - M);  // (a warp without a tile)
-      float x = oo[(size_t)(w * 8 * NH + h) * D + j];
-      if constexpr (kPack) x += oo[(size_t)(w * 8 * NH + h + 4) * D + j];
-      acc = fmaf(x, wgt, acc);
+      mm[w * 8 * NH + h] = wgt;
       lsum = fmaf(ll[w * 8 * NH + h], wgt, lsum);
     }
     const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
-    P.ws_o[(hq * P.nc + c) * D + j] = acc;
-    if (j == 0) {
-      P.ws_m[hq * P.nc + c] = M;
-      P.ws_l[hq * P.nc + c] = lsum;
+    P.ws_m[hq * P.nc + c] = M;
+    P.ws_l[hq * P.nc + c] = lsum;
+  }
+  __syncthreads();
+  for (int e = tid; e < G * (D / 4); e += kThreads4) {
+    const int h = e / (D / 4), j = e % (D / 4) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps4; ++w) {
+      const float wgt = mm[w * 8 * NH + h];
+      const float* r = oo + (w * 8 * NH + h) * C::kOStride + j;
+      float4 x = *reinterpret_cast<const float4*>(r);
+      if constexpr (kPack) {
+        const float4 lo = *reinterpret_cast<const float4*>(r + 4 * C::kOStride);
+        x.x += lo.x, x.y += lo.y, x.z += lo.z, x.w += lo.w;
+      }
+      acc.x = fmaf(x.x, wgt, acc.x);
+      acc.y = fmaf(x.y, wgt, acc.y);
+      acc.z = fmaf(x.z, wgt, acc.z);
+      acc.w = fmaf(x.w, wgt, acc.w);
     }
+    const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
+    *reinterpret_cast<float4*>(P.ws_o + (hq * P.nc + c) * D + j) = acc;
   }
 }
 
