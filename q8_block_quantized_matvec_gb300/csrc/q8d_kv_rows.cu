@@ -6,9 +6,16 @@
 // it, so HBM bounds them (and the launch does for a few rows).  A thread
 // takes eight consecutive elements: one or two 16-byte accesses outside the
 // cache, and four neighbouring threads make a packed block of 32, whose
-// largest element they find with two shuffles.  grid.y runs over the
-// sequences and grid.z over k and v, so a ragged batch's unused threads are
-// whole CTAs that leave at once.
+// largest element they find with two shuffles.  Large calls give a thread
+// several such groups, loaded before any is used, because a CTA that moves
+// 8 KB spends as long starting as working: 8 x 2047 rows of 1024, f32 and
+// Q8_0, took 21.8 us to append and 18.9 to read with one group a thread, 16.7
+// and 13.5 with four; 102400 rows of 512 out of 4 bits into f16 57.6, now 51
+// (6.7 TB/s).  Staging the 34-byte blocks through shared memory, for whole
+// 16-byte lines on the cache's side, was slower than the 2-byte accesses (21.8
+// against 18.9 us to read): the lines are put together in L1 and L2 anyway.
+// grid.y runs over the sequences and grid.z over k and v, so a ragged batch's
+// unused threads are whole CTAs that leave at once.
 #include <algorithm>
 
 #include "q8d_attn.cuh"
@@ -91,8 +98,8 @@ struct CacheT<Q8D_KV_F16> {
   using T = __half;
 };
 
-// The four lanes of a Q8_0 block quantize its 32 elements (the operations
-// of quantize_q8_0_warp: the bytes are the same).
+// The four lanes of a Q8_0 block quantize its 32 elements (the operations of
+// quantize_q8_0_warp, so the bytes are the same).
 __device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f)[kGroupE], bool live) {
   float amax = 0.f;
 #pragma unroll
@@ -105,8 +112,13 @@ __device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f
   unsigned short* q = reinterpret_cast<unsigned short*>(blk + 2 + 8 * part);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int a = (int)roundf(__fmul_rn(f[2 * i], id)), b = (int)roundf(__fmul_rn(f[2 * i + 1], id));
-    q[i] = (unsigned short)((a & 0xff) | (b & 0xff) << 8);
+    uint32_t pair = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = (int)roundf(__fmul_rn(f[2 * i + k], id));
+      pair |= (uint32_t)(uint8_t)(int8_t)r << (8 * k);
+    }
+    q[i] = (unsigned short)pair;
   }
   if (part == 0) *reinterpret_cast<unsigned short*>(blk) = __half_as_ushort(__float2half_rn(d));
 }
@@ -134,130 +146,189 @@ __device__ __forceinline__ void put_q4(uint8_t* quants, uint8_t* scale, int part
   if (part == 0) *reinterpret_cast<unsigned short*>(scale) = __half_as_ushort(__float2half_rn(d));
 }
 
-template <typename T, int KV, bool kVec>
+template <typename T, int KV, bool kVec, int kPer>
 __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvRowsParams P) {
   griddep_launch_dependents();
   griddep_wait();  // (a programmatic dependent: the previous work is complete)
   const T* src = static_cast<const T*>(blockIdx.z ? P.v : P.k);
   uint8_t* cache = blockIdx.z ? P.vc : P.kc;
-  const int groups = (P.width + kGroupE - 1) / kGroupE;
-  const long long item = (long long)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t groups = P.groups.d, first = blockIdx.x * (kRowThreads * kPer);
   for (int s = blockIdx.y; s < P.batch; s += gridDim.y) {
     int pos, count;
     seq_rows(P, s, blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0, pos, count);
-    const long long items = (long long)count * groups;
-    if ((long long)blockIdx.x * kRowThreads >= items) continue;  // (the whole CTA)
-    const bool live = item < items;
-    const int i = live ? (int)(item / groups) : 0, g = live ? (int)(item - (long long)i * groups) : 0;
-    const int n = min(kGroupE, P.width - g * kGroupE);
-    float f[kGroupE];
-    load8<T, kVec>(src + ((long long)s * P.rows + i) * P.ld + g * kGroupE, n, f);
+    const uint32_t items = (uint32_t)count * groups;
+    if (first >= items) continue;  // (the whole CTA)
+    const T* rows = src + (long long)s * P.rows * P.ld;
     uint8_t* seq = cache + P.seq_bytes * s;
-    const long long row = pos + i;
-    if constexpr (KV == Q8D_KV_Q4) {
-      const int blk = g >> 2;
-      put_q4(seq + row * (P.width / 2) + blk * 16,
-             seq + q4_scale_plane(P.cap, P.width) + row * (P.width / 16) + blk * 2, g & 3, f, live);
-    } else if constexpr (KV == Q8D_KV_Q8_0) {
-      put_q8_0(seq + (row * (P.width / kQBlock) + (g >> 2)) * kQBlockBytes, g & 3, f, live);
-    } else {
-      using C = typename CacheT<KV>::T;
-      C* dst = reinterpret_cast<C*>(seq) + row * P.width + g * kGroupE;
-      if (live) {
+    float f[kPer][kGroupE];
+    int row[kPer], g[kPer];
+    bool live[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const uint32_t item = first + threadIdx.x + u * kRowThreads;
+      live[u] = item < items;
+      row[u] = live[u] ? (int)P.groups.div(item) : 0;
+      g[u] = live[u] ? (int)(item - (uint32_t)row[u] * groups) : 0;
+      load8<T, kVec>(rows + (long long)row[u] * P.ld + g[u] * kGroupE, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
+      row[u] += pos;
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const long long r = row[u];
+      if constexpr (KV == Q8D_KV_Q4) {
+        const int blk = g[u] >> 2;
+        put_q4(seq + r * (P.width / 2) + blk * 16,
+               seq + q4_scale_plane(P.cap, P.width) + r * (P.width / 16) + blk * 2, g[u] & 3, f[u], live[u]);
+      } else if constexpr (KV == Q8D_KV_Q8_0) {
+        put_q8_0(seq + (r * (P.width / kQBlock) + (g[u] >> 2)) * kQBlockBytes, g[u] & 3, f[u], live[u]);
+      } else {
+        using C = typename CacheT<KV>::T;
+        C* dst = reinterpret_cast<C*>(seq) + r * P.width + g[u] * kGroupE;
+        if (!live[u]) continue;
         if (P.width % kGroupE == 0)
-          store8<C, true>(dst, n, f);
+          store8<C, true>(dst, kGroupE, f[u]);
         else
-          store8<C, false>(dst, n, f);
+          store8<C, false>(dst, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
       }
     }
   }
 }
 
-// Reading: for a packed 4-bit row a thread takes half a block (8 bytes:
-// elements 8h .. 8h+7 and 16+8h .. 16+8h+7), so every access outside is 16
-// bytes or more; otherwise eight consecutive elements.
-template <typename T, int KV, bool kVec>
+// Reading: for a 4-bit row an item is half a block (8 bytes: elements 8h ..
+// 8h+7 and 16+8h .. 16+8h+7, so every access outside is 16 bytes or more),
+// otherwise eight consecutive elements; kPer items a thread, kRowThreads
+// apart, loaded before any is converted.
+template <int KV>
+constexpr int read_item() {
+  return KV == Q8D_KV_Q4 ? 16 : kGroupE;
+}
+
+// What an item holds of a packed row, and its values.
+template <int KV>
+struct Packed {
+  uint32_t w[4];
+  float d;
+};
+template <>
+struct Packed<Q8D_KV_Q4> {
+  uint2 w;
+  float d;
+};
+
+template <typename T, int KV, bool kVec, int kPer>
 __global__ void __launch_bounds__(kRowThreads) kv_read_rows_kernel(const KvRowsParams P) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kItemE = KV == Q8D_KV_Q4 ? 16 : kGroupE;
   T* dst = static_cast<T*>(blockIdx.z ? P.v : P.k);
   const uint8_t* cache = blockIdx.z ? P.vc : P.kc;
-  const int groups = (P.width + kItemE - 1) / kItemE;
-  const long long item = (long long)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t groups = P.groups.d, first = blockIdx.x * (kRowThreads * kPer);
+  const float nan = __int_as_float(0x7fc00000);
   for (int s = blockIdx.y; s < P.batch; s += gridDim.y) {
     int pos, count;
     const bool ok =
         seq_rows(P, s, blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0, pos, count);
     // (the rows of a refused sequence become NaN)
-    if (item >= (long long)(ok ? count : P.rows) * groups) continue;
-    const int i = (int)(item / groups), g = (int)(item - (long long)i * groups);
-    T* out = dst + ((long long)s * P.rows + i) * P.ld;
+    const uint32_t items = (uint32_t)(ok ? count : P.rows) * groups;
+    if (first >= items) continue;  // (the whole CTA)
     const uint8_t* seq = cache + P.seq_bytes * s;
-    const long long row = pos + i;
-    float f[kGroupE];
-    if constexpr (KV == Q8D_KV_Q4) {
-      const int blk = g >> 1, h = g & 1;
-      uint2 w = make_uint2(0u, 0u);
-      float d = __int_as_float(0x7fc00000);
-      if (ok) {
-        w = *reinterpret_cast<const uint2*>(seq + row * (P.width / 2) + blk * 16 + h * 8);
-        d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(
-            seq + q4_scale_plane(P.cap, P.width) + row * (P.width / 16) + blk * 2));
-      }
+    T* rows = dst + (long long)s * P.rows * P.ld;
+    Packed<KV> in[kPer];
+    float f[kPer][kGroupE];
+    int row[kPer], g[kPer];
+    bool live[kPer];
 #pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-#pragma unroll
-        for (int e = 0; e < kGroupE; ++e) {
-          const uint32_t word = e < 4 ? w.x : w.y;
-          f[e] = d * ((float)((word >> (8 * (e & 3) + 4 * hi)) & 15u) - 8.f);
-        }
-        store8<T, kVec>(out + blk * 32 + hi * 16 + h * 8, kGroupE, f);
-      }
-    } else {
-      const int n = min(kGroupE, P.width - g * kGroupE);
-      if (!ok) {
-#pragma unroll
-        for (int e = 0; e < kGroupE; ++e) f[e] = __int_as_float(0x7fc00000);
+    for (int u = 0; u < kPer; ++u) {
+      const uint32_t item = first + threadIdx.x + u * kRowThreads;
+      live[u] = item < items;
+      row[u] = live[u] ? (int)P.groups.div(item) : 0;
+      g[u] = live[u] ? (int)(item - (uint32_t)row[u] * groups) : 0;
+      const long long r = ok ? pos + row[u] : 0;  // (row 0 for a refused sequence: not used)
+      if constexpr (KV == Q8D_KV_Q4) {
+        const int blk = g[u] >> 1, h = g[u] & 1;
+        in[u].w = *reinterpret_cast<const uint2*>(seq + r * (P.width / 2) + blk * 16 + h * 8);
+        in[u].d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(
+            seq + q4_scale_plane(P.cap, P.width) + r * (P.width / 16) + blk * 2));
       } else if constexpr (KV == Q8D_KV_Q8_0) {
-        const uint8_t* blk = seq + (row * (P.width / kQBlock) + (g >> 2)) * kQBlockBytes;
-        const float d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(blk));
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(blk + 2 + 8 * (g & 3));
+        const uint8_t* blk = seq + (r * (P.width / kQBlock) + (g[u] >> 2)) * kQBlockBytes;
+        in[u].d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(blk));
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(blk + 2 + 8 * (g[u] & 3));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const unsigned short u = q[e];
-          f[2 * e] = d * (float)(int8_t)(u & 0xff);
-          f[2 * e + 1] = d * (float)(int8_t)(u >> 8);
-        }
+        for (int e = 0; e < 4; ++e) in[u].w[e] = q[e];
       } else {
         using C = typename CacheT<KV>::T;
-        const C* p = reinterpret_cast<const C*>(seq) + row * P.width + g * kGroupE;
+        const C* p = reinterpret_cast<const C*>(seq) + r * P.width + g[u] * kGroupE;
         if (P.width % kGroupE == 0)
-          load8<C, true>(p, n, f);
+          load8<C, true>(p, kGroupE, f[u]);
         else
-          load8<C, false>(p, n, f);
+          load8<C, false>(p, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
       }
-      store8<T, kVec>(out + g * kGroupE, n, f);
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      if (!live[u]) continue;
+      T* out = rows + (long long)row[u] * P.ld;
+      if constexpr (KV == Q8D_KV_Q4) {
+        const float d = ok ? in[u].d : nan;
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+#pragma unroll
+          for (int e = 0; e < kGroupE; ++e) {
+            // half-byte n under the exponent of 2^23: 2^23 + n, exactly
+            const uint32_t n = ((e < 4 ? in[u].w.x : in[u].w.y) >> (8 * (e & 3) + 4 * hi)) & 15u;
+            f[u][e] = d * (__uint_as_float(n | 0x4B000000u) - 8388616.f);
+          }
+          store8<T, kVec>(out + (g[u] >> 1) * 32 + (g[u] & 1) * 8 + hi * 16, kGroupE, f[u]);
+        }
+      } else {
+        if constexpr (KV == Q8D_KV_Q8_0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t q = in[u].w[e] ^ 0x8080u;
+            f[u][2 * e] = in[u].d * (__uint_as_float((q & 0xffu) | kMagicHi) - kMagicBias);
+            f[u][2 * e + 1] = in[u].d * (__uint_as_float((q >> 8) | kMagicHi) - kMagicBias);
+          }
+        }
+        if (!ok) {
+#pragma unroll
+          for (int e = 0; e < kGroupE; ++e) f[u][e] = nan;
+        }
+        store8<T, kVec>(out + g[u] * kGroupE, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
+      }
     }
   }
 }
 
+template <bool kRead, typename T, int KV, bool kVec, int kPer>
+int launch_rows_per(const KvRowsParams& P, cudaStream_t stream) {
+  const long long items = (long long)P.rows * P.groups.d, cta = kRowThreads * kPer;
+  const dim3 grid((unsigned)((items + cta - 1) / cta), (unsigned)std::min(P.batch, 65535), 2);
+  if constexpr (kRead)
+    return launch_ex(kv_read_rows_kernel<T, KV, kVec, kPer>, grid, dim3(kRowThreads), 0, stream, true, P);
+  else
+    return launch_ex(kv_append_rows_kernel<T, KV, kVec, kPer>, grid, dim3(kRowThreads), 0, stream, true, P);
+}
+
 template <bool kRead, typename T, int KV>
-int launch_rows(const KvRowsParams& P, cudaStream_t stream) {
-  const int item_e = kRead && KV == Q8D_KV_Q4 ? 16 : kGroupE;
-  const long long items = (long long)P.rows * ((P.width + item_e - 1) / item_e);
-  const long long gx = (items + kRowThreads - 1) / kRowThreads;
-  if (gx > 0x7fffffffLL) return Q8D_EUNSUPPORTED;
-  const dim3 grid((unsigned)gx, (unsigned)std::min(P.batch, 65535), 2);
+int launch_rows(KvRowsParams P, cudaStream_t stream) {
+  const int item_e = kRead ? read_item<KV>() : kGroupE;
+  P.groups = fast_div((uint32_t)((P.width + item_e - 1) / item_e));
+  const long long items = (long long)P.rows * P.groups.d;
+  if (items > 0xffff0000LL) return Q8D_EUNSUPPORTED;  // (item numbers are 32 bits)
   // 16-byte accesses outside the cache where every row allows them
   const bool vec = P.width % kGroupE == 0 && (reinterpret_cast<uintptr_t>(P.k) % 16) == 0 &&
                    (reinterpret_cast<uintptr_t>(P.v) % 16) == 0 && (P.ld * sizeof(T)) % 16 == 0;
-  if constexpr (kRead)
-    return vec ? launch_ex(kv_read_rows_kernel<T, KV, true>, grid, dim3(kRowThreads), 0, stream, true, P)
-               : launch_ex(kv_read_rows_kernel<T, KV, false>, grid, dim3(kRowThreads), 0, stream, true, P);
-  else
-    return vec ? launch_ex(kv_append_rows_kernel<T, KV, true>, grid, dim3(kRowThreads), 0, stream, true, P)
-               : launch_ex(kv_append_rows_kernel<T, KV, false>, grid, dim3(kRowThreads), 0, stream, true, P);
+  // Several items a thread once one each would take more than two full
+  // machines (at one: 5.3 against 5.0 us for 4096 rows of 1024 f16 into 4
+  // bits).  Four or two, whichever measured better, us: Q8_0 8 x 2047 rows of
+  // 1024 f32, append 15.8 / 16.4 (with a rounding of fewer instructions that
+  // was not roundf's for NaN), read 13.4 / 14.0; 4 bits, 32768 rows of
+  // 1024, append 67.8 / 59.1 (it holds 32 f32 values a thread at four), read
+  // 27.1 / 27.0; 16384 rows f32 from f16, read 41.0 / 38.0.
+  constexpr int kMany = KV == Q8D_KV_Q8_0 ? 4 : 2;
+  const bool many = items * P.batch * 2 > 2LL * 2048 * sm_count();
+  if (!vec) return launch_rows_per<kRead, T, KV, false, 1>(P, stream);
+  return many ? launch_rows_per<kRead, T, KV, true, kMany>(P, stream)
+              : launch_rows_per<kRead, T, KV, true, 1>(P, stream);
 }
 
 template <bool kRead, typename T>

@@ -9,6 +9,25 @@
 
 namespace q8d {
 
+// n / d for any 32-bit n by a multiplication (d fixed by the host): q =
+// (((n - t) >> 1) + t) >> s with t = n * m >> 32.
+struct FastDiv {
+  uint32_t d, m, s;
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    const uint32_t t = __umulhi(n, m);
+    return d == 1 ? n : ((n - t) / 2 + t) >> s;
+  }
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;  // ceil(log2 d)
+  while (l < 32 && (1ull << l) < d) ++l;
+  FastDiv f;
+  f.d = d;
+  f.m = (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+  f.s = l ? l - 1 : 0;
+  return f;
+}
+
 struct KvRowsParams {
   void* k;  // rows outside the cache: row i of sequence s at element (s * rows + i) * ld
   void* v;
@@ -22,6 +41,7 @@ struct KvRowsParams {
   const int* d_pos;
   const int* d_counts;  // or nullptr: `rows` rows of every sequence
   int* d_err;
+  FastDiv groups;  // items a row (set by the launch)
 };
 
 int kv_append_rows_launch(const KvRowsParams& P, cudaStream_t stream);
@@ -47,10 +67,13 @@ __device__ __forceinline__ void q4_scale(float m, float& d, float& id) {
   id = __fdiv_rn(1.0f, d);
   if (!isfinite(id)) id = 0.f;  // (an all-zero block, or 1 / d beyond f32: all nibbles 8)
 }
-// n = clamp(floor(x / d + 8.5), 0, 15) in single correctly rounded f32 steps
+// n = clamp(floor(x / d + 8.5), 0, 15) in single correctly rounded f32 steps.
+// The floor is the sum with 2^23 rounded down (its low bits): the rounding
+// and conversion instructions run at a quarter of the rate and would bound
+// the store.
 __device__ __forceinline__ uint32_t q4_nibble(float x, float id) {
-  const float n = floorf(__fadd_rn(__fmul_rn(x, id), 8.5f));
-  return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+  const float t = __fadd_rn(__fmul_rn(x, id), 8.5f);
+  return __float_as_uint(__fadd_rd(fminf(fmaxf(t, 0.f), 15.5f), 8388608.f)) & 15u;
 }
 // Keeps of (m, o) the larger magnitude, on a tie the one of lower index.
 __device__ __forceinline__ float q4_larger(float m, float o, bool o_first) {
