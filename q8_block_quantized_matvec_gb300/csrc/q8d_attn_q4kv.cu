@@ -1,26 +1,32 @@
 // Split-K decode attention over a 4-bit KV cache (Q8D_KV_Q4) on the tensor
-// cores: the contract and the split of the other decode-attention kernels.
+// cores: the contract of the other decode-attention kernels.
 //
 // At 9/16 byte an element the arithmetic, not HBM, is what such a kernel runs
 // out of first: at the copy rate an SM gets one token of one KV head (144
-// bytes at head_dim 128) every 6 cycles, about 390 warp instructions for 16
-// tokens.  So the layout below spends nothing on moving values between lanes
-// and about five integer instructions on eight quants:
+// bytes at head_dim 128) every 6 cycles, 780 issue slots for a tile of 32
+// tokens; the tile takes 740 warp instructions with up to four heads a KV
+// head, 920 with five to eight, 288 of them to unpack its quants, and sixteen
+// warps an SM (128 registers each) fill 55 to 60 percent of the slots.  So
+// the layout saves instructions:
 //  * A half-byte n put under the exponent of 1024 is the f16 1024 + n (1024 +
 //    16 n for the upper one): one LOP3 a pair, and one sub.f16x2 leaves the
 //    exact n - 8 (16 (n - 8)).  (Masked out alone it would be the subnormal
 //    n * 2^-24, without a subtraction; but the tensor core aligns products by
 //    the operands' exponent fields, and a subnormal's loses it 7 bits.)
-//  * Q.K^T: rows of A are the heads' q, hi and lo f16 parts in rows g and
-//    g + 8 (so one MMA does both and they meet in one lane), columns of B
-//    eight tokens.  A block's two k-steps are scaled by the token's block
-//    scale.  Lane (g, c) ends with head g and tokens 2c,
-//    2c+1: exactly the B fragment that P.V wants.
-//  * P.V: rows of A are dims, columns of B heads, the contraction runs over
-//    tokens; ldmatrix.trans hands a lane the same two bytes of tokens 2c and
-//    2c+1.  V's scale depends on the token and the block, so it multiplies P
-//    once per block before the hi + lo split.  With at most four heads a KV
-//    head the eight columns hold hi and lo of four heads: half the MMAs.
+//  * Rows of A are what the cache holds (16 tokens for K.Q^T, 16 dims for
+//    V.P^T) and columns of B the heads, so the few heads of a KV head fill
+//    the short side.  q, and P times V's scale, are f16 hi + lo parts: results
+//    keep f32's accuracy.  With at most four heads a KV head, hi and lo are
+//    neighbouring columns and one MMA does both; else each takes its own.
+//    (Heads as rows of A, hi and lo in rows g and g + 8, took 920
+//    instructions a tile with two heads: 62 us for 32 sequences of up to 8192
+//    tokens, 16 query and 8 KV heads of 128, against 45 now.)
+//  * A lane's scores are tokens g, g + 8, .. of heads 2c, 2c + 1 (packed: of
+//    head c), so a token's scale and a head's factors are loaded or kept
+//    once.  V's scale depends on the token and the block, so it multiplies P
+//    once per block before the hi + lo split; movmatrix turns the halves into
+//    the B operand; ldmatrix.trans hands a lane the same two bytes of V of
+//    tokens 2c and 2c + 1.
 //  * P * scale * 2^fe stays inside f16: fe follows the largest V scale seen
 //    (a power of two, so changing it is exact).  Both fe and the running
 //    maximum move only when they must (the maximum when a score exceeds it
@@ -46,7 +52,7 @@ constexpr float kLog2e4 = 1.4426950408889634f;
 constexpr int kTile4 = 32;        // tokens a warp step
 constexpr int kStages4 = 2;
 constexpr float kSlack4 = 8.f;    // the running maximum may lag by this (log2)
-constexpr int kSeqCtas4 = 4;
+constexpr int kSeqCost4 = 16;     // a sequence's fixed work, in tiles
 constexpr int kFe0 = 7;           // P <= 2^8, |scale| < 2^ev, 2^fe = 2^(7 - ev): products < 2^15
 
 template <int D, int NH>
@@ -117,20 +123,26 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// The NB halves of each of two neighbouring tokens' scales.
+// The NB halves of a token's scales.
 template <int NB>
-__device__ __forceinline__ void scales2(const uint8_t* p, uint32_t (&w)[NB]) {
+__device__ __forceinline__ void scales4(const uint8_t* p, uint32_t (&w)[NB / 2]) {
   if constexpr (NB == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  } else {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x;
     w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
+}
+__device__ __forceinline__ float half_of(uint32_t w, int i) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&w);
+  return i ? __high2float(h) : __low2float(h);
+}
+// An 8 x 8 matrix of halves (lane (g, c): row g, columns 2c, 2c+1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
 }
 // n - 8 of the low half-bytes n of bytes 0 and 2 of w as an exact f16 pair
 // (kHi: 16 (n - 8) of the high half-bytes).
@@ -145,20 +157,22 @@ __device__ __forceinline__ uint32_t nib8(uint32_t w, uint32_t k1024) {
 __device__ __forceinline__ float2 h2f(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// Half bb of both tokens of scales2, as an f32 pair.
-template <int NB>
-__device__ __forceinline__ uint64_t scale_pair(const uint32_t (&w)[NB], int bb) {
-  const float2 a = h2f(w[bb / 2]), b = h2f(w[NB / 2 + bb / 2]);
-  return bb & 1 ? pack2(a.y, b.y) : pack2(a.x, b.x);
-}
 __device__ __forceinline__ uint32_t f2h(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// ---- the split: q8d_attn.cuh's rule in f32 steps, a sequence a lane ----
-// (There one thread walks the batch with 64-bit divisions: 32 sequences cost
-// it more than a tile of attention.)
+// ---- the split ----
+// The batch's tiles of kTile4 rows, sequence after sequence, are cut into
+// pieces of equal length, one a CTA (of each KV head), whatever sequences
+// they lie in: one wave of CTAs that end together.  A sequence counts
+// kSeqCost4 tiles more than it has (its queries, the first loads, the merge),
+// in front of its rows.  The lengths live in device memory, so every CTA and
+// the combine derive the same cut from them.  (Chunks of one sequence each,
+// four a sequence on average and 3.4 waves: 62 us in the case above, 54 so
+// with the same tile; kSeqCost4 of 6, 12, 16, 28: 45.9, 44.9, 45.2, 45.9 us
+// there and 31.2, 30.5, 29.8, 30.4 for 8 sequences of up to 32768, 28 query
+// and 4 KV heads.)
 __device__ __forceinline__ int window_len4(const AttnParams& P, int b) {
   if (!P.d_runs) {
     const int L = __ldcg(P.d_lens + b);
@@ -166,67 +180,118 @@ __device__ __forceinline__ int window_len4(const AttnParams& P, int b) {
   }
   return attn_window_len(P, b);
 }
-// (nct - batch) / (the batch's rows), a shade less than exact so that the
-// chunks never outnumber the CTAs: the f32 sum and products are off by under
-// 2^-20.  Every lane of a warp calls.
-__device__ __forceinline__ float chunk_rate4(const AttnParams& P, int lane) {
-  if (P.batch == 1) return 0.f;
-  float t = 0.f;
-  for (int s = lane; s < P.batch; s += 32) t += (float)max(window_len4(P, s), 0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t > 0.f ? 0.99999f * (float)(P.nct - P.batch) / t : 0.f;
-}
-__device__ __forceinline__ int nchunks4(const AttnParams& P, int L, float rate) {
-  int n = P.batch == 1 ? P.nct : 1 + (int)(rate * (float)L);
-  n = min(n, min((L + kMinChunk - 1) / kMinChunk, P.nc));
-  return max(n, 1);
+__device__ __forceinline__ int tiles4(int L) { return L < 1 ? 0 : (L + kTile4 - 1) / kTile4; }
+
+struct Split4 {
+  int piece;  // tiles a CTA
+  bool bad;   // an invalid length
+  // With a single workspace slot a sequence (caches of up to kMinChunk rows)
+  // goes whole to the CTA in whose piece it starts.
+  bool whole;
+  int len;    // of sequence `lane`
+};
+// Every lane of a warp calls.
+__device__ __forceinline__ Split4 split4(const AttnParams& P, int lane) {
+  Split4 S;
+  S.whole = P.nc == 1;
+  if (P.batch == 1) {  // (no sums to wait for)
+    S.len = window_len4(P, 0);
+    S.bad = S.len < 1;
+    const int ctas = min(P.nct, P.nc);
+    S.piece = max(kMinChunk / kTile4, (tiles4(S.len) + ctas - 1) / ctas);
+    return S;
+  }
+  int sum = 0, most = 0;
+  bool bad = false;
+  S.len = -1;
+  for (int s = lane; s < P.batch; s += 32) {
+    const int L = window_len4(P, s), n = tiles4(L);
+    if (s < 32) S.len = L;
+    bad = bad || n == 0;
+    sum += n ? n + kSeqCost4 : 0;
+    most = max(most, n);
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  most = __reduce_max_sync(0xffffffffu, most);
+  S.bad = __any_sync(0xffffffffu, bad);
+  S.piece = max(kMinChunk / kTile4, (sum + P.nct - 1) / P.nct);
+  // a sequence's pieces fit its slots: with rows that start anywhere in a
+  // piece, k pieces' length touches k + 1
+  if (P.nc > 1) S.piece = max(S.piece, (most + P.nc - 2) / (P.nc - 1));
+  return S;
 }
 
-// This CTA's sequence, chunk (of n) and the sequence's rows.
-__device__ __forceinline__ bool chunk_of_warp(const AttnParams& P, int k, int lane, int& b, int& c,
-                                              int& n, int& L) {
-  if (P.batch == 1) {
-    b = 0;
-    c = k;
-    L = window_len4(P, 0);
-    n = nchunks4(P, L, 0.f);
-    return k < n;
+// The length of sequence b and where its rows start.  Every lane of a warp
+// calls.
+__device__ __forceinline__ int seq_of4(const AttnParams& P, const Split4& S, int b, int lane, int& L) {
+  L = S.len;
+  if (P.batch == 1) return 0;
+  int sum = 0;
+  for (int s = lane; s < b; s += 32) {
+    const int n = tiles4(s < 32 ? S.len : window_len4(P, s));
+    sum += n ? n + kSeqCost4 : 0;
   }
-  const float rate = chunk_rate4(P, lane);
-  int first = 0;
+  L = b < 32 ? __shfl_sync(0xffffffffu, S.len, b) : window_len4(P, b);
+  return (int)__reduce_add_sync(0xffffffffu, sum) + kSeqCost4;
+}
+
+// A sequence with rows in a CTA's piece, and where its first row lies.
+struct Seq4 {
+  int b, L, at;
+};
+// The first sequence with rows at or after tile `from` (whole: that starts
+// there); false if there is none.  Every lane of a warp calls.
+__device__ __forceinline__ bool seq_from4(const AttnParams& P, const Split4& S, int from, int lane, Seq4& q) {
+  if (P.batch == 1) {
+    q.b = q.at = 0;
+    q.L = S.len;
+    return from < tiles4(S.len);
+  }
+  int before = 0;
   for (int s0 = 0; s0 < P.batch; s0 += 32) {
     const int s = s0 + lane;
-    const int len = s < P.batch ? window_len4(P, s) : 0;
-    const int ns = s < P.batch ? nchunks4(P, len, rate) : 0;
-    int end = ns;  // inclusive prefix sum
+    const int L = s0 == 0 ? S.len : s < P.batch ? window_len4(P, s) : -1;
+    const int n = tiles4(L);
+    int end = n ? n + kSeqCost4 : 0;  // inclusive prefix sum
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += v;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, k < first + end && s < P.batch);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      b = s0 + at;
-      n = __shfl_sync(0xffffffffu, ns, at);
-      c = k - first - (__shfl_sync(0xffffffffu, end, at) - n);
-      L = __shfl_sync(0xffffffffu, len, at);
+    end += before;
+    const uint32_t hit = __ballot_sync(0xffffffffu, n && (S.whole ? end - n >= from : end > from));
+    if (hit) {
+      const int x = __ffs(hit) - 1;
+      q.b = s0 + x;
+      q.L = __shfl_sync(0xffffffffu, L, x);
+      q.at = __shfl_sync(0xffffffffu, end - n, x);
       return true;
     }
-    first += __shfl_sync(0xffffffffu, end, 31);
+    before = __shfl_sync(0xffffffffu, end, 31);
+  }
+  return false;
+}
+// The next sequence with rows; false if there is none.
+__device__ __forceinline__ bool seq_next4(const AttnParams& P, Seq4& q) {
+  q.at += tiles4(q.L) + kSeqCost4;
+  while (++q.b < P.batch) {
+    q.L = window_len4(P, q.b);
+    if (q.L >= 1) return true;
   }
   return false;
 }
 
-// NH: tiles of eight heads (1 or 2).  kPack: at most four heads, hi and lo
-// parts of P side by side in one tile.
+// NH: column tiles (2 for nine to sixteen heads).  kPack: at most four heads,
+// a head's hi and lo parts in columns 2h and 2h + 1 of one tile; else a tile
+// is eight heads and hi and lo take an MMA each.
 template <int D, int NH, bool kPack>
 __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(const AttnParams P) {
   using C = Cfg4<D, NH>;
   constexpr int NB = C::kNB;
   constexpr int KS = D / 16;
-  constexpr int NT = kTile4 / 8;  // 8-token columns of a tile
+  constexpr int NT = kTile4 / 8;      // groups of eight tokens of a tile
+  constexpr int HC = kPack ? 1 : 2;   // heads a lane keeps scores of, of each column tile
+  constexpr int kHeads = kPack ? 4 : 8 * NH;
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
   float* fh = reinterpret_cast<float*>(smem + C::kOffF);
@@ -240,50 +305,16 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   // after the wait: the combine, scheduled from here on, may read the lengths
   // before this grid is done
   griddep_launch_dependents();
-  int b, c, n, L;
-  if (!chunk_of_warp(P, blockIdx.x, lane, b, c, n, L)) return;
-  if (L < 1) {  // (the combine writes NaN outputs)
-    if (g == 0 && tid == 0 && P.d_err) atomicOr(P.d_err, Q8D_DERR_LEN_RANGE);
-    return;
-  }
-  const int tpc = (L + n - 1) / n;
-  const int t_begin = c * tpc;
-  if (t_begin >= L) return;
-  const int t_end = min(L, t_begin + tpc);
+  const Split4 sp = split4(P, lane);
+  // (the combine writes NaN outputs)
+  if (sp.bad && blockIdx.x == 0 && g == 0 && tid == 0 && P.d_err) atomicOr(P.d_err, Q8D_DERR_LEN_RANGE);
+  const int p_begin = blockIdx.x * sp.piece;
+  Seq4 sq;
+  if (!seq_from4(P, sp, p_begin, lane, sq)) return;
+
   const int width = P.n_kv_heads * D;
-  const long long seq_off = (long long)b * (P.batch_stride / kQBlock) * 18;
   const long long splane = q4_scale_plane(P.cap, width);
   const uint32_t rowq = (uint32_t)width / 2, rows = (uint32_t)width / 16;  // bytes a row
-  uint8_t* kq = static_cast<uint8_t*>(P.kcache) + seq_off + g * C::kRow;
-  uint8_t* vq = static_cast<uint8_t*>(P.vcache) + seq_off + g * C::kRow;
-  uint8_t* ks = static_cast<uint8_t*>(P.kcache) + seq_off + splane + g * C::kSRow;
-  uint8_t* vs = static_cast<uint8_t*>(P.vcache) + seq_off + splane + g * C::kSRow;
-
-  // In-kernel append of row L-1 by the CTA that owns it; read back below.
-  if (P.k_new != nullptr && t_end == L && warp < 2) {
-    const float* src = (warp ? P.v_new : P.k_new) + (long long)b * width + (long long)g * D;
-    const long long row = attn_cell(P, b, L - 1);
-#pragma unroll
-    for (int t = 0; t < NB; ++t)
-      quantize_q4_warp(src[lane + 32 * t], (warp ? vq : kq) + row * rowq + 16 * t,
-                       (warp ? vs : ks) + row * rows + 2 * t, lane);
-  }
-  // a causal window is the one run (0, L): only run maps and the appended row
-  // need the CTA's threads to meet here
-  int run0_len = L, run0_cell = 0;
-  if (P.d_runs) {
-    if (tid == 0) attn_window_store(P, b, &s_win);
-    __syncthreads();
-    run0_len = s_win.len[0];
-    run0_cell = s_win.cell[0];
-  } else if (P.k_new != nullptr && t_end == L) {
-    __syncthreads();
-  }
-  const auto cell_of = [&](int t) { return t < run0_len ? run0_cell + t : s_win.cell_of(t); };
-
-  // ---- this warp's ring over its tiles (tile i: tokens t_begin + 32 (warp + 8 i)) ----
-  const int ntiles = (t_end - t_begin + kTile4 - 1) / kTile4;
-  const int my_tiles = ntiles > warp ? (ntiles - warp + kWarps4 - 1) / kWarps4 : 0;
   const uint32_t ring = smem_u32(smem) + warp * kStages4 * C::kStage;
   constexpr int kCh = C::kRow / 16;          // 16-byte chunks of a head row
   constexpr int kRowsPass = 32 / kCh;        // rows the lanes copy at once
@@ -291,110 +322,10 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   // (the swizzle repeats every 8 rows: it does not depend on the pass)
   constexpr int kSwz = D == 128 ? 1 : 2;
   const uint32_t ld_dst = ld_r * C::kRow + ((ld_c ^ ((ld_r >> kSwz) & (kCh - 1))) << 4);
-  auto load_tile = [&](int i) {
-    if (i < my_tiles) {
-      const int t0 = t_begin + (warp + kWarps4 * i) * kTile4;
-      const int nr = min(kTile4, t_end - t0);
-      const uint32_t st = ring + (i % kStages4) * C::kStage;
-      if (nr == kTile4 && t0 + kTile4 <= run0_len) {
-        const long long row = run0_cell + t0 + ld_r;
-        const uint8_t* kp = kq + row * rowq + ld_c * 16;
-        const uint8_t* vp = vq + row * rowq + ld_c * 16;
-#pragma unroll
-        for (int k = 0; k < kTile4 / kRowsPass; ++k) {
-          cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kp + k * kRowsPass * rowq, true);
-          cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vp + k * kRowsPass * rowq, true);
-        }
-        const long long sr = run0_cell + t0 + lane;
-        cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + sr * rows, true);
-        cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + sr * rows, true);
-      } else {
-        // rows past the chunk become zeros: scale 0, so they add nothing
-        for (int k = 0; k < kTile4 / kRowsPass; ++k) {
-          const int r = k * kRowsPass + ld_r;
-          const bool live = r < nr;
-          const long long off = (long long)cell_of(t0 + (live ? r : 0)) * rowq + ld_c * 16;
-          cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kq + off, live);
-          cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vq + off, live);
-        }
-        const bool live = lane < nr;
-        const long long off = (long long)cell_of(t0 + (live ? lane : 0)) * rows;
-        cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + off, live);
-        cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + off, live);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");  // (possibly empty: a uniform count)
-  };
-#pragma unroll
-  for (int i = 0; i < kStages4 - 1; ++i) load_tile(i);
-
-  // ---- q * scale * log2(e), rows times 2^sh into [2^14, 2^15), 2^-sh ----
-#pragma unroll
-  for (int u = 0; u < NH; ++u) {
-    const int hh = warp + 8 * u;                       // fragment row
-    const int head = kPack ? hh & 3 : hh;              // (packed: heads 0-3 twice)
-    float v[NB];
-    float mx = 0.f;
-#pragma unroll
-    for (int t = 0; t < NB; ++t) {
-      v[t] = head < G ? P.q[((long long)b * P.n_heads + g * G + head) * D + lane + 32 * t] * (P.scale * kLog2e4) : 0.f;
-      mx = fmaxf(mx, fabsf(v[t]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // mx < 2^(field - 126); sh in [-126, 126] keeps 2^sh and 2^-sh normal
-    const int field = (int)(__float_as_uint(mx) >> 23);
-    const int sh = max(-126, min(126, 15 + 126 - field));
-    const float up = __int_as_float((127 + sh) << 23);
-#pragma unroll
-    for (int t = 0; t < NB; ++t) qs[hh * D + lane + 32 * t] = v[t] * up;
-    if (lane == 0) fh[hh] = __int_as_float((127 - sh) << 23);
-  }
-  __syncthreads();
-  // A fragments: lane (g, c) of k-step kk = 2 blk + half holds dims 32 blk + 16
-  // half + 4c + {0, 2} (k slots 2c, 2c+1) and + {1, 3} (slots 2c+8, 2c+9), hi
-  // in row g, lo in row g + 8; the upper half-bytes count 16-fold, so theirs
-  // are divided by 16.
-  uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQf);
-  for (int i = tid; i < NH * KS * 32; i += kThreads4) {
-    const int ln = i & 31, kk = (i >> 5) % KS, ht = i / (32 * KS);
-    const float* q = qs + (ht * 8 + (ln >> 2)) * D + 16 * kk + 4 * (ln & 3);
-    const float f = kk & 1 ? 0.0625f : 1.f;
-    uint4 a;
-    attn_split2(q[0] * f, q[2] * f, a.x, a.y);
-    attn_split2(q[1] * f, q[3] * f, a.z, a.w);
-    qf[i] = a;
-  }
-  __syncthreads();
-  float fac[NH];
-#pragma unroll
-  for (int u = 0; u < NH; ++u) fac[u] = fh[u * 8 + gq];
-
-  // o[u][2 blk + half]: dims 32 blk + 16 half + 2 gq + {0 (rows g), 1 (rows g + 8)}, columns 2cq, 2cq+1
-  float o[NH][2 * NB][4];
-  // head gq of each tile: the running maximum m (log2), the raw score that
-  // moves it, m - fe, and this lane's sum of 2^fe P
-  float m[NH], top[NH], mf[NH];
-  uint64_t l2[NH];
-#pragma unroll
-  for (int u = 0; u < NH; ++u) {
-    m[u] = top[u] = -INFINITY;
-    mf[u] = 0.f;
-    l2[u] = pack2(0.f, 0.f);
-#pragma unroll
-    for (int t = 0; t < 2 * NB; ++t) o[u][t][0] = o[u][t][1] = o[u][t][2] = o[u][t][3] = 0.f;
-  }
-  int lim = -1;       // exponent field of the largest V scale allowed for (-1: none yet)
-  // what the second rounding of P * scale leaves off the first: the part
-  // already held by hi (packed: by the hi columns, for the lo columns)
-  const float hi_off = kPack && gq < 4 ? 0.f : -1.f;
-  const uint64_t hi_off2 = pack2(hi_off, hi_off);
-
   uint32_t k1024;  // (1024, 1024), kept out of the compiler's sight as a constant
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
-  const uint4* qfl = qf + lane;
   // ldmatrix row addresses.  K (x4): 8 tokens, blocks 0-3 (head_dim 64: 8
-  // tokens each of two columns, blocks 0-1); V (x4, transposed): tokens 0-7
+  // tokens each of two groups, blocks 0-1); V (x4, transposed): tokens 0-7
   // and 8-15 of block 2 i, then of block 2 i + 1.
   const int mi = lane >> 3, mr = lane & 7;
   const uint32_t k_row = D == 128 ? mr : (mi >> 1) * 8 + mr, k_blk = D == 128 ? mi : mi & 1;
@@ -405,233 +336,404 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   for (int i = 0; i < NB / 2; ++i)
     v_off[i] = C::kQuants + v_row * C::kRow + (((2 * i + (mi >> 1)) ^ ((v_row >> kSwz) & (kCh - 1))) << 4);
 
-  for (int i = 0; i < my_tiles; ++i) {
-    load_tile(i + kStages4 - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages4 - 1) : "memory");
-    __syncwarp();
-    const int nr = min(kTile4, t_end - (t_begin + (warp + kWarps4 * i) * kTile4));
-    const uint32_t st = ring + (i % kStages4) * C::kStage;
-    const uint8_t* stp = smem + (st - smem_u32(smem));
-
-    // ---- S = Q.K^T ----
-    uint32_t kw[NT][NB];
-    if constexpr (D == 128) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) ldsm4(st + k_off + j * 8 * C::kRow, kw[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NT; j += 2) {
-        uint32_t r[4];
-        ldsm4(st + k_off + j * 8 * C::kRow, r);
-        kw[j][0] = r[0];
-        kw[j][1] = r[1];
-        kw[j + 1][0] = r[2];
-        kw[j + 1][1] = r[3];
-      }
+  for (bool first = true; sq.at < p_begin + sp.piece; first = false) {  // the piece's sequences
+    const int b = sq.b, L = sq.L;
+    int t_begin = 0, t_end = L, c = 0;
+    if (!sp.whole) {
+      t_begin = max(p_begin - sq.at, 0) * kTile4;
+      t_end = min(L, (p_begin + sp.piece - sq.at) * kTile4);
+      c = blockIdx.x - (P.batch == 1 ? 0 : sq.at / sp.piece);
     }
-    // raw scores of tokens 8j + 2cq, + 1 in units of fac
-    uint64_t s2[NH][NT];
+    if (!first) __syncthreads();  // (the merge buffer lies over the ring)
+    const long long seq_off = (long long)b * (P.batch_stride / kQBlock) * 18;
+    uint8_t* kq = static_cast<uint8_t*>(P.kcache) + seq_off + g * C::kRow;
+    uint8_t* vq = static_cast<uint8_t*>(P.vcache) + seq_off + g * C::kRow;
+    uint8_t* ks = static_cast<uint8_t*>(P.kcache) + seq_off + splane + g * C::kSRow;
+    uint8_t* vs = static_cast<uint8_t*>(P.vcache) + seq_off + splane + g * C::kSRow;
+
+    // In-kernel append of row L-1 by the CTA that owns it; read back below.
+    if (P.k_new != nullptr && t_end == L && warp < 2) {
+      const float* src = (warp ? P.v_new : P.k_new) + (long long)b * width + (long long)g * D;
+      const long long row = attn_cell(P, b, L - 1);
+#pragma unroll
+      for (int t = 0; t < NB; ++t)
+        quantize_q4_warp(src[lane + 32 * t], (warp ? vq : kq) + row * rowq + 16 * t,
+                         (warp ? vs : ks) + row * rows + 2 * t, lane);
+    }
+    // a causal window is the one run (0, L): only run maps and the appended row
+    // need the CTA's threads to meet here
+    int run0_len = L, run0_cell = 0;
+    if (P.d_runs) {
+      if (tid == 0) attn_window_store(P, b, &s_win);
+      __syncthreads();
+      run0_len = s_win.len[0];
+      run0_cell = s_win.cell[0];
+    } else if (P.k_new != nullptr && t_end == L) {
+      __syncthreads();
+    }
+    const auto cell_of = [&](int t) { return t < run0_len ? run0_cell + t : s_win.cell_of(t); };
+
+    // ---- this warp's ring over its tiles (tile i: tokens t_begin + 32 (warp + 8 i)) ----
+    const int ntiles = (t_end - t_begin + kTile4 - 1) / kTile4;
+    const int my_tiles = ntiles > warp ? (ntiles - warp + kWarps4 - 1) / kWarps4 : 0;
+    auto load_tile = [&](int i) {
+      if (i < my_tiles) {
+        const int t0 = t_begin + (warp + kWarps4 * i) * kTile4;
+        const int nr = min(kTile4, t_end - t0);
+        const uint32_t st = ring + (i % kStages4) * C::kStage;
+        if (nr == kTile4 && t0 + kTile4 <= run0_len) {
+          const long long row = run0_cell + t0 + ld_r;
+          const uint8_t* kp = kq + row * rowq + ld_c * 16;
+          const uint8_t* vp = vq + row * rowq + ld_c * 16;
+#pragma unroll
+          for (int k = 0; k < kTile4 / kRowsPass; ++k) {
+            cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kp + k * kRowsPass * rowq, true);
+            cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vp + k * kRowsPass * rowq, true);
+          }
+          const long long sr = run0_cell + t0 + lane;
+          cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + sr * rows, true);
+          cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + sr * rows, true);
+        } else {
+          // rows past the chunk become zeros: scale 0, so they add nothing
+          for (int k = 0; k < kTile4 / kRowsPass; ++k) {
+            const int r = k * kRowsPass + ld_r;
+            const bool live = r < nr;
+            const long long off = (long long)cell_of(t0 + (live ? r : 0)) * rowq + ld_c * 16;
+            cp4<16>(st + ld_dst + k * kRowsPass * C::kRow, kq + off, live);
+            cp4<16>(st + C::kQuants + ld_dst + k * kRowsPass * C::kRow, vq + off, live);
+          }
+          const bool live = lane < nr;
+          const long long off = (long long)cell_of(t0 + (live ? lane : 0)) * rows;
+          cp4<C::kSRow>(st + 2 * C::kQuants + lane * C::kSRow, ks + off, live);
+          cp4<C::kSRow>(st + 2 * C::kQuants + C::kScales + lane * C::kSRow, vs + off, live);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");  // (possibly empty: a uniform count)
+    };
+#pragma unroll
+    for (int i = 0; i < kStages4 - 1; ++i) load_tile(i);
+
+    // ---- q * scale * log2(e), rows times 2^sh into [2^14, 2^15), 2^-sh ----
+#pragma unroll
+    for (int u = 0; u < NH; ++u) {
+      const int hh = warp + 8 * u;
+      if (hh >= kHeads) break;
+      float v[NB];
+      float mx = 0.f;
+#pragma unroll
+      for (int t = 0; t < NB; ++t) {
+        v[t] = hh < G ? P.q[((long long)b * P.n_heads + g * G + hh) * D + lane + 32 * t] * (P.scale * kLog2e4) : 0.f;
+        mx = fmaxf(mx, fabsf(v[t]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // mx < 2^(field - 126); sh in [-126, 126] keeps 2^sh and 2^-sh normal
+      const int field = (int)(__float_as_uint(mx) >> 23);
+      const int sh = max(-126, min(126, 15 + 126 - field));
+      const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+      for (int t = 0; t < NB; ++t) qs[hh * D + lane + 32 * t] = v[t] * up;
+      if (lane == 0) fh[hh] = __int_as_float((127 - sh) << 23);
+    }
+    __syncthreads();
+    // B fragments: lane (g, c) of k-step kk = 2 blk + half holds, of column g,
+    // dims 32 blk + 16 half + 4c + {0, 2} (k slots 2c, 2c+1) and + {1, 3} (slots
+    // 2c+8, 2c+9), hi and lo (packed: the column's part); the upper half-bytes
+    // count 16-fold, so theirs are divided by 16.
+    uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQf);
+    for (int i = tid; i < NH * KS * 32; i += kThreads4) {
+      const int ln = i & 31, kk = (i >> 5) % KS, ht = i / (32 * KS);
+      const int head = kPack ? ln >> 3 : ht * 8 + (ln >> 2);
+      const float* q = qs + head * D + 16 * kk + 4 * (ln & 3);
+      const float f = kk & 1 ? 0.0625f : 1.f;
+      uint4 a;  // {hi, hi, lo, lo}
+      attn_split2(q[0] * f, q[2] * f, a.x, a.z);
+      attn_split2(q[1] * f, q[3] * f, a.y, a.w);
+      if constexpr (kPack)
+        reinterpret_cast<uint2*>(qf)[i] = ln & 4 ? make_uint2(a.z, a.w) : make_uint2(a.x, a.y);
+      else
+        qf[i] = a;
+    }
+    __syncthreads();
+    float fac[NH][HC];
 #pragma unroll
     for (int u = 0; u < NH; ++u)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) s2[u][j] = pack2(0.f, 0.f);
-    const uint8_t* sc = stp + 2 * C::kQuants + 2 * cq * C::kSRow;
-    uint32_t ksc[NT][NB];
+      for (int x = 0; x < HC; ++x) fac[u][x] = fh[u * 8 + HC * cq + x];
+
+    // o[u][2 blk + half]: dims 32 blk + 16 half + 2 gq + {0 ([0], [1]), 1 ([2], [3])}, columns 2cq, 2cq+1
+    float o[NH][2 * NB][4];
+    // this lane's heads: the running maximum m (log2), the raw score that
+    // moves it, m - fe, and this lane's sum of 2^fe P
+    float m[NH][HC], top[NH][HC], mf[NH][HC], l[NH][HC];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) scales2<NB>(sc + j * 8 * C::kSRow, ksc[j]);
+    for (int u = 0; u < NH; ++u) {
 #pragma unroll
-    for (int bb = 0; bb < NB; ++bb) {
+      for (int x = 0; x < HC; ++x) {
+        m[u][x] = top[u][x] = -INFINITY;
+        mf[u][x] = l[u][x] = 0.f;
+      }
 #pragma unroll
-      for (int u = 0; u < NH; ++u) {
-        const uint4 a0 = qfl[(u * KS + 2 * bb) * 32], a1 = qfl[(u * KS + 2 * bb + 1) * 32];
+      for (int t = 0; t < 2 * NB; ++t) o[u][t][0] = o[u][t][1] = o[u][t][2] = o[u][t][3] = 0.f;
+    }
+    int lim = -1;       // exponent field of the largest V scale allowed for (-1: none yet)
+
+    for (int i = 0; i < my_tiles; ++i) {
+      load_tile(i + kStages4 - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages4 - 1) : "memory");
+      __syncwarp();
+      const int nr = min(kTile4, t_end - (t_begin + (warp + kWarps4 * i) * kTile4));
+      const uint32_t st = ring + (i % kStages4) * C::kStage;
+      const uint8_t* sc = smem + (st - smem_u32(smem)) + 2 * C::kQuants + gq * C::kSRow;  // token gq's scales
+
+      // ---- S = K.Q^T ----
+      uint32_t kw[NT][NB];
+      if constexpr (D == 128) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ldsm4(st + k_off + j * 8 * C::kRow, kw[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
+          uint32_t r[4];
+          ldsm4(st + k_off + j * 8 * C::kRow, r);
+          kw[j][0] = r[0];
+          kw[j][1] = r[1];
+          kw[j + 1][0] = r[2];
+          kw[j + 1][1] = r[3];
+        }
+      }
+      uint32_t ksc[NT][NB / 2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) scales4<NB>(sc + j * 8 * C::kSRow, ksc[j]);
+      // raw scores of tokens 8j + gq, columns 2cq, 2cq+1 of each tile, in units of fac
+      float s[NH][NT][2];
+#pragma unroll
+      for (int bb = 0; bb < NB; ++bb) {
+        uint32_t a[NT / 2][8];  // A fragments of 16 tokens: k-steps 2 bb and 2 bb + 1
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const uint32_t w = kw[j][bb], w8 = w >> 8;
-          float acc[4];
-          mma4z(acc, a0.x, a0.y, a0.z, a0.w, nib8<false>(w, k1024), nib8<false>(w8, k1024));
-          mma4(acc, a1.x, a1.y, a1.z, a1.w, nib8<true>(w, k1024), nib8<true>(w8, k1024));
-          s2[u][j] = fma2(scale_pair<NB>(ksc[j], bb), add2(pack2(acc[0], acc[1]), pack2(acc[2], acc[3])),
-                          s2[u][j]);
-        }
-      }
-    }
-
-    // ---- the running maximum ----
-    float s[NH][NT][2], mx[NH];
-    bool above = false;
-#pragma unroll
-    for (int u = 0; u < NH; ++u) {
-      mx[u] = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        unpack2(s2[u][j], s[u][j][0], s[u][j][1]);
-        if (nr < kTile4) {
-          if (8 * j + 2 * cq >= nr) s[u][j][0] = -INFINITY;
-          if (8 * j + 2 * cq + 1 >= nr) s[u][j][1] = -INFINITY;
-        }
-        mx[u] = fmaxf(mx[u], fmaxf(s[u][j][0], s[u][j][1]));
-      }
-      above = above || mx[u] > top[u];
-    }
-    // the V scales of this lane's tokens and their largest exponent
-    uint32_t vsc[NT][NB];
-    uint32_t vm = 0u;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      scales2<NB>(sc + C::kScales + j * 8 * C::kSRow, vsc[j]);
-#pragma unroll
-      for (int t = 0; t < NB; ++t) vm = max_abs2(vm, vsc[j][t]);
-    }
-    vm &= 0x7fff7fffu;
-    int ve = (int)(max(vm & 0xffffu, vm >> 16) >> 10);
-    if (__any_sync(0xffffffffu, above || ve > lim)) {  // (rare after the first tiles)
-#pragma unroll
-      for (int of = 1; of < 32; of <<= 1) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, of));
-      float r = 1.f;
-      if (ve > lim) {  // 2^fe for |scale| < 2^(field - 14)
-        r = lim < 0 ? 0.f : __int_as_float((127 + max(lim, 1) - max(ve, 1)) << 23);
-        lim = ve;
-      }
-      const float fe = (float)(kFe0 + 14 - max(lim, 1));
-#pragma unroll
-      for (int u = 0; u < NH; ++u) {
-        float x = mx[u];
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = fmaxf(m[u], x * fac[u]);
-        const float cr = m[u] == -INFINITY ? 0.f : exp2f(m[u] - mn) * r;
-        m[u] = mn;
-        mf[u] = mn - fe;
-        top[u] = (mn + kSlack4) / fac[u];
-        l2[u] = mul2(l2[u], pack2(cr, cr));
-        const float c0 = __shfl_sync(0xffffffffu, cr, 8 * cq), c1 = __shfl_sync(0xffffffffu, cr, 8 * cq + 4);
-#pragma unroll
-        for (int t = 0; t < 2 * NB; ++t) {
-          o[u][t][0] *= c0;
-          o[u][t][1] *= c1;
-          o[u][t][2] *= c0;
-          o[u][t][3] *= c1;
-        }
-      }
-    }
-
-    // ---- 2^fe P, then O += (2^fe P * scale) . V per block ----
-#pragma unroll
-    for (int h = 0; h < NT / 2; ++h) {  // 16 tokens
-      if (h * 16 >= nr) break;
-      uint64_t p2[NH][2];
-#pragma unroll
-      for (int u = 0; u < NH; ++u)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          p2[u][j] = pack2(ex2(fmaf(s[u][2 * h + j][0], fac[u], -mf[u])),
-                           ex2(fmaf(s[u][2 * h + j][1], fac[u], -mf[u])));
-          l2[u] = add2(l2[u], p2[u][j]);
+          uint32_t* f = a[j / 2] + j % 2;
+          f[0] = nib8<false>(w, k1024);
+          f[2] = nib8<false>(w8, k1024);
+          f[4] = nib8<true>(w, k1024);
+          f[6] = nib8<true>(w8, k1024);
         }
 #pragma unroll
-      for (int bp = 0; bp < NB / 2; ++bp) {
-        uint32_t vw[4];
-        ldsm4t(st + v_off[bp] + h * 16 * C::kRow, vw);
+        for (int u = 0; u < NH; ++u) {
+          uint4 q0, q1;
+          if constexpr (kPack) {
+            const uint2* f = reinterpret_cast<const uint2*>(qf) + 2 * bb * 32 + lane;
+            const uint2 x0 = f[0], x1 = f[32];
+            q0 = make_uint4(x0.x, x0.y, 0u, 0u);
+            q1 = make_uint4(x1.x, x1.y, 0u, 0u);
+          } else {
+            const uint4* f = qf + (u * KS + 2 * bb) * 32 + lane;
+            q0 = f[0];
+            q1 = f[32];
+          }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int bb = 2 * bp + x;
-          const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1], w0s = w0 >> 8, w1s = w1 >> 8;
-          const uint32_t l0 = nib8<false>(w0, k1024), l1 = nib8<false>(w0s, k1024), l2w = nib8<false>(w1, k1024), l3 = nib8<false>(w1s, k1024);
-          const uint32_t u0 = nib8<true>(w0, k1024), u1 = nib8<true>(w0s, k1024), u2 = nib8<true>(w1, k1024), u3 = nib8<true>(w1s, k1024);
+          for (int h = 0; h < NT / 2; ++h) {
+            float acc[4];
+            mma4z(acc, a[h][0], a[h][1], a[h][2], a[h][3], q0.x, q0.y);
+            if constexpr (!kPack) mma4(acc, a[h][0], a[h][1], a[h][2], a[h][3], q0.z, q0.w);
+            mma4(acc, a[h][4], a[h][5], a[h][6], a[h][7], q1.x, q1.y);
+            if constexpr (!kPack) mma4(acc, a[h][4], a[h][5], a[h][6], a[h][7], q1.z, q1.w);
 #pragma unroll
-          for (int u = 0; u < NH; ++u) {
-            uint32_t ph[2], pl[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint64_t pd = mul2(p2[u][j], scale_pair<NB>(vsc[2 * h + j], bb));
-              float a, d;
-              unpack2(pd, a, d);
-              ph[j] = f2h(a, d);
-              const float2 hf = h2f(ph[j]);
-              unpack2(fma2(pack2(hf.x, hf.y), hi_off2, pd), a, d);
-              pl[j] = f2h(a, d);
+            for (int y = 0; y < 2; ++y) {
+              const float d = half_of(ksc[2 * h + y][bb / 2], bb & 1);
+              float* r = s[u][2 * h + y];
+              r[0] = bb ? fmaf(d, acc[2 * y], r[0]) : d * acc[2 * y];
+              r[1] = bb ? fmaf(d, acc[2 * y + 1], r[1]) : d * acc[2 * y + 1];
             }
-            if constexpr (!kPack) {
-              mma4(o[u][2 * bb], l0, l1, l2w, l3, ph[0], ph[1]);
-              mma4(o[u][2 * bb + 1], u0, u1, u2, u3, ph[0], ph[1]);
-            }
-            mma4(o[u][2 * bb], l0, l1, l2w, l3, pl[0], pl[1]);
-            mma4(o[u][2 * bb + 1], u0, u1, u2, u3, pl[0], pl[1]);
           }
         }
       }
-    }
-    __syncwarp();  // the stage is rewritten next
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-  // ---- merge the warps' {m, l, O}; write the chunk's partial ----
-  __syncthreads();
-  float* mm = reinterpret_cast<float*>(smem);
-  float* ll = mm + kWarps4 * 8 * NH;
-  float* oo = ll + kWarps4 * 8 * NH;
-  const float inv_f = lim < 0 ? 0.f : __int_as_float((127 - kFe0 - 14 + max(lim, 1)) << 23);  // 2^-fe
+      // ---- the running maximum ----
+      float mx[NH][HC];
+      bool above = false;
 #pragma unroll
-  for (int u = 0; u < NH; ++u) {
-    float sum, odd;
-    unpack2(l2[u], sum, odd);
-    sum = (sum + odd) * inv_f;
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (cq == 0) {
-      mm[warp * 8 * NH + 8 * u + gq] = m[u];
-      ll[warp * 8 * NH + 8 * u + gq] = sum;
+      for (int u = 0; u < NH; ++u) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (kPack) s[u][j][0] += s[u][j][1];
+          if (nr < kTile4 && 8 * j + gq >= nr) s[u][j][0] = s[u][j][1] = -INFINITY;
+        }
+#pragma unroll
+        for (int x = 0; x < HC; ++x) {
+          mx[u][x] = fmaxf(fmaxf(s[u][0][x], s[u][1][x]), fmaxf(s[u][2][x], s[u][3][x]));
+          above = above || mx[u][x] > top[u][x];
+        }
+      }
+      // the V scales of this lane's tokens and their largest exponent
+      uint32_t vsc[NT][NB / 2];
+      uint32_t vm = 0u;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        scales4<NB>(sc + C::kScales + j * 8 * C::kSRow, vsc[j]);
+#pragma unroll
+        for (int t = 0; t < NB / 2; ++t) vm = max_abs2(vm, vsc[j][t]);
+      }
+      vm &= 0x7fff7fffu;
+      int ve = (int)(max(vm & 0xffffu, vm >> 16) >> 10);
+      if (__any_sync(0xffffffffu, above || ve > lim)) {  // (rare after the first tiles)
+#pragma unroll
+        for (int of = 1; of < 32; of <<= 1) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, of));
+        float r = 1.f;
+        if (ve > lim) {  // 2^fe for |scale| < 2^(field - 14)
+          r = lim < 0 ? 0.f : __int_as_float((127 + max(lim, 1) - max(ve, 1)) << 23);
+          lim = ve;
+        }
+        const float fe = (float)(kFe0 + 14 - max(lim, 1));
+#pragma unroll
+        for (int u = 0; u < NH; ++u) {
+          float cr[HC];
+#pragma unroll
+          for (int x = 0; x < HC; ++x) {
+            float z = mx[u][x];
+#pragma unroll
+            for (int of = 4; of < 32; of <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, of));
+            const float mn = fmaxf(m[u][x], z * fac[u][x]);
+            cr[x] = m[u][x] == -INFINITY ? 0.f : ex2(m[u][x] - mn) * r;
+            m[u][x] = mn;
+            mf[u][x] = mn - fe;
+            // (fac is a power of two: its inverse, exactly)
+            top[u][x] = (mn + kSlack4) * __uint_as_float(0x7f000000u - __float_as_uint(fac[u][x]));
+            l[u][x] *= cr[x];
+          }
+#pragma unroll
+          for (int t = 0; t < 2 * NB; ++t) {
+            o[u][t][0] *= cr[0];
+            o[u][t][1] *= cr[HC - 1];
+            o[u][t][2] *= cr[0];
+            o[u][t][3] *= cr[HC - 1];
+          }
+        }
+      }
+
+      // ---- 2^fe P, then O += (2^fe P * scale) . V per block ----
+#pragma unroll
+      for (int h = 0; h < NT / 2; ++h) {  // 16 tokens
+        if (h * 16 >= nr) break;
+        float p[NH][2][HC];
+#pragma unroll
+        for (int u = 0; u < NH; ++u)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < HC; ++x) {
+              p[u][y][x] = ex2(fmaf(s[u][2 * h + y][x], fac[u][x], -mf[u][x]));
+              l[u][x] += p[u][y][x];
+            }
+#pragma unroll
+        for (int bp = 0; bp < NB / 2; ++bp) {
+          uint32_t vw[4];
+          ldsm4t(st + v_off[bp] + h * 16 * C::kRow, vw);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int bb = 2 * bp + x;
+            const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1], w0s = w0 >> 8, w1s = w1 >> 8;
+            const uint32_t l0 = nib8<false>(w0, k1024), l1 = nib8<false>(w0s, k1024), l2 = nib8<false>(w1, k1024),
+                           l3 = nib8<false>(w1s, k1024);
+            const uint32_t u0 = nib8<true>(w0, k1024), u1 = nib8<true>(w0s, k1024), u2 = nib8<true>(w1, k1024),
+                           u3 = nib8<true>(w1s, k1024);
+            const float d0 = half_of(vsc[2 * h][bp], x), d1 = half_of(vsc[2 * h + 1][bp], x);
+#pragma unroll
+            for (int u = 0; u < NH; ++u) {
+              // tokens gq and gq + 8 of the columns 2cq, 2cq+1, transposed into
+              // B fragments
+              if constexpr (kPack) {
+                const float a0 = p[u][0][0] * d0, a1 = p[u][1][0] * d1;
+                const float2 hi = h2f(f2h(a0, a1));
+                const uint32_t b0 = transpose8(f2h(a0, a0 - hi.x)), b1 = transpose8(f2h(a1, a1 - hi.y));
+                mma4(o[u][2 * bb], l0, l1, l2, l3, b0, b1);
+                mma4(o[u][2 * bb + 1], u0, u1, u2, u3, b0, b1);
+              } else {
+                uint32_t ph[2], pl[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const float d = y ? d1 : d0, a0 = p[u][y][0] * d, a1 = p[u][y][HC - 1] * d;
+                  ph[y] = f2h(a0, a1);
+                  const float2 hi = h2f(ph[y]);
+                  pl[y] = transpose8(f2h(a0 - hi.x, a1 - hi.y));
+                  ph[y] = transpose8(ph[y]);
+                }
+                mma4(o[u][2 * bb], l0, l1, l2, l3, ph[0], ph[1]);
+                mma4(o[u][2 * bb + 1], u0, u1, u2, u3, ph[0], ph[1]);
+                mma4(o[u][2 * bb], l0, l1, l2, l3, pl[0], pl[1]);
+                mma4(o[u][2 * bb + 1], u0, u1, u2, u3, pl[0], pl[1]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();  // the stage is rewritten next
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // ---- merge the warps' {m, l, O}; write the chunk's partial ----
+    __syncthreads();
+    float* mm = reinterpret_cast<float*>(smem);
+    float* ll = mm + kWarps4 * kHeads;
+    float* oo = ll + kWarps4 * kHeads;
+    const float inv_f = lim < 0 ? 0.f : __int_as_float((127 - kFe0 - 14 + max(lim, 1)) << 23);  // 2^-fe
 #pragma unroll
-    for (int t = 0; t < NB; ++t) {
+    for (int u = 0; u < NH; ++u) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float sc = (h ? 0.0625f : 1.f) * inv_f;  // (upper half-bytes count 16-fold)
-        const int d0 = 32 * t + 16 * h + 2 * gq;
-        float* r0 = oo + (warp * 8 * NH + 8 * u + 2 * cq) * C::kOStride + d0;
-        *reinterpret_cast<float2*>(r0) = make_float2(o[u][2 * t + h][0] * sc, o[u][2 * t + h][2] * sc);
-        *reinterpret_cast<float2*>(r0 + C::kOStride) = make_float2(o[u][2 * t + h][1] * sc, o[u][2 * t + h][3] * sc);
+      for (int x = 0; x < HC; ++x) {
+        const int row = warp * kHeads + 8 * u + HC * cq + x;
+        float sum = l[u][x] * inv_f;
+#pragma unroll
+        for (int of = 4; of < 32; of <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, of);
+        if (gq == 0) {
+          mm[row] = m[u][x];
+          ll[row] = sum;
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t) {
+          const float f = (t & 1 ? 0.0625f : 1.f) * inv_f;  // (upper half-bytes count 16-fold)
+          const float* v = o[u][t];
+          *reinterpret_cast<float2*>(oo + row * C::kOStride + 16 * t + 2 * gq) =
+              kPack ? make_float2((v[0] + v[1]) * f, (v[2] + v[3]) * f) : make_float2(v[x] * f, v[2 + x] * f);
+        }
       }
     }
-  }
-  __syncthreads();
-  // head h's weights of the warps (each replaces its maximum), its sum
-  if (tid < G) {
-    const int h = tid;
-    float M = -INFINITY, lsum = 0.f;
+    __syncthreads();
+    // head h's weights of the warps (each replaces its maximum), its sum
+    if (tid < G) {
+      const int h = tid;
+      float M = -INFINITY, lsum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps4; ++w) M = fmaxf(M, mm[w * 8 * NH + h]);
+      for (int w = 0; w < kWarps4; ++w) M = fmaxf(M, mm[w * kHeads + h]);
 #pragma unroll
-    for (int w = 0; w < kWarps4; ++w) {
-      const float mw = mm[w * 8 * NH + h];
-      const float wgt = mw == -INFINITY ? 0.f : ex2(mw - M);  // (a warp without a tile)
-      mm[w * 8 * NH + h] = wgt;
-      lsum = fmaf(ll[w * 8 * NH + h], wgt, lsum);
-    }
-    const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
-    P.ws_m[hq * P.nc + c] = M;
-    P.ws_l[hq * P.nc + c] = lsum;
-  }
-  __syncthreads();
-  for (int e = tid; e < G * (D / 4); e += kThreads4) {
-    const int h = e / (D / 4), j = e % (D / 4) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps4; ++w) {
-      const float wgt = mm[w * 8 * NH + h];
-      const float* r = oo + (w * 8 * NH + h) * C::kOStride + j;
-      float4 x = *reinterpret_cast<const float4*>(r);
-      if constexpr (kPack) {
-        const float4 lo = *reinterpret_cast<const float4*>(r + 4 * C::kOStride);
-        x.x += lo.x, x.y += lo.y, x.z += lo.z, x.w += lo.w;
+      for (int w = 0; w < kWarps4; ++w) {
+        const float mw = mm[w * kHeads + h];
+        const float wgt = mw == -INFINITY ? 0.f : ex2(mw - M);  // (a warp without a tile)
+        mm[w * kHeads + h] = wgt;
+        lsum = fmaf(ll[w * kHeads + h], wgt, lsum);
       }
-      acc.x = fmaf(x.x, wgt, acc.x);
-      acc.y = fmaf(x.y, wgt, acc.y);
-      acc.z = fmaf(x.z, wgt, acc.z);
-      acc.w = fmaf(x.w, wgt, acc.w);
+      const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
+      P.ws_m[hq * P.nc + c] = M;
+      P.ws_l[hq * P.nc + c] = lsum;
     }
-    const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
-    *reinterpret_cast<float4*>(P.ws_o + (hq * P.nc + c) * D + j) = acc;
+    __syncthreads();
+    for (int e = tid; e < G * (D / 4); e += kThreads4) {
+      const int h = e / (D / 4), j = e % (D / 4) * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps4; ++w) {
+        const float wgt = mm[w * kHeads + h];
+        const float4 x = *reinterpret_cast<const float4*>(oo + (w * kHeads + h) * C::kOStride + j);
+        acc.x = fmaf(x.x, wgt, acc.x);
+        acc.y = fmaf(x.y, wgt, acc.y);
+        acc.z = fmaf(x.z, wgt, acc.z);
+        acc.w = fmaf(x.w, wgt, acc.w);
+      }
+      const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
+      *reinterpret_cast<float4*>(P.ws_o + (hq * P.nc + c) * D + j) = acc;
+    }
+    if (!seq_next4(P, sq)) break;
   }
 }
 
@@ -654,11 +756,10 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
   const int j = tid % kLanes, grp = tid / kLanes;
   // the attention grid released this one after its own wait: the lengths are
   // readable
-  const float rate = chunk_rate4(P, lane);
-  const int L = window_len4(P, b);
-  const int n = nchunks4(P, L, rate);
-  const int tpc = L >= 1 ? (L + n - 1) / n : 1;
-  const int nact = L >= 1 ? (L + tpc - 1) / tpc : 0;
+  const Split4 sp = split4(P, lane);
+  int L;
+  const int at = seq_of4(P, sp, b, lane, L);
+  const int nact = sp.whole ? 1 : (at + tiles4(L) - 1) / sp.piece - at / sp.piece + 1;
   griddep_wait();               // the partials are complete and visible
   griddep_launch_dependents();  // (not earlier: the next kernel would take SMs from this one)
   float* o = P.out + (long long)hq * D;
@@ -756,11 +857,7 @@ int launch_q4kv_g(const AttnParams& P, cudaStream_t stream) {
 
 int attn_q4kv_launch(const AttnParams& A, cudaStream_t stream) {
   AttnParams P = A;
-  // About two CTAs an SM in all suit a few sequences; a larger batch gets at
-  // least kSeqCtas4 chunks a sequence on average, so that the longest of a
-  // ragged batch does not set the time (more than one wave of CTAs then).
-  const long long by_len = (long long)P.batch * ((P.cap + kMinChunk - 1) / kMinChunk);
-  if (P.batch > 1) P.nct = (int)std::min<long long>(by_len, std::max(P.nct, kSeqCtas4 * P.batch));
+  P.nct = std::min(P.nct, std::max(1, 2 * sm_count() / P.n_kv_heads));  // one wave
   return P.head_dim == 128 ? launch_q4kv_g<128>(P, stream) : launch_q4kv_g<64>(P, stream);
 }
 
