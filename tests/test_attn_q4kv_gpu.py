@@ -288,3 +288,37 @@ def test_cache_past_2_to_the_32_bytes(q8d, orc):
     ref, ab = oracle_attn(orc, q[-1], small[0], small[1], H, Hk, D, 300, 300, 0.09)
     close(got[-1], ref, ab)
     assert np.all(got[0] == 0)
+
+
+@pytest.mark.parametrize("H,Hk,D,cap,batch,kind", [
+    (4, 2, 64, 6000, 40, "one long"), (3, 1, 128, 3000, 9, "one long"), (2, 2, 64, 128, 130, "short caches"),
+    (96, 96, 64, 300, 7, "more heads than CTAs"), (16, 1, 64, 500, 35, "even"), (4, 4, 128, 130, 90, "two slots"),
+    (8, 8, 64, 90, 2, "short caches"),
+])
+def test_batches_cut_into_pieces(q8d, orc, H, Hk, D, cap, batch, kind):
+    """Pieces that hold many short sequences, sequences of many pieces among
+    one-row ones, caches with a single workspace slot; nothing is written
+    behind the workspace."""
+    width = Hk * D
+    stride = -(-cap * width // 256) * 256
+    lens = [1 + (i * 613) % cap for i in range(batch)]
+    if kind == "one long":
+        lens = [1 + i % 3 for i in range(batch)]
+        lens[batch // 3] = cap
+    kc, vc = (np.zeros((batch, kp.cache_bytes(Q4, stride)), np.uint8) for _ in range(2))
+    for s in range(batch):
+        for c, x in ((kc, "k"), (vc, "v")):
+            one = q4_cache(s, f"cut.{x}", cap, width, lens[s], noise=True)
+            c[s, :one.size] = one
+    q = synth.normal_f32(0, "cut.q", (batch, H * D))
+    n = q8d.q8d_gqa_workspace_bytes(batch, H, Hk, D, cap)
+    ws = torch.full((n // 4 + 1024,), 7.0, device="cuda")
+    out, err = torch.full((batch, H * D), -7.0, device="cuda"), ints([0])
+    q8d.q8d_gqa_decode_attn(dev(q), None, None, dev(kc), dev(vc), Q4, out, batch, H, Hk, D, cap, stride, ints(lens),
+                            0.11, ws, n, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    assert torch.all(ws[(n + 3) // 4:] == 7.0)
+    for s in range(batch):
+        ref, ab = oracle_attn(orc, q[s], kc[s], vc[s], H, Hk, D, cap, lens[s], 0.11)
+        close(out[s].cpu().numpy(), ref, ab)
