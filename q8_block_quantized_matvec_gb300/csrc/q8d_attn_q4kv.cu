@@ -831,18 +831,89 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
   }
 }
 
+// The same by a warp a (sequence, query head), lanes holding D/32 dims: for
+// many heads, which as blocks of their own would take several waves, and for
+// few chunks.  The whole call, blocks / warps: 42 sequences of 96 heads, 179
+// rows, 57 / 16.8 us; 32 ragged sequences of 16 heads up to 8192 rows, 44.5 /
+// 41.5; 9 of 28 heads, 274 rows, 9.5 / 7.9.  With many chunks and few heads
+// its loads are too few at a time: 8 ragged of 28 heads up to 32768 rows, 29.4
+// / 34.6; 6 of 24 heads, 2000 rows, 9.0 / 12.7.
+constexpr int kFewThreads4 = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads4) gqa_q4kv_combine_few_kernel(const AttnParams P) {
+  constexpr int kV = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int hq = blockIdx.x * (kFewThreads4 / 32) + (threadIdx.x >> 5);
+  const Split4 sp = split4(P, lane);  // (readable, as above)
+  const bool live = hq < P.batch * P.n_heads;
+  int L;
+  const int b = live ? hq / P.n_heads : 0, at = seq_of4(P, sp, b, lane, L);
+  const int nact = sp.whole ? 1 : (at + tiles4(L) - 1) / sp.piece - at / sp.piece + 1;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!live) return;
+  float* o = P.out + (long long)hq * D + kV * lane;
+  const float* O = P.ws_o + (long long)hq * P.nc * D + kV * lane;
+  const float *wm = P.ws_m + (long long)hq * P.nc, *wl = P.ws_l + (long long)hq * P.nc;
+  float acc[kV], M = -INFINITY, lsum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  if (L < 1) lsum = __int_as_float(0x7fc00000);
+  for (int c0 = 0; L >= 1 && c0 < nact; c0 += 32) {
+    const int nc = min(32, nact - c0);
+    const float mc = lane < nc ? __ldcg(wm + c0 + lane) : -INFINITY;
+    const float lc = lane < nc ? __ldcg(wl + c0 + lane) : 0.f;
+    float mx = mc;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    mx = fmaxf(M, mx);
+    const float old = M == -INFINITY ? 0.f : ex2(M - mx);
+    M = mx;
+    const float w = mc == -INFINITY ? 0.f : ex2(mc - M);
+    float ls = lc * w;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+    lsum = fmaf(lsum, old, ls);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] *= old;
+#pragma unroll 4
+    for (int c = 0; c < nc; ++c) {
+      const float g = __shfl_sync(0xffffffffu, w, c);
+      const float* r = O + (long long)(c0 + c) * D;
+      if constexpr (kV == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(r));
+        acc[0] = fmaf(v.x, g, acc[0]), acc[1] = fmaf(v.y, g, acc[1]);
+        acc[2] = fmaf(v.z, g, acc[2]), acc[3] = fmaf(v.w, g, acc[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(r));
+        acc[0] = fmaf(v.x, g, acc[0]), acc[1] = fmaf(v.y, g, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kV; ++i) o[i] = acc[i] / lsum;
+}
+
 template <int D, int NH, bool kPack>
-int launch_q4kv(const AttnParams& P, cudaStream_t stream) {
+int launch_q4kv(AttnParams P, cudaStream_t stream) {
   using C = Cfg4<D, NH>;
   const auto fn = gqa_q4kv_kernel<D, NH, kPack>;
   // (no carveout preference: a change of carveout between this kernel and
   // the next drains the SMs, 2 us a call)
   int rc = configure_kernel(reinterpret_cast<const void*>(fn), C::kSmem, false);
   if (rc) return rc;
+  // one wave (two column tiles: a CTA an SM)
+  P.nct = std::min(P.nct, std::max(1, (NH == 1 ? 2 : 1) * sm_count() / P.n_kv_heads));
   rc = launch_ex(fn, dim3(P.nct, P.n_kv_heads), dim3(kThreads4), (size_t)C::kSmem, stream, true, P);
   if (rc) return rc;
-  return launch_ex(gqa_q4kv_combine_kernel<D>, dim3((unsigned)(P.batch * P.n_heads)),
-                   dim3(kCombThreads4), 0, stream, true, P);
+  const long long heads = (long long)P.batch * P.n_heads;
+  if (heads > 2LL * sm_count() || P.nc <= 4) {
+    constexpr int kPer = kFewThreads4 / 32;
+    return launch_ex(gqa_q4kv_combine_few_kernel<D>, dim3((unsigned)((heads + kPer - 1) / kPer)),
+                     dim3(kFewThreads4), 0, stream, true, P);
+  }
+  return launch_ex(gqa_q4kv_combine_kernel<D>, dim3((unsigned)heads), dim3(kCombThreads4), 0, stream, true, P);
 }
 
 template <int D>
@@ -855,9 +926,7 @@ int launch_q4kv_g(const AttnParams& P, cudaStream_t stream) {
 
 }  // namespace
 
-int attn_q4kv_launch(const AttnParams& A, cudaStream_t stream) {
-  AttnParams P = A;
-  P.nct = std::min(P.nct, std::max(1, 2 * sm_count() / P.n_kv_heads));  // one wave
+int attn_q4kv_launch(const AttnParams& P, cudaStream_t stream) {
   return P.head_dim == 128 ? launch_q4kv_g<128>(P, stream) : launch_q4kv_g<64>(P, stream);
 }
 
