@@ -300,18 +300,26 @@ constexpr int kTiles = 4;    // A tiles of a unit: a warp multiplies all four wi
 constexpr int kGuRows = 32;  // h rows of a gate / up unit: one block of the down products' rows
 constexpr int kSubBytes = kSlots * 8 * kQBlockBytes;  // 64 row slots of 8 blocks
 
+// How a matrix's rows come.
+constexpr int kRowCopies = 0;   // a bulk copy a row and slice, into padded slots
+constexpr int kTensor = 1;      // tensor copies of 8 blocks by 32 or 64 rows
+constexpr int kContiguous = 2;  // whole rows, one bulk copy a matrix and stage
+
 // How a product kernel lays out its shared memory (host plan).
 struct MoePlan {
+  int mode;         // kRowCopies ..
   int bpr;          // blocks a row
   int S, nsl;       // blocks a slice, slices a row
-  int stages;       // of a unit: a slice each (tensor copies), or a tile and slice each
+  int stages;       // of a unit: a slice each (tensor copies), a tile and slice each (rows), or `tr` tiles each
+  int tr, lq;       // tiles a stage; log2 of the rows between a tile's rows g and g + 1
   int SR;           // slot bytes (tensor copies: of 8 blocks)
   int x_off;        // the images' offset in a stage
   int tg;           // tokens a group (1, 2, 4 or 8)
-  int XR;           // image bytes a token of a stage
+  int XR;           // image bytes a token of a stage, or of a resident buffer
+  int img_bytes;    // a resident buffer
   int stage_bytes, nst;
   int items;        // (expert, token group) pairs at most
-  int o_part, o_hq, o_mask, o_ebase, o_item, o_tok, o_bar;  // offsets
+  int o_img, o_part, o_hq, o_mask, o_ebase, o_item, o_tok, o_bar;  // offsets
   int smem;
 };
 
@@ -324,7 +332,8 @@ struct MoeShared {
   float* pw;                 // [pairs] weight of a row
   unsigned short* ppair;     // [pairs] pair (token * top_k + slot) of a row
   unsigned short* ptok;      // [pairs] its token
-  uint64_t *full, *empty;
+  uint64_t *full, *empty;    // [nst]
+  uint64_t *ifull, *iempty;  // [2] resident images
   int n_items;
 };
 
@@ -340,6 +349,8 @@ __device__ __forceinline__ MoeShared carve(const MoePlan& L, uint8_t* smem, int 
   S.ptok = S.ppair + pairs;
   S.full = reinterpret_cast<uint64_t*>(smem + L.o_bar);
   S.empty = S.full + L.nst;
+  S.ifull = S.empty + L.nst;
+  S.iempty = S.ifull + 2;
   S.n_items = 0;
   return S;
 }
@@ -372,8 +383,12 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
   for (int e = threadIdx.x; e < E; e += kThreads) S.mask[e] = 0ull;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L.nst; ++i) {
-      mbar_init(&S.full[i], kProducers);
+      mbar_init(&S.full[i], L.mode == kContiguous ? 1 : kProducers);
       mbar_init(&S.empty[i], kGroupWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.ifull[i], 1);
+      mbar_init(&S.iempty[i], kConsumers);
     }
     fence_barrier_init();
   }
@@ -469,9 +484,30 @@ __device__ __forceinline__ void row_tail(uint8_t* slot, const uint8_t* base, con
     *reinterpret_cast<unsigned short*>(slot + (x - R.lo)) = *reinterpret_cast<const unsigned short*>(base + x);
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
+// Shared loads at an immediate offset: the blocks' words lie at constant
+// distances, and an address register each would cost an addition a load.
+template <int OFF>
+__device__ __forceinline__ uint4 lds128i(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4+%5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint2 lds64i(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(v.x), "=r"(v.y) : "r"(a), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds32i(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds16i(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.shared.b16 %0, [%1+%2];" : "=h"(v) : "r"(a), "n"(OFF));
   return v;
 }
 
@@ -489,35 +525,17 @@ struct BlockIn {
 
 template <bool kPack, int kN>
 __device__ __forceinline__ void load_x(uint32_t xa, uint32_t x0, uint32_t x1, BlockIn<kPack, kN>& B) {
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if constexpr (kPack) {
-      const uint2 v = tc::lds64a(xa + 64u * s);
-      B.b[s][0] = v.x;
-      B.b[s][1] = v.y;
-    } else {
-      const uint4 v = lds128(xa + 64u * s);
-      B.b[s][0] = v.x;
-      B.b[s][1] = v.y;
-      B.b[s][2] = v.z;
-      B.b[s][3] = v.w;
-    }
+  if constexpr (kPack) {
+    const uint2 u = lds64i<0>(xa), v = lds64i<64>(xa);
+    B.b[0][0] = u.x, B.b[0][1] = u.y;
+    B.b[1][0] = v.x, B.b[1][1] = v.y;
+  } else {
+    const uint4 u = lds128i<0>(xa), v = lds128i<64>(xa);
+    B.b[0][0] = u.x, B.b[0][1] = u.y, B.b[0][2] = u.z, B.b[0][3] = u.w;
+    B.b[1][0] = v.x, B.b[1][1] = v.y, B.b[1][2] = v.z, B.b[1][3] = v.w;
   }
-  B.xi0 = tc::lds32f(x0 + 128u);
-  B.xi1 = tc::lds32f(x1 + 128u);
-}
-
-template <int OFF>
-__device__ __forceinline__ uint32_t lds32i(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
-  return v;
-}
-template <int OFF>
-__device__ __forceinline__ uint32_t lds16i(uint32_t a) {
-  unsigned short v;
-  asm volatile("ld.shared.b16 %0, [%1+%2];" : "=h"(v) : "r"(a), "n"(OFF));
-  return v;
+  B.xi0 = __uint_as_float(lds32i<128>(x0));
+  B.xi1 = __uint_as_float(lds32i<128>(x1));
 }
 
 // Slot of row g + 8 h of tile t, less g.
@@ -549,9 +567,20 @@ __device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, Bloc
 template <bool kPack>
 __device__ __forceinline__ void load_unaligned(uint32_t ba, int h, int c, BlockIn<kPack, 1>& B) {
   const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
-  B.w[0][h][0] = __byte_perm(tc::lds32a(a), tc::lds32a(a + 4u), sel);
-  B.w[0][h][1] = __byte_perm(tc::lds32a(a + 16u), tc::lds32a(a + 20u), sel);
-  B.w[0][h][2] = tc::lds16a(ba);
+  const uint32_t w0 = lds32i<0>(a), w1 = lds32i<4>(a), w4 = lds32i<16>(a), w5 = lds32i<20>(a);
+  B.w[0][h][2] = lds16i<0>(ba);
+  B.w[0][h][0] = __byte_perm(w0, w1, sel);
+  B.w[0][h][1] = __byte_perm(w4, w5, sel);
+}
+
+// The unit's row that slot (tile t, half h, row g) holds.  Tensor and row
+// copies: in order (gate: h is the matrix).  Whole rows lie bpr * 34 bytes
+// apart, which puts eight rows' words into few banks for many widths, so
+// there a tile takes every 2^lq-th row of the stage.
+template <bool kGate>
+__device__ __forceinline__ int slot_row(const MoePlan& L, int t, int h, int g) {
+  const int tt = t & (L.tr - 1), s = kGate ? tt : 2 * tt + h;
+  return (t - tt) * (kGate ? 8 : 16) + ((s >> L.lq) << (3 + L.lq)) + (g << L.lq) + (s & ((1 << L.lq) - 1));
 }
 
 __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -656,11 +685,13 @@ __device__ __forceinline__ void finish(const MoeParams& P, volatile int* abort) 
 
 // Launches 2 (kGate) and 3.  P.ypart row p = token * top_k + slot receives
 // that pair's weighted down product.
-template <bool kAl, bool kGate, bool kPack>
+template <int kMode, bool kGate, bool kPack>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_product_kernel(const MoeParams P, const MoePlan L, bool hperm,
                                                                   const __grid_constant__ CUtensorMap map0,
                                                                   const __grid_constant__ CUtensorMap map1) {
+  constexpr bool kAl = kMode == kTensor;
+  constexpr bool kResident = kMode == kContiguous;  // images stay for an item, in two buffers
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_abort;
   MoeShared S = carve(L, smem, P.m * P.top_k);
@@ -677,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nq = (rows + kRows - 1) / kRows;       // units an item
   const long long units = (long long)S.n_items * nq;
   const int q0 = (int)(units * blockIdx.x / gridDim.x), q1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  const int it0 = kResident ? q0 / nq : 0, n_it = kResident && q1 > q0 ? (q1 - 1) / nq - it0 + 1 : 0;  // the CTA's items
   if (warp >= kConsumers) {
     const int rb = L.bpr * kQBlockBytes;
     const long long mat = (long long)P.n_experts * rows * rb;
@@ -687,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pw = warp - kConsumers;
     const uint64_t pol = policy_evict_first(), keep = policy_evict_last();
     uint32_t filled = 0, parity = 0;
+    int images = 0;  // resident buffers filled by this warp
     Place w;
     w.q = q0;
     const auto ready = [&]() {  // the stage may be filled
@@ -715,6 +748,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+      }
+    } else if (kMode == kContiguous && pw == 0) {
+      constexpr int kTileRows = kGate ? 8 : 16;
+      for (; w.q < q1; w.next(L, q1)) {
+        if (!ready()) break;
+        if (lane == 0) {
+          const int it = w.unit() / nq, r0 = (w.unit() - it * nq) * kRows + w.sl * L.tr * kTileRows;
+          // (rows are a multiple of 32: every piece starts and ends on 16 bytes)
+          const uint32_t bytes = (uint32_t)max(0, min(L.tr * kTileRows, rows - r0)) * (uint32_t)rb;
+          const long long off = ((long long)(S.item[it].x & 0xffff) * rows + r0) * rb;
+          uint8_t* st = smem + (size_t)w.s * L.stage_bytes;
+          uint64_t* full = &S.full[w.s];
+          mbar_arrive_expect_tx(full, (kGate ? 2u : 1u) * bytes);
+          if (bytes) {
+            bulk_g2s(st, (kGate ? P.wg : P.wd) + off, bytes, full, pol);
+            if (kGate) bulk_g2s(st + L.tr * kTileRows * L.SR, P.wu + off, bytes, full, pol);
+          }
+        }
+        __syncwarp();
+      }
+    } else if (kResident) {
+      if (pw == 1) {
+        if (!kGate) griddep_wait();  // (h)
+        fence_proxy_async_global();  // (the images were written by ordinary stores)
+        for (; images < n_it; ++images) {
+          uint64_t* full = &S.ifull[images & 1];
+          const bool ok = images < 2 || ring_wait(&S.iempty[images & 1], (uint32_t)(images / 2 - 1) & 1u, &s_abort);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const int2 I = S.item[it0 + images];
+          const int n = I.x >> 16;
+          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(n * L.bpr * kImgBlock));
+          __syncwarp();
+          bulk_images(L, smem + L.o_img + (size_t)(images & 1) * L.img_bytes, full, 0, 1, n, 0, L.bpr,
+                      [&](int k) { return img(I.y + k); }, keep, lane);
+        }
       }
     } else if (kAl) {
       if (!kGate) griddep_wait();  // (h)
@@ -762,11 +830,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     drain(L, S, filled, parity, &s_abort);
+    if (kResident && *(volatile int*)&s_abort)
+      for (int i = max(0, images - 2); i < images; ++i) mbar_wait(&S.ifull[i & 1], (uint32_t)(i / 2) & 1u);
   } else {
     if (!kGate) griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
     const uint32_t smem32 = smem_u32(smem);
-    const uint32_t xoff = (uint32_t)L.x_off;
+    const uint32_t xoff = kResident ? 0u : (uint32_t)L.x_off;
     // column g is token g (packed: token g % 4, hi or lo)
     const auto col = [&](int n) { return xoff + token_off(L.XR, min(kPack ? n & 3 : n, L.tg - 1)); };
     const uint32_t xl = col(gq) + (uint32_t)(cq * 16 + (kPack ? 8 * (gq >> 2) : 0));
@@ -776,10 +846,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* hq = reinterpret_cast<float*>(smem + L.o_hq) + group * kGuRows * 9;  // gate: [32 rows][8 tokens + 1]
     int s = group;
     uint32_t ph = 0;
+    int held = -1;  // resident images: the item whose buffer this group holds
+    const auto next_images = [&]() {  // every item in turn, also those without a unit of this group
+      if (held >= 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.iempty[held & 1]);
+      }
+      ++held;
+      ring_wait(&S.ifull[held & 1], (uint32_t)(held >> 1) & 1u, &s_abort);
+    };
     for (int q = q0 + group; q < q1; q += kGroups) {
       const int it = q / nq;
       const int2 I = S.item[it];
       const int ntok = I.x >> 16, u = q - it * nq, r0 = u * kRows;
+      if (kResident)
+        while (held < it - it0) next_images();
+      const uint32_t xres = smem32 + (uint32_t)(L.o_img + (held & 1) * L.img_bytes);
       uint64_t y[kTiles][2];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = pack2(0.f, 0.f);
@@ -810,6 +892,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             block_mma<kAl, kPack>(B, !(j & 1), cq, y);
           }
           release();
+        }
+      } else if (kMode == kContiguous) {
+        const uint32_t base = (uint32_t)((gq << L.lq) * L.SR + member * kQBlockBytes);
+        const auto tile = [&](uint32_t ba, int t, int j, uint32_t xo, BlockIn<kPack, 1>& B, uint64_t (&yy)[2]) {
+          const int s0 = kGate ? t : 2 * t;
+          const uint32_t at = ba + (uint32_t)((((s0 >> L.lq) << (3 + L.lq)) + (s0 & ((1 << L.lq) - 1))) * L.SR);
+          const int s1 = 2 * t + 1;
+          const uint32_t at1 = kGate ? at + (uint32_t)(L.tr * 8 * L.SR)
+                                     : ba + (uint32_t)((((s1 >> L.lq) << (3 + L.lq)) + (s1 & ((1 << L.lq) - 1))) * L.SR);
+          load_unaligned<kPack>(at, 0, cq, B);
+          load_unaligned<kPack>(at1, 1, cq, B);
+          uint64_t yt[1][2] = {{yy[0], yy[1]}};
+          block_mma<kAl, kPack>(B, !(j & 1), cq, yt);
+          yy[0] = yt[0][0];
+          yy[1] = yt[0][1];
+        };
+        if (L.tr == kTiles) {
+          const uint32_t st = stage();
+          for (int j = member; j < L.bpr; j += kGroupWarps) {
+            const uint32_t xo = xres + (uint32_t)(j * kImgBlock), ba = st + base + (uint32_t)((j - member) * kQBlockBytes);
+            BlockIn<kPack, 1> B;
+            load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) tile(ba, t, j, xo, B, y[t]);
+          }
+          release();
+        } else {
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            const uint32_t st = stage();
+            for (int j = member; j < L.bpr; j += kGroupWarps) {
+              const uint32_t xo = xres + (uint32_t)(j * kImgBlock);
+              BlockIn<kPack, 1> B;
+              load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
+              tile(st + base + (uint32_t)((j - member) * kQBlockBytes), 0, j, xo, B, y[t]);
+            }
+            release();
+          }
         }
       } else {
 #pragma unroll
@@ -859,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kGate) {
         const int t = tid >> 6, r = (tid >> 3) & 7;
         const float g = total(16 * t + r), v = total(16 * t + r + 8);
-        hq[(t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
+        hq[(kResident ? slot_row<true>(L, t, 0, r) : t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
         group_sync(group);
         if (tid < 64) {  // the unit is block u of its tokens' h: token i, word w
           const int i = tid >> 3, w = tid & 7;
@@ -871,14 +991,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // 64 rows x 8 tokens
-          const int r = (tid >> 3) + 32 * k;
-          const float v = total(r);
+          const int slot = (tid >> 3) + 32 * k, r = kResident ? slot_row<false>(L, slot >> 4, slot >> 3 & 1, slot & 7) : slot;
+          const float v = total(slot);
           if (n < ntok && r0 + r < rows)
             P.ypart[(size_t)S.ppair[I.y + n] * P.hidden + r0 + r] = S.pw[I.y + n] * v;
         }
         group_sync(group);  // (the shares are rewritten next)
       }
     }
+    if (kResident)
+      while (held < n_it - 1) next_images();
   }
   finish(P, &s_abort);
 }
@@ -947,48 +1069,82 @@ int group_tokens(const MoeParams& P) {
   return tg;
 }
 
-// Lays out a product kernel over rows of bpr blocks: slices of 16 or 8 blocks
-// where tensor copies bring the rows, else the longest of up to 64 that leaves
-// two stages a group.
-int plan_product(const MoeParams& P, int bpr, MoePlan* L) {
+// Banks: the most of eight rows' words (rows `step` bytes apart) that one
+// bank holds.
+int bank_rows(int step) {
+  int most = 0;
+  for (int bank = 0; bank < 32; ++bank) {
+    int n = 0;
+    for (int g = 0; g < 8; ++g)
+      for (int c = 0; c < 4; ++c) n += (g * step / 4 + c) % 32 == bank;
+    most = std::max(most, n);
+  }
+  return most;
+}
+
+// Lays out a product kernel over rows of bpr blocks.  Where rows are whole
+// 16-byte lines: tensor copies of slices of 16 or 8 blocks.  Else, up to 64
+// blocks, whole rows, 64 of them a stage while they are short, and the images
+// of two items beside the ring.  Longer rows, or where those leave no four
+// stages: a tile's rows in slices of up to 64 blocks.
+int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
   const bool al = bpr % 8 == 0;
   const int pairs = P.m * P.top_k;
   L->bpr = bpr;
-  for (int tg = group_tokens(P); tg >= 1; tg /= 2)
-    for (int s = al ? 16 : 64; s >= 8; s -= 8) {
-      L->nsl = (bpr + s - 1) / s;
-      L->S = (bpr + L->nsl - 1) / L->nsl;  // (equal slices; whole groups of 8 blocks where rows are aligned)
-      if (al) L->S = (L->S + 7) / 8 * 8;
-      L->stages = al ? L->nsl : kTiles * L->nsl;
-      L->SR = al ? 8 * kQBlockBytes : slot_bytes(L->S);
-      L->x_off = al ? L->S / 8 * kSubBytes : 16 * L->SR;
+  for (int tg = group_tokens(P); tg >= 1; tg /= 2) {
+    L->tg = tg;
+    L->items = std::min(pairs, P.n_experts + pairs / tg);
+    int o = 0;  // behind the ring
+    L->o_part = o;
+    o += kConsumers * kSlots * 8 * 4;
+    L->o_hq = o;
+    o += up16i(kGroups * kGuRows * 9 * 4);
+    L->o_mask = o;
+    o += 8 * P.n_experts;
+    L->o_ebase = o;
+    o = up16i(o + 4 * P.n_experts);
+    L->o_item = o;
+    o = up16i(o + 8 * L->items);
+    L->o_tok = o;
+    o = up16i(o + 8 * pairs);
+    L->o_bar = o;
+    const int behind = o;
+    const auto slices = [&](int mode, int s) {  // of at most s blocks; false if four stages do not fit
+      const bool whole = mode == kContiguous;
+      L->mode = mode;
+      L->nsl = whole ? 1 : (bpr + s - 1) / s;
+      L->S = (bpr + L->nsl - 1) / L->nsl;  // (equal slices; whole groups of 8 blocks for tensor copies)
+      if (mode == kTensor) L->S = (L->S + 7) / 8 * 8;
+      L->tr = mode == kRowCopies || (whole && bpr > 16) ? 1 : kTiles;
+      L->lq = 0;
+      if (whole)
+        for (int lq = 1; 1 << lq <= L->tr * (gate ? 1 : 2); ++lq)
+          if (bank_rows((bpr * kQBlockBytes) << lq) < bank_rows((bpr * kQBlockBytes) << L->lq)) L->lq = lq;
+      L->stages = mode == kTensor ? L->nsl : whole ? kTiles / L->tr : kTiles * L->nsl;
+      L->SR = mode == kTensor ? 8 * kQBlockBytes : whole ? bpr * kQBlockBytes : slot_bytes(L->S);
+      L->x_off = mode == kTensor ? L->S / 8 * kSubBytes : 16 * L->tr * L->SR;
       // token rows half a bank cycle apart: the two tokens of a quarter warp's
       // 16-byte loads lie in distinct banks
       L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
-      L->tg = tg;
-      L->stage_bytes = (L->x_off + tg * L->XR + 64 + 127) / 128 * 128;  // (tensor copies land on 128 bytes)
-      L->items = std::min(pairs, P.n_experts + pairs / tg);
-      int o = 0;  // behind the ring
-      L->o_part = o;
-      o += kConsumers * kSlots * 8 * 4;
-      L->o_hq = o;
-      o += up16i(kGroups * kGuRows * 9 * 4);
-      L->o_mask = o;
-      o += 8 * P.n_experts;
-      L->o_ebase = o;
-      o = up16i(o + 4 * P.n_experts);
-      L->o_item = o;
-      o = up16i(o + 8 * L->items);
-      L->o_tok = o;
-      o = up16i(o + 8 * pairs);
-      L->o_bar = o;
-      L->nst = std::min(12, (kMaxSmem - o) / (L->stage_bytes + 16)) / kGroups * kGroups;
-      if (L->nst < 2 * kGroups) continue;
+      const int images = tg * L->XR + 64;
+      L->img_bytes = whole ? images : 0;
+      // (tensor copies land on 128 bytes; a row's last word is read 4 bytes past)
+      L->stage_bytes = (L->x_off + (whole ? 16 : images) + 127) / 128 * 128;
+      L->o_img = up16i(behind + 32);
+      L->smem = L->o_img + 2 * L->img_bytes;
+      L->nst = std::min(12, (kMaxSmem - L->smem) / (L->stage_bytes + 16)) / kGroups * kGroups;
+      if (L->nst < 2 * kGroups) return false;
       const int ring = L->nst * L->stage_bytes;
-      for (int* f : {&L->o_part, &L->o_hq, &L->o_mask, &L->o_ebase, &L->o_item, &L->o_tok, &L->o_bar}) *f += ring;
-      L->smem = ring + o + 16 * L->nst;
-      return Q8D_OK;
-    }
+      for (int* f : {&L->o_part, &L->o_hq, &L->o_mask, &L->o_ebase, &L->o_item, &L->o_tok, &L->o_bar, &L->o_img})
+        *f += ring;
+      L->o_img += 16 * L->nst;  // (the barriers: 16 bytes a stage and the images' 32)
+      L->smem += ring + 16 * L->nst;
+      return true;
+    };
+    if (!al && bpr <= 64 && slices(kContiguous, bpr)) return Q8D_OK;
+    for (int s = al ? 16 : 64; s >= 8; s -= 8)
+      if (slices(al ? kTensor : kRowCopies, s)) return Q8D_OK;
+  }
   return Q8D_EUNSUPPORTED;
 }
 
@@ -1016,17 +1172,19 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   if (!P.weights) P.weights = reinterpret_cast<float*>(ws);
 
   MoePlan gu{}, dn{};
-  int rc = plan_product(P, bx, &gu);
-  if (!rc) rc = plan_product(P, bh, &dn);
+  int rc = plan_product(P, bx, true, &gu);
+  if (!rc) rc = plan_product(P, bh, false, &dn);
   if (rc) return rc;
   const bool gal = bx % 8 == 0, dal = bh % 8 == 0;
   typedef void (*Product)(MoeParams, MoePlan, bool, CUtensorMap, CUtensorMap);
-  static const Product fns[2][2][2] = {
-      {{moe_product_kernel<false, false, false>, moe_product_kernel<false, false, true>},
-       {moe_product_kernel<false, true, false>, moe_product_kernel<false, true, true>}},
-      {{moe_product_kernel<true, false, false>, moe_product_kernel<true, false, true>},
-       {moe_product_kernel<true, true, false>, moe_product_kernel<true, true, true>}}};
-  const Product gu_fn = fns[gal][1][gu.tg <= 4], dn_fn = fns[dal][0][dn.tg <= 4];
+  static const Product fns[3][2][2] = {
+      {{moe_product_kernel<kRowCopies, false, false>, moe_product_kernel<kRowCopies, false, true>},
+       {moe_product_kernel<kRowCopies, true, false>, moe_product_kernel<kRowCopies, true, true>}},
+      {{moe_product_kernel<kTensor, false, false>, moe_product_kernel<kTensor, false, true>},
+       {moe_product_kernel<kTensor, true, false>, moe_product_kernel<kTensor, true, true>}},
+      {{moe_product_kernel<kContiguous, false, false>, moe_product_kernel<kContiguous, false, true>},
+       {moe_product_kernel<kContiguous, true, false>, moe_product_kernel<kContiguous, true, true>}}};
+  const Product gu_fn = fns[gu.mode][1][gu.tg <= 4], dn_fn = fns[dn.mode][0][dn.tg <= 4];
   CUtensorMap mg{}, mu{}, md{};
   if (gal) {
     rc = weight_map(P.wg, bx, (long long)P.n_experts * P.ffn, kGuRows, &mg);
