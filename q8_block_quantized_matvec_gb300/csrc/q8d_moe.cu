@@ -315,8 +315,8 @@ struct MoePlan {
   int SR;           // slot bytes (tensor copies: of 8 blocks)
   int x_off;        // the images' offset in a stage
   int tg;           // tokens a group (1, 2, 4 or 8)
-  int XR;           // image bytes a token of a stage, or of a resident buffer
-  int img_bytes;    // a resident buffer
+  int XR;           // image bytes a token of a stage, or of a buffer
+  int img_bytes;    // an image buffer beside the ring (0: images lie in the stages)
   int stage_bytes, nst;
   int items;        // (expert, token group) pairs at most
   int o_img, o_part, o_hq, o_mask, o_ebase, o_item, o_tok, o_bar;  // offsets
@@ -333,7 +333,7 @@ struct MoeShared {
   unsigned short* ppair;     // [pairs] pair (token * top_k + slot) of a row
   unsigned short* ptok;      // [pairs] its token
   uint64_t *full, *empty;    // [nst]
-  uint64_t *ifull, *iempty;  // [2] resident images
+  uint64_t *ifull, *iempty;  // [4] image buffers beside the ring
   int n_items;
 };
 
@@ -350,7 +350,7 @@ __device__ __forceinline__ MoeShared carve(const MoePlan& L, uint8_t* smem, int 
   S.full = reinterpret_cast<uint64_t*>(smem + L.o_bar);
   S.empty = S.full + L.nst;
   S.ifull = S.empty + L.nst;
-  S.iempty = S.ifull + 2;
+  S.iempty = S.ifull + 4;
   S.n_items = 0;
   return S;
 }
@@ -386,9 +386,9 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
       mbar_init(&S.full[i], L.mode == kContiguous ? 1 : kProducers);
       mbar_init(&S.empty[i], kGroupWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.ifull[i], 1);
-      mbar_init(&S.iempty[i], kConsumers);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.ifull[i], L.mode == kContiguous ? 1 : kProducers);
+      mbar_init(&S.iempty[i], L.mode == kContiguous ? kConsumers : kGroupWarps);
     }
     fence_barrier_init();
   }
@@ -462,26 +462,19 @@ __device__ __forceinline__ void bulk_images(const MoePlan& L, uint8_t* dst, uint
     bulk_g2s(dst + token_off(L.XR, i), img(i) + (size_t)c0 * kImgBlock, (uint32_t)nb * kImgBlock, full, pol);
 }
 
-// The lines that blocks [c0, c0 + nb) of a row touch: rows start on any even
-// byte (off: the row's start in its matrix).
+// The 16-byte lines that blocks [c0, c0 + nb) of a row touch: rows start on
+// any even byte (off: the row's start in its matrix).  A matrix of 32 n rows
+// ends with a line.
 struct RowLines {
   long long lo;    // the first line's start
-  uint32_t bytes;  // whole lines inside the matrix
-  long long end;   // the blocks' end
+  uint32_t bytes;
 };
-__device__ __forceinline__ RowLines row_lines(long long off, int c0, int nb, long long mat_bytes) {
+__device__ __forceinline__ RowLines row_lines(long long off, int c0, int nb) {
   RowLines R;
   const long long a = off + (long long)c0 * kQBlockBytes;
   R.lo = a & ~15LL;
-  R.end = a + (long long)nb * kQBlockBytes;
-  const long long hi = min((R.end + 15) & ~15LL, mat_bytes & ~15LL);
-  R.bytes = (uint32_t)(hi - R.lo);
+  R.bytes = (uint32_t)(((a + (long long)nb * kQBlockBytes + 15) & ~15LL) - R.lo);
   return R;
-}
-// A matrix that ends inside a line: its last bytes, by plain stores.
-__device__ __forceinline__ void row_tail(uint8_t* slot, const uint8_t* base, const RowLines& R) {
-  for (long long x = R.lo + R.bytes; x < R.end; x += 2)
-    *reinterpret_cast<unsigned short*>(slot + (x - R.lo)) = *reinterpret_cast<const unsigned short*>(base + x);
 }
 
 // Shared loads at an immediate offset: the blocks' words lie at constant
@@ -711,7 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int it0 = kResident ? q0 / nq : 0, n_it = kResident && q1 > q0 ? (q1 - 1) / nq - it0 + 1 : 0;  // the CTA's items
   if (warp >= kConsumers) {
     const int rb = L.bpr * kQBlockBytes;
-    const long long mat = (long long)P.n_experts * rows * rb;
     const uint32_t smem32 = smem_u32(smem);
     const auto img = [&](int row) {
       return kGate ? P.ximg + (size_t)S.ptok[row] * L.bpr * kImgBlock : P.himg + (size_t)row * L.bpr * kImgBlock;
@@ -719,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pw = warp - kConsumers;
     const uint64_t pol = policy_evict_first(), keep = policy_evict_last();
     uint32_t filled = 0, parity = 0;
-    int images = 0;  // resident buffers filled by this warp
+    int images = 0;  // whole rows: items whose images this warp fetched
+    uint32_t ifilled = 0, iparity = 0;  // rows in slices: image buffers filled, parity of the last fill
     Place w;
     w.q = q0;
     const auto ready = [&]() {  // the stage may be filled
@@ -801,11 +794,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kGate) griddep_wait();
       fence_proxy_async_global();
       for (; w.q < q1; w.next(L, q1)) {
-        if (!ready()) break;
         const int it = w.unit() / nq;
         const int2 I = S.item[it];
-        const int tile = w.sl / L.nsl, c0 = (w.sl - tile * L.nsl) * L.S, nb = min(L.S, L.bpr - c0);
-        const int n = I.x >> 16, r0 = (w.unit() - it * nq) * kRows;
+        const int tile = w.sl % kTiles, c0 = w.sl / kTiles * L.S, nb = min(L.S, L.bpr - c0);
+        const int r0 = (w.unit() - it * nq) * kRows;
+        if (tile == 0) {  // the slice's images, for its four tiles
+          const int n = I.x >> 16, c = (w.q - q0) / 2 * L.nsl + w.sl / kTiles, buf = 2 * w.half + (c & 1);
+          const bool ok = c < 2 || ring_wait(&S.iempty[buf], (uint32_t)(c / 2 - 1) & 1u, &s_abort);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const int mine = pw < n ? (n - pw + kProducers - 1) / kProducers : 0;  // tokens pw, pw + 4, ..
+          if (lane == 0) mbar_arrive_expect_tx(&S.ifull[buf], (uint32_t)(mine * nb * kImgBlock));
+          __syncwarp();
+          bulk_images(L, smem + L.o_img + (size_t)buf * L.img_bytes, &S.ifull[buf], pw, kProducers, n, c0, nb,
+                      [&](int k) { return img(I.y + k); }, keep, lane);
+          ifilled |= 1u << buf;
+          iparity = (iparity & ~(1u << buf)) | (uint32_t)(c / 2 & 1) << buf;
+        }
+        if (!ready()) break;
         uint8_t* st = smem + (size_t)w.s * L.stage_bytes;
         uint64_t* full = &S.full[w.s];
         // lanes 0-3: a row of the tile's sixteen each; a warp's rows are one matrix's
@@ -815,28 +820,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = kGate ? 8 * tile + (slot & 7) : 16 * tile + slot;
         const bool live = lane < kMine && r0 + r < rows;
         RowLines R{};
-        if (live) {
-          R = row_lines(((long long)(I.x & 0xffff) * rows + r0 + r) * rb, c0, nb, mat);
-          row_tail(st + (size_t)slot * L.SR, base, R);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (plain stores before later copies)
-        __syncwarp();
-        const int mine = pw < n ? (n - pw + kProducers - 1) / kProducers : 0;  // tokens pw, pw + 4, ..
+        if (live) R = row_lines(((long long)(I.x & 0xffff) * rows + r0 + r) * rb, c0, nb);
         const uint32_t sum = __reduce_add_sync(0xffffffffu, live ? R.bytes : 0u);
-        if (lane == 0) mbar_arrive_expect_tx(full, sum + (uint32_t)(mine * nb * kImgBlock));
+        if (lane == 0) mbar_arrive_expect_tx(full, sum);
         __syncwarp();
-        if (live && R.bytes) bulk_g2s(st + (size_t)slot * L.SR, base + R.lo, R.bytes, full, pol);
-        bulk_images(L, st + L.x_off, full, pw, kProducers, n, c0, nb, [&](int k) { return img(I.y + k); }, keep, lane);
+        if (live) bulk_g2s(st + (size_t)slot * L.SR, base + R.lo, R.bytes, full, pol);
       }
     }
     drain(L, S, filled, parity, &s_abort);
+    if (kMode == kRowCopies && *(volatile int*)&s_abort)
+      for (int i = 0; i < 4; ++i)
+        if (ifilled >> i & 1u) mbar_wait(&S.ifull[i], iparity >> i & 1u);
     if (kResident && *(volatile int*)&s_abort)
       for (int i = max(0, images - 2); i < images; ++i) mbar_wait(&S.ifull[i & 1], (uint32_t)(i / 2) & 1u);
   } else {
     if (!kGate) griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
     const uint32_t smem32 = smem_u32(smem);
-    const uint32_t xoff = kResident ? 0u : (uint32_t)L.x_off;
+    const uint32_t xoff = !kAl ? 0u : (uint32_t)L.x_off;
     // column g is token g (packed: token g % 4, hi or lo)
     const auto col = [&](int n) { return xoff + token_off(L.XR, min(kPack ? n & 3 : n, L.tg - 1)); };
     const uint32_t xl = col(gq) + (uint32_t)(cq * 16 + (kPack ? 8 * (gq >> 2) : 0));
@@ -846,6 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* hq = reinterpret_cast<float*>(smem + L.o_hq) + group * kGuRows * 9;  // gate: [32 rows][8 tokens + 1]
     int s = group;
     uint32_t ph = 0;
+    int chunk = 0;  // rows in slices: this group's slices so far
     int held = -1;  // resident images: the item whose buffer this group holds
     const auto next_images = [&]() {  // every item in turn, also those without a unit of this group
       if (held >= 0) {
@@ -932,19 +934,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
+        for (int sl = 0; sl < L.nsl; ++sl, ++chunk) {
+          const int buf = 2 * group + (chunk & 1), c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
+          ring_wait(&S.ifull[buf], (uint32_t)(chunk >> 1) & 1u, &s_abort);
+          const uint32_t xs = smem32 + (uint32_t)(L.o_img + buf * L.img_bytes);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          uint64_t yt[1][2] = {{y[t][0], y[t][1]}};
-          for (int sl = 0; sl < L.nsl; ++sl) {
+          for (int t = 0; t < kTiles; ++t) {
             const uint32_t st = stage();
-            const int c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
             // where row g's slice starts in its slot (row g + 8's, 8 * 272
             // bytes of the matrix on or in the other one: as far into a line)
             const uint32_t r = (uint32_t)(r0 + (kGate ? 8 : 16) * t + gq);
             const uint32_t mis = (((uint32_t)(I.x & 0xffff) * (uint32_t)rows + r) * (uint32_t)L.bpr + (uint32_t)c0) *
                                  (uint32_t)kQBlockBytes & 15u;
+            uint64_t yt[1][2] = {{y[t][0], y[t][1]}};
             for (int j = member; j < nb; j += kGroupWarps) {
-              const uint32_t xo = st + (uint32_t)(j * kImgBlock);
+              const uint32_t xo = xs + (uint32_t)(j * kImgBlock);
               const uint32_t ba = st + (uint32_t)(gq * L.SR) + mis + (uint32_t)(j * kQBlockBytes);
               BlockIn<kPack, 1> B;
               load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
@@ -952,10 +956,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_unaligned<kPack>(ba + (uint32_t)(8 * L.SR), 1, cq, B);
               block_mma<kAl, kPack>(B, !(j & 1), cq, yt);
             }
+            y[t][0] = yt[0][0];
+            y[t][1] = yt[0][1];
             release();
           }
-          y[t][0] = yt[0][0];
-          y[t][1] = yt[0][1];
+          if (lane == 0) mbar_arrive(&S.iempty[buf]);  // (every lane is past its loads: release())
         }
       }
       // the warps' shares of the unit
@@ -1109,7 +1114,8 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
     o = up16i(o + 8 * pairs);
     L->o_bar = o;
     const int behind = o;
-    const auto slices = [&](int mode, int s) {  // of at most s blocks; false if four stages do not fit
+    // of at most s blocks; false if four stages, or a ring of `least` bytes, do not fit
+    const auto slices = [&](int mode, int s, int least) {
       const bool whole = mode == kContiguous;
       L->mode = mode;
       L->nsl = whole ? 1 : (bpr + s - 1) / s;
@@ -1127,23 +1133,25 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
       // 16-byte loads lie in distinct banks
       L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
       const int images = tg * L->XR + 64;
-      L->img_bytes = whole ? images : 0;
+      L->img_bytes = mode == kTensor ? 0 : images;
+      const int bufs = whole ? 2 : 4;  // two items', or two slices' of each group
       // (tensor copies land on 128 bytes; a row's last word is read 4 bytes past)
-      L->stage_bytes = (L->x_off + (whole ? 16 : images) + 127) / 128 * 128;
-      L->o_img = up16i(behind + 32);
-      L->smem = L->o_img + 2 * L->img_bytes;
+      L->stage_bytes = (L->x_off + (mode != kTensor ? 16 : images) + 127) / 128 * 128;
+      L->o_img = up16i(behind + 64);
+      L->smem = L->o_img + bufs * L->img_bytes;
       L->nst = std::min(12, (kMaxSmem - L->smem) / (L->stage_bytes + 16)) / kGroups * kGroups;
-      if (L->nst < 2 * kGroups) return false;
+      if (L->nst < 2 * kGroups || L->nst * L->stage_bytes < least) return false;
       const int ring = L->nst * L->stage_bytes;
       for (int* f : {&L->o_part, &L->o_hq, &L->o_mask, &L->o_ebase, &L->o_item, &L->o_tok, &L->o_bar, &L->o_img})
         *f += ring;
-      L->o_img += 16 * L->nst;  // (the barriers: 16 bytes a stage and the images' 32)
+      L->o_img += 16 * L->nst;  // (the barriers: 16 bytes a stage and the images' 64)
       L->smem += ring + 16 * L->nst;
       return true;
     };
-    if (!al && bpr <= 64 && slices(kContiguous, bpr)) return Q8D_OK;
-    for (int s = al ? 16 : 64; s >= 8; s -= 8)
-      if (slices(al ? kTensor : kRowCopies, s)) return Q8D_OK;
+    if (!al && bpr <= 64 && slices(kContiguous, bpr, 0)) return Q8D_OK;
+    for (int least : {al ? 0 : 64 * 1024, 0})
+      for (int s = al ? 16 : 64; s >= 8; s -= 8)
+        if (slices(al ? kTensor : kRowCopies, s, least)) return Q8D_OK;
   }
   return Q8D_EUNSUPPORTED;
 }

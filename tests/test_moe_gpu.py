@@ -253,3 +253,25 @@ def test_back_to_back_calls_and_a_graph(q8d):
             _, _, ref, tol = plain(layers[i], xi, E, hidden, ffn, k, True, xi)
             y = bufs[i + 1].cpu().numpy()
             assert np.all(np.abs(y - ref) <= tol), (np.abs(y - ref) / tol).max()
+
+
+# Widths by how their rows lie in memory: whole 16-byte lines or not, short
+# rows, rows cut into slices; with one, few and many tokens an expert, enough
+# units that a CTA's buffers are reused, a last unit of half the rows.
+@pytest.mark.parametrize("hidden,ffn", [
+    (32, 160), (160, 480), (480, 32), (1824, 608), (608, 1824), (3552, 96), (96, 3552), (2080, 4128), (544, 992),
+    (1056, 800), (2048, 768), (2304, 1312), (1504, 1536),
+])
+@pytest.mark.parametrize("m,E,k", [(1, 3, 2), (3, 6, 1), (13, 7, 2), (40, 5, 3)])
+def test_row_layouts(q8d, hidden, ffn, m, E, k):
+    L = layer(hidden + ffn, E, hidden, ffn)
+    check(q8d, L, synth.normal_f32(m, "rows.x", (m, hidden)), E, hidden, ffn, k, True)
+
+
+@pytest.mark.parametrize("hidden,ffn,m,E,k", [
+    (2336, 1376, 9, 40, 4), (1184, 1184, 24, 48, 6), (2048, 512, 30, 64, 4), (3488, 32, 16, 64, 8), (352, 96, 64, 300, 12),
+])
+def test_many_experts_a_block(q8d, hidden, ffn, m, E, k):
+    """More items than buffers in every CTA."""
+    L = layer(hidden + ffn, E, hidden, ffn)
+    check(q8d, L, synth.normal_f32(m, "many.x", (m, hidden)), E, hidden, ffn, k, False)
