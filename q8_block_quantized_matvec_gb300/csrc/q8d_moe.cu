@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "q8d_gemv.cuh"
 #include "q8d_internal.cuh"
@@ -314,7 +315,7 @@ struct MoePlan {
   int tr, lq;       // tiles a stage; log2 of the rows between a tile's rows g and g + 1
   int SR;           // slot bytes (tensor copies: of 8 blocks)
   int x_off;        // the images' offset in a stage
-  int tg;           // tokens a group (1, 2, 4 or 8)
+  int tg;           // tokens a group (1, 2, 4, 8 or 16)
   int XR;           // image bytes a token of a stage, or of a buffer
   int img_bytes;    // an image buffer beside the ring (0: images lie in the stages)
   int stage_bytes, nst;
@@ -504,31 +505,45 @@ __device__ __forceinline__ uint32_t lds16i(uint32_t a) {
   return v;
 }
 
-// What a lane reads of one block: its words of kN A tiles, their scales,
-// its columns' operand and inverse scales.  All loads of a block are issued
+// How a product's columns hold an item's tokens.
+constexpr int kPacked = 0;  // up to four: columns 0-3 their hi parts, 4-7 their lo parts
+constexpr int kEight = 1;   // up to eight, hi and lo an MMA each
+constexpr int kSixteen = 2; // up to sixteen: two column tiles share every decoded A
+constexpr int col_tiles(int cols) { return cols == kSixteen ? 2 : 1; }
+
+// What a lane reads of one block: words and scales of kN A tiles; and its
+// columns' operand and inverse scales.  All loads of a piece are issued
 // before its arithmetic (asm volatile keeps their order).
-// kPack: at most four tokens; columns 0-3 are their hi parts, 4-7 their lo
-// parts, so one MMA a step does what two do otherwise.
-template <bool kPack, int kN>
-struct BlockIn {
+template <int kN>
+struct RowsIn {
   uint32_t w[kN][2][3];  // row g or g + 8: words of steps 0 and 1, the scale (even blocks: and quants 0, 1)
-  uint32_t b[2][kPack ? 2 : 4];
-  float xi0, xi1;
+};
+template <int kCols>
+struct ColsIn {
+  uint32_t b[col_tiles(kCols)][2][kCols == kPacked ? 2 : 4];
+  float xi[col_tiles(kCols)][2];
 };
 
-template <bool kPack, int kN>
-__device__ __forceinline__ void load_x(uint32_t xa, uint32_t x0, uint32_t x1, BlockIn<kPack, kN>& B) {
-  if constexpr (kPack) {
-    const uint2 u = lds64i<0>(xa), v = lds64i<64>(xa);
-    B.b[0][0] = u.x, B.b[0][1] = u.y;
-    B.b[1][0] = v.x, B.b[1][1] = v.y;
-  } else {
-    const uint4 u = lds128i<0>(xa), v = lds128i<64>(xa);
-    B.b[0][0] = u.x, B.b[0][1] = u.y, B.b[0][2] = u.z, B.b[0][3] = u.w;
-    B.b[1][0] = v.x, B.b[1][1] = v.y, B.b[1][2] = v.z, B.b[1][3] = v.w;
+// xa: this lane's column's words, x0 and x1: the images whose inverse scales
+// its results take; of each column tile.
+template <int kCols>
+__device__ __forceinline__ void load_x(uint32_t xo, const uint32_t (&xa)[col_tiles(kCols)],
+                                       const uint32_t (&x0)[col_tiles(kCols)], const uint32_t (&x1)[col_tiles(kCols)],
+                                       ColsIn<kCols>& B) {
+#pragma unroll
+  for (int i = 0; i < col_tiles(kCols); ++i) {
+    if constexpr (kCols == kPacked) {
+      const uint2 u = lds64i<0>(xo + xa[i]), v = lds64i<64>(xo + xa[i]);
+      B.b[i][0][0] = u.x, B.b[i][0][1] = u.y;
+      B.b[i][1][0] = v.x, B.b[i][1][1] = v.y;
+    } else {
+      const uint4 u = lds128i<0>(xo + xa[i]), v = lds128i<64>(xo + xa[i]);
+      B.b[i][0][0] = u.x, B.b[i][0][1] = u.y, B.b[i][0][2] = u.z, B.b[i][0][3] = u.w;
+      B.b[i][1][0] = v.x, B.b[i][1][1] = v.y, B.b[i][1][2] = v.z, B.b[i][1][3] = v.w;
+    }
+    B.xi[i][0] = __uint_as_float(lds32i<128>(xo + x0[i]));
+    B.xi[i][1] = __uint_as_float(lds32i<128>(xo + x1[i]));
   }
-  B.xi0 = __uint_as_float(lds32i<128>(x0));
-  B.xi1 = __uint_as_float(lds32i<128>(x1));
 }
 
 // Slot of row g + 8 h of tile t, less g.
@@ -540,10 +555,11 @@ __host__ __device__ constexpr int slot_of(int t, int h) {
 // Rows from tensor copies: 272 bytes a slot, so that a slot is an immediate
 // offset.  bg: block start in slot g.  Words are aligned in odd blocks; an
 // even block's word 7 is its first two and last two quants (tc::word_quant).
-template <bool kGate, bool kPack, int I = 0>
-__device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, BlockIn<kPack, kTiles>& B) {
-  if constexpr (I < 2 * kTiles) {
-    constexpr int t = I / 2, h = I % 2, so = slot_of<kGate>(t, h) * 8 * kQBlockBytes;
+// Tiles T0 .. T0 + kN - 1.
+template <bool kGate, int T0, int kN, int I = 0>
+__device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, RowsIn<kN>& B) {
+  if constexpr (I < 2 * kN) {
+    constexpr int t = I / 2, h = I % 2, so = slot_of<kGate>(T0 + t, h) * 8 * kQBlockBytes;
     if (even) {
       B.w[t][h][0] = lds32i<so + 4>(bg + 4u * c);
       B.w[t][h][1] = lds32i<so>(bg + (c == 3 ? 32u : 20u + 4u * c));
@@ -553,12 +569,11 @@ __device__ __forceinline__ void load_aligned(uint32_t bg, bool even, int c, Bloc
       B.w[t][h][1] = lds32i<so + 18>(bg + 4u * c);
       B.w[t][h][2] = lds16i<so>(bg);
     }
-    load_aligned<kGate, kPack, I + 1>(bg, even, c, B);
+    load_aligned<kGate, T0, kN, I + 1>(bg, even, c, B);
   }
 }
 // Other rows: a block starts at any even address, quants in order.
-template <bool kPack>
-__device__ __forceinline__ void load_unaligned(uint32_t ba, int h, int c, BlockIn<kPack, 1>& B) {
+__device__ __forceinline__ void load_unaligned(uint32_t ba, int h, int c, RowsIn<1>& B) {
   const uint32_t q = ba + 2u + 4u * c, a = q & ~3u, sel = (q & 2u) ? 0x5432u : 0x3210u;
   const uint32_t w0 = lds32i<0>(a), w1 = lds32i<4>(a), w4 = lds32i<16>(a), w5 = lds32i<20>(a);
   B.w[0][h][2] = lds16i<0>(ba);
@@ -586,35 +601,52 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // y[t] += the products of a loaded block: columns 2c and 2c + 1 of rows g
-// ([0]) and g + 8 ([1]) of tile t.
-template <bool kAl, bool kPack, int kN>
-__device__ __forceinline__ void block_mma(const BlockIn<kPack, kN>& B, bool even, int c, uint64_t (&y)[kN][2]) {
-  const uint64_t xi = pack2(B.xi0, B.xi1);
+// ([0]) and g + 8 ([1]) of tile t, of each column tile.
+template <bool kAl, int kCols, int T0, int kN, int kT>
+__device__ __forceinline__ void block_mma(const RowsIn<kN>& A, const ColsIn<kCols>& B, bool even, int c,
+                                          uint64_t (&y)[col_tiles(kCols)][kT][2]) {
   const uint32_t sel = c == 3 ? 0x5432u : 0x7654u;
 #pragma unroll
   for (int t = 0; t < kN; ++t) {
-    float acc[4];
-    uint32_t a0, a1, a2, a3;
-    tc::quant_pairs(B.w[t][0][0], a0, a2);
-    tc::quant_pairs(B.w[t][1][0], a1, a3);
-    mma_zero(acc, a0, a1, a2, a3, B.b[0][0], B.b[0][1]);
-    if constexpr (!kPack) tc::mma_f16(acc, a0, a1, a2, a3, B.b[0][2], B.b[0][3]);
-    uint32_t w0 = B.w[t][0][1], w1 = B.w[t][1][1];
+    uint32_t a0, a1, a2, a3, e0, e1, e2, e3;
+    tc::quant_pairs(A.w[t][0][0], a0, a2);
+    tc::quant_pairs(A.w[t][1][0], a1, a3);
+    uint32_t w0 = A.w[t][0][1], w1 = A.w[t][1][1];
     if (kAl && even) {
-      w0 = __byte_perm(B.w[t][0][2], w0, sel);
-      w1 = __byte_perm(B.w[t][1][2], w1, sel);
+      w0 = __byte_perm(A.w[t][0][2], w0, sel);
+      w1 = __byte_perm(A.w[t][1][2], w1, sel);
     }
-    tc::quant_pairs(w0, a0, a2);
-    tc::quant_pairs(w1, a1, a3);
-    tc::mma_f16(acc, a0, a1, a2, a3, B.b[1][0], B.b[1][1]);
-    if constexpr (!kPack) tc::mma_f16(acc, a0, a1, a2, a3, B.b[1][2], B.b[1][3]);
+    const float d0 = __low2float(*reinterpret_cast<const __half2*>(&A.w[t][0][2]));
+    const float d1 = __low2float(*reinterpret_cast<const __half2*>(&A.w[t][1][2]));
+    float acc[col_tiles(kCols)][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float d = __low2float(*reinterpret_cast<const __half2*>(&B.w[t][h][2]));
-      y[t][h] = fma2(mul2(pack2(d, d), xi), pack2(acc[2 * h], acc[2 * h + 1]), y[t][h]);
+    for (int i = 0; i < col_tiles(kCols); ++i) {
+      mma_zero(acc[i], a0, a1, a2, a3, B.b[i][0][0], B.b[i][0][1]);
+      if constexpr (kCols != kPacked) tc::mma_f16(acc[i], a0, a1, a2, a3, B.b[i][0][2], B.b[i][0][3]);
+    }
+    tc::quant_pairs(w0, e0, e2);
+    tc::quant_pairs(w1, e1, e3);
+#pragma unroll
+    for (int i = 0; i < col_tiles(kCols); ++i) {
+      tc::mma_f16(acc[i], e0, e1, e2, e3, B.b[i][1][0], B.b[i][1][1]);
+      if constexpr (kCols != kPacked) tc::mma_f16(acc[i], e0, e1, e2, e3, B.b[i][1][2], B.b[i][1][3]);
+      const uint64_t xi = pack2(B.xi[i][0], B.xi[i][1]);
+      uint64_t(&yy)[2] = y[i][T0 + t];
+      yy[0] = fma2(mul2(pack2(d0, d0), xi), pack2(acc[i][0], acc[i][1]), yy[0]);
+      yy[1] = fma2(mul2(pack2(d1, d1), xi), pack2(acc[i][2], acc[i][3]), yy[1]);
     }
   }
 }
+
+// f of 0 .. kTiles - 1 as constants.
+template <typename F>
+__device__ __forceinline__ void each_tile(F f) {
+  f(std::integral_constant<int, 0>{});
+  f(std::integral_constant<int, 1>{});
+  f(std::integral_constant<int, 2>{});
+  f(std::integral_constant<int, 3>{});
+}
+static_assert(kTiles == 4, "");
 
 // Bounded wait that gives up when another thread of the CTA has.  (try_wait
 // without a time hint: with one it polls through nanosleep, and twenty
@@ -678,12 +710,13 @@ __device__ __forceinline__ void finish(const MoeParams& P, volatile int* abort) 
 
 // Launches 2 (kGate) and 3.  P.ypart row p = token * top_k + slot receives
 // that pair's weighted down product.
-template <int kMode, bool kGate, bool kPack>
+template <int kMode, bool kGate, int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_product_kernel(const MoeParams P, const MoePlan L, bool hperm,
                                                                   const __grid_constant__ CUtensorMap map0,
                                                                   const __grid_constant__ CUtensorMap map1) {
   constexpr bool kAl = kMode == kTensor;
+  constexpr int kCt = col_tiles(kCols);
   constexpr bool kResident = kMode == kContiguous;  // images stay for an item, in two buffers
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_abort;
@@ -838,10 +871,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gq = lane >> 2, cq = lane & 3;
     const uint32_t smem32 = smem_u32(smem);
     const uint32_t xoff = !kAl ? 0u : (uint32_t)L.x_off;
-    // column g is token g (packed: token g % 4, hi or lo)
-    const auto col = [&](int n) { return xoff + token_off(L.XR, min(kPack ? n & 3 : n, L.tg - 1)); };
-    const uint32_t xl = col(gq) + (uint32_t)(cq * 16 + (kPack ? 8 * (gq >> 2) : 0));
-    const uint32_t x0 = col(2 * cq), x1 = col(2 * cq + 1);
+    // column g of tile i is token 8 i + g (packed: token g % 4, hi or lo)
+    uint32_t xl[kCt], x0[kCt], x1[kCt];
+#pragma unroll
+    for (int i = 0; i < kCt; ++i) {
+      const auto col = [&](int n) {
+        return xoff + token_off(L.XR, min(kCols == kPacked ? n & 3 : 8 * i + n, L.tg - 1));
+      };
+      xl[i] = col(gq) + (uint32_t)(cq * 16 + (kCols == kPacked ? 8 * (gq >> 2) : 0));
+      x0[i] = col(2 * cq);
+      x1[i] = col(2 * cq + 1);
+    }
     const int group = warp / kGroupWarps, member = warp % kGroupWarps, tid = threadIdx.x - group * kGroupThreads;
     float* part = S.part + group * kGroupWarps * kSlots * 8;                                 // [warp][slot][token]
     float* hq = reinterpret_cast<float*>(smem + L.o_hq) + group * kGuRows * 9;  // gate: [32 rows][8 tokens + 1]
@@ -864,9 +904,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kResident)
         while (held < it - it0) next_images();
       const uint32_t xres = smem32 + (uint32_t)(L.o_img + (held & 1) * L.img_bytes);
-      uint64_t y[kTiles][2];
+      uint64_t y[kCt][kTiles][2];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) y[t][0] = y[t][1] = pack2(0.f, 0.f);
+      for (int i = 0; i < kCt; ++i)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) y[i][t][0] = y[i][t][1] = pack2(0.f, 0.f);
       const auto stage = [&]() {  // the group's next stage
         ring_wait(&S.full[s], ph, &s_abort);
         return after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
@@ -885,123 +927,127 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t st = stage();
           const int nb = min(L.S, L.bpr - sl * L.S);
           for (int j = member; j < nb; j += kGroupWarps) {
-            const uint32_t xo = st + (uint32_t)(j * kImgBlock);
-            BlockIn<kPack, kTiles> B;
-            load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
+            ColsIn<kCols> B;
+            load_x<kCols>(st + (uint32_t)(j * kImgBlock), xl, x0, x1, B);
             // (sub-stages of 8 blocks)
-            load_aligned<kGate, kPack>(
-                st + (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes + gq * 8 * kQBlockBytes), !(j & 1), cq, B);
-            block_mma<kAl, kPack>(B, !(j & 1), cq, y);
+            const uint32_t bg = st + (uint32_t)((j >> 3) * kSubBytes + (j & 7) * kQBlockBytes + gq * 8 * kQBlockBytes);
+            if constexpr (kCt == 1) {
+              RowsIn<kTiles> A;
+              load_aligned<kGate, 0>(bg, !(j & 1), cq, A);
+              block_mma<kAl, kCols, 0>(A, B, !(j & 1), cq, y);
+            } else {  // (four tiles' words at once would spill)
+              RowsIn<2> A;
+              load_aligned<kGate, 0>(bg, !(j & 1), cq, A);
+              block_mma<kAl, kCols, 0>(A, B, !(j & 1), cq, y);
+              load_aligned<kGate, 2>(bg, !(j & 1), cq, A);
+              block_mma<kAl, kCols, 2>(A, B, !(j & 1), cq, y);
+            }
           }
           release();
         }
       } else if (kMode == kContiguous) {
         const uint32_t base = (uint32_t)((gq << L.lq) * L.SR + member * kQBlockBytes);
-        const auto tile = [&](uint32_t ba, int t, int j, uint32_t xo, BlockIn<kPack, 1>& B, uint64_t (&yy)[2]) {
-          const int s0 = kGate ? t : 2 * t;
+        // tile t of the stage into y[T]
+        const auto tile = [&](uint32_t ba, int t, const ColsIn<kCols>& B, auto T) {
+          const int s0 = kGate ? t : 2 * t, s1 = 2 * t + 1;
           const uint32_t at = ba + (uint32_t)((((s0 >> L.lq) << (3 + L.lq)) + (s0 & ((1 << L.lq) - 1))) * L.SR);
-          const int s1 = 2 * t + 1;
           const uint32_t at1 = kGate ? at + (uint32_t)(L.tr * 8 * L.SR)
                                      : ba + (uint32_t)((((s1 >> L.lq) << (3 + L.lq)) + (s1 & ((1 << L.lq) - 1))) * L.SR);
-          load_unaligned<kPack>(at, 0, cq, B);
-          load_unaligned<kPack>(at1, 1, cq, B);
-          uint64_t yt[1][2] = {{yy[0], yy[1]}};
-          block_mma<kAl, kPack>(B, !(j & 1), cq, yt);
-          yy[0] = yt[0][0];
-          yy[1] = yt[0][1];
+          RowsIn<1> A;
+          load_unaligned(at, 0, cq, A);
+          load_unaligned(at1, 1, cq, A);
+          block_mma<kAl, kCols, decltype(T)::value>(A, B, false, cq, y);
         };
         if (L.tr == kTiles) {
           const uint32_t st = stage();
           for (int j = member; j < L.bpr; j += kGroupWarps) {
-            const uint32_t xo = xres + (uint32_t)(j * kImgBlock), ba = st + base + (uint32_t)((j - member) * kQBlockBytes);
-            BlockIn<kPack, 1> B;
-            load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) tile(ba, t, j, xo, B, y[t]);
+            const uint32_t ba = st + base + (uint32_t)((j - member) * kQBlockBytes);
+            ColsIn<kCols> B;
+            load_x<kCols>(xres + (uint32_t)(j * kImgBlock), xl, x0, x1, B);
+            each_tile([&](auto T) { tile(ba, T.value, B, T); });
           }
           release();
         } else {
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
+          each_tile([&](auto T) {
             const uint32_t st = stage();
             for (int j = member; j < L.bpr; j += kGroupWarps) {
-              const uint32_t xo = xres + (uint32_t)(j * kImgBlock);
-              BlockIn<kPack, 1> B;
-              load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
-              tile(st + base + (uint32_t)((j - member) * kQBlockBytes), 0, j, xo, B, y[t]);
+              ColsIn<kCols> B;
+              load_x<kCols>(xres + (uint32_t)(j * kImgBlock), xl, x0, x1, B);
+              tile(st + base + (uint32_t)((j - member) * kQBlockBytes), 0, B, T);
             }
             release();
-          }
+          });
         }
       } else {
         for (int sl = 0; sl < L.nsl; ++sl, ++chunk) {
           const int buf = 2 * group + (chunk & 1), c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
           ring_wait(&S.ifull[buf], (uint32_t)(chunk >> 1) & 1u, &s_abort);
           const uint32_t xs = smem32 + (uint32_t)(L.o_img + buf * L.img_bytes);
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
+          each_tile([&](auto T) {
             const uint32_t st = stage();
             // where row g's slice starts in its slot (row g + 8's, 8 * 272
             // bytes of the matrix on or in the other one: as far into a line)
-            const uint32_t r = (uint32_t)(r0 + (kGate ? 8 : 16) * t + gq);
+            const uint32_t r = (uint32_t)(r0 + (kGate ? 8 : 16) * T.value + gq);
             const uint32_t mis = (((uint32_t)(I.x & 0xffff) * (uint32_t)rows + r) * (uint32_t)L.bpr + (uint32_t)c0) *
                                  (uint32_t)kQBlockBytes & 15u;
-            uint64_t yt[1][2] = {{y[t][0], y[t][1]}};
             for (int j = member; j < nb; j += kGroupWarps) {
-              const uint32_t xo = xs + (uint32_t)(j * kImgBlock);
               const uint32_t ba = st + (uint32_t)(gq * L.SR) + mis + (uint32_t)(j * kQBlockBytes);
-              BlockIn<kPack, 1> B;
-              load_x<kPack>(xo + xl, xo + x0, xo + x1, B);
-              load_unaligned<kPack>(ba, 0, cq, B);
-              load_unaligned<kPack>(ba + (uint32_t)(8 * L.SR), 1, cq, B);
-              block_mma<kAl, kPack>(B, !(j & 1), cq, yt);
+              ColsIn<kCols> B;
+              load_x<kCols>(xs + (uint32_t)(j * kImgBlock), xl, x0, x1, B);
+              RowsIn<1> A;
+              load_unaligned(ba, 0, cq, A);
+              load_unaligned(ba + (uint32_t)(8 * L.SR), 1, cq, A);
+              block_mma<kAl, kCols, decltype(T)::value>(A, B, false, cq, y);
             }
-            y[t][0] = yt[0][0];
-            y[t][1] = yt[0][1];
             release();
-          }
+          });
           if (lane == 0) mbar_arrive(&S.iempty[buf]);  // (every lane is past its loads: release())
         }
       }
-      // the warps' shares of the unit
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        float* p = part + ((member * kTiles + t) * 16 + gq) * 8 + 2 * cq;
-        *reinterpret_cast<uint64_t*>(p) = y[t][0];
-        *reinterpret_cast<uint64_t*>(p + 64) = y[t][1];
-      }
-      group_sync(group);
-      const int n = tid & 7;
-      const auto total = [&](int row) {  // of slot `row` of the unit's A tiles, column n
-        float v = 0.f;
+      for (int i = 0; i < kCt; ++i) {
+        const int n0 = 8 * i, nt = min(ntok - n0, 8);  // the tile's tokens
+        if (nt <= 0) break;
+        // the warps' shares of the unit
 #pragma unroll
-        for (int k = 0; k < kGroupWarps; ++k) {
-          const float* p = part + (k * kSlots + row) * 8;
-          v += kPack ? p[n & 3] + p[(n & 3) | 4] : p[n];
+        for (int t = 0; t < kTiles; ++t) {
+          float* p = part + ((member * kTiles + t) * 16 + gq) * 8 + 2 * cq;
+          *reinterpret_cast<uint64_t*>(p) = y[i][t][0];
+          *reinterpret_cast<uint64_t*>(p + 64) = y[i][t][1];
         }
-        return v;
-      };
-      if constexpr (kGate) {
-        const int t = tid >> 6, r = (tid >> 3) & 7;
-        const float g = total(16 * t + r), v = total(16 * t + r + 8);
-        hq[(kResident ? slot_row<true>(L, t, 0, r) : t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
         group_sync(group);
-        if (tid < 64) {  // the unit is block u of its tokens' h: token i, word w
-          const int i = tid >> 3, w = tid & 7;
-          float x[4];
+        const int n = tid & 7;
+        const auto total = [&](int row) {  // of slot `row` of the unit's A tiles, column n
+          float v = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = hq[tc::word_quant(hperm && !(u & 1), w, k) * 9 + i];
-          image_word(x, i < ntok, P.himg + ((size_t)(I.y + i) * nq + u) * kImgBlock, w);
-        }
-      } else {
+          for (int k = 0; k < kGroupWarps; ++k) {
+            const float* p = part + (k * kSlots + row) * 8;
+            v += kCols == kPacked ? p[n & 3] + p[(n & 3) | 4] : p[n];
+          }
+          return v;
+        };
+        if constexpr (kGate) {
+          const int t = tid >> 6, r = (tid >> 3) & 7;
+          const float g = total(16 * t + r), v = total(16 * t + r + 8);
+          hq[(kResident ? slot_row<true>(L, t, 0, r) : t * 8 + r) * 9 + n] = g / (1.f + expf(-g)) * v;
+          group_sync(group);
+          if (tid < 64) {  // the unit is block u of its tokens' h: token x, word w
+            const int x = tid >> 3, w = tid & 7;
+            float v4[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {  // 64 rows x 8 tokens
-          const int slot = (tid >> 3) + 32 * k, r = kResident ? slot_row<false>(L, slot >> 4, slot >> 3 & 1, slot & 7) : slot;
-          const float v = total(slot);
-          if (n < ntok && r0 + r < rows)
-            P.ypart[(size_t)S.ppair[I.y + n] * P.hidden + r0 + r] = S.pw[I.y + n] * v;
+            for (int k = 0; k < 4; ++k) v4[k] = hq[tc::word_quant(hperm && !(u & 1), w, k) * 9 + x];
+            image_word(v4, x < nt, P.himg + ((size_t)(I.y + n0 + x) * nq + u) * kImgBlock, w);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {  // 64 rows x 8 tokens
+            const int slot = (tid >> 3) + 32 * k, r = kResident ? slot_row<false>(L, slot >> 4, slot >> 3 & 1, slot & 7) : slot;
+            const float v = total(slot);
+            if (n < nt && r0 + r < rows)
+              P.ypart[(size_t)S.ppair[I.y + n0 + n] * P.hidden + r0 + r] = S.pw[I.y + n0 + n] * v;
+          }
+          group_sync(group);  // (the shares are rewritten next)
         }
-        group_sync(group);  // (the shares are rewritten next)
       }
     }
     if (kResident)
@@ -1066,12 +1112,22 @@ int weight_map(const uint8_t* w, int bpr, long long n_rows, int box_rows, CUtens
 
 // Tokens a group: about twice an expert's share of the (token, slot) pairs,
 // a power of two up to 8 (an expert with more is read once a group; with
-// fewer, its stage space idles).
-int group_tokens(const MoeParams& P) {
-  const int want = std::min(P.m, 2 * P.m * P.top_k / P.n_experts + 2);
+// fewer, its stage space idles).  Sixteen where that is clearly fewer units:
+// one of sixteen tokens takes up to 1.7 times one of eight, and the two groups
+// of every SM take a unit (nq an item) each a turn.  Measured, eight /
+// sixteen, us: 64 tokens, 2048 x 1024, 6 of 16 experts, 106 / 90; 48, 2048 x
+// 1408, 6 of 8, 127 / 111; 32, 2048 x 1024, 2 of 8 (one turn), 37.2 / 35.1; but
+// 64, 2048 x 1024, 2 of 16, 54 / 56; 33, 2944 x 704, 4 of 16, 79 / 89; 64, 2048
+// x 768, 8 of 128, 174 / 207.
+int group_tokens(const MoeParams& P, int nq) {
+  const double share = (double)P.m * P.top_k / P.n_experts;
+  const int want = std::min(P.m, (int)(2 * share) + 2);
   int tg = 1;
   while (tg < 8 && tg < want) tg *= 2;
-  return tg;
+  const auto turns = [&](int n) {  // (an expert's last group is half full on average)
+    return std::max(1.0, share / n + 0.5) * P.n_experts * nq / (kGroups * sm_count());
+  };
+  return share >= 8 && (1.7 * turns(16) < turns(8) || (turns(16) <= 1 && turns(8) > 1)) ? 16 : tg;
 }
 
 // Banks: the most of eight rows' words (rows `step` bytes apart) that one
@@ -1096,7 +1152,8 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
   const bool al = bpr % 8 == 0;
   const int pairs = P.m * P.top_k;
   L->bpr = bpr;
-  for (int tg = group_tokens(P); tg >= 1; tg /= 2) {
+  const int nq = gate ? P.ffn / kGuRows : (P.hidden + kSlots - 1) / kSlots;
+  for (int tg = group_tokens(P, nq); tg >= 1; tg /= 2) {
     L->tg = tg;
     L->items = std::min(pairs, P.n_experts + pairs / tg);
     int o = 0;  // behind the ring
@@ -1132,7 +1189,7 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
       // token rows half a bank cycle apart: the two tokens of a quarter warp's
       // 16-byte loads lie in distinct banks
       L->XR = (L->S * kImgBlock + 127) / 128 * 128 + 64;
-      const int images = tg * L->XR + 64;
+      const int images = up16i(tg * L->XR + 8 * tg);
       L->img_bytes = mode == kTensor ? 0 : images;
       const int bufs = whole ? 2 : 4;  // two items', or two slices' of each group
       // (tensor copies land on 128 bytes; a row's last word is read 4 bytes past)
@@ -1185,14 +1242,18 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   if (rc) return rc;
   const bool gal = bx % 8 == 0, dal = bh % 8 == 0;
   typedef void (*Product)(MoeParams, MoePlan, bool, CUtensorMap, CUtensorMap);
-  static const Product fns[3][2][2] = {
-      {{moe_product_kernel<kRowCopies, false, false>, moe_product_kernel<kRowCopies, false, true>},
-       {moe_product_kernel<kRowCopies, true, false>, moe_product_kernel<kRowCopies, true, true>}},
-      {{moe_product_kernel<kTensor, false, false>, moe_product_kernel<kTensor, false, true>},
-       {moe_product_kernel<kTensor, true, false>, moe_product_kernel<kTensor, true, true>}},
-      {{moe_product_kernel<kContiguous, false, false>, moe_product_kernel<kContiguous, false, true>},
-       {moe_product_kernel<kContiguous, true, false>, moe_product_kernel<kContiguous, true, true>}}};
-  const Product gu_fn = fns[gu.mode][1][gu.tg <= 4], dn_fn = fns[dn.mode][0][dn.tg <= 4];
+  const auto fn = [](const MoePlan& L, auto gate) -> Product {
+    constexpr bool kGate = decltype(gate)::value;
+    static const Product fns[3][3] = {
+        {moe_product_kernel<kRowCopies, kGate, kPacked>, moe_product_kernel<kRowCopies, kGate, kEight>,
+         moe_product_kernel<kRowCopies, kGate, kSixteen>},
+        {moe_product_kernel<kTensor, kGate, kPacked>, moe_product_kernel<kTensor, kGate, kEight>,
+         moe_product_kernel<kTensor, kGate, kSixteen>},
+        {moe_product_kernel<kContiguous, kGate, kPacked>, moe_product_kernel<kContiguous, kGate, kEight>,
+         moe_product_kernel<kContiguous, kGate, kSixteen>}};
+    return fns[L.mode][L.tg <= 4 ? kPacked : L.tg == 8 ? kEight : kSixteen];
+  };
+  const Product gu_fn = fn(gu, std::true_type{}), dn_fn = fn(dn, std::false_type{});
   CUtensorMap mg{}, mu{}, md{};
   if (gal) {
     rc = weight_map(P.wg, bx, (long long)P.n_experts * P.ffn, kGuRows, &mg);
