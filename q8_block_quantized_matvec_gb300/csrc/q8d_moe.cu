@@ -1112,14 +1112,15 @@ int weight_map(const uint8_t* w, int bpr, long long n_rows, int box_rows, CUtens
 
 // Tokens a group: about twice an expert's share of the (token, slot) pairs,
 // a power of two up to 8 (an expert with more is read once a group; with
-// fewer, its stage space idles).  Sixteen where that is clearly fewer units:
-// one of sixteen tokens takes up to 1.7 times one of eight, and the two groups
-// of every SM take a unit (nq an item) each a turn.  Measured, eight /
-// sixteen, us: 64 tokens, 2048 x 1024, 6 of 16 experts, 106 / 90; 48, 2048 x
-// 1408, 6 of 8, 127 / 111; 32, 2048 x 1024, 2 of 8 (one turn), 37.2 / 35.1; but
-// 64, 2048 x 1024, 2 of 16, 54 / 56; 33, 2944 x 704, 4 of 16, 79 / 89; 64, 2048
-// x 768, 8 of 128, 174 / 207.
-int group_tokens(const MoeParams& P, int nq) {
+// fewer, its stage space idles).  Sixteen where that is clearly fewer units
+// (nq an item; the two groups of every SM take one each a turn): by 1.35 for
+// tensor copies and two turns or more, else by 1.7.  Measured, eight /
+// sixteen, us: 64 tokens, 4096 x 4096, 2 of 8 experts, 268 / 215, 1 of 8, 174 /
+// 153; 64, 2048 x 1024, 6 of 16, 106 / 90; 32, 2048 x 1024, 2 of 8 (one turn),
+// 37.2 / 35.1; but 64, 2048 x 1024, 2 of 16, 54 / 56; 40, 3360 x 1120, 3 of 8,
+// 107 / 116; 33, 2944 x 704, 4 of 16, 79 / 89; 64, 2048 x 768, 8 of 128, 174 /
+// 207.
+int group_tokens(const MoeParams& P, int nq, bool al) {
   const double share = (double)P.m * P.top_k / P.n_experts;
   const int want = std::min(P.m, (int)(2 * share) + 2);
   int tg = 1;
@@ -1127,7 +1128,8 @@ int group_tokens(const MoeParams& P, int nq) {
   const auto turns = [&](int n) {  // (an expert's last group is half full on average)
     return std::max(1.0, share / n + 0.5) * P.n_experts * nq / (kGroups * sm_count());
   };
-  return share >= 8 && (1.7 * turns(16) < turns(8) || (turns(16) <= 1 && turns(8) > 1)) ? 16 : tg;
+  const double few = turns(16), many = turns(8);
+  return share >= 8 && ((al && few >= 2 ? 1.35 : 1.7) * few < many || (few <= 1 && many > 1)) ? 16 : tg;
 }
 
 // Banks: the most of eight rows' words (rows `step` bytes apart) that one
@@ -1153,7 +1155,7 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
   const int pairs = P.m * P.top_k;
   L->bpr = bpr;
   const int nq = gate ? P.ffn / kGuRows : (P.hidden + kSlots - 1) / kSlots;
-  for (int tg = group_tokens(P, nq); tg >= 1; tg /= 2) {
+  for (int tg = group_tokens(P, nq, al); tg >= 1; tg /= 2) {
     L->tg = tg;
     L->items = std::min(pairs, P.n_experts + pairs / tg);
     int o = 0;  // behind the ring
