@@ -196,7 +196,8 @@ size_t q8d_kv_cache_bytes(int kv_dtype, int kv_width, int cap);
  *   Q8D_DERR_LEN_RANGE, a row outside [0, cap) Q8D_DERR_POS_RANGE in *d_err
  *   (may be NULL), and nothing of that sequence is written; a count of 0
  *   writes nothing whatever the position.
- * kv_width % 32 == 0 for a packed or 4-bit cache.  rows == 0: no-op.
+ * kv_width % 32 == 0 for a packed or 4-bit cache; rows * kv_width below
+ *   2^34, else Q8D_EUNSUPPORTED.  rows == 0: no-op.
  * ---------------------------------------------------------------------- */
 int q8d_kv_append_rows(const void* k, const void* v, int row_dtype, int ld, void* kcache,
                        void* vcache, int kv_dtype, int batch, int rows, int kv_width, int cap,
@@ -324,9 +325,11 @@ int q8d_gqa_decode_attn_noalloc(const float* q, const float* k_new, const float*
  *   Y[t] = residual[t] + sum_k w_k * Wd_k (silu(Wg_k x) * (Wu_k x))
  * The logits, the softmax and the choice are computed beyond f32 accuracy,
  * so that neighbours in rank are told apart as 64-bit arithmetic would.
- * The products are f32-accurate (within 1e-5 of their sums of |terms|), and
- * every expert's weights are read once per call however many tokens chose
- * it.  Nothing depends on the order in which threads finish.
+ * The products are f32-accurate (within 1e-5 of their sums of |terms|).
+ * Weights of experts that no token chose are not read; an expert's are read
+ * once for every group of up to 16 tokens (8 where few tokens an expert are
+ * expected) that chose it.  Nothing depends on the order in which threads
+ * finish.
  *   X: device f32, token t at X + t*ldx (ldx >= hidden, ldx % 4 == 0),
  *      16-byte aligned
  *   router: device f32 [n_experts][hidden], 16-byte aligned

@@ -8,10 +8,10 @@
 // cache, and four neighbouring threads make a packed block of 32, whose
 // largest element they find with two shuffles.  Large calls give a thread
 // several such groups, loaded before any is used, because a CTA that moves
-// 8 KB spends as long starting as working: 8 x 2047 rows of 1024, f32 and
-// Q8_0, took 21.8 us to append and 18.9 to read with one group a thread, 16.7
-// and 13.5 with four; 102400 rows of 512 out of 4 bits into f16 57.6, now 51
-// (6.7 TB/s).  Staging the 34-byte blocks through shared memory, for whole
+// 8 KB spends as long starting as working: 8 sequences of up to 2047 rows of
+// 1024, f16 and Q8_0, took 21.8 us to append and 18.9 to read with one group a
+// thread, 16.7 and 13.5 with four; 131071 rows of 512 out of 4 bits into f16
+// 57.6, now 51 (6.7 TB/s).  Staging the 34-byte blocks through shared memory, for whole
 // 16-byte lines on the cache's side, was slower than the 2-byte accesses (21.8
 // against 18.9 us to read): the lines are put together in L1 and L2 anyway.
 // grid.y runs over the sequences and grid.z over k and v, so a ragged batch's
@@ -318,11 +318,12 @@ int launch_rows(KvRowsParams P, cudaStream_t stream) {
   const bool vec = P.width % kGroupE == 0 && (reinterpret_cast<uintptr_t>(P.k) % 16) == 0 &&
                    (reinterpret_cast<uintptr_t>(P.v) % 16) == 0 && (P.ld * sizeof(T)) % 16 == 0;
   // Several items a thread once one each would take more than two full
-  // machines (at one: 5.3 against 5.0 us for 4096 rows of 1024 f16 into 4
-  // bits).  Four or two, whichever measured better, us: Q8_0 8 x 2047 rows of
-  // 1024 f32, append 15.8 / 16.4 (with a rounding of fewer instructions that
-  // was not roundf's for NaN), read 13.4 / 14.0; 4 bits, 32768 rows of
-  // 1024, append 67.8 / 59.1 (it holds 32 f32 values a thread at four), read
+  // machines (from one on: 5.3 against 5.0 us for 4096 rows of 512 f32
+  // into 4 bits).  Four or two, whichever measured better, us: Q8_0, 8
+  // sequences of up to 2047 rows of 1024 f16, append 15.8 / 16.4 (with a
+  // rounding of fewer instructions that was not roundf's for NaN), read 13.4 /
+  // 14.0; 4 bits, 32768 rows of 1024 f32, append 67.8 / 59.1 (it holds 32 f32
+  // values a thread at four), read
   // 27.1 / 27.0; 16384 rows f32 from f16, read 41.0 / 38.0.
   constexpr int kMany = KV == Q8D_KV_Q8_0 ? 4 : 2;
   const bool many = items * P.batch * 2 > 2LL * 2048 * sm_count();

@@ -10,15 +10,9 @@
 // of 34 bytes a block of 32, and a token adds only a column to each product.
 // So both are streaming kernels: producer warps keep a ring of shared memory
 // stages filled, and sixteen consumer warps multiply with mma.sync m16n8k16.
-// Where rows are whole 16-byte lines (a multiple of 8 blocks) one TMA tensor
-// copy brings 8 blocks of 32 or 64 rows, 272 bytes a row: rows then lie 4 (mod
-// 32) banks apart and eight rows' words in distinct banks without padding.
-// Other rows come as a bulk copy each into padded slots, by four warps (a warp
-// issues such copies a lane at a time, some 90 cycles each), so their stages
-// are one tile of 16 rows by up to 64 blocks: fewer and longer pieces.
 //  * A: sixteen weight rows, a lane's word of four quants made two exact f16
-//    pairs (one PRMT and one subtraction a pair); B: up to eight tokens of
-//    the expert; the warps split the blocks of a row.
+//    pairs (one PRMT and one subtraction a pair); B: the expert's tokens;
+//    the warps split the blocks of a row.
 //  * The tokens' values are f16 hi + lo under a power-of-two scale for each
 //    block of 32 (the scheme of q8d_mma_frag.cuh): products are exact in f32
 //    and a block's sum is scaled once by weight scale * inverse scale, so
@@ -28,16 +22,31 @@
 //    rows), 16 bytes {hi01, hi23, lo01, lo23} a word, 144 a block with its
 //    inverse scale, so the products copy them beside the weights and never
 //    convert.
-//  * An expert's tokens are taken eight at a time (fewer where long rows
-//    leave no room); experts nobody chose are not touched.
 //  * A work unit is 64 slots of rows of one expert (32 gate and 32 up rows,
-//    or 64 down rows): four A tiles that share every B load.  Units are dealt
-//    to the CTAs in contiguous ranges.  (Giving each CTA a few output rows of
-//    every expert instead saves launch 4 but has every CTA fetch every h, 2.3
-//    bytes for one of weights at 64 tokens, and one tile per B load: 118
-//    against 62 us for the down products of moe_64.)
+//    or 64 down rows) for a group of its tokens: four A tiles.  Units are
+//    dealt to the CTAs in contiguous ranges; experts nobody chose are not
+//    touched.  (Giving each CTA a few output rows of every expert instead
+//    saves launch 4 but has every CTA fetch every h, 2.3 bytes for one of
+//    weights at 64 tokens, and one tile per B load: 118 against 62 us for
+//    the down products of 128 experts of 2048 x 768.)
+//  * How rows come depends on where they lie.  Whole 16-byte lines (a
+//    multiple of 8 blocks): a TMA tensor copy brings 8 blocks of 32 or 64
+//    rows, 272 bytes a row, so rows lie 4 (mod 32) banks apart and eight
+//    rows' words in distinct banks without padding; an image's slice comes
+//    with them.  Else, up to 64 blocks: rows are contiguous, so a stage's are
+//    one bulk copy a matrix, and the images stay in shared memory for all
+//    units of an item (fetched with every stage they were up to twice the
+//    weights' bytes, and rows copied singly were bound by the copies' issue:
+//    21 tokens, 2560 x 1120, 7 of 64 experts, 183 us for the layer, now 137;
+//    27 tokens, 1376 x 160, 6 of 128, 81, now 47).  Longer rows: a bulk copy
+//    each into padded slots, in slices whose images serve four tiles.
 //  * Sums are taken in a fixed order throughout and nothing is added to
 //    memory atomically: the same bits every time.
+// 64 tokens, 2048 x 768, 8 of 128 experts (630 MB of weights): router 14, gate
+// / up 104, down and sum 53 us.  The gate / up products alone would take 82 us
+// (55 percent of the issue slots at 20 warps an SM) and their copies alone 75
+// (weights and images, 650 MB through L2); they share shared memory and the
+// issue slots, and 104 is what both take.
 #include <cuda.h>
 
 #include <algorithm>

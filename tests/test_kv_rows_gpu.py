@@ -255,3 +255,38 @@ def test_rows_on_another_stream_and_in_a_graph(q8d):
         assert err.item() == 0
         assert np.array_equal(kc.cpu().numpy(), want) and np.array_equal(vc.cpu().numpy(), want)
         assert np.array_equal(ko.cpu().numpy().reshape(want_o.shape), want_o)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rt", [F32, F16])
+@pytest.mark.parametrize("width", [992, 1024])
+def test_large_calls(q8d, kind, rt, width):
+    """Calls large enough that a thread takes several groups: ragged ends
+    inside a thread's groups, a sequence of one row, an empty and a refused
+    one."""
+    batch, rows, cap = 5, 2111, 2200
+    stride = stride_of(cap, width)
+    counts, starts = [2111, 1, 2109, 0, 2000], [89, 2199, 0, 5, 201]  # the last: past the end
+    k, kx = rows_in(4, "large.k", batch, rows, width, rt, width, 0)
+    v, vx = rows_in(5, "large.v", batch, rows, width, rt, width, 0)
+    kc, vc = (torch.full((batch, kp.cache_bytes(kind, stride)), 0x11, dtype=torch.uint8, device="cuda") for _ in range(2))
+    want = [c.cpu().numpy() for c in (kc, vc)]
+    err = ints([0])
+    q8d.q8d_kv_append_rows(k, v, rt, width, kc, vc, kind, batch, rows, width, cap, stride, ints(starts), ints(counts), err)
+    torch.cuda.synchronize()
+    assert err.item() == q8d.Q8D_DERR_POS_RANGE
+    for s in range(4):
+        for w, x in zip(want, (kx, vx)):
+            kp.store(w[s], kind, width, cap, starts[s], x[s, :counts[s]])
+    assert np.array_equal(kc.cpu().numpy(), want[0]) and np.array_equal(vc.cpu().numpy(), want[1])
+    ko, vo = (torch.full((batch, rows, width), -7.0, dtype=TT[rt], device="cuda") for _ in range(2))
+    q8d.q8d_kv_read_rows(kc, vc, kind, ko, vo, rt, width, batch, rows, width, cap, stride, ints(starts), ints(counts), err)
+    torch.cuda.synchronize()
+    for o, w in ((ko, want[0]), (vo, want[1])):
+        o = o.cpu().numpy()
+        for s in range(4):
+            with np.errstate(over="ignore"):
+                vals = kp.values(w[s], kind, width, cap)[starts[s]:starts[s] + counts[s]].astype(NP[rt])
+            assert np.array_equal(o[s, :counts[s]], vals)
+            assert np.all(o[s, counts[s]:] == -7.0)
+        assert np.isnan(o[4]).all()
