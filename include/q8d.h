@@ -249,7 +249,9 @@ size_t q8d_gqa_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_
  *            bytes (contents need no initialisation)
  * head_dim in {64, 128}; n_heads % n_kv_heads == 0; n_heads/n_kv_heads <= 16;
  * every kv_dtype (a packed or 4-bit cache's stride is still in elements:
- * a multiple of 256, so that sequences start on 16-byte boundaries).
+ * a multiple of 256, so that sequences start on 16-byte boundaries);
+ * for a 4-bit cache batch * (cap / 32 + 17) below 2^30 (with run maps 4 cap),
+ * else Q8D_EUNSUPPORTED.
  * ---------------------------------------------------------------------- */
 int q8d_gqa_decode_attn(const float* q, const float* k_new, const float* v_new, void* kcache,
                         void* vcache, int kv_dtype, float* out, int batch, int n_heads,

@@ -184,6 +184,7 @@ __device__ __forceinline__ int tiles4(int L) { return L < 1 ? 0 : (L + kTile4 - 
 
 struct Split4 {
   int piece;  // tiles a CTA
+  int total;  // tiles of the batch
   bool bad;   // an invalid length
   // With a single workspace slot a sequence (caches of up to kMinChunk rows)
   // goes whole to the CTA in whose piece it starts.
@@ -198,7 +199,8 @@ __device__ __forceinline__ Split4 split4(const AttnParams& P, int lane) {
     S.len = window_len4(P, 0);
     S.bad = S.len < 1;
     const int ctas = min(P.nct, P.nc);
-    S.piece = max(kMinChunk / kTile4, (tiles4(S.len) + ctas - 1) / ctas);
+    S.total = tiles4(S.len);
+    S.piece = max(kMinChunk / kTile4, (S.total + ctas - 1) / ctas);
     return S;
   }
   int sum = 0, most = 0;
@@ -214,6 +216,7 @@ __device__ __forceinline__ Split4 split4(const AttnParams& P, int lane) {
   sum = __reduce_add_sync(0xffffffffu, sum);
   most = __reduce_max_sync(0xffffffffu, most);
   S.bad = __any_sync(0xffffffffu, bad);
+  S.total = sum;
   S.piece = max(kMinChunk / kTile4, (sum + P.nct - 1) / P.nct);
   // a sequence's pieces fit its slots: with rows that start anywhere in a
   // piece, k pieces' length touches k + 1
@@ -308,6 +311,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   const Split4 sp = split4(P, lane);
   // (the combine writes NaN outputs)
   if (sp.bad && blockIdx.x == 0 && g == 0 && tid == 0 && P.d_err) atomicOr(P.d_err, Q8D_DERR_LEN_RANGE);
+  if ((long long)blockIdx.x * sp.piece >= sp.total) return;
   const int p_begin = blockIdx.x * sp.piece;
   Seq4 sq;
   if (!seq_from4(P, sp, p_begin, lane, sq)) return;

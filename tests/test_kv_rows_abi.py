@@ -98,3 +98,21 @@ def test_q4_append_and_attention_refusals(q8d):
     assert attn(stride=64 * 128 + 32) == EALIGN
     assert attn(stride=64 * 64) == EINVAL
     assert attn(n=ws - 1) == q8d.Q8D_ERANGE
+
+
+def test_q4_attention_counts_tiles_in_32_bits(q8d):
+    """A batch whose tiles of 32 rows (and a sequence's fixed ones) pass 2^30
+    is refused before anything else is looked at."""
+    L, big = q8d.lib(), 1 << 62
+
+    def attn(batch, cap, kv=4):
+        return L.q8d_gqa_decode_attn(A, None, None, C_, D_, kv, B, batch, 2, 2, 64, cap, big, E, 0.125, A + 65536, 0, None, None)
+
+    def window(batch, cap):
+        return L.q8d_gqa_decode_attn_window(A, None, None, C_, D_, 4, B, batch, 2, 2, 64, cap, 0, E, 0.125, A + 65536, 0,
+                                            None, None)
+
+    for call, n, cap in ((attn, 32768, 1 << 20), (attn, 1 << 26, 1), (window, 8192, 1 << 20)):
+        assert call(n, cap) == q8d.Q8D_EUNSUPPORTED
+        assert call(n // 2, cap) == q8d.Q8D_ERANGE  # (no workspace)
+    assert attn(32768, 1 << 20, 0) == q8d.Q8D_ERANGE  # other caches
