@@ -376,12 +376,44 @@ constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups, kGroupThreads = k
 constexpr int kThreads = (kConsumers + kProducers) * 32;
 constexpr int kPairsThread = (kMoeMaxTokens * kMoeMaxTop + kThreads - 1) / kThreads;
 
+// The barriers and the experts' masks, before anything is waited for.  The
+// whole CTA calls.
+__device__ __forceinline__ void start(const MoeParams& P, const MoePlan& L, const MoeShared& S) {
+  for (int e = threadIdx.x; e < P.n_experts; e += kThreads) S.mask[e] = 0ull;
+  if (threadIdx.x == 0) {
+    const int full = L.mode == kContiguous ? 1 : kProducers;
+    for (int i = 0; i < L.nst; ++i) {
+      mbar_init(&S.full[i], full);
+      mbar_init(&S.empty[i], kGroupWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.ifull[i], full);
+      mbar_init(&S.iempty[i], L.mode == kContiguous ? kConsumers : kGroupWarps);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+}
+
 // Groups the (token, slot) pairs by expert, in every CTA alike: experts in
 // order, an expert's tokens in order; a pair's row is its place in that
-// order.  The whole CTA calls.
+// order.  (One token: a pair is an item, in the order of the choice.)  The
+// whole CTA calls.
 __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) {
   __shared__ int s_items;
   const int pairs = P.m * P.top_k, E = P.n_experts;
+  if (P.m == 1) {
+    const int p = threadIdx.x;
+    if (p < pairs) {
+      S.item[p] = make_int2(__ldcg(P.experts + p) | 1 << 16, p);
+      S.pw[p] = __ldcg(P.weights + p);
+      S.ppair[p] = (unsigned short)p;
+      S.ptok[p] = 0;
+    }
+    __syncthreads();
+    S.n_items = pairs;
+    return;
+  }
   int ex[kPairsThread];
   float we[kPairsThread];
 #pragma unroll
@@ -390,19 +422,6 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
     ex[i] = p < pairs ? __ldcg(P.experts + p) : 0;
     we[i] = p < pairs ? __ldcg(P.weights + p) : 0.f;
   }
-  for (int e = threadIdx.x; e < E; e += kThreads) S.mask[e] = 0ull;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L.nst; ++i) {
-      mbar_init(&S.full[i], L.mode == kContiguous ? 1 : kProducers);
-      mbar_init(&S.empty[i], kGroupWarps);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&S.ifull[i], L.mode == kContiguous ? 1 : kProducers);
-      mbar_init(&S.iempty[i], L.mode == kContiguous ? kConsumers : kGroupWarps);
-    }
-    fence_barrier_init();
-  }
-  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPairsThread; ++i) {
     const int p = threadIdx.x + i * kThreads;
@@ -735,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The gate / up kernel lets the down kernel start once it has itself waited
   // for the router, so the down kernel may read the choice, and fill its ring
   // with weights, before it waits for h.
+  start(P, L, S);
   if (kGate) griddep_wait();
   griddep_launch_dependents();
   group_pairs(P, L, S);
