@@ -324,7 +324,8 @@ struct MoePlan {
   int tr, lq;       // tiles a stage; log2 of the rows between a tile's rows g and g + 1
   int SR;           // slot bytes (tensor copies: of 8 blocks)
   int x_off;        // the images' offset in a stage
-  int tg;           // tokens a group (1, 2, 4, 8 or 16)
+  int tg, lg;       // tokens a group (1, 2, 4, 8 or 16), log2 of it
+  float inv_k;      // 1 / top_k
   int XR;           // image bytes a token of a stage, or of a buffer
   int img_bytes;    // an image buffer beside the ring (0: images lie in the stages)
   int stage_bytes, nst;
@@ -374,7 +375,7 @@ constexpr int kConsumers = 16;                              // consumer warps
 // barrier's parity tells two neighbouring phases apart, no more).
 constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups, kGroupThreads = kGroupWarps * 32;
 constexpr int kThreads = (kConsumers + kProducers) * 32;
-constexpr int kPairsThread = (kMoeMaxTokens * kMoeMaxTop + kThreads - 1) / kThreads;
+static_assert(2 * kMoeMaxTokens * kMoeMaxTop <= kConsumers * kSlots * 8, "the pairs fit the sums' space");
 
 // The barriers and the experts' masks, before anything is waited for.  The
 // whole CTA calls.
@@ -414,56 +415,53 @@ __device__ void group_pairs(const MoeParams& P, const MoePlan& L, MoeShared& S) 
     S.n_items = pairs;
     return;
   }
-  int ex[kPairsThread];
-  float we[kPairsThread];
-#pragma unroll
-  for (int i = 0; i < kPairsThread; ++i) {
-    const int p = threadIdx.x + i * kThreads;
-    ex[i] = p < pairs ? __ldcg(P.experts + p) : 0;
-    we[i] = p < pairs ? __ldcg(P.weights + p) : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < kPairsThread; ++i) {
-    const int p = threadIdx.x + i * kThreads;
-    if (p < pairs) atomicOr(&S.mask[ex[i]], 1ull << (p / P.top_k));
+  // (loops are kept rolled: code that runs once costs its fetch)
+  const auto token = [&](int p) { return (int)(((float)p + 0.5f) * L.inv_k); };
+  int* pe = reinterpret_cast<int*>(S.part);  // (the sums' space is free so far)
+  float* pw = S.part + pairs;
+#pragma unroll 1
+  for (int p = threadIdx.x; p < pairs; p += kThreads) {
+    const int e = __ldcg(P.experts + p);
+    pw[p] = __ldcg(P.weights + p);
+    pe[p] = e;
+    atomicOr(&S.mask[e], 1ull << token(p));
   }
   __syncthreads();
   if (threadIdx.x < 32) {
-    const int lane = threadIdx.x, per = (E + 31) / 32;
-    int items = 0, rows = 0;
-    for (int e = lane * per; e < min(E, (lane + 1) * per); ++e) {
+    const int lane = threadIdx.x, per = (E + 31) / 32, e0 = lane * per, e1 = min(E, e0 + per);
+    int x = 0;  // items | rows << 16 (both fit 12 bits)
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
       const int c = __popcll(S.mask[e]);
-      items += (c + L.tg - 1) / L.tg;
-      rows += c;
+      x += ((c + L.tg - 1) >> L.lg) | c << 16;
     }
-    int x = items | rows << 16, incl = x;  // (both fit 12 bits)
+    int incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
     x = incl - x;
-    for (int e = lane * per; e < min(E, (lane + 1) * per); ++e) {
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
       S.ebase[e] = x;
-      const int c = __popcll(S.mask[e]);
-      for (int g = 0; g < c; g += L.tg) {
-        S.item[x & 0xffff] = make_int2(e | min(L.tg, c - g) << 16, (x >> 16));
-        x += 1 + (min(L.tg, c - g) << 16);
+#pragma unroll 1
+      for (int c = __popcll(S.mask[e]); c > 0; c -= L.tg) {
+        const int n = min(L.tg, c);
+        S.item[x & 0xffff] = make_int2(e | n << 16, x >> 16);
+        x += 1 | n << 16;
       }
     }
     if (lane == 31) s_items = incl & 0xffff;
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPairsThread; ++i) {
-    const int p = threadIdx.x + i * kThreads;
-    if (p < pairs) {
-      const int tok = p / P.top_k;
-      const int row = (S.ebase[ex[i]] >> 16) + __popcll(S.mask[ex[i]] & ((1ull << tok) - 1ull));
-      S.ptok[row] = (unsigned short)tok;
-      S.ppair[row] = (unsigned short)p;
-      S.pw[row] = we[i];
-    }
+#pragma unroll 1
+  for (int p = threadIdx.x; p < pairs; p += kThreads) {
+    const int e = pe[p], tok = token(p);
+    const int row = (S.ebase[e] >> 16) + __popcll(S.mask[e] & ((1ull << tok) - 1ull));
+    S.ptok[row] = (unsigned short)tok;
+    S.ppair[row] = (unsigned short)p;
+    S.pw[row] = pw[p];
   }
   __syncthreads();
   S.n_items = s_items;
@@ -1186,6 +1184,8 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
   const int nq = gate ? P.ffn / kGuRows : (P.hidden + kSlots - 1) / kSlots;
   for (int tg = group_tokens(P, nq, al); tg >= 1; tg /= 2) {
     L->tg = tg;
+    for (L->lg = 0; 1 << L->lg < tg;) ++L->lg;
+    L->inv_k = 1.f / (float)P.top_k;
     L->items = std::min(pairs, P.n_experts + pairs / tg);
     int o = 0;  // behind the ring
     L->o_part = o;
