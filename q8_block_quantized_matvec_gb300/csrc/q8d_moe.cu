@@ -381,16 +381,11 @@ static_assert(2 * kMoeMaxTokens * kMoeMaxTop <= kConsumers * kSlots * 8, "the pa
 // whole CTA calls.
 __device__ __forceinline__ void start(const MoeParams& P, const MoePlan& L, const MoeShared& S) {
   for (int e = threadIdx.x; e < P.n_experts; e += kThreads) S.mask[e] = 0ull;
-  if (threadIdx.x == 0) {
-    const int full = L.mode == kContiguous ? 1 : kProducers;
-    for (int i = 0; i < L.nst; ++i) {
-      mbar_init(&S.full[i], full);
-      mbar_init(&S.empty[i], kGroupWarps);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&S.ifull[i], full);
-      mbar_init(&S.iempty[i], L.mode == kContiguous ? kConsumers : kGroupWarps);
-    }
+  // (the barriers lie one behind the other: a thread each)
+  const int i = threadIdx.x, full = L.mode == kContiguous ? 1 : kProducers;
+  if (i < 2 * L.nst + 8) {
+    const int group = L.mode == kContiguous && i >= 2 * L.nst ? kConsumers : kGroupWarps;
+    mbar_init(&S.full[i], i < L.nst || (i >= 2 * L.nst && i < 2 * L.nst + 4) ? full : group);
     fence_barrier_init();
   }
   __syncthreads();
@@ -759,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kRows = kGate ? kGuRows : kSlots;  // rows of a unit
   const int rows = kGate ? P.ffn : P.hidden;       // rows of a matrix
   const int nq = (rows + kRows - 1) / kRows;       // units an item
-  const long long units = (long long)S.n_items * nq;
+  const unsigned units = (unsigned)S.n_items * (unsigned)nq;  // (at most 2048 x 512)
   const int q0 = (int)(units * blockIdx.x / gridDim.x), q1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
   const int it0 = kResident ? q0 / nq : 0, n_it = kResident && q1 > q0 ? (q1 - 1) / nq - it0 + 1 : 0;  // the CTA's items
   if (warp >= kConsumers) {
