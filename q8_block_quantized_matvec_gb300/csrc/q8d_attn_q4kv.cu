@@ -33,7 +33,8 @@
 //    by 2^8), so an ordinary tile does no reduction across lanes.
 //  * Eight warps, each with its own softmax over 32-token tiles and its own
 //    two-stage cp.async ring (16-byte chunks, XOR-swizzled for ldmatrix),
-//    merge once; partials are combined as in the other kernels.
+//    merge once; partials are combined as in the other kernels.  Short caches
+//    are not cut, and then there is nothing to combine.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -53,6 +54,14 @@ constexpr int kTile4 = 32;        // tokens a warp step
 constexpr int kStages4 = 2;
 constexpr float kSlack4 = 8.f;    // the running maximum may lag by this (log2)
 constexpr int kSeqCost4 = 16;     // a sequence's fixed work, in tiles
+// Caches of up to this many rows: sequences are not cut, so the attention
+// kernel writes the outputs itself and there is no second launch.  Graph /
+// single call, us, cut and combined against whole: 28 / 4 heads of 128, 256
+// rows, 5.8 / 8.9 against 4.9 / 6.7; 512 rows, 7.0 / 8.7 against 6.6 / 6.9; 1024
+// rows, 6.0 / 9.1 against 9.9 / 10.2; 32 ragged sequences of 16 / 8 heads, 512
+// rows, 12.7 / 13.0 against 10.8 / 11.0; 1024 rows, 15.4 / 15.7 against 16.4 /
+// 16.7.
+constexpr int kWholeCap4 = 512;
 constexpr int kFe0 = 7;           // P <= 2^8, |scale| < 2^ev, 2^fe = 2^(7 - ev): products < 2^15
 
 template <int D, int NH>
@@ -186,19 +195,17 @@ struct Split4 {
   int piece;  // tiles a CTA
   int total;  // tiles of the batch
   bool bad;   // an invalid length
-  // With a single workspace slot a sequence (caches of up to kMinChunk rows)
-  // goes whole to the CTA in whose piece it starts.
-  bool whole;
   int len;    // of sequence `lane`
 };
-// Every lane of a warp calls.
+// Every lane of a warp calls.  kWhole: a sequence goes whole to the CTA in
+// whose piece it starts.
+template <bool kWhole>
 __device__ __forceinline__ Split4 split4(const AttnParams& P, int lane) {
   Split4 S;
-  S.whole = P.nc == 1;
   if (P.batch == 1) {  // (no sums to wait for)
     S.len = window_len4(P, 0);
     S.bad = S.len < 1;
-    const int ctas = min(P.nct, P.nc);
+    const int ctas = kWhole ? 1 : min(P.nct, P.nc);
     S.total = tiles4(S.len);
     S.piece = max(kMinChunk / kTile4, (S.total + ctas - 1) / ctas);
     return S;
@@ -220,7 +227,7 @@ __device__ __forceinline__ Split4 split4(const AttnParams& P, int lane) {
   S.piece = max(kMinChunk / kTile4, (sum + P.nct - 1) / P.nct);
   // a sequence's pieces fit its slots: with rows that start anywhere in a
   // piece, k pieces' length touches k + 1
-  if (P.nc > 1) S.piece = max(S.piece, (most + P.nc - 2) / (P.nc - 1));
+  if (!kWhole && P.nc > 1) S.piece = max(S.piece, (most + P.nc - 2) / (P.nc - 1));
   return S;
 }
 
@@ -242,8 +249,9 @@ __device__ __forceinline__ int seq_of4(const AttnParams& P, const Split4& S, int
 struct Seq4 {
   int b, L, at;
 };
-// The first sequence with rows at or after tile `from` (whole: that starts
+// The first sequence with rows at or after tile `from` (kWhole: that starts
 // there); false if there is none.  Every lane of a warp calls.
+template <bool kWhole>
 __device__ __forceinline__ bool seq_from4(const AttnParams& P, const Split4& S, int from, int lane, Seq4& q) {
   if (P.batch == 1) {
     q.b = q.at = 0;
@@ -262,7 +270,7 @@ __device__ __forceinline__ bool seq_from4(const AttnParams& P, const Split4& S, 
       if (lane >= o) end += v;
     }
     end += before;
-    const uint32_t hit = __ballot_sync(0xffffffffu, n && (S.whole ? end - n >= from : end > from));
+    const uint32_t hit = __ballot_sync(0xffffffffu, n && (kWhole ? end - n >= from : end > from));
     if (hit) {
       const int x = __ffs(hit) - 1;
       q.b = s0 + x;
@@ -287,7 +295,7 @@ __device__ __forceinline__ bool seq_next4(const AttnParams& P, Seq4& q) {
 // NH: column tiles (2 for nine to sixteen heads).  kPack: at most four heads,
 // a head's hi and lo parts in columns 2h and 2h + 1 of one tile; else a tile
 // is eight heads and hi and lo take an MMA each.
-template <int D, int NH, bool kPack>
+template <int D, int NH, bool kPack, bool kWhole>
 __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(const AttnParams P) {
   using C = Cfg4<D, NH>;
   constexpr int NB = C::kNB;
@@ -308,13 +316,17 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   // after the wait: the combine, scheduled from here on, may read the lengths
   // before this grid is done
   griddep_launch_dependents();
-  const Split4 sp = split4(P, lane);
-  // (the combine writes NaN outputs)
+  const Split4 sp = split4<kWhole>(P, lane);
   if (sp.bad && blockIdx.x == 0 && g == 0 && tid == 0 && P.d_err) atomicOr(P.d_err, Q8D_DERR_LEN_RANGE);
+  if (kWhole && sp.bad && blockIdx.x == 0)  // (else the combine does)
+    for (int b = 0; b < P.batch; ++b)
+      if (window_len4(P, b) < 1)
+        for (int e = tid; e < G * D; e += kThreads4)
+          P.out[((long long)b * P.n_heads + (long long)g * G) * D + e] = __int_as_float(0x7fc00000);
   if ((long long)blockIdx.x * sp.piece >= sp.total) return;
   const int p_begin = blockIdx.x * sp.piece;
   Seq4 sq;
-  if (!seq_from4(P, sp, p_begin, lane, sq)) return;
+  if (!seq_from4<kWhole>(P, sp, p_begin, lane, sq)) return;
 
   const int width = P.n_kv_heads * D;
   const long long splane = q4_scale_plane(P.cap, width);
@@ -343,7 +355,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   for (bool first = true; sq.at < p_begin + sp.piece; first = false) {  // the piece's sequences
     const int b = sq.b, L = sq.L;
     int t_begin = 0, t_end = L, c = 0;
-    if (!sp.whole) {
+    if (!kWhole) {
       t_begin = max(p_begin - sq.at, 0) * kTile4;
       t_end = min(L, (p_begin + sp.piece - sq.at) * kTile4);
       c = blockIdx.x - (P.batch == 1 ? 0 : sq.at / sp.piece);
@@ -717,9 +729,13 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         mm[w * kHeads + h] = wgt;
         lsum = fmaf(ll[w * kHeads + h], wgt, lsum);
       }
-      const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
-      P.ws_m[hq * P.nc + c] = M;
-      P.ws_l[hq * P.nc + c] = lsum;
+      if (kWhole) {
+        ll[h] = lsum;  // (its own column's first entry)
+      } else {
+        const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
+        P.ws_m[hq * P.nc + c] = M;
+        P.ws_l[hq * P.nc + c] = lsum;
+      }
     }
     __syncthreads();
     for (int e = tid; e < G * (D / 4); e += kThreads4) {
@@ -735,7 +751,13 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         acc.w = fmaf(x.w, wgt, acc.w);
       }
       const long long hq = (long long)b * P.n_heads + (long long)g * G + h;
-      *reinterpret_cast<float4*>(P.ws_o + (hq * P.nc + c) * D + j) = acc;
+      if (kWhole) {
+        float* o1 = P.out + hq * D + j;
+        const float sum = ll[h];
+        o1[0] = acc.x / sum, o1[1] = acc.y / sum, o1[2] = acc.z / sum, o1[3] = acc.w / sum;
+      } else {
+        *reinterpret_cast<float4*>(P.ws_o + (hq * P.nc + c) * D + j) = acc;
+      }
     }
     if (!seq_next4(P, sq)) break;
   }
@@ -760,10 +782,10 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
   const int j = tid % kLanes, grp = tid / kLanes;
   // the attention grid released this one after its own wait: the lengths are
   // readable
-  const Split4 sp = split4(P, lane);
+  const Split4 sp = split4<false>(P, lane);
   int L;
   const int at = seq_of4(P, sp, b, lane, L);
-  const int nact = sp.whole ? 1 : (at + tiles4(L) - 1) / sp.piece - at / sp.piece + 1;
+  const int nact = (at + tiles4(L) - 1) / sp.piece - at / sp.piece + 1;
   griddep_wait();               // the partials are complete and visible
   griddep_launch_dependents();  // (not earlier: the next kernel would take SMs from this one)
   float* o = P.out + (long long)hq * D;
@@ -835,13 +857,12 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
   }
 }
 
-// The same by a warp a (sequence, query head), lanes holding D/32 dims: for
-// many heads, which as blocks of their own would take several waves, and for
-// few chunks.  The whole call, blocks / warps: 42 sequences of 96 heads, 179
-// rows, 57 / 16.8 us; 32 ragged sequences of 16 heads up to 8192 rows, 44.5 /
-// 41.5; 9 of 28 heads, 274 rows, 9.5 / 7.9.  With many chunks and few heads
-// its loads are too few at a time: 8 ragged of 28 heads up to 32768 rows, 29.4
-// / 34.6; 6 of 24 heads, 2000 rows, 9.0 / 12.7.
+// The same by a warp a (sequence, query head), lanes holding D/32 dims, for
+// many heads, which as blocks of their own would take several waves.  The
+// whole call, blocks / warps: 32 ragged sequences of 16 heads up to 8192 rows,
+// 44.5 / 41.5 us; 20 of 32 heads up to 1000 rows, 18.1 / 14.5.  With many
+// chunks and few heads its loads are too few at a time: 8 ragged of 28 heads
+// up to 32768 rows, 29.4 / 34.6; 6 of 24 heads, 2000 rows, 9.0 / 12.7.
 constexpr int kFewThreads4 = 256;
 
 template <int D>
@@ -849,11 +870,11 @@ __global__ void __launch_bounds__(kFewThreads4) gqa_q4kv_combine_few_kernel(cons
   constexpr int kV = D / 32;
   const int lane = threadIdx.x & 31;
   const int hq = blockIdx.x * (kFewThreads4 / 32) + (threadIdx.x >> 5);
-  const Split4 sp = split4(P, lane);  // (readable, as above)
+  const Split4 sp = split4<false>(P, lane);  // (readable, as above)
   const bool live = hq < P.batch * P.n_heads;
   int L;
   const int b = live ? hq / P.n_heads : 0, at = seq_of4(P, sp, b, lane, L);
-  const int nact = sp.whole ? 1 : (at + tiles4(L) - 1) / sp.piece - at / sp.piece + 1;
+  const int nact = (at + tiles4(L) - 1) / sp.piece - at / sp.piece + 1;
   griddep_wait();
   griddep_launch_dependents();
   if (!live) return;
@@ -899,20 +920,21 @@ __global__ void __launch_bounds__(kFewThreads4) gqa_q4kv_combine_few_kernel(cons
   for (int i = 0; i < kV; ++i) o[i] = acc[i] / lsum;
 }
 
-template <int D, int NH, bool kPack>
+template <int D, int NH, bool kPack, bool kWhole>
 int launch_q4kv(AttnParams P, cudaStream_t stream) {
   using C = Cfg4<D, NH>;
-  const auto fn = gqa_q4kv_kernel<D, NH, kPack>;
+  const auto fn = gqa_q4kv_kernel<D, NH, kPack, kWhole>;
   // (no carveout preference: a change of carveout between this kernel and
   // the next drains the SMs, 2 us a call)
   int rc = configure_kernel(reinterpret_cast<const void*>(fn), C::kSmem, false);
   if (rc) return rc;
   // one wave (two column tiles: a CTA an SM)
-  P.nct = std::min(P.nct, std::max(1, (NH == 1 ? 2 : 1) * sm_count() / P.n_kv_heads));
+  const int wave = std::max(1, (NH == 1 ? 2 : 1) * sm_count() / P.n_kv_heads);
+  P.nct = !kWhole ? std::min(P.nct, wave) : P.batch == 1 ? 1 : wave;
   rc = launch_ex(fn, dim3(P.nct, P.n_kv_heads), dim3(kThreads4), (size_t)C::kSmem, stream, true, P);
-  if (rc) return rc;
+  if (rc || kWhole) return rc;
   const long long heads = (long long)P.batch * P.n_heads;
-  if (heads > 2LL * sm_count() || P.nc <= 4) {
+  if (heads > 2LL * sm_count()) {
     constexpr int kPer = kFewThreads4 / 32;
     return launch_ex(gqa_q4kv_combine_few_kernel<D>, dim3((unsigned)((heads + kPer - 1) / kPer)),
                      dim3(kFewThreads4), 0, stream, true, P);
@@ -920,18 +942,20 @@ int launch_q4kv(AttnParams P, cudaStream_t stream) {
   return launch_ex(gqa_q4kv_combine_kernel<D>, dim3((unsigned)heads), dim3(kCombThreads4), 0, stream, true, P);
 }
 
-template <int D>
+template <int D, bool kWhole>
 int launch_q4kv_g(const AttnParams& P, cudaStream_t stream) {
   const int G = P.n_heads / P.n_kv_heads;
-  if (G <= 4) return launch_q4kv<D, 1, true>(P, stream);
-  if (G <= 8) return launch_q4kv<D, 1, false>(P, stream);
-  return launch_q4kv<D, 2, false>(P, stream);
+  if (G <= 4) return launch_q4kv<D, 1, true, kWhole>(P, stream);
+  if (G <= 8) return launch_q4kv<D, 1, false, kWhole>(P, stream);
+  return launch_q4kv<D, 2, false, kWhole>(P, stream);
 }
 
 }  // namespace
 
 int attn_q4kv_launch(const AttnParams& P, cudaStream_t stream) {
-  return P.head_dim == 128 ? launch_q4kv_g<128>(P, stream) : launch_q4kv_g<64>(P, stream);
+  if (P.cap <= kWholeCap4)
+    return P.head_dim == 128 ? launch_q4kv_g<128, true>(P, stream) : launch_q4kv_g<64, true>(P, stream);
+  return P.head_dim == 128 ? launch_q4kv_g<128, false>(P, stream) : launch_q4kv_g<64, false>(P, stream);
 }
 
 }  // namespace q8d

@@ -103,9 +103,11 @@ def test_one_row_returns_v(q8d):
 
 
 @pytest.mark.parametrize("batch", [2, 5, 33, 70])
-def test_ragged_batch(q8d, orc, batch):
-    """Unequal lengths, strides with a gap, refused sequences among them."""
-    H, Hk, D, cap = 12, 2, 64, 515
+@pytest.mark.parametrize("cap", [515, 400])
+def test_ragged_batch(q8d, orc, batch, cap):
+    """Unequal lengths, strides with a gap, refused sequences among them, with
+    sequences cut into pieces and whole."""
+    H, Hk, D = 12, 2, 64
     width = Hk * D
     stride = -(-cap * width // 256) * 256 + 512
     lens = [1 + (i * 7919) % cap for i in range(batch)]
@@ -290,9 +292,21 @@ def test_cache_past_2_to_the_32_bytes(q8d, orc):
     assert np.all(got[0] == 0)
 
 
+@pytest.mark.parametrize("cap", [512, 513])
+def test_refused_alone(q8d, cap):
+    """One sequence without rows: NaN, and nothing else is read."""
+    H, Hk, D = 20, 2, 128
+    kc, vc = (dev(q4_cache(4, f"ref.{x}", cap, Hk * D)) for x in "kv")
+    q = dev(synth.normal_f32(4, "ref.q", H * D))
+    for L in (0, -1, cap + 1):
+        got, err = run(q8d, q, kc, vc, H, Hk, D, [L], cap, 0.1)
+        assert err == q8d.Q8D_DERR_LEN_RANGE and np.isnan(got).all()
+
+
 @pytest.mark.parametrize("H,Hk,D,cap,batch,kind", [
     (4, 2, 64, 6000, 40, "one long"), (3, 1, 128, 3000, 9, "one long"), (2, 2, 64, 128, 130, "short caches"),
-    (96, 96, 64, 300, 7, "more heads than CTAs"), (16, 1, 64, 500, 35, "even"), (4, 4, 128, 130, 90, "two slots"),
+    (96, 96, 64, 300, 7, "more heads than CTAs"), (160, 160, 64, 600, 3, "more heads than CTAs"),
+    (200, 200, 64, 520, 1, "more heads than CTAs"), (16, 1, 64, 500, 35, "even"), (4, 4, 128, 130, 90, "two slots"),
     (8, 8, 64, 90, 2, "short caches"),
 ])
 def test_batches_cut_into_pieces(q8d, orc, H, Hk, D, cap, batch, kind):
