@@ -54,7 +54,6 @@ int kv_read_rows_launch(const KvRowsParams& P, cudaStream_t stream);
 // and both planes start on 16-byte boundaries, so the attention copies and
 // ldmatrix-reads them as whole 16-byte blocks; blocks with their scale
 // inside (18 bytes) would start on any even byte.
-__host__ __device__ constexpr int kQ4BlockBytes() { return 16; }
 __host__ __device__ inline long long q4_scale_plane(int cap, int width) {
   return (long long)cap * (width / 2);
 }
