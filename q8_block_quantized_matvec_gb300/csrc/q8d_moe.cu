@@ -154,23 +154,25 @@ __device__ void choose(const MoeParams& P, int t, const float2* logits, int lane
     const float x = expf(d);
     return isinf(d) ? x : fmaf(x, r, x);
   };
-  float all = 0.f, all2 = 0.f;
+  const float w = lane < P.top_k ? ex(mine) : 0.f;
+  // the sum of the chosen, or of all, in two parts
+  float sum = P.norm ? w : 0.f, sum2 = 0.f;
+  bool bad = isnan(top.x) || isinf(top.x);
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < E) add_pair(all, all2, ex(lane + 32 * i), 0.f);
-  const float w = lane < P.top_k ? ex(mine) : 0.f;
-  float chosen = w, chosen2 = 0.f;
+    if (lane + 32 * i < E) {
+      if (!P.norm) add_pair(sum, sum2, ex(lane + 32 * i), 0.f);
+      bad = bad || isnan(logits[lane + 32 * i].x);
+    }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float a = __shfl_xor_sync(0xffffffffu, all, o), a2 = __shfl_xor_sync(0xffffffffu, all2, o);
-    const float c = __shfl_xor_sync(0xffffffffu, chosen, o), c2 = __shfl_xor_sync(0xffffffffu, chosen2, o);
-    add_pair(all, all2, a, a2);
-    add_pair(chosen, chosen2, c, c2);
+    const float a = __shfl_xor_sync(0xffffffffu, sum, o), a2 = __shfl_xor_sync(0xffffffffu, sum2, o);
+    add_pair(sum, sum2, a, a2);
   }
+  bad = __any_sync(0xffffffffu, bad);  // (then the softmax is NaN throughout)
   if (lane < P.top_k) {
     P.experts[t * P.top_k + lane] = mine;
-    P.weights[t * P.top_k + lane] =
-        isnan(all) ? __int_as_float(0x7fc00000) : __fdiv_rn(w, P.norm ? chosen + chosen2 : all + all2);
+    P.weights[t * P.top_k + lane] = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(w, sum + sum2);
   }
 }
 
@@ -277,19 +279,20 @@ __global__ void __launch_bounds__(kRtThreads, 2) moe_router_kernel(const MoePara
   if constexpr (kT == 1)  // (two experts at once share a token's loads; with two tokens they spill)
     for (; e + kWarps < e1; e += 2 * kWarps) logits_of<kT, 2>(P, t0, nt, e, kWarps, e1, logits, lane);
   for (; e < e1; e += kWarps) logits_of<kT, 1>(P, t0, nt, e, kWarps, e1, logits, lane);
-  // the tokens' operand images, a word a thread, blocks dealt over the cluster
-  const int bpr = P.hidden / kQBlock, words = nt * bpr * 8;
-  for (int i0 = (rank * kRtThreads + warp * 32); i0 < words; i0 += kRtCluster * kRtThreads) {
-    const int i = i0 + lane, ii = min(i, words - 1);
-    const int t = ii / (bpr * 8), b = (ii >> 3) % bpr, w = ii & 7;
-    float v[4];
-    const float* x = P.X + (size_t)(t0 + t) * P.ldx + (size_t)b * kQBlock;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = x[tc::word_quant(perm && !(b & 1), w, k)];
-    image_word(v, i < words, P.ximg + ((size_t)(t0 + t) * bpr + b) * kImgBlock, w);
-  }
   cluster_sync();  // the logits are complete
-  if (rank == 0 && warp < nt) {
+  if (rank > 0) {
+    // meanwhile the others make the tokens' operand images, a word a thread
+    const int bpr = P.hidden / kQBlock, words = nt * bpr * 8;
+    for (int i0 = (rank - 1) * kRtThreads + warp * 32; i0 < words; i0 += (kRtCluster - 1) * kRtThreads) {
+      const int i = i0 + lane, ii = min(i, words - 1);
+      const int t = ii / (bpr * 8), b = (ii >> 3) - t * bpr, w = ii & 7;
+      float v[4];
+      const float* x = P.X + (size_t)(t0 + t) * P.ldx + (size_t)b * kQBlock;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = x[tc::word_quant(perm && !(b & 1), w, k)];
+      image_word(v, i < words, P.ximg + ((size_t)(t0 + t) * bpr + b) * kImgBlock, w);
+    }
+  } else if (warp < nt) {
     const float2* l = logits[warp];
     if (P.n_experts <= 64)
       choose<2>(P, t0 + warp, l, lane);
