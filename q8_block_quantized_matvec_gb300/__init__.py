@@ -141,36 +141,40 @@ def last_cuda_error() -> int:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return int(t)
+        raise
 
 
-_raw_stream = None
+_raw_stream = _device = None
 
 
-def _current_stream() -> int:
-    """torch's current stream on the current device.  torch.cuda.current_stream
-    builds a Stream object (3 us on the Arm host, more than a launch); its raw
-    handle comes from the same place without one."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        torch.cuda.current_stream()  # (initialises CUDA)
-        try:
-            get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            get(device())
-            _raw_stream = lambda: get(device())  # noqa: E731
-        except AttributeError:
-            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-    return _raw_stream()
+def _find_stream() -> None:
+    """Sets _raw_stream and _device: torch's current stream on the current
+    device.  torch.cuda.current_stream builds a Stream object (3 us on the Arm
+    host, more than a launch); its raw handle comes from the same place
+    without one."""
+    global _raw_stream, _device
+    import torch
+    torch.cuda.current_stream()  # (initialises CUDA)
+    try:
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        raw(device())
+    except AttributeError:
+        raw, device = lambda _: torch.cuda.current_stream().cuda_stream, lambda: 0  # noqa: E731
+    _raw_stream, _device = raw, device
 
 
 def _stream(stream):
     if stream is None:
-        return _current_stream()
+        if _raw_stream is None:
+            _find_stream()
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
