@@ -1160,13 +1160,9 @@ int group_tokens(const MoeParams& P, int nq, bool al) {
 // Banks: the most of eight rows' words (rows `step` bytes apart) that one
 // bank holds.
 int bank_rows(int step) {
-  int most = 0;
-  for (int bank = 0; bank < 32; ++bank) {
-    int n = 0;
-    for (int g = 0; g < 8; ++g)
-      for (int c = 0; c < 4; ++c) n += (g * step / 4 + c) % 32 == bank;
-    most = std::max(most, n);
-  }
+  int n[32] = {}, most = 0;
+  for (int g = 0; g < 8; ++g)
+    for (int c = 0; c < 4; ++c) most = std::max(most, ++n[(g * step / 4 + c) % 32]);
   return most;
 }
 
@@ -1209,9 +1205,13 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
       if (mode == kTensor) L->S = (L->S + 7) / 8 * 8;
       L->tr = mode == kRowCopies || (whole && bpr > 16) ? 1 : kTiles;
       L->lq = 0;
-      if (whole)
-        for (int lq = 1; 1 << lq <= L->tr * (gate ? 1 : 2); ++lq)
-          if (bank_rows((bpr * kQBlockBytes) << lq) < bank_rows((bpr * kQBlockBytes) << L->lq)) L->lq = lq;
+      if (whole) {
+        int least_rows = bank_rows(bpr * kQBlockBytes);
+        for (int lq = 1; 1 << lq <= L->tr * (gate ? 1 : 2); ++lq) {
+          const int n = bank_rows((bpr * kQBlockBytes) << lq);
+          if (n < least_rows) least_rows = n, L->lq = lq;
+        }
+      }
       L->stages = mode == kTensor ? L->nsl : whole ? kTiles / L->tr : kTiles * L->nsl;
       L->SR = mode == kTensor ? 8 * kQBlockBytes : whole ? bpr * kQBlockBytes : slot_bytes(L->S);
       L->x_off = mode == kTensor ? L->S / 8 * kSubBytes : 16 * L->tr * L->SR;
