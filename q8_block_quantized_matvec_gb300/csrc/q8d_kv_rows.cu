@@ -68,6 +68,33 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&f)[kGroupE]) {
   }
 }
 
+// Four elements, all of which exist where kVec.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load4(const T* p, int n, float (&f)[4]) {
+  if constexpr (kVec && sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  } else if constexpr (kVec) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? (float)p[i] : 0.f;
+  }
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void store4(T* p, int n, const float (&f)[4]) {
+  if constexpr (kVec) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = (T)f[i];
+  }
+}
+
 template <typename T, bool kVec>
 __device__ __forceinline__ void store8(T* p, int n, const float (&f)[kGroupE]) {
   if constexpr (kVec && sizeof(T) == 4) {
@@ -86,6 +113,21 @@ __device__ __forceinline__ void store8(T* p, int n, const float (&f)[kGroupE]) {
     for (int i = 0; i < kGroupE; ++i)
       if (i < n) p[i] = (T)f[i];
   }
+}
+
+template <typename T, bool kVec, int kE>
+__device__ __forceinline__ void load_e(const T* p, int n, float (&f)[kE]) {
+  if constexpr (kE == 4)
+    load4<T, kVec>(p, n, f);
+  else
+    load8<T, kVec>(p, n, f);
+}
+template <typename T, bool kVec, int kE>
+__device__ __forceinline__ void store_e(T* p, int n, const float (&f)[kE]) {
+  if constexpr (kE == 4)
+    store4<T, kVec>(p, n, f);
+  else
+    store8<T, kVec>(p, n, f);
 }
 
 // Element i of the group in the cache: types F32 / F16 as T.
@@ -135,9 +177,11 @@ __device__ __forceinline__ void put_q4(uint8_t* quants, uint8_t* scale, int part
   m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 2), (part & 2) != 0);
   float d, id;
   q4_scale(m, d, id);
-  uint32_t w[2] = {0u, 0u};
+  uint32_t w[2];  // a byte an element
 #pragma unroll
-  for (int i = 0; i < kGroupE; ++i) w[i >> 2] |= q4_nibble(f[i], id) << (8 * (i & 3));
+  for (int i = 0; i < 2; ++i)
+    w[i] = __byte_perm(__byte_perm(q4_bits(f[4 * i], id), q4_bits(f[4 * i + 1], id), 0x0040),
+                       __byte_perm(q4_bits(f[4 * i + 2], id), q4_bits(f[4 * i + 3], id), 0x0040), 0x5410);
   const bool high = part >= 2;
   const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[0] : w[1], 2);
   if (!live) return;
@@ -146,8 +190,17 @@ __device__ __forceinline__ void put_q4(uint8_t* quants, uint8_t* scale, int part
   if (part == 0) *reinterpret_cast<unsigned short*>(scale) = __half_as_ushort(__float2half_rn(d));
 }
 
+// Elements an append's thread takes at once: a packed block's quarter, or 16
+// bytes of the cache (eight of an f32 cache would be two stores, each of half
+// of every 32-byte sector).
+template <int KV>
+constexpr int append_item() {
+  return KV == Q8D_KV_F32 ? 4 : kGroupE;
+}
+
 template <typename T, int KV, bool kVec, int kPer>
 __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvRowsParams P) {
+  constexpr int kE = append_item<KV>();
   griddep_launch_dependents();
   griddep_wait();  // (a programmatic dependent: the previous work is complete)
   const T* src = static_cast<const T*>(blockIdx.z ? P.v : P.k);
@@ -160,7 +213,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvRow
     if (first >= items) continue;  // (the whole CTA)
     const T* rows = src + (long long)s * P.rows * P.ld;
     uint8_t* seq = cache + P.seq_bytes * s;
-    float f[kPer][kGroupE];
+    float f[kPer][kE];
     int row[kPer], g[kPer];
     bool live[kPer];
 #pragma unroll
@@ -169,7 +222,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvRow
       live[u] = item < items;
       row[u] = live[u] ? (int)P.groups.div(item) : 0;
       g[u] = live[u] ? (int)(item - (uint32_t)row[u] * groups) : 0;
-      load8<T, kVec>(rows + (long long)row[u] * P.ld + g[u] * kGroupE, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
+      load_e<T, kVec, kE>(rows + (long long)row[u] * P.ld + g[u] * kE, min(kE, P.width - g[u] * kE), f[u]);
       row[u] += pos;
     }
 #pragma unroll
@@ -183,40 +236,36 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvRow
         put_q8_0(seq + (r * (P.width / kQBlock) + (g[u] >> 2)) * kQBlockBytes, g[u] & 3, f[u], live[u]);
       } else {
         using C = typename CacheT<KV>::T;
-        C* dst = reinterpret_cast<C*>(seq) + r * P.width + g[u] * kGroupE;
+        C* dst = reinterpret_cast<C*>(seq) + r * P.width + g[u] * kE;
         if (!live[u]) continue;
-        if (P.width % kGroupE == 0)
-          store8<C, true>(dst, kGroupE, f[u]);
+        if (P.width % kE == 0)
+          store_e<C, true, kE>(dst, kE, f[u]);
         else
-          store8<C, false>(dst, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
+          store_e<C, false, kE>(dst, min(kE, P.width - g[u] * kE), f[u]);
       }
     }
   }
 }
 
-// Reading: for a 4-bit row an item is half a block (8 bytes: elements 8h ..
-// 8h+7 and 16+8h .. 16+8h+7, so every access outside is 16 bytes or more),
-// otherwise eight consecutive elements; kPer items a thread, kRowThreads
-// apart, loaded before any is converted.
-template <int KV>
-constexpr int read_item() {
-  return KV == Q8D_KV_Q4 ? 16 : kGroupE;
+// Reading: a store outside is 16 bytes, kE elements (with two stores a lane
+// of f32 each instruction would fill half of every 32-byte sector: 16384 rows
+// of 1024 from f16 37.6 us, now 30.3; 12 x 10127 of 128 from 4 bits, 21.9, now
+// 14.5),
+// and an item one store; for a 4-bit row two: kE / 2 of a block's bytes, their
+// low and their high halves.  kPer items a thread, kRowThreads apart, loaded
+// before any is converted.
+template <typename T>
+constexpr int store_e() {
+  return 16 / sizeof(T);
 }
-
-// What an item holds of a packed row, and its values.
-template <int KV>
-struct Packed {
-  uint32_t w[4];
-  float d;
-};
-template <>
-struct Packed<Q8D_KV_Q4> {
-  uint2 w;
-  float d;
-};
-
+template <int KV, typename T>
+constexpr int read_item() {
+  return (KV == Q8D_KV_Q4 ? 2 : 1) * store_e<T>();
+}
 template <typename T, int KV, bool kVec, int kPer>
 __global__ void __launch_bounds__(kRowThreads) kv_read_rows_kernel(const KvRowsParams P) {
+  constexpr int kE = store_e<T>();
+  constexpr int kParts = KV == Q8D_KV_Q4 ? 16 / kE : kQBlock / kE;  // items a block
   griddep_launch_dependents();
   griddep_wait();
   T* dst = static_cast<T*>(blockIdx.z ? P.v : P.k);
@@ -232,8 +281,9 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_rows_kernel(const KvRowsP
     if (first >= items) continue;  // (the whole CTA)
     const uint8_t* seq = cache + P.seq_bytes * s;
     T* rows = dst + (long long)s * P.rows * P.ld;
-    Packed<KV> in[kPer];
-    float f[kPer][kGroupE];
+    uint32_t w[kPer][kE / 2];  // packed: two quants a word; 4 bits: four bytes a word
+    float scale[kPer];
+    float f[kPer][kE];
     int row[kPer], g[kPer];
     bool live[kPer];
 #pragma unroll
@@ -244,23 +294,30 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_rows_kernel(const KvRowsP
       g[u] = live[u] ? (int)(item - (uint32_t)row[u] * groups) : 0;
       const long long r = ok ? pos + row[u] : 0;  // (row 0 for a refused sequence: not used)
       if constexpr (KV == Q8D_KV_Q4) {
-        const int blk = g[u] >> 1, h = g[u] & 1;
-        in[u].w = *reinterpret_cast<const uint2*>(seq + r * (P.width / 2) + blk * 16 + h * 8);
-        in[u].d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(
+        const int blk = g[u] / kParts, part = g[u] % kParts;
+        const uint8_t* q = seq + r * (P.width / 2) + blk * 16 + part * kE;
+        if constexpr (kE == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(q);
+          w[u][0] = v.x;
+          w[u][1] = v.y;
+        } else {
+          w[u][0] = *reinterpret_cast<const uint32_t*>(q);
+        }
+        scale[u] = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(
             seq + q4_scale_plane(P.cap, P.width) + r * (P.width / 16) + blk * 2));
       } else if constexpr (KV == Q8D_KV_Q8_0) {
-        const uint8_t* blk = seq + (r * (P.width / kQBlock) + (g[u] >> 2)) * kQBlockBytes;
-        in[u].d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(blk));
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(blk + 2 + 8 * (g[u] & 3));
+        const uint8_t* blk = seq + (r * (P.width / kQBlock) + g[u] / kParts) * kQBlockBytes;
+        scale[u] = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(blk));
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(blk + 2 + kE * (g[u] % kParts));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) in[u].w[e] = q[e];
+        for (int e = 0; e < kE / 2; ++e) w[u][e] = q[e];
       } else {
         using C = typename CacheT<KV>::T;
-        const C* p = reinterpret_cast<const C*>(seq) + r * P.width + g[u] * kGroupE;
-        if (P.width % kGroupE == 0)
-          load8<C, true>(p, kGroupE, f[u]);
+        const C* p = reinterpret_cast<const C*>(seq) + r * P.width + g[u] * kE;
+        if (P.width % kE == 0)
+          load_e<C, true, kE>(p, kE, f[u]);
         else
-          load8<C, false>(p, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
+          load_e<C, false, kE>(p, min(kE, P.width - g[u] * kE), f[u]);
       }
     }
 #pragma unroll
@@ -268,31 +325,31 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_rows_kernel(const KvRowsP
       if (!live[u]) continue;
       T* out = rows + (long long)row[u] * P.ld;
       if constexpr (KV == Q8D_KV_Q4) {
-        const float d = ok ? in[u].d : nan;
+        const float d = ok ? scale[u] : nan;
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
 #pragma unroll
-          for (int e = 0; e < kGroupE; ++e) {
+          for (int e = 0; e < kE; ++e) {
             // half-byte n under the exponent of 2^23: 2^23 + n, exactly
-            const uint32_t n = ((e < 4 ? in[u].w.x : in[u].w.y) >> (8 * (e & 3) + 4 * hi)) & 15u;
+            const uint32_t n = (w[u][e / 4] >> (8 * (e & 3) + 4 * hi)) & 15u;
             f[u][e] = d * (__uint_as_float(n | 0x4B000000u) - 8388616.f);
           }
-          store8<T, kVec>(out + (g[u] >> 1) * 32 + (g[u] & 1) * 8 + hi * 16, kGroupE, f[u]);
+          store_e<T, kVec, kE>(out + g[u] / kParts * 32 + g[u] % kParts * kE + hi * 16, kE, f[u]);
         }
       } else {
         if constexpr (KV == Q8D_KV_Q8_0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t q = in[u].w[e] ^ 0x8080u;
-            f[u][2 * e] = in[u].d * (__uint_as_float((q & 0xffu) | kMagicHi) - kMagicBias);
-            f[u][2 * e + 1] = in[u].d * (__uint_as_float((q >> 8) | kMagicHi) - kMagicBias);
+          for (int e = 0; e < kE / 2; ++e) {
+            const uint32_t q = w[u][e] ^ 0x8080u;
+            f[u][2 * e] = scale[u] * (__uint_as_float((q & 0xffu) | kMagicHi) - kMagicBias);
+            f[u][2 * e + 1] = scale[u] * (__uint_as_float((q >> 8) | kMagicHi) - kMagicBias);
           }
         }
         if (!ok) {
 #pragma unroll
-          for (int e = 0; e < kGroupE; ++e) f[u][e] = nan;
+          for (int e = 0; e < kE; ++e) f[u][e] = nan;
         }
-        store8<T, kVec>(out + g[u] * kGroupE, min(kGroupE, P.width - g[u] * kGroupE), f[u]);
+        store_e<T, kVec, kE>(out + g[u] * kE, min(kE, P.width - g[u] * kE), f[u]);
       }
     }
   }
@@ -310,7 +367,7 @@ int launch_rows_per(const KvRowsParams& P, cudaStream_t stream) {
 
 template <bool kRead, typename T, int KV>
 int launch_rows(KvRowsParams P, cudaStream_t stream) {
-  const int item_e = kRead ? read_item<KV>() : kGroupE;
+  const int item_e = kRead ? read_item<KV, T>() : append_item<KV>();
   P.groups = fast_div((uint32_t)((P.width + item_e - 1) / item_e));
   const long long items = (long long)P.rows * P.groups.d;
   if (items > 0xffff0000LL) return Q8D_EUNSUPPORTED;  // (item numbers are 32 bits)
@@ -323,9 +380,9 @@ int launch_rows(KvRowsParams P, cudaStream_t stream) {
   // sequences of up to 2047 rows of 1024 f16, append 15.8 / 16.4 (with a
   // rounding of fewer instructions that was not roundf's for NaN), read 13.4 /
   // 14.0; 4 bits, 32768 rows of 1024 f32, append 67.8 / 59.1 (it holds 32 f32
-  // values a thread at four), read
-  // 27.1 / 27.0; 16384 rows f32 from f16, read 41.0 / 38.0.
-  constexpr int kMany = KV == Q8D_KV_Q8_0 ? 4 : 2;
+  // values a thread at four), read 27.1 / 27.0; f32 rows in 16-byte items,
+  // 16384 of 1024 from f16, read 30.3 / 33.8.
+  constexpr int kMany = KV == Q8D_KV_Q8_0 || KV == Q8D_KV_F32 || (kRead && sizeof(T) == 4) ? 4 : 2;
   const bool many = items * P.batch * 2 > 2LL * 2048 * sm_count();
   if (!vec) return launch_rows_per<kRead, T, KV, false, 1>(P, stream);
   return many ? launch_rows_per<kRead, T, KV, true, kMany>(P, stream)

@@ -70,9 +70,9 @@ __device__ __forceinline__ void q4_scale(float m, float& d, float& id) {
 // The floor is the sum with 2^23 rounded down (its low bits): the rounding
 // and conversion instructions run at a quarter of the rate and would bound
 // the store.
-__device__ __forceinline__ uint32_t q4_nibble(float x, float id) {
+__device__ __forceinline__ uint32_t q4_bits(float x, float id) {  // n in the low byte
   const float t = __fadd_rn(__fmul_rn(x, id), 8.5f);
-  return __float_as_uint(__fadd_rd(fminf(fmaxf(t, 0.f), 15.5f), 8388608.f)) & 15u;
+  return __float_as_uint(__fadd_rd(fminf(fmaxf(t, 0.f), 15.5f), 8388608.f));
 }
 // Keeps of (m, o) the larger magnitude, on a tie the one of lower index.
 __device__ __forceinline__ float q4_larger(float m, float o, bool o_first) {
@@ -89,7 +89,7 @@ __device__ __forceinline__ void quantize_q4_warp(float x, uint8_t* quants, uint8
     m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, o), (lane & o) != 0);
   float d, id;
   q4_scale(m, d, id);
-  const uint32_t n = q4_nibble(x, id);
+  const uint32_t n = q4_bits(x, id) & 15u;
   const uint32_t hi = __shfl_down_sync(0xffffffffu, n, 16);
   if (lane < 16) quants[lane] = (uint8_t)(n | hi << 4);
   if (lane == 0) *reinterpret_cast<unsigned short*>(scale) = __half_as_ushort(__float2half_rn(d));
