@@ -150,7 +150,7 @@ __device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   if (!live) return;
   const float d = __fdiv_rn(amax, 127.0f);
-  const float id = d != 0.f ? __fdiv_rn(1.0f, d) : 0.f;
+  const float id = d != 0.f ? __frcp_rn(d) : 0.f;
   unsigned short* q = reinterpret_cast<unsigned short*>(blk + 2 + 8 * part);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -170,11 +170,27 @@ __device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f
 // and lane p ^ 2 exchange four nibbles each and write one word each.
 __device__ __forceinline__ void put_q4(uint8_t* quants, uint8_t* scale, int part,
                                        const float (&f)[kGroupE], bool live) {
-  float m = f[0];
+  // the largest magnitude among the positive and among the negative elements;
+  // only where they tie (a block of zeros, say) does the order decide
+  float hi = f[0], lo = f[0];
 #pragma unroll
-  for (int i = 1; i < kGroupE; ++i) m = q4_larger(m, f[i], false);
-  m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 1), (part & 1) != 0);
-  m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 2), (part & 2) != 0);
+  for (int i = 1; i < kGroupE; ++i) {
+    hi = fmaxf(hi, f[i]);
+    lo = fminf(lo, f[i]);
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  float m = hi > -lo ? hi : lo;
+  if (__any_sync(0xffffffffu, hi == -lo)) {
+    m = f[0];
+#pragma unroll
+    for (int i = 1; i < kGroupE; ++i) m = q4_larger(m, f[i], false);
+    m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 1), (part & 1) != 0);
+    m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 2), (part & 2) != 0);
+  }
   float d, id;
   q4_scale(m, d, id);
   uint32_t w[2];  // a byte an element
@@ -380,7 +396,7 @@ int launch_rows(KvRowsParams P, cudaStream_t stream) {
   // sequences of up to 2047 rows of 1024 f16, append 15.8 / 16.4 (with a
   // rounding of fewer instructions that was not roundf's for NaN), read 13.4 /
   // 14.0; 4 bits, 32768 rows of 1024 f32, append 67.8 / 59.1 (it holds 32 f32
-  // values a thread at four), read 27.1 / 27.0; f32 rows in 16-byte items,
+  // values a thread at four; 51 now), read 27.1 / 27.0; f32 rows in 16-byte items,
   // 16384 of 1024 from f16, read 30.3 / 33.8.
   constexpr int kMany = KV == Q8D_KV_Q8_0 || KV == Q8D_KV_F32 || (kRead && sizeof(T) == 4) ? 4 : 2;
   const bool many = items * P.batch * 2 > 2LL * 2048 * sm_count();

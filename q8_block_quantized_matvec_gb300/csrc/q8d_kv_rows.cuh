@@ -63,16 +63,16 @@ __host__ __device__ inline long long q4_scale_plane(int cap, int width) {
 // every element lies in [-8 d, 8 d].
 __device__ __forceinline__ void q4_scale(float m, float& d, float& id) {
   d = m * -0.125f;
-  id = __fdiv_rn(1.0f, d);
+  id = __frcp_rn(d);
   if (!isfinite(id)) id = 0.f;  // (an all-zero block, or 1 / d beyond f32: all nibbles 8)
 }
-// n = clamp(floor(x / d + 8.5), 0, 15) in single correctly rounded f32 steps.
-// The floor is the sum with 2^23 rounded down (its low bits): the rounding
-// and conversion instructions run at a quarter of the rate and would bound
-// the store.
+// n = min(floor(x / d + 8.5), 15) in single correctly rounded f32 steps (the
+// sum is never below 0.49).  The floor is the sum with 2^23 rounded down (its
+// low bits): the rounding and conversion instructions run at a quarter of the
+// rate and would bound the store.
 __device__ __forceinline__ uint32_t q4_bits(float x, float id) {  // n in the low byte
   const float t = __fadd_rn(__fmul_rn(x, id), 8.5f);
-  return __float_as_uint(__fadd_rd(fminf(fmaxf(t, 0.f), 15.5f), 8388608.f));
+  return __float_as_uint(__fadd_rd(fminf(t, 15.5f), 8388608.f));
 }
 // Keeps of (m, o) the larger magnitude, on a tie the one of lower index.
 __device__ __forceinline__ float q4_larger(float m, float o, bool o_first) {
