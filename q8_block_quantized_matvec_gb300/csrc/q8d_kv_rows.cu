@@ -3,19 +3,20 @@
 // caches.  The rows outside the cache are f32 or f16.
 //
 // Both directions move every byte once and do a handful of operations on
-// it, so HBM bounds them (and the launch does for a few rows).  A thread
-// takes eight consecutive elements: one or two 16-byte accesses outside the
-// cache, and four neighbouring threads make a packed block of 32, whose
-// largest element they find with two shuffles.  Large calls give a thread
-// several such groups, loaded before any is used, because a CTA that moves
-// 8 KB spends as long starting as working: 8 sequences of up to 2047 rows of
-// 1024, f16 and Q8_0, took 21.8 us to append and 18.9 to read with one group a
-// thread, 16.7 and 13.5 with four; 131071 rows of 512 out of 4 bits into f16
-// 57.6, now 51 (6.7 TB/s).  Staging the 34-byte blocks through shared memory, for whole
-// 16-byte lines on the cache's side, was slower than the 2-byte accesses (21.8
-// against 18.9 us to read): the lines are put together in L1 and L2 anyway.
-// grid.y runs over the sequences and grid.z over k and v, so a ragged batch's
-// unused threads are whole CTAs that leave at once.
+// it, so HBM bounds them (and the launch does for a few rows; storing packed
+// blocks, the conversions' instructions).  A thread that stores takes eight
+// consecutive elements (four into an f32 cache), one that reads 16 bytes of
+// the output; four neighbours make a packed block of 32, whose largest element
+// they find with two shuffles.  Large calls give a thread several such groups,
+// loaded before any is used, because a CTA that moves 8 KB spends as long
+// starting as working: 8 sequences of up to 2047 rows of 1024, f16 and Q8_0,
+// took 21.8 us to append and 18.9 to read with one group a thread, 16.4 and
+// 13.4 with four; 131071 rows of 512 out of 4 bits into f16 57.6, now 51 (6.7
+// TB/s).  Staging the 34-byte blocks through shared memory, for whole 16-byte
+// lines on the cache's side, was slower than the 2-byte accesses (21.8 against
+// 18.9 us to read): the lines are put together in L1 and L2 anyway.  grid.y
+// runs over the sequences and grid.z over k and v, so a ragged batch's unused
+// threads are whole CTAs that leave at once.
 #include <algorithm>
 
 #include "q8d_attn.cuh"
