@@ -275,3 +275,14 @@ def test_many_experts_a_block(q8d, hidden, ffn, m, E, k):
     """More items than buffers in every CTA."""
     L = layer(hidden + ffn, E, hidden, ffn)
     check(q8d, L, synth.normal_f32(m, "many.x", (m, hidden)), E, hidden, ffn, k, False)
+
+
+@pytest.mark.parametrize("hidden,ffn,m,E,k", [
+    (16384, 32, 3, 2, 1), (32, 16384, 3, 2, 2), (16384, 64, 64, 2, 2), (16352, 32, 20, 2, 1), (32, 16352, 20, 2, 2),
+    (64, 32, 64, 32, 32), (96, 64, 64, 33, 32), (256, 128, 64, 1, 1),
+])
+def test_largest_sizes(q8d, hidden, ffn, m, E, k):
+    """The longest rows, whole and off 16-byte lines; every token asking every
+    expert."""
+    L = layer(hidden + ffn, E, hidden, ffn)
+    check(q8d, L, synth.normal_f32(m, "largest.x", (m, hidden)), E, hidden, ffn, k, True)
