@@ -83,9 +83,11 @@ __device__ __forceinline__ float q4_larger(float m, float o, bool o_first) {
 // Stores one 32-element block held by a warp (lane j: element j): byte i is
 // element i in its low half and element i + 16 in its high half.
 __device__ __forceinline__ void quantize_q4_warp(float x, uint8_t* quants, uint8_t* scale, int lane) {
+  // (distances upwards: at each step a lane stands for `o` neighbouring
+  // elements, all before or all behind those of the lane it asks)
   float m = x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = 1; o < 32; o <<= 1)
     m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, o), (lane & o) != 0);
   float d, id;
   q4_scale(m, d, id);
