@@ -252,6 +252,10 @@ size_t q8d_gqa_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_
  * a multiple of 256, so that sequences start on 16-byte boundaries);
  * for a 4-bit cache batch * (cap / 32 + 17) below 2^30 (with run maps 4 cap),
  * else Q8D_EUNSUPPORTED.
+ * Over a 4-bit cache a score is off by at most 2^-21 of scale * sum_i
+ * max(|q_i|, 2^-18 max |q|) |K_i|, in natural units, and given the scores an
+ * output by 1e-5 of sum_t p_t |V_t|, however far apart the p_t and V's scales
+ * lie (weights below 2^-126 of the largest are 0).
  * ---------------------------------------------------------------------- */
 int q8d_gqa_decode_attn(const float* q, const float* k_new, const float* v_new, void* kcache,
                         void* vcache, int kv_dtype, float* out, int batch, int n_heads,

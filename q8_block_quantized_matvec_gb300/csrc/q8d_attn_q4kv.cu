@@ -4,9 +4,9 @@
 // At 9/16 byte an element the arithmetic, not HBM, is what such a kernel runs
 // out of first: at the copy rate an SM gets one token of one KV head (144
 // bytes at head_dim 128) every 6 cycles, 780 issue slots for a tile of 32
-// tokens; the tile takes 740 warp instructions with up to four heads a KV
-// head, 920 with five to eight, 288 of them to unpack its quants, and sixteen
-// warps an SM (128 registers each) fill 55 to 60 percent of the slots.  So
+// tokens; the tile takes 790 warp instructions with up to four heads a KV
+// head, 990 with five to eight, 320 of them to unpack its quants, and sixteen
+// warps an SM (128 registers each) fill 53 to 58 percent of the slots.  So
 // the layout saves instructions:
 //  * A half-byte n put under the exponent of 1024 is the f16 1024 + n (1024 +
 //    16 n for the upper one): one LOP3 a pair, and one sub.f16x2 leaves the
@@ -15,22 +15,29 @@
 //    the operands' exponent fields, and a subnormal's loses it 7 bits.)
 //  * Rows of A are what the cache holds (16 tokens for K.Q^T, 16 dims for
 //    V.P^T) and columns of B the heads, so the few heads of a KV head fill
-//    the short side.  q, and P times V's scale, are f16 hi + lo parts: results
-//    keep f32's accuracy.  With at most four heads a KV head, hi and lo are
-//    neighbouring columns and one MMA does both; else each takes its own.
+//    the short side.  q is f16 hi + lo parts.  With at most four heads a KV
+//    head, parts are neighbouring columns and one MMA does two; else each takes
+//    its own.
 //    (Heads as rows of A, hi and lo in rows g and g + 8, took 920
-//    instructions a tile with two heads: 62 us for 32 sequences of up to 8192
-//    tokens, 16 query and 8 KV heads of 128, against 45 now.)
+//    instructions a tile with two heads, against 740 so, P in two parts both
+//    times: 62 and 45 us for 32 sequences of up to 8192 tokens, 16 query and 8
+//    KV heads of 128.)
 //  * A lane's scores are tokens g, g + 8, .. of heads 2c, 2c + 1 (packed: of
 //    head c), so a token's scale and a head's factors are loaded or kept
 //    once.  V's scale depends on the token and the block, so it multiplies P
-//    once per block before the hi + lo split; movmatrix turns the halves into
-//    the B operand; ldmatrix.trans hands a lane the same two bytes of V of
-//    tokens 2c and 2c + 1.
-//  * P * scale * 2^fe stays inside f16: fe follows the largest V scale seen
-//    (a power of two, so changing it is exact).  Both fe and the running
-//    maximum move only when they must (the maximum when a score exceeds it
-//    by 2^8), so an ordinary tile does no reduction across lanes.
+//    once per block before the split; movmatrix turns the parts into the B
+//    operand; ldmatrix.trans hands a lane the same two bytes of V of tokens 2c
+//    and 2c + 1.
+//  * P times V's scale is three bf16 parts, exactly the f32 product, and the
+//    quants are bf16 (n under the exponent of 128).  Its terms may lie far
+//    apart within a head: the token that takes the softmax may have no V, one
+//    block's scales lie far above another's.  f16 hi + lo under one power of two
+//    a warp (a third fewer MMAs, upper half-bytes without their shift: 42.0 us
+//    for that batch, 46.3 so; 29.4 and 32.6 for 8 sequences of up to 32768, 28
+//    and 4 heads) is off by 2^-32 of the largest P times the largest scale, and
+//    outputs made of terms 2^-15 below that leave f32's accuracy.
+//  * The running maximum moves only when a score exceeds it by 2^8, so an
+//    ordinary tile does no reduction across lanes.
 //  * Eight warps, each with its own softmax over 32-token tiles and its own
 //    two-stage cp.async ring (16-byte chunks, XOR-swizzled for ldmatrix),
 //    merge once; partials are combined as in the other kernels.  Short caches
@@ -57,12 +64,11 @@ constexpr int kSeqCost4 = 16;     // a sequence's fixed work, in tiles
 // Caches of up to this many rows: sequences are not cut, so the attention
 // kernel writes the outputs itself and there is no second launch.  Graph /
 // single call, us, cut and combined against whole: 28 / 4 heads of 128, 256
-// rows, 5.8 / 8.9 against 4.9 / 6.7; 512 rows, 7.0 / 8.7 against 6.6 / 6.9; 1024
-// rows, 6.0 / 9.1 against 9.9 / 10.2; 32 ragged sequences of 16 / 8 heads, 512
-// rows, 12.7 / 13.0 against 10.8 / 11.0; 1024 rows, 15.4 / 15.7 against 16.4 /
-// 16.7.
+// rows, 6.0 / 8.8 against 4.8 / 6.4; 512 rows, 6.1 / 8.7 against 6.7 / 6.9; 1024
+// rows, 6.2 / 8.8 against 10.1 / 10.2; 32 ragged sequences of 16 / 8 heads, 512
+// rows, 13.0 / 13.5 against 10.8 / 11.2; 1024 rows, 16.2 / 16.6 against 17.2 /
+// 17.5.
 constexpr int kWholeCap4 = 512;
-constexpr int kFe0 = 7;           // P <= 2^8, |scale| < 2^ev, 2^fe = 2^(7 - ev): products < 2^15
 
 template <int D, int NH>
 struct Cfg4 {
@@ -119,18 +125,21 @@ __device__ __forceinline__ void mma4z(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// The same with bf16 operands.
+__device__ __forceinline__ void mma4b(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                      uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 // 2^x to two units in the last place; results below 2^-126 are 0 (a weight
 // that small next to 1 is beyond every sum's accuracy).
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// The larger magnitudes of two f16 pairs (signs mixed).
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 // The NB halves of a token's scales.
 template <int NB>
@@ -163,12 +172,34 @@ __device__ __forceinline__ uint32_t nib8(uint32_t w, uint32_t k1024) {
   asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(kHi ? 0x64806480u : 0x64086408u));
   return r;
 }
-__device__ __forceinline__ float2 h2f(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+// n - 8 of the low half-bytes n of bytes 0 and 2 of w as an exact bf16 pair
+// (under the exponent of 128: 128 + n).
+__device__ __forceinline__ uint32_t nib8b(uint32_t w, uint32_t k128) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "n"(0x000f000f), "r"(k128));
+  uint32_t r;
+  asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
+  return r;
 }
-__device__ __forceinline__ uint32_t f2h(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// A pair of f32 values as three bf16 each, which add up to it exactly: a bf16
+// is the upper half of an f32, eight leading bits.  hi and mid hold the value
+// and what its upper half leaves; their upper halves are the parts.
+struct Parts3 {
+  float hi[2], mid[2], lo[2];
+  __device__ __forceinline__ explicit Parts3(uint64_t a) {
+    unpack2(a, hi[0], hi[1]);
+    const uint64_t m = add2(a, upper_neg(hi));
+    unpack2(m, mid[0], mid[1]);
+    unpack2(add2(m, upper_neg(mid)), lo[0], lo[1]);
+  }
+  static __device__ __forceinline__ uint64_t upper_neg(const float (&v)[2]) {  // (one LOP3 each)
+    return pack2(__uint_as_float((__float_as_uint(v[0]) & 0xffff0000u) ^ 0x80000000u),
+                 __uint_as_float((__float_as_uint(v[1]) & 0xffff0000u) ^ 0x80000000u));
+  }
+};
+// The upper halves of a and b.
+__device__ __forceinline__ uint32_t upper2(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 
 // ---- the split ----
@@ -179,8 +210,8 @@ __device__ __forceinline__ uint32_t f2h(float a, float b) {
 // in front of its rows.  The lengths live in device memory, so every CTA and
 // the combine derive the same cut from them.  (Chunks of one sequence each,
 // four a sequence on average and 3.4 waves: 62 us in the case above, 54 so
-// with the same tile; kSeqCost4 of 6, 12, 16, 28: 45.9, 44.9, 45.2, 45.9 us
-// there and 31.2, 30.5, 29.8, 30.4 for 8 sequences of up to 32768, 28 query
+// with the same tile; kSeqCost4 of 6, 12, 16, 28: 46.9, 46.2, 46.3, 47.9 us
+// there and 33.8, 33.0, 32.6, 33.3 for 8 sequences of up to 32768, 28 query
 // and 4 KV heads.)
 __device__ __forceinline__ int window_len4(const AttnParams& P, int b) {
   if (!P.d_runs) {
@@ -340,6 +371,8 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
   const uint32_t ld_dst = ld_r * C::kRow + ((ld_c ^ ((ld_r >> kSwz) & (kCh - 1))) << 4);
   uint32_t k1024;  // (1024, 1024), kept out of the compiler's sight as a constant
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
+  uint32_t k128;  // (128, 128) in bf16, as well
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(k128));
   // ldmatrix row addresses.  K (x4): 8 tokens, blocks 0-3 (head_dim 64: 8
   // tokens each of two groups, blocks 0-1); V (x4, transposed): tokens 0-7
   // and 8-15 of block 2 i, then of block 2 i + 1.
@@ -480,19 +513,18 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
     // o[u][2 blk + half]: dims 32 blk + 16 half + 2 gq + {0 ([0], [1]), 1 ([2], [3])}, columns 2cq, 2cq+1
     float o[NH][2 * NB][4];
     // this lane's heads: the running maximum m (log2), the raw score that
-    // moves it, m - fe, and this lane's sum of 2^fe P
-    float m[NH][HC], top[NH][HC], mf[NH][HC], l[NH][HC];
+    // moves it, and this lane's sum of P
+    float m[NH][HC], top[NH][HC], l[NH][HC];
 #pragma unroll
     for (int u = 0; u < NH; ++u) {
 #pragma unroll
       for (int x = 0; x < HC; ++x) {
         m[u][x] = top[u][x] = -INFINITY;
-        mf[u][x] = l[u][x] = 0.f;
+        l[u][x] = 0.f;
       }
 #pragma unroll
       for (int t = 0; t < 2 * NB; ++t) o[u][t][0] = o[u][t][1] = o[u][t][2] = o[u][t][3] = 0.f;
     }
-    int lim = -1;       // exponent field of the largest V scale allowed for (-1: none yet)
 
     for (int i = 0; i < my_tiles; ++i) {
       load_tile(i + kStages4 - 1);
@@ -582,26 +614,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
           above = above || mx[u][x] > top[u][x];
         }
       }
-      // the V scales of this lane's tokens and their largest exponent
-      uint32_t vsc[NT][NB / 2];
-      uint32_t vm = 0u;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        scales4<NB>(sc + C::kScales + j * 8 * C::kSRow, vsc[j]);
-#pragma unroll
-        for (int t = 0; t < NB / 2; ++t) vm = max_abs2(vm, vsc[j][t]);
-      }
-      vm &= 0x7fff7fffu;
-      int ve = (int)(max(vm & 0xffffu, vm >> 16) >> 10);
-      if (__any_sync(0xffffffffu, above || ve > lim)) {  // (rare after the first tiles)
-#pragma unroll
-        for (int of = 1; of < 32; of <<= 1) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, of));
-        float r = 1.f;
-        if (ve > lim) {  // 2^fe for |scale| < 2^(field - 14)
-          r = lim < 0 ? 0.f : __int_as_float((127 + max(lim, 1) - max(ve, 1)) << 23);
-          lim = ve;
-        }
-        const float fe = (float)(kFe0 + 14 - max(lim, 1));
+      if (__any_sync(0xffffffffu, above)) {  // (rare after the first tiles)
 #pragma unroll
         for (int u = 0; u < NH; ++u) {
           float cr[HC];
@@ -611,9 +624,8 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 #pragma unroll
             for (int of = 4; of < 32; of <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, of));
             const float mn = fmaxf(m[u][x], z * fac[u][x]);
-            cr[x] = m[u][x] == -INFINITY ? 0.f : ex2(m[u][x] - mn) * r;
+            cr[x] = m[u][x] == -INFINITY ? 0.f : ex2(m[u][x] - mn);
             m[u][x] = mn;
-            mf[u][x] = mn - fe;
             // (fac is a power of two: its inverse, exactly)
             top[u][x] = (mn + kSlack4) * __uint_as_float(0x7f000000u - __float_as_uint(fac[u][x]));
             l[u][x] *= cr[x];
@@ -628,10 +640,13 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         }
       }
 
-      // ---- 2^fe P, then O += (2^fe P * scale) . V per block ----
+      // ---- P, then O += (P * scale) . V per block ----
 #pragma unroll
       for (int h = 0; h < NT / 2; ++h) {  // 16 tokens
         if (h * 16 >= nr) break;
+        uint32_t vsc[2][NB / 2];  // V's scales of tokens gq and gq + 8
+        scales4<NB>(sc + C::kScales + 2 * h * 8 * C::kSRow, vsc[0]);
+        scales4<NB>(sc + C::kScales + (2 * h + 1) * 8 * C::kSRow, vsc[1]);
         float p[NH][2][HC];
 #pragma unroll
         for (int u = 0; u < NH; ++u)
@@ -639,7 +654,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int x = 0; x < HC; ++x) {
-              p[u][y][x] = ex2(fmaf(s[u][2 * h + y][x], fac[u][x], -mf[u][x]));
+              p[u][y][x] = ex2(fmaf(s[u][2 * h + y][x], fac[u][x], -m[u][x]));
               l[u][x] += p[u][y][x];
             }
 #pragma unroll
@@ -649,36 +664,41 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int bb = 2 * bp + x;
-            const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1], w0s = w0 >> 8, w1s = w1 >> 8;
-            const uint32_t l0 = nib8<false>(w0, k1024), l1 = nib8<false>(w0s, k1024), l2 = nib8<false>(w1, k1024),
-                           l3 = nib8<false>(w1s, k1024);
-            const uint32_t u0 = nib8<true>(w0, k1024), u1 = nib8<true>(w0s, k1024), u2 = nib8<true>(w1, k1024),
-                           u3 = nib8<true>(w1s, k1024);
-            const float d0 = half_of(vsc[2 * h][bp], x), d1 = half_of(vsc[2 * h + 1][bp], x);
+            const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1];
+            const uint32_t l0 = nib8b(w0, k128), l1 = nib8b(w0 >> 8, k128), l2 = nib8b(w1, k128),
+                           l3 = nib8b(w1 >> 8, k128);
+            const uint32_t u0 = nib8b(w0 >> 4, k128), u1 = nib8b(w0 >> 12, k128), u2 = nib8b(w1 >> 4, k128),
+                           u3 = nib8b(w1 >> 12, k128);
+            const float d0 = half_of(vsc[0][bp], x), d1 = half_of(vsc[1][bp], x);
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
               // tokens gq and gq + 8 of the columns 2cq, 2cq+1, transposed into
               // B fragments
-              if constexpr (kPack) {
-                const float a0 = p[u][0][0] * d0, a1 = p[u][1][0] * d1;
-                const float2 hi = h2f(f2h(a0, a1));
-                const uint32_t b0 = transpose8(f2h(a0, a0 - hi.x)), b1 = transpose8(f2h(a1, a1 - hi.y));
-                mma4(o[u][2 * bb], l0, l1, l2, l3, b0, b1);
-                mma4(o[u][2 * bb + 1], u0, u1, u2, u3, b0, b1);
+              float(&lo)[4] = o[u][2 * bb], (&up)[4] = o[u][2 * bb + 1];
+              if constexpr (kPack) {  // columns (hi, mid), then (0, lo)
+                const Parts3 a(mul2(pack2(p[u][0][0], p[u][1][0]), pack2(d0, d1)));
+                const uint32_t b0 = transpose8(upper2(a.hi[0], a.mid[0])), b1 = transpose8(upper2(a.hi[1], a.mid[1]));
+                mma4b(lo, l0, l1, l2, l3, b0, b1);
+                mma4b(up, u0, u1, u2, u3, b0, b1);
+                const uint32_t c0 = transpose8(__float_as_uint(a.lo[0]) & 0xffff0000u),
+                               c1 = transpose8(__float_as_uint(a.lo[1]) & 0xffff0000u);
+                mma4b(lo, l0, l1, l2, l3, c0, c1);
+                mma4b(up, u0, u1, u2, u3, c0, c1);
               } else {
-                uint32_t ph[2], pl[2];
+                uint32_t b[3][2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const float d = y ? d1 : d0, a0 = p[u][y][0] * d, a1 = p[u][y][HC - 1] * d;
-                  ph[y] = f2h(a0, a1);
-                  const float2 hi = h2f(ph[y]);
-                  pl[y] = transpose8(f2h(a0 - hi.x, a1 - hi.y));
-                  ph[y] = transpose8(ph[y]);
+                  const float d = y ? d1 : d0;
+                  const Parts3 a(mul2(pack2(p[u][y][0], p[u][y][HC - 1]), pack2(d, d)));
+                  b[0][y] = transpose8(upper2(a.hi[0], a.hi[1]));
+                  b[1][y] = transpose8(upper2(a.mid[0], a.mid[1]));
+                  b[2][y] = transpose8(upper2(a.lo[0], a.lo[1]));
                 }
-                mma4(o[u][2 * bb], l0, l1, l2, l3, ph[0], ph[1]);
-                mma4(o[u][2 * bb + 1], u0, u1, u2, u3, ph[0], ph[1]);
-                mma4(o[u][2 * bb], l0, l1, l2, l3, pl[0], pl[1]);
-                mma4(o[u][2 * bb + 1], u0, u1, u2, u3, pl[0], pl[1]);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                  mma4b(lo, l0, l1, l2, l3, b[i][0], b[i][1]);
+                  mma4b(up, u0, u1, u2, u3, b[i][0], b[i][1]);
+                }
               }
             }
           }
@@ -693,13 +713,12 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
     float* mm = reinterpret_cast<float*>(smem);
     float* ll = mm + kWarps4 * kHeads;
     float* oo = ll + kWarps4 * kHeads;
-    const float inv_f = lim < 0 ? 0.f : __int_as_float((127 - kFe0 - 14 + max(lim, 1)) << 23);  // 2^-fe
 #pragma unroll
     for (int u = 0; u < NH; ++u) {
 #pragma unroll
       for (int x = 0; x < HC; ++x) {
         const int row = warp * kHeads + 8 * u + HC * cq + x;
-        float sum = l[u][x] * inv_f;
+        float sum = l[u][x];
 #pragma unroll
         for (int of = 4; of < 32; of <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, of);
         if (gq == 0) {
@@ -708,10 +727,9 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         }
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
-          const float f = (t & 1 ? 0.0625f : 1.f) * inv_f;  // (upper half-bytes count 16-fold)
           const float* v = o[u][t];
           *reinterpret_cast<float2*>(oo + row * C::kOStride + 16 * t + 2 * gq) =
-              kPack ? make_float2((v[0] + v[1]) * f, (v[2] + v[3]) * f) : make_float2(v[x] * f, v[2 + x] * f);
+              kPack ? make_float2(v[0] + v[1], v[2] + v[3]) : make_float2(v[x], v[2 + x]);
         }
       }
     }
@@ -860,9 +878,9 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
 // The same by a warp a (sequence, query head), lanes holding D/32 dims, for
 // many heads, which as blocks of their own would take several waves.  The
 // whole call, blocks / warps: 32 ragged sequences of 16 heads up to 8192 rows,
-// 44.5 / 41.5 us; 20 of 32 heads up to 1000 rows, 18.1 / 14.5.  With many
+// 48.9 / 46.3 us; 20 of 32 heads up to 1000 rows, 19.0 / 15.6.  With many
 // chunks and few heads its loads are too few at a time: 8 ragged of 28 heads
-// up to 32768 rows, 29.4 / 34.6; 6 of 24 heads, 2000 rows, 9.0 / 12.7.
+// up to 32768 rows, 32.7 / 36.9; 6 of 24 heads, 2000 rows, 9.4 / 13.2.
 constexpr int kFewThreads4 = 256;
 
 template <int D>
