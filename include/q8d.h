@@ -255,7 +255,8 @@ size_t q8d_gqa_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_
  * Over a 4-bit cache a score is off by at most 2^-21 of scale * sum_i
  * max(|q_i|, 2^-18 max |q|) |K_i|, in natural units, and given the scores an
  * output by 1e-5 of sum_t p_t |V_t|, however far apart the p_t and V's scales
- * lie (weights below 2^-126 of the largest are 0).
+ * lie (weights below 2^-126 of the largest are 0), for up to 2^20 rows a
+ * sequence.
  * ---------------------------------------------------------------------- */
 int q8d_gqa_decode_attn(const float* q, const float* k_new, const float* v_new, void* kcache,
                         void* vcache, int kv_dtype, float* out, int batch, int n_heads,

@@ -4,9 +4,9 @@
 // At 9/16 byte an element the arithmetic, not HBM, is what such a kernel runs
 // out of first: at the copy rate an SM gets one token of one KV head (144
 // bytes at head_dim 128) every 6 cycles, 780 issue slots for a tile of 32
-// tokens; the tile takes 790 warp instructions with up to four heads a KV
-// head, 990 with five to eight, 320 of them to unpack its quants, and sixteen
-// warps an SM (128 registers each) fill 53 to 58 percent of the slots.  So
+// tokens; the tile takes 800 warp instructions with up to four heads a KV
+// head, 1000 with five to eight, 320 of them to unpack its quants, and sixteen
+// warps an SM (128 registers each) fill 51 to 58 percent of the slots.  So
 // the layout saves instructions:
 //  * A half-byte n put under the exponent of 1024 is the f16 1024 + n (1024 +
 //    16 n for the upper one): one LOP3 a pair, and one sub.f16x2 leaves the
@@ -36,6 +36,12 @@
 //    for that batch, 46.3 so; 29.4 and 32.6 for 8 sequences of up to 32768, 28
 //    and 4 heads) is off by 2^-32 of the largest P times the largest scale, and
 //    outputs made of terms 2^-15 below that leave f32's accuracy.
+//  * A tile's products are summed from zero and added to O with rounded f32
+//    additions.  The tensor core cuts its running sums off, always towards zero:
+//    over 16384 rows a warp of V of one sign, 3 to 5e-5 of the output, 4e-7 so
+//    (46.3 and 32.6 us for the batches above with O as the accumulators, 47.4 and
+//    33.3 so).  For the same reason lo stands beside mid: added to hi, it would
+//    be a small remainder of one sign that every rounding drops.
 //  * The running maximum moves only when a score exceeds it by 2^8, so an
 //    ordinary tile does no reduction across lanes.
 //  * Eight warps, each with its own softmax over 32-token tiles and its own
@@ -64,10 +70,10 @@ constexpr int kSeqCost4 = 16;     // a sequence's fixed work, in tiles
 // Caches of up to this many rows: sequences are not cut, so the attention
 // kernel writes the outputs itself and there is no second launch.  Graph /
 // single call, us, cut and combined against whole: 28 / 4 heads of 128, 256
-// rows, 6.0 / 8.8 against 4.8 / 6.4; 512 rows, 6.1 / 8.7 against 6.7 / 6.9; 1024
-// rows, 6.2 / 8.8 against 10.1 / 10.2; 32 ragged sequences of 16 / 8 heads, 512
-// rows, 13.0 / 13.5 against 10.8 / 11.2; 1024 rows, 16.2 / 16.6 against 17.2 /
-// 17.5.
+// rows, 6.1 / 8.6 against 4.9 / 6.6; 512 rows, 6.1 / 8.4 against 6.9 / 7.0; 1024
+// rows, 6.2 / 8.4 against 10.5 / 10.7; 32 ragged sequences of 16 / 8 heads, 512
+// rows, 13.2 / 13.6 against 11.2 / 11.5; 1024 rows, 16.3 / 16.7 against 17.4 /
+// 17.9.
 constexpr int kWholeCap4 = 512;
 
 template <int D, int NH>
@@ -133,6 +139,20 @@ __device__ __forceinline__ void mma4b(float (&d)[4], uint32_t a0, uint32_t a1, u
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma4bz(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// d += v, rounded.
+__device__ __forceinline__ void add4(float (&d)[4], const float (&v)[4]) {
+  unpack2(add2(pack2(d[0], d[1]), pack2(v[0], v[1])), d[0], d[1]);
+  unpack2(add2(pack2(d[2], d[3]), pack2(v[2], v[3])), d[2], d[3]);
 }
 // 2^x to two units in the last place; results below 2^-126 are 0 (a weight
 // that small next to 1 is beyond every sum's accuracy).
@@ -210,8 +230,8 @@ __device__ __forceinline__ uint32_t upper2(float a, float b) {
 // in front of its rows.  The lengths live in device memory, so every CTA and
 // the combine derive the same cut from them.  (Chunks of one sequence each,
 // four a sequence on average and 3.4 waves: 62 us in the case above, 54 so
-// with the same tile; kSeqCost4 of 6, 12, 16, 28: 46.9, 46.2, 46.3, 47.9 us
-// there and 33.8, 33.0, 32.6, 33.3 for 8 sequences of up to 32768, 28 query
+// with the same tile; kSeqCost4 of 6, 12, 16, 28: 47.7, 47.1, 47.4, 49.3 us
+// there and 34.4, 33.5, 33.3, 34.0 for 8 sequences of up to 32768, 28 query
 // and 4 KV heads.)
 __device__ __forceinline__ int window_len4(const AttnParams& P, int b) {
   if (!P.d_runs) {
@@ -640,67 +660,82 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
         }
       }
 
-      // ---- P, then O += (P * scale) . V per block ----
+      // ---- P, then O += (P * scale) . V per block; a block's products of the
+      // tile from zero ----
+      float p[NT / 2][NH][2][HC];
 #pragma unroll
-      for (int h = 0; h < NT / 2; ++h) {  // 16 tokens
-        if (h * 16 >= nr) break;
-        uint32_t vsc[2][NB / 2];  // V's scales of tokens gq and gq + 8
-        scales4<NB>(sc + C::kScales + 2 * h * 8 * C::kSRow, vsc[0]);
-        scales4<NB>(sc + C::kScales + (2 * h + 1) * 8 * C::kSRow, vsc[1]);
-        float p[NH][2][HC];
+      for (int h = 0; h < NT / 2; ++h)
 #pragma unroll
         for (int u = 0; u < NH; ++u)
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int x = 0; x < HC; ++x) {
-              p[u][y][x] = ex2(fmaf(s[u][2 * h + y][x], fac[u][x], -m[u][x]));
-              l[u][x] += p[u][y][x];
-            }
+            for (int x = 0; x < HC; ++x)
+              p[h][u][y][x] = ex2(fmaf(s[u][2 * h + y][x], fac[u][x], -m[u][x]));
 #pragma unroll
-        for (int bp = 0; bp < NB / 2; ++bp) {
-          uint32_t vw[4];
-          ldsm4t(st + v_off[bp] + h * 16 * C::kRow, vw);
+      for (int u = 0; u < NH; ++u)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int bb = 2 * bp + x;
-            const uint32_t w0 = vw[2 * x], w1 = vw[2 * x + 1];
+        for (int x = 0; x < HC; ++x) l[u][x] += (p[0][u][0][x] + p[0][u][1][x]) + (p[1][u][0][x] + p[1][u][1][x]);
+      static_assert(NT == 4, "");
+#pragma unroll
+      for (int bp = 0; bp < NB / 2; ++bp) {
+        uint32_t vw[NT / 2][4], vsc[NT];  // 16 tokens' words each; the scales of tokens gq, gq + 8, ..
+#pragma unroll
+        for (int h = 0; h < NT / 2; ++h) ldsm4t(st + v_off[bp] + h * 16 * C::kRow, vw[h]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          vsc[j] = *reinterpret_cast<const uint32_t*>(sc + C::kScales + j * 8 * C::kSRow + 4 * bp);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int bb = 2 * bp + x;
+          float lo[NH][4], up[NH][4];
+#pragma unroll
+          for (int h = 0; h < NT / 2; ++h) {
+            const uint32_t w0 = vw[h][2 * x], w1 = vw[h][2 * x + 1];
             const uint32_t l0 = nib8b(w0, k128), l1 = nib8b(w0 >> 8, k128), l2 = nib8b(w1, k128),
                            l3 = nib8b(w1 >> 8, k128);
             const uint32_t u0 = nib8b(w0 >> 4, k128), u1 = nib8b(w0 >> 12, k128), u2 = nib8b(w1 >> 4, k128),
                            u3 = nib8b(w1 >> 12, k128);
-            const float d0 = half_of(vsc[0][bp], x), d1 = half_of(vsc[1][bp], x);
+            const float d0 = half_of(vsc[2 * h], x), d1 = half_of(vsc[2 * h + 1], x);
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
               // tokens gq and gq + 8 of the columns 2cq, 2cq+1, transposed into
               // B fragments
-              float(&lo)[4] = o[u][2 * bb], (&up)[4] = o[u][2 * bb + 1];
+              const float(&ph)[2][HC] = p[h][u];
+              uint32_t b[3][2];
               if constexpr (kPack) {  // columns (hi, mid), then (0, lo)
-                const Parts3 a(mul2(pack2(p[u][0][0], p[u][1][0]), pack2(d0, d1)));
-                const uint32_t b0 = transpose8(upper2(a.hi[0], a.mid[0])), b1 = transpose8(upper2(a.hi[1], a.mid[1]));
-                mma4b(lo, l0, l1, l2, l3, b0, b1);
-                mma4b(up, u0, u1, u2, u3, b0, b1);
-                const uint32_t c0 = transpose8(__float_as_uint(a.lo[0]) & 0xffff0000u),
-                               c1 = transpose8(__float_as_uint(a.lo[1]) & 0xffff0000u);
-                mma4b(lo, l0, l1, l2, l3, c0, c1);
-                mma4b(up, u0, u1, u2, u3, c0, c1);
+                const Parts3 a(mul2(pack2(ph[0][0], ph[1][0]), pack2(d0, d1)));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  b[0][y] = transpose8(upper2(a.hi[y], a.mid[y]));
+                  b[1][y] = transpose8(__float_as_uint(a.lo[y]) & 0xffff0000u);
+                }
               } else {
-                uint32_t b[3][2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const float d = y ? d1 : d0;
-                  const Parts3 a(mul2(pack2(p[u][y][0], p[u][y][HC - 1]), pack2(d, d)));
+                  const Parts3 a(mul2(pack2(ph[y][0], ph[y][HC - 1]), pack2(d, d)));
                   b[0][y] = transpose8(upper2(a.hi[0], a.hi[1]));
                   b[1][y] = transpose8(upper2(a.mid[0], a.mid[1]));
                   b[2][y] = transpose8(upper2(a.lo[0], a.lo[1]));
                 }
+              }
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                  mma4b(lo, l0, l1, l2, l3, b[i][0], b[i][1]);
-                  mma4b(up, u0, u1, u2, u3, b[i][0], b[i][1]);
+              for (int i = 0; i < (kPack ? 2 : 3); ++i) {
+                if (h == 0 && i == 0) {
+                  mma4bz(lo[u], l0, l1, l2, l3, b[i][0], b[i][1]);
+                  mma4bz(up[u], u0, u1, u2, u3, b[i][0], b[i][1]);
+                } else {
+                  mma4b(lo[u], l0, l1, l2, l3, b[i][0], b[i][1]);
+                  mma4b(up[u], u0, u1, u2, u3, b[i][0], b[i][1]);
                 }
               }
             }
+          }
+#pragma unroll
+          for (int u = 0; u < NH; ++u) {
+            add4(o[u][2 * bb], lo[u]);
+            add4(o[u][2 * bb + 1], up[u]);
           }
         }
       }
@@ -878,9 +913,9 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
 // The same by a warp a (sequence, query head), lanes holding D/32 dims, for
 // many heads, which as blocks of their own would take several waves.  The
 // whole call, blocks / warps: 32 ragged sequences of 16 heads up to 8192 rows,
-// 48.9 / 46.3 us; 20 of 32 heads up to 1000 rows, 19.0 / 15.6.  With many
+// 50.0 / 47.4 us; 20 of 32 heads up to 1000 rows, 19.2 / 15.8.  With many
 // chunks and few heads its loads are too few at a time: 8 ragged of 28 heads
-// up to 32768 rows, 32.7 / 36.9; 6 of 24 heads, 2000 rows, 9.4 / 13.2.
+// up to 32768 rows, 33.3 / 37.9; 6 of 24 heads, 2000 rows, 9.4 / 13.5.
 constexpr int kFewThreads4 = 256;
 
 template <int D>
