@@ -276,9 +276,10 @@ __device__ __forceinline__ Split4 split4(const AttnParams& P, int lane) {
   S.bad = __any_sync(0xffffffffu, bad);
   S.total = sum;
   S.piece = max(kMinChunk / kTile4, (sum + P.nct - 1) / P.nct);
-  // a sequence's pieces fit its slots: with rows that start anywhere in a
-  // piece, k pieces' length touches k + 1
-  if (!kWhole && P.nc > 1) S.piece = max(S.piece, (most + P.nc - 2) / (P.nc - 1));
+  // a sequence's pieces fit its slots (two or more: batches of caches that are
+  // cut have them): with rows that start anywhere in a piece, k pieces' length
+  // touches k + 1
+  if (!kWhole) S.piece = max(S.piece, (most + P.nc - 2) / (P.nc - 1));
   return S;
 }
 
@@ -821,14 +822,13 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
 // so it asks for everything at once: the lengths before it waits for the
 // partials, then D/4 lanes a chunk keep up to kMine4 16-byte pieces of O in
 // flight while the first threads fetch m and l and work out the weights.
-constexpr int kCombThreads4 = 512;
-constexpr int kMine4 = 5;  // chunks a thread, per pass
-constexpr int kPass4 = 512;  // chunks a pass at most (weights in shared memory)
+constexpr int kCombThreads4 = 512;  // and chunks at most: a thread has one's m and l
+constexpr int kMine4 = 5;  // chunks a thread, at a time
 
 template <int D>
 __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const AttnParams P) {
   constexpr int kLanes = D / 4, kGroups = kCombThreads4 / kLanes;
-  __shared__ float wt[kPass4], red[2][kCombThreads4 / 32];
+  __shared__ float wt[kCombThreads4], red[2][kCombThreads4 / 32];
   __shared__ float4 so[kGroups][kLanes];
   const int hq = blockIdx.x, b = hq / P.n_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -850,55 +850,45 @@ __global__ void __launch_bounds__(kCombThreads4) gqa_q4kv_combine_kernel(const A
     return;
   }
   const float* O = P.ws_o + (long long)hq * P.nc * D;
+  float4 v[kMine4];
+#pragma unroll
+  for (int u = 0; u < kMine4; ++u) {
+    const int c = grp + u * kGroups;
+    v[u] = c < nact ? __ldcg(reinterpret_cast<const float4*>(O + (long long)c * D) + j)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const float mc = tid < nact ? __ldcg(P.ws_m + (long long)hq * P.nc + tid) : -INFINITY;
+  const float lc = tid < nact ? __ldcg(P.ws_l + (long long)hq * P.nc + tid) : 0.f;
+  float M = mc;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kCombThreads4 / 32; ++w) M = fmaxf(M, red[0][w]);
+  const float w = mc == -INFINITY ? 0.f : ex2(mc - M);
+  wt[tid] = w;
+  float ls = lc * w;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+  if (lane == 0) red[1][warp] = ls;
+  __syncthreads();
+  float lsum = 0.f;
+#pragma unroll
+  for (int x = 0; x < kCombThreads4 / 32; ++x) lsum += red[1][x];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float M = -INFINITY, lsum = 0.f;
-  for (int c0 = 0; c0 < nact; c0 += kPass4) {  // (one pass up to 512 chunks)
-    const int nc = min(kPass4, nact - c0);
-    float4 v[kMine4];
+  for (int u0 = 0; grp + u0 * kGroups < nact; u0 += kMine4) {
 #pragma unroll
     for (int u = 0; u < kMine4; ++u) {
-      const int c = grp + u * kGroups;
-      v[u] = c < nc ? __ldcg(reinterpret_cast<const float4*>(O + (long long)(c0 + c) * D) + j)
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int c = grp + (u0 + u) * kGroups;
+      if (c >= nact) break;
+      const float4 x = u0 == 0 ? v[u] : __ldcg(reinterpret_cast<const float4*>(O + (long long)c * D) + j);
+      const float g = wt[c];
+      acc.x = fmaf(x.x, g, acc.x);
+      acc.y = fmaf(x.y, g, acc.y);
+      acc.z = fmaf(x.z, g, acc.z);
+      acc.w = fmaf(x.w, g, acc.w);
     }
-    const float mc = tid < nc ? __ldcg(P.ws_m + (long long)hq * P.nc + c0 + tid) : -INFINITY;
-    const float lc = tid < nc ? __ldcg(P.ws_l + (long long)hq * P.nc + c0 + tid) : 0.f;
-    float mx = mc;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    if (lane == 0) red[0][warp] = mx;
-    __syncthreads();
-    mx = M;
-#pragma unroll
-    for (int w = 0; w < kCombThreads4 / 32; ++w) mx = fmaxf(mx, red[0][w]);
-    const float old = M == -INFINITY ? 0.f : ex2(M - mx);
-    M = mx;
-    const float w = mc == -INFINITY ? 0.f : ex2(mc - M);
-    wt[tid] = w;
-    float ls = lc * w;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
-    if (lane == 0) red[1][warp] = ls;
-    __syncthreads();
-    lsum *= old;
-#pragma unroll
-    for (int x = 0; x < kCombThreads4 / 32; ++x) lsum += red[1][x];
-    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-    for (int u0 = 0; grp + u0 * kGroups < nc; u0 += kMine4) {
-#pragma unroll
-      for (int u = 0; u < kMine4; ++u) {
-        const int c = grp + (u0 + u) * kGroups;
-        if (c >= nc) break;
-        const float4 x = u0 == 0 ? v[u]
-                                 : __ldcg(reinterpret_cast<const float4*>(O + (long long)(c0 + c) * D) + j);
-        const float g = wt[c];
-        acc.x = fmaf(x.x, g, acc.x);
-        acc.y = fmaf(x.y, g, acc.y);
-        acc.z = fmaf(x.z, g, acc.z);
-        acc.w = fmaf(x.w, g, acc.w);
-      }
-    }
-    __syncthreads();  // (wt and red are rewritten by another pass)
   }
   so[grp][j] = acc;
   __syncthreads();
@@ -981,9 +971,10 @@ int launch_q4kv(AttnParams P, cudaStream_t stream) {
   // the next drains the SMs, 2 us a call)
   int rc = configure_kernel(reinterpret_cast<const void*>(fn), C::kSmem, false);
   if (rc) return rc;
-  // one wave (two column tiles: a CTA an SM)
+  // one wave (two column tiles: a CTA an SM), and no more pieces than the
+  // combine has threads
   const int wave = std::max(1, (NH == 1 ? 2 : 1) * sm_count() / P.n_kv_heads);
-  P.nct = !kWhole ? std::min(P.nct, wave) : P.batch == 1 ? 1 : wave;
+  P.nct = !kWhole ? std::min({P.nct, wave, kCombThreads4}) : P.batch == 1 ? 1 : wave;
   rc = launch_ex(fn, dim3(P.nct, P.n_kv_heads), dim3(kThreads4), (size_t)C::kSmem, stream, true, P);
   if (rc || kWhole) return rc;
   const long long heads = (long long)P.batch * P.n_heads;
