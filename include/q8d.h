@@ -250,8 +250,8 @@ size_t q8d_gqa_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_
  * head_dim in {64, 128}; n_heads % n_kv_heads == 0; n_heads/n_kv_heads <= 16;
  * every kv_dtype (a packed or 4-bit cache's stride is still in elements:
  * a multiple of 256, so that sequences start on 16-byte boundaries);
- * for a 4-bit cache batch * (cap / 32 + 17) below 2^30 (with run maps 4 cap),
- * else Q8D_EUNSUPPORTED.
+ * for a 4-bit cache cap at most 2^30 and batch * (cap / 32 + 17) below 2^30
+ * (with run maps 4 cap), else Q8D_EUNSUPPORTED.
  * Over a 4-bit cache a score is off by at most 2^-21 of scale * sum_i
  * max(|q_i|, 2^-18 max |q|) |K_i|, in natural units, and given the scores an
  * output by 1e-5 of sum_t p_t |V_t|, however far apart the p_t and V's scales
@@ -276,14 +276,16 @@ int q8d_gqa_decode_attn(const float* q, const float* k_new, const float* v_new, 
  *            len 0.  A span [lo, hi) is the single run (lo, hi - lo).
  *            Every run must lie in [0, cap) (0 <= cell, 0 <= len,
  *            cell + len <= cap) and the runs must hold at least one row in
- *            all, else Q8D_DERR_LEN_RANGE is set in *d_err and the
- *            sequence's outputs are NaN.
+ *            all and at most 2^31 - 1 (2^30 over a 4-bit cache), else
+ *            Q8D_DERR_LEN_RANGE is set in *d_err and the sequence's outputs
+ *            are NaN.
  *   cache_batch_stride: as for q8d_gqa_decode_attn, or 0: every sequence
  *            reads the same cache (shared cells, e.g. a common prefix).
  * With k_new/v_new the rounded new rows are first written at the LAST row
  * of each sequence's window (the last row of its last non-empty run) and
  * attended to; that row must not be read by another sequence of the same
- * call (the calls' writes and reads would race).
+ * call, nor lie in another run of its own window (writes and reads would
+ * race).
  * Other arguments, the workspace and the results are those of
  * q8d_gqa_decode_attn (f32, f16, packed Q8_0 and 4-bit caches).
  * ---------------------------------------------------------------------- */

@@ -407,8 +407,9 @@ static int attn_entry(const float* q, const float* k_new, const float* v_new, vo
   if (head_dim != 64 && head_dim != 128) return Q8D_EUNSUPPORTED;
   if (n_heads % n_kv_heads || n_heads / n_kv_heads > 16) return Q8D_EUNSUPPORTED;
   if (!kv_known(kv_dtype)) return Q8D_EUNSUPPORTED;
-  // (the 4-bit kernel counts the batch's tiles in 32 bits; a window may take
-  // every row of the cache in each of its runs)
+  // (the 4-bit kernel counts a sequence's rows and the batch's tiles in 32
+  // bits; a window may take every row of the cache in each of its runs)
+  if (kv_dtype == Q8D_KV_Q4 && cap > kAttnQ4MaxRows) return Q8D_EUNSUPPORTED;
   if (kv_dtype == Q8D_KV_Q4 &&
       batch * (((d_runs ? Q8D_MAX_RUNS : 1) * (long long)cap + 31) / 32 + 17) >= 1LL << 30)
     return Q8D_EUNSUPPORTED;

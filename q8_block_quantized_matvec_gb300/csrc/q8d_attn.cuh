@@ -48,6 +48,7 @@ struct AttnParams {
 // of a KV head takes chunk k - (n_0 + ... + n_{s-1}) of the sequence s whose
 // range holds k; CTAs past the last chunk have no work.
 constexpr int kMinChunk = 128;
+constexpr int kAttnQ4MaxRows = 1 << 30;  // rows a sequence attends over a 4-bit cache (32-bit row arithmetic)
 constexpr int kMaxRuns = 4;  // runs per window map ("minfer Metal Backend Design": <= 4 spans)
 
 // A sequence's attended cache rows: the causal window [0, L), or the cells
@@ -99,8 +100,8 @@ __device__ __forceinline__ int attn_cell(const AttnParams& P, int b, int t) {
   return r[2 * (kMaxRuns - 1)];
 }
 
-// Rows attended by sequence b (-1 if its window is invalid): the total of
-// attn_window without building the run table.
+// Rows attended by sequence b (-1 if its window is invalid, or holds more rows
+// than an int counts): the total of attn_window without building the run table.
 __device__ __forceinline__ int attn_window_len(const AttnParams& P, int b) {
   if (!P.d_runs) {
     const int L = P.d_lens[b];
@@ -115,7 +116,7 @@ __device__ __forceinline__ int attn_window_len(const AttnParams& P, int b) {
     ok = ok && cell >= 0 && len >= 0 && (long long)cell + len <= P.cap;
     tot += len > 0 ? len : 0;
   }
-  return (ok && tot >= 1) ? (int)tot : -1;
+  return (ok && tot >= 1 && tot <= 0x7fffffff) ? (int)tot : -1;
 }
 
 // Sum of the valid window lengths of the batch.

@@ -238,7 +238,8 @@ __device__ __forceinline__ int window_len4(const AttnParams& P, int b) {
     const int L = __ldcg(P.d_lens + b);
     return (L >= 1 && L <= P.cap) ? L : -1;
   }
-  return attn_window_len(P, b);
+  const int L = attn_window_len(P, b);
+  return L <= kAttnQ4MaxRows ? L : -1;
 }
 __device__ __forceinline__ int tiles4(int L) { return L < 1 ? 0 : (L + kTile4 - 1) / kTile4; }
 
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kThreads4, NH == 1 ? 2 : 1) gqa_q4kv_kernel(co
     int t_begin = 0, t_end = L, c = 0;
     if (!kWhole) {
       t_begin = max(p_begin - sq.at, 0) * kTile4;
-      t_end = min(L, (p_begin + sp.piece - sq.at) * kTile4);
+      t_end = min(L, min(tiles4(L), p_begin + sp.piece - sq.at) * kTile4);  // (below 2^31)
       c = blockIdx.x - (P.batch == 1 ? 0 : sq.at / sp.piece);
     }
     if (!first) __syncthreads();  // (the merge buffer lies over the ring)
