@@ -385,7 +385,7 @@ int launch_rows_per(const KvRowsParams& P, cudaStream_t stream) {
 template <bool kRead, typename T, int KV>
 int launch_rows(KvRowsParams P, cudaStream_t stream) {
   const int item_e = kRead ? read_item<KV, T>() : append_item<KV>();
-  P.groups = fast_div((uint32_t)((P.width + item_e - 1) / item_e));
+  P.groups = fast_div(((uint32_t)P.width + item_e - 1) / item_e);
   const long long items = (long long)P.rows * P.groups.d;
   if (items > 0xffff0000LL) return Q8D_EUNSUPPORTED;  // (item numbers are 32 bits)
   // 16-byte accesses outside the cache where every row allows them
