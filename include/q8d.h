@@ -56,8 +56,8 @@
  *               largest magnitude (the first of them), d = m / -8, id = 1/d
  *               (0 where that is not finite), n_j = floor(x_j * id + 8.5)
  *               limited to [0, 15], scale = d rounded to binary16, all in
- *               f32; inputs must be finite, and below 2^19 in magnitude for
- *               a finite scale.
+ *               f32; inputs must be finite, and below 524160 in magnitude for
+ *               a finite scale (65520 and more round to infinity).
  */
 #ifndef Q8D_H
 #define Q8D_H
@@ -196,8 +196,9 @@ size_t q8d_kv_cache_bytes(int kv_dtype, int kv_width, int cap);
  *   Q8D_DERR_LEN_RANGE, a row outside [0, cap) Q8D_DERR_POS_RANGE in *d_err
  *   (may be NULL), and nothing of that sequence is written; a count of 0
  *   writes nothing whatever the position.
- * kv_width % 32 == 0 for a packed or 4-bit cache; rows * kv_width below
- *   2^34, else Q8D_EUNSUPPORTED.  rows == 0: no-op.
+ * kv_width % 32 == 0 for a packed or 4-bit cache; rows * (kv_width / 4,
+ *   rounded up) at most 2^32 - 2^16, else Q8D_EUNSUPPORTED (above that, types
+ *   that move eight elements at once still run).  rows == 0: no-op.
  * ---------------------------------------------------------------------- */
 int q8d_kv_append_rows(const void* k, const void* v, int row_dtype, int ld, void* kcache,
                        void* vcache, int kv_dtype, int batch, int rows, int kv_width, int cap,

@@ -38,3 +38,22 @@ def test_the_widest_rows(q8d, kind):
     assert err.item() == 0
     for o, r in zip(outs, rows):
         assert torch.equal(o[:n], r) and torch.all(o[n:] == -7)
+
+
+@pytest.mark.parametrize("top,finite", [(524159.9, True), (524160.0, False), (524287.0, False)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_largest_element_with_a_finite_scale(q8d, top, finite, sign):
+    """A scale is the largest element / -8 as binary16: infinite from 65520 on."""
+    width, cap = 64, 3
+    x = np.ones((1, width), np.float32)
+    x[0, 40] = sign * np.float32(top)
+    kc, vc = (torch.zeros(kp.cache_bytes(Q4, cap * width), dtype=torch.uint8, device="cuda") for _ in range(2))
+    err = ints([0])
+    q8d.q8d_kv_append_rows(dev(x), dev(x), F32, width, kc, vc, Q4, 1, 1, width, cap, 0, ints([1]), None, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    want = np.zeros(kp.cache_bytes(Q4, cap * width), np.uint8)
+    kp.store(want, Q4, width, cap, 1, x)
+    assert np.array_equal(kc.cpu().numpy(), want) and np.array_equal(vc.cpu().numpy(), want)
+    scale = kc.cpu().numpy()[cap * width // 2:].view(np.float16).reshape(cap, 2)[1, 1]
+    assert np.isfinite(scale) == finite
