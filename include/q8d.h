@@ -356,7 +356,8 @@ int q8d_gqa_decode_attn_noalloc(const float* q, const float* k_new, const float*
  *      initialisation and belong to the call until its work on `stream` is
  *      done (calls that may overlap, or graphs replayed at the same time,
  *      need one each)
- *   d_err: device int error word (OR-ed into) or NULL
+ *   d_err: device int error word (OR-ed into) or NULL; a wait that ran out
+ *      sets Q8D_DERR_WAIT and makes the entries of Y it concerns NaN
  * 0 <= m <= 64 (m == 0: no-op), hidden % 32 == 0, ffn % 32 == 0,
  * 1 <= n_experts <= 512, 1 <= top_k <= min(n_experts, 32), hidden and ffn
  * at most 16384; else Q8D_EUNSUPPORTED.  Outputs must not overlap inputs
@@ -367,6 +368,14 @@ int q8d_moe_ffn(const float* X, int ldx, const float* router, const void* wg, co
                 const void* wd, const float* residual, int ldr, float* Y, int ldy, int m,
                 int hidden, int ffn, int n_experts, int top_k, int norm_topk, int* experts,
                 float* weights, void* workspace, size_t ws_bytes, int* d_err, void* stream);
+
+/* Sets at which poll a wait inside the expert layer's products gives up (1:
+ * without waiting; 0: the default, 2^24), for every later call of the process
+ * and the graphs that capture it.  On expiry the call sets Q8D_DERR_WAIT, the
+ * outputs that the unfinished products enter are NaN, the copies in flight are
+ * waited for, and the CUDA context stays usable.  A small value is a way to
+ * check that a caller's error handling sees such a call. */
+int q8d_moe_set_wait_limit(unsigned polls);
 
 /* ------------------------------------------------------------------------
  * Decode step graph ("IV.4: One command buffer per token", "One command

@@ -112,6 +112,8 @@ def lib():
         L.q8d_moe_ffn.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32,
                                   i32, vp, vp, vp, sz, vp, vp]
         L.q8d_moe_ffn.restype = i32
+        L.q8d_moe_set_wait_limit.argtypes = [C.c_uint]
+        L.q8d_moe_set_wait_limit.restype = i32
         L.q8d_step_create.argtypes = [C.POINTER(StepDesc), vp, C.POINTER(vp)]
         L.q8d_step_create.restype = i32
         L.q8d_step_launch.argtypes = [vp, vp]
@@ -296,6 +298,10 @@ def q8d_moe_ffn(X, ldx: int, router, wg, wu, wd, residual, ldr: int, Y, ldy: int
         _ptr(Y), int(ldy), int(m), int(hidden), int(ffn), int(n_experts), int(top_k),
         int(norm_topk), _ptr(experts), _ptr(weights), _ptr(workspace), int(ws_bytes), _ptr(d_err),
         _stream(stream)), "q8d_moe_ffn")
+
+
+def q8d_moe_set_wait_limit(polls: int) -> int:
+    return _check(lib().q8d_moe_set_wait_limit(int(polls)), "q8d_moe_set_wait_limit")
 
 
 class Step:

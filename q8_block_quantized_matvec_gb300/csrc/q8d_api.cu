@@ -560,4 +560,9 @@ int q8d_moe_ffn(const float* X, int ldx, const float* router, const void* wg, co
   return moe_launch(P, workspace, static_cast<cudaStream_t>(stream));
 }
 
+int q8d_moe_set_wait_limit(unsigned polls) {
+  moe_set_wait_limit(polls);
+  return Q8D_OK;
+}
+
 }  // extern "C"

@@ -50,6 +50,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -672,11 +673,11 @@ __device__ __forceinline__ void each_tile(F f) {
 }
 static_assert(kTiles == 4, "");
 
-// Bounded wait that gives up when another thread of the CTA has.  (try_wait
-// without a time hint: with one it polls through nanosleep, and twenty
-// waiting warps then take the issue slots of those that work.)
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+// Bounded wait (limit - 1 polls) that gives up when another thread of the CTA
+// has.  (try_wait without a time hint: with one it polls through nanosleep, and
+// twenty waiting warps then take the issue slots of those that work.)
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+  for (uint32_t i = 1; i < limit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
   }
@@ -713,27 +714,20 @@ struct Place {
   }
 };
 
-// After a wait gave up: every announced copy has landed (stages in `filled`,
-// the parity of their last fill in `parity`).
-__device__ __forceinline__ void drain(const MoePlan& L, const MoeShared& S, uint32_t filled, uint32_t parity,
-                                      volatile int* abort) {
-  if (*abort)
-    for (int s = 0; s < L.nst; ++s)
-      if (filled >> s & 1u) mbar_wait(&S.full[s], parity >> s & 1u);
-}
+// Barrier of the whole CTA, which its roles reach at places of their own.
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
 // Barrier among one group's threads.
 __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(kGroupThreads) : "memory");
 }
 
-// Ends a product kernel: a wait that gave up is reported.
-__device__ __forceinline__ void finish(const MoeParams& P, volatile int* abort) {
-  __syncthreads();
-  if (threadIdx.x == 0 && *abort && P.d_err) atomicOr(P.d_err, Q8D_DERR_WAIT);
-}
-
 // Launches 2 (kGate) and 3.  P.ypart row p = token * top_k + slot receives
 // that pair's weighted down product.
+//
+// A wait that gives up ends every wait of its CTA.  A consumer then makes the
+// sums it could not finish NaN, here and in the units to come, and hands no
+// stage back; producers start no more copies, and settle those in flight before
+// the CTA ends.
 template <int kMode, bool kGate, int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_product_kernel(const MoeParams P, const MoePlan L, bool hperm,
@@ -743,10 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kCt = col_tiles(kCols);
   constexpr bool kResident = kMode == kContiguous;  // images stay for an item, in two buffers
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_fills, s_ifills;
   MoeShared S = carve(L, smem, P.m * P.top_k);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) s_abort = 0;
+  if (threadIdx.x == 0) s_abort = s_fills = s_ifills = 0;
   // The gate / up kernel lets the down kernel start once it has itself waited
   // for the router, so the down kernel may read the choice, and fill its ring
   // with weights, before it waits for h.
@@ -771,14 +765,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t filled = 0, parity = 0;
     int images = 0;  // whole rows: items whose images this warp fetched
     uint32_t ifilled = 0, iparity = 0;  // rows in slices: image buffers filled, parity of the last fill
+    int fills = 0, ifills = 0;  // stages, image buffers this warp arrived at
+    bool have = false;          // rows in slices: the slice's images are asked for
     Place w;
     w.q = q0;
-    const auto ready = [&]() {  // the stage may be filled
-      const bool ok = !w.again || ring_wait(&S.empty[w.s], (uint32_t)w.ph ^ 1u, &s_abort);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+    const auto announced = [&]() {  // this warp's arrival at the stage is due
       filled |= 1u << w.s;
       parity = (parity & ~(1u << w.s)) | (uint32_t)w.ph << w.s;
+      ++fills;
+    };
+    const auto ready = [&]() {  // the stage may be filled
+      const bool ok = !w.again || ring_wait(&S.empty[w.s], (uint32_t)w.ph ^ 1u, P.wait_limit, &s_abort);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      announced();
       return true;
+    };
+    // rows in slices: the buffer of the slice's images, and how often it was filled before
+    const auto image_buffer = [&](int& buf) {
+      const int c = (w.q - q0) / 2 * L.nsl + w.sl / kTiles;
+      buf = 2 * w.half + (c & 1);
+      return c / 2;
+    };
+    const auto images_announced = [&](int buf, int turn) {
+      ifilled |= 1u << buf;
+      iparity = (iparity & ~(1u << buf)) | (uint32_t)(turn & 1) << buf;
+      ++ifills;
+      have = true;
     };
     // Weights depend on nothing in flight, so the down kernel fills its ring
     // with them before it waits for h.
@@ -825,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_global();  // (the images were written by ordinary stores)
         for (; images < n_it; ++images) {
           uint64_t* full = &S.ifull[images & 1];
-          const bool ok = images < 2 || ring_wait(&S.iempty[images & 1], (uint32_t)(images / 2 - 1) & 1u, &s_abort);
+          const bool ok = images < 2 || ring_wait(&S.iempty[images & 1], (uint32_t)(images / 2 - 1) & 1u, P.wait_limit, &s_abort);
           if (!__all_sync(0xffffffffu, ok)) break;
           const int2 I = S.item[it0 + images];
           const int n = I.x >> 16;
@@ -857,18 +869,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tile = w.sl % kTiles, c0 = w.sl / kTiles * L.S, nb = min(L.S, L.bpr - c0);
         const int r0 = (w.unit() - it * nq) * kRows;
         if (tile == 0) {  // the slice's images, for its four tiles
-          const int n = I.x >> 16, c = (w.q - q0) / 2 * L.nsl + w.sl / kTiles, buf = 2 * w.half + (c & 1);
-          const bool ok = c < 2 || ring_wait(&S.iempty[buf], (uint32_t)(c / 2 - 1) & 1u, &s_abort);
+          int buf;
+          const int n = I.x >> 16, turn = image_buffer(buf);
+          const bool ok = turn < 1 || ring_wait(&S.iempty[buf], (uint32_t)(turn - 1) & 1u, P.wait_limit, &s_abort);
           if (!__all_sync(0xffffffffu, ok)) break;
+          images_announced(buf, turn);
           const int mine = pw < n ? (n - pw + kProducers - 1) / kProducers : 0;  // tokens pw, pw + 4, ..
           if (lane == 0) mbar_arrive_expect_tx(&S.ifull[buf], (uint32_t)(mine * nb * kImgBlock));
           __syncwarp();
           bulk_images(L, smem + L.o_img + (size_t)buf * L.img_bytes, &S.ifull[buf], pw, kProducers, n, c0, nb,
                       [&](int k) { return img(I.y + k); }, keep, lane);
-          ifilled |= 1u << buf;
-          iparity = (iparity & ~(1u << buf)) | (uint32_t)(c / 2 & 1) << buf;
         }
         if (!ready()) break;
+        have = false;
         uint8_t* st = smem + (size_t)w.s * L.stage_bytes;
         uint64_t* full = &S.full[w.s];
         // lanes 0-3: a row of the tile's sixteen each; a warp's rows are one matrix's
@@ -885,12 +898,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) bulk_g2s(st + (size_t)slot * L.SR, base + R.lo, R.bytes, full, pol);
       }
     }
-    drain(L, S, filled, parity, &s_abort);
-    if (kMode == kRowCopies && *(volatile int*)&s_abort)
+    cta_sync();
+    if (*(volatile int*)&s_abort) {
+      // a barrier's phase ends when all its producers have arrived: those that
+      // gave up earlier than others make up for it, without copies
+      if (kMode != kContiguous) {
+        if (lane == 0) atomicMax(&s_fills, fills), atomicMax(&s_ifills, ifills);
+        asm volatile("bar.sync 3, %0;" ::"n"(kProducers * 32) : "memory");
+        const int all = *(volatile int*)&s_fills, iall = *(volatile int*)&s_ifills;
+        for (;; w.next(L, q1), have = false) {
+          if (kMode == kRowCopies && w.sl % kTiles == 0 && !have && ifills < iall) {
+            int buf;
+            const int turn = image_buffer(buf);
+            if (lane == 0) mbar_arrive(&S.ifull[buf]);
+            images_announced(buf, turn);
+          }
+          if (fills == all) break;
+          if (lane == 0) mbar_arrive(&S.full[w.s]);
+          announced();
+        }
+      }
+      for (int s = 0; s < L.nst; ++s)
+        if (filled >> s & 1u) mbar_wait(&S.full[s], parity >> s & 1u);
       for (int i = 0; i < 4; ++i)
         if (ifilled >> i & 1u) mbar_wait(&S.ifull[i], iparity >> i & 1u);
-    if (kResident && *(volatile int*)&s_abort)
       for (int i = max(0, images - 2); i < images; ++i) mbar_wait(&S.ifull[i & 1], (uint32_t)(i / 2) & 1u);
+    }
   } else {
     if (!kGate) griddep_wait();
     const int gq = lane >> 2, cq = lane & 3;
@@ -914,13 +947,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0;
     int chunk = 0;  // rows in slices: this group's slices so far
     int held = -1;  // resident images: the item whose buffer this group holds
+    bool ok = true; // no wait of this lane gave up
     const auto next_images = [&]() {  // every item in turn, also those without a unit of this group
       if (held >= 0) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.iempty[held & 1]);
+        if (lane == 0 && ok) mbar_arrive(&S.iempty[held & 1]);
       }
       ++held;
-      ring_wait(&S.ifull[held & 1], (uint32_t)(held >> 1) & 1u, &s_abort);
+      ok = ok && ring_wait(&S.ifull[held & 1], (uint32_t)(held >> 1) & 1u, P.wait_limit, &s_abort);
     };
     for (int q = q0 + group; q < q1; q += kGroups) {
       const int it = q / nq;
@@ -935,12 +969,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) y[i][t][0] = y[i][t][1] = pack2(0.f, 0.f);
       const auto stage = [&]() {  // the group's next stage
-        ring_wait(&S.full[s], ph, &s_abort);
+        ok = ok && ring_wait(&S.full[s], ph, P.wait_limit, &s_abort);
         return after_wait(smem32 + (uint32_t)s * (uint32_t)L.stage_bytes);
       };
       const auto release = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.empty[s]);
+        if (lane == 0 && ok) mbar_arrive(&S.empty[s]);
         s += kGroups;
         if (s >= L.nst) {
           s -= L.nst;
@@ -1006,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         for (int sl = 0; sl < L.nsl; ++sl, ++chunk) {
           const int buf = 2 * group + (chunk & 1), c0 = sl * L.S, nb = min(L.S, L.bpr - c0);
-          ring_wait(&S.ifull[buf], (uint32_t)(chunk >> 1) & 1u, &s_abort);
+          ok = ok && ring_wait(&S.ifull[buf], (uint32_t)(chunk >> 1) & 1u, P.wait_limit, &s_abort);
           const uint32_t xs = smem32 + (uint32_t)(L.o_img + buf * L.img_bytes);
           each_tile([&](auto T) {
             const uint32_t st = stage();
@@ -1026,8 +1060,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             release();
           });
-          if (lane == 0) mbar_arrive(&S.iempty[buf]);  // (every lane is past its loads: release())
+          if (lane == 0 && ok) mbar_arrive(&S.iempty[buf]);  // (every lane is past its loads: release())
         }
+      }
+      if (!ok) {
+        const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+        for (int i = 0; i < kCt; ++i)
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) y[i][t][0] = y[i][t][1] = pack2(nan, nan);
       }
 #pragma unroll
       for (int i = 0; i < kCt; ++i) {
@@ -1077,8 +1118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kResident)
       while (held < n_it - 1) next_images();
+    cta_sync();
+    if (threadIdx.x == 0 && *(volatile int*)&s_abort && P.d_err) atomicOr(P.d_err, Q8D_DERR_WAIT);
   }
-  finish(P, &s_abort);
 }
 
 // 4. A thread an output: the experts' rows in the order of the choice.
@@ -1244,6 +1286,9 @@ int plan_product(const MoeParams& P, int bpr, bool gate, MoePlan* L) {
 
 }  // namespace
 
+static std::atomic<uint32_t> g_wait_limit{kWaitLimit};
+void moe_set_wait_limit(uint32_t polls) { g_wait_limit = polls ? polls : kWaitLimit; }
+
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k) {
   (void)n_experts;
   const size_t pairs = (size_t)m * top_k;
@@ -1264,6 +1309,7 @@ int moe_launch(MoeParams P, void* workspace, cudaStream_t stream) {
   if (!P.experts) P.experts = reinterpret_cast<int*>(ws);
   ws += up16(4 * pairs);
   if (!P.weights) P.weights = reinterpret_cast<float*>(ws);
+  P.wait_limit = g_wait_limit;
 
   MoePlan gu{}, dn{};
   int rc = plan_product(P, bx, true, &gu);

@@ -27,9 +27,11 @@ struct MoeParams {
   // block of 32
   uint8_t *ximg, *himg;  // [m], [m * top_k]
   float* ypart;          // [m * top_k][hidden]
+  uint32_t wait_limit;   // of the products' waits
 };
 
 size_t moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);
 int moe_launch(MoeParams P, void* workspace, cudaStream_t stream);
+void moe_set_wait_limit(uint32_t polls);  // of launches from now on; 0: the default
 
 }  // namespace q8d
