@@ -333,13 +333,16 @@ int q8d_gqa_decode_attn_noalloc(const float* q, const float* k_new, const float*
  *   the top_k experts of largest l (ties: the lower index; NaN last),
  *   largest first; w_k = p of the k-th, divided by their sum if norm_topk
  *   Y[t] = residual[t] + sum_k w_k * Wd_k (silu(Wg_k x) * (Wu_k x))
- * The logits, the softmax and the choice are computed beyond f32 accuracy,
- * so that neighbours in rank are told apart as 64-bit arithmetic would.
+ * The logits and the choice are computed in pairs of f32 (about 48 bits), so
+ * that neighbours in rank whose logits an f32 sum would confuse are told
+ * apart; the weights w are f32 results, within 2^-21 of the softmax's.
  * The products are f32-accurate (within 1e-5 of their sums of |terms|).
- * Weights of experts that no token chose are not read; an expert's are read
- * once for every group of up to 16 tokens (8 where few tokens an expert are
- * expected) that chose it.  Nothing depends on the order in which threads
- * finish.
+ * Matrices of experts that no token chose are not read (but for up to 32 rows
+ * behind an asked expert's down matrix); an expert's are read once for every
+ * group of its tokens.  A group is 1, 2, 4, 8 or 16 tokens for the whole call,
+ * about twice the mean m * top_k / n_experts and fewer where the experts' rows
+ * leave no room: few experts that most tokens ask for are read several times.
+ * Nothing depends on the order in which threads finish.
  *   X: device f32, token t at X + t*ldx (ldx >= hidden, ldx % 4 == 0),
  *      16-byte aligned
  *   router: device f32 [n_experts][hidden], 16-byte aligned

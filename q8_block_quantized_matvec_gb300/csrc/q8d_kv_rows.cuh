@@ -9,8 +9,9 @@
 
 namespace q8d {
 
-// n / d for any 32-bit n by a multiplication (d fixed by the host): q =
-// (((n - t) >> 1) + t) >> s with t = n * m >> 32.
+// n / d for any 32-bit n by a multiplication (d fixed by the host; Granlund and
+// Montgomery's division by an invariant integer): q = (((n - t) >> 1) + t) >> s
+// with t = n * m >> 32.
 struct FastDiv {
   uint32_t d, m, s;
   __device__ __forceinline__ uint32_t div(uint32_t n) const {

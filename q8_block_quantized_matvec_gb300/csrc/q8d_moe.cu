@@ -25,7 +25,8 @@
 //  * A work unit is 64 slots of rows of one expert (32 gate and 32 up rows,
 //    or 64 down rows) for a group of its tokens: four A tiles.  Units are
 //    dealt to the CTAs in contiguous ranges; experts nobody chose are not
-//    touched.  (Giving each CTA a few output rows of every expert instead
+//    touched (but for the rows behind a last down unit of half the rows, which
+//    a tensor copy brings along).  (Giving each CTA a few output rows of every expert instead
 //    saves launch 4 but has every CTA fetch every h, 2.3 bytes for one of
 //    weights at 64 tokens, and one tile per B load: 118 against 62 us for
 //    the down products of 128 experts of 2048 x 768.)
@@ -75,7 +76,8 @@ constexpr int kRtCluster = 8;
 __device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
 
 // (s, c) += a * b as an unevaluated sum: the product's rounding error (one
-// FMA) and the sum's (TwoSum) go to c, so s + c carries about 48 bits.  (f64
+// FMA) and the sum's (Knuth's TwoSum) go to c, the compensated dot product of
+// Ogita, Rump and Oishi, so s + c carries about 48 bits.  (f64
 // arithmetic would do as well, but an SM of this GPU does two a cycle.)
 __device__ __forceinline__ void dot2(uint64_t& s, uint64_t& c, uint64_t a, uint64_t b) {
   const uint64_t m1 = pack2(-1.f, -1.f);
@@ -1179,7 +1181,9 @@ int weight_map(const uint8_t* w, int bpr, long long n_rows, int box_rows, CUtens
 
 // Tokens a group: about twice an expert's share of the (token, slot) pairs,
 // a power of two up to 8 (an expert with more is read once a group; with
-// fewer, its stage space idles).  Sixteen where that is clearly fewer units
+// fewer, its stage space idles).  The mean decides, so where the choice is
+// lopsided a popular expert is read more often: 64 tokens that all ask for one
+// of 512 experts are 32 groups of two.  Sixteen where that is clearly fewer units
 // (nq an item; the two groups of every SM take one each a turn): by 1.35 for
 // tensor copies and two turns or more, else by 1.7.  Measured, eight /
 // sixteen, us: 64 tokens, 4096 x 4096, 2 of 8 experts, 268 / 215, 1 of 8, 174 /
