@@ -364,7 +364,8 @@ int q8d_gqa_decode_attn_noalloc(const float* q, const float* k_new, const float*
  * 0 <= m <= 64 (m == 0: no-op), hidden % 32 == 0, ffn % 32 == 0,
  * 1 <= n_experts <= 512, 1 <= top_k <= min(n_experts, 32), hidden and ffn
  * at most 16384; else Q8D_EUNSUPPORTED.  Outputs must not overlap inputs
- * (but Y may be residual), the workspace or each other.
+ * (but Y may be residual), the workspace or each other, a strided operand
+ * counted whole from its first row's start to its last row's end.
  * ---------------------------------------------------------------------- */
 size_t q8d_moe_workspace_bytes(int m, int hidden, int ffn, int n_experts, int top_k);
 int q8d_moe_ffn(const float* X, int ldx, const float* router, const void* wg, const void* wu,
