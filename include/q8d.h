@@ -382,6 +382,178 @@ int q8d_moe_ffn(const float* X, int ldx, const float* router, const void* wg, co
 int q8d_moe_set_wait_limit(unsigned polls);
 
 /* ------------------------------------------------------------------------
+ * The operators between the products of a dense layer, and products with
+ * 4-bit weights: norm -> projections -> rotary positions and cache ->
+ * attention -> projection + residual -> norm -> gated projections ->
+ * projection + residual.  None needs a workspace.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * q8d_rmsnorm_rows - root-mean-square norm of rows, with the residual's
+ * addition before it:
+ *   h = x + residual (h = x without one),  sum_out = h,
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ * in f32: h is rounded to f32 (and for sum_out to the rows' type; the norm
+ * takes the f32 value), the mean is that of 64-bit arithmetic (within 2^-40),
+ * the factor 1 / sqrt(...) is rounded to f32 once, and each product once, so
+ * that an 8-bit output is that of the plain formula.
+ *   x, residual, sum_out: device rows of row_dtype (Q8D_KV_F32 or Q8D_KV_F16),
+ *      ldx, ldr, lds elements apart (>= n); residual and sum_out may be NULL,
+ *      sum_out may be x or residual itself (same pointer and distance)
+ *   weight: device f32[n]
+ *   y: device rows of y_dtype, ldy elements apart (>= n): Q8D_KV_F32,
+ *      Q8D_KV_F16, or Q8D_KV_Q8_0: rows of Q8_0 blocks, quantized as in a packed
+ *      cache (n % 32 == 0; ldy % 32 == 0, row i at byte i * ldy / 32 * 34)
+ * 1 <= n <= 16384 (else Q8D_EUNSUPPORTED), eps >= 0, rows >= 0 (0: no-op).
+ * Pointers are aligned to their elements (y as Q8_0 to 2 bytes); 16-byte
+ * accesses where all pointers and distances allow them.  y must not overlap
+ * any other operand, nor sum_out one that it is not.  A row that holds a NaN or
+ * an infinity gives what the formula gives in 64 bits (NaN or zeros).
+ * ---------------------------------------------------------------------- */
+int q8d_rmsnorm_rows(const void* x, const void* residual, void* sum_out, int row_dtype,
+                     long long ldx, long long ldr, long long lds, const float* weight, float eps,
+                     void* y, int y_dtype, long long ldy, int rows, int n, void* stream);
+
+/* How the angles of rotary positions are scaled for long contexts. */
+#define Q8D_ROPE_PLAIN 0
+#define Q8D_ROPE_LINEAR 1 /* every angle / factor */
+#define Q8D_ROPE_NTK 2    /* theta * factor^(rot_dim / (rot_dim - 2)) for theta */
+#define Q8D_ROPE_YARN 3   /* fast pairs as they are, slow ones / factor, a ramp between */
+
+/* Which elements of a head make a pair. */
+#define Q8D_ROPE_HALF 0  /* i and i + rot_dim / 2 */
+#define Q8D_ROPE_PAIRS 1 /* 2 i and 2 i + 1       */
+
+/* ------------------------------------------------------------------------
+ * q8d_rope_table - the cosines and sines of a model's rotary positions:
+ *   table[pos][i] = mscale * cos(pos * f_i),
+ *   table[pos][rot_dim / 2 + i] = mscale * sin(pos * f_i),
+ *   pos < max_pos, i < rot_dim / 2, f_i = theta^(-2 i / rot_dim), scaled:
+ *   linear f_i / factor; NTK as above; YaRN f_i / factor * r_i + f_i * (1 - r_i)
+ *   with r_i = (i - low) / (high - low) limited to [0, 1], low and high the
+ *   pairs that turn beta_fast and beta_slow times in orig_ctx positions
+ *   (rot_dim ln(orig_ctx / (2 pi beta)) / (2 ln theta), low rounded down to at
+ *   least 0, high up to at most rot_dim - 1, apart by at least 0.001)
+ * worked out in 64 bits and rounded to f32 once.  table: device
+ * f32[max_pos][rot_dim], 16-byte aligned.  rot_dim even and positive, theta > 1,
+ * factor > 0, mscale finite (1 for none; YaRN's is 0.1 ln(factor) + 1);
+ * orig_ctx, beta_fast and beta_slow > 0 are read for YaRN only; NTK needs
+ * rot_dim > 2.
+ * ---------------------------------------------------------------------- */
+int q8d_rope_table(float* table, int max_pos, int rot_dim, double theta, int scaling,
+                   double factor, double orig_ctx, double beta_fast, double beta_slow,
+                   double mscale, void* stream);
+
+/* What does not change from call to call of q8d_rope_append_rows (a host
+ * struct, read during the call). */
+typedef struct q8d_rope_desc {
+  int n_heads, n_kv_heads, head_dim;
+  int rot_dim;      /* elements of a head that turn: even, 0 .. head_dim */
+  int layout;       /* Q8D_ROPE_HALF or Q8D_ROPE_PAIRS                   */
+  int max_pos;      /* rows of the table                                */
+  int row_dtype;    /* of q, k, v: Q8D_KV_F32 or Q8D_KV_F16             */
+  int q_dtype;      /* of q_out: Q8D_KV_F32 or Q8D_KV_F16               */
+  int kv_dtype;     /* of the caches: any Q8D_KV_*                      */
+  int cap;          /* rows of a sequence's cache                       */
+  float eps;        /* of the heads' norms                              */
+  long long ldq;    /* elements from a row of q to the next             */
+  long long ldkv;   /* of k and of v                                    */
+  long long ldo;    /* of q_out                                         */
+  long long cache_batch_stride; /* elements, as for q8d_kv_append_rows  */
+  const float* table;           /* q8d_rope_table's; NULL if rot_dim is 0 */
+  const float *bq, *bk, *bv;    /* f32 [heads * head_dim], or all NULL  */
+  const float *q_norm, *k_norm; /* f32 [head_dim], or both NULL         */
+} q8d_rope_desc;
+
+/* ------------------------------------------------------------------------
+ * q8d_rope_append_rows - up to `rows` rows of q, k and v of every sequence of
+ * a batch (a prompt, or a token each) made ready for attention: the bias is
+ * added, each q and k head normed (x / sqrt(mean(x^2) + eps) * q_norm or
+ * k_norm), its first rot_dim elements turned by the row's position
+ *   (a, b) -> (a cos - b sin, a sin + b cos),
+ * q written to q_out, k and v stored in the caches as q8d_kv_append_rows
+ * stores them.  Each step is one f32 rounding.
+ *   Row i of sequence s, i < d_counts[s] (`rows` for every one if NULL), is row
+ *   s * rows + i of q, k, v and q_out, goes to cache row d_pos[s] + i and is
+ *   turned by position d_rope_pos[s] + i (d_pos[s] + i if d_rope_pos is NULL).
+ *   q, k, v: device, row_dtype; they may be columns of one projection's output.
+ *   q_out: device rows of q_dtype; may be q itself (same pointer, type and
+ *      distance).  q and q_out may be NULL (k and v alone), or k, v, kcache and
+ *      vcache (q alone; then d_pos gives the position only, unless d_rope_pos
+ *      does).
+ *   A count outside [0, rows] sets Q8D_DERR_LEN_RANGE, a row outside [0, cap) or
+ *   a position outside [0, max_pos) Q8D_DERR_POS_RANGE in *d_err (may be NULL);
+ *   nothing of that sequence is stored and all its `rows` rows of q_out become
+ *   NaN.  Rows behind a count are left as they were.
+ * head_dim a multiple of 8 (of 32 for a packed or 4-bit cache) up to 256,
+ * else Q8D_EUNSUPPORTED; the caches' alignment and overlaps are those of
+ * q8d_kv_append_rows, table 16-byte aligned.  rows == 0: no-op.
+ * ---------------------------------------------------------------------- */
+int q8d_rope_append_rows(const q8d_rope_desc* desc, const void* q, const void* k, const void* v,
+                         void* q_out, void* kcache, void* vcache, int batch, int rows,
+                         const int* d_pos, const int* d_rope_pos, const int* d_counts, int* d_err,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit weight matrices [p][n], n % 32 == 0, with a binary16 scale for every
+ * group of 32, 64 or 128 neighbours of a row (the last group of a row may be
+ * shorter): value = scale * (n_j - 8), n_j in 0..15.  The quantizer is the
+ * 4-bit cache's, over a group: scale = the element of largest magnitude (the
+ * first of them) / -8, n_j = floor(x_j / scale + 8.5) limited to [0, 15]; inputs
+ * must be finite and below 524160 in magnitude.  The bytes are laid out for the
+ * products (q8d_q4_pack makes them, once for a model):
+ *   q8d_q4_matrix_bytes(p, n, group) bytes, 16-byte aligned: tiles of 16 rows by
+ *   128 columns (filled up with zeros), those of 16 rows one behind the other;
+ *   a tile is 1024 bytes of quants, then 16 * 128 / group scales.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of such a matrix; 0 for sizes that none has. */
+size_t q8d_q4_matrix_bytes(int p, int n, int group);
+
+/* Quantizes rows into a matrix.  src: device rows of src_dtype (Q8D_KV_F32,
+ * Q8D_KV_F16, or Q8D_KV_Q8_0: rows of Q8_0 blocks), ld elements apart (>= n; for
+ * Q8_0 ld % 32 == 0), aligned to their elements (Q8_0: 2 bytes); w_q4 must not
+ * overlap it.  p == 0: no-op. */
+int q8d_q4_pack(const void* src, int src_dtype, long long ld, void* w_q4, int p, int n, int group,
+                void* stream);
+
+/* The values of a matrix as rows of dst_dtype (Q8D_KV_F32, exact, or
+ * Q8D_KV_F16, rounded to nearest even once), ld elements apart. */
+int q8d_q4_unpack(const void* w_q4, void* dst, int dst_dtype, long long ld, int p, int n,
+                  int group, void* stream);
+
+/* ------------------------------------------------------------------------
+ * q8d_q4_matmul - a 4-bit matrix applied to m rows of activations:
+ *   Y[i][r] = sum_k X[i][k] * W[r][k] (+ bias[r]) (+ residual[i][r])
+ * within 1e-5 of the sum of |terms|.
+ *   X: device rows of x_dtype, ldx elements apart (>= n): Q8D_KV_F32 or
+ *      Q8D_KV_F16 (16-byte aligned, ldx % 4 == 0, f16 % 8 == 0), or Q8D_KV_Q8_0:
+ *      rows of Q8_0 blocks as q8d_rmsnorm_rows writes them (2-byte aligned,
+ *      ldx % 32 == 0).  A row with an infinity or NaN makes its row of Y NaN or
+ *      infinite.
+ *   bias: device f32[p] or NULL; residual: device f32 rows ldr apart (>= p) or
+ *      NULL, may be Y itself (same pointer, ldr == ldy)
+ *   Y: device f32 rows, ldy apart (>= p); only the first p entries of a row are
+ *      written; must not overlap any other operand
+ * 0 <= m <= 16, 32 <= n <= 32768, n % 32 == 0, p <= 2^30; else
+ * Q8D_EUNSUPPORTED.  m == 0 or p == 0: no-op.  Matrices are read once (f32 rows:
+ * once for every eight).  Nothing depends on the order in which threads finish.
+ * ---------------------------------------------------------------------- */
+int q8d_q4_matmul(const void* X, int x_dtype, long long ldx, const void* w_q4, int group,
+                  const float* bias, const float* residual, long long ldr, float* Y, long long ldy,
+                  int m, int n, int p, void* stream);
+
+/* ------------------------------------------------------------------------
+ * q8d_q4_gated - the gated projections of a feed-forward block in one kernel:
+ *   H[i][r] = silu(sum_k X[i][k] Wg[r][k]) * sum_k X[i][k] Wu[r][k],
+ *   silu(v) = v / (1 + exp(-v))
+ * Wg, Wu: 4-bit matrices [p][n] of the same group.  Other arguments as for
+ * q8d_q4_matmul.
+ * ---------------------------------------------------------------------- */
+int q8d_q4_gated(const void* X, int x_dtype, long long ldx, const void* wg_q4, const void* wu_q4,
+                 int group, float* H, long long ldh, int m, int n, int p, void* stream);
+
+/* ------------------------------------------------------------------------
  * Decode step graph ("IV.4: One command buffer per token", "One command
  * buffer": the whole step encoded once and submitted as one unit).
  * The step, per layer: RMSNorm -> q/k/v Q8_0 matvecs -> (q/k/v bias) ->

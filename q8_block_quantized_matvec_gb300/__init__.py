@@ -31,6 +31,13 @@ Q8D_KV_Q4 = 4
 
 Q8D_MAX_RUNS = 4
 
+Q8D_ROPE_PLAIN = 0
+Q8D_ROPE_LINEAR = 1
+Q8D_ROPE_NTK = 2
+Q8D_ROPE_YARN = 3
+Q8D_ROPE_HALF = 0
+Q8D_ROPE_PAIRS = 1
+
 Q8D_DERR_POS_RANGE = 0x1
 Q8D_DERR_LEN_RANGE = 0x2
 Q8D_DERR_TOKEN_RANGE = 0x4
@@ -60,6 +67,17 @@ class StepDesc(C.Structure):
                 ("d_logits", C.c_void_p)]
 
 
+class RopeDesc(C.Structure):
+    _fields_ = [("n_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("rot_dim", C.c_int), ("layout", C.c_int), ("max_pos", C.c_int),
+                ("row_dtype", C.c_int), ("q_dtype", C.c_int), ("kv_dtype", C.c_int),
+                ("cap", C.c_int), ("eps", C.c_float), ("ldq", C.c_longlong),
+                ("ldkv", C.c_longlong), ("ldo", C.c_longlong),
+                ("cache_batch_stride", C.c_longlong), ("table", C.c_void_p), ("bq", C.c_void_p),
+                ("bk", C.c_void_p), ("bv", C.c_void_p), ("q_norm", C.c_void_p),
+                ("k_norm", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -72,6 +90,7 @@ def lib():
                               "q8_block_quantized_matvec_gb300.build.build()")
         L = C.CDLL(LIB_PATH)
         vp, i32, i64, f32, sz = C.c_void_p, C.c_int, C.c_longlong, C.c_float, C.c_size_t
+        f64 = C.c_double
         L.q8d_version.restype = i32
         L.q8d_strerror.argtypes = [i32]
         L.q8d_strerror.restype = C.c_char_p
@@ -114,6 +133,24 @@ def lib():
         L.q8d_moe_ffn.restype = i32
         L.q8d_moe_set_wait_limit.argtypes = [C.c_uint]
         L.q8d_moe_set_wait_limit.restype = i32
+        L.q8d_rmsnorm_rows.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, f32, vp, i32, i64, i32,
+                                       i32, vp]
+        L.q8d_rmsnorm_rows.restype = i32
+        L.q8d_rope_table.argtypes = [vp, i32, i32, f64, i32, f64, f64, f64, f64, f64, vp]
+        L.q8d_rope_table.restype = i32
+        L.q8d_rope_append_rows.argtypes = [C.POINTER(RopeDesc), vp, vp, vp, vp, vp, vp, i32, i32,
+                                           vp, vp, vp, vp, vp]
+        L.q8d_rope_append_rows.restype = i32
+        L.q8d_q4_matrix_bytes.argtypes = [i32, i32, i32]
+        L.q8d_q4_matrix_bytes.restype = sz
+        L.q8d_q4_pack.argtypes = [vp, i32, i64, vp, i32, i32, i32, vp]
+        L.q8d_q4_pack.restype = i32
+        L.q8d_q4_unpack.argtypes = [vp, vp, i32, i64, i32, i32, i32, vp]
+        L.q8d_q4_unpack.restype = i32
+        L.q8d_q4_matmul.argtypes = [vp, i32, i64, vp, i32, vp, vp, i64, vp, i64, i32, i32, i32, vp]
+        L.q8d_q4_matmul.restype = i32
+        L.q8d_q4_gated.argtypes = [vp, i32, i64, vp, vp, i32, vp, i64, i32, i32, i32, vp]
+        L.q8d_q4_gated.restype = i32
         L.q8d_step_create.argtypes = [C.POINTER(StepDesc), vp, C.POINTER(vp)]
         L.q8d_step_create.restype = i32
         L.q8d_step_launch.argtypes = [vp, vp]
@@ -302,6 +339,71 @@ def q8d_moe_ffn(X, ldx: int, router, wg, wu, wd, residual, ldr: int, Y, ldy: int
 
 def q8d_moe_set_wait_limit(polls: int) -> int:
     return _check(lib().q8d_moe_set_wait_limit(int(polls)), "q8d_moe_set_wait_limit")
+
+
+def q8d_rmsnorm_rows(x, residual, sum_out, row_dtype: int, ldx: int, ldr: int, lds: int, weight,
+                     eps: float, y, y_dtype: int, ldy: int, rows: int, n: int, stream=None) -> int:
+    return _check(lib().q8d_rmsnorm_rows(
+        _ptr(x), _ptr(residual), _ptr(sum_out), int(row_dtype), int(ldx), int(ldr), int(lds),
+        _ptr(weight), float(eps), _ptr(y), int(y_dtype), int(ldy), int(rows), int(n),
+        _stream(stream)), "q8d_rmsnorm_rows")
+
+
+def q8d_rope_table(table, max_pos: int, rot_dim: int, theta: float, scaling: int, factor: float,
+                   orig_ctx: float, beta_fast: float, beta_slow: float, mscale: float,
+                   stream=None) -> int:
+    return _check(lib().q8d_rope_table(_ptr(table), int(max_pos), int(rot_dim), float(theta),
+                                       int(scaling), float(factor), float(orig_ctx),
+                                       float(beta_fast), float(beta_slow), float(mscale),
+                                       _stream(stream)), "q8d_rope_table")
+
+
+def rope_desc(**fields) -> RopeDesc:
+    """A RopeDesc from its fields' values; tensors among them stay alive with it."""
+    desc = RopeDesc()
+    for name, value in fields.items():
+        if not hasattr(RopeDesc, name):
+            raise TypeError(f"q8d_rope_desc has no field {name!r}")
+        setattr(desc, name, _ptr(value) if hasattr(value, "data_ptr") else value)
+    desc._tensors = fields
+    return desc
+
+
+def q8d_rope_append_rows(desc: RopeDesc, q, k, v, q_out, kcache, vcache, batch: int, rows: int,
+                         d_pos, d_rope_pos, d_counts, d_err, stream=None) -> int:
+    return _check(lib().q8d_rope_append_rows(
+        desc, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(kcache), _ptr(vcache), int(batch),
+        int(rows), _ptr(d_pos), _ptr(d_rope_pos), _ptr(d_counts), _ptr(d_err), _stream(stream)),
+        "q8d_rope_append_rows")
+
+
+def q8d_q4_matrix_bytes(p: int, n: int, group: int) -> int:
+    return int(lib().q8d_q4_matrix_bytes(int(p), int(n), int(group)))
+
+
+def q8d_q4_pack(src, src_dtype: int, ld: int, w_q4, p: int, n: int, group: int, stream=None) -> int:
+    return _check(lib().q8d_q4_pack(_ptr(src), int(src_dtype), int(ld), _ptr(w_q4), int(p), int(n),
+                                    int(group), _stream(stream)), "q8d_q4_pack")
+
+
+def q8d_q4_unpack(w_q4, dst, dst_dtype: int, ld: int, p: int, n: int, group: int,
+                  stream=None) -> int:
+    return _check(lib().q8d_q4_unpack(_ptr(w_q4), _ptr(dst), int(dst_dtype), int(ld), int(p),
+                                      int(n), int(group), _stream(stream)), "q8d_q4_unpack")
+
+
+def q8d_q4_matmul(X, x_dtype: int, ldx: int, w_q4, group: int, bias, residual, ldr: int, Y,
+                  ldy: int, m: int, n: int, p: int, stream=None) -> int:
+    return _check(lib().q8d_q4_matmul(
+        _ptr(X), int(x_dtype), int(ldx), _ptr(w_q4), int(group), _ptr(bias), _ptr(residual),
+        int(ldr), _ptr(Y), int(ldy), int(m), int(n), int(p), _stream(stream)), "q8d_q4_matmul")
+
+
+def q8d_q4_gated(X, x_dtype: int, ldx: int, wg_q4, wu_q4, group: int, H, ldh: int, m: int, n: int,
+                 p: int, stream=None) -> int:
+    return _check(lib().q8d_q4_gated(
+        _ptr(X), int(x_dtype), int(ldx), _ptr(wg_q4), _ptr(wu_q4), int(group), _ptr(H), int(ldh),
+        int(m), int(n), int(p), _stream(stream)), "q8d_q4_gated")
 
 
 class Step:

@@ -11,6 +11,7 @@
 #include <thread>
 #include <utility>
 
+#include "q8d_args.cuh"
 #include "q8d_attn.cuh"
 #include "q8d_internal.cuh"
 #include "q8d_kv_rows.cuh"
@@ -82,30 +83,7 @@ int wait_event_bounded(cudaEvent_t ev, int timeout_ms, const int* src, int* dst)
   return Q8D_OK;
 }
 
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na && nb && x < y + nb && y < x + na;
-}
-
 static size_t q8_bytes(long long rows, int n) { return (size_t)rows * (size_t)(n / 32) * 34; }
-
-// Bytes of n cache elements of a type (a whole number of blocks for the
-// packed types).
-static long long kv_bytes(int kv_dtype, long long n) {
-  switch (kv_dtype) {
-    case Q8D_KV_F32: return n * 4;
-    case Q8D_KV_F16: return n * 2;
-    case Q8D_KV_Q8_0: return n / 32 * 34;
-    default: return n / 32 * 18;
-  }
-}
-static bool kv_known(int kv_dtype) {
-  return kv_dtype == Q8D_KV_F32 || kv_dtype == Q8D_KV_F16 || kv_dtype == Q8D_KV_Q8_0 ||
-         kv_dtype == Q8D_KV_Q4;
-}
-static bool kv_packed(int kv_dtype) { return kv_dtype == Q8D_KV_Q8_0 || kv_dtype == Q8D_KV_Q4; }
 
 int step_validate(const q8d_step_desc* d) {
   if (!d || !d->layers || !d->embed || !d->out_norm || !d->lm_head || !d->d_token || !d->d_pos ||

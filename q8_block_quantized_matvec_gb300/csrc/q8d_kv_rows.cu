@@ -141,72 +141,6 @@ struct CacheT<Q8D_KV_F16> {
   using T = __half;
 };
 
-// The four lanes of a Q8_0 block quantize its 32 elements (the operations of
-// quantize_q8_0_warp, so the bytes are the same).
-__device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f)[kGroupE], bool live) {
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kGroupE; ++i) amax = fmaxf(amax, fabsf(f[i]));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  if (!live) return;
-  const float d = __fdiv_rn(amax, 127.0f);
-  const float id = d != 0.f ? __frcp_rn(d) : 0.f;
-  unsigned short* q = reinterpret_cast<unsigned short*>(blk + 2 + 8 * part);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t pair = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = (int)roundf(__fmul_rn(f[2 * i + k], id));
-      pair |= (uint32_t)(uint8_t)(int8_t)r << (8 * k);
-    }
-    q[i] = (unsigned short)pair;
-  }
-  if (part == 0) *reinterpret_cast<unsigned short*>(blk) = __half_as_ushort(__float2half_rn(d));
-}
-
-// The four lanes of a 4-bit block.  Lanes 0, 1 hold elements 0-15 (low
-// halves of the 16 bytes), lanes 2, 3 elements 16-31 (high halves): lane p
-// and lane p ^ 2 exchange four nibbles each and write one word each.
-__device__ __forceinline__ void put_q4(uint8_t* quants, uint8_t* scale, int part,
-                                       const float (&f)[kGroupE], bool live) {
-  // the largest magnitude among the positive and among the negative elements;
-  // only where they tie (a block of zeros, say) does the order decide
-  float hi = f[0], lo = f[0];
-#pragma unroll
-  for (int i = 1; i < kGroupE; ++i) {
-    hi = fmaxf(hi, f[i]);
-    lo = fminf(lo, f[i]);
-  }
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-  }
-  float m = hi > -lo ? hi : lo;
-  if (__any_sync(0xffffffffu, hi == -lo)) {
-    m = f[0];
-#pragma unroll
-    for (int i = 1; i < kGroupE; ++i) m = q4_larger(m, f[i], false);
-    m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 1), (part & 1) != 0);
-    m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, 2), (part & 2) != 0);
-  }
-  float d, id;
-  q4_scale(m, d, id);
-  uint32_t w[2];  // a byte an element
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = __byte_perm(__byte_perm(q4_bits(f[4 * i], id), q4_bits(f[4 * i + 1], id), 0x0040),
-                       __byte_perm(q4_bits(f[4 * i + 2], id), q4_bits(f[4 * i + 3], id), 0x0040), 0x5410);
-  const bool high = part >= 2;
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[0] : w[1], 2);
-  if (!live) return;
-  const uint32_t word = high ? (got | w[1] << 4) : (w[0] | got << 4);
-  reinterpret_cast<uint32_t*>(quants)[2 * (part & 1) + (high ? 1 : 0)] = word;
-  if (part == 0) *reinterpret_cast<unsigned short*>(scale) = __half_as_ushort(__float2half_rn(d));
-}
-
 // Elements an append's thread takes at once: a packed block's quarter, or 16
 // bytes of the cache (eight of an f32 cache would be two stores, each of half
 // of every 32-byte sector).
@@ -247,10 +181,10 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvRow
       const long long r = row[u];
       if constexpr (KV == Q8D_KV_Q4) {
         const int blk = g[u] >> 2;
-        put_q4(seq + r * (P.width / 2) + blk * 16,
+        put_q4<kE>(seq + r * (P.width / 2) + blk * 16,
                seq + q4_scale_plane(P.cap, P.width) + r * (P.width / 16) + blk * 2, g[u] & 3, f[u], live[u]);
       } else if constexpr (KV == Q8D_KV_Q8_0) {
-        put_q8_0(seq + (r * (P.width / kQBlock) + (g[u] >> 2)) * kQBlockBytes, g[u] & 3, f[u], live[u]);
+        put_q8_0<kE>(seq + (r * (P.width / kQBlock) + (g[u] >> 2)) * kQBlockBytes, g[u] & 3, f[u], live[u]);
       } else {
         using C = typename CacheT<KV>::T;
         C* dst = reinterpret_cast<C*>(seq) + r * P.width + g[u] * kE;

@@ -98,4 +98,97 @@ __device__ __forceinline__ void quantize_q4_warp(float x, uint8_t* quants, uint8
   if (lane == 0) *reinterpret_cast<unsigned short*>(scale) = __half_as_ushort(__float2half_rn(d));
 }
 
+// ---- blocks shared by neighbouring lanes ------------------------------------
+// The 32 / kE lanes of a Q8_0 block (lane `part` holds its elements kE * part
+// and on) quantize it with the operations of quantize_q8_0_warp, so the bytes
+// are the same.  Every lane of the warp calls; lanes that are not live store
+// nothing.
+template <int kE>
+__device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f)[kE], bool live) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) amax = fmaxf(amax, fabsf(f[i]));
+#pragma unroll
+  for (int o = 1; o < 32 / kE; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (!live) return;
+  const float d = __fdiv_rn(amax, 127.0f);
+  const float id = d != 0.f ? __frcp_rn(d) : 0.f;
+  if constexpr (kE == 1) {
+    blk[2 + part] = (uint8_t)(int8_t)(int)roundf(__fmul_rn(f[0], id));
+  } else {
+    unsigned short* q = reinterpret_cast<unsigned short*>(blk + 2 + kE * part);
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) {
+      uint32_t pair = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = (int)roundf(__fmul_rn(f[2 * i + k], id));
+        pair |= (uint32_t)(uint8_t)(int8_t)r << (8 * k);
+      }
+      q[i] = (unsigned short)pair;
+    }
+  }
+  if (part == 0) *reinterpret_cast<unsigned short*>(blk) = __half_as_ushort(__float2half_rn(d));
+}
+
+// The element of largest magnitude (the first of them) among the values of
+// `lanes` neighbouring lanes, lane after lane.
+template <int kE>
+__device__ __forceinline__ float first_largest(const float (&f)[kE], int lanes) {
+  // the largest magnitude among the positive and among the negative elements;
+  // only where they tie (a block of zeros, say) does the order decide
+  float hi = f[0], lo = f[0];
+#pragma unroll
+  for (int i = 1; i < kE; ++i) {
+    hi = fmaxf(hi, f[i]);
+    lo = fminf(lo, f[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < lanes; o <<= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  float m = hi > -lo ? hi : lo;
+  if (__any_sync(0xffffffffu, hi == -lo)) {
+    m = f[0];
+#pragma unroll
+    for (int i = 1; i < kE; ++i) m = q4_larger(m, f[i], false);
+#pragma unroll
+    for (int o = 1; o < lanes; o <<= 1)
+      m = q4_larger(m, __shfl_xor_sync(0xffffffffu, m, o), (threadIdx.x & o) != 0);
+  }
+  return m;
+}
+
+// The 32 / kE lanes of a 4-bit block (kE 4 or 8).  The lower half of them holds
+// elements 0-15 (low halves of the 16 bytes), the upper half elements 16-31
+// (high halves): a lane and its opposite exchange the nibbles of one word and
+// write a word each (kE 8), or the lower one writes (kE 4).
+template <int kE>
+__device__ __forceinline__ void put_q4(uint8_t* quants, uint8_t* scale, int part, const float (&f)[kE],
+                                       bool live) {
+  const float m = first_largest<kE>(f, 32 / kE);
+  float d, id;
+  q4_scale(m, d, id);
+  uint32_t w[kE / 4];  // a byte an element
+#pragma unroll
+  for (int i = 0; i < kE / 4; ++i)
+    w[i] = __byte_perm(__byte_perm(q4_bits(f[4 * i], id), q4_bits(f[4 * i + 1], id), 0x0040),
+                       __byte_perm(q4_bits(f[4 * i + 2], id), q4_bits(f[4 * i + 3], id), 0x0040), 0x5410);
+  constexpr int kHalf = 16 / kE;
+  const bool high = part >= kHalf;
+  if constexpr (kE == 8) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[0] : w[1], kHalf);
+    if (!live) return;
+    const uint32_t word = high ? (got | w[1] << 4) : (w[0] | got << 4);
+    reinterpret_cast<uint32_t*>(quants)[2 * (part & 1) + (high ? 1 : 0)] = word;
+  } else {
+    static_assert(kE == 4, "");
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, w[0], kHalf);
+    if (!live) return;
+    if (!high) reinterpret_cast<uint32_t*>(quants)[part] = w[0] | got << 4;
+  }
+  if (part == 0) *reinterpret_cast<unsigned short*>(scale) = __half_as_ushort(__float2half_rn(d));
+}
+
 }  // namespace q8d
