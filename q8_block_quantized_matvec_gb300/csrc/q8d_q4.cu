@@ -10,8 +10,11 @@
 //    as f16 hi and lo) its 8 columns.  tcgen05's smallest shape spends 93 clocks
 //    on as many weights as mma.sync multiplies in 32 a column group.
 //  * Tiles lie in memory in the order in which lanes feed them (q8d_layer.cuh):
-//    two 16-byte loads a lane bring a tile into registers, no byte twice, with
-//    no shared memory between.  Four tiles a warp are in flight.
+//    two 16-byte reads a lane take a tile from shared memory, no byte twice and
+//    no bank twice.  Each warp has a ring of its own there, filled by bulk copies
+//    of two tiles that one lane issues: nothing but the warp itself waits for
+//    them.  (Loads straight into registers, four tiles ahead, waited for the
+//    newest of them too: 27.0 us for the gated pair 3584 -> 18944 of one token.)
 //  * A pair of quants costs one LOP3 under the exponent of 1024 (1024 + n, or
 //    1024 + 16 n of the half-byte above) and one exact f16 subtraction or fma
 //    that leaves n - 8.
@@ -35,14 +38,15 @@
 namespace q8d {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
-constexpr int kAhead = 4;       // tiles a warp has in flight
-// Strips (of either matrix) summed up at once, for mp rows of the batch, and
-// how many of them a warp's range of a pass may touch.
-__host__ __device__ constexpr int pass_parts(int mp) { return mp <= 8 ? 32 : 16; }
-__host__ __device__ constexpr int pass_slots(int mp) { return pass_parts(mp) / kWarps + 2; }
-constexpr int kMaxSmem = 232448;
+constexpr int kMaxStages = 4;   // copies of a warp in flight
+// Tiles a copy.
+__host__ __device__ constexpr int chunk_tiles(int ng) { return ng == 1 ? 4 : 2; }
+// Strips (of either matrix) that a pass sums up at most, and how many of them a
+// warp's range of a pass may touch.
+constexpr int kMaxParts = 128;
+__host__ __device__ constexpr int pass_slots(int warps, int parts) { return parts / warps + 2; }
+constexpr int kMaxSmem = 232448;   // of a CTA alone on its SM
+constexpr int kHalfSmem = 115712;  // of two (228 KB an SM, 1 KB of it for each CTA)
 
 enum Mode { kF32 = 0, kF16 = 1, kQ8 = 2 };
 
@@ -54,55 +58,76 @@ struct Q4Args {
   int kt;        // tiles a strip
   int cs, ncl;   // CTAs a cluster, clusters
   int ncol;      // columns of the operand in use
-  int passes;
+  int passes, parts;  // strips a pass, at most
+  int stages;         // of a warp's ring
 };
 
+// The operand of the activations in shared memory: a column (a row of X, or its
+// hi or lo part) is ktl tiles of 128 f16 and 64 bytes, so that two neighbouring
+// columns lie in different halves of the banks.
+__host__ __device__ constexpr int x_stride(int ktl) { return ktl * kQ4Cols + 32; }  // f16
+// Scales of the activations a column: a power of two a tile, or one a block of 32.
+__host__ __device__ constexpr int s_stride(int mode, int ktl) {
+  return mode == kF32 ? ktl : mode == kQ8 ? 4 * ktl : 0;
+}
 struct Smem {  // offsets
-  int scale, part, red, total;
+  int scale, part, red, meets, bars, ring;  // (the ring's stages take what is left)
 };
-__host__ __device__ inline Smem smem_layout(int mode, int ng, int ktl, int ncol, bool cluster) {
+__host__ __device__ inline Smem smem_layout(int warps, int mode, int ng, int ktl, int ncol, int parts,
+                                            bool cluster) {
   const int mp = ng * group_rows(mode);
   Smem s;
-  s.scale = ktl * 4 * ncol * 64;
-  // the power of two of every 128 columns, or the scales of every 32
-  s.part = s.scale + (mode == kF32 ? ktl * mp * 4 : mode == kQ8 ? ktl * 4 * mp * 4 : 0);
-  s.part = (s.part + 15) & ~15;
-  s.red = s.part + kWarps * pass_slots(mp) * mp * 16 * 4;
-  s.total = s.red + (cluster ? pass_parts(mp) * mp * 16 * 4 : 0);
+  s.scale = ncol * x_stride(ktl) * 2;
+  s.part = s.scale + ((mp * s_stride(mode, ktl) * 4 + 15) & ~15);
+  s.red = s.part + warps * pass_slots(warps, parts) * mp * 16 * 4;
+  s.meets = s.red + (cluster ? parts * mp * 16 * 4 : 0);
+  s.bars = s.meets + (parts * 4 + 15 & ~15);
+  s.ring = (s.bars + warps * kMaxStages * 8 + 127) & ~127;
   return s;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// The same from zero.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{0f00000000,0f00000000,0f00000000,0f00000000};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Constants of unpack(), kept out of the compiler's sight: with them in
+// registers (w & mask) | magic is one LOP3, as a constant it is two.
+struct Magic {
+  uint32_t k1024, off, sixteenth, off16;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));      // 1024, twice
+    asm volatile("mov.b32 %0, 0x64086408;" : "=r"(off));        // 1032
+    asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));  // 1 / 16
+    asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(off16));      // -72
+  }
+};
 // Eight quants of a word as four pairs of f16 n - 8, columns ascending.
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&p)[4]) {
-  const uint32_t magic = 0x64006400u;  // 1024, twice
-  const __half2 off = __half2half2(__ushort_as_half(0x6408));    // 1032
-  const __half2 sixteenth = __half2half2(__ushort_as_half(0x2c00));  // 1 / 16
-  const __half2 off16 = __half2half2(__ushort_as_half(0xd480));  // -72
+__device__ __forceinline__ void unpack(uint32_t w, const Magic& m, uint32_t (&p)[4]) {
   const uint32_t v = w >> 8;
-  const uint32_t q[4] = {(w & 0x000f000fu) | magic, (w & 0x00f000f0u) | magic, (v & 0x000f000fu) | magic,
-                         (v & 0x00f000f0u) | magic};
+  uint32_t q[4];
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q[0]) : "r"(w), "n"(0x000f000f), "r"(m.k1024));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q[1]) : "r"(w), "n"(0x00f000f0), "r"(m.k1024));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q[2]) : "r"(v), "n"(0x000f000f), "r"(m.k1024));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q[3]) : "r"(v), "n"(0x00f000f0), "r"(m.k1024));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = *reinterpret_cast<const __half2*>(&q[i]);
-    const __half2 r = (i & 1) ? __hfma2(h, sixteenth, off16) : __hsub2(h, off);
-    p[i] = *reinterpret_cast<const uint32_t*>(&r);
+  for (int i = 0; i < 4; i += 2) {
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(q[i]), "r"(m.off));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[i + 1]) : "r"(q[i + 1]), "r"(m.sixteenth), "r"(m.off16));
   }
 }
 
@@ -113,24 +138,26 @@ struct Tile {
 };
 // NS: scales a row and tile (4, 2, 1): words of the two rows' scales
 template <int NS>
-__device__ __forceinline__ void load_tile(const uint8_t* tile, int lane, Tile<NS>& t) {
-  t.a[0] = load_once(tile + 16 * lane);
-  t.a[1] = load_once(tile + 512 + 16 * lane);
+__device__ __forceinline__ void read_tile(const uint8_t* tile, int lane, Tile<NS>& t) {
+  t.a[0] = *reinterpret_cast<const uint4*>(tile + 16 * lane);
+  t.a[1] = *reinterpret_cast<const uint4*>(tile + 512 + 16 * lane);
   const uint8_t* s = tile + kQ4QuantBytes + (lane >> 2) * (4 * NS);
   if constexpr (NS == 4) {
-    const uint4 v = load_once(s);
+    const uint4 v = *reinterpret_cast<const uint4*>(s);
     t.s[0] = v.x, t.s[1] = v.y, t.s[2] = v.z, t.s[3] = v.w;
   } else if constexpr (NS == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(t.s[0]), "=r"(t.s[1]) : "l"(s));
+    const uint2 v = *reinterpret_cast<const uint2*>(s);
+    t.s[0] = v.x, t.s[1] = v.y;
   } else {
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(t.s[0]) : "l"(s));
+    t.s[0] = *reinterpret_cast<const uint32_t*>(s);
   }
 }
 // The scale of row g (h = 0) or g + 8 for block b of 32 columns.
 template <int NS>
 __device__ __forceinline__ float scale_of(const Tile<NS>& t, int h, int b) {
   const int i = h * NS + b * NS / 4;  // the half word
-  return f16_bits_to_f32(i & 1 ? t.s[i / 2] >> 16 : t.s[i / 2] & 0xffffu);
+  const __half2 v = *reinterpret_cast<const __half2*>(&t.s[i / 2]);
+  return i & 1 ? __high2float(v) : __low2float(v);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -140,243 +167,325 @@ __device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
   uint32_t a;
   float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
 
-// The activations' columns [128 k0, 128 (k0 + ktl)) as the MMA's second operand:
-// [tile][block of 32][column][32] f16, eight neighbouring values a lane.
-template <int MODE>
-__device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mp, __half* xf, float* scale) {
+// The activations' columns [128 k0, 128 (k0 + ktl)) as the MMA's second operand.
+// xstep, sstep: x_stride and s_stride.
+template <int MODE, int kWarps>
+__device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int xstep, int sstep, __half* xf,
+                                        float* scale) {
+  constexpr int kLoads = kWarps / 2;  // items a warp loads before it uses the first
   const Q4Params& P = A.P;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int b = lane / 8, at = (lane & 7) * 4;
-  for (int it = warp; it < P.m * ktl; it += kWarps) {
-    const int j = it / ktl, k = it - j * ktl;
-    const int col = (k0 + k) * kQ4Cols + 4 * lane;
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    __half* dst = xf + ((k * 4 + b) * A.ncol + (MODE == kF32 ? 2 * j : j)) * 32 + at;
-    if constexpr (MODE == kF32) {
-      if (col < P.n) {
-        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(P.X) + j * P.ldx + col);
-        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-      }
-      // (bits of magnitudes are ordered as they are; infinities and NaN, the
-      // largest, stay what they are and make the row's sums NaN)
-      uint32_t top = 0;
+  const int at = (lane & 7) * 4;  // in the block of 32
+  // (item 128 columns of a row; rows one behind the other)
+  int j = 0, k = warp;
+  const auto wrap = [&]() {
+    while (k >= ktl && j < P.m) {
+      k -= ktl;
+      ++j;
+    }
+  };
+  wrap();
+  while (j < P.m) {
+    int js[kLoads], ks[kLoads];
+    float4 f[kLoads];                // f32
+    uint2 u[kLoads];                 // f16, or four quants
+    unsigned short d[kLoads];        // the quants' scale
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
-      top = __reduce_max_sync(0xffffffffu, top);
-      const int up = top ? min(14 - ((int)(top >> 23) - 127), 126) : 0;  // largest into [2^14, 2^15)
-      const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-      __half hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = f[e] * by;
-        hi[e] = __float2half_rn(v);
-        lo[e] = __float2half_rn(v - __half2float(hi[e]));
-      }
-      *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(hi);
-      *reinterpret_cast<uint2*>(dst + 32) = *reinterpret_cast<const uint2*>(lo);
-      if (lane == 0) scale[k * mp + j] = __uint_as_float((uint32_t)(127 - up) << 23);
-    } else if constexpr (MODE == kF16) {
-      uint2 v = make_uint2(0, 0);
-      if (col < P.n) v = *reinterpret_cast<const uint2*>(static_cast<const __half*>(P.X) + j * P.ldx + col);
-      *reinterpret_cast<uint2*>(dst) = v;
-    } else {
-      __half q[4] = {};
-      float d = 0.f;
-      if (col < P.n) {
+    for (int l = 0; l < kLoads; ++l) {
+      js[l] = j;
+      ks[l] = k;
+      const int col = (k0 + k) * kQ4Cols + 4 * lane;
+      f[l] = make_float4(0.f, 0.f, 0.f, 0.f);
+      u[l] = make_uint2(0, 0);
+      d[l] = 0;
+      k += kWarps;
+      wrap();
+      const int j = js[l];
+      if (j >= P.m || col >= P.n) continue;
+      if constexpr (MODE == kF32) {
+        f[l] = *reinterpret_cast<const float4*>(static_cast<const float*>(P.X) + j * P.ldx + col);
+      } else if constexpr (MODE == kF16) {
+        u[l] = *reinterpret_cast<const uint2*>(static_cast<const __half*>(P.X) + j * P.ldx + col);
+      } else {
         const uint8_t* blk = static_cast<const uint8_t*>(P.X) + (j * (P.ldx / 32) + col / 32) * kQBlockBytes;
         const unsigned short* w = reinterpret_cast<const unsigned short*>(blk + 2 + at);
-        d = f16_bits_to_f32(*reinterpret_cast<const unsigned short*>(blk));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = __int2half_rn((int)(int8_t)(w[e / 2] >> (8 * (e & 1))));
+        d[l] = *reinterpret_cast<const unsigned short*>(blk);
+        u[l].x = w[0] | (uint32_t)w[1] << 16;
       }
-      *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(q);
-      if (at == 0) scale[(k * 4 + b) * mp + j] = d;
+    }
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int j = js[l], k = ks[l];
+      if (j >= P.m) break;  // (the whole warp)
+      __half* dst = xf + (MODE == kF32 ? 2 * j : j) * xstep + k * kQ4Cols + 4 * lane;
+      if constexpr (MODE == kF32) {
+        const float v[4] = {f[l].x, f[l].y, f[l].z, f[l].w};
+        // (bits of magnitudes are ordered as they are; infinities and NaN, the
+        // largest, stay what they are and make the row's sums NaN)
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int up = top ? min(14 - ((int)(top >> 23) - 127), 126) : 0;  // largest into [2^14, 2^15)
+        const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+        __half hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = v[e] * by;
+          hi[e] = __float2half_rn(w);
+          lo[e] = __float2half_rn(w - __half2float(hi[e]));
+        }
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(hi);
+        *reinterpret_cast<uint2*>(dst + xstep) = *reinterpret_cast<const uint2*>(lo);
+        if (lane == 0) scale[j * sstep + k] = __uint_as_float((uint32_t)(127 - up) << 23);
+      } else if constexpr (MODE == kF16) {
+        *reinterpret_cast<uint2*>(dst) = u[l];
+      } else {
+        __half q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = __int2half_rn((int)(int8_t)(u[l].x >> (8 * e)));
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(q);
+        if (at == 0) scale[j * sstep + k * 4 + lane / 8] = f16_bits_to_f32(d[l]);
+      }
     }
   }
 }
 
-template <int MODE, int NG, int NS>
-__global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Args A) {
-  extern __shared__ __align__(16) uint8_t smem[];
+// kWarps warps a CTA, sixteen an SM
+template <int kWarps, int MODE, int NG, int NS>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Args A) {
+  extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kMp = NG * group_rows(MODE);     // rows of the batch that fit
-  constexpr int kSlots = pass_slots(kMp);
-  constexpr int kSums = MODE == kF32 ? 2 : 4;    // a lane and column group
+  constexpr int kThreads = kWarps * 32;
+  constexpr int kSums = MODE == kF32 ? 2 : 4;  // a lane and column group
+  constexpr int kRec = kQ4QuantBytes + kQ4Rows * NS * 2;
+  constexpr int kChunk = chunk_tiles(NG), kStage = kChunk * kRec;
   const Q4Params& P = A.P;
+  const int slot_floats = pass_slots(kWarps, A.parts) * kMp * 16;  // a warp's parts
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cluster = blockIdx.x / A.cs, rank = blockIdx.x - cluster * A.cs;
-  const int strips = (int)((P.p + kQ4Rows - 1LL) / kQ4Rows), rec = q4_tile_bytes(P.group);
+  const int strips = (int)((P.p + kQ4Rows - 1LL) / kQ4Rows);
   const int u0 = (int)((long long)cluster * strips / A.ncl), u1 = (int)((cluster + 1LL) * strips / A.ncl);
   const int k0 = rank * A.kt / A.cs, ktl = (rank + 1) * A.kt / A.cs - k0;
   const int ktl_max = (A.kt + A.cs - 1) / A.cs;
-  const Smem L = smem_layout(MODE, NG, ktl_max, A.ncol, A.cs > 1);
+  const Smem L = smem_layout(kWarps, MODE, NG, ktl_max, A.ncol, A.parts, A.cs > 1);
   __half* xf = reinterpret_cast<__half*>(smem);
   float* xs = reinterpret_cast<float*>(smem + L.scale);
   float* part = reinterpret_cast<float*>(smem + L.part);
   float* red = reinterpret_cast<float*>(smem + L.red);
+  uint32_t* meets = reinterpret_cast<uint32_t*>(smem + L.meets);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars) + warp * kMaxStages;
+  uint8_t* ring = smem + L.ring + warp * A.stages * kStage;
 
   // The tiles of a pass: parts (a strip of one matrix) one behind the other.
-  const auto address = [&](int unit0, int i) {
-    const int sp = i / ktl, k = i - sp * ktl;
-    const int unit = unit0 + (P.nmat == 2 ? sp >> 1 : sp);
-    return (P.nmat == 2 && (sp & 1) ? P.w[1] : P.w[0]) + ((long long)unit * A.kt + k0 + k) * rec;
+  // This warp's range of them, cut where a part ends, is walked twice: by the
+  // copies and, some stages behind, by the products.
+  struct Walk {
+    int pass, ua, ub;  // the pass and its strips
+    int sp, k, n;      // the part; the next tile of it; tiles left of it here
+    int left;          // tiles left of the range behind those
   };
-  const auto pass_units = [&](int pass, int& a, int& b) {
-    a = u0 + (int)((long long)pass * (u1 - u0) / A.passes);
-    b = u0 + (int)((pass + 1LL) * (u1 - u0) / A.passes);
+  const auto enter = [&](Walk& w, int pass) {  // (n 0: a pass without tiles)
+    w.pass = pass;
+    w.ua = u0 + (int)((long long)pass * (u1 - u0) / A.passes);
+    w.ub = u0 + (int)((pass + 1LL) * (u1 - u0) / A.passes);
+    const int n = (w.ub - w.ua) * P.nmat * ktl, i0 = warp * n / kWarps;
+    w.left = (warp + 1) * n / kWarps - i0;
+    w.sp = i0 / ktl;
+    w.k = i0 - w.sp * ktl;
+    w.n = min(ktl - w.k, w.left);
+    w.left -= w.n;
   };
-  const auto range = [&](int n, int& a, int& b) {
-    a = warp * n / kWarps;
-    b = (warp + 1) * n / kWarps;
+  const auto next_part = [&](Walk& w) {
+    ++w.sp;
+    w.k = 0;
+    w.n = min(ktl, w.left);
+    w.left -= w.n;
   };
 
-  int ua, ub, i0, i1;
-  pass_units(0, ua, ub);
-  range((ub - ua) * P.nmat * ktl, i0, i1);
-  griddep_launch_dependents();
-  // (weights wait for nothing, but another kernel may be writing them: only the
-  // L2 is asked for them before the work in front is done)
-  for (int i = i0; i < min(i1, i0 + kAhead); ++i) {
-    const uint8_t* p = address(ua, i) + lane * 128;
-    if (lane * 128 < rec) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-  }
-  griddep_wait();
-
-  Tile<NS> buf[kAhead];
-  const uint8_t* next;  // the tile behind those in flight
-  int next_i, next_k;   // its place in the pass and in its part
-  const auto start = [&](int unit0) {
-    next_i = i0;
-    if (i0 >= i1) return;
-    next = address(unit0, i0);
-    next_k = i0 % ktl;
+  Walk ahead;  // where the next copy starts
+  int issued = 0;
+  const uint8_t* src = nullptr;
+  const auto locate = [&]() {
+    while (ahead.n == 0) {
+      if (ahead.pass + 1 >= A.passes) return;
+      enter(ahead, ahead.pass + 1);
+    }
+    const int unit = ahead.ua + (P.nmat == 2 ? ahead.sp >> 1 : ahead.sp);
+    src = (P.nmat == 2 && (ahead.sp & 1) ? P.w[1] : P.w[0]) + ((long long)unit * A.kt + k0 + ahead.k) * kRec;
   };
-  const auto fetch = [&](int unit0, Tile<NS>& b) {
-    if (next_i >= i1) return;
-    load_tile<NS>(next, lane, b);
-    ++next_i;
-    next += rec;
-    if (++next_k == ktl) {
-      next_k = 0;
-      if (next_i < i1) next = address(unit0, next_i);
+  const uint64_t policy = policy_evict_first();
+  const auto issue = [&](int stage) {
+    const int n = min(kChunk, ahead.n);
+    if (n == 0) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bars + stage, n * kRec);
+      bulk_g2s(ring + stage * kStage, src, n * kRec, bars + stage, policy);
+    }
+    ++issued;
+    ahead.n -= n;
+    src += n * kRec;
+    if (ahead.n == 0) {
+      next_part(ahead);
+      locate();
     }
   };
-  start(ua);
-#pragma unroll
-  for (int d = 0; d < kAhead; ++d) fetch(ua, buf[d]);
+  griddep_launch_dependents();
+  if (lane == 0)
+    for (int s = 0; s < A.stages; ++s) mbar_init(bars + s, 1);
+  fence_barrier_init();
+  __syncwarp();
+  enter(ahead, 0);
+  locate();
+  // (weights wait for nothing, but another kernel may be writing them: only the
+  // L2 is asked for the first ones before the work in front is done)
+  if (lane == 0 && ahead.n) bulk_prefetch_l2(src, min(A.stages * kChunk, ahead.n) * kRec);
+  griddep_wait();
+  for (int s = 0; s < A.stages; ++s) issue(s);
 
-  build_x<MODE>(A, k0, ktl, kMp, xf, xs);
+  const int xstep = x_stride(ktl_max), sstep = s_stride(MODE, ktl_max);
+  build_x<MODE, kWarps>(A, k0, ktl, xstep, sstep, xf, xs);
   __syncthreads();
 
+  const Magic magic;
+  int stage = 0, taken = 0;
+  uint32_t parity = 0;
+  bool dead = false;  // a copy did not land within the limit: the sums become NaN
+  // (a lane whose column is not in use takes another one's values: its sums are
+  // not looked at)
+  const __half* xq[NG];
+  const float* xsq[NG];  // of row 4 q + t, or of rows 8 q + 2 t and the next
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+    xq[q] = xf + min(8 * q + g, A.ncol - 1) * xstep + 8 * t;
+    xsq[q] = xs + (MODE == kF32 ? 4 * q + t : 8 * q + 2 * t) * sstep;
+  }
   for (int pass = 0; pass < A.passes; ++pass) {
+    Walk w;
+    enter(w, pass);
     float acc[NG][kSums];
 #pragma unroll
     for (int q = 0; q < NG; ++q)
 #pragma unroll
       for (int e = 0; e < kSums; ++e) acc[q][e] = 0.f;
-    int k = i0 < i1 ? i0 % ktl : 0, slot = 0;
-    // a part's sums, [slot][row of the batch][16]
-    const auto flush = [&]() {
-      float* dst = part + (warp * kSlots + slot) * kMp * 16;
+    float* dst = part + warp * slot_floats;  // [part of this warp][row of the batch][16]
+    while (w.n) {
+      const int n = min(kChunk, w.n), k = w.k;
+      if (!dead && !mbar_wait(bars + stage, parity)) dead = true;
+      if (dead) {
 #pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        if constexpr (MODE == kF32) {
-          dst[(4 * q + t) * 16 + g] = acc[q][0];
-          dst[(4 * q + t) * 16 + g + 8] = acc[q][1];
-        } else {
+        for (int q = 0; q < NG; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[(8 * q + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[q][e];
-        }
+          for (int e = 0; e < kSums; ++e) acc[q][e] = __int_as_float(0x7fc00000);
+      } else {
+        const uint8_t* tile = ring + stage * kStage;
 #pragma unroll
-        for (int e = 0; e < kSums; ++e) acc[q][e] = 0.f;
-      }
-      ++slot;
-    };
-    for (int i = i0; i < i1; i += kAhead) {
+        for (int c = 0; c < kChunk; ++c) {
+          if (c < n) {
+            Tile<NS> T;
+            read_tile<NS>(tile + c * kRec, lane, T);
+            float sum[NG][2];  // (f32 rows: of a tile)
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        if (i + d < i1) {
-          const Tile<NS>& T = buf[d];
-          float sum[NG][2];
-          if constexpr (MODE == kF32) {
+            for (int b = 0; b < 4; ++b) {
+              const uint32_t w0 = b == 0 ? T.a[0].x : b == 1 ? T.a[0].y : b == 2 ? T.a[0].z : T.a[0].w;
+              const uint32_t w1 = b == 0 ? T.a[1].x : b == 1 ? T.a[1].y : b == 2 ? T.a[1].z : T.a[1].w;
+              uint32_t r0[4], r1[4];
+              unpack(w0, magic, r0);
+              unpack(w1, magic, r1);
+              const float s0 = scale_of<NS>(T, 0, b), s1 = scale_of<NS>(T, 1, b);
 #pragma unroll
-            for (int q = 0; q < NG; ++q) sum[q][0] = sum[q][1] = 0.f;
-          }
+              for (int q = 0; q < NG; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4*>(xq[q] + k * kQ4Cols + (4 * c + b) * 32);
+                float d[4];
+                mma16816_first(d, r0[0], r1[0], r0[1], r1[1], v.x, v.y);
+                mma16816(d, r0[2], r1[2], r0[3], r1[3], v.z, v.w);
+                if constexpr (MODE == kF32) {
+                  sum[q][0] = b ? fmaf(s0, d[0] + d[1], sum[q][0]) : s0 * (d[0] + d[1]);
+                  sum[q][1] = b ? fmaf(s1, d[2] + d[3], sum[q][1]) : s1 * (d[2] + d[3]);
+                } else if constexpr (MODE == kF16) {
+                  acc[q][0] = fmaf(s0, d[0], acc[q][0]);
+                  acc[q][1] = fmaf(s0, d[1], acc[q][1]);
+                  acc[q][2] = fmaf(s1, d[2], acc[q][2]);
+                  acc[q][3] = fmaf(s1, d[3], acc[q][3]);
+                } else {
+                  const float e0 = xsq[q][(k + c) * 4 + b], e1 = xsq[q][sstep + (k + c) * 4 + b];
+                  acc[q][0] = fmaf(s0 * e0, d[0], acc[q][0]);
+                  acc[q][1] = fmaf(s0 * e1, d[1], acc[q][1]);
+                  acc[q][2] = fmaf(s1 * e0, d[2], acc[q][2]);
+                  acc[q][3] = fmaf(s1 * e1, d[3], acc[q][3]);
+                }
+              }
+            }
+            if constexpr (MODE == kF32) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t w0 = b == 0 ? T.a[0].x : b == 1 ? T.a[0].y : b == 2 ? T.a[0].z : T.a[0].w;
-            const uint32_t w1 = b == 0 ? T.a[1].x : b == 1 ? T.a[1].y : b == 2 ? T.a[1].z : T.a[1].w;
-            uint32_t r0[4], r1[4];
-            unpack(w0, r0);
-            unpack(w1, r1);
-            const float s0 = scale_of<NS>(T, 0, b), s1 = scale_of<NS>(T, 1, b);
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (8 * q + g < A.ncol)
-                x = *reinterpret_cast<const uint4*>(xf + ((k * 4 + b) * A.ncol + 8 * q + g) * 32 + 8 * t);
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816(c, r0[0], r1[0], r0[1], r1[1], x.x, x.y);
-              mma16816(c, r0[2], r1[2], r0[3], r1[3], x.z, x.w);
-              if constexpr (MODE == kF32) {
-                sum[q][0] = fmaf(s0, c[0] + c[1], sum[q][0]);
-                sum[q][1] = fmaf(s1, c[2] + c[3], sum[q][1]);
-              } else if constexpr (MODE == kF16) {
-                acc[q][0] = fmaf(s0, c[0], acc[q][0]);
-                acc[q][1] = fmaf(s0, c[1], acc[q][1]);
-                acc[q][2] = fmaf(s1, c[2], acc[q][2]);
-                acc[q][3] = fmaf(s1, c[3], acc[q][3]);
-              } else {
-                const float2 d2 = *reinterpret_cast<const float2*>(xs + (k * 4 + b) * kMp + 8 * q + 2 * t);
-                acc[q][0] = fmaf(s0 * d2.x, c[0], acc[q][0]);
-                acc[q][1] = fmaf(s0 * d2.y, c[1], acc[q][1]);
-                acc[q][2] = fmaf(s1 * d2.x, c[2], acc[q][2]);
-                acc[q][3] = fmaf(s1 * d2.y, c[3], acc[q][3]);
+              for (int q = 0; q < NG; ++q) {
+                const float by = xsq[q][k + c];
+                acc[q][0] = fmaf(by, sum[q][0], acc[q][0]);
+                acc[q][1] = fmaf(by, sum[q][1], acc[q][1]);
               }
             }
           }
-          if constexpr (MODE == kF32) {
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-              const float by = xs[k * kMp + 4 * q + t];
-              acc[q][0] = fmaf(by, sum[q][0], acc[q][0]);
-              acc[q][1] = fmaf(by, sum[q][1], acc[q][1]);
-            }
-          }
-          fetch(ua, buf[d]);
-          if (++k == ktl) {
-            k = 0;
-            flush();
-          }
+        }
+        __syncwarp();  // (every lane has read the stage)
+        ++taken;
+        issue(stage);
+        if (++stage == A.stages) {
+          stage = 0;
+          parity ^= 1;
         }
       }
-    }
-    if (k != 0) flush();
-    const int n = (ub - ua) * P.nmat * ktl, pa = ua, pu = ub - ua;
-    const int first_n = n;
-    if (pass + 1 < A.passes) {  // the next pass's first tiles
-      pass_units(pass + 1, ua, ub);
-      range((ub - ua) * P.nmat * ktl, i0, i1);
-      start(ua);
+      w.k += n;
+      w.n -= n;
+      if (w.n == 0) {
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) fetch(ua, buf[d]);
+        for (int q = 0; q < NG; ++q) {
+          if constexpr (MODE == kF32) {
+            dst[(4 * q + t) * 16 + g] = acc[q][0];
+            dst[(4 * q + t) * 16 + g + 8] = acc[q][1];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[(8 * q + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[q][e];
+          }
+#pragma unroll
+          for (int e = 0; e < kSums; ++e) acc[q][e] = 0.f;
+        }
+        dst += kMp * 16;
+        next_part(w);
+      }
+    }
+    // Which warps met a part (their ranges follow one another) and which of the
+    // first one's parts it is; it is the others' first.
+    const int pa = w.ua, pu = w.ub - w.ua, parts = pu * P.nmat, all = parts * ktl;
+    for (int sp = threadIdx.x; sp < parts; sp += kThreads) {
+      const int a = ((sp * ktl + 1) * kWarps - 1) / all, b = ((sp + 1) * ktl * kWarps - 1) / all;
+      uint32_t met = 0;
+      for (int v = a; v <= b; ++v)
+        if ((v + 1) * all / kWarps > v * all / kWarps) met |= 1u << v;  // (a warp may have no tile)
+      meets[sp] = met | (uint32_t)(sp - a * all / kWarps / ktl) << 24;
     }
     __syncthreads();
-    // a part's sum over the warps whose ranges meet it, in their order
-    const auto cta_sum = [&](int sp, int j, int row) {
-      const int a = ((sp * ktl + 1) * kWarps - 1) / first_n, b = ((sp + 1) * ktl * kWarps - 1) / first_n;
-      float v = 0.f;
-      for (int w = a; w <= b; ++w) {
-        const int s0 = w * first_n / kWarps;
-        if ((w + 1) * first_n / kWarps == s0) continue;  // (a warp without tiles)
-        v += part[((w * kSlots + sp - s0 / ktl) * kMp + j) * 16 + row];
+    const auto cta_sum = [&](int sp, int j, int row) {  // (in the warps' order)
+      uint32_t met = meets[sp];
+      const float* p = part + j * 16 + row;
+      int v = __ffs(met) - 1;
+      float sum = p[v * slot_floats + (met >> 24) * kMp * 16];
+      met &= (met & 0xffffffu) - 1;
+      while (met & 0xffffffu) {
+        v = __ffs(met) - 1;
+        sum += p[v * slot_floats];
+        met &= met - 1;
       }
-      return v;
+      return sum;
     };
-    const auto finish = [&](int unit, int j, int row, float v, float up) {
+    // pairs (strip, row of the batch) go to half warps; 2048 of them at most
+    const uint32_t by_m = 65536u / P.m + 1;
+    const auto over_m = [&](int x) { return (int)((uint32_t)x * by_m >> 16); };
+    const int row = threadIdx.x & 15, first = threadIdx.x / 16;
+    const auto finish = [&](int unit, int j, float v, float up) {
       const int r = (pa + unit) * kQ4Rows + row;
       if (r >= P.p) return;
       if (P.nmat == 2) {
@@ -388,44 +497,55 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Args A) {
       P.Y[j * P.ldy + r] = v;
     };
     if (A.cs == 1) {
-      for (int o = threadIdx.x; o < pu * P.m * 16; o += kThreads) {
-        const int row = o & 15, j = (o >> 4) % P.m, unit = (o >> 4) / P.m;
+      for (int o = first; o < pu * P.m; o += kThreads / 16) {
+        const int unit = over_m(o), j = o - unit * P.m;
         if (P.nmat == 2)
-          finish(unit, j, row, cta_sum(2 * unit, j, row), cta_sum(2 * unit + 1, j, row));
+          finish(unit, j, cta_sum(2 * unit, j, row), cta_sum(2 * unit + 1, j, row));
         else
-          finish(unit, j, row, cta_sum(unit, j, row), 0.f);
+          finish(unit, j, cta_sum(unit, j, row), 0.f);
       }
-      __syncthreads();
+      if (pass + 1 < A.passes) __syncthreads();
     } else {
-      for (int o = threadIdx.x; o < pu * P.nmat * P.m * 16; o += kThreads) {
-        const int row = o & 15, j = (o >> 4) % P.m, sp = (o >> 4) / P.m;
-        red[o] = cta_sum(sp, j, row);
+      for (int o = first; o < parts * P.m; o += kThreads / 16) {
+        const int sp = over_m(o), j = o - sp * P.m;
+        red[o * 16 + row] = cta_sum(sp, j, row);
       }
       cluster_sync();
-      for (int o = rank * kThreads + threadIdx.x; o < pu * P.m * 16; o += A.cs * kThreads) {
-        const int row = o & 15, j = (o >> 4) % P.m, unit = (o >> 4) / P.m;
-        const int at = ((P.nmat * unit) * P.m + j) * 16 + row;
-        float v = 0.f, up = 0.f;
-        for (int c = 0; c < A.cs; ++c) {
-          v += cluster_load(red + at, c);
-          if (P.nmat == 2) up += cluster_load(red + at + P.m * 16, c);
+      for (int o = rank * (kThreads / 16) + first; o < pu * P.m; o += A.cs * (kThreads / 16)) {
+        const int unit = over_m(o), j = o - unit * P.m;
+        const int at = (P.nmat * unit * P.m + j) * 16 + row;
+        float v[8], up[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[c] = c < A.cs ? cluster_load(red + at, c) : 0.f;
+          up[c] = c < A.cs && P.nmat == 2 ? cluster_load(red + at + P.m * 16, c) : 0.f;
         }
-        finish(unit, j, row, v, up);
+#pragma unroll
+        for (int c = 1; c < 8; ++c) v[0] += v[c], up[0] += up[c];
+        finish(unit, j, v[0], up[0]);
       }
       cluster_sync();  // (the sums are read before they change or their CTA leaves)
+    }
+  }
+  // (no copy is left behind: one that did not land in time is given as long again)
+  for (; taken < issued; ++taken) {
+    mbar_wait(bars + stage, parity);
+    if (++stage == A.stages) {
+      stage = 0;
+      parity ^= 1;
     }
   }
 }
 
 // ---- plan and launch --------------------------------------------------------
-int max_clusters(const void* fn, int cs, int smem, int* out) {
+int max_clusters(const void* fn, int cs, int threads, int smem, int* out) {
   static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int>, int> known;
+  static std::map<std::tuple<const void*, int, int, int>, int> known;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return record_cuda(e);
   std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_tuple(fn, cs, dev);
+  const auto key = std::make_tuple(fn, cs, smem, dev);
   const auto it = known.find(key);
   if (it != known.end()) {
     *out = it->second;
@@ -433,7 +553,7 @@ int max_clusters(const void* fn, int cs, int smem, int* out) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs * 64);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -448,61 +568,97 @@ int max_clusters(const void* fn, int cs, int smem, int* out) {
   return Q8D_OK;
 }
 
-template <int MODE, int NG, int NS>
-int launch(const Q4Params& P, cudaStream_t stream) {
-  const auto kernel = q4_kernel<MODE, NG, NS>;
-  const void* fn = reinterpret_cast<const void*>(kernel);
-  int rc = configure_kernel(fn, kMaxSmem, false);
+// A way of cutting a product up, and what it is expected to take.
+struct Plan {
+  int warps, cs, ncl, passes, parts, stages, smem;
+  double ns;
+};
+// The ways with kWarps warps a CTA against the best so far.
+template <int kWarps, int MODE, int NG, int NS>
+int consider(const Q4Args& A, int strips, Plan* best) {
+  const auto fn = reinterpret_cast<const void*>(q4_kernel<kWarps, MODE, NG, NS>);
+  int rc = configure_kernel(fn, kMaxSmem, true);
   if (rc) return rc;
-  Q4Args A{};
-  A.P = P;
-  A.kt = q4_tiles(P.n);
-  A.ncol = (MODE == kF32 ? 2 : 1) * P.m;
-  const int strips = (int)q4_strips(P.p);
-  // CTAs a cluster: a strip's columns in more parts fill the machine where it
-  // has few strips or leaves a part of it idle in the last round, for two
-  // meetings of the cluster; and many rows of activations need the parts to fit
-  // shared memory.
-  long long best = -1;
-  int smem = 0;
+  constexpr int kStage = chunk_tiles(NG) * (kQ4QuantBytes + kQ4Rows * NS * 2) * kWarps;
+  constexpr int kLimit = kWarps == 8 ? kHalfSmem : kMaxSmem, kCtas = 16 / kWarps;
   for (int cs = 1; cs <= 8 && cs <= A.kt; cs *= 2) {
     const int ktl = (A.kt + cs - 1) / cs;
-    const Smem L = smem_layout(MODE, NG, ktl, A.ncol, cs > 1);
-    if (L.total > kMaxSmem) continue;
-    int most = sm_count();
+    int most = kCtas * sm_count();
     if (cs > 1) {
-      rc = max_clusters(fn, cs, kMaxSmem, &most);
+      rc = max_clusters(fn, cs, kWarps * 32, kLimit, &most);
       if (rc) return rc;
       if (most < 1) continue;
     }
-    const int ncl = std::min(most, strips);
-    const long long cost = (long long)((strips + ncl - 1) / ncl) * P.nmat * ktl + (cs > 1 ? 40 : 0);
-    if (best < 0 || cost < best) {
-      best = cost;
-      A.cs = cs;
-      A.ncl = ncl;
-      smem = L.total;
-    }
+    const int ncl = std::min(most, strips), ctas = ncl * cs > sm_count() ? kCtas : 1;
+    const int units = (strips + ncl - 1) / ncl;
+    // as few passes as leave the rings two copies a warp (or one)
+    int stages = 0, passes = 0, parts = 0, ring = 0;
+    for (int least = std::min(2, kMaxStages); least >= 1 && !stages; --least)
+      for (passes = 1; passes <= units; ++passes) {
+        parts = (units + passes - 1) / passes * A.P.nmat;
+        ring = smem_layout(kWarps, MODE, NG, ktl, A.ncol, parts, cs > 1).ring;
+        if (parts <= kMaxParts && (kLimit - ring) / kStage >= least) {
+          stages = std::min(kMaxStages, (kLimit - ring) / kStage);
+          break;
+        }
+        if (passes > units / 2 && passes < units) passes = units - 1;
+      }
+    if (!stages) continue;
+    // What an SM does, in ns: its CTAs' tiles; 128 columns of a row of X at a
+    // time made into operands, several of them loaded by a warp at once; the
+    // passes' ends; and the two meetings of a cluster.  (With eight warps a CTA
+    // the next call's CTAs start beside this one's; with sixteen the operands of
+    // X are made once an SM.  3584 -> 4608, one row: 5.5 us with eight, 5.8 with
+    // sixteen, 6.4 with two CTAs a cluster; gated 3584 -> 18944, eight rows: 27.6,
+    // 23.8, 25.5; 18944 -> 3584, one row: 15.5 us with one CTA, 12.5 with two.)
+    const double tiles = (double)units * A.P.nmat * ktl * ctas;
+    const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
+    const double ns = tiles * (NG == 1 ? 27 : MODE == kQ8 ? 50 : 36) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
+                      (cs > 1 ? 1000 : 0) +
+                      (kWarps == 16 ? 300 : 0);
+    if (best->cs == 0 || ns < best->ns)
+      *best = {kWarps, cs, ncl, passes, parts, stages, ring + stages * kStage, ns};
   }
-  if (best < 0) return Q8D_EUNSUPPORTED;
-  const int units = (strips + A.ncl - 1) / A.ncl;
-  constexpr int kParts = pass_parts(NG * group_rows(MODE));
-  A.passes = (units * P.nmat + kParts - 1) / kParts;
+  return Q8D_OK;
+}
+
+template <int kWarps, int MODE, int NG, int NS>
+int launch_plan(const Q4Args& A, const Plan& plan, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(A.cs * A.ncl);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(plan.cs * plan.ncl);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = plan.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = A.cs;
+  attr[1].val.clusterDim.x = plan.cs;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, A);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, q4_kernel<kWarps, MODE, NG, NS>, A);
   return e == cudaSuccess ? Q8D_OK : record_cuda(e);
+}
+
+template <int MODE, int NG, int NS>
+int launch(const Q4Params& P, cudaStream_t stream) {
+  Q4Args A{};
+  A.P = P;
+  A.kt = q4_tiles(P.n);
+  A.ncol = (MODE == kF32 ? 2 : 1) * P.m;
+  const int strips = (int)q4_strips(P.p);
+  Plan plan{};
+  int rc = consider<8, MODE, NG, NS>(A, strips, &plan);
+  if (!rc) rc = consider<16, MODE, NG, NS>(A, strips, &plan);
+  if (rc) return rc;
+  if (plan.cs == 0) return Q8D_EUNSUPPORTED;
+  A.cs = plan.cs;
+  A.ncl = plan.ncl;
+  A.stages = plan.stages;
+  A.passes = plan.passes;
+  A.parts = plan.parts;
+  return plan.warps == 8 ? launch_plan<8, MODE, NG, NS>(A, plan, stream) : launch_plan<16, MODE, NG, NS>(A, plan, stream);
 }
 
 template <int MODE, int NG>
