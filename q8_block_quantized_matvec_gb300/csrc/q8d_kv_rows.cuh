@@ -99,6 +99,22 @@ __device__ __forceinline__ void quantize_q4_warp(float x, uint8_t* quants, uint8
 }
 
 // ---- blocks shared by neighbouring lanes ------------------------------------
+// amax / 127 rounded to nearest, without a division: a quotient from the rounded
+// reciprocal, corrected by its exact remainder, is the rounded one (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990), as long as nothing leaves the normal range.
+__device__ __forceinline__ float q8_0_step(float amax) {
+  constexpr float kInv = 1.0f / 127.0f;
+  const float q = __fmul_rn(amax, kInv);
+  const float d = __fmaf_rn(__fmaf_rn(-127.0f, q, amax), kInv, q);
+  return amax > 0x1p-100f && amax < 0x1p100f ? d : __fdiv_rn(amax, 127.0f);
+}
+// (int)roundf(v), halves away from zero: half a step added towards zero cannot
+// reach the next whole number unless the exact sum does.
+__device__ __forceinline__ uint32_t q8_0_round(float v) {
+  return (uint32_t)__float2int_rz(__fadd_rz(v, copysignf(0.5f, v)));
+}
+
 // The 32 / kE lanes of a Q8_0 block (lane `part` holds its elements kE * part
 // and on) quantize it with the operations of quantize_q8_0_warp, so the bytes
 // are the same.  Every lane of the warp calls; lanes that are not live store
@@ -111,23 +127,12 @@ __device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f
 #pragma unroll
   for (int o = 1; o < 32 / kE; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (!live) return;
-  const float d = __fdiv_rn(amax, 127.0f);
+  const float d = q8_0_step(amax);
   const float id = d != 0.f ? __frcp_rn(d) : 0.f;
-  if constexpr (kE == 1) {
-    blk[2 + part] = (uint8_t)(int8_t)(int)roundf(__fmul_rn(f[0], id));
-  } else {
-    unsigned short* q = reinterpret_cast<unsigned short*>(blk + 2 + kE * part);
+  unsigned short* q = reinterpret_cast<unsigned short*>(blk + 2 + kE * part);
 #pragma unroll
-    for (int i = 0; i < kE / 2; ++i) {
-      uint32_t pair = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = (int)roundf(__fmul_rn(f[2 * i + k], id));
-        pair |= (uint32_t)(uint8_t)(int8_t)r << (8 * k);
-      }
-      q[i] = (unsigned short)pair;
-    }
-  }
+  for (int i = 0; i < kE / 2; ++i)
+    q[i] = (unsigned short)__byte_perm(q8_0_round(__fmul_rn(f[2 * i], id)), q8_0_round(__fmul_rn(f[2 * i + 1], id)), 0x0040);
   if (part == 0) *reinterpret_cast<unsigned short*>(blk) = __half_as_ushort(__float2half_rn(d));
 }
 

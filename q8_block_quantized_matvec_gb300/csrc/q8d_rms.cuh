@@ -7,8 +7,8 @@
 // (hi, lo), each square exact as product and fma remainder, each addition with
 // its rounding error by Knuth's two-sum (Moller, Knuth; Dekker's pairs): about
 // 2^-44 relative, so that the factor is 1 / sqrt in 64 bits rounded to f32 but
-// for one row in 10^6.  That costs eleven f32 instructions an element; the FP64
-// pipe (two operations a clock and SM) would take eight clocks for each.
+// for one row in 10^6.  That costs eight packed f32x2 instructions for two
+// elements, four an element; the FP64 pipe takes half a clock of the SM for each.
 #pragma once
 #include "q8d_internal.cuh"
 
@@ -36,16 +36,39 @@ __device__ __forceinline__ void pair_add_square(Pair& p, float v) {
   pair_add(p, s);
   p.lo = __fadd_rn(p.lo, __fmaf_rn(v, v, -s));
 }
+// Two sums side by side, in packed f32x2 arithmetic: p + v^2.  (v * v's own
+// rounding needs no term: what t leaves of v^2 itself is one fma.)
+struct Pair2 {
+  uint64_t hi, lo;
+};
+__device__ __forceinline__ void pair2_add_square(Pair2& p, uint64_t v) {
+  const uint64_t minus = 0xbf800000bf800000ull;  // -1, -1
+  const uint64_t t = add2(p.hi, mul2(v, v));
+  const uint64_t nw = fma2(t, minus, p.hi);  // -(t - hi)
+  const uint64_t e = fma2(add2(t, nw), minus, p.hi);
+  p.lo = add2(add2(p.lo, e), fma2(v, v, nw));
+  p.hi = t;
+}
+__device__ __forceinline__ Pair pair2_join(const Pair2& p) {
+  Pair a, b;
+  unpack2(p.hi, a.hi, b.hi);
+  unpack2(p.lo, a.lo, b.lo);
+  pair_add(a, b);
+  return a;
+}
 // Sum over the lanes that differ in the bits below `width` (a power of two, at
-// most 32); every one of them gets the same value.
+// most 32); every one of them gets the same value (two-sum's error and the sum of
+// the low parts do not depend on the order of two lanes).
 __device__ __forceinline__ Pair pair_sum(Pair p, int width, uint32_t mask) {
-  for (int o = 1; o < width; o <<= 1) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o >= width) break;
     const Pair q{__shfl_xor_sync(mask, p.hi, o), __shfl_xor_sync(mask, p.lo, o)};
-    // (both lanes add the lower one's sum first: the order decides lo's rounding)
-    const bool up = threadIdx.x & o;
-    Pair a = up ? q : p;
-    pair_add(a, up ? p : q);
-    p = a;
+    const float t = __fadd_rn(p.hi, q.hi);
+    const float w = __fsub_rn(t, p.hi);
+    const float e = __fadd_rn(__fsub_rn(p.hi, __fsub_rn(t, w)), __fsub_rn(q.hi, w));
+    p.lo = __fadd_rn(__fadd_rn(p.lo, q.lo), e);
+    p.hi = t;
   }
   return p;
 }
