@@ -21,9 +21,10 @@
 //  * An f32 row enters as f16 hi + lo under a power of two for every 128 columns
 //    (2^-22 relative, at least 2^-39 of the tile's largest), f16 rows as they
 //    are, Q8_0 rows as their whole numbers, their scales applied to the sums.
-//    The products of 32 columns are exact in f32 and summed from zero on the
-//    tensor cores; the scales are applied outside and all further sums are
-//    rounded f32 additions, because the tensor core cuts its own off.
+//    The products are exact in f32; those of one scale, 128 columns at most, are
+//    summed from zero on the tensor cores, the scales are applied outside and all
+//    further sums are rounded f32 additions, because the tensor core cuts its own
+//    off.
 //  * A cluster of CTAs takes whole strips of 16 rows, each of its CTAs a part of
 //    their columns; a CTA's tiles, strip after strip, are cut into equal ranges
 //    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs'
@@ -31,13 +32,16 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <set>
 #include <tuple>
+#include <utility>
 
 #include "q8d_layer.cuh"
 
 namespace q8d {
 namespace {
 
+constexpr int kMaxCluster = 16;  // CTAs (more than eight are no portable size)
 constexpr int kMaxStages = 4;   // copies of a warp in flight
 // Tiles a copy.
 __host__ __device__ constexpr int chunk_tiles(int ng) { return ng == 1 ? 4 : 2; }
@@ -245,10 +249,12 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int xs
       } else if constexpr (MODE == kF16) {
         *reinterpret_cast<uint2*>(dst) = u[l];
       } else {
-        __half q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = __int2half_rn((int)(int8_t)(u[l].x >> (8 * e)));
-        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(q);
+        // (a byte q + 128 under the exponent of 1024, less 1152)
+        const uint32_t w = u[l].x ^ 0x80808080u;
+        uint2 q;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(q.x) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(q.y) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+        *reinterpret_cast<uint2*>(dst) = q;
         if (at == 0) scale[j * sstep + k * 4 + lane / 8] = f16_bits_to_f32(d[l]);
       }
     }
@@ -389,6 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
             Tile<NS> T;
             read_tile<NS>(tile + c * kRec, lane, T);
             float sum[NG][2];  // (f32 rows: of a tile)
+            float d[NG][4];    // (of a scale's columns)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               const uint32_t w0 = b == 0 ? T.a[0].x : b == 1 ? T.a[0].y : b == 2 ? T.a[0].z : T.a[0].w;
@@ -400,23 +407,28 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
 #pragma unroll
               for (int q = 0; q < NG; ++q) {
                 const uint4 v = *reinterpret_cast<const uint4*>(xq[q] + k * kQ4Cols + (4 * c + b) * 32);
-                float d[4];
-                mma16816_first(d, r0[0], r1[0], r0[1], r1[1], v.x, v.y);
-                mma16816(d, r0[2], r1[2], r0[3], r1[3], v.z, v.w);
+                // (Q8_0 rows have a scale of their own every 32 columns)
+                constexpr int kSame = MODE == kQ8 ? 1 : 4 / NS;
+                if (b % kSame == 0)
+                  mma16816_first(d[q], r0[0], r1[0], r0[1], r1[1], v.x, v.y);
+                else
+                  mma16816(d[q], r0[0], r1[0], r0[1], r1[1], v.x, v.y);
+                mma16816(d[q], r0[2], r1[2], r0[3], r1[3], v.z, v.w);
+                if (b % kSame != kSame - 1) continue;
                 if constexpr (MODE == kF32) {
-                  sum[q][0] = b ? fmaf(s0, d[0] + d[1], sum[q][0]) : s0 * (d[0] + d[1]);
-                  sum[q][1] = b ? fmaf(s1, d[2] + d[3], sum[q][1]) : s1 * (d[2] + d[3]);
+                  sum[q][0] = b >= kSame ? fmaf(s0, d[q][0] + d[q][1], sum[q][0]) : s0 * (d[q][0] + d[q][1]);
+                  sum[q][1] = b >= kSame ? fmaf(s1, d[q][2] + d[q][3], sum[q][1]) : s1 * (d[q][2] + d[q][3]);
                 } else if constexpr (MODE == kF16) {
-                  acc[q][0] = fmaf(s0, d[0], acc[q][0]);
-                  acc[q][1] = fmaf(s0, d[1], acc[q][1]);
-                  acc[q][2] = fmaf(s1, d[2], acc[q][2]);
-                  acc[q][3] = fmaf(s1, d[3], acc[q][3]);
+                  acc[q][0] = fmaf(s0, d[q][0], acc[q][0]);
+                  acc[q][1] = fmaf(s0, d[q][1], acc[q][1]);
+                  acc[q][2] = fmaf(s1, d[q][2], acc[q][2]);
+                  acc[q][3] = fmaf(s1, d[q][3], acc[q][3]);
                 } else {
                   const float e0 = xsq[q][(k + c) * 4 + b], e1 = xsq[q][sstep + (k + c) * 4 + b];
-                  acc[q][0] = fmaf(s0 * e0, d[0], acc[q][0]);
-                  acc[q][1] = fmaf(s0 * e1, d[1], acc[q][1]);
-                  acc[q][2] = fmaf(s1 * e0, d[2], acc[q][2]);
-                  acc[q][3] = fmaf(s1 * e1, d[3], acc[q][3]);
+                  acc[q][0] = fmaf(s0 * e0, d[q][0], acc[q][0]);
+                  acc[q][1] = fmaf(s0 * e1, d[q][1], acc[q][1]);
+                  acc[q][2] = fmaf(s1 * e0, d[q][2], acc[q][2]);
+                  acc[q][3] = fmaf(s1 * e1, d[q][3], acc[q][3]);
                 }
               }
             }
@@ -514,15 +526,14 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
       for (int o = rank * (kThreads / 16) + first; o < pu * P.m; o += A.cs * (kThreads / 16)) {
         const int unit = over_m(o), j = o - unit * P.m;
         const int at = (P.nmat * unit * P.m + j) * 16 + row;
-        float v[8], up[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          v[c] = c < A.cs ? cluster_load(red + at, c) : 0.f;
-          up[c] = c < A.cs && P.nmat == 2 ? cluster_load(red + at + P.m * 16, c) : 0.f;
+        float v = 0.f, up = 0.f;
+        for (int c0 = 0; c0 < A.cs; c0 += 2) {
+          const float a = cluster_load(red + at, c0), b = cluster_load(red + at, c0 + 1);
+          float d = 0.f, e = 0.f;
+          if (P.nmat == 2) d = cluster_load(red + at + P.m * 16, c0), e = cluster_load(red + at + P.m * 16, c0 + 1);
+          v += a, v += b, up += d, up += e;
         }
-#pragma unroll
-        for (int c = 1; c < 8; ++c) v[0] += v[c], up[0] += up[c];
-        finish(unit, j, v[0], up[0]);
+        finish(unit, j, v, up);
       }
       cluster_sync();  // (the sums are read before they change or their CTA leaves)
     }
@@ -568,20 +579,42 @@ int max_clusters(const void* fn, int cs, int threads, int smem, int* out) {
   return Q8D_OK;
 }
 
+// Lets a kernel be launched in clusters of sixteen (once a device).
+int allow_wide_clusters(const void* fn) {
+  static std::mutex mu;
+  static std::set<std::pair<const void*, int>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return record_cuda(e);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({fn, dev})) return Q8D_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return record_cuda(e);
+  done.insert({fn, dev});
+  return Q8D_OK;
+}
+
 // A way of cutting a product up, and what it is expected to take.
 struct Plan {
   int warps, cs, ncl, passes, parts, stages, smem;
   double ns;
 };
+// ns of an SM a tile, measured with calls of 400 and more: the issue slots bound
+// them, and with many columns the operand's reads from shared memory.
+constexpr double tile_ns(int mode, int ng) {
+  return ng == 4 ? 95 : ng == 2 ? (mode == kF32 ? 39 : mode == kF16 ? 45 : 65) : mode == kQ8 ? 35 : 27;
+}
 // The ways with kWarps warps a CTA against the best so far.
 template <int kWarps, int MODE, int NG, int NS>
 int consider(const Q4Args& A, int strips, Plan* best) {
   const auto fn = reinterpret_cast<const void*>(q4_kernel<kWarps, MODE, NG, NS>);
   int rc = configure_kernel(fn, kMaxSmem, true);
   if (rc) return rc;
+  rc = allow_wide_clusters(fn);
+  if (rc) return rc;
   constexpr int kStage = chunk_tiles(NG) * (kQ4QuantBytes + kQ4Rows * NS * 2) * kWarps;
   constexpr int kLimit = kWarps == 8 ? kHalfSmem : kMaxSmem, kCtas = 16 / kWarps;
-  for (int cs = 1; cs <= 8 && cs <= A.kt; cs *= 2) {
+  for (int cs = 1; cs <= kMaxCluster && cs <= A.kt; cs *= 2) {
     const int ktl = (A.kt + cs - 1) / cs;
     int most = kCtas * sm_count();
     if (cs > 1) {
@@ -613,7 +646,7 @@ int consider(const Q4Args& A, int strips, Plan* best) {
     // 23.8, 25.5; 18944 -> 3584, one row: 15.5 us with one CTA, 12.5 with two.)
     const double tiles = (double)units * A.P.nmat * ktl * ctas;
     const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
-    const double ns = tiles * (NG == 1 ? 27 : MODE == kQ8 ? 50 : 36) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
+    const double ns = tiles * tile_ns(MODE, NG) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
                       (cs > 1 ? 1000 : 0) +
                       (kWarps == 16 ? 300 : 0);
     if (best->cs == 0 || ns < best->ns)
@@ -641,24 +674,61 @@ int launch_plan(const Q4Args& A, const Plan& plan, cudaStream_t stream) {
   return e == cudaSuccess ? Q8D_OK : record_cuda(e);
 }
 
+// The best way for a product of P.m rows (plan.cs 0: none fits).
+template <int MODE, int NG, int NS>
+int make_plan(const Q4Params& P, Q4Args* A, Plan* plan) {
+  *A = Q4Args{};
+  A->P = P;
+  A->kt = q4_tiles(P.n);
+  A->ncol = (MODE == kF32 ? 2 : 1) * P.m;
+  *plan = Plan{};
+  const int strips = (int)q4_strips(P.p);
+  int rc = consider<8, MODE, NG, NS>(*A, strips, plan);
+  if (!rc) rc = consider<16, MODE, NG, NS>(*A, strips, plan);
+  A->cs = plan->cs;
+  A->ncl = plan->ncl;
+  A->stages = plan->stages;
+  A->passes = plan->passes;
+  A->parts = plan->parts;
+  return rc;
+}
+
+template <int MODE, int NG, int NS>
+int launch_made(const Q4Args& A, const Plan& plan, cudaStream_t stream) {
+  if (plan.cs == 0) return Q8D_EUNSUPPORTED;
+  return plan.warps == 8 ? launch_plan<8, MODE, NG, NS>(A, plan, stream) : launch_plan<16, MODE, NG, NS>(A, plan, stream);
+}
+
 template <int MODE, int NG, int NS>
 int launch(const Q4Params& P, cudaStream_t stream) {
-  Q4Args A{};
-  A.P = P;
-  A.kt = q4_tiles(P.n);
-  A.ncol = (MODE == kF32 ? 2 : 1) * P.m;
-  const int strips = (int)q4_strips(P.p);
-  Plan plan{};
-  int rc = consider<8, MODE, NG, NS>(A, strips, &plan);
-  if (!rc) rc = consider<16, MODE, NG, NS>(A, strips, &plan);
+  Q4Args A;
+  Plan plan;
+  const int rc = make_plan<MODE, NG, NS>(P, &A, &plan);
+  return rc ? rc : launch_made<MODE, NG, NS>(A, plan, stream);
+}
+
+// 9 to 16 f32 rows: in one launch, or as eight and the others, whichever is
+// expected to be faster (16 rows, us for one / two: 3584 -> 3584 11.3 / 16.8, 18944
+// -> 3584 32.3 / 38.7, gated 3584 -> 18944 50.8 / 46.4).
+template <int NS>
+int launch_wide(const Q4Params& P, cudaStream_t stream) {
+  Q4Args all, head;
+  Plan pa, ph;
+  int rc = make_plan<kF32, 4, NS>(P, &all, &pa);
   if (rc) return rc;
-  if (plan.cs == 0) return Q8D_EUNSUPPORTED;
-  A.cs = plan.cs;
-  A.ncl = plan.ncl;
-  A.stages = plan.stages;
-  A.passes = plan.passes;
-  A.parts = plan.parts;
-  return plan.warps == 8 ? launch_plan<8, MODE, NG, NS>(A, plan, stream) : launch_plan<16, MODE, NG, NS>(A, plan, stream);
+  Q4Params Q = P;
+  Q.m = 8;
+  rc = make_plan<kF32, 2, NS>(Q, &head, &ph);
+  if (rc) return rc;
+  // (eight rows take as long as five, and four about two thirds of that; a launch 4 us)
+  if (pa.cs && (!ph.cs || pa.ns <= ph.ns * (P.m > 12 ? 2.0 : 1.7) + 4000)) return launch_made<kF32, 4, NS>(all, pa, stream);
+  rc = launch_made<kF32, 2, NS>(head, ph, stream);
+  if (rc) return rc;
+  Q.m = P.m - 8;
+  Q.X = static_cast<const float*>(P.X) + 8 * P.ldx;
+  Q.Y = P.Y + 8 * P.ldy;
+  Q.residual = P.residual ? P.residual + 8 * P.ldr : nullptr;
+  return Q.m > 4 ? launch<kF32, 2, NS>(Q, stream) : launch<kF32, 1, NS>(Q, stream);
 }
 
 template <int MODE, int NG>
@@ -670,27 +740,15 @@ int launch_g(const Q4Params& P, cudaStream_t stream) {
   }
 }
 
-template <int MODE>
-int launch_m(const Q4Params& P, cudaStream_t stream) {
-  return P.m <= group_rows(MODE) ? launch_g<MODE, 1>(P, stream) : launch_g<MODE, 2>(P, stream);
-}
-
 }  // namespace
 
 int q4_launch(const Q4Params& P, cudaStream_t stream) {
-  if (P.x_dtype == Q8D_KV_F16) return launch_m<kF16>(P, stream);
-  if (P.x_dtype == Q8D_KV_Q8_0) return launch_m<kQ8>(P, stream);
-  // f32 rows take two columns each: eight rows a launch
-  Q4Params Q = P;
-  for (int j = 0; j < P.m; j += 8) {
-    Q.m = std::min(8, P.m - j);
-    Q.X = static_cast<const float*>(P.X) + j * P.ldx;
-    Q.Y = P.Y + j * P.ldy;
-    Q.residual = P.residual ? P.residual + j * P.ldr : nullptr;
-    const int rc = launch_m<kF32>(Q, stream);
-    if (rc) return rc;
-  }
-  return Q8D_OK;
+  if (P.x_dtype == Q8D_KV_F16) return P.m <= 8 ? launch_g<kF16, 1>(P, stream) : launch_g<kF16, 2>(P, stream);
+  if (P.x_dtype == Q8D_KV_Q8_0) return P.m <= 8 ? launch_g<kQ8, 1>(P, stream) : launch_g<kQ8, 2>(P, stream);
+  // (f32 rows take two columns each)
+  if (P.m <= 4) return launch_g<kF32, 1>(P, stream);
+  if (P.m <= 8) return launch_g<kF32, 2>(P, stream);
+  return P.group == 32 ? launch_wide<4>(P, stream) : P.group == 64 ? launch_wide<2>(P, stream) : launch_wide<1>(P, stream);
 }
 
 }  // namespace q8d

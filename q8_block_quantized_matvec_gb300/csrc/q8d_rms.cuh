@@ -56,19 +56,24 @@ __device__ __forceinline__ Pair pair2_join(const Pair2& p) {
   pair_add(a, b);
   return a;
 }
+// p + q, the same whichever of two lanes adds: two-sum's error does not depend on
+// the order, nor does the sum of the low parts.
+__device__ __forceinline__ Pair pair_meet(const Pair& p, const Pair& q) {
+  const float t = __fadd_rn(p.hi, q.hi);
+  const float w = __fsub_rn(t, p.hi);
+  const float e = __fadd_rn(__fsub_rn(p.hi, __fsub_rn(t, w)), __fsub_rn(q.hi, w));
+  return {t, __fadd_rn(__fadd_rn(p.lo, q.lo), e)};
+}
+__device__ __forceinline__ Pair pair_shfl_xor(const Pair& p, int o, uint32_t mask) {
+  return {__shfl_xor_sync(mask, p.hi, o), __shfl_xor_sync(mask, p.lo, o)};
+}
 // Sum over the lanes that differ in the bits below `width` (a power of two, at
-// most 32); every one of them gets the same value (two-sum's error and the sum of
-// the low parts do not depend on the order of two lanes).
+// most 32); every one of them gets the same value.
 __device__ __forceinline__ Pair pair_sum(Pair p, int width, uint32_t mask) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     if (o >= width) break;
-    const Pair q{__shfl_xor_sync(mask, p.hi, o), __shfl_xor_sync(mask, p.lo, o)};
-    const float t = __fadd_rn(p.hi, q.hi);
-    const float w = __fsub_rn(t, p.hi);
-    const float e = __fadd_rn(__fsub_rn(p.hi, __fsub_rn(t, w)), __fsub_rn(q.hi, w));
-    p.lo = __fadd_rn(__fadd_rn(p.lo, q.lo), e);
-    p.hi = t;
+    p = pair_meet(p, pair_shfl_xor(p, o, mask));
   }
   return p;
 }

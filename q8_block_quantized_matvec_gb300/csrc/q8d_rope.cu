@@ -27,6 +27,7 @@
 // plain formulas whatever the compiler contracts.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "q8d_kv_rows.cuh"
 #include "q8d_layer.cuh"
@@ -67,102 +68,184 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableArgs A) {
 
 // ---- the rows ---------------------------------------------------------------
 constexpr int kWarps = 8;
-constexpr int kHeads = 4;  // heads (or groups of narrow ones) a warp at most
+constexpr int kSteps = 4;  // steps a warp at most
 
+// A row's work is steps of one head each (several narrow ones).  A warp takes up
+// to kSteps of q, of k or of v.
 struct RopeArgs {
   RopeRowsParams P;
   FastDiv chunks;  // warps a row
-  int cq, ck;      // of them for q and for each of k and v
-  int per;         // heads (groups) a warp
+  int cq, ck;      // of them for q, and for each of k and v
+  int per;         // steps a warp
+  int rpw;         // rows a warp, one after the other
   int lph;         // lanes a head: a power of two
   Pair inv_n;
-  bool vec_in, vec_out;
 };
 
-template <typename T, int kE>
-__device__ __forceinline__ void get(const T* p, bool vec, float (&f)[kE]) {
-  if (!vec) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) f[e] = (float)p[e];
-    return;
-  }
-  if constexpr (sizeof(T) == 4) {
+// How rows are moved and turned: 16 bytes (8 of f16) at once with a lane's
+// partners in one other lane (kHalves) or beside them (kPairs); or element by
+// element, partners through shared memory, which serves every case.
+enum Way { kHalves, kPairs, kAny };
+
+// kE elements of a row as they lie in memory.
+template <typename T, int kE, bool vec>
+__device__ __forceinline__ void get_raw(const T* p, uint32_t (&w)[kE * sizeof(T) / 4]) {
+  if constexpr (vec) {
 #pragma unroll
     for (int e = 0; e < kE; e += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(p + e);
-      f[e] = a.x, f[e + 1] = a.y, f[e + 2] = a.z, f[e + 3] = a.w;
+      if constexpr (sizeof(T) == 4) {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p + e));
+        w[e] = a.x, w[e + 1] = a.y, w[e + 2] = a.z, w[e + 3] = a.w;
+      } else {
+        const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p + e));
+        w[e / 2] = a.x, w[e / 2 + 1] = a.y;
+      }
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < kE; e += 4) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p + e);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-      f[e] = a.x, f[e + 1] = a.y, f[e + 2] = b.x, f[e + 3] = b.y;
+    for (int e = 0; e < kE; ++e) {
+      if constexpr (sizeof(T) == 4)
+        w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+      else
+        w[e / 2] = e & 1 ? w[e / 2] | (uint32_t) reinterpret_cast<const unsigned short*>(p)[e] << 16
+                         : reinterpret_cast<const unsigned short*>(p)[e];
     }
   }
 }
 template <typename T, int kE>
-__device__ __forceinline__ void put(T* p, bool vec, const float (&f)[kE]) {
-  if (!vec) {
+__device__ __forceinline__ void expand(const uint32_t (&w)[kE * sizeof(T) / 4], uint64_t (&f)[kE / 2]) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) p[e] = (T)f[e];
-    return;
+  for (int i = 0; i < kE / 2; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[i] = pack2(t.x, t.y);
+    }
   }
+}
+template <typename T, int kE, bool vec>
+__device__ __forceinline__ void put(T* p, const uint64_t (&f)[kE / 2]) {
+  float v[kE];
+#pragma unroll
+  for (int i = 0; i < kE / 2; ++i) unpack2(f[i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
   for (int e = 0; e < kE; e += 4) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    if constexpr (!vec) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[e + i] = (T)v[e + i];
+    } else if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     } else {
-      const __half2 a = __floats2half2_rn(f[e], f[e + 1]), b = __floats2half2_rn(f[e + 2], f[e + 3]);
+      const __half2 a = __floats2half2_rn(v[e], v[e + 1]), b = __floats2half2_rn(v[e + 2], v[e + 3]);
       *reinterpret_cast<uint2*>(p + e) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
   }
 }
 // f32 vectors that every row reads.
-template <int kE>
-__device__ __forceinline__ void get_shared(const float* p, float (&f)[kE]) {
+template <int kE, bool vec>
+__device__ __forceinline__ void get_shared(const float* p, uint64_t (&f)[kE / 2]) {
 #pragma unroll
-  for (int e = 0; e < kE; ++e) f[e] = __ldg(p + e);
+  for (int e = 0; e < kE; e += 4) {
+    const float4 a = vec ? __ldg(reinterpret_cast<const float4*>(p + e))
+                         : make_float4(__ldg(p + e), __ldg(p + e + 1), __ldg(p + e + 2), __ldg(p + e + 3));
+    f[e / 2] = pack2(a.x, a.y);
+    f[e / 2 + 1] = pack2(a.z, a.w);
+  }
 }
 
 // cos and signed sin of kE elements from el on of the rotated part: element e
 // becomes c[e] x[e] + s[e] partner[e].
-template <int kE>
-__device__ __forceinline__ void angles(const float* row, int half, int layout, int el, float (&c)[kE],
-                                       float (&s)[kE]) {
-  if (layout == Q8D_ROPE_HALF && half % kE == 0) {
+template <int kE, int WAY>
+__device__ __forceinline__ void angles(const float* row, int half, int layout, int el, uint64_t (&c)[kE / 2],
+                                       uint64_t (&s)[kE / 2]) {
+  if constexpr (WAY == kHalves) {
     const bool up = el >= half;
     const float* p = row + (up ? el - half : el);
+    const float sign = up ? 1.f : -1.f;
+    get_shared<kE, true>(p, c);
+    get_shared<kE, true>(p + half, s);
 #pragma unroll
-    for (int e = 0; e < kE; e += 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p + e));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(p + half + e));
-      c[e] = a.x, c[e + 1] = a.y, c[e + 2] = a.z, c[e + 3] = a.w;
-      s[e] = b.x, s[e + 1] = b.y, s[e + 2] = b.z, s[e + 3] = b.w;
+    for (int e = 0; e < kE / 2; ++e) s[e] = mul2(s[e], pack2(sign, sign));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; e += 2) {
+    if (WAY == kPairs || layout == Q8D_ROPE_PAIRS) {
+      const int i = (el + e) / 2;
+      const float cv = i < half ? __ldg(row + i) : 1.f, sv = i < half ? __ldg(row + half + i) : 0.f;
+      c[e / 2] = pack2(cv, cv);
+      s[e / 2] = pack2(-sv, sv);
+      continue;
     }
+    float cv[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < kE; ++e) s[e] = up ? s[e] : -s[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int j = el + e;
-      c[e] = 1.f;
-      s[e] = 0.f;
+    for (int o = 0; o < 2; ++o) {
+      const int j = el + e + o;
       if (j >= 2 * half) continue;
-      const bool up = layout == Q8D_ROPE_HALF ? j >= half : (j & 1);
-      const int i = layout == Q8D_ROPE_HALF ? (up ? j - half : j) : j / 2;
-      c[e] = __ldg(row + i);
-      s[e] = __ldg(row + half + i);
-      s[e] = up ? s[e] : -s[e];
+      const bool up = j >= half;
+      const int i = up ? j - half : j;
+      cv[o] = __ldg(row + i);
+      sv[o] = __ldg(row + half + i);
+      if (!up) sv[o] = -sv[o];
     }
+    c[e / 2] = pack2(cv[0], cv[1]);
+    s[e / 2] = pack2(sv[0], sv[1]);
   }
 }
 
-template <typename T, int KV, int kE>
-__global__ void __launch_bounds__(kWarps * 32) rope_rows_kernel(const RopeArgs A) {
-  __shared__ float turn[kWarps][32 * kE];  // (half layouts whose halves cut a lane's elements)
+// The factors of kSteps heads' norms.  ss: this lane's squares of each step;
+// valid(u): whether step u of this lane's head is normed.  The sums of four
+// steps are folded together: lanes that differ in bit 0 exchange two of them
+// each, in bit 1 one, and from there on lane l carries step l & 3, so that a
+// warp adds six times where one step after the other would take twenty.
+template <int kE, typename Valid>
+__device__ __forceinline__ void head_factors(const Pair (&ss)[kSteps], const uint64_t (&f)[kSteps][kE / 2],
+                                             const RopeArgs& A, int lane, Valid valid, float (&inv)[kSteps]) {
+  static_assert(kSteps == 4, "");
+  const auto meet = [](const Pair& keep, const Pair& send, int o) {
+    return pair_meet(keep, pair_shfl_xor(send, o, 0xffffffffu));
+  };
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const Pair a0 = meet(b0 ? ss[1] : ss[0], b0 ? ss[0] : ss[1], 1);
+  const Pair a1 = meet(b0 ? ss[3] : ss[2], b0 ? ss[2] : ss[3], 1);
+  Pair p = meet(b1 ? a1 : a0, b1 ? a0 : a1, 2);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+    if (o < A.lph) p = meet(p, p, o);
+  const float eps = A.P.d.eps;
+  const int mine = lane & 3;
+  float r = rms_factor(p, A.inv_n, eps);
+  const bool good = !valid(mine) || rms_in_range(p);
+  if (!__all_sync(0xffffffffu, good)) {
+    double d[kSteps];
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      d[u] = 0.0;
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        float x, y;
+        unpack2(f[u][e], x, y);
+        d[u] += (double)x * (double)x;
+        d[u] += (double)y * (double)y;
+      }
+      for (int o = 1; o < A.lph; o <<= 1) d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
+    }
+    const double all = mine == 0 ? d[0] : mine == 1 ? d[1] : mine == 2 ? d[2] : d[3];
+    if (!good) r = rms_factor_wide(all, A.P.d.head_dim, eps);
+  }
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) inv[u] = __shfl_sync(0xffffffffu, r, (lane & ~3) | u);
+}
+
+// (three CTAs an SM, us for 4096 rows of 16 / 8 heads of 128 from f32 into f16: two
+// 27.5, three 25.6, four 31.7)
+template <typename T, int KV, int kE, bool kNorm, int WAY>
+__global__ void __launch_bounds__(kWarps * 32, kE == 4 ? 3 : 2) rope_rows_kernel(const RopeArgs A) {
+  constexpr int kP = kE / 2, kW = kE * sizeof(T) / 4;
+  constexpr bool kVec = WAY != kAny;
+  __shared__ float turn[WAY == kAny ? kWarps : 1][32 * kE];
   griddep_launch_dependents();
   griddep_wait();
   const RopeRowsParams& P = A.P;
@@ -171,125 +254,181 @@ __global__ void __launch_bounds__(kWarps * 32) rope_rows_kernel(const RopeArgs A
   const int sub = lane / A.lph, hpw = 32 / A.lph, el = (lane & (A.lph - 1)) * kE;
   const int half = D.rot_dim / 2;
   const uint32_t item = blockIdx.x * kWarps + warp;
+  const int row0 = (int)A.chunks.div(item), chunk = (int)(item - (uint32_t)row0 * A.chunks.d);
+  // the segment (0 q, 1 k, 2 v), this lane's first head and how many steps have one
+  const int g = chunk < A.cq ? 0 : chunk < A.cq + A.ck ? 1 : 2;
+  const int first = (chunk - (g == 0 ? 0 : g == 1 ? A.cq : A.cq + A.ck)) * A.per * hpw;
+  const int heads = g ? D.n_kv_heads : D.n_heads, head = first + sub;
+  const int steps = min(A.per, (heads - first + hpw - 1) / hpw);  // (the warp's)
+  const int mine = el < D.head_dim ? min(steps, (heads - head + hpw - 1) / hpw) : 0;
+  const int col = head * D.head_dim + el, stride = hpw * D.head_dim;  // a step's elements
   const int width = D.n_kv_heads * D.head_dim;
+  const bool turns = g < 2 && el < D.rot_dim;
+  const float* bias = g == 0 ? D.bq : g == 1 ? D.bk : D.bv;
+  const long long ld = g ? D.ldkv : D.ldq;
+  uint64_t wn[kP];  // the heads' norm weights
+#pragma unroll
+  for (int e = 0; e < kP; ++e) wn[e] = 0;
+  if (kNorm && g < 2 && el < D.head_dim) get_shared<kE, kVec>((g ? D.k_norm : D.q_norm) + el, wn);
   for (int s = blockIdx.y; s < P.batch; s += gridDim.y) {
     const int pos = P.d_pos[s], rpos = P.d_rope_pos ? P.d_rope_pos[s] : pos;
-    int count = P.d_counts ? P.d_counts[s] : P.rows;
+    const int count = P.d_counts ? P.d_counts[s] : P.rows;
     int bad = 0;
     if (count < 0 || count > P.rows)
       bad = Q8D_DERR_LEN_RANGE;
     else if (count > 0 && ((P.k && (pos < 0 || pos > D.cap - count)) || rpos < 0 || rpos > D.max_pos - count))
       bad = Q8D_DERR_POS_RANGE;
     if (bad && P.d_err && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.d_err, bad);
-    // (a refused sequence: its q rows become NaN, nothing of it is stored)
-    if (bad) count = P.rows;
-    if (item >= (uint32_t)count * A.chunks.d) continue;  // (the whole warp)
-    const int row = (int)A.chunks.div(item), chunk = (int)(item - (uint32_t)row * A.chunks.d);
-    const int seg = chunk < A.cq ? 0 : chunk < A.cq + A.ck ? 1 : 2;
-    if (bad && seg) continue;
-    const int heads = seg ? D.n_kv_heads : D.n_heads;
-    const int h0 = (chunk - (seg == 0 ? 0 : seg == 1 ? A.cq : A.cq + A.ck)) * A.per * hpw + sub;
-    const long long ld = seg ? D.ldkv : D.ldq, r = (long long)s * P.rows + row;
-    const T* src = static_cast<const T*>(seg == 0 ? P.q : seg == 1 ? P.k : P.v) + r * ld + el;
-    const float* bias = seg == 0 ? D.bq : seg == 1 ? D.bk : D.bv;
-    const float* norm = seg == 0 ? D.q_norm : seg == 1 ? D.k_norm : nullptr;
-    const bool in = el < D.head_dim;
-    float f[kHeads][kE], c[kE], sn[kE], wn[kE];
+    // (a refused sequence: its q rows become NaN, nothing is stored)
+    if (bad && g) continue;
+    int row = row0 * A.rpw;
+    const int end = min(bad ? P.rows : count, row + A.rpw);
+    if (row >= end) continue;  // (the whole warp)
+    long long r = (long long)s * P.rows + row;
+    const T* src = static_cast<const T*>(g == 0 ? P.q : g == 1 ? P.k : P.v) + r * ld + col;
+    const float* table = D.table + (bad ? 0 : ((long long)rpos + row) * D.rot_dim);
+    // the next row's values and angles are on their way while a row is worked on
+    uint32_t raw[kSteps][kW];
+    uint64_t c[kP], sn[kP];
+    const auto fetch = [&]() {
 #pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      const int head = h0 + u * hpw;
+      for (int u = 0; u < kSteps; ++u) {
 #pragma unroll
-      for (int e = 0; e < kE; ++e) f[u][e] = 0.f;
-      if (u < A.per && head < heads && in) get<T, kE>(src + head * D.head_dim, A.vec_in, f[u]);
+        for (int e = 0; e < kW; ++e) raw[u][e] = 0;
+        if (u < mine) get_raw<T, kE, kVec>(src + u * stride, raw[u]);
+      }
+#pragma unroll
+      for (int e = 0; e < kP; ++e) c[e] = sn[e] = 0;
+      if (turns && !bad) angles<kE, WAY>(table, half, D.layout, el, c, sn);
+    };
+    fetch();
+   for (;; ++row, ++r) {
+    uint64_t f[kSteps][kP], cc[kP], cs[kP];
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) expand<T, kE>(raw[u], f[u]);
+#pragma unroll
+    for (int e = 0; e < kP; ++e) cc[e] = c[e], cs[e] = sn[e];
+    if (row + 1 < end) {
+      src += ld;
+      if (!bad) table += D.rot_dim;
+      fetch();
     }
-    const bool turns = seg < 2 && el < D.rot_dim && !bad;
+    if (bias) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) c[e] = 1.f, sn[e] = 0.f, wn[e] = 0.f;
-    if (turns) angles<kE>(D.table + ((long long)rpos + row) * D.rot_dim, half, D.layout, el, c, sn);
-    if (norm && in) get_shared<kE>(norm + el, wn);
+      for (int u = 0; u < kSteps; ++u) {
+        if (u >= mine) continue;
+        uint64_t b[kP];
+        get_shared<kE, kVec>(bias + col + u * stride, b);
 #pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      if (u >= A.per) break;
-      const int head = h0 + u * hpw;
-      const bool live = head < heads && in;
-      if (bias && live) {
-        float b[kE];
-        get_shared<kE>(bias + head * D.head_dim + el, b);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) f[u][e] = __fadd_rn(f[u][e], b[e]);
+        for (int e = 0; e < kP; ++e) f[u][e] = add2(f[u][e], b[e]);
       }
-      if (norm) {
-        Pair ss{0.f, 0.f};
+    }
+    if constexpr (kNorm) {
+      if (g < 2) {
+        Pair ss[kSteps];
 #pragma unroll
-        for (int e = 0; e < kE; ++e) pair_add_square(ss, f[u][e]);
-        ss = pair_sum(ss, A.lph, 0xffffffffu);
-        float inv = rms_factor(ss, A.inv_n, D.eps);
-        const bool good = head >= heads || rms_in_range(ss);
-        if (!__all_sync(0xffffffffu, good)) {
-          double d = 0.0;
+        for (int u = 0; u < kSteps; ++u) {
+          Pair2 both{0, 0};
 #pragma unroll
-          for (int e = 0; e < kE; ++e) d += (double)f[u][e] * (double)f[u][e];
-          for (int o = 1; o < A.lph; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-          if (!good) inv = rms_factor_wide(d, D.head_dim, D.eps);
+          for (int e = 0; e < kP; ++e) pair2_add_square(both, f[u][e]);
+          ss[u] = pair2_join(both);
         }
+        float inv[kSteps];
+        head_factors<kE>(ss, f, A, lane, [&](int u) { return head + u * hpw < heads && u < steps; }, inv);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) f[u][e] = __fmul_rn(__fmul_rn(f[u][e], inv), wn[e]);
+        for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+          for (int e = 0; e < kP; ++e) f[u][e] = mul2(mul2(f[u][e], pack2(inv[u], inv[u])), wn[e]);
       }
-      if (seg < 2 && half) {
-        float g[kE];
-        if (D.layout == Q8D_ROPE_PAIRS) {
+    }
+    if (g < 2 && half) {
+      const int by = half / kE, from = turns ? (el < half ? lane + by : lane - by) : lane;
 #pragma unroll
-          for (int e = 0; e < kE; ++e) g[e] = f[u][e ^ 1];
-        } else if (half % kE == 0) {
-          const int by = half / kE, from = turns ? (el < half ? lane + by : lane - by) : lane;
+      for (int u = 0; u < kSteps; ++u) {
+        if (u >= steps) break;
+        float p[kE];  // the partners
+        if constexpr (WAY == kPairs) {
 #pragma unroll
-          for (int e = 0; e < kE; ++e) g[e] = __shfl_sync(0xffffffffu, f[u][e], from);
+          for (int e = 0; e < kP; ++e) unpack2(f[u][e], p[2 * e + 1], p[2 * e]);
+        } else if constexpr (WAY == kHalves) {
+#pragma unroll
+          for (int e = 0; e < kP; ++e) unpack2(__shfl_sync(0xffffffffu, f[u][e], from), p[2 * e], p[2 * e + 1]);
         } else {
+          float* t = turn[warp] + lane * kE;
           __syncwarp();
 #pragma unroll
-          for (int e = 0; e < kE; ++e) turn[warp][lane * kE + e] = f[u][e];
+          for (int e = 0; e < kP; ++e) unpack2(f[u][e], t[2 * e], t[2 * e + 1]);
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < kE; ++e) {
             const int j = el + e;
-            g[e] = turn[warp][lane * kE + e + (j < half ? half : j < 2 * half ? -half : 0)];
+            p[e] = t[e + (j >= 2 * half                    ? 0
+                          : D.layout == Q8D_ROPE_PAIRS     ? 1 - 2 * (j & 1)
+                          : j < half                       ? half
+                                                           : -half)];
           }
         }
+        // (elements behind rot_dim, which may end inside a lane's, are as they were;
+        // scalar steps, each rounded: packed products are contracted into the sum)
         if (turns) {
 #pragma unroll
-          for (int e = 0; e < kE; ++e)
-            if (el + e < 2 * half) f[u][e] = __fadd_rn(__fmul_rn(f[u][e], c[e]), __fmul_rn(g[e], sn[e]));
+          for (int e = 0; e < kP; ++e) {
+            if (el + 2 * e >= 2 * half) break;
+            float x[2], cv[2], sv[2];
+            unpack2(f[u][e], x[0], x[1]);
+            unpack2(cc[e], cv[0], cv[1]);
+            unpack2(cs[e], sv[0], sv[1]);
+            f[u][e] = pack2(__fadd_rn(__fmul_rn(x[0], cv[0]), __fmul_rn(p[2 * e], sv[0])),
+                            __fadd_rn(__fmul_rn(x[1], cv[1]), __fmul_rn(p[2 * e + 1], sv[1])));
+          }
         }
-      }
-      if (seg == 0) {
-        if (bad) {
-#pragma unroll
-          for (int e = 0; e < kE; ++e) f[u][e] = __int_as_float(0x7fc00000);
-        }
-        const long long at = r * D.ldo + head * D.head_dim + el;
-        if (live) {
-          if (D.q_dtype == Q8D_KV_F16)
-            put<__half, kE>(static_cast<__half*>(P.q_out) + at, A.vec_out, f[u]);
-          else
-            put<float, kE>(static_cast<float*>(P.q_out) + at, A.vec_out, f[u]);
-        }
-        continue;
-      }
-      uint8_t* cache = (seg == 1 ? P.kc : P.vc) + P.seq_bytes * s;
-      const long long cr = (long long)pos + row;
-      const int col = head * D.head_dim + el;
-      if constexpr (KV == Q8D_KV_Q4) {
-        put_q4<kE>(cache + cr * (width / 2) + col / 32 * 16,
-                   cache + q4_scale_plane(D.cap, width) + cr * (width / 16) + col / 32 * 2,
-                   lane & (32 / kE - 1), f[u], live);
-      } else if constexpr (KV == Q8D_KV_Q8_0) {
-        put_q8_0<kE>(cache + (cr * (width / kQBlock) + col / 32) * kQBlockBytes, lane & (32 / kE - 1), f[u], live);
-      } else if constexpr (KV == Q8D_KV_F16) {
-        if (live) put<__half, kE>(reinterpret_cast<__half*>(cache) + cr * width + col, true, f[u]);
-      } else {
-        if (live) put<float, kE>(reinterpret_cast<float*>(cache) + cr * width + col, true, f[u]);
       }
     }
+    if (g == 0) {
+      if (bad) {
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+          for (int e = 0; e < kP; ++e) f[u][e] = 0x7fc000007fc00000ull;
+      }
+      const long long at = r * D.ldo + col;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        if (u >= mine) break;
+        if (D.q_dtype == Q8D_KV_F16)
+          put<__half, kE, kVec>(static_cast<__half*>(P.q_out) + at + u * stride, f[u]);
+        else
+          put<float, kE, kVec>(static_cast<float*>(P.q_out) + at + u * stride, f[u]);
+      }
+      if (row + 1 >= end) break;
+      continue;
+    }
+    uint8_t* cache = (g == 1 ? P.kc : P.vc) + P.seq_bytes * s;
+    const long long cr = (long long)pos + row;
+    if constexpr (KV == Q8D_KV_Q4 || KV == Q8D_KV_Q8_0) {
+      uint8_t* blk = KV == Q8D_KV_Q4 ? cache + cr * (width / 2) + col / 32 * 16
+                                     : cache + (cr * (width / kQBlock) + col / 32) * kQBlockBytes;
+      uint8_t* scale = cache + q4_scale_plane(D.cap, width) + cr * (width / 16) + col / 32 * 2;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        if (u >= steps) break;
+        float v[kE];
+#pragma unroll
+        for (int e = 0; e < kP; ++e) unpack2(f[u][e], v[2 * e], v[2 * e + 1]);
+        if constexpr (KV == Q8D_KV_Q4)
+          put_q4<kE>(blk + u * (stride / 2), scale + u * (stride / 16), lane & (32 / kE - 1), v, u < mine);
+        else
+          put_q8_0<kE>(blk + u * (stride / 32 * kQBlockBytes), lane & (32 / kE - 1), v, u < mine);
+      }
+    } else {
+      using C = typename std::conditional<KV == Q8D_KV_F16, __half, float>::type;
+      C* dst = reinterpret_cast<C*>(cache) + cr * width + col;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+        if (u < mine) put<C, kE, true>(dst + u * stride, f[u]);
+    }
+    if (row + 1 >= end) break;
+   }
   }
 }
 
@@ -303,23 +442,34 @@ int launch_rope(const RopeRowsParams& P, cudaStream_t stream) {
   if (A.lph < 32 / kE) A.lph = 32 / kE;  // (a packed block's lanes)
   const int hpw = 32 / A.lph;
   const int sq = P.q ? (D.n_heads + hpw - 1) / hpw : 0, sk = P.k ? (D.n_kv_heads + hpw - 1) / hpw : 0;
-  // four heads a warp once that leaves two full machines of warps, else one,
-  // for the latency
-  A.per = (long long)P.batch * P.rows * (sq + 2 * sk) >= 4LL * 2 * 64 * sm_count() ? kHeads : 1;
+  // four steps a warp once that leaves two full machines of warps, else one, for
+  // the latency
+  A.per = (long long)P.batch * P.rows * (sq + 2 * sk) >= 4LL * 2 * 64 * sm_count() ? kSteps : 1;
   A.cq = (sq + A.per - 1) / A.per;
   A.ck = (sk + A.per - 1) / A.per;
   A.chunks = fast_div((uint32_t)(A.cq + 2 * A.ck));
   A.inv_n = pair_inverse(D.head_dim);
-  const long long items = (long long)P.rows * A.chunks.d;
+  // several rows a warp once that leaves two machines of warps, too
+  A.rpw = (int)std::max(1LL, std::min(8LL, (long long)P.batch * P.rows * A.chunks.d / (2LL * 16 * sm_count())));
+  const long long items = (P.rows + A.rpw - 1LL) / A.rpw * A.chunks.d;
   if (items > 0xffff0000LL) return Q8D_EUNSUPPORTED;  // (item numbers are 32 bits)
   // 16-byte accesses (8 of f16) where every row allows them
   const uintptr_t in = 4 * sizeof(T), out = D.q_dtype == Q8D_KV_F16 ? 8 : 16;
   const auto on = [](const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; };
-  A.vec_in = (!P.q || (on(P.q, in) && D.ldq % 4 == 0)) &&
-             (!P.k || (on(P.k, in) && on(P.v, in) && D.ldkv % 4 == 0));
-  A.vec_out = !P.q || (on(P.q_out, out) && D.ldo % 4 == 0);
+  const bool vec = (!P.q || (on(P.q, in) && D.ldq % 4 == 0 && on(P.q_out, out) && D.ldo % 4 == 0)) &&
+                   (!P.k || (on(P.k, in) && on(P.v, in) && D.ldkv % 4 == 0)) && on(D.bq, 16) && on(D.bk, 16) &&
+                   on(D.bv, 16) && on(D.q_norm, 16) && on(D.k_norm, 16);
+  const bool whole = D.layout == Q8D_ROPE_PAIRS || D.rot_dim % (2 * kE) == 0;
   const dim3 grid((unsigned)((items + kWarps - 1) / kWarps), (unsigned)std::min(P.batch, 65535));
-  return launch_ex(rope_rows_kernel<T, KV, kE>, grid, dim3(kWarps * 32), 0, stream, true, A);
+  const auto run = [&](auto* kernel) { return launch_ex(kernel, grid, dim3(kWarps * 32), 0, stream, true, A); };
+  if (D.q_norm) {
+    if (!vec || !whole) return run(rope_rows_kernel<T, KV, kE, true, kAny>);
+    return D.layout == Q8D_ROPE_PAIRS ? run(rope_rows_kernel<T, KV, kE, true, kPairs>)
+                                      : run(rope_rows_kernel<T, KV, kE, true, kHalves>);
+  }
+  if (!vec || !whole) return run(rope_rows_kernel<T, KV, kE, false, kAny>);
+  return D.layout == Q8D_ROPE_PAIRS ? run(rope_rows_kernel<T, KV, kE, false, kPairs>)
+                                    : run(rope_rows_kernel<T, KV, kE, false, kHalves>);
 }
 
 template <typename T, int KV>
