@@ -601,8 +601,8 @@ struct Plan {
 };
 // ns of an SM a tile, measured with calls of 400 and more: the issue slots bound
 // them, and with many columns the operand's reads from shared memory.
-constexpr double tile_ns(int mode, int ng) {
-  return ng == 4 ? 95 : ng == 2 ? (mode == kF32 ? 39 : mode == kF16 ? 45 : 65) : mode == kQ8 ? 35 : 27;
+constexpr double tile_ns(int mode, int ng, int scales) {
+  return ng == 4 ? 70 + 6 * scales : ng == 2 ? (mode == kF32 ? 39 : mode == kF16 ? 45 : 65) : mode == kQ8 ? 35 : 27;
 }
 // The ways with kWarps warps a CTA against the best so far.
 template <int kWarps, int MODE, int NG, int NS>
@@ -646,7 +646,7 @@ int consider(const Q4Args& A, int strips, Plan* best) {
     // 23.8, 25.5; 18944 -> 3584, one row: 15.5 us with one CTA, 12.5 with two.)
     const double tiles = (double)units * A.P.nmat * ktl * ctas;
     const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
-    const double ns = tiles * tile_ns(MODE, NG) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
+    const double ns = tiles * tile_ns(MODE, NG, NS) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
                       (cs > 1 ? 1000 : 0) +
                       (kWarps == 16 ? 300 : 0);
     if (best->cs == 0 || ns < best->ns)
