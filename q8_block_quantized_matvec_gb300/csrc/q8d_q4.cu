@@ -30,6 +30,7 @@
 //    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs'
 //    through the cluster's, both in a fixed order.
 #include <algorithm>
+#include <array>
 #include <map>
 #include <mutex>
 #include <set>
@@ -674,23 +675,43 @@ int launch_plan(const Q4Args& A, const Plan& plan, cudaStream_t stream) {
   return e == cudaSuccess ? Q8D_OK : record_cuda(e);
 }
 
-// The best way for a product of P.m rows (plan.cs 0: none fits).
+// The best way for a product of P.m rows (plan.cs 0: none fits).  It depends on
+// sizes alone and takes the host about as long as a launch: it is kept for them.
 template <int MODE, int NG, int NS>
 int make_plan(const Q4Params& P, Q4Args* A, Plan* plan) {
+  static std::mutex mu;
+  static std::map<std::array<int, 5>, Plan> known;
   *A = Q4Args{};
   A->P = P;
   A->kt = q4_tiles(P.n);
   A->ncol = (MODE == kF32 ? 2 : 1) * P.m;
   *plan = Plan{};
   const int strips = (int)q4_strips(P.p);
-  int rc = consider<8, MODE, NG, NS>(*A, strips, plan);
-  if (!rc) rc = consider<16, MODE, NG, NS>(*A, strips, plan);
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return record_cuda(e);
+  const std::array<int, 5> key = {dev, P.m, A->kt, strips, P.nmat};
+  bool found = false;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = known.find(key);
+    found = it != known.end();
+    if (found) *plan = it->second;
+  }
+  if (!found) {
+    int rc = consider<8, MODE, NG, NS>(*A, strips, plan);
+    if (!rc) rc = consider<16, MODE, NG, NS>(*A, strips, plan);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(mu);
+    if (known.size() >= 4096) known.clear();
+    known[key] = *plan;
+  }
   A->cs = plan->cs;
   A->ncl = plan->ncl;
   A->stages = plan->stages;
   A->passes = plan->passes;
   A->parts = plan->parts;
-  return rc;
+  return Q8D_OK;
 }
 
 template <int MODE, int NG, int NS>

@@ -449,8 +449,20 @@ int launch_rope(const RopeRowsParams& P, cudaStream_t stream) {
   A.ck = (sk + A.per - 1) / A.per;
   A.chunks = fast_div((uint32_t)(A.cq + 2 * A.ck));
   A.inv_n = pair_inverse(D.head_dim);
-  // several rows a warp once that leaves two machines of warps, too
-  A.rpw = (int)std::max(1LL, std::min(8LL, (long long)P.batch * P.rows * A.chunks.d / (2LL * 16 * sm_count())));
+  // Rows a warp: whole rounds of resident CTAs, of which one costs its rows and
+  // about one and a half for starting (4096 rows of 16 / 8 heads: 8 rows make 512
+  // CTAs, a round and an eighth of them).
+  const long long slots = (kE == 4 ? 3LL : 2LL) * sm_count();
+  double best = 0.0;
+  for (int r = 1; r <= 32; ++r) {
+    long long ctas = ((P.rows + r - 1LL) / r * A.chunks.d + kWarps - 1) / kWarps * P.batch;
+    if (P.batch > 1 && P.d_counts) ctas = ctas * 5 / 8;  // (what a ragged batch's may be)
+    const double cost = (double)((ctas + slots - 1) / slots) * (r + 1.5);
+    if (r == 1 || cost < best) {
+      best = cost;
+      A.rpw = r;
+    }
+  }
   const long long items = (P.rows + A.rpw - 1LL) / A.rpw * A.chunks.d;
   if (items > 0xffff0000LL) return Q8D_EUNSUPPORTED;  // (item numbers are 32 bits)
   // 16-byte accesses (8 of f16) where every row allows them
