@@ -165,7 +165,7 @@ int q8d_rope_append_rows(const q8d_rope_desc* d, const void* q, const void* k, c
     if (!aligned(p, 4)) return Q8D_EALIGN;
   if (d->rot_dim && !aligned(d->table, 16)) return Q8D_EALIGN;
   const long long all = (long long)batch * rows;
-  if (all > 0x7fffffffLL) return Q8D_EUNSUPPORTED;
+  if (all > 0x7fff0000LL) return Q8D_EUNSUPPORTED;  // (row numbers are 32 bits)
   if (rows == 0) return Q8D_OK;
   const Span sq = rows_span(q, d->row_dtype, all, d->ldq, qw), sk = rows_span(k, d->row_dtype, all, d->ldkv, kw),
              sv = rows_span(v, d->row_dtype, all, d->ldkv, kw),
