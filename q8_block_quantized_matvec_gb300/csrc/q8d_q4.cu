@@ -605,53 +605,58 @@ struct Plan {
 constexpr double tile_ns(int mode, int ng, int scales) {
   return ng == 4 ? 70 + 6 * scales : ng == 2 ? (mode == kF32 ? 39 : mode == kF16 ? 45 : 65) : mode == kQ8 ? 35 : 27;
 }
-// The ways with kWarps warps a CTA against the best so far.
+// Clusters of cs CTAs of kWarps warps, at most `most` of them, against the best
+// way so far.
+template <int kWarps, int MODE, int NG, int NS>
+void weigh(const Q4Args& A, int strips, int cs, int most, Plan* best) {
+  constexpr int kStage = chunk_tiles(NG) * (kQ4QuantBytes + kQ4Rows * NS * 2) * kWarps;
+  constexpr int kLimit = kWarps == 8 ? kHalfSmem : kMaxSmem;
+  const int ktl = (A.kt + cs - 1) / cs, ncl = std::min(most, strips), units = (strips + ncl - 1) / ncl;
+  const int ctas = ncl * cs > sm_count() ? 16 / kWarps : 1;  // an SM
+  // as few passes as leave the rings two copies a warp (or one)
+  int stages = 0, passes = 0, parts = 0, ring = 0;
+  for (int least = 2; least >= 1 && !stages; --least)
+    for (int u = std::min(units, kMaxParts / A.P.nmat); u >= 1; u -= (u + 7) / 8) {
+      passes = (units + u - 1) / u;
+      parts = (units + passes - 1) / passes * A.P.nmat;
+      ring = smem_layout(kWarps, MODE, NG, ktl, A.ncol, parts, cs > 1).ring;
+      if ((kLimit - ring) / kStage >= least) {
+        stages = std::min(kMaxStages, (kLimit - ring) / kStage);
+        break;
+      }
+    }
+  if (!stages) return;
+  // What an SM does, in ns: its CTAs' tiles (one CTA of eight warps is a little
+  // slower at them); 128 columns of a row of X at a time made into operands,
+  // several of them loaded by a warp at once; the passes' ends; the two meetings
+  // of a cluster; and what a call takes longer whose CTAs leave no room for the
+  // next one's.
+  const double tiles = (double)units * A.P.nmat * ktl * ctas * (kWarps == 8 && ctas == 1 ? 1.12 : 1.0);
+  const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
+  const double ns = tiles * tile_ns(MODE, NG, NS) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
+                    (cs > 1 ? 1000 : 0) + (kWarps == 16 ? 800 : ctas == 2 ? 500 : 0);
+  if (best->cs == 0 || ns < best->ns)
+    *best = {kWarps, cs, ncl, passes, parts, stages, ring + stages * kStage, ns};
+}
+
+// The ways with kWarps warps a CTA: clusters of every size, and eight warps also
+// as one CTA an SM.  Measured, us: 3584 -> 4608, one row, eight warps 5.3, two such
+// CTAs an SM 5.6, sixteen warps 5.8, two CTAs a cluster 6.4; gated 3584 -> 18944,
+// eight rows, 27.6 (clusters of four), -, 23.2, 24.5; 18944 -> 3584, one row, -,
+// 12.2 (clusters of eight), 15.5, 12.4.
 template <int kWarps, int MODE, int NG, int NS>
 int consider(const Q4Args& A, int strips, Plan* best) {
   const auto fn = reinterpret_cast<const void*>(q4_kernel<kWarps, MODE, NG, NS>);
   int rc = configure_kernel(fn, kMaxSmem, true);
+  if (!rc) rc = allow_wide_clusters(fn);
   if (rc) return rc;
-  rc = allow_wide_clusters(fn);
-  if (rc) return rc;
-  constexpr int kStage = chunk_tiles(NG) * (kQ4QuantBytes + kQ4Rows * NS * 2) * kWarps;
-  constexpr int kLimit = kWarps == 8 ? kHalfSmem : kMaxSmem, kCtas = 16 / kWarps;
-  for (int cs = 1; cs <= kMaxCluster && cs <= A.kt; cs *= 2) {
-    const int ktl = (A.kt + cs - 1) / cs;
-    int most = kCtas * sm_count();
-    if (cs > 1) {
-      rc = max_clusters(fn, cs, kWarps * 32, kLimit, &most);
-      if (rc) return rc;
-      if (most < 1) continue;
-    }
-    const int ncl = std::min(most, strips), ctas = ncl * cs > sm_count() ? kCtas : 1;
-    const int units = (strips + ncl - 1) / ncl;
-    // as few passes as leave the rings two copies a warp (or one)
-    int stages = 0, passes = 0, parts = 0, ring = 0;
-    for (int least = std::min(2, kMaxStages); least >= 1 && !stages; --least)
-      for (passes = 1; passes <= units; ++passes) {
-        parts = (units + passes - 1) / passes * A.P.nmat;
-        ring = smem_layout(kWarps, MODE, NG, ktl, A.ncol, parts, cs > 1).ring;
-        if (parts <= kMaxParts && (kLimit - ring) / kStage >= least) {
-          stages = std::min(kMaxStages, (kLimit - ring) / kStage);
-          break;
-        }
-        if (passes > units / 2 && passes < units) passes = units - 1;
-      }
-    if (!stages) continue;
-    // What an SM does, in ns: its CTAs' tiles; 128 columns of a row of X at a
-    // time made into operands, several of them loaded by a warp at once; the
-    // passes' ends; and the two meetings of a cluster.  (With eight warps a CTA
-    // the next call's CTAs start beside this one's; with sixteen the operands of
-    // X are made once an SM.  3584 -> 4608, one row: 5.5 us with eight, 5.8 with
-    // sixteen, 6.4 with two CTAs a cluster; gated 3584 -> 18944, eight rows: 27.6,
-    // 23.8, 25.5; 18944 -> 3584, one row: 15.5 us with one CTA, 12.5 with two.)
-    const double tiles = (double)units * A.P.nmat * ktl * ctas;
-    const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
-    const double ns = tiles * tile_ns(MODE, NG, NS) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
-                      (cs > 1 ? 1000 : 0) +
-                      (kWarps == 16 ? 300 : 0);
-    if (best->cs == 0 || ns < best->ns)
-      *best = {kWarps, cs, ncl, passes, parts, stages, ring + stages * kStage, ns};
+  if (kWarps == 8) weigh<kWarps, MODE, NG, NS>(A, strips, 1, sm_count(), best);
+  weigh<kWarps, MODE, NG, NS>(A, strips, 1, 16 / kWarps * sm_count(), best);
+  for (int cs = 2; cs <= kMaxCluster && cs <= A.kt; cs *= 2) {
+    int most = 0;
+    rc = max_clusters(fn, cs, kWarps * 32, kWarps == 8 ? kHalfSmem : kMaxSmem, &most);
+    if (rc) return rc;
+    if (most >= 1) weigh<kWarps, MODE, NG, NS>(A, strips, cs, most, best);
   }
   return Q8D_OK;
 }
