@@ -71,9 +71,10 @@ struct Q4Args {
 // hi or lo part) is ktl tiles of 128 f16 and 64 bytes, so that two neighbouring
 // columns lie in different halves of the banks.
 __host__ __device__ constexpr int x_stride(int ktl) { return ktl * kQ4Cols + 32; }  // f16
-// Scales of the activations a column: a power of two a tile, or one a block of 32.
-__host__ __device__ constexpr int s_stride(int mode, int ktl) {
-  return mode == kF32 ? ktl : mode == kQ8 ? 4 * ktl : 0;
+// Scales of the activations: a power of two a row and tile, [row][tile], or one a
+// row and block of 32, [block][row], so that a lane's two rows lie side by side.
+__host__ __device__ constexpr int scale_floats(int mode, int mp, int ktl) {
+  return mode == kF32 ? mp * ktl : mode == kQ8 ? mp * 4 * ktl : 0;
 }
 struct Smem {  // offsets
   int scale, part, red, meets, bars, ring;  // (the ring's stages take what is left)
@@ -83,7 +84,7 @@ __host__ __device__ inline Smem smem_layout(int warps, int mode, int ng, int ktl
   const int mp = ng * group_rows(mode);
   Smem s;
   s.scale = ncol * x_stride(ktl) * 2;
-  s.part = s.scale + ((mp * s_stride(mode, ktl) * 4 + 15) & ~15);
+  s.part = s.scale + ((scale_floats(mode, mp, ktl) * 4 + 15) & ~15);
   s.red = s.part + warps * pass_slots(warps, parts) * mp * 16 * 4;
   s.meets = s.red + (cluster ? parts * mp * 16 * 4 : 0);
   s.bars = s.meets + (parts * 4 + 15 & ~15);
@@ -177,9 +178,9 @@ __device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
 }
 
 // The activations' columns [128 k0, 128 (k0 + ktl)) as the MMA's second operand.
-// xstep, sstep: x_stride and s_stride.
-template <int MODE, int kWarps>
-__device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int xstep, int sstep, __half* xf,
+// xstep: x_stride; most: tiles of the largest part of a row.
+template <int MODE, int kWarps, int kMp>
+__device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int most, int xstep, __half* xf,
                                         float* scale) {
   constexpr int kLoads = kWarps / 2;  // items a warp loads before it uses the first
   const Q4Params& P = A.P;
@@ -246,7 +247,7 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int xs
         }
         *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(hi);
         *reinterpret_cast<uint2*>(dst + xstep) = *reinterpret_cast<const uint2*>(lo);
-        if (lane == 0) scale[j * sstep + k] = __uint_as_float((uint32_t)(127 - up) << 23);
+        if (lane == 0) scale[j * most + k] = __uint_as_float((uint32_t)(127 - up) << 23);
       } else if constexpr (MODE == kF16) {
         *reinterpret_cast<uint2*>(dst) = u[l];
       } else {
@@ -256,7 +257,7 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int xs
         asm("sub.f16x2 %0, %1, %2;" : "=r"(q.x) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
         asm("sub.f16x2 %0, %1, %2;" : "=r"(q.y) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
         *reinterpret_cast<uint2*>(dst) = q;
-        if (at == 0) scale[j * sstep + k * 4 + lane / 8] = f16_bits_to_f32(d[l]);
+        if (at == 0) scale[(k * 4 + lane / 8) * kMp + j] = f16_bits_to_f32(d[l]);
       }
     }
   }
@@ -354,8 +355,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
   griddep_wait();
   for (int s = 0; s < A.stages; ++s) issue(s);
 
-  const int xstep = x_stride(ktl_max), sstep = s_stride(MODE, ktl_max);
-  build_x<MODE, kWarps>(A, k0, ktl, xstep, sstep, xf, xs);
+  const int xstep = x_stride(ktl_max);
+  build_x<MODE, kWarps, kMp>(A, k0, ktl, ktl_max, xstep, xf, xs);
   __syncthreads();
 
   const Magic magic;
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
 #pragma unroll
   for (int q = 0; q < NG; ++q) {
     xq[q] = xf + min(8 * q + g, A.ncol - 1) * xstep + 8 * t;
-    xsq[q] = xs + (MODE == kF32 ? 4 * q + t : 8 * q + 2 * t) * sstep;
+    xsq[q] = xs + (MODE == kF32 ? (4 * q + t) * ktl_max : 8 * q + 2 * t);
   }
   for (int pass = 0; pass < A.passes; ++pass) {
     Walk w;
@@ -425,11 +426,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
                   acc[q][2] = fmaf(s1, d[q][2], acc[q][2]);
                   acc[q][3] = fmaf(s1, d[q][3], acc[q][3]);
                 } else {
-                  const float e0 = xsq[q][(k + c) * 4 + b], e1 = xsq[q][sstep + (k + c) * 4 + b];
-                  acc[q][0] = fmaf(s0 * e0, d[q][0], acc[q][0]);
-                  acc[q][1] = fmaf(s0 * e1, d[q][1], acc[q][1]);
-                  acc[q][2] = fmaf(s1 * e0, d[q][2], acc[q][2]);
-                  acc[q][3] = fmaf(s1 * e1, d[q][3], acc[q][3]);
+                  const float2 e = *reinterpret_cast<const float2*>(xsq[q] + ((k + c) * 4 + b) * kMp);
+                  acc[q][0] = fmaf(s0 * e.x, d[q][0], acc[q][0]);
+                  acc[q][1] = fmaf(s0 * e.y, d[q][1], acc[q][1]);
+                  acc[q][2] = fmaf(s1 * e.x, d[q][2], acc[q][2]);
+                  acc[q][3] = fmaf(s1 * e.y, d[q][3], acc[q][3]);
                 }
               }
             }
