@@ -12,8 +12,8 @@
 //  * Tiles lie in memory in the order in which lanes feed them (q8d_layer.cuh):
 //    two 16-byte reads a lane take a tile from shared memory, no byte twice and
 //    no bank twice.  Each warp has a ring of its own there, filled by bulk copies
-//    of two tiles that one lane issues: nothing but the warp itself waits for
-//    them.  (Loads straight into registers, four tiles ahead, waited for the
+//    of two or four tiles that one lane issues: nothing but the warp itself waits
+//    for them.  (Loads straight into registers, four tiles ahead, waited for the
 //    newest of them too: 27.0 us for the gated pair 3584 -> 18944 of one token.)
 //  * A pair of quants costs one LOP3 under the exponent of 1024 (1024 + n, or
 //    1024 + 16 n of the half-byte above) and one exact f16 subtraction or fma
@@ -43,7 +43,7 @@ namespace q8d {
 namespace {
 
 constexpr int kMaxCluster = 16;  // CTAs (more than eight are no portable size)
-constexpr int kMaxStages = 4;   // copies of a warp in flight
+constexpr int kMaxStages = 4;    // copies of a warp in flight
 // Tiles a copy.
 __host__ __device__ constexpr int chunk_tiles(int ng) { return ng == 1 ? 4 : 2; }
 // Strips (of either matrix) that a pass sums up at most, and how many of them a
@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
     float* dst = part + warp * slot_floats;  // [part of this warp][row of the batch][16]
     while (w.n) {
       const int n = min(kChunk, w.n), k = w.k;
-      if (!dead && !mbar_wait(bars + stage, parity)) dead = true;
+      // (all lanes see the copy, or the warp goes on without it)
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bars + stage, parity));
       if (dead) {
 #pragma unroll
         for (int q = 0; q < NG; ++q)
@@ -769,13 +770,21 @@ int launch_g(const Q4Params& P, cudaStream_t stream) {
 
 }  // namespace
 
-int q4_launch(const Q4Params& P, cudaStream_t stream) {
+static int launch_any(const Q4Params& P, cudaStream_t stream) {
   if (P.x_dtype == Q8D_KV_F16) return P.m <= 8 ? launch_g<kF16, 1>(P, stream) : launch_g<kF16, 2>(P, stream);
   if (P.x_dtype == Q8D_KV_Q8_0) return P.m <= 8 ? launch_g<kQ8, 1>(P, stream) : launch_g<kQ8, 2>(P, stream);
   // (f32 rows take two columns each)
   if (P.m <= 4) return launch_g<kF32, 1>(P, stream);
   if (P.m <= 8) return launch_g<kF32, 2>(P, stream);
   return P.group == 32 ? launch_wide<4>(P, stream) : P.group == 64 ? launch_wide<2>(P, stream) : launch_wide<1>(P, stream);
+}
+
+int q4_launch(const Q4Params& P, cudaStream_t stream) {
+  try {
+    return launch_any(P, stream);
+  } catch (...) {  // (the host's memory ran out under the plans)
+    return Q8D_ENOMEM;
+  }
 }
 
 }  // namespace q8d

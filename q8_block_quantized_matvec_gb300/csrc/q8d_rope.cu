@@ -57,10 +57,10 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableArgs A) {
     const double ramp = fmin(fmax((i - A.low) / fmax(A.high - A.low, 0.001), 0.0), 1.0);
     f = f / A.factor * ramp + f * (1.0 - ramp);
   }
-  for (int pos = blockIdx.x * 8 + threadIdx.y; pos < A.max_pos; pos += gridDim.x * 8) {
+  for (long long pos = blockIdx.x * 8 + threadIdx.y; pos < A.max_pos; pos += gridDim.x * 8) {
     double s, c;
     sincos((double)pos * f, &s, &c);
-    float* row = A.table + (long long)pos * 2 * A.half;
+    float* row = A.table + pos * 2 * A.half;
     row[i] = (float)(c * A.mscale);
     row[A.half + i] = (float)(s * A.mscale);
   }
@@ -302,133 +302,133 @@ __global__ void __launch_bounds__(kWarps * 32, kE == 4 ? 3 : 2) rope_rows_kernel
       if (turns && !bad) angles<kE, WAY>(table, half, D.layout, el, c, sn);
     };
     fetch();
-   for (;; ++row, ++r) {
-    uint64_t f[kSteps][kP], cc[kP], cs[kP];
+    for (;; ++row, ++r) {
+      uint64_t f[kSteps][kP], cc[kP], cs[kP];
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) expand<T, kE>(raw[u], f[u]);
+      for (int u = 0; u < kSteps; ++u) expand<T, kE>(raw[u], f[u]);
 #pragma unroll
-    for (int e = 0; e < kP; ++e) cc[e] = c[e], cs[e] = sn[e];
-    if (row + 1 < end) {
-      src += ld;
-      if (!bad) table += D.rot_dim;
-      fetch();
-    }
-    if (bias) {
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        if (u >= mine) continue;
-        uint64_t b[kP];
-        get_shared<kE, kVec>(bias + col + u * stride, b);
-#pragma unroll
-        for (int e = 0; e < kP; ++e) f[u][e] = add2(f[u][e], b[e]);
+      for (int e = 0; e < kP; ++e) cc[e] = c[e], cs[e] = sn[e];
+      if (row + 1 < end) {
+        src += ld;
+        if (!bad) table += D.rot_dim;
+        fetch();
       }
-    }
-    if constexpr (kNorm) {
-      if (g < 2) {
-        Pair ss[kSteps];
+      if (bias) {
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-          Pair2 both{0, 0};
+          if (u >= mine) continue;
+          uint64_t b[kP];
+          get_shared<kE, kVec>(bias + col + u * stride, b);
 #pragma unroll
-          for (int e = 0; e < kP; ++e) pair2_add_square(both, f[u][e]);
-          ss[u] = pair2_join(both);
+          for (int e = 0; e < kP; ++e) f[u][e] = add2(f[u][e], b[e]);
         }
-        float inv[kSteps];
-        head_factors<kE>(ss, f, A, lane, [&](int u) { return head + u * hpw < heads && u < steps; }, inv);
-#pragma unroll
-        for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-          for (int e = 0; e < kP; ++e) f[u][e] = mul2(mul2(f[u][e], pack2(inv[u], inv[u])), wn[e]);
       }
-    }
-    if (g < 2 && half) {
-      const int by = half / kE, from = turns ? (el < half ? lane + by : lane - by) : lane;
+      if constexpr (kNorm) {
+        if (g < 2) {
+          Pair ss[kSteps];
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        if (u >= steps) break;
-        float p[kE];  // the partners
-        if constexpr (WAY == kPairs) {
+          for (int u = 0; u < kSteps; ++u) {
+            Pair2 both{0, 0};
 #pragma unroll
-          for (int e = 0; e < kP; ++e) unpack2(f[u][e], p[2 * e + 1], p[2 * e]);
-        } else if constexpr (WAY == kHalves) {
+            for (int e = 0; e < kP; ++e) pair2_add_square(both, f[u][e]);
+            ss[u] = pair2_join(both);
+          }
+          float inv[kSteps];
+          head_factors<kE>(ss, f, A, lane, [&](int u) { return head + u * hpw < heads && u < steps; }, inv);
 #pragma unroll
-          for (int e = 0; e < kP; ++e) unpack2(__shfl_sync(0xffffffffu, f[u][e], from), p[2 * e], p[2 * e + 1]);
-        } else {
-          float* t = turn[warp] + lane * kE;
-          __syncwarp();
+          for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-          for (int e = 0; e < kP; ++e) unpack2(f[u][e], t[2 * e], t[2 * e + 1]);
-          __syncwarp();
+            for (int e = 0; e < kP; ++e) f[u][e] = mul2(mul2(f[u][e], pack2(inv[u], inv[u])), wn[e]);
+        }
+      }
+      if (g < 2 && half) {
+        const int by = half / kE, from = turns ? (el < half ? lane + by : lane - by) : lane;
 #pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            const int j = el + e;
-            p[e] = t[e + (j >= 2 * half                    ? 0
-                          : D.layout == Q8D_ROPE_PAIRS     ? 1 - 2 * (j & 1)
-                          : j < half                       ? half
-                                                           : -half)];
+        for (int u = 0; u < kSteps; ++u) {
+          if (u >= steps) break;
+          float p[kE];  // the partners
+          if constexpr (WAY == kPairs) {
+#pragma unroll
+            for (int e = 0; e < kP; ++e) unpack2(f[u][e], p[2 * e + 1], p[2 * e]);
+          } else if constexpr (WAY == kHalves) {
+#pragma unroll
+            for (int e = 0; e < kP; ++e) unpack2(__shfl_sync(0xffffffffu, f[u][e], from), p[2 * e], p[2 * e + 1]);
+          } else {
+            float* t = turn[warp] + lane * kE;
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < kP; ++e) unpack2(f[u][e], t[2 * e], t[2 * e + 1]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+              const int j = el + e;
+              p[e] = t[e + (j >= 2 * half                    ? 0
+                            : D.layout == Q8D_ROPE_PAIRS     ? 1 - 2 * (j & 1)
+                            : j < half                       ? half
+                                                             : -half)];
+            }
+          }
+          // (elements behind rot_dim, which may end inside a lane's, are as they were;
+          // scalar steps, each rounded: packed products are contracted into the sum)
+          if (turns) {
+#pragma unroll
+            for (int e = 0; e < kP; ++e) {
+              if (el + 2 * e >= 2 * half) break;
+              float x[2], cv[2], sv[2];
+              unpack2(f[u][e], x[0], x[1]);
+              unpack2(cc[e], cv[0], cv[1]);
+              unpack2(cs[e], sv[0], sv[1]);
+              f[u][e] = pack2(__fadd_rn(__fmul_rn(x[0], cv[0]), __fmul_rn(p[2 * e], sv[0])),
+                              __fadd_rn(__fmul_rn(x[1], cv[1]), __fmul_rn(p[2 * e + 1], sv[1])));
+            }
           }
         }
-        // (elements behind rot_dim, which may end inside a lane's, are as they were;
-        // scalar steps, each rounded: packed products are contracted into the sum)
-        if (turns) {
-#pragma unroll
-          for (int e = 0; e < kP; ++e) {
-            if (el + 2 * e >= 2 * half) break;
-            float x[2], cv[2], sv[2];
-            unpack2(f[u][e], x[0], x[1]);
-            unpack2(cc[e], cv[0], cv[1]);
-            unpack2(cs[e], sv[0], sv[1]);
-            f[u][e] = pack2(__fadd_rn(__fmul_rn(x[0], cv[0]), __fmul_rn(p[2 * e], sv[0])),
-                            __fadd_rn(__fmul_rn(x[1], cv[1]), __fmul_rn(p[2 * e + 1], sv[1])));
-          }
-        }
       }
-    }
-    if (g == 0) {
-      if (bad) {
+      if (g == 0) {
+        if (bad) {
+#pragma unroll
+          for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+            for (int e = 0; e < kP; ++e) f[u][e] = 0x7fc000007fc00000ull;
+        }
+        const long long at = r * D.ldo + col;
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          if (u >= mine) break;
+          if (D.q_dtype == Q8D_KV_F16)
+            put<__half, kE, kVec>(static_cast<__half*>(P.q_out) + at + u * stride, f[u]);
+          else
+            put<float, kE, kVec>(static_cast<float*>(P.q_out) + at + u * stride, f[u]);
+        }
+        if (row + 1 >= end) break;
+        continue;
+      }
+      uint8_t* cache = (g == 1 ? P.kc : P.vc) + P.seq_bytes * s;
+      const long long cr = (long long)pos + row;
+      if constexpr (KV == Q8D_KV_Q4 || KV == Q8D_KV_Q8_0) {
+        uint8_t* blk = KV == Q8D_KV_Q4 ? cache + cr * (width / 2) + col / 32 * 16
+                                       : cache + (cr * (width / kQBlock) + col / 32) * kQBlockBytes;
+        uint8_t* scale = cache + q4_scale_plane(D.cap, width) + cr * (width / 16) + col / 32 * 2;
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          if (u >= steps) break;
+          float v[kE];
+#pragma unroll
+          for (int e = 0; e < kP; ++e) unpack2(f[u][e], v[2 * e], v[2 * e + 1]);
+          if constexpr (KV == Q8D_KV_Q4)
+            put_q4<kE>(blk + u * (stride / 2), scale + u * (stride / 16), lane & (32 / kE - 1), v, u < mine);
+          else
+            put_q8_0<kE>(blk + u * (stride / 32 * kQBlockBytes), lane & (32 / kE - 1), v, u < mine);
+        }
+      } else {
+        using C = typename std::conditional<KV == Q8D_KV_F16, __half, float>::type;
+        C* dst = reinterpret_cast<C*>(cache) + cr * width + col;
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-          for (int e = 0; e < kP; ++e) f[u][e] = 0x7fc000007fc00000ull;
-      }
-      const long long at = r * D.ldo + col;
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        if (u >= mine) break;
-        if (D.q_dtype == Q8D_KV_F16)
-          put<__half, kE, kVec>(static_cast<__half*>(P.q_out) + at + u * stride, f[u]);
-        else
-          put<float, kE, kVec>(static_cast<float*>(P.q_out) + at + u * stride, f[u]);
+          if (u < mine) put<C, kE, true>(dst + u * stride, f[u]);
       }
       if (row + 1 >= end) break;
-      continue;
     }
-    uint8_t* cache = (g == 1 ? P.kc : P.vc) + P.seq_bytes * s;
-    const long long cr = (long long)pos + row;
-    if constexpr (KV == Q8D_KV_Q4 || KV == Q8D_KV_Q8_0) {
-      uint8_t* blk = KV == Q8D_KV_Q4 ? cache + cr * (width / 2) + col / 32 * 16
-                                     : cache + (cr * (width / kQBlock) + col / 32) * kQBlockBytes;
-      uint8_t* scale = cache + q4_scale_plane(D.cap, width) + cr * (width / 16) + col / 32 * 2;
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        if (u >= steps) break;
-        float v[kE];
-#pragma unroll
-        for (int e = 0; e < kP; ++e) unpack2(f[u][e], v[2 * e], v[2 * e + 1]);
-        if constexpr (KV == Q8D_KV_Q4)
-          put_q4<kE>(blk + u * (stride / 2), scale + u * (stride / 16), lane & (32 / kE - 1), v, u < mine);
-        else
-          put_q8_0<kE>(blk + u * (stride / 32 * kQBlockBytes), lane & (32 / kE - 1), v, u < mine);
-      }
-    } else {
-      using C = typename std::conditional<KV == Q8D_KV_F16, __half, float>::type;
-      C* dst = reinterpret_cast<C*>(cache) + cr * width + col;
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u)
-        if (u < mine) put<C, kE, true>(dst + u * stride, f[u]);
-    }
-    if (row + 1 >= end) break;
-   }
   }
 }
 
@@ -513,7 +513,7 @@ int rope_table_launch(float* table, int max_pos, int rot_dim, double theta, int 
     A.low = std::max(std::floor(at(beta_fast)), 0.0);
     A.high = std::min(std::ceil(at(beta_slow)), rot_dim - 1.0);
   }
-  const dim3 grid((unsigned)std::min((max_pos + 7) / 8, 4096), (unsigned)((A.half + 31) / 32));
+  const dim3 grid((unsigned)std::min((max_pos + 7LL) / 8, 4096LL), (unsigned)((A.half + 31) / 32));
   return launch_ex(rope_table_kernel, grid, dim3(32, 8), 0, stream, true, A);
 }
 

@@ -259,3 +259,18 @@ def test_same_bits_every_time(q8d):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, first) and torch.equal(h, want)
+
+
+@pytest.mark.parametrize("m,p,n", [(1, 70, 224), (7, 200, 672), (14, 90, 2016)])
+def test_first_call_of_a_size_in_a_capture(q8d, m, p, n):
+    """Nothing of a size has to be known before a graph is captured."""
+    W = Matrix(q8d, 39, p, n, 64)
+    x, v, ld = activations(40, m, n, F32)
+    y, st, g = torch.full((m, p), 7.0, device="cuda"), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        q8d.q8d_q4_matmul(x, F32, ld, W.bytes, 64, None, None, 0, y, p, m, n, p, st)
+    torch.cuda.synchronize()
+    assert torch.all(y == 7)
+    g.replay()
+    check(y, W, v)

@@ -272,3 +272,17 @@ def test_rows_in_a_graph(q8d):
         assert torch.equal(c.out, want.out)
         pos.add_(1)
     assert c.err.item() == 0
+
+
+def test_more_sequences_than_a_grid_is_high(q8d):
+    batch = 70_000
+    c = Case(q8d, 1, 1, 8, 8, PAIRS, F16, batch, 1, 32, [i % 32 for i in range(batch)], None, max_pos=40)
+    c.call()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    pos = np.arange(batch) % 32
+    k = c.head_rows(c.k, None, None, pos, True).astype(np.float16)
+    got = c.kc.view(torch.float16).view(batch, -1).cpu().numpy()[:, :32 * 8].reshape(batch, 32, 8)
+    before = c.before[0].view(np.float16).reshape(batch, -1)[:, :32 * 8].reshape(batch, 32, 8).copy()
+    before[np.arange(batch), pos] = k
+    assert np.array_equal(got.view(np.uint16), before.view(np.uint16))
