@@ -68,10 +68,12 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableArgs A) {
 
 // ---- the rows ---------------------------------------------------------------
 constexpr int kWarps = 8;
-constexpr int kSteps = 4;  // steps a warp at most
+// Steps a warp at most: 64 bytes of f32 a lane (heads wider than 128 with four
+// steps spilled: 4 x 1000 ragged rows of 8 / 4 heads of 256 43.3 us, now 17.1).
+constexpr int steps_of(int e) { return 16 / e; }
 
-// A row's work is steps of one head each (several narrow ones).  A warp takes up
-// to kSteps of q, of k or of v.
+// A row's work is steps of one head each (several narrow ones).  A warp takes
+// several of q, of k or of v.
 struct RopeArgs {
   RopeRowsParams P;
   FastDiv chunks;  // warps a row
@@ -195,27 +197,33 @@ __device__ __forceinline__ void angles(const float* row, int half, int layout, i
   }
 }
 
-// The factors of kSteps heads' norms.  ss: this lane's squares of each step;
+// The factors of a warp's steps' norms.  ss: this lane's squares of each step;
 // valid(u): whether step u of this lane's head is normed.  The sums of four
 // steps are folded together: lanes that differ in bit 0 exchange two of them
 // each, in bit 1 one, and from there on lane l carries step l & 3, so that a
-// warp adds six times where one step after the other would take twenty.
+// warp adds six times where one step after the other would take twenty.  (Two
+// steps: one exchange, lane l carries step l & 1.)
 template <int kE, typename Valid>
-__device__ __forceinline__ void head_factors(const Pair (&ss)[kSteps], const uint64_t (&f)[kSteps][kE / 2],
-                                             const RopeArgs& A, int lane, Valid valid, float (&inv)[kSteps]) {
-  static_assert(kSteps == 4, "");
+__device__ __forceinline__ void head_factors(const Pair (&ss)[steps_of(kE)],
+                                             const uint64_t (&f)[steps_of(kE)][kE / 2], const RopeArgs& A,
+                                             int lane, Valid valid, float (&inv)[steps_of(kE)]) {
+  constexpr int kSteps = steps_of(kE);
+  static_assert(kSteps == 4 || kSteps == 2, "");
   const auto meet = [](const Pair& keep, const Pair& send, int o) {
     return pair_meet(keep, pair_shfl_xor(send, o, 0xffffffffu));
   };
-  const bool b0 = lane & 1, b1 = lane & 2;
-  const Pair a0 = meet(b0 ? ss[1] : ss[0], b0 ? ss[0] : ss[1], 1);
-  const Pair a1 = meet(b0 ? ss[3] : ss[2], b0 ? ss[2] : ss[3], 1);
-  Pair p = meet(b1 ? a1 : a0, b1 ? a0 : a1, 2);
+  const bool b0 = lane & 1;
+  Pair p = meet(b0 ? ss[1] : ss[0], b0 ? ss[0] : ss[1], 1);
+  if constexpr (kSteps == 4) {
+    const bool b1 = lane & 2;
+    const Pair q = meet(b0 ? ss[3] : ss[2], b0 ? ss[2] : ss[3], 1);
+    p = meet(b1 ? q : p, b1 ? p : q, 2);
+  }
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1)
+  for (int o = kSteps; o < 32; o <<= 1)
     if (o < A.lph) p = meet(p, p, o);
   const float eps = A.P.d.eps;
-  const int mine = lane & 3;
+  const int mine = lane & (kSteps - 1);
   float r = rms_factor(p, A.inv_n, eps);
   const bool good = !valid(mine) || rms_in_range(p);
   if (!__all_sync(0xffffffffu, good)) {
@@ -232,18 +240,20 @@ __device__ __forceinline__ void head_factors(const Pair (&ss)[kSteps], const uin
       }
       for (int o = 1; o < A.lph; o <<= 1) d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
     }
-    const double all = mine == 0 ? d[0] : mine == 1 ? d[1] : mine == 2 ? d[2] : d[3];
+    double all = d[0];
+#pragma unroll
+    for (int u = 1; u < kSteps; ++u) all = mine == u ? d[u] : all;
     if (!good) r = rms_factor_wide(all, A.P.d.head_dim, eps);
   }
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) inv[u] = __shfl_sync(0xffffffffu, r, (lane & ~3) | u);
+  for (int u = 0; u < kSteps; ++u) inv[u] = __shfl_sync(0xffffffffu, r, (lane & ~(kSteps - 1)) | u);
 }
 
 // (three CTAs an SM, us for 4096 rows of 16 / 8 heads of 128 from f32 into f16: two
 // 27.5, three 25.6, four 31.7)
 template <typename T, int KV, int kE, bool kNorm, int WAY>
 __global__ void __launch_bounds__(kWarps * 32, kE == 4 ? 3 : 2) rope_rows_kernel(const RopeArgs A) {
-  constexpr int kP = kE / 2, kW = kE * sizeof(T) / 4;
+  constexpr int kP = kE / 2, kW = kE * sizeof(T) / 4, kSteps = steps_of(kE);
   constexpr bool kVec = WAY != kAny;
   __shared__ float turn[WAY == kAny ? kWarps : 1][32 * kE];
   griddep_launch_dependents();
@@ -442,9 +452,10 @@ int launch_rope(const RopeRowsParams& P, cudaStream_t stream) {
   if (A.lph < 32 / kE) A.lph = 32 / kE;  // (a packed block's lanes)
   const int hpw = 32 / A.lph;
   const int sq = P.q ? (D.n_heads + hpw - 1) / hpw : 0, sk = P.k ? (D.n_kv_heads + hpw - 1) / hpw : 0;
-  // four steps a warp once that leaves two full machines of warps, else one, for
-  // the latency
-  A.per = (long long)P.batch * P.rows * (sq + 2 * sk) >= 4LL * 2 * 64 * sm_count() ? kSteps : 1;
+  // as many steps a warp as it may take once that leaves two full machines of
+  // warps, else one, for the latency
+  constexpr int kSteps = steps_of(kE);
+  A.per = (long long)P.batch * P.rows * (sq + 2 * sk) >= kSteps * 2LL * 64 * sm_count() ? kSteps : 1;
   A.cq = (sq + A.per - 1) / A.per;
   A.ck = (sk + A.per - 1) / A.per;
   A.chunks = fast_div((uint32_t)(A.cq + 2 * A.ck));
