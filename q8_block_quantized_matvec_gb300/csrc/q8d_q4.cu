@@ -179,9 +179,10 @@ __device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
 
 // The activations' columns [128 k0, 128 (k0 + ktl)) as the MMA's second operand.
 // xstep: x_stride; most: tiles of the largest part of a row.
-template <int MODE, int kWarps, int kMp>
+// then(): what is to be started once the first loads are on their way.
+template <int MODE, int kWarps, int kMp, typename Then>
 __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int most, int xstep, __half* xf,
-                                        float* scale) {
+                                        float* scale, Then then) {
   constexpr int kLoads = kWarps / 2;  // items a warp loads before it uses the first
   const Q4Params& P = A.P;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -195,7 +196,8 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mo
     }
   };
   wrap();
-  while (j < P.m) {
+  if (j >= P.m) then();
+  for (bool started = false; j < P.m; started = true) {
     int js[kLoads], ks[kLoads];
     float4 f[kLoads];                // f32
     uint2 u[kLoads];                 // f16, or four quants
@@ -223,6 +225,7 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mo
         u[l].x = w[0] | (uint32_t)w[1] << 16;
       }
     }
+    if (!started) then();
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
       const int j = js[l], k = ks[l];
@@ -353,10 +356,19 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
   // L2 is asked for the first ones before the work in front is done)
   if (lane == 0 && ahead.n) bulk_prefetch_l2(src, min(A.stages * kChunk, ahead.n) * kRec);
   griddep_wait();
-  for (int s = 0; s < A.stages; ++s) issue(s);
-
   const int xstep = x_stride(ktl_max);
-  build_x<MODE, kWarps, kMp>(A, k0, ktl, ktl_max, xstep, xf, xs);
+  // One or two rows of X are asked for before the weights: every warp waits for
+  // them, and all SMs' copies are microseconds of HBM (gated 3584 -> 18944, us with
+  // the rows / the weights first: one row 15.6 / 16.3, four 17.4 / 17.1; 16 Q8_0
+  // rows 3584 -> 4736 15.3 / 14.7).
+  const auto start = [&]() {
+    for (int s = 0; s < A.stages; ++s) issue(s);
+  };
+  const bool rows_first = P.m <= 2;
+  if (!rows_first) start();
+  build_x<MODE, kWarps, kMp>(A, k0, ktl, ktl_max, xstep, xf, xs, [&]() {
+    if (rows_first) start();
+  });
   __syncthreads();
 
   const Magic magic;
