@@ -404,9 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
           for (int e = 0; e < kSums; ++e) acc[q][e] = __int_as_float(0x7fc00000);
       } else {
         const uint8_t* tile = ring + stage * kStage;
-#pragma unroll
-        for (int c = 0; c < kChunk; ++c) {
-          if (c < n) {
+        const auto work = [&](int c) {
             Tile<NS> T;
             read_tile<NS>(tile + c * kRec, lane, T);
             float sum[NG][2];  // (f32 rows: of a tile)
@@ -455,7 +453,13 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
                 acc[q][1] = fmaf(by, sum[q][1], acc[q][1]);
               }
             }
-          }
+        };
+        if (n == kChunk) {
+#pragma unroll
+          for (int c = 0; c < kChunk; ++c) work(c);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < n; ++c) work(c);
         }
         __syncwarp();  // (every lane has read the stage)
         ++taken;
