@@ -644,31 +644,29 @@ void weigh(const Q4Args& A, int strips, int cs, int most, Plan* best) {
       }
     }
   if (!stages) return;
-  // What an SM does, in ns: its CTAs' tiles (one CTA of eight warps is a little
-  // slower at them); 128 columns of a row of X at a time made into operands,
-  // several of them loaded by a warp at once; the passes' ends; the two meetings
-  // of a cluster; and what a call takes longer whose CTAs leave no room for the
-  // next one's.
-  const double tiles = (double)units * A.P.nmat * ktl * ctas * (kWarps == 8 && ctas == 1 ? 1.12 : 1.0);
+  // What an SM does, in ns: its CTAs' tiles; 128 columns of a row of X at a time
+  // made into operands, several of them loaded by a warp at once; the passes' ends;
+  // the two meetings of a cluster; and what sixteen warps take longer to start.
+  const double tiles = (double)units * A.P.nmat * ktl * ctas;
   const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
   const double ns = tiles * tile_ns(MODE, NG, NS) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
-                    (cs > 1 ? 1000 : 0) + (kWarps == 16 ? 800 : ctas == 2 ? 500 : 0);
+                    (cs > 1 ? 1000 : 0) + (kWarps == 16 ? 300 : 0);
   if (best->cs == 0 || ns < best->ns)
     *best = {kWarps, cs, ncl, passes, parts, stages, ring + stages * kStage, ns};
 }
 
-// The ways with kWarps warps a CTA: clusters of every size, and eight warps also
-// as one CTA an SM.  Measured, us: 3584 -> 4608, one row, eight warps 5.3, two such
-// CTAs an SM 5.6, sixteen warps 5.8, two CTAs a cluster 6.4; gated 3584 -> 18944,
-// eight rows, 27.6 (clusters of four), -, 23.2, 24.5; 18944 -> 3584, one row, -,
-// 12.2 (clusters of eight), 15.5, 12.4.
+// The ways with kWarps warps a CTA: clusters of every size.  Measured, us: 3584 ->
+// 4608, one row, eight warps 5.6, sixteen 5.8, two CTAs a cluster 6.4; gated 3584
+// -> 18944, eight rows, 27.6 (clusters of four), 23.2, 24.5; 18944 -> 3584, one
+// row, 12.2 (clusters of eight), 15.5, 12.4.  (One CTA of eight warps an SM, beside
+// which the next call's starts, takes 5.1 in a graph and 6.9 where single calls
+// arrive one by one.)
 template <int kWarps, int MODE, int NG, int NS>
 int consider(const Q4Args& A, int strips, Plan* best) {
   const auto fn = reinterpret_cast<const void*>(q4_kernel<kWarps, MODE, NG, NS>);
   int rc = configure_kernel(fn, kMaxSmem, true);
   if (!rc) rc = allow_wide_clusters(fn);
   if (rc) return rc;
-  if (kWarps == 8) weigh<kWarps, MODE, NG, NS>(A, strips, 1, sm_count(), best);
   weigh<kWarps, MODE, NG, NS>(A, strips, 1, 16 / kWarps * sm_count(), best);
   for (int cs = 2; cs <= kMaxCluster && cs <= A.kt; cs *= 2) {
     int most = 0;
@@ -693,7 +691,7 @@ int launch_plan(const Q4Args& A, const Plan& plan, cudaStream_t stream) {
   attr[1].val.clusterDim.x = plan.cs;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = plan.cs > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, q4_kernel<kWarps, MODE, NG, NS>, A);
   return e == cudaSuccess ? Q8D_OK : record_cuda(e);
 }
