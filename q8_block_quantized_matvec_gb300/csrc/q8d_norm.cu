@@ -4,9 +4,16 @@
 //
 // Every element is read once, kept in registers between the sum of squares and
 // the product, and written once (and the sum once), so HBM bounds it; a few rows
-// take a launch and one reduction.  A row belongs to a group of threads, at most
-// 32 elements each; f32 is moved in 16 bytes a thread, f16 in 16 where the
-// output is no wider.  See q8d_rms.cuh for the sum.
+// take a launch and one reduction.  A row belongs to a group of threads, 64 bytes
+// of each operand a thread at most; f32 is moved in 16 bytes a thread, f16 in 16
+// where the output is no wider.  See q8d_rms.cuh for the sum.
+//
+// us in a graph (and TB/s): 4096 rows of 3584 with the residual in f16 20.8 (5.65),
+// in f32 39.1 (6.0), from f16 into Q8_0 26.0 (4.0: a quarter of the instructions
+// are the quantizer's); 4000 rows of 2887 f32 35.0 (5.3); one row 2.5.  What is
+// left is latency: half the issue slots are used, by 27 warps an SM whose rows are
+// loaded, summed and written in turn.  (A block that walks several rows, the next
+// one's loads in flight, needed more registers: 41.7 for 39.1.)
 #include <algorithm>
 #include <type_traits>
 

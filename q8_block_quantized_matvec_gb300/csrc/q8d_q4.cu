@@ -29,6 +29,13 @@
 //    their columns; a CTA's tiles, strip after strip, are cut into equal ranges
 //    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs'
 //    through the cluster's, both in a fixed order.
+//
+// us in a graph (and TB/s of weights): one row, 896 -> 151936 15.1 (4.8), gated 3584
+// -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 24.7, sixteen f16 rows 26.7,
+// Q8_0 37.4; 18944 -> 3584, sixteen rows 31.7.  A call spends about four
+// microseconds starting and meeting; then a tile takes 50 to 55 clocks with one
+// column group (150 instructions, 58 % of the issue slots), 80 with two (latency:
+// sixteen warps of 128 registers).
 #include <algorithm>
 #include <array>
 #include <map>

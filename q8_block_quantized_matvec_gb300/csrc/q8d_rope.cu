@@ -18,13 +18,21 @@
 // model's layers share: the row of a position is read by all its heads, where
 // working it out in 64 bits would take longer than moving the row.
 //
-// The rows are memory bound: a warp takes up to four heads (or pairs of narrow
-// heads) of one row and segment, with the angles in registers and all loads in
-// flight before any is used; a lane has four consecutive elements (eight of
-// heads wider than 128), so that 16 bytes an access fill the sectors, and eight
-// (four) neighbours make a packed block.  Each step of the arithmetic is
-// rounded to f32 by itself, so that the packed caches' codes are those of the
-// plain formulas whatever the compiler contracts.
+// The rows are memory bound, but for the instructions that norms and packed
+// caches add: a warp takes up to four heads (or pairs of narrow ones) of q, of k
+// or of v and walks several rows with them, the next row's values and angles in
+// flight while it turns one; a lane has four consecutive elements (eight of heads
+// wider than 128), so that 16 bytes an access fill the sectors, and eight (four)
+// neighbours make a packed block.  Each step of the arithmetic is rounded to f32 by
+// itself, so that the packed caches' codes are those of the plain formulas whatever
+// the compiler contracts.
+//
+// us in a graph (and TB/s): 4096 rows of 16 / 8 heads of 128 from f32 into f16 22.5
+// (5.3), with norms 28.9, into Q8_0 24.8, with norms and YaRN 33.8; 28 / 4 heads
+// 26.7 (5.4); 8 sequences of up to 1999 f16 rows of 14 / 2 heads of 64 into f16 17.3
+// (3.3: short rows, a kilobyte a warp), into 4 bits 19.4; one token of 64 sequences
+// 3.3.  (A row a warp, loaded when it was due: 46.3, 64.2 and 70.0 for the first,
+// second and fourth.)
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

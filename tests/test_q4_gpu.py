@@ -274,3 +274,24 @@ def test_first_call_of_a_size_in_a_capture(q8d, m, p, n):
     assert torch.all(y == 7)
     g.replay()
     check(y, W, v)
+
+
+@pytest.mark.parametrize("m", [9, 13, 16])
+def test_sixteen_rows_of_a_large_matrix(q8d, m):
+    """Rows that go in one launch or in two, with everything that has a row's place."""
+    p, n = 18944, 3584
+    W, U = Matrix(q8d, 41, p, n, 32), Matrix(q8d, 42, p, n, 32)
+    x, v, ld = activations(43, m, n, F32, n + 4)
+    bias, res = synth.normal_f32(44, "q4.b16", p), synth.normal_f32(45, "q4.r16", (m, p))
+    check(product(q8d, W, x, F32, ld, m, dev(bias), dev(res), p + 5, True), W, v, bias.astype(np.float64),
+          res.astype(np.float64))
+    h = torch.full((m, p + 1), 7.0, device="cuda")
+    q8d.q8d_q4_gated(x, F32, ld, W.bytes, U.bytes, 32, h, p + 1, m, n, p)
+    torch.cuda.synchronize()
+    g, u = v @ W.values.T, v @ U.values.T
+    gt, ut = (1e-5 * (np.abs(v) @ np.abs(w.values).T) for w in (W, U))
+    with np.errstate(over="ignore"):
+        silu = g / (1 + np.exp(-g))
+    tol = 1.1 * gt * (np.abs(u) + ut) + np.abs(silu) * ut + 2.0 ** -20 * np.abs(silu * u) + 1e-37
+    got = h.cpu().numpy()
+    assert np.all(np.abs(got[:, :p] - silu * u) <= tol) and np.all(got[:, p:] == 7)
