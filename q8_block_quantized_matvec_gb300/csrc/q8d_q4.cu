@@ -27,12 +27,12 @@
 //    off.
 //  * A cluster of CTAs takes whole strips of 16 rows, each of its CTAs a part of
 //    their columns; a CTA's tiles, strip after strip, are cut into equal ranges
-//    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs'
-//    through the cluster's, both in a fixed order.
+//    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs' in
+//    that of the one that finishes them, both in a fixed order.
 //
 // us in a graph (and TB/s of weights): one row, 896 -> 151936 15.1 (4.8), gated 3584
-// -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 24.7, sixteen f16 rows 26.7,
-// Q8_0 37.4; 18944 -> 3584, sixteen rows 31.7.  A call spends about four
+// -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 23.3, sixteen f16 rows 28.4,
+// Q8_0 35.2; 18944 -> 3584, sixteen rows 32.1.  A call spends about four
 // microseconds starting and meeting; then a tile takes 50 to 55 clocks with one
 // column group (150 instructions, 58 % of the issue slots), 80 with two (latency:
 // sixteen warps of 128 registers).
@@ -87,13 +87,13 @@ struct Smem {  // offsets
   int scale, part, red, meets, bars, ring;  // (the ring's stages take what is left)
 };
 __host__ __device__ inline Smem smem_layout(int warps, int mode, int ng, int ktl, int ncol, int parts,
-                                            bool cluster) {
+                                            int cs) {
   const int mp = ng * group_rows(mode);
   Smem s;
   s.scale = ncol * x_stride(ktl) * 2;
   s.part = s.scale + ((scale_floats(mode, mp, ktl) * 4 + 15) & ~15);
   s.red = s.part + warps * pass_slots(warps, parts) * mp * 16 * 4;
-  s.meets = s.red + (cluster ? parts * mp * 16 * 4 : 0);
+  s.meets = s.red + (cs > 1 ? (parts * mp + 2 * cs) * 16 * 4 : 0);
   s.bars = s.meets + (parts * 4 + 15 & ~15);
   s.ring = (s.bars + warps * kMaxStages * 8 + 127) & ~127;
   return s;
@@ -173,15 +173,19 @@ __device__ __forceinline__ float scale_of(const Tile<NS>& t, int h, int b) {
   return i & 1 ? __high2float(v) : __low2float(v);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// The cluster's barrier in two halves: what a CTA wrote before it arrived is seen
+// by those that have waited.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores v at p's place in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ void cluster_store(float* p, uint32_t rank, float v) {
   uint32_t a;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 // The activations' columns [128 k0, 128 (k0 + ktl)) as the MMA's second operand.
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
   const int u0 = (int)((long long)cluster * strips / A.ncl), u1 = (int)((cluster + 1LL) * strips / A.ncl);
   const int k0 = rank * A.kt / A.cs, ktl = (rank + 1) * A.kt / A.cs - k0;
   const int ktl_max = (A.kt + A.cs - 1) / A.cs;
-  const Smem L = smem_layout(kWarps, MODE, NG, ktl_max, A.ncol, A.parts, A.cs > 1);
+  const Smem L = smem_layout(kWarps, MODE, NG, ktl_max, A.ncol, A.parts, A.cs);
   __half* xf = reinterpret_cast<__half*>(smem);
   float* xs = reinterpret_cast<float*>(smem + L.scale);
   float* part = reinterpret_cast<float*>(smem + L.part);
@@ -353,6 +357,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
     }
   };
   griddep_launch_dependents();
+  if (A.cs > 1) cluster_arrive();  // (waited for before the first store into another CTA)
   if (lane == 0)
     for (int s = 0; s < A.stages; ++s) mbar_init(bars + s, 1);
   fence_barrier_init();
@@ -544,24 +549,30 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
       }
       if (pass + 1 < A.passes) __syncthreads();
     } else {
-      for (int o = first; o < parts * P.m; o += kThreads / 16) {
-        const int sp = over_m(o), j = o - sp * P.m;
-        red[o * 16 + row] = cta_sum(sp, j, row);
+      // pair o is finished by CTA o % cs, to which every CTA sends its sums: [CTA][its
+      // pairs][matrix][16]
+      const int pairs = pu * P.m, share = (pairs + A.cs - 1) / A.cs, mine = 16 * P.nmat;
+      cluster_wait();  // (all of the cluster's CTAs run, and have read the last pass's)
+      for (int o = first; o < pairs; o += kThreads / 16) {
+        const int unit = over_m(o), j = o - unit * P.m, owner = o & (A.cs - 1);
+        float* dst = red + (rank * share + o / A.cs) * mine + row;
+        for (int e = 0; e < P.nmat; ++e) cluster_store(dst + 16 * e, owner, cta_sum(P.nmat * unit + e, j, row));
       }
-      cluster_sync();
-      for (int o = rank * (kThreads / 16) + first; o < pu * P.m; o += A.cs * (kThreads / 16)) {
+      cluster_arrive();
+      cluster_wait();
+      for (int i = first; i < share; i += kThreads / 16) {
+        const int o = i * A.cs + rank;
+        if (o >= pairs) break;
         const int unit = over_m(o), j = o - unit * P.m;
-        const int at = (P.nmat * unit * P.m + j) * 16 + row;
+        const float* src = red + i * mine + row;
         float v = 0.f, up = 0.f;
-        for (int c0 = 0; c0 < A.cs; c0 += 2) {
-          const float a = cluster_load(red + at, c0), b = cluster_load(red + at, c0 + 1);
-          float d = 0.f, e = 0.f;
-          if (P.nmat == 2) d = cluster_load(red + at + P.m * 16, c0), e = cluster_load(red + at + P.m * 16, c0 + 1);
-          v += a, v += b, up += d, up += e;
+        for (int c = 0; c < A.cs; ++c) {
+          v += src[c * share * mine];
+          if (P.nmat == 2) up += src[c * share * mine + 16];
         }
         finish(unit, j, v, up);
       }
-      cluster_sync();  // (the sums are read before they change or their CTA leaves)
+      if (pass + 1 < A.passes) cluster_arrive();
     }
   }
   // (no copy is left behind: one that did not land in time is given as long again)
@@ -644,7 +655,7 @@ void weigh(const Q4Args& A, int strips, int cs, int most, Plan* best) {
     for (int u = std::min(units, kMaxParts / A.P.nmat); u >= 1; u -= (u + 7) / 8) {
       passes = (units + u - 1) / u;
       parts = (units + passes - 1) / passes * A.P.nmat;
-      ring = smem_layout(kWarps, MODE, NG, ktl, A.ncol, parts, cs > 1).ring;
+      ring = smem_layout(kWarps, MODE, NG, ktl, A.ncol, parts, cs).ring;
       if ((kLimit - ring) / kStage >= least) {
         stages = std::min(kMaxStages, (kLimit - ring) / kStage);
         break;
@@ -652,11 +663,13 @@ void weigh(const Q4Args& A, int strips, int cs, int most, Plan* best) {
     }
   if (!stages) return;
   // What an SM does, in ns: its CTAs' tiles; 128 columns of a row of X at a time
-  // made into operands, several of them loaded by a warp at once; the passes' ends;
-  // the two meetings of a cluster; and what sixteen warps take longer to start.
+  // made into operands, several of them loaded by a warp at once; sixteen sums of a
+  // strip and row brought together, in a cluster through another CTA; the passes'
+  // ends; a cluster's meetings; and what sixteen warps take longer to start.
   const double tiles = (double)units * A.P.nmat * ktl * ctas;
   const int items = A.P.m * ktl, rounds = (items + kWarps * kWarps / 2 - 1) / (kWarps * kWarps / 2);
-  const double ns = tiles * tile_ns(MODE, NG, NS) + items * ctas * 7.5 + rounds * 500 + (passes - 1) * 2500 +
+  const double ns = tiles * tile_ns(MODE, NG, NS) + items * ctas * 7.5 + rounds * 500 +
+                    (double)passes * parts * A.P.m * (cs > 1 ? 6 : 5 * ctas) + (passes - 1) * 3000 +
                     (cs > 1 ? 1000 : 0) + (kWarps == 16 ? 300 : 0);
   if (best->cs == 0 || ns < best->ns)
     *best = {kWarps, cs, ncl, passes, parts, stages, ring + stages * kStage, ns};
@@ -664,8 +677,8 @@ void weigh(const Q4Args& A, int strips, int cs, int most, Plan* best) {
 
 // The ways with kWarps warps a CTA: clusters of every size.  Measured, us: 3584 ->
 // 4608, one row, eight warps 5.6, sixteen 5.8, two CTAs a cluster 6.4; gated 3584
-// -> 18944, eight rows, 27.6 (clusters of four), 23.2, 24.5; 18944 -> 3584, one
-// row, 12.2 (clusters of eight), 15.5, 12.4.  (One CTA of eight warps an SM, beside
+// -> 18944, eight rows, 27.6 (clusters of four), 23.2, 24.8; 18944 -> 3584, one
+// row, 13.4 (clusters of eight), 15.1, 12.0.  (One CTA of eight warps an SM, beside
 // which the next call's starts, takes 5.1 in a graph and 6.9 where single calls
 // arrive one by one.)
 template <int kWarps, int MODE, int NG, int NS>
