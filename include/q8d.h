@@ -14,7 +14,8 @@
  *     Q8D_ERANGE      an index/length outside its buffer (host-visible args)
  *     Q8D_ECUDA       a CUDA call failed; q8d_last_cuda_error() has the code
  *     Q8D_ETIMEOUT    a bounded host wait ran out
- *     Q8D_ENOMEM      the library's own allocation failed (step create only)
+ *     Q8D_ENOMEM      the library's own allocation failed (step create; the
+ *                     host's memory under a product's plan)
  * On any non-zero status nothing was launched.  There is no fallback path:
  * an unsupported case is refused, never computed another way.
  *
@@ -536,8 +537,9 @@ int q8d_q4_unpack(const void* w_q4, void* dst, int dst_dtype, long long ld, int 
  *   Y: device f32 rows, ldy apart (>= p); only the first p entries of a row are
  *      written; must not overlap any other operand
  * 0 <= m <= 16, 32 <= n <= 32768, n % 32 == 0, p <= 2^30; else
- * Q8D_EUNSUPPORTED.  m == 0 or p == 0: no-op.  Matrices are read once (f32 rows:
- * once for every eight).  Nothing depends on the order in which threads finish.
+ * Q8D_EUNSUPPORTED.  m == 0 or p == 0: no-op.  Matrices are read once (with more than
+ * eight f32 rows at most twice).  Nothing depends on the order in which threads
+ * finish.  Waits inside are bounded (seconds); the sums that miss a copy are NaN.
  * ---------------------------------------------------------------------- */
 int q8d_q4_matmul(const void* X, int x_dtype, long long ldx, const void* w_q4, int group,
                   const float* bias, const float* residual, long long ldr, float* Y, long long ldy,

@@ -341,20 +341,22 @@ def q8d_moe_set_wait_limit(polls: int) -> int:
     return _check(lib().q8d_moe_set_wait_limit(int(polls)), "q8d_moe_set_wait_limit")
 
 
+# (numbers go to ctypes as they are: it takes whole numbers of any type and
+# refuses others, and ten conversions cost a call 0.6 us)
 def q8d_rmsnorm_rows(x, residual, sum_out, row_dtype: int, ldx: int, ldr: int, lds: int, weight,
                      eps: float, y, y_dtype: int, ldy: int, rows: int, n: int, stream=None) -> int:
     return _check(lib().q8d_rmsnorm_rows(
-        _ptr(x), _ptr(residual), _ptr(sum_out), int(row_dtype), int(ldx), int(ldr), int(lds),
-        _ptr(weight), float(eps), _ptr(y), int(y_dtype), int(ldy), int(rows), int(n),
+        _ptr(x), _ptr(residual), _ptr(sum_out), row_dtype, ldx, ldr, lds,
+        _ptr(weight), eps, _ptr(y), y_dtype, ldy, rows, n,
         _stream(stream)), "q8d_rmsnorm_rows")
 
 
 def q8d_rope_table(table, max_pos: int, rot_dim: int, theta: float, scaling: int, factor: float,
                    orig_ctx: float, beta_fast: float, beta_slow: float, mscale: float,
                    stream=None) -> int:
-    return _check(lib().q8d_rope_table(_ptr(table), int(max_pos), int(rot_dim), float(theta),
-                                       int(scaling), float(factor), float(orig_ctx),
-                                       float(beta_fast), float(beta_slow), float(mscale),
+    return _check(lib().q8d_rope_table(_ptr(table), max_pos, rot_dim, theta,
+                                       scaling, factor, orig_ctx,
+                                       beta_fast, beta_slow, mscale,
                                        _stream(stream)), "q8d_rope_table")
 
 
@@ -372,8 +374,8 @@ def rope_desc(**fields) -> RopeDesc:
 def q8d_rope_append_rows(desc: RopeDesc, q, k, v, q_out, kcache, vcache, batch: int, rows: int,
                          d_pos, d_rope_pos, d_counts, d_err, stream=None) -> int:
     return _check(lib().q8d_rope_append_rows(
-        desc, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(kcache), _ptr(vcache), int(batch),
-        int(rows), _ptr(d_pos), _ptr(d_rope_pos), _ptr(d_counts), _ptr(d_err), _stream(stream)),
+        desc, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(kcache), _ptr(vcache), batch,
+        rows, _ptr(d_pos), _ptr(d_rope_pos), _ptr(d_counts), _ptr(d_err), _stream(stream)),
         "q8d_rope_append_rows")
 
 
@@ -382,28 +384,28 @@ def q8d_q4_matrix_bytes(p: int, n: int, group: int) -> int:
 
 
 def q8d_q4_pack(src, src_dtype: int, ld: int, w_q4, p: int, n: int, group: int, stream=None) -> int:
-    return _check(lib().q8d_q4_pack(_ptr(src), int(src_dtype), int(ld), _ptr(w_q4), int(p), int(n),
-                                    int(group), _stream(stream)), "q8d_q4_pack")
+    return _check(lib().q8d_q4_pack(_ptr(src), src_dtype, ld, _ptr(w_q4), p, n,
+                                    group, _stream(stream)), "q8d_q4_pack")
 
 
 def q8d_q4_unpack(w_q4, dst, dst_dtype: int, ld: int, p: int, n: int, group: int,
                   stream=None) -> int:
-    return _check(lib().q8d_q4_unpack(_ptr(w_q4), _ptr(dst), int(dst_dtype), int(ld), int(p),
-                                      int(n), int(group), _stream(stream)), "q8d_q4_unpack")
+    return _check(lib().q8d_q4_unpack(_ptr(w_q4), _ptr(dst), dst_dtype, ld, p,
+                                      n, group, _stream(stream)), "q8d_q4_unpack")
 
 
 def q8d_q4_matmul(X, x_dtype: int, ldx: int, w_q4, group: int, bias, residual, ldr: int, Y,
                   ldy: int, m: int, n: int, p: int, stream=None) -> int:
     return _check(lib().q8d_q4_matmul(
-        _ptr(X), int(x_dtype), int(ldx), _ptr(w_q4), int(group), _ptr(bias), _ptr(residual),
-        int(ldr), _ptr(Y), int(ldy), int(m), int(n), int(p), _stream(stream)), "q8d_q4_matmul")
+        _ptr(X), x_dtype, ldx, _ptr(w_q4), group, _ptr(bias), _ptr(residual),
+        ldr, _ptr(Y), ldy, m, n, p, _stream(stream)), "q8d_q4_matmul")
 
 
 def q8d_q4_gated(X, x_dtype: int, ldx: int, wg_q4, wu_q4, group: int, H, ldh: int, m: int, n: int,
                  p: int, stream=None) -> int:
     return _check(lib().q8d_q4_gated(
-        _ptr(X), int(x_dtype), int(ldx), _ptr(wg_q4), _ptr(wu_q4), int(group), _ptr(H), int(ldh),
-        int(m), int(n), int(p), _stream(stream)), "q8d_q4_gated")
+        _ptr(X), x_dtype, ldx, _ptr(wg_q4), _ptr(wu_q4), group, _ptr(H), ldh,
+        m, n, p, _stream(stream)), "q8d_q4_gated")
 
 
 class Step:

@@ -295,3 +295,22 @@ def test_sixteen_rows_of_a_large_matrix(q8d, m):
     tol = 1.1 * gt * (np.abs(u) + ut) + np.abs(silu) * ut + 2.0 ** -20 * np.abs(silu * u) + 1e-37
     got = h.cpu().numpy()
     assert np.all(np.abs(got[:, :p] - silu * u) <= tol) and np.all(got[:, p:] == 7)
+
+
+@pytest.mark.parametrize("m,p,n,group,kind", [(1, 900_001, 64, 32, F32), (5, 700_000, 32, 64, F32), (16, 3584, 18944, 128, F32),
+                                              (16, 30000, 2048, 64, Q8_0), (12, 400_000, 96, 128, F16)])
+def test_many_strips(q8d, m, p, n, group, kind):
+    """More strips than a CTA sums up at once."""
+    W = Matrix(q8d, 46, p, n, group)
+    x, v, ld = activations(47, m, n, kind)
+    check(product(q8d, W, x, kind, ld, m), W, v)
+    if p * n < 4e7:
+        U = Matrix(q8d, 48, p, n, group)
+        h, y = torch.empty(m, p, device="cuda"), product(q8d, U, x, kind, ld, m)
+        q8d.q8d_q4_gated(x, kind, ld, W.bytes, U.bytes, group, h, p, m, n, p)
+        g = product(q8d, W, x, kind, ld, m)
+        torch.cuda.synchronize()
+        g, y = g.double(), y.double()
+        # (of the products as the other entry makes them, which cuts them up elsewhere: the bounds of both)
+        tol = dev(np.abs(v) @ np.abs(W.values).T) * y.abs() + g.abs() * dev(np.abs(v) @ np.abs(U.values).T)
+        assert torch.all((h.double() - g * torch.sigmoid(g) * y).abs() <= 2.5e-5 * tol + 2.0 ** -20 * (g * y).abs())
