@@ -32,7 +32,7 @@
 //
 // us in a graph (and TB/s of weights): one row, 896 -> 151936 15.1 (4.8), gated 3584
 // -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 23.3, sixteen f16 rows 28.4,
-// Q8_0 35.2; 18944 -> 3584, sixteen rows 32.1.  A call spends about four
+// Q8_0 35.2; 18944 -> 3584, sixteen rows 26.2.  A call spends about four
 // microseconds starting and meeting; then a tile takes 50 to 55 clocks with one
 // column group (150 instructions, 58 % of the issue slots), 80 with two (latency:
 // sixteen warps of 128 registers).
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
       const int pairs = pu * P.m, share = (pairs + A.cs - 1) / A.cs, mine = 16 * P.nmat;
       cluster_wait();  // (all of the cluster's CTAs run, and have read the last pass's)
       for (int o = first; o < pairs; o += kThreads / 16) {
-        const int unit = over_m(o), j = o - unit * P.m, owner = o & (A.cs - 1);
+        const int unit = over_m(o), j = o - unit * P.m, owner = o % A.cs;
         float* dst = red + (rank * share + o / A.cs) * mine + row;
         for (int e = 0; e < P.nmat; ++e) cluster_store(dst + 16 * e, owner, cta_sum(P.nmat * unit + e, j, row));
       }
@@ -688,7 +688,11 @@ int consider(const Q4Args& A, int strips, Plan* best) {
   if (!rc) rc = allow_wide_clusters(fn);
   if (rc) return rc;
   weigh<kWarps, MODE, NG, NS>(A, strips, 1, 16 / kWarps * sm_count(), best);
-  for (int cs = 2; cs <= kMaxCluster && cs <= A.kt; cs *= 2) {
+  // (six and nine fit the GPCs three and two times, where eight does twice and
+  // sixteen once: 18944 -> 3584, sixteen rows, 33.1, 31.8 and, with nine, 26.0 us)
+  constexpr int kSizes[] = {2, 4, 6, 8, 9, kMaxCluster};
+  for (const int cs : kSizes) {
+    if (cs > A.kt) break;
     int most = 0;
     rc = max_clusters(fn, cs, kWarps * 32, kWarps == 8 ? kHalfSmem : kMaxSmem, &most);
     if (rc) return rc;
@@ -771,7 +775,7 @@ int launch(const Q4Params& P, cudaStream_t stream) {
 
 // 9 to 16 f32 rows: in one launch, or as eight and the others, whichever is
 // expected to be faster (16 rows, us for one / two: 3584 -> 3584 11.3 / 16.8, 18944
-// -> 3584 32.3 / 38.7, gated 3584 -> 18944 50.8 / 46.4).
+// -> 3584 26.2 / 36.7, gated 3584 -> 18944 50.8 / 46.4).
 template <int NS>
 int launch_wide(const Q4Params& P, cudaStream_t stream) {
   Q4Args all, head;
