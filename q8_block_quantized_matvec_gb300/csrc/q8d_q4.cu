@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
     w.left -= w.n;
   };
 
-  Walk ahead;  // where the next copy starts
+  Walk ahead{};  // where the next copy starts
   int issued = 0;
   const uint8_t* src = nullptr;
   const auto locate = [&]() {

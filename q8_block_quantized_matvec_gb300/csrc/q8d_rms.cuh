@@ -4,9 +4,9 @@
 // An output in 8 or 4 bits is decided at borders between two codes, and a
 // factor that is off by one unit in the last place moves one of about 10^5
 // values across one.  The sum is therefore kept as an unevaluated pair of f32
-// (hi, lo), each square exact as product and fma remainder, each addition with
-// its rounding error by Knuth's two-sum (Moller, Knuth; Dekker's pairs): about
-// 2^-44 relative, so that the factor is 1 / sqrt in 64 bits rounded to f32 but
+// (hi, lo), each addition with its rounding error by Knuth's two-sum (Moller,
+// Knuth; Dekker's pairs), what it leaves of a square by one fma: about 2^-44
+// relative, so that the factor is 1 / sqrt in 64 bits rounded to f32 but
 // for one row in 10^6.  That costs eight packed f32x2 instructions for two
 // elements, four an element; the FP64 pipe takes half a clock of the SM for each.
 #pragma once
@@ -29,12 +29,6 @@ __device__ __forceinline__ void pair_add(Pair& p, float v) {
 __device__ __forceinline__ void pair_add(Pair& p, const Pair& o) {
   pair_add(p, o.hi);
   p.lo = __fadd_rn(p.lo, o.lo);
-}
-// p + v^2: the square is v * v and its remainder, exactly.
-__device__ __forceinline__ void pair_add_square(Pair& p, float v) {
-  const float s = __fmul_rn(v, v);
-  pair_add(p, s);
-  p.lo = __fadd_rn(p.lo, __fmaf_rn(v, v, -s));
 }
 // Two sums side by side, in packed f32x2 arithmetic: p + v^2.  (v * v's own
 // rounding needs no term: what t leaves of v^2 itself is one fma.)

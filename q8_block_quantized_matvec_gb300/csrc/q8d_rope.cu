@@ -190,30 +190,30 @@ __device__ __forceinline__ void angles(const float* row, int half, int layout, i
     get_shared<kE, true>(p + half, s);
 #pragma unroll
     for (int e = 0; e < kE / 2; ++e) s[e] = mul2(s[e], pack2(sign, sign));
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int e = 0; e < kE; e += 2) {
-    if (WAY == kPairs || layout == Q8D_ROPE_PAIRS) {
-      const int i = (el + e) / 2;
-      const float cv = i < half ? __ldg(row + i) : 1.f, sv = i < half ? __ldg(row + half + i) : 0.f;
-      c[e / 2] = pack2(cv, cv);
-      s[e / 2] = pack2(-sv, sv);
-      continue;
-    }
-    float cv[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f};
+    for (int e = 0; e < kE; e += 2) {
+      if (WAY == kPairs || layout == Q8D_ROPE_PAIRS) {
+        const int i = (el + e) / 2;
+        const float cv = i < half ? __ldg(row + i) : 1.f, sv = i < half ? __ldg(row + half + i) : 0.f;
+        c[e / 2] = pack2(cv, cv);
+        s[e / 2] = pack2(-sv, sv);
+        continue;
+      }
+      float cv[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f};
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      const int j = el + e + o;
-      if (j >= 2 * half) continue;
-      const bool up = j >= half;
-      const int i = up ? j - half : j;
-      cv[o] = __ldg(row + i);
-      sv[o] = __ldg(row + half + i);
-      if (!up) sv[o] = -sv[o];
+      for (int o = 0; o < 2; ++o) {
+        const int j = el + e + o;
+        if (j >= 2 * half) continue;
+        const bool up = j >= half;
+        const int i = up ? j - half : j;
+        cv[o] = __ldg(row + i);
+        sv[o] = __ldg(row + half + i);
+        if (!up) sv[o] = -sv[o];
+      }
+      c[e / 2] = pack2(cv[0], cv[1]);
+      s[e / 2] = pack2(sv[0], sv[1]);
     }
-    c[e / 2] = pack2(cv[0], cv[1]);
-    s[e / 2] = pack2(sv[0], sv[1]);
   }
 }
 
