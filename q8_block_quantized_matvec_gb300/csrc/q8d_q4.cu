@@ -31,8 +31,8 @@
 //    that of the one that finishes them, both in a fixed order.
 //
 // us in a graph (and TB/s of weights): one row, 896 -> 151936 15.1 (4.8), gated 3584
-// -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 23.3, sixteen f16 rows 28.4,
-// Q8_0 35.2; 18944 -> 3584, sixteen rows 26.2.  A call spends about four
+// -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 23.3, sixteen f16 rows 27.5,
+// Q8_0 34.8; 18944 -> 3584, sixteen rows 26.2.  A call spends about four
 // microseconds starting and meeting; then a tile takes 50 to 55 clocks with one
 // column group (150 instructions, 58 % of the issue slots), 80 with two (latency:
 // sixteen warps of 128 registers).
@@ -49,18 +49,18 @@
 namespace q8d {
 namespace {
 
+enum Mode { kF32 = 0, kF16 = 1, kQ8 = 2 };  // the rows of X
+
 constexpr int kMaxCluster = 16;  // CTAs (more than eight are no portable size)
 constexpr int kMaxStages = 4;    // copies of a warp in flight
 // Tiles a copy.
-__host__ __device__ constexpr int chunk_tiles(int ng) { return ng == 1 ? 4 : 2; }
+__host__ __device__ constexpr int chunk_tiles(int mode, int ng) { return ng > 1 && mode == kF32 ? 2 : 4; }
 // Strips (of either matrix) that a pass sums up at most, and how many of them a
 // warp's range of a pass may touch.
 constexpr int kMaxParts = 128;
 __host__ __device__ constexpr int pass_slots(int warps, int parts) { return parts / warps + 2; }
 constexpr int kMaxSmem = 232448;   // of a CTA alone on its SM
 constexpr int kHalfSmem = 115712;  // of two (228 KB an SM, 1 KB of it for each CTA)
-
-enum Mode { kF32 = 0, kF16 = 1, kQ8 = 2 };
 
 // Rows of the batch a column group of eight takes, and sums a lane keeps of it.
 __host__ __device__ constexpr int group_rows(int mode) { return mode == kF32 ? 4 : 8; }
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
   constexpr int kThreads = kWarps * 32;
   constexpr int kSums = MODE == kF32 ? 2 : 4;  // a lane and column group
   constexpr int kRec = kQ4QuantBytes + kQ4Rows * NS * 2;
-  constexpr int kChunk = chunk_tiles(NG), kStage = kChunk * kRec;
+  constexpr int kChunk = chunk_tiles(MODE, NG), kStage = kChunk * kRec;
   const Q4Params& P = A.P;
   const int slot_floats = pass_slots(kWarps, A.parts) * kMp * 16;  // a warp's parts
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -466,7 +466,13 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
               }
             }
         };
-        if (n == kChunk) {
+        // (us, whole copies unrolled / tiles unrolled with a branch each / a loop: one
+        // row, gated 3584 -> 18944, 15.2 / 15.6 / -; eight 23.3 / 23.5 / 25.3; sixteen
+        // Q8_0 rows, gated 3584 -> 4736, 15.1 / 15.1 / 14.6, 18944 28.4 / 26.6 / 27.6 in f16)
+        if (MODE != kF32 && NG > 1) {
+#pragma unroll 1
+          for (int c = 0; c < n; ++c) work(c);
+        } else if (n == kChunk) {
 #pragma unroll
           for (int c = 0; c < kChunk; ++c) work(c);
         } else {
@@ -645,7 +651,7 @@ constexpr double tile_ns(int mode, int ng, int scales) {
 // way so far.
 template <int kWarps, int MODE, int NG, int NS>
 void weigh(const Q4Args& A, int strips, int cs, int most, Plan* best) {
-  constexpr int kStage = chunk_tiles(NG) * (kQ4QuantBytes + kQ4Rows * NS * 2) * kWarps;
+  constexpr int kStage = chunk_tiles(MODE, NG) * (kQ4QuantBytes + kQ4Rows * NS * 2) * kWarps;
   constexpr int kLimit = kWarps == 8 ? kHalfSmem : kMaxSmem;
   const int ktl = (A.kt + cs - 1) / cs, ncl = std::min(most, strips), units = (strips + ncl - 1) / ncl;
   const int ctas = ncl * cs > sm_count() ? 16 / kWarps : 1;  // an SM
