@@ -526,7 +526,8 @@ int q8d_q4_unpack(const void* w_q4, void* dst, int dst_dtype, long long ld, int 
 /* ------------------------------------------------------------------------
  * q8d_q4_matmul - a 4-bit matrix applied to m rows of activations:
  *   Y[i][r] = sum_k X[i][k] * W[r][k] (+ bias[r]) (+ residual[i][r])
- * within 1e-5 of the sum of |terms|.
+ * within 1e-5 of the sum of |terms| (and 2^-126, below f32's normal range),
+ * however far the elements of a row lie apart.
  *   X: device rows of x_dtype, ldx elements apart (>= n): Q8D_KV_F32 or
  *      Q8D_KV_F16 (16-byte aligned, ldx % 4 == 0, f16 % 8 == 0), or Q8D_KV_Q8_0:
  *      rows of Q8_0 blocks as q8d_rmsnorm_rows writes them (2-byte aligned,
@@ -538,7 +539,8 @@ int q8d_q4_unpack(const void* w_q4, void* dst, int dst_dtype, long long ld, int 
  *      written; must not overlap any other operand
  * 0 <= m <= 16, 32 <= n <= 32768, n % 32 == 0, p <= 2^30; else
  * Q8D_EUNSUPPORTED.  m == 0 or p == 0: no-op.  Matrices are read once (with more than
- * eight f32 rows at most twice).  Nothing depends on the order in which threads
+ * eight f32 rows at most twice; what meets f32 elements below 2^-32 of the largest
+ * of their 128 columns once more).  Nothing depends on the order in which threads
  * finish.  Waits inside are bounded (seconds); the sums that miss a copy are NaN.
  * ---------------------------------------------------------------------- */
 int q8d_q4_matmul(const void* X, int x_dtype, long long ldx, const void* w_q4, int group,

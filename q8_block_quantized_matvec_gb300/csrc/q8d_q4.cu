@@ -18,9 +18,12 @@
 //  * A pair of quants costs one LOP3 under the exponent of 1024 (1024 + n, or
 //    1024 + 16 n of the half-byte above) and one exact f16 subtraction or fma
 //    that leaves n - 8.
-//  * An f32 row enters as f16 hi + lo under a power of two for every 128 columns
-//    (2^-22 relative, at least 2^-39 of the tile's largest), f16 rows as they
-//    are, Q8_0 rows as their whole numbers, their scales applied to the sums.
+//  * An f32 row enters as f16 hi + 2^-12 lo under a power of two for every 128
+//    columns (2^-22 relative, 2^-51 of the tile's largest at worst), f16 rows as
+//    they are, Q8_0 rows as their whole numbers, their scales applied to the sums.
+//    What that leaves of elements below 2^-32 of their tile's largest (kFar) is
+//    added in 64 bits where the sums meet, so that an outlier on a weight of zero
+//    costs its neighbours nothing.
 //    The products are exact in f32; those of one scale, 128 columns at most, are
 //    summed from zero on the tensor cores, the scales are applied outside and all
 //    further sums are rounded f32 additions, because the tensor core cuts its own
@@ -30,9 +33,9 @@
 //    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs' in
 //    that of the one that finishes them, both in a fixed order.
 //
-// us in a graph (and TB/s of weights): one row, 896 -> 151936 15.1 (4.8), gated 3584
-// -> 18944 15.2 (5.0), 3584 -> 4608 5.6; gated, eight rows 23.3, sixteen f16 rows 27.5,
-// Q8_0 34.8; 18944 -> 3584, sixteen rows 26.2.  A call spends about four
+// us in a graph (and TB/s of weights): one row, 896 -> 151936 15.3 (4.8), gated 3584
+// -> 18944 15.5 (4.9), 3584 -> 4608 5.8; gated, eight rows 23.5, sixteen f16 rows 27.6,
+// Q8_0 34.8; 18944 -> 3584, sixteen rows 26.4.  A call spends about four
 // microseconds starting and meeting; then a tile takes 50 to 55 clocks with one
 // column group (150 instructions, 58 % of the issue slots), 80 with two (latency:
 // sixteen warps of 128 registers).
@@ -84,17 +87,18 @@ __host__ __device__ constexpr int scale_floats(int mode, int mp, int ktl) {
   return mode == kF32 ? mp * ktl : mode == kQ8 ? mp * 4 * ktl : 0;
 }
 struct Smem {  // offsets
-  int scale, part, red, meets, bars, ring;  // (the ring's stages take what is left)
+  int scale, far, part, red, meets, bars, ring;  // (the ring's stages take what is left)
 };
 __host__ __device__ inline Smem smem_layout(int warps, int mode, int ng, int ktl, int ncol, int parts,
                                             int cs) {
   const int mp = ng * group_rows(mode);
   Smem s;
   s.scale = ncol * x_stride(ktl) * 2;
-  s.part = s.scale + ((scale_floats(mode, mp, ktl) * 4 + 15) & ~15);
+  s.far = s.scale + ((scale_floats(mode, mp, ktl) * 4 + 15) & ~15);
+  s.part = s.far + (mode == kF32 ? (mp * ktl + 15) & ~15 : 0);
   s.red = s.part + warps * pass_slots(warps, parts) * mp * 16 * 4;
   s.meets = s.red + (cs > 1 ? (parts * mp + 2 * cs) * 16 * 4 : 0);
-  s.bars = s.meets + (parts * 4 + 15 & ~15);
+  s.bars = s.meets + (parts * 4 + 4 + 15 & ~15);  // (and whether rows have far elements)
   s.ring = (s.bars + warps * kMaxStages * 8 + 127) & ~127;
   return s;
 }
@@ -188,12 +192,79 @@ __device__ __forceinline__ void cluster_store(float* p, uint32_t rank, float v) 
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
+// f32 elements below this under their tile's power of two are `far`: hi + 2^-12 lo,
+// 2^-37 at best, is no longer within 2^-19 of them.
+constexpr float kFar = 0x1p-18f;
+// Two elements x times `by` as f16 hi and what that leaves (exactly, times 2^12 too).
+__device__ __forceinline__ void split2(uint64_t x, float by, __half2& hi, __half2& lo) {
+  float a, b;
+  unpack2(mul2(x, pack2(by, by)), a, b);
+  hi = __floats2half2_rn(a, b);
+  const float2 h = __half22float2(hi);
+  const float by12 = by * 0x1p12f;
+  unpack2(fma2(pack2(h.x, h.y), pack2(-0x1p12f, -0x1p12f), mul2(x, pack2(by12, by12))), a, b);
+  lo = __floats2half2_rn(a, b);
+}
+// Adds what the operand lacks of the far elements, times their weights, to the sums
+// of a pass (its strips pa .. pa + pu - 1), into those of the first warp that met a
+// part.  Its CTA's tiles of a strip are the ktl from k0 on.  (Rows of real streams
+// hold no such elements; 3584 -> 18944, gated, one row: 15.3 us, with one of them 20.3,
+// with one in every tile 73.)
+template <int kWarps, int NG, int NS>
+__device__ __noinline__ void add_far_terms(const Q4Args& A, uint8_t* smem, int pa, int pu, int k0, int ktl) {
+  constexpr int kRec = kQ4QuantBytes + kQ4Rows * NS * 2, kMp = NG * group_rows(kF32);
+  const Q4Params& P = A.P;
+  const int most = (A.kt + A.cs - 1) / A.cs, parts = pu * P.nmat, cols = min(ktl * kQ4Cols, P.n - k0 * kQ4Cols);
+  const Smem L = smem_layout(kWarps, kF32, NG, most, A.ncol, A.parts, A.cs);
+  const int row = threadIdx.x & 15, h = row / 8, g = row & 7;
+  const uint32_t half = 0xffffu << (threadIdx.x & 16);  // the sixteen threads of a strip and row of X
+  for (int o = threadIdx.x / 16; o < parts * P.m; o += kWarps * 2) {
+    const int sp = o / P.m, j = o - sp * P.m, unit = pa + sp / P.nmat;
+    const float* scale = reinterpret_cast<const float*>(smem + L.scale) + j * most;
+    const float* x = static_cast<const float*>(P.X) + j * P.ldx + k0 * kQ4Cols;
+    const uint8_t* tiles = P.w[sp % P.nmat] + ((long long)unit * A.kt + k0) * kRec;
+    double sum = 0.0;
+    for (int k = 0; k < ktl; ++k) {
+      if (!smem[L.far + j * most + k]) continue;
+      const float back = scale[k], by = 1.f / back;  // (powers of two)
+      const uint8_t* tile = tiles + (long long)k * kRec;
+      float v[kQ4Cols / 16];
+#pragma unroll
+      for (int i = 0; i < kQ4Cols / 16; ++i) {
+        const int c = k * kQ4Cols + 16 * i + row;
+        v[i] = c < cols ? x[c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kQ4Cols / 16; ++i) {
+        uint32_t hits = __ballot_sync(half, v[i] != 0.f && fabsf(v[i]) < kFar * back) >> (threadIdx.x & 16) & 0xffffu;
+        for (; hits; hits &= hits - 1) {
+          const int c = 16 * i + __ffs(hits) - 1, b = c / 32, t = c / 8 & 3, e = c & 7;
+          const float f = __shfl_sync(half, v[i], c & 15, 16);
+          __half2 hi, lo;
+          split2(pack2(f, f), by, hi, lo);
+          const double held = (double)__low2float(hi) + (double)__low2float(lo) * 0x1p-12;
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + 512 * h + 16 * (4 * g + t) + 4 * b);
+          const unsigned short s =
+              *reinterpret_cast<const unsigned short*>(tile + kQ4QuantBytes + 2 * (NS * (2 * g + h) + b * NS / 4));
+          sum += (f - held * back) * ((int)(w >> (4 * (e / 2 + 4 * (e & 1))) & 15u) - 8) * (double)f16_bits_to_f32(s);
+        }
+      }
+    }
+    const uint32_t met = reinterpret_cast<const uint32_t*>(smem + L.meets)[sp];
+    const int slot = (__ffs(met) - 1) * pass_slots(kWarps, A.parts) + (int)(met >> 24);
+    reinterpret_cast<float*>(smem + L.part)[(slot * kMp + j) * 16 + row] += (float)sum;
+  }
+  __syncthreads();
+}
+
 // The activations' columns [128 k0, 128 (k0 + ktl)) as the MMA's second operand.
 // xstep: x_stride; most: tiles of the largest part of a row.
+// far: whether a tile of an f32 row has far elements, [row][tile];
+// returns whether this thread met one.
 // then(): what is to be started once the first loads are on their way.
 template <int MODE, int kWarps, int kMp, typename Then>
-__device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int most, int xstep, __half* xf,
-                                        float* scale, Then then) {
+__device__ __forceinline__ bool build_x(const Q4Args& A, int k0, int ktl, int most, int xstep, __half* xf,
+                                        float* scale, uint8_t* far, Then then) {
   constexpr int kLoads = kWarps / 2;  // items a warp loads before it uses the first
   const Q4Params& P = A.P;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -207,6 +278,7 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mo
     }
   };
   wrap();
+  bool met_far = false;
   if (j >= P.m) then();
   for (bool started = false; j < P.m; started = true) {
     int js[kLoads], ks[kLoads];
@@ -237,6 +309,7 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mo
       }
     }
     if (!started) then();
+    uint32_t suspects = 0;  // items with elements that may be far
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
       const int j = js[l], k = ks[l];
@@ -250,18 +323,21 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mo
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
         top = __reduce_max_sync(0xffffffffu, top);
-        const int up = top ? min(14 - ((int)(top >> 23) - 127), 126) : 0;  // largest into [2^14, 2^15)
+        const int up = top ? min(14 - ((int)(top >> 23) - 127), 114) : 0;  // largest into [2^14, 2^15)
         const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-        __half hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = v[e] * by;
-          hi[e] = __float2half_rn(w);
-          lo[e] = __float2half_rn(w - __half2float(hi[e]));
-        }
+        __half2 hi[2], lo[2];
+        split2(pack2(v[0], v[1]), by, hi[0], lo[0]);
+        split2(pack2(v[2], v[3]), by, hi[1], lo[1]);
         *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(hi);
         *reinterpret_cast<uint2*>(dst + xstep) = *reinterpret_cast<const uint2*>(lo);
-        if (lane == 0) scale[j * most + k] = __uint_as_float((uint32_t)(127 - up) << 23);
+        if (lane == 0) {
+          scale[j * most + k] = __uint_as_float((uint32_t)(127 - up) << 23);
+          far[j * most + k] = 0;
+        }
+        // (zeros are no far elements, but are told apart below)
+        const __half2 least = __hmin2(__habs2(hi[0]), __habs2(hi[1]));
+        const bool small = !__hbge2(least, __float2half2_rn(kFar));
+        suspects |= (__any_sync(0xffffffffu, small) ? 1u : 0u) << l;
       } else if constexpr (MODE == kF16) {
         *reinterpret_cast<uint2*>(dst) = u[l];
       } else {
@@ -274,12 +350,28 @@ __device__ __forceinline__ void build_x(const Q4Args& A, int k0, int ktl, int mo
         if (at == 0) scale[(k * 4 + lane / 8) * kMp + j] = f16_bits_to_f32(d[l]);
       }
     }
+    if (MODE == kF32 && suspects) {
+      __syncwarp();
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        if (!(suspects >> l & 1u)) continue;
+        const int at = js[l] * most + ks[l];
+        const float limit = kFar * scale[at], v[4] = {f[l].x, f[l].y, f[l].z, f[l].w};
+        bool out = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out |= v[e] != 0.f && fabsf(v[e]) < limit;
+        out = __any_sync(0xffffffffu, out);
+        met_far |= out;
+        if (lane == 0 && out) far[at] = 1;
+      }
+    }
   }
+  return met_far;
 }
 
 // kWarps warps a CTA, sixteen an SM
 template <int kWarps, int MODE, int NG, int NS>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Args A) {
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const __grid_constant__ Q4Args A) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kMp = NG * group_rows(MODE);     // rows of the batch that fit
   constexpr int kThreads = kWarps * 32;
@@ -297,6 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
   const Smem L = smem_layout(kWarps, MODE, NG, ktl_max, A.ncol, A.parts, A.cs);
   __half* xf = reinterpret_cast<__half*>(smem);
   float* xs = reinterpret_cast<float*>(smem + L.scale);
+  uint8_t* far = smem + L.far;
   float* part = reinterpret_cast<float*>(smem + L.part);
   float* red = reinterpret_cast<float*>(smem + L.red);
   uint32_t* meets = reinterpret_cast<uint32_t*>(smem + L.meets);
@@ -378,10 +471,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
   };
   const bool rows_first = P.m <= 2;
   if (!rows_first) start();
-  build_x<MODE, kWarps, kMp>(A, k0, ktl, ktl_max, xstep, xf, xs, [&]() {
+  const bool mine_far = build_x<MODE, kWarps, kMp>(A, k0, ktl, ktl_max, xstep, xf, xs, far, [&]() {
     if (rows_first) start();
   });
-  __syncthreads();
+  const bool any_far = __syncthreads_or(mine_far);
+  if (threadIdx.x == 0) meets[A.parts] = any_far;  // (read behind the next barrier)
 
   const Magic magic;
   int stage = 0, taken = 0;
@@ -441,8 +535,9 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
                 mma16816(d[q], r0[2], r1[2], r0[3], r1[3], v.z, v.w);
                 if (b % kSame != kSame - 1) continue;
                 if constexpr (MODE == kF32) {
-                  sum[q][0] = b >= kSame ? fmaf(s0, d[q][0] + d[q][1], sum[q][0]) : s0 * (d[q][0] + d[q][1]);
-                  sum[q][1] = b >= kSame ? fmaf(s1, d[q][2] + d[q][3], sum[q][1]) : s1 * (d[q][2] + d[q][3]);
+                  const float v0 = fmaf(d[q][1], 0x1p-12f, d[q][0]), v1 = fmaf(d[q][3], 0x1p-12f, d[q][2]);
+                  sum[q][0] = b >= kSame ? fmaf(s0, v0, sum[q][0]) : s0 * v0;
+                  sum[q][1] = b >= kSame ? fmaf(s1, v1, sum[q][1]) : s1 * v1;
                 } else if constexpr (MODE == kF16) {
                   acc[q][0] = fmaf(s0, d[q][0], acc[q][0]);
                   acc[q][1] = fmaf(s0, d[q][1], acc[q][1]);
@@ -534,6 +629,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const Q4Ar
     const uint32_t by_m = 65536u / P.m + 1;
     const auto over_m = [&](int x) { return (int)((uint32_t)x * by_m >> 16); };
     const int row = threadIdx.x & 15, first = threadIdx.x / 16;
+    if constexpr (MODE == kF32)
+      if (meets[A.parts]) add_far_terms<kWarps, NG, NS>(A, smem, pa, pu, k0, ktl);
     const auto finish = [&](int unit, int j, float v, float up) {
       const int r = (pa + unit) * kQ4Rows + row;
       if (r >= P.p) return;
