@@ -45,7 +45,9 @@
  *               Rows are written by the Q8_0 quantizer: per block
  *               d = max|x| / 127, q_j = x_j * (1/d) rounded to nearest with
  *               halves away from zero, scale = d rounded to binary16, all in
- *               f32 (an all-zero block stores zeros); inputs must be finite.
+ *               f32 (an all-zero block stores zeros); inputs must be finite
+ *               (a NaN or an infinity leaves a block whose scale is NaN or
+ *               infinite).
  *   4-bit KV    Q8D_KV_Q4: blocks of 32 elements as 16 bytes of quants and
  *               one binary16 scale, kept as two planes: row t's quants are
  *               the kv_width/2 bytes from byte t * kv_width/2 of the
@@ -409,7 +411,8 @@ int q8d_moe_set_wait_limit(unsigned polls);
  * Pointers are aligned to their elements (y as Q8_0 to 2 bytes); 16-byte
  * accesses where all pointers and distances allow them.  y must not overlap
  * any other operand, nor sum_out one that it is not.  A row that holds a NaN or
- * an infinity gives what the formula gives in 64 bits (NaN or zeros).
+ * an infinity gives what the formula gives in 64 bits (NaN or zeros; as Q8_0 a
+ * block with a NaN among its values has the scale NaN).
  * ---------------------------------------------------------------------- */
 int q8d_rmsnorm_rows(const void* x, const void* residual, void* sum_out, int row_dtype,
                      long long ldx, long long ldr, long long lds, const float* weight, float eps,

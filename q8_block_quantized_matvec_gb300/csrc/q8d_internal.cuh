@@ -169,6 +169,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// max(a, b), a NaN where either is one (fmaxf drops it): a Q8_0 block that meets a
+// NaN must not come out as finite numbers.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ---- Q8_0 decoding helpers ------------------------------------------------
 // Signed byte q placed in the mantissa of 2^23: the float 2^23 + (q + 128)
 // is exact, so subtracting 2^23 + 128 yields q exactly with one add.  The

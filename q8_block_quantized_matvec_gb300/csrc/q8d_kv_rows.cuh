@@ -123,9 +123,9 @@ template <int kE>
 __device__ __forceinline__ void put_q8_0(uint8_t* blk, int part, const float (&f)[kE], bool live) {
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < kE; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  for (int i = 0; i < kE; ++i) amax = max_nan(amax, fabsf(f[i]));
 #pragma unroll
-  for (int o = 1; o < 32 / kE; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 1; o < 32 / kE; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (!live) return;
   const float d = q8_0_step(amax);
   const float id = d != 0.f ? __frcp_rn(d) : 0.f;
