@@ -16,7 +16,8 @@
  *     Q8D_ETIMEOUT    a bounded host wait ran out
  *     Q8D_ENOMEM      the library's own allocation failed (step create; the
  *                     host's memory under a product's plan)
- * On any non-zero status nothing was launched.  There is no fallback path:
+ * On any non-zero status nothing was launched (but where a call of several
+ * launches gets Q8D_ECUDA for one behind the first).  There is no fallback path:
  * an unsupported case is refused, never computed another way.
  *
  * Quantities that live in device memory (positions, lengths, token ids) are

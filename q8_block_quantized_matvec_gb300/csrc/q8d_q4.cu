@@ -877,7 +877,7 @@ int launch(const Q4Params& P, cudaStream_t stream) {
 }
 
 // 9 to 16 f32 rows: in one launch, or as eight and the others, whichever is
-// expected to be faster (16 rows, us for one / two: 3584 -> 3584 11.3 / 16.8, 18944
+// expected to be faster; both are planned before the first is launched (16 rows, us for one / two: 3584 -> 3584 11.3 / 16.8, 18944
 // -> 3584 26.2 / 36.7, gated 3584 -> 18944 50.8 / 46.4).
 template <int NS>
 int launch_wide(const Q4Params& P, cudaStream_t stream) {
@@ -891,13 +891,17 @@ int launch_wide(const Q4Params& P, cudaStream_t stream) {
   if (rc) return rc;
   // (eight rows take as long as five, and four about two thirds of that; a launch 4 us)
   if (pa.cs && (!ph.cs || pa.ns <= ph.ns * (P.m > 12 ? 2.0 : 1.7) + 4000)) return launch_made<kF32, 4, NS>(all, pa, stream);
-  rc = launch_made<kF32, 2, NS>(head, ph, stream);
-  if (rc) return rc;
   Q.m = P.m - 8;
   Q.X = static_cast<const float*>(P.X) + 8 * P.ldx;
   Q.Y = P.Y + 8 * P.ldy;
   Q.residual = P.residual ? P.residual + 8 * P.ldr : nullptr;
-  return Q.m > 4 ? launch<kF32, 2, NS>(Q, stream) : launch<kF32, 1, NS>(Q, stream);
+  Q4Args rest;
+  Plan pr;
+  rc = Q.m > 4 ? make_plan<kF32, 2, NS>(Q, &rest, &pr) : make_plan<kF32, 1, NS>(Q, &rest, &pr);
+  if (!rc && (ph.cs == 0 || pr.cs == 0)) rc = Q8D_EUNSUPPORTED;
+  if (!rc) rc = launch_made<kF32, 2, NS>(head, ph, stream);
+  if (rc) return rc;
+  return Q.m > 4 ? launch_made<kF32, 2, NS>(rest, pr, stream) : launch_made<kF32, 1, NS>(rest, pr, stream);
 }
 
 template <int MODE, int NG>

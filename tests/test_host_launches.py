@@ -1,0 +1,56 @@
+"""What the entry points launch, seen from the host: the library runs in a child
+process behind a stand-in for the CUDA runtime (fake_cudart.c) that launches
+nothing, counts, and fails where it is told to.  No GPU."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+CHILD = """
+import ctypes as C, sys
+fake, L = C.CDLL(sys.argv[1]), C.CDLL(sys.argv[2])
+vp, i32, i64, f32 = C.c_void_p, C.c_int, C.c_longlong, C.c_float
+L.q8d_q4_matmul.argtypes = [vp, i32, i64, vp, i32, vp, vp, i64, vp, i64, i32, i32, i32, vp]
+L.q8d_q4_gated.argtypes = [vp, i32, i64, vp, vp, i32, vp, i64, i32, i32, i32, vp]
+L.q8d_rmsnorm_rows.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, f32, vp, i32, i64, i32, i32, vp]
+M = 1 << 40  # addresses, far apart
+"""
+
+
+@pytest.fixture(scope="module")
+def child(tmp_path_factory):
+    from q8_block_quantized_matvec_gb300 import build
+    lib = build.build()
+    fake = str(tmp_path_factory.mktemp("fake") / "libfake_cudart.so")
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-o", fake, os.path.join(HERE, "fake_cudart.c")], check=True)
+
+    def run(code):
+        env = dict(os.environ, LD_PRELOAD=fake)
+        r = subprocess.run([sys.executable, "-S", "-c", CHILD + code, fake, lib], env=env, capture_output=True, text=True,
+                           timeout=120)
+        assert r.returncode == 0, r.stderr
+        return [tuple(int(v) for v in line.split()) for line in r.stdout.splitlines()]
+    return run
+
+
+GATED = "L.q8d_q4_gated(M, 0, 3584, 2 * M, 3 * M, 32, 4 * M, 18944, {m}, 3584, 18944, None)"
+
+
+@pytest.mark.parametrize("m", [11, 16])
+def test_nothing_is_launched_where_a_call_fails(child, m):
+    """The two launches of 9 to 16 f32 rows: whichever call of the runtime fails,
+    only a launch's own failure may leave one behind."""
+    call = GATED.format(m=m)
+    (rc, calls, launches), = child(f"fake.fake_reset(0)\nprint({call}, fake.fake_calls(), fake.fake_launches())")
+    assert rc == 0 and launches == 2
+    refused = 0
+    for at in range(1, calls + 1):
+        (rc, done, launch), = child(
+            f"fake.fake_reset({at})\nprint({call}, fake.fake_launches(), fake.fake_failed_launch())")
+        # (a number of SMs that is not to be had is no failure: one is taken)
+        assert (rc == 0 and not launch) or (rc == -5 and (done == 0 or launch)), at
+        refused += rc != 0 and not launch
+    assert refused > 10
