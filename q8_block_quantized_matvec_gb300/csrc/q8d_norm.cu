@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(most_threads(kV * kK)) rmsnorm_kernel(const No
 
 template <typename T, int OUT, int kV, int ACCESS, int kK>
 int launch_k(const NormArgs& A, cudaStream_t stream) {
-  const dim3 grid((unsigned)((A.P.rows + A.per - 1) / A.per));
+  const dim3 grid((unsigned)((A.P.rows + (A.per - 1LL)) / A.per));
   return launch_ex(rmsnorm_kernel<T, OUT, kV, kK, ACCESS>, grid, dim3(A.tpr, A.per), 0, stream, true, A);
 }
 

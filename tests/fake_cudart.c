@@ -5,7 +5,7 @@
 
 enum { kFails = 2 }; /* cudaErrorMemoryAllocation */
 static int calls, fail_at, launches, failed_launch;
-static unsigned grids[64][3];
+static unsigned grids[64][6];
 
 void fake_reset(int at) { calls = launches = failed_launch = 0, fail_at = at; }
 int fake_calls(void) { return calls; }
@@ -36,11 +36,11 @@ int cudaOccupancyMaxActiveClusters(int* n, const void* fn, const void* config) {
 }
 int cudaLaunchKernelExC(const void* config, const void* fn, void** args) {
   (void)fn, (void)args;
-  const unsigned* grid = config; /* the configuration begins with the grid */
+  const unsigned* grid = config; /* the configuration begins with the grid and the block */
   const int rc = next();
   failed_launch |= rc != 0;
   if (rc == 0 && launches < 64) {
-    for (int i = 0; i < 3; ++i) grids[launches][i] = grid[i];
+    for (int i = 0; i < 6; ++i) grids[launches][i] = grid[i];
     ++launches;
   }
   return rc;

@@ -54,3 +54,15 @@ def test_nothing_is_launched_where_a_call_fails(child, m):
         assert (rc == 0 and not launch) or (rc == -5 and (done == 0 or launch)), at
         refused += rc != 0 and not launch
     assert refused > 10
+
+
+@pytest.mark.parametrize("n", [1, 7, 32, 100, 3584])
+@pytest.mark.parametrize("rows", [1, 2 ** 31 - 40, 2 ** 31 - 31, 2 ** 31 - 1])
+def test_blocks_of_a_norm(child, rows, n):
+    """Every row has a block, up to the largest count of rows."""
+    (rc, launches, x, y, z, _, per, _), = child(f"""
+fake.fake_reset(0)
+rc = L.q8d_rmsnorm_rows(M, None, None, 1, {n}, 0, 0, 64 * M, 1e-6, 128 * M, 1, {n}, {rows}, {n}, None)
+print(rc, fake.fake_launches(), *(fake.fake_grid(0, i) for i in range(6)))""")
+    # (a block is threads of a row by rows)
+    assert rc == 0 and launches == 1 and (x, y, z) == (-(-rows // per), 1, 1)
