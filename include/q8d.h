@@ -390,6 +390,9 @@ int q8d_moe_set_wait_limit(unsigned polls);
  * 4-bit weights: norm -> projections -> rotary positions and cache ->
  * attention -> projection + residual -> norm -> gated projections ->
  * projection + residual.  None needs a workspace.
+ *   Operands that must not overlap may be columns of one buffer, where their
+ * rows are the same number of bytes apart and share none; operands whose rows
+ * are not count whole, from the first row's start to the last one's end.
  * ---------------------------------------------------------------------- */
 
 /* ------------------------------------------------------------------------

@@ -11,17 +11,29 @@ namespace {
 bool row_type(int t) { return t == Q8D_KV_F32 || t == Q8D_KV_F16; }
 int row_align(int t) { return t == Q8D_KV_F32 ? 4 : 2; }  // (Q8_0 rows: 2)
 
+// An operand's bytes: n of them from p on; rows of `row` bytes, `pitch` apart (0: in
+// one piece).
 struct Span {
   const void* p;
   size_t n;
+  long long row = 0, pitch = 0;
 };
-// `rows` rows of n elements, ld apart, counted whole from the first one's start
-// to the last one's end (nothing without a pointer).
+// `rows` rows of n elements, ld apart (nothing without a pointer).
 Span rows_span(const void* p, int dtype, long long rows, long long ld, long long n) {
   if (!p || rows <= 0) return {nullptr, 0};
-  return {p, (size_t)(kv_bytes(dtype, ld) * (rows - 1) + kv_bytes(dtype, n))};
+  const long long row = kv_bytes(dtype, n), pitch = kv_bytes(dtype, ld);
+  return {p, (size_t)(pitch * (rows - 1) + row), row, pitch};
 }
-bool meets(const Span& a, const Span& b) { return overlap(a.p, a.n, b.p, b.n); }
+// Whether two operands share a byte.  Rows of one pitch may be other columns of one
+// buffer; those of different ones are counted whole, from the first one's start to
+// the last one's end.
+bool meets(const Span& a, const Span& b) {
+  if (!overlap(a.p, a.n, b.p, b.n)) return false;
+  if (!a.pitch || a.pitch != b.pitch) return true;
+  const long long off = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  const long long at = (off % a.pitch + a.pitch) % a.pitch;  // where b's rows start between a's
+  return at < a.row || at + b.row > a.pitch;
+}
 
 // Largest distance between rows: (2^31 - 1) rows of it stay below 2^63 bytes.
 constexpr long long kMaxLd = 1LL << 29;
@@ -175,17 +187,8 @@ int q8d_rope_append_rows(const q8d_rope_desc* d, const void* q, const void* k, c
   const Span out[] = {so, {kcache, cb}, {vcache, cb}}, in[] = {sq, sk, sv, st};
   const bool same = q == q_out && d->ldq == d->ldo && d->row_dtype == d->q_dtype;
   for (const Span& o : out)
-    for (const Span& i : in) {
-      // (q turned in place: k and v may be other columns of the same rows)
-      if (&o == &out[0] && same && &i == &in[0]) continue;
-      if (&o == &out[0] && same && (&i == &in[1] || &i == &in[2]) && d->ldkv == d->ldq) {
-        const long long pitch = kv_bytes(d->row_dtype, d->ldq);
-        const long long off = reinterpret_cast<intptr_t>(i.p) - reinterpret_cast<intptr_t>(q);
-        const long long at = ((off % pitch) + pitch) % pitch;
-        if (at >= kv_bytes(d->row_dtype, qw) && at + kv_bytes(d->row_dtype, kw) <= pitch) continue;
-      }
-      if (meets(o, i)) return Q8D_EINVAL;
-    }
+    for (const Span& i : in)
+      if (meets(o, i) && !(&o == &out[0] && &i == &in[0] && same)) return Q8D_EINVAL;  // (q turned in place)
   for (int x = 0; x < 3; ++x)
     for (int y = x + 1; y < 3; ++y)
       if (meets(out[x], out[y])) return Q8D_EINVAL;

@@ -66,3 +66,35 @@ rc = L.q8d_rmsnorm_rows(M, None, None, 1, {n}, 0, 0, 64 * M, 1e-6, 128 * M, 1, {
 print(rc, fake.fake_launches(), *(fake.fake_grid(0, i) for i in range(6)))""")
     # (a block is threads of a row by rows)
     assert rc == 0 and launches == 1 and (x, y, z) == (-(-rows // per), 1, 1)
+
+
+def statuses(child, calls):
+    lines = "".join(f"print({c})\n" for c in calls)
+    return [rc for rc, in child("fake.fake_reset(0)\n" + lines)]
+
+
+def test_columns_of_one_buffer(child):
+    """Operands that lie beside each other in the rows of one buffer are taken, and
+    refused by the first byte that they share."""
+    # rows of 200 f32: x from column 0, y from column 64, the sums from column 128
+    norm = "L.q8d_rmsnorm_rows(M + {x}, {r}, {s}, 0, {ldx}, 200, 200, 64 * M, 1e-6, M + {y}, {yt}, {ldy}, 5, 64, None)"
+
+    def n(x=0, r=None, s=None, ldx=200, y=256, yt=0, ldy=200):
+        at = lambda v: "None" if v is None else f"M + {v}"  # noqa: E731
+        return norm.format(x=x, r=at(r), s=at(s), ldx=ldx, y=y, yt=yt, ldy=ldy)
+    good = [n(), n(s=512), n(r=512, s=512), n(y=0, x=256), n(y=800 + 256), n(x=800, y=544), n(y=256, yt=1, ldy=400),
+            n(x=0, y=544, s=256)]
+    bad = [n(y=252), n(y=4), n(y=548), n(x=256, y=4), n(s=316), n(r=512, s=516), n(y=256, ldy=196), n(y=256, yt=1, ldy=200),
+           n(y=800 + 252), n(y=800 - 252), n(x=800, y=548)]
+    assert statuses(child, good) == [0] * len(good)
+    assert statuses(child, bad) == [-1] * len(bad)
+    # rows of 160 f32: X 64 wide, Y and its residual 48
+    mul = "L.q8d_q4_matmul(M + {x}, 0, 160, 2 * M, 32, None, {r}, 160, M + {y}, {ldy}, 3, 64, 48, None)"
+    good = [mul.format(x=0, r="None", y=256, ldy=160), mul.format(x=0, r="M + 448", y=256, ldy=160),
+            mul.format(x=0, r="M + 256", y=256, ldy=160), mul.format(x=192, r="None", y=0, ldy=160),
+            mul.format(x=0, r="None", y=640 + 256, ldy=160)]
+    bad = [mul.format(x=0, r="None", y=252, ldy=160), mul.format(x=0, r="M + 444", y=256, ldy=160),
+           mul.format(x=192, r="None", y=4, ldy=160), mul.format(x=0, r="None", y=256, ldy=156),
+           mul.format(x=0, r="None", y=452, ldy=160)]
+    assert statuses(child, good) == [0] * len(good)
+    assert statuses(child, bad) == [-1] * len(bad)
