@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(most_threads(kV * kK)) rmsnorm_kernel(const No
     ss = pair_sum(ss, A.warps, 0xffffffffu);
   }
   float inv = rms_factor(ss, A.inv_n, P.eps);
-  const bool good = !live || rms_in_range(ss);
+  const bool good = !live || rms_in_range(ss, P.eps);
   // (whole rows enter together; of rows that share a warp each keeps its own
   // factor, whatever the others hold)
   if (!__all_sync(0xffffffffu, good)) {

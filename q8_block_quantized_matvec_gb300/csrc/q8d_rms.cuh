@@ -73,8 +73,11 @@ __device__ __forceinline__ Pair pair_sum(Pair p, int width, uint32_t mask) {
 }
 
 // Sums outside these lose their squares' remainders below f32, or are no
-// number: such rows are summed again in 64 bits.
-__device__ __forceinline__ bool rms_in_range(const Pair& p) { return p.hi > 0x1p-80f && p.hi < 0x1p100f; }
+// number, and above 2^100 the estimate's square loses its own: such rows are summed
+// again in 64 bits.
+__device__ __forceinline__ bool rms_in_range(const Pair& p, float eps) {
+  return p.hi > 0x1p-80f && p.hi < 0x1p100f && eps < 0x1p100f;
+}
 
 // 1 / sqrt(ss / n + eps) rounded to f32; inv_n: 1 / n as a pair.  One Newton
 // step on the hardware's estimate, its residual 1 - m y^2 in pairs.

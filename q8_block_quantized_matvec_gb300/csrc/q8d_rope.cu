@@ -238,7 +238,7 @@ __device__ __forceinline__ void head_factors(const Pair (&ss)[steps_of(kE)],
   const float eps = A.P.d.eps;
   const int mine = lane & (kSteps - 1);
   float r = rms_factor(p, A.inv_n, eps);
-  const bool good = !valid(mine) || rms_in_range(p);
+  const bool good = !valid(mine) || rms_in_range(p, eps);
   if (!__all_sync(0xffffffffu, good)) {
     double d[kSteps];
 #pragma unroll
