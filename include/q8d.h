@@ -548,7 +548,8 @@ int q8d_q4_unpack(const void* w_q4, void* dst, int dst_dtype, long long ld, int 
  * Q8D_EUNSUPPORTED.  m == 0 or p == 0: no-op.  Matrices are read once (with more than
  * eight f32 rows at most twice; what meets f32 elements below 2^-32 of the largest
  * of their 128 columns once more).  Nothing depends on the order in which threads
- * finish.  Waits inside are bounded (seconds); the sums that miss a copy are NaN.
+ * finish.  Waits inside are bounded (seconds); the sums that miss a copy are NaN
+ * (these calls have no error word: NaN is the only sign).
  * ---------------------------------------------------------------------- */
 int q8d_q4_matmul(const void* X, int x_dtype, long long ldx, const void* w_q4, int group,
                   const float* bias, const float* residual, long long ldr, float* Y, long long ldy,
@@ -563,6 +564,13 @@ int q8d_q4_matmul(const void* X, int x_dtype, long long ldx, const void* w_q4, i
  * ---------------------------------------------------------------------- */
 int q8d_q4_gated(const void* X, int x_dtype, long long ldx, const void* wg_q4, const void* wu_q4,
                  int group, float* H, long long ldh, int m, int n, int p, void* stream);
+
+/* Sets at which poll a wait inside these products gives up (1: without waiting;
+ * 0: the default, 2^24), for every later call of the process and the graphs that
+ * capture it.  On expiry the sums that miss a copy are NaN, the copies in flight
+ * are waited for, and the CUDA context stays usable.  A small value is a way to
+ * check that a caller's error handling sees such a call. */
+int q8d_q4_set_wait_limit(unsigned polls);
 
 /* ------------------------------------------------------------------------
  * Decode step graph ("IV.4: One command buffer per token", "One command

@@ -151,6 +151,8 @@ def lib():
         L.q8d_q4_matmul.restype = i32
         L.q8d_q4_gated.argtypes = [vp, i32, i64, vp, vp, i32, vp, i64, i32, i32, i32, vp]
         L.q8d_q4_gated.restype = i32
+        L.q8d_q4_set_wait_limit.argtypes = [C.c_uint]
+        L.q8d_q4_set_wait_limit.restype = i32
         L.q8d_step_create.argtypes = [C.POINTER(StepDesc), vp, C.POINTER(vp)]
         L.q8d_step_create.restype = i32
         L.q8d_step_launch.argtypes = [vp, vp]
@@ -406,6 +408,10 @@ def q8d_q4_gated(X, x_dtype: int, ldx: int, wg_q4, wu_q4, group: int, H, ldh: in
     return _check(lib().q8d_q4_gated(
         _ptr(X), x_dtype, ldx, _ptr(wg_q4), _ptr(wu_q4), group, _ptr(H), ldh,
         m, n, p, _stream(stream)), "q8d_q4_gated")
+
+
+def q8d_q4_set_wait_limit(polls: int) -> int:
+    return _check(lib().q8d_q4_set_wait_limit(int(polls)), "q8d_q4_set_wait_limit")
 
 
 class Step:

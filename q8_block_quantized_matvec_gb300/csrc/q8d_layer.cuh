@@ -89,5 +89,6 @@ struct Q4Params {
   int m, n, p;
 };
 int q4_launch(const Q4Params& P, cudaStream_t stream);
+void q4_set_wait_limit(uint32_t polls);  // of launches from now on; 0: the default
 
 }  // namespace q8d

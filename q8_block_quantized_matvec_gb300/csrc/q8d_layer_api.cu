@@ -241,4 +241,9 @@ int q8d_q4_gated(const void* X, int x_dtype, long long ldx, const void* wg_q4, c
   return q4_product(X, x_dtype, ldx, wg_q4, wu_q4, 2, group, nullptr, nullptr, 0, H, ldh, m, n, p, stream);
 }
 
+int q8d_q4_set_wait_limit(unsigned polls) {
+  q4_set_wait_limit(polls);
+  return Q8D_OK;
+}
+
 }  // extern "C"
