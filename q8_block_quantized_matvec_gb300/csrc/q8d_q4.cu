@@ -571,10 +571,16 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_kernel(const __gr
         };
         // (us, whole copies unrolled / tiles unrolled with a branch each / a loop: one
         // row, gated 3584 -> 18944, 15.2 / 15.6 / -; eight 23.3 / 23.5 / 25.3; sixteen
-        // Q8_0 rows, gated 3584 -> 4736, 15.1 / 15.1 / 14.6, 18944 28.4 / 26.6 / 27.6 in f16)
-        if (MODE != kF32 && NG > 1) {
+        // Q8_0 rows 34.4 / 34.4 / 34.9, 3584 -> 4736 14.6 / 14.4 / 14.5; sixteen f16 rows in
+        // groups of 32, 64, 128 27.9 / 27.8 / 27.5, 27.7 / 26.4 / 26.8, 26.6 / 25.9 / 26.3:
+        // unrolled, those of 32 spill)
+        if (MODE == kF16 && NG > 1 && NS == 4) {
 #pragma unroll 1
           for (int c = 0; c < n; ++c) work(c);
+        } else if (MODE != kF32 && NG > 1) {
+#pragma unroll
+          for (int c = 0; c < kChunk; ++c)
+            if (c < n) work(c);
         } else if (n == kChunk) {
 #pragma unroll
           for (int c = 0; c < kChunk; ++c) work(c);
@@ -750,7 +756,9 @@ struct Plan {
   double ns;
 };
 // ns of an SM a tile, measured with calls of 400 and more: the issue slots bound
-// them, and with many columns the operand's reads from shared memory.
+// them, and with many columns the operand's reads from shared memory.  (Of 396 ways of
+// cutting up products of 9 to 16 f16 and Q8_0 rows one changes between 41 and 55, 60
+// and 72 ns for the 45 and 65.)
 constexpr double tile_ns(int mode, int ng, int scales) {
   return ng == 4 ? 70 + 6 * scales : ng == 2 ? (mode == kF32 ? 39 : mode == kF16 ? 45 : 65) : mode == kQ8 ? 35 : 27;
 }
