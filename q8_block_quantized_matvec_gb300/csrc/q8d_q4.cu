@@ -7,8 +7,10 @@
 // 190 issue slots.  On CUDA cores its 2048 products alone take 64 (and their
 // unpacking twice that); the tensor cores take them in eight mma.sync m16n8k16.
 //  * The weights are the 16 x 16 operand, eight rows of the batch (four f32 ones
-//    as f16 hi and lo) its 8 columns.  tcgen05's smallest shape spends 93 clocks
-//    on as many weights as mma.sync multiplies in 32 a column group.
+//    as f16 hi and lo) its 8 columns: 16 clocks of the tensor pipe a tile and column
+//    group (counters of one and of sixteen rows), where a tcgen05.mma of as many
+//    weights takes 93 for any number of columns up to 128 (q8d_mma.cu) and wants
+//    them written out as f16 first.
 //  * Tiles lie in memory in the order in which lanes feed them (q8d_layer.cuh):
 //    two 16-byte reads a lane take a tile from shared memory, no byte twice and
 //    no bank twice.  Each warp has a ring of its own there, filled by bulk copies
@@ -33,12 +35,14 @@
 //    for its warps.  The warps' sums of a strip meet in shared memory, the CTAs' in
 //    that of the one that finishes them, both in a fixed order.
 //
-// us in a graph (and TB/s of weights): one row, 896 -> 151936 15.3 (4.8), gated 3584
-// -> 18944 15.5 (4.9), 3584 -> 4608 5.8; gated, eight rows 23.5, sixteen f16 rows 27.6,
-// Q8_0 34.8; 18944 -> 3584, sixteen rows 26.4.  A call spends about four
+// us in a graph (and TB/s of weights): one row, 896 -> 151936 15.2 (4.8), gated 3584
+// -> 18944 15.6 (4.9), 3584 -> 4608 5.8; gated, eight rows 23.5, sixteen f16 rows 27.6,
+// Q8_0 34.5; 18944 -> 3584, sixteen rows 26.1.  A call spends about four
 // microseconds starting and meeting; then a tile takes 50 to 55 clocks with one
 // column group (150 instructions, 58 % of the issue slots), 80 with two (latency:
-// sixteen warps of 128 registers).
+// sixteen warps of 128 registers).  Four groups keep 8 to 44 bytes a thread in local
+// memory beside those registers; of 18944 -> 3584, sixteen rows, the tensor pipe is
+// busy 30 % and the issue slots 47 %.
 #include <algorithm>
 #include <array>
 #include <atomic>
@@ -124,6 +128,10 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Whole numbers under the exponent of 1024 become f16 by a mask and one exact
+// operation (the conversion that Kim, Henry, Fahim and Awadalla, "Who Says Elephants
+// Can't Run: Bringing Large Scale MoE Models into Cloud Scale Production", 2022,
+// describe for 4- and 8-bit weights).
 // Constants of unpack(), kept out of the compiler's sight: with them in
 // registers (w & mask) | magic is one LOP3, as a constant it is two.
 struct Magic {

@@ -4,7 +4,9 @@
 // The quantizer is the 4-bit cache's over groups of 32, 64 or 128: the element
 // of largest magnitude (the first of them) / -8 is the scale.  A block of 256
 // threads takes a tile: sixteen neighbouring lanes a row of it, eight columns
-// (one word) a lane.  Run once for a model: HBM bounds it.
+// (one word) a lane.  Run once for a model, and not made fast: 18944 x 3584 in groups
+// of 32 from f32 takes 63 us (46 at the copy rate), from f16 63 (26), from Q8_0 70
+// (16), back into f32 61, into f16 129, whose elements are moved one by one.
 #include "q8d_kv_rows.cuh"
 #include "q8d_layer.cuh"
 

@@ -54,9 +54,10 @@ struct TableArgs {
 // The angle of an entry is the rounded product pos * f, as the plain formula has
 // it, and each is handed to the functions: turning a neighbour's angle on, two to
 // four times as fast, is as near to the true value but rounds elsewhere, and one of
-// 3000 entries at positions near 131072 came out a unit apart (1.1 ms for 131072
-// positions of 128, once a model).
-__global__ void __launch_bounds__(256) rope_table_kernel(const TableArgs A) {
+// 3000 entries at positions near 131072 came out a unit apart (0.9 to 1.1 ms for
+// 131072 positions of 128, 0.15 for 8192, once a model; every thread works out its
+// frequency, and the FP64 pipe bounds it).
+__global__ void __launch_bounds__(256) rope_positions_kernel(const TableArgs A) {
   griddep_launch_dependents();
   griddep_wait();
   const int i = blockIdx.y * 32 + threadIdx.x;
@@ -263,7 +264,10 @@ __device__ __forceinline__ void head_factors(const Pair (&ss)[steps_of(kE)],
 }
 
 // (three CTAs an SM, us for 4096 rows of 16 / 8 heads of 128 from f32 into f16: two
-// 27.5, three 25.6, four 31.7)
+// 27.5, three 25.6, four 31.7.  With the norms, and into packed caches, the 80
+// registers of three do not hold a lane's four steps: the instances with norms keep
+// 24 to 108 bytes a thread in local memory, from f16 rows 24 to 44, those without at
+// most 60; two CTAs were not measured for these.)
 template <typename T, int KV, int kE, bool kNorm, int WAY>
 __global__ void __launch_bounds__(kWarps * 32, kE == 4 ? 3 : 2) rope_rows_kernel(const RopeArgs A) {
   constexpr int kP = kE / 2, kW = kE * sizeof(T) / 4, kSteps = steps_of(kE);
@@ -538,7 +542,7 @@ int rope_table_launch(float* table, int max_pos, int rot_dim, double theta, int 
     A.high = std::min(std::ceil(at(beta_slow)), rot_dim - 1.0);
   }
   const dim3 grid((unsigned)std::min((max_pos + 7LL) / 8, 4096LL), (unsigned)((A.half + 31) / 32));
-  return launch_ex(rope_table_kernel, grid, dim3(32, 8), 0, stream, true, A);
+  return launch_ex(rope_positions_kernel, grid, dim3(32, 8), 0, stream, true, A);
 }
 
 int rope_rows_launch(const RopeRowsParams& P, cudaStream_t stream) {
