@@ -534,7 +534,8 @@ int q8d_q4_unpack(const void* w_q4, void* dst, int dst_dtype, long long ld, int 
  * q8d_q4_matmul - a 4-bit matrix applied to m rows of activations:
  *   Y[i][r] = sum_k X[i][k] * W[r][k] (+ bias[r]) (+ residual[i][r])
  * within 1e-5 of the sum of |terms| (and 2^-126, below f32's normal range),
- * however far the elements of a row lie apart.
+ * however far the elements of a row lie apart; where that sum passes f32's range,
+ * infinite or NaN.
  *   X: device rows of x_dtype, ldx elements apart (>= n): Q8D_KV_F32 or
  *      Q8D_KV_F16 (16-byte aligned, ldx % 4 == 0, f16 % 8 == 0), or Q8D_KV_Q8_0:
  *      rows of Q8_0 blocks as q8d_rmsnorm_rows writes them (2-byte aligned,
