@@ -217,9 +217,9 @@ __device__ __forceinline__ void split2(uint64_t x, float by, __half2& hi, __half
 }
 // Adds what the operand lacks of the far elements, times their weights, to the sums
 // of a pass (its strips pa .. pa + pu - 1), into those of the first warp that met a
-// part.  Its CTA's tiles of a strip are the ktl from k0 on.  (Rows of real streams
-// hold no such elements; 3584 -> 18944, gated, one row: 15.4 us, of half zeros 15.7,
-// with one of them 20.3, with one in every tile 72.)
+// part.  Its CTA's tiles of a strip are the ktl from k0 on.  (Rows seldom hold
+// such elements; 3584 -> 18944, gated, one row: 15.4 us, of half zeros 15.8, with one
+// of them 18.9, with one in every tile 73.)
 template <int kWarps, int NG, int NS>
 __device__ __noinline__ void add_far_terms(const Q4Args& A, uint8_t* smem, int pa, int pu, int k0, int ktl) {
   constexpr int kRec = kQ4QuantBytes + kQ4Rows * NS * 2, kMp = NG * group_rows(kF32);
@@ -228,14 +228,14 @@ __device__ __noinline__ void add_far_terms(const Q4Args& A, uint8_t* smem, int p
   const Smem L = smem_layout(kWarps, kF32, NG, most, A.ncol, A.parts, A.cs);
   const int row = threadIdx.x & 15, h = row / 8, g = row & 7;
   const uint32_t half = 0xffffu << (threadIdx.x & 16);  // the sixteen threads of a strip and row of X
+  const auto ballot = [&](bool yes) { return __ballot_sync(half, yes) >> (threadIdx.x & 16) & 0xffffu; };
   for (int o = threadIdx.x / 16; o < parts * P.m; o += kWarps * 2) {
     const int sp = o / P.m, j = o - sp * P.m, unit = pa + sp / P.nmat;
     const float* scale = reinterpret_cast<const float*>(smem + L.scale) + j * most;
     const float* x = static_cast<const float*>(P.X) + j * P.ldx + k0 * kQ4Cols;
     const uint8_t* tiles = P.w[sp % P.nmat] + ((long long)unit * A.kt + k0) * kRec;
     double sum = 0.0;
-    for (int k = 0; k < ktl; ++k) {
-      if (!smem[L.far + j * most + k]) continue;
+    const auto tile_terms = [&](int k) {
       const float back = scale[k], by = 1.f / back;  // (powers of two)
       const uint8_t* tile = tiles + (long long)k * kRec;
       float v[kQ4Cols / 16];
@@ -246,8 +246,7 @@ __device__ __noinline__ void add_far_terms(const Q4Args& A, uint8_t* smem, int p
       }
 #pragma unroll
       for (int i = 0; i < kQ4Cols / 16; ++i) {
-        uint32_t hits = __ballot_sync(half, v[i] != 0.f && fabsf(v[i]) < kFar * back) >> (threadIdx.x & 16) & 0xffffu;
-        for (; hits; hits &= hits - 1) {
+        for (uint32_t hits = ballot(v[i] != 0.f && fabsf(v[i]) < kFar * back); hits; hits &= hits - 1) {
           const int c = 16 * i + __ffs(hits) - 1, b = c / 32, t = c / 8 & 3, e = c & 7;
           const float f = __shfl_sync(half, v[i], c & 15, 16);
           __half2 hi, lo;
@@ -259,7 +258,10 @@ __device__ __noinline__ void add_far_terms(const Q4Args& A, uint8_t* smem, int p
           sum += (f - held * back) * ((int)(w >> (4 * (e / 2 + 4 * (e & 1))) & 15u) - 8) * (double)f16_bits_to_f32(s);
         }
       }
-    }
+    };
+    for (int k = 0; k < ktl; k += 16)
+      for (uint32_t far = ballot(k + row < ktl && smem[L.far + j * most + k + row]); far; far &= far - 1)
+        tile_terms(k + __ffs(far) - 1);
     const uint32_t met = reinterpret_cast<const uint32_t*>(smem + L.meets)[sp];
     const int slot = (__ffs(met) - 1) * pass_slots(kWarps, A.parts) + (int)(met >> 24);
     reinterpret_cast<float*>(smem + L.part)[(slot * kMp + j) * 16 + row] += (float)sum;
